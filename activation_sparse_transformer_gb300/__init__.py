@@ -21,6 +21,19 @@ rows):
 
 The calls are asynchronous on the current stream and can be captured in a CUDA
 graph; twell_pack / twell_unpack convert between dense bf16 H and the packed form.
+
+One decode step around the layer (R requests, each with new tokens; examples/decode_step.py
+runs it whole):
+
+    cache = tw.alloc_kv_cache(n_pages, 64, kv_heads, 128, tw.KV_E4M3, "cuda")
+    plan = tw.alloc_kv_plan(R, n_tokens, "cuda")
+    tw.twell_kv_plan(kv_lens, new_tokens, block_table, ring, pool, 64, plan)
+    tw.twell_kv_append(K, V, plan.cu_q, plan.slots, cache)       # [n_tokens, kv_heads, 128] bf16
+    tw.twell_kv_attention(Q, cache, block_table, plan.cu_q, plan.positions, plan.kv_lens, max_kv_len,
+                          max_q_len, 128 ** -0.5, O, workspace)  # [n_tokens, q_heads, 128] bf16
+    ...                                                          # the sparse layer, the output projection
+    tw.twell_logprobs(logits, targets, 1.0, logprob, entropy, lse, top_logprob, top_index)
+    tw.twell_logprobs_bwd(logits, targets, 1.0, lse, entropy, d_logprob, d_entropy, d_logits)
 """
 from __future__ import annotations
 
@@ -36,7 +49,8 @@ TWELL_OK = 0
 KERNELS = {
     "up_pack": 0, "route": 1, "fb_assemble": 2, "spmm": 4, "fb_down": 5, "pack": 6,
     "check_format": 3, "unpack": 7, "sddmm": 8, "dx": 9, "dw": 10, "dense_gemm": 11, "aux": 12,
-    "dw_fallback": 13, "dx_fallback": 14,
+    "dw_fallback": 13, "dx_fallback": 14, "kv_plan": 15, "kv_append": 16, "kv_attention": 17, "kv_join": 18,
+    "logprobs": 19, "logprobs_bwd": 20,
 }
 EXPORTED = [
     "twell_pack", "twell_unpack", "twell_ffn_fwd", "twell_fwd_workspace_bytes", "twell_ffn_bwd",
@@ -47,6 +61,8 @@ EXPORTED = [
     "twell_selftest_wait_timeout", "twell_check_format", "twell_dense_ffn_bwd", "twell_dense_bwd_workspace_bytes",
     "twell_bwd_tiles_workspace_bytes", "twell_gated_ffn_fwd_train", "twell_gated_ffn_bwd",
     "twell_gated_bwd_workspace_bytes", "twell_gated_bwd_tiles_workspace_bytes",
+    "twell_kv_plan", "twell_kv_append", "twell_kv_attention", "twell_kv_attention_workspace_bytes",
+    "twell_kv_read_status", "twell_logprobs", "twell_logprobs_bwd",
 ]
 
 
@@ -66,6 +82,15 @@ class twell_t(ctypes.Structure):
     ]
 
 
+class twell_kv_t(ctypes.Structure):
+    _fields_ = [
+        ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+    ]
+
+
 _lib_handle = None
 
 
@@ -79,6 +104,7 @@ def load_library() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     L = ctypes.POINTER(twell_t)
+    KV = ctypes.POINTER(twell_kv_t)
     sig = {
         "twell_pack": (ctypes.c_int, [P, I64, L, P]),
         "twell_unpack": (ctypes.c_int, [L, P, I64, P]),
@@ -109,6 +135,14 @@ def load_library() -> ctypes.CDLL:
         "twell_check_format": (ctypes.c_int, [L, P, P]),
         "twell_dense_ffn_bwd": (ctypes.c_int, [P, P, P, P, I32, I32, I32, P, ctypes.c_float, P, P, P, P, P, SZ, P]),
         "twell_dense_bwd_workspace_bytes": (SZ, [I32, I32, I32]),
+        "twell_kv_plan": (ctypes.c_int, [P, P, I32, I32, I32, I32, P, P, P, P, P, P, P, P, I32, P, P]),
+        "twell_kv_append": (ctypes.c_int, [P, I64, P, I64, P, P, I32, I32, KV, P]),
+        "twell_kv_attention": (ctypes.c_int, [P, I64, KV, P, I32, P, P, P, I32, I32, I32, I32, I32, ctypes.c_float, P,
+                                              I64, P, P, SZ, P]),
+        "twell_kv_attention_workspace_bytes": (SZ, [I32, I32, I32, I32, I32]),
+        "twell_kv_read_status": (ctypes.c_int, [KV, P]),
+        "twell_logprobs": (ctypes.c_int, [P, I32, I64, I32, I32, P, ctypes.c_float, P, P, P, I32, P, P, P]),
+        "twell_logprobs_bwd": (ctypes.c_int, [P, I32, I64, I32, I32, P, ctypes.c_float, P, P, P, P, P, I64, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -419,3 +453,232 @@ def twell_profile_read(kernel) -> tuple:
     ms = ctypes.c_double(0.0)
     _check(load_library().twell_profile_read(k, ctypes.byref(n), ctypes.byref(ms)), "twell_profile_read")
     return int(n.value), float(ms.value)
+
+
+# ---------------------------------------------------------------- decode step
+KV_E4M3, KV_INT8 = 0, 1
+
+
+def _need_type(t, dtype, n: int, name: str) -> None:
+    """A contiguous device tensor of dtype with at least n elements."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, the call takes {dtype}")
+    if t.numel() < n:
+        raise ValueError(f"{name}: {t.numel()} elements, the call needs {n}")
+
+
+def _need_rows(t, dtype, tail: tuple, name: str) -> int:
+    """The distance between the tokens of a device tensor [tokens, *tail], which
+    may be a slice of wider rows but holds each token in one piece."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, the call takes {dtype}")
+    if not t.is_cuda:
+        raise ValueError("tensors passed to libtwell must be CUDA tensors")
+    if tuple(t.shape[1:]) != tail:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, the call takes [tokens, {', '.join(map(str, tail))}]")
+    step, ok = 1, True
+    for size, stride in zip(reversed(tail), reversed(t.stride()[1:])):
+        ok = ok and (stride == step or size == 1)
+        step *= size
+    if not ok:
+        raise ValueError(f"{name}: strides {t.stride()}, a token's {step} elements must lie together")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), step)
+
+
+@dataclass
+class KVCache:
+    """An 8-bit paged cache: k and v [n_pages, n_heads, page_size, head_dim] of
+    torch.float8_e4m3fn or torch.int8, k_scale and v_scale [n_pages, n_heads]
+    float32, status int32.  The buffers stay the caller's."""
+    k: "object"
+    v: "object"
+    k_scale: "object"
+    v_scale: "object"
+    status: "object"
+
+    def __post_init__(self):
+        import torch
+        formats = {torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_INT8}
+        if self.k.dtype not in formats or self.v.dtype != self.k.dtype:
+            raise ValueError(f"k, v: {self.k.dtype}, {self.v.dtype}; a cache holds float8_e4m3fn or int8")
+        if self.k.dim() != 4 or self.v.shape != self.k.shape:
+            raise ValueError(f"k, v: shapes {tuple(self.k.shape)}, {tuple(self.v.shape)}")
+        self.n_pages, self.n_heads, self.page_size, self.head_dim = self.k.shape
+        for t, name in ((self.k_scale, "k_scale"), (self.v_scale, "v_scale")):
+            _need_type(t, torch.float32, self.n_pages * self.n_heads, name)
+        _need_type(self.status, torch.int32, 1, "status")
+        self.format = formats[self.k.dtype]
+        self._struct = None
+
+    def struct(self):
+        if self._struct is None:
+            self._struct = ctypes.pointer(twell_kv_t(
+                self.n_pages, self.page_size, self.n_heads, self.head_dim, self.format, 0, _ptr(self.k),
+                _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale), _ptr(self.status)))
+        return self._struct
+
+
+def alloc_kv_cache(n_pages: int, page_size: int, n_heads: int, head_dim: int, fmt: int = KV_E4M3,
+                   device="cuda") -> KVCache:
+    import torch
+    shape, dt = (n_pages, n_heads, page_size, head_dim), (torch.float8_e4m3fn if fmt == KV_E4M3 else torch.int8)
+    return KVCache(k=torch.empty(shape, dtype=dt, device=device), v=torch.empty(shape, dtype=dt, device=device),
+                   k_scale=torch.zeros(shape[:2], dtype=torch.float32, device=device),
+                   v_scale=torch.zeros(shape[:2], dtype=torch.float32, device=device),
+                   status=torch.zeros((4,), dtype=torch.int32, device=device))
+
+
+@dataclass
+class KVPlan:
+    """What twell_kv_plan writes: kv_lens [R], cu_q [R + 1], slots [n_tokens]
+    int64, positions [n_tokens], pool [2] (for the next step's plan), status."""
+    kv_lens: "object"
+    cu_q: "object"
+    slots: "object"
+    positions: "object"
+    pool: "object"
+    status: "object"
+
+
+def alloc_kv_plan(n_requests: int, n_tokens: int, device="cuda") -> KVPlan:
+    import torch
+    i32 = lambda n: torch.zeros((n,), dtype=torch.int32, device=device)  # noqa: E731
+    return KVPlan(kv_lens=i32(n_requests), cu_q=i32(n_requests + 1),
+                  slots=torch.zeros((n_tokens,), dtype=torch.int64, device=device), positions=i32(n_tokens),
+                  pool=i32(2), status=i32(4))
+
+
+def alloc_page_ring(n_pages: int, device="cuda") -> tuple:
+    """(ring, pool) of a cache whose pages are all free."""
+    import torch
+    return (torch.arange(n_pages, dtype=torch.int32, device=device),
+            torch.tensor([0, n_pages], dtype=torch.int32, device=device))
+
+
+def twell_kv_plan(kv_lens, new_tokens, block_table, ring, pool, page_size: int, plan: KVPlan, stream=None) -> None:
+    """Block tables and slot maps of one step; the pages are ring.numel()."""
+    import torch
+    R, n_tokens = kv_lens.numel(), plan.slots.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table: the call takes [requests, blocks]")
+    width = block_table.shape[1]
+    i32 = torch.int32
+    _need_type(kv_lens, i32, R, "kv_lens")
+    _need_type(new_tokens, i32, R, "new_tokens")
+    _need_type(block_table, i32, R * width, "block_table")
+    _need_type(ring, i32, 1, "ring")
+    _need_type(pool, i32, 2, "pool")
+    _need_type(plan.kv_lens, i32, R, "plan.kv_lens")
+    _need_type(plan.cu_q, i32, R + 1, "plan.cu_q")
+    _need_type(plan.slots, torch.int64, n_tokens, "plan.slots")
+    _need_type(plan.positions, i32, n_tokens, "plan.positions")
+    _need_type(plan.pool, i32, 2, "plan.pool")
+    _need_type(plan.status, i32, 1, "plan.status")
+    _check(load_library().twell_kv_plan(_ptr(kv_lens), _ptr(new_tokens), R, page_size, ring.numel(), width,
+                                        _ptr(block_table), _ptr(ring), _ptr(pool), _ptr(plan.pool),
+                                        _ptr(plan.kv_lens), _ptr(plan.cu_q), _ptr(plan.slots), _ptr(plan.positions),
+                                        n_tokens, _ptr(plan.status), _stream(stream)), "twell_kv_plan")
+
+
+def twell_kv_append(K, V, cu_q, slots, cache: KVCache, stream=None) -> None:
+    """Keys and values [n_tokens, n_heads, head_dim] bf16 into the cache's slots."""
+    import torch
+    tail = (cache.n_heads, cache.head_dim)
+    ldk, ldv = _need_rows(K, torch.bfloat16, tail, "K"), _need_rows(V, torch.bfloat16, tail, "V")
+    n, R = K.shape[0], cu_q.numel() - 1
+    if V.shape[0] != n:
+        raise ValueError(f"V: {V.shape[0]} tokens, K has {n}")
+    _need_type(cu_q, torch.int32, 1, "cu_q")
+    _need_type(slots, torch.int64, n, "slots")
+    _check(load_library().twell_kv_append(K.data_ptr(), ldk, V.data_ptr(), ldv, _ptr(cu_q), _ptr(slots), n, R,
+                                          cache.struct(), _stream(stream)), "twell_kv_append")
+
+
+def kv_attention_workspace_bytes(n_tokens, n_requests, n_q_heads, n_kv_heads, head_dim) -> int:
+    return int(load_library().twell_kv_attention_workspace_bytes(n_tokens, n_requests, n_q_heads, n_kv_heads,
+                                                                 head_dim))
+
+
+def twell_kv_attention(Q, cache: KVCache, block_table, cu_q, positions, kv_lens, max_kv_len: int, max_q_len: int,
+                       softmax_scale: float, O, workspace, lse=None, stream=None) -> None:
+    """O [n_tokens, n_q_heads, head_dim] bf16 = attention of Q over the cache;
+    lse [n_tokens, n_q_heads] float32 when given."""
+    import torch
+    n, heads = Q.shape[0], Q.shape[1]
+    tail = (heads, cache.head_dim)
+    ldq, ldo = _need_rows(Q, torch.bfloat16, tail, "Q"), _need_rows(O, torch.bfloat16, tail, "O")
+    if O.shape[0] != n:
+        raise ValueError(f"O: {O.shape[0]} tokens, Q has {n}")
+    R = kv_lens.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table: the call takes [requests, blocks]")
+    width = block_table.shape[1]
+    _need_type(block_table, torch.int32, R * width, "block_table")
+    _need_type(cu_q, torch.int32, R + 1, "cu_q")
+    _need_type(positions, torch.int32, n, "positions")
+    _need_type(kv_lens, torch.int32, R, "kv_lens")
+    if lse is not None:
+        _need_type(lse, torch.float32, n * heads, "lse")
+    _check(load_library().twell_kv_attention(Q.data_ptr(), ldq, cache.struct(), _ptr(block_table), width, _ptr(cu_q),
+                                             _ptr(positions), _ptr(kv_lens), n, R, heads, max_kv_len, max_q_len,
+                                             softmax_scale, O.data_ptr(), ldo, _ptr(lse), _ptr(workspace),
+                                             workspace.numel() * workspace.element_size(), _stream(stream)),
+           "twell_kv_attention")
+
+
+def twell_kv_read_status(cache: KVCache, stream=None) -> int:
+    return int(load_library().twell_kv_read_status(cache.struct(), _stream(stream)))
+
+
+def _logits(t, name: str) -> tuple:
+    """(dtype code, rows, vocabulary, distance between rows) of a logits tensor."""
+    import torch
+    codes = {torch.bfloat16: 0, torch.float32: 1}
+    if t.dtype not in codes or t.dim() != 2:
+        raise ValueError(f"{name}: {t.dtype} of {t.dim()} dimensions, the call takes [rows, vocab] of bfloat16 or float32")
+    if not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: a CUDA tensor whose rows are contiguous")
+    return codes[t.dtype], t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]) if t.shape[0] < 2 else t.stride(0)
+
+
+def twell_logprobs(logits, targets, inv_temperature: float, logprob, entropy, lse, top_logprob=None, top_index=None,
+                   stream=None) -> None:
+    """logprob, entropy, lse [rows] float32 (None: not wanted; targets and logprob
+    together) and the top_logprob.shape[1] best alternatives [rows, k]."""
+    import torch
+    code, rows, vocab, ld = _logits(logits, "logits")
+    for t, name in ((logprob, "logprob"), (entropy, "entropy"), (lse, "lse")):
+        if t is not None:
+            _need_type(t, torch.float32, rows, name)
+    if targets is not None:
+        _need_type(targets, torch.int32, rows, "targets")
+    k = 0
+    if top_logprob is not None or top_index is not None:
+        if top_logprob is None or top_index is None:
+            raise ValueError("top_logprob, top_index: give both or neither")
+        k = top_logprob.shape[1]
+        _need_type(top_logprob, torch.float32, rows * k, "top_logprob")
+        _need_type(top_index, torch.int32, rows * k, "top_index")
+    _check(load_library().twell_logprobs(logits.data_ptr(), code, ld, rows, vocab, _ptr(targets), inv_temperature,
+                                         _ptr(logprob), _ptr(entropy), _ptr(lse), k, _ptr(top_logprob),
+                                         _ptr(top_index), _stream(stream)), "twell_logprobs")
+
+
+def twell_logprobs_bwd(logits, targets, inv_temperature: float, lse, entropy, d_logprob, d_entropy, d_logits,
+                       stream=None) -> None:
+    """d_logits (type of logits; may be logits itself) from the upstream gradients
+    of logprob and entropy; targets with d_logprob, or entropy with d_entropy, may be None."""
+    import torch
+    code, rows, vocab, ld = _logits(logits, "logits")
+    code_d, rows_d, vocab_d, ldd = _logits(d_logits, "d_logits")
+    if (code_d, rows_d, vocab_d) != (code, rows, vocab):
+        raise ValueError("d_logits: type and shape are those of logits")
+    for t, name in ((lse, "lse"), (entropy, "entropy"), (d_logprob, "d_logprob"), (d_entropy, "d_entropy")):
+        if t is not None:
+            _need_type(t, torch.float32, rows, name)
+    if targets is not None:
+        _need_type(targets, torch.int32, rows, "targets")
+    _check(load_library().twell_logprobs_bwd(logits.data_ptr(), code, ld, rows, vocab, _ptr(targets),
+                                             inv_temperature, _ptr(lse), _ptr(entropy), _ptr(d_logprob),
+                                             _ptr(d_entropy), d_logits.data_ptr(), ldd, _stream(stream)),
+           "twell_logprobs_bwd")

@@ -760,7 +760,9 @@ const char* twell_status_string(int code) {
     case TWELL_ERR_FALLBACK_OVERFLOW: return "more dense-fallback rows than fb_cap";
     case TWELL_ERR_WAIT_TIMEOUT: return "a bounded pipeline wait on the GPU expired";
     case TWELL_ERR_NO_DEVICE: return "no sm_103a device is current";
-    case TWELL_ERR_BAD_FORMAT: return "packed layout breaks a format rule";
+    case TWELL_ERR_BAD_FORMAT: return "packed layout breaks a format rule, or a page number is outside the cache";
+    case TWELL_ERR_CACHE_FULL: return "a request was refused: no free page, or no room in the step's tables";
+    case TWELL_ERR_NOT_FINITE: return "an infinity or a NaN was to be stored in the 8-bit cache";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,236 @@
+// Keys and values of a step into the 8-bit paged cache (twell_kv_append).
+//
+// A run is the tokens of one request that fall into one page.  One CTA takes
+// one run of one head of K or of V: it reads the run's 2-byte values once into
+// registers, takes their largest magnitude, sets the scale 2^e from its bits and
+// writes the codes.  Reads 2 bytes and writes 1 byte per value, so HBM bounds
+// long runs and the launch plus three dependent latencies (request, slot, values)
+// bound single tokens.  The tokens of a run lie ld apart, each with 2 D bytes
+// in one piece: 16-byte loads, D / 8 lanes a token.
+#include <cuda_bf16.h>
+
+#include "kv_internal.h"
+
+namespace twell {
+namespace {
+
+constexpr int kAppendThreads = 128;
+constexpr int kMinExponent = -100;
+
+struct AppendArgs {
+  const uint16_t *k, *v;
+  int64_t ldk, ldv;
+  uint8_t *k_codes, *v_codes;
+  float *k_scale, *v_scale;
+  const int32_t* cu_q;
+  const int64_t* slots;
+  int32_t* status;
+  int n_tokens, n_requests, n_pages, heads;
+};
+
+// Least e with amax <= q 2^e (q = 448 = 1.75 * 2^8 or 127 = 1.984375 * 2^6),
+// from the bits of a finite amax >= 0.
+template <int FMT>
+__device__ __forceinline__ int scale_exponent(float amax) {
+  const int bits = __float_as_int(amax);
+  const int k = (bits >> 23) - 127, frac = bits & 0x7FFFFF;
+  const int e = FMT == TWELL_KV_E4M3 ? k - 8 + (frac > 0x600000) : k - 6 + (frac > 0x7E0000);
+  return max(e, kMinExponent);
+}
+
+__device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127) << 23); }
+
+// Two codes (low byte first) of two values that are already divided by the scale.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+  if (FMT == TWELL_KV_E4M3) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+    return c;
+  }
+  return (static_cast<uint32_t>(__float2int_rn(lo)) & 0xFFu) | ((static_cast<uint32_t>(__float2int_rn(hi)) & 0xFFu) << 8);
+}
+
+template <int FMT>
+__device__ __forceinline__ float2 decode2(uint32_t codes) {
+  if (FMT == TWELL_KV_E4M3) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+    float2 f;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(h));
+    return f;
+  }
+  return make_float2(static_cast<float>(static_cast<int8_t>(codes & 0xFF)),
+                     static_cast<float>(static_cast<int8_t>((codes >> 8) & 0xFF)));
+}
+
+// bf16 bits with an infinity made the largest finite value and a NaN made 0;
+// *bad is set when there was one.
+__device__ __forceinline__ uint32_t finite2(uint32_t w, bool* bad) {
+  const uint32_t lo = w & 0xFFFFu, hi = w >> 16;
+  const bool bl = (lo & 0x7F80u) == 0x7F80u, bh = (hi & 0x7F80u) == 0x7F80u;
+  if (!(bl || bh)) return w;
+  *bad = true;
+  const uint32_t l = !bl ? lo : (lo & 0x7Fu) ? 0u : (lo & 0x8000u) | 0x7F7Fu;
+  const uint32_t h = !bh ? hi : (hi & 0x7Fu) ? 0u : (hi & 0x8000u) | 0x7F7Fu;
+  return l | (h << 16);
+}
+
+template <int FMT, int D, int P>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+  constexpr int kLanes = D / 8;                       // lanes of one token, 8 values each
+  constexpr int kRows = kAppendThreads / kLanes;      // tokens of one pass
+  constexpr int kPasses = (P + kRows - 1) / kRows;
+  __shared__ float warp_max[kAppendThreads / 32];
+  grid_dependency_wait();
+  const int tid = threadIdx.x;
+  // run x of the grid: request r has room for floor(cu[r + 1] / P) -
+  // floor(cu[r] / P) + 2 runs, at least as many as its tokens can touch pages
+  const int64_t x = blockIdx.x;
+  const int r = warp_upper(a.n_requests, x, [&](int i) {
+    return static_cast<int64_t>(min(max(a.cu_q[i], 0), a.n_tokens) / P) + 2 * i;
+  });
+  const int t0 = min(max(a.cu_q[r], 0), a.n_tokens), t1 = min(a.cu_q[r + 1], a.n_tokens);
+  const int k = static_cast<int>(x - (t0 / P + 2 * r));
+  if (t1 <= t0) return;
+  const int64_t slot0 = a.slots[t0];
+  if (slot0 < 0) return;
+  const int o = static_cast<int>(slot0 % P);
+  const int beg = max(t0, t0 + k * P - o), end = min(t1, t0 + (k + 1) * P - o);
+  if (beg >= end) return;
+  const int64_t slot = a.slots[beg];
+  const int64_t page = slot / P;
+  const int first = static_cast<int>(slot % P);
+  if (slot < 0 || page >= a.n_pages || first + (end - beg) > P) {
+    if (tid == 0) report_error(a.status, TWELL_ERR_BAD_FORMAT);
+    return;
+  }
+  const int head = blockIdx.y;
+  const bool is_v = blockIdx.z != 0;
+  const int lane_col = (tid % kLanes) * 8, row0 = tid / kLanes;
+  const uint16_t* src = (is_v ? a.v : a.k) + static_cast<int64_t>(head) * D + lane_col;
+  const int64_t ld = is_v ? a.ldv : a.ldk;
+  const int n = end - beg;
+
+  uint4 w[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int t = row0 + i * kRows;
+    w[i] = t < n ? __ldg(reinterpret_cast<const uint4*>(src + (beg + t) * ld)) : make_uint4(0, 0, 0, 0);
+  }
+  const int64_t cell = page * a.heads + head;
+  float* const scale_at = (is_v ? a.v_scale : a.k_scale) + cell;
+  const float was = first > 0 ? *scale_at : 0.0f;
+  bool bad = false;
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    uint32_t* q = &w[i].x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      q[j] = finite2(q[j], &bad);
+      amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q[j])), fabsf(bf16_hi(q[j]))));
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+  if ((tid & 31) == 0) warp_max[tid / 32] = amax;
+  if (bad) report_error(a.status, TWELL_ERR_NOT_FINITE);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, warp_max[i]);
+  const int e = scale_exponent<FMT>(amax);
+  const float own = two_to(e);
+  const float scale = fmaxf(own, was);
+  uint8_t* const dst = (is_v ? a.v_codes : a.k_codes) + cell * (P * D);
+  // earlier tokens of the page move to the larger scale
+  if (first > 0 && scale > was) {
+    const float ratio = was / scale;
+    for (int t = row0; t < first; t += kRows) {
+      uint2* at = reinterpret_cast<uint2*>(dst + t * D + lane_col);
+      uint2 c = *at;
+      uint32_t* q = &c.x;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float2 lo = decode2<FMT>(q[j] & 0xFFFFu), hi = decode2<FMT>(q[j] >> 16);
+        q[j] = encode2<FMT>(lo.x * ratio, lo.y * ratio) | (encode2<FMT>(hi.x * ratio, hi.y * ratio) << 16);
+      }
+      *at = c;
+    }
+  }
+  // 1 / scale is exact for a power of two; another scale (a cache written by
+  // someone else) divides
+  const bool pow2 = (__float_as_uint(scale) & 0x7FFFFFu) == 0;
+  const float inv = 1.0f / scale;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int t = row0 + i * kRows;
+    if (t >= n) continue;
+    const uint32_t* q = &w[i].x;
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float lo = bf16_lo(q[j]), hi = bf16_hi(q[j]);
+      c[j] = pow2 ? encode2<FMT>(lo * inv, hi * inv) : encode2<FMT>(lo / scale, hi / scale);
+    }
+    *reinterpret_cast<uint2*>(dst + (first + t) * D + lane_col) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  }
+  if (tid == 0 && scale != was) *scale_at = scale;
+}
+
+template <int FMT, int D>
+int launch_append(const AppendArgs& a, int page, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(a.n_tokens / page + 2 * static_cast<int64_t>(a.n_requests)),
+                  static_cast<unsigned>(a.heads), 2);
+  LaunchScope scope(TWELL_KERNEL_KV_APPEND, s);
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (page) {
+    case 16: e = launch_pdl(append_kernel<FMT, D, 16>, grid, dim3(kAppendThreads), 0, s, a); break;
+    case 32: e = launch_pdl(append_kernel<FMT, D, 32>, grid, dim3(kAppendThreads), 0, s, a); break;
+    case 64: e = launch_pdl(append_kernel<FMT, D, 64>, grid, dim3(kAppendThreads), 0, s, a); break;
+    case 128: e = launch_pdl(append_kernel<FMT, D, 128>, grid, dim3(kAppendThreads), 0, s, a); break;
+  }
+  return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace twell
+
+using namespace twell;
+
+extern "C" TWELL_API int twell_kv_append(const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv,
+                                         const int32_t* cu_q, const int64_t* slots, int32_t n_tokens,
+                                         int32_t n_requests, const twell_kv_t* cache, twell_stream_t stream) {
+  KV_TRY(check_kv(cache));
+  if (n_tokens < 0 || n_requests < 0) return TWELL_ERR_INVALID_ARG;
+  if (n_tokens > 0 && n_requests > 0) {
+    KV_TRY(check_rows(K, ldk, cache->n_heads, cache->head_dim));
+    KV_TRY(check_rows(V, ldv, cache->n_heads, cache->head_dim));
+    KV_TRY(check_array(cu_q, 4));
+    KV_TRY(check_array(slots, 8));
+    if (cache->n_heads > 65535) return TWELL_ERR_UNSUPPORTED;
+    // the grid's runs: 2 a request and one more for every page of tokens
+    if (n_tokens / cache->page_size + 2 * static_cast<int64_t>(n_requests) > INT32_MAX) return TWELL_ERR_UNSUPPORTED;
+  }
+  if (!device_is_sm103()) return TWELL_ERR_NO_DEVICE;
+  if (n_tokens == 0 || n_requests == 0) return TWELL_OK;
+  const AppendArgs a{K, V, ldk, ldv, cache->k, cache->v, cache->k_scale, cache->v_scale, cu_q, slots,
+                     cache->status, n_tokens, n_requests, cache->n_pages, cache->n_heads};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cache->format == TWELL_KV_E4M3)
+    return cache->head_dim == 64 ? launch_append<TWELL_KV_E4M3, 64>(a, cache->page_size, s)
+                                 : launch_append<TWELL_KV_E4M3, 128>(a, cache->page_size, s);
+  return cache->head_dim == 64 ? launch_append<TWELL_KV_INT8, 64>(a, cache->page_size, s)
+                               : launch_append<TWELL_KV_INT8, 128>(a, cache->page_size, s);
+}
+
+extern "C" TWELL_API int twell_kv_read_status(const twell_kv_t* cache, twell_stream_t stream) {
+  if (!cache || !cache->status) return TWELL_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cudaStreamSynchronize(s) != cudaSuccess) return TWELL_ERR_CUDA;
+  int32_t st = 0;
+  if (cudaMemcpy(&st, cache->status, sizeof st, cudaMemcpyDeviceToHost) != cudaSuccess) return TWELL_ERR_CUDA;
+  return st;
+}

@@ -91,7 +91,10 @@ enum {
   TWELL_ERR_FALLBACK_OVERFLOW = -6,  /* device: more fallback rows than fb_cap */
   TWELL_ERR_WAIT_TIMEOUT = -7,       /* device: a bounded pipeline wait expired */
   TWELL_ERR_NO_DEVICE = -8,          /* no sm_103a device current */
-  TWELL_ERR_BAD_FORMAT = -9          /* device: twell_check_format found a broken rule */
+  TWELL_ERR_BAD_FORMAT = -9,         /* device: twell_check_format found a broken rule; a page or slot
+                                        number outside the cache */
+  TWELL_ERR_CACHE_FULL = -10,        /* device: twell_kv_plan had to refuse a request */
+  TWELL_ERR_NOT_FINITE = -11         /* device: twell_kv_append met an infinity or a NaN */
 };
 
 enum {
@@ -331,6 +334,166 @@ TWELL_API int twell_dense_ffn_bwd(const uint16_t* X, const uint16_t* W_inT, cons
 
 TWELL_API size_t twell_dense_bwd_workspace_bytes(int32_t n_rows, int32_t d_model, int32_t d_ff);
 
+/* ------------------------------------------------------------------ decode step
+ * What a decode step needs around the feed-forward layer: which cache pages
+ * the step's tokens go to (twell_kv_plan), the write of their keys and values
+ * into an 8-bit paged cache (twell_kv_append), the attention that reads that
+ * cache (twell_kv_attention), and the log probabilities of the answer with
+ * their gradient (twell_logprobs, twell_logprobs_bwd).  The same calls serve
+ * prompts (many new tokens of a request) and single tokens.
+ *
+ * The step's tokens lie in one batch: request r has tokens
+ * [cu_q[r], cu_q[r + 1]), consecutive in its sequence, at positions[t] (0 =
+ * the sequence's first token).  A request's i-th page is
+ * block_table[r][i]; its token at position p lies in the page
+ * block_table[r][p / page_size], and its slot number is page * page_size +
+ * p % page_size.
+ * Arrays of int32 / int64 / fp32 need their natural alignment only. */
+enum {
+  TWELL_KV_E4M3 = 0,  /* codes are 8-bit floats: sign, 4 exponent bits (bias 7), 3 fraction bits, 0x7F = NaN */
+  TWELL_KV_INT8 = 1   /* codes are int8 in [-127, 127] */
+};
+
+/* A paged cache of keys and values in 8 bits.  A key is code * k_scale of its
+ * page and head (a value likewise); twell_kv_append writes powers of two as
+ * scales, the attention takes any positive finite ones.  The struct lives in
+ * host memory; the pointers are device pointers to caller-owned memory. */
+typedef struct twell_kv_t {
+  int32_t n_pages;    /* >= 1 */
+  int32_t page_size;  /* tokens per page: 16, 32, 64 or 128 */
+  int32_t n_heads;    /* key / value heads, >= 1 */
+  int32_t head_dim;   /* 64 or 128 */
+  int32_t format;     /* TWELL_KV_E4M3 or TWELL_KV_INT8 */
+  int32_t reserved;   /* 0 */
+  uint8_t* k;         /* [n_pages][n_heads][page_size][head_dim] codes, 16-byte aligned */
+  uint8_t* v;         /* the same */
+  float* k_scale;     /* [n_pages][n_heads] */
+  float* v_scale;     /* the same */
+  int32_t* status;    /* device scalar, zero at first: the first TWELL_ERR_* code a kernel met */
+} twell_kv_t;
+
+/* Block tables and slot maps of one step, from the requests' lengths.
+ *   kv_lens     [n_requests] tokens each request has in the cache
+ *   new_tokens  [n_requests] tokens it adds in this step (>= 0), or a negative
+ *               number: the request is finished and gives its pages back
+ *   block_table [n_requests][max_blocks] in / out: new pages are entered, other
+ *               entries stay as they are
+ *   ring        [n_pages] in / out, pool [2] in, pool_out [2] out: the free
+ *               pages are ring[(pool[0] + i) mod n_pages], i < pool[1].  New
+ *               pages are taken from the front, requests in order; the pages
+ *               given back go behind the last free one, requests in order, and
+ *               can be taken from the next step on.
+ *   kv_lens_out [n_requests] lengths after the step (0 for a finished request)
+ *   cu_q        [n_requests + 1] prefix sums of max(new_tokens, 0), at most n_tokens
+ *   slots       [n_tokens] slot of each token, -1 where there is none
+ *   positions   [n_tokens] position of each token, -1 where there is none
+ *   n_tokens    size of slots and positions: the step's tokens, or more (a
+ *               batch padded to a fixed size)
+ *   status      0, or TWELL_ERR_CACHE_FULL when a request was refused: it wants
+ *               pages but the requests up to it want more than are free (counting the
+ *               refused ones), or more blocks than max_blocks, or its tokens
+ *               end past n_tokens.  A refused request keeps its length and
+ *               takes no page; its tokens have slot and position -1, which
+ *               twell_kv_append skips and twell_kv_attention answers with zeros.
+ * Nothing that is read is overwritten (kv_lens and kv_lens_out, pool and
+ * pool_out are different buffers), so the call can be repeated with the same
+ * result.  n_requests <= 16384.  One launch. */
+TWELL_API int twell_kv_plan(const int32_t* kv_lens, const int32_t* new_tokens, int32_t n_requests, int32_t page_size,
+                            int32_t n_pages, int32_t max_blocks, int32_t* block_table, int32_t* ring,
+                            const int32_t* pool, int32_t* pool_out, int32_t* kv_lens_out, int32_t* cu_q,
+                            int64_t* slots, int32_t* positions, int32_t n_tokens, int32_t* status,
+                            twell_stream_t stream);
+
+/* Writes the step's keys and values into the cache.
+ *   K, V   token t's head h at K + t * ldk + h * head_dim (bf16), ldk >=
+ *          n_heads * head_dim, a multiple of 8, 16-byte aligned
+ *   cu_q   [n_requests + 1], slots [n_tokens] as from twell_kv_plan: a request's
+ *          slots are consecutive positions of its pages; a request whose first slot
+ *          is -1 is skipped
+ * For every page and head that gets tokens, with a = the largest magnitude of
+ * the new ones and q = 448 (e4m3) or 127 (int8):
+ *   s = 2^e with the least e >= -100 such that a <= q 2^e; where the page holds
+ *   earlier tokens (its first new token is not its first token), s is at least
+ *   the page's scale, and if that made it larger the earlier codes c are
+ *   replaced by round(c * old / s);
+ *   new codes are round(x / s), both to nearest even.
+ * Powers of two make every quotient exact, so the codes do not depend on how
+ * it is computed; e4m3 codes move to a larger scale unchanged unless they get
+ * below 2^-6.  An infinity counts as the largest finite bf16 of its sign and a NaN
+ * as 0; cache->status then reports TWELL_ERR_NOT_FINITE.  A slot outside the
+ * cache is skipped with TWELL_ERR_BAD_FORMAT.  Two requests never share a
+ * page that gets tokens. */
+TWELL_API int twell_kv_append(const uint16_t* K, int64_t ldk, const uint16_t* V, int64_t ldv, const int32_t* cu_q,
+                              const int64_t* slots, int32_t n_tokens, int32_t n_requests, const twell_kv_t* cache,
+                              twell_stream_t stream);
+
+/* Attention over the cache.  Query head h reads key / value head
+ * h / (n_q_heads / n_heads).  Token t of request r sees the positions below
+ *   L = min(positions[t] + 1, kv_lens[r], max_blocks * page_size)
+ *   x_j = softmax_scale * (q . k_j),  o = sum_j softmax(x)_j v_j,  lse = log sum_j exp(x_j)
+ * A row that sees nothing (L <= 0: an empty request, a refused one, a token past
+ * cu_q[n_requests]) has o = 0 and lse = -inf.
+ *   Q, O   token t's head h at Q + t * ldq + h * head_dim (bf16), ldq and ldo as ldk
+ *          above; lse [n_tokens][n_q_heads] fp32 or null
+ *   n_q_heads  a multiple of cache->n_heads
+ *   max_kv_len, max_q_len  bounds the caller knows on kv_lens and on a
+ *          request's tokens (>= 0).  They choose launch shapes only: the results hold
+ *          when a bound is exceeded.
+ * The cache's codes enter the tensor cores exactly (as fp16, which holds every
+ * e4m3 and int8 value); q enters as fp16 scaled by a power of two per row
+ * (exact for components above 2^-13 of the row's largest); probabilities are rounded to fp16,
+ * every sum and the softmax's statistics are fp32.  Long caches are split
+ * over the GPU and joined in a fixed order: the same call gives the same bits.
+ * workspace: device, >= twell_kv_attention_workspace_bytes(...) bytes, 256-byte
+ * aligned, contents need no initialisation.  A page number outside the cache
+ * reads page 0 and reports TWELL_ERR_BAD_FORMAT in cache->status.
+ * n_requests <= 4096. */
+TWELL_API int twell_kv_attention(const uint16_t* Q, int64_t ldq, const twell_kv_t* cache, const int32_t* block_table,
+                                 int32_t max_blocks, const int32_t* cu_q, const int32_t* positions,
+                                 const int32_t* kv_lens, int32_t n_tokens, int32_t n_requests, int32_t n_q_heads,
+                                 int32_t max_kv_len, int32_t max_q_len, float softmax_scale, uint16_t* O, int64_t ldo,
+                                 float* lse, void* workspace, size_t workspace_bytes, twell_stream_t stream);
+
+/* Host arithmetic only (0 for arguments the call would refuse). */
+TWELL_API size_t twell_kv_attention_workspace_bytes(int32_t n_tokens, int32_t n_requests, int32_t n_q_heads,
+                                                    int32_t n_kv_heads, int32_t head_dim);
+
+/* Synchronises `stream`, then returns *cache->status. */
+TWELL_API int twell_kv_read_status(const twell_kv_t* cache, twell_stream_t stream);
+
+enum { TWELL_BF16 = 0, TWELL_F32 = 1 };
+
+/* Log probabilities of given tokens, with the entropy and the best alternatives.
+ * With x = logits * inv_temperature (fp32) and p = softmax(x) for each row:
+ *   lse = log sum_j exp(x_j)       logprob = x_target - lse (0 where the target
+ *   entropy = -sum_j p_j log p_j             is outside [0, vocab): no target)
+ *   top_logprob, top_index: x - lse and index of the top_k largest x, in
+ *   descending order, equal ones by ascending index
+ * logits: [n_rows] rows of vocab values of type dtype (TWELL_BF16 / TWELL_F32),
+ * ld >= vocab elements apart (any ld; the base 16-byte aligned).  -inf is a
+ * masked token (p = 0).  A row of -inf only: lse = -inf, logprob of a target
+ * -inf, entropy 0, top_logprob -inf with the lowest indices.  A row with a NaN
+ * or +inf: everything NaN, top_index -1.  targets with logprob, entropy and lse
+ * may be null when not wanted; top_k = 0 leaves the alternatives out.
+ * 0 <= top_k <= min(32, vocab).  1 <= vocab <= 400000.  inv_temperature > 0. */
+TWELL_API int twell_logprobs(const void* logits, int32_t dtype, int64_t ld, int32_t n_rows, int32_t vocab,
+                             const int32_t* targets, float inv_temperature, float* logprob, float* entropy,
+                             float* lse, int32_t top_k, float* top_logprob, int32_t* top_index,
+                             twell_stream_t stream);
+
+/* Gradient of twell_logprobs with respect to the logits, from what that call
+ * left (lse, entropy) and the upstream gradients of logprob and entropy:
+ *   d_logits_j = inv_temperature * (d_logprob (1[j = target] - p_j)
+ *                                   - d_entropy p_j (log p_j + entropy))
+ * A row without a target takes d_logprob as 0; p_j = 0 gives 0; a row of -inf
+ * only gives zeros.  d_logits: type dtype, ldd >= vocab apart, base 16-byte
+ * aligned; it may be the logits themselves (with ldd == ld).  targets with
+ * d_logprob, or entropy with d_entropy, may be null: that term is left out. */
+TWELL_API int twell_logprobs_bwd(const void* logits, int32_t dtype, int64_t ld, int32_t n_rows, int32_t vocab,
+                                 const int32_t* targets, float inv_temperature, const float* lse,
+                                 const float* entropy, const float* d_logprob, const float* d_entropy,
+                                 void* d_logits, int64_t ldd, twell_stream_t stream);
+
 /* Synchronises `stream`, then returns *layout->status if non-zero, else
  * TWELL_ERR_FALLBACK_OVERFLOW when *layout->n_fb exceeds the capacity (fb_cap
  * rows, or fb_cap * d_ff / tile dense tiles for the tile-granular variant),
@@ -399,7 +562,13 @@ enum {
   TWELL_KERNEL_AUX = 12,         /* small helpers (clears, transposed indexes) */
   TWELL_KERNEL_DW_FALLBACK = 13, /* backward: the fallback rows' dW_down, dW_inT, db share */
   TWELL_KERNEL_DX_FALLBACK = 14, /* backward: the fallback rows' dX */
-  TWELL_KERNEL_COUNT = 15
+  TWELL_KERNEL_KV_PLAN = 15,     /* block tables and slot maps of a step */
+  TWELL_KERNEL_KV_APPEND = 16,   /* keys and values into the 8-bit cache */
+  TWELL_KERNEL_KV_ATTENTION = 17, /* attention over the cache */
+  TWELL_KERNEL_KV_JOIN = 18,     /* join of the split caches' partial results */
+  TWELL_KERNEL_LOGPROBS = 19,    /* log probabilities, entropy, best alternatives */
+  TWELL_KERNEL_LOGPROBS_BWD = 20, /* their gradient */
+  TWELL_KERNEL_COUNT = 21
 };
 TWELL_API int twell_profile_enable(int on);
 TWELL_API int twell_profile_reset(void);
