@@ -52,11 +52,15 @@ __device__ __forceinline__ int blocks_of(int64_t tokens, int page) {
   return static_cast<int>((tokens + page - 1) / page);
 }
 
-// What one request asks for.
+// What one request asks for.  One that wants more blocks than its table has
+// is refused whatever is free, so it asks for no pages.  Of the others, once
+// the running sum passes the free pages (or the tokens' capacity) every later
+// one with a need is refused too: the accepted ones' pages are one run.
 __device__ __forceinline__ Sums asks(const PlanArgs& a, int len, int add) {
   const int have = blocks_of(len, a.page);
   if (add < 0) return {0, 0, min(have, a.max_blocks)};
-  return {add, blocks_of(static_cast<int64_t>(len) + add, a.page) - have, 0};
+  const int upto = blocks_of(static_cast<int64_t>(len) + add, a.page);
+  return {add, upto > a.max_blocks ? 0 : upto - have, 0};
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
@@ -100,7 +104,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     const int len = max(a.kv_lens[r], 0), add = a.new_tokens[r];
     const Sums s = asks(a, len, add), upto = run + s;
     const bool no = add > 0 && ((s.need > 0 && upto.need > free_pages) ||
-                                blocks_of(len, a.page) + s.need > a.max_blocks || upto.tokens > cap);
+                                blocks_of(static_cast<int64_t>(len) + add, a.page) > a.max_blocks ||
+                                upto.tokens > cap);
     cu[r] = static_cast<int32_t>(min(run.tokens, static_cast<int64_t>(cap)));
     base[r] = add < 0 ? -2 - static_cast<int>(run.back) : no ? -1 : static_cast<int>(run.need);
     if (!no && s.need > 0) taken = static_cast<int>(upto.need);

@@ -259,7 +259,8 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
     E::unpack(chunks[j], x);
 #pragma unroll
     for (int i = 0; i < E::kVec; ++i) {
-      const float d = fmaf(x[i], a.inv_temperature, -m);
+      // the product rounded as m's was: fused, a row of -1e30 would be far from its own maximum
+      const float d = __fmul_rn(x[i], a.inv_temperature) - m;
       const float e = ex2(d * kLog2e);
       s += e;
       u = fmaf(e, fmaxf(d, -1000.0f), u);  // a masked token adds 0, not 0 * inf
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_bwd_kernel(const BwdArgs 
   const bool empty = lse == -INFINITY;
   target -= beg;
   const auto grad = [&](float x, int at) {
-    const float logp = fmaf(x, inv_t, -lse);
+    const float logp = __fmul_rn(x, inv_t) - lse;
     const float p = ex2(logp * kLog2e);
     float d = p == 0.0f ? 0.0f : -p * fmaf(gh, logp, base);
     if (at == target) d += g;

@@ -389,10 +389,10 @@ typedef struct twell_kv_t {
  *   positions   [n_tokens] position of each token, -1 where there is none
  *   n_tokens    size of slots and positions: the step's tokens, or more (a
  *               batch padded to a fixed size)
- *   status      0, or TWELL_ERR_CACHE_FULL when a request was refused: it wants
- *               pages but the requests up to it want more than are free (counting the
- *               refused ones), or more blocks than max_blocks, or its tokens
- *               end past n_tokens.  A refused request keeps its length and
+ *   status      0, or TWELL_ERR_CACHE_FULL when a request was refused: it needs
+ *               more blocks than max_blocks; or it wants pages and the requests up to
+ *               it (those of too many blocks left out) want more than are free; or
+ *               its tokens end past n_tokens.  A refused request keeps its length and
  *               takes no page; its tokens have slot and position -1, which
  *               twell_kv_append skips and twell_kv_attention answers with zeros.
  * Nothing that is read is overwritten (kv_lens and kv_lens_out, pool and
