@@ -19,6 +19,8 @@
 // match; V's lanes take the same 16 (D = 128) or 8 bytes of four tokens, whose
 // bytes are paired to fp16 registers, and the output columns come out in runs.
 // No transposition and no shared memory lies between the cache and the mma.
+#include <algorithm>
+
 #include "kv_internal.h"
 
 namespace twell {
@@ -224,6 +226,24 @@ __device__ __forceinline__ void step16(TileState<D>& s, const uint32_t (&qa)[D /
   }
 }
 
+// Eight dims of one finished row: o 2^(n - m) / sum, rounded once, and the row's lse.
+template <int D>
+__device__ __forceinline__ void store_row(const AttArgs& a, int t0, int row, int head, int d0, float m, float n,
+                                          float sum, const float (&o)[8]) {
+  const float f = m > -INFINITY ? exp2_fast(n - m) / sum : 0.0f;
+  const int64_t token = t0 + row / a.group;
+  const int h = head * a.group + row % a.group;
+  uint32_t out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    out[i] = static_cast<uint32_t>(float_to_bf16_bits(o[2 * i] * f)) |
+             (static_cast<uint32_t>(float_to_bf16_bits(o[2 * i + 1] * f)) << 16);
+  *reinterpret_cast<uint4*>(a.o + token * a.ldo + static_cast<int64_t>(h) * D + d0) =
+      make_uint4(out[0], out[1], out[2], out[3]);
+  if (a.lse && d0 == 0)
+    a.lse[token * a.q_heads + h] = m > -INFINITY ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
 template <int D>
 __device__ __forceinline__ void zero_row(const AttArgs& a, int64_t t, int tid, int n_threads) {
   for (int i = tid; i < a.q_heads * (D / 8); i += n_threads)
@@ -232,150 +252,452 @@ __device__ __forceinline__ void zero_row(const AttArgs& a, int64_t t, int tid, i
     for (int i = tid; i < a.q_heads; i += n_threads) a.lse[t * a.q_heads + i] = -INFINITY;
 }
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(kAttThreads) attention_kernel(const AttArgs a) {
-  __shared__ float sh_o[kAttWarps][kAttRows][D + 4];
-  __shared__ float sh_m[kAttWarps][kAttRows], sh_n[kAttWarps][kAttRows], sh_sum[kAttWarps][kAttRows];
-  grid_dependency_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, quad = lane & 3;
-  const int head = blockIdx.y;
-  // row blocks: request r has room for floor(cu[r + 1] G / 16) - floor(cu[r] G / 16) + 1
-  const int64_t x = blockIdx.x;
-  const auto first_block = [&](int i) {
-    return static_cast<int64_t>(min(max(a.cu_q[i], 0), a.n_tokens)) * a.group / kAttRows + i;
-  };
-  const int r = warp_upper(a.n_requests, x, first_block);
+// ------------------------------------------------------------ work split
+// A segment is one tile of 16 rows of one key head with all its cached tokens,
+// in units of 64 of them.  The segments of all requests, laid end to end, are
+// cut into as many equal pieces as CTAs run, so the lengths of the requests
+// do not matter for the balance.  A piece's cut segments leave partial results in the
+// workspace (two a CTA: of the segment it starts in the middle of, and of the
+// one it ends in the middle of), which join_kernel adds in order.
+constexpr int kUnit = kAttGroup * kAttWarps;  // cached tokens of a unit: 16 a warp
+constexpr int kMaxCtas = 608;
+// Segments of up to this many units are never cut: their join would cost more
+// than the imbalance of leaving them whole.
+constexpr int kWholeUnits = 4;
+// Whole segments of up to this many units (512 tokens) go to single warps.
+constexpr int kWarpUnits = 8;
+
+struct Piece {   // of a segment that goes on in the next CTA, for join_kernel
+  int32_t t0, n_rows, row0, head, last_cta, pad[3];
+};
+
+template <int D>
+constexpr size_t partial_floats() { return static_cast<size_t>(kAttRows) * (D + 4); }
+
+__device__ __forceinline__ int visible_len(const AttArgs& a, int r) {
+  const int64_t room = static_cast<int64_t>(a.max_blocks) << a.page_shift;
+  return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(a.kv_lens[r]), room)));
+}
+
+struct Request {
+  int t0, n_rows, len;
+};
+
+__device__ __forceinline__ Request request(const AttArgs& a, int r) {
   const int t0 = min(max(a.cu_q[r], 0), a.n_tokens), t1 = min(max(a.cu_q[r + 1], t0), a.n_tokens);
-  const int n_rows = (t1 - t0) * a.group, row0 = static_cast<int>(x - first_block(r)) * kAttRows;
-  if (row0 >= n_rows) return;
-  const int len = min(a.kv_lens[r], static_cast<int>(min(static_cast<int64_t>(a.max_blocks) << a.page_shift,
-                                                         static_cast<int64_t>(INT32_MAX))));
-  // what each row sees; rows past the last see everything and are not stored
-  int limit[2], most = 0, least = INT32_MAX;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int row = row0 + g + 8 * half;
-    limit[half] = INT32_MAX;
-    if (row < n_rows) {
-      const int pos = a.positions[t0 + row / a.group];
-      limit[half] = max(0, min(pos < INT32_MAX ? pos + 1 : pos, len));
-      most = max(most, limit[half]);
-      least = min(least, limit[half]);
-    }
+  return {t0, (t1 - t0) * a.group, visible_len(a, r)};
+}
+
+__device__ __forceinline__ int units_of(const Request& q) { return (q.len + kUnit - 1) / kUnit; }
+__device__ __forceinline__ int row_blocks_of(const Request& q) { return (q.n_rows + kAttRows - 1) / kAttRows; }
+
+// start[r] = units of the requests before r, start[n_requests] = all; by the whole CTA.
+__device__ __forceinline__ void scan_requests(const AttArgs& a, int64_t* start, int64_t* warp_sum) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.n_requests + kAttThreads - 1) / kAttThreads;
+  const int r0 = min(a.n_requests, tid * per), r1 = min(a.n_requests, r0 + per);
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    const Request q = request(a, r);
+    const int64_t w = static_cast<int64_t>(units_of(q)) * row_blocks_of(q) * a.heads;
+    start[r] = w;
+    mine += w;
   }
+  int64_t inc = mine;
 #pragma unroll
-  for (int d = 16; d >= 4; d /= 2) {
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-    least = min(least, __shfl_xor_sync(0xffffffffu, least, d));
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += o;
   }
-  uint32_t qa[D / 16][4];
-  float factor[2];
-  load_q<D>(a, t0, n_rows, row0, head, qa, factor);
-  TileState<D> s;
-  reset(s);
-  const int page_mask = (1 << a.page_shift) - 1;
-  for (int j0 = warp * kAttGroup; j0 < most; j0 += kAttWarps * kAttGroup) {
-    int page = a.block_table[static_cast<int64_t>(r) * a.max_blocks + (j0 >> a.page_shift)];
-    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.n_pages)) {
-      if (lane == 0) report_error(a.status, TWELL_ERR_BAD_FORMAT);
-      page = 0;
-    }
-    const int64_t cell = static_cast<int64_t>(page) * a.heads + head;
-    const int64_t at = ((cell << a.page_shift) + (j0 & page_mask)) * D;
-    const float ks = a.k_scale[cell], vs = a.v_scale[cell];
-    uint32_t kw[2][D / 16], vw[4][D / 32];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i)
-        *reinterpret_cast<uint4*>(&kw[nt][4 * i]) =
-            __ldg(reinterpret_cast<const uint4*>(a.k + at + (nt * 8 + g) * D + 64 * i + 16 * quad));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int token = (i >> 1) * 8 + 2 * quad + (i & 1);
-      const uint8_t* src = a.v + at + token * D + (D / 8) * g;
-      // a token nobody sees may hold anything, and 0 * NaN is not 0
-      const bool seen = j0 + token < most;
-      if constexpr (D == 128) {
-        *reinterpret_cast<uint4*>(vw[i]) =
-            seen ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
-      } else {
-        *reinterpret_cast<uint2*>(vw[i]) = seen ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0, 0);
-      }
-    }
-    step16<FMT, D>(s, qa, factor, kw, vw, ks, vs, j0, limit, j0 + kAttGroup > least);
-  }
-  // the four warps' results of the tile, joined in warp order
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    s.sum[half] += __shfl_xor_sync(0xffffffffu, s.sum[half], 1);
-    s.sum[half] += __shfl_xor_sync(0xffffffffu, s.sum[half], 2);
-    const int row = g + 8 * half;
-    if (quad == 0) {
-      sh_m[warp][row] = s.m[half];
-      sh_n[warp][row] = s.n[half];
-      sh_sum[warp][row] = s.sum[half];
-    }
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      sh_o[warp][row][(D / 8) * (2 * quad) + i] = s.acc[i][2 * half];
-      sh_o[warp][row][(D / 8) * (2 * quad + 1) + i] = s.acc[i][2 * half + 1];
-    }
-  }
+  if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
-  constexpr int kLanes = D / 8;
-  for (int row = tid / kLanes; row < min(kAttRows, n_rows - row0); row += kAttThreads / kLanes) {
-    const int d0 = (tid % kLanes) * 8;
-    float m = -INFINITY, n = -INFINITY;
+  int64_t run = inc - mine, all = 0;
 #pragma unroll
-    for (int w = 0; w < kAttWarps; ++w) {
-      m = fmaxf(m, sh_m[w][row]);
-      n = fmaxf(n, sh_n[w][row]);
-    }
-    float sum = 0.0f, o[8] = {};
-    if (m > -INFINITY) {
-#pragma unroll
-      for (int w = 0; w < kAttWarps; ++w) {
-        sum += sh_sum[w][row] * exp2_fast(sh_m[w][row] - m);
-        const float f = exp2_fast(sh_n[w][row] - n);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += sh_o[w][row][d0 + i] * f;
-      }
-    }
-    const float f = m > -INFINITY ? exp2_fast(n - m) / sum : 0.0f;
-    const int grow = row0 + row, token = grow / a.group, h = head * a.group + grow % a.group;
-    uint32_t out[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      out[i] = static_cast<uint32_t>(float_to_bf16_bits(o[2 * i] * f)) |
-               (static_cast<uint32_t>(float_to_bf16_bits(o[2 * i + 1] * f)) << 16);
-    *reinterpret_cast<uint4*>(a.o + (t0 + token) * a.ldo + static_cast<int64_t>(h) * D + d0) =
-        make_uint4(out[0], out[1], out[2], out[3]);
-    if (a.lse && d0 == 0)
-      a.lse[static_cast<int64_t>(t0 + token) * a.q_heads + h] =
-          m > -INFINITY ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+  for (int w = 0; w < kAttWarps; ++w) {
+    if (w < warp) run += warp_sum[w];
+    all += warp_sum[w];
   }
+  for (int r = r0; r < r1; ++r) {
+    const int64_t w = start[r];
+    start[r] = run;
+    run += w;
+  }
+  if (tid == 0) start[a.n_requests] = all;
+  __syncthreads();
+}
+
+// The last request that starts at or before unit u and has units.
+__device__ __forceinline__ int request_at(const int64_t* start, int n, int64_t u) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (start[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Cut b of n_cuts over all units: moved to its segment's start where the segment stays whole.
+__device__ __forceinline__ int64_t cut_at(const AttArgs& a, const int64_t* start, int64_t b, int64_t n_cuts,
+                                          bool whole) {
+  const int64_t all = start[a.n_requests];
+  const int64_t u = b * all / n_cuts;
+  if (b == 0 || u >= all) return b == 0 ? 0 : all;
+  const int r = request_at(start, a.n_requests, u);
+  const int units = units_of(request(a, r));
+  const int64_t in = (u - start[r]) % units;
+  return whole || units <= kWholeUnits ? u - in : u;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kAttThreads) attention_rest_kernel(const AttArgs a) {
-  grid_dependency_wait();
-  // tokens of no request
-  const int beg = min(max(a.cu_q[a.n_requests], 0), a.n_tokens);
-  for (int t = beg + blockIdx.x; t < a.n_tokens; t += gridDim.x) zero_row<D>(a, t, threadIdx.x, kAttThreads);
+struct Ring {
+  static constexpr int kStages = 4;
+  static constexpr int kK = kAttGroup * D, kStage = 2 * kK + 16;  // bytes: keys, values, two scales
+  static constexpr int kWarp = kStages * kStage;
+  static_assert(kWarp >= static_cast<int>(partial_floats<D>() * 4), "a warp's results take the ring's place");
+};
+
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool on) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(kBytes),
+                 "r"(on ? kBytes : 0)
+                 : "memory");
+}
+
+// One warp's way through the segments seg, seg + 4, ... < seg_end of a request
+// (row blocks of a head, then the next head): n_steps steps of 16 cached
+// tokens each, j_stride tokens apart from j_first on.
+struct Stream {
+  const int32_t* table;
+  int len, j_first, j_stride, n_steps, seg, seg_end, blocks;
+};
+
+// The copies run kStages - 1 steps ahead of the arithmetic, over the ends of
+// segments too.  Several segments need n_steps <= 32 (their page numbers stay
+// in one register a lane).
+template <int FMT, int D, typename Emit>
+__device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, const Request& q, uint8_t* ring,
+                                           Emit emit) {
+  using R = Ring<D>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
+  const int page_mask = (1 << a.page_shift) - 1;
+  // page numbers of 32 steps at a time, one a lane, and the next 32 behind them
+  const auto pages_from = [&](int step) {
+    int page = 0;
+    if (step + lane < st.n_steps) {
+      page = st.table[(st.j_first + (step + lane) * st.j_stride) >> a.page_shift];
+      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.n_pages)) {
+        report_error(a.status, TWELL_ERR_BAD_FORMAT);
+        page = 0;
+      }
+    }
+    return page;
+  };
+  int pages = 0, pages_next = 0;
+  if (st.seg < st.seg_end) {
+    pages = pages_from(0);
+    if (st.n_steps > 32) pages_next = pages_from(32);
+  }
+  int f_seg = st.seg, f_step = 0, f_slot = 0;  // the next copy
+  const auto fetch = [&]() {
+    if (f_seg < st.seg_end && st.n_steps > 0) {
+      if (f_step > 0 && (f_step & 31) == 0) {
+        pages = pages_next;
+        if (f_step + 32 < st.n_steps) pages_next = pages_from(f_step + 32);
+      }
+      const int page = __shfl_sync(0xffffffffu, pages, f_step & 31);
+      uint8_t* const stage = ring + f_slot * R::kStage;
+      const int j0 = st.j_first + f_step * st.j_stride;
+      const int64_t cell = static_cast<int64_t>(page) * a.heads + f_seg / st.blocks;
+      const int64_t at = ((cell << a.page_shift) + (j0 & page_mask)) * D;
+      // lane l's bytes of each load lie together: it reads back what it copied
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+          copy_async<16>(stage + ((nt * (D / 64) + i) * 32 + lane) * 16,
+                         a.k + at + (nt * 8 + g) * D + 64 * i + 16 * quad, true);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int token = (i >> 1) * 8 + 2 * quad + (i & 1);
+        // past the request's tokens the page may hold anything, and 0 * NaN is
+        // not 0: zeros in its place
+        copy_async<D / 8>(stage + R::kK + (i * 32 + lane) * (D / 8), a.v + at + token * D + (D / 8) * g,
+                          j0 + token < st.len);
+      }
+      if (lane < 2) copy_async<4>(stage + 2 * R::kK + 4 * lane, (lane == 0 ? a.k_scale : a.v_scale) + cell, true);
+      if (++f_step == st.n_steps) f_step = 0, f_seg += kAttWarps;
+    }
+    f_slot = f_slot + 1 == R::kStages ? 0 : f_slot + 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < R::kStages - 1; ++i) fetch();
+  int slot = 0;
+  for (int seg = st.seg; seg < st.seg_end; seg += kAttWarps) {
+    const int head = seg / st.blocks, row0 = seg % st.blocks * kAttRows;
+    // what each row sees; rows past the last see everything and are not stored
+    int limit[2], least = INT32_MAX;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int row = row0 + g + 8 * half;
+      limit[half] = INT32_MAX;
+      if (row < q.n_rows) {
+        const int p = a.positions[q.t0 + row / a.group];
+        limit[half] = max(0, min(p < INT32_MAX ? p + 1 : p, q.len));
+        least = min(least, limit[half]);
+      }
+    }
+#pragma unroll
+    for (int d = 16; d >= 4; d /= 2) least = min(least, __shfl_xor_sync(0xffffffffu, least, d));
+    least = min(least, st.len);
+    uint32_t qa[D / 16][4];
+    float factor[2];
+    load_q<D>(a, q.t0, q.n_rows, row0, head, qa, factor);
+    TileState<D> s;
+    reset(s);
+    for (int step = 0; step < st.n_steps; ++step) {
+      __syncwarp();  // the scales that fetch replaces have been read by all lanes
+      fetch();
+      asm volatile("cp.async.wait_group %0;" ::"n"(R::kStages - 1) : "memory");
+      __syncwarp();  // the scales came in by two lanes
+      const uint8_t* const stage = ring + slot * R::kStage;
+      slot = slot + 1 == R::kStages ? 0 : slot + 1;
+      const int j0 = st.j_first + step * st.j_stride;
+      uint32_t kw[2][D / 16], vw[4][D / 32];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+          *reinterpret_cast<uint4*>(&kw[nt][4 * i]) =
+              *reinterpret_cast<const uint4*>(stage + ((nt * (D / 64) + i) * 32 + lane) * 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* src = stage + R::kK + (i * 32 + lane) * (D / 8);
+        if constexpr (D == 128)
+          *reinterpret_cast<uint4*>(vw[i]) = *reinterpret_cast<const uint4*>(src);
+        else
+          *reinterpret_cast<uint2*>(vw[i]) = *reinterpret_cast<const uint2*>(src);
+      }
+      const float2 scales = *reinterpret_cast<const float2*>(stage + 2 * R::kK);
+      step16<FMT, D>(s, qa, factor, kw, vw, scales.x, scales.y, j0, limit, j0 + kAttGroup > least);
+    }
+    if (seg + kAttWarps >= st.seg_end) asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      s.sum[half] += __shfl_xor_sync(0xffffffffu, s.sum[half], 1);
+      s.sum[half] += __shfl_xor_sync(0xffffffffu, s.sum[half], 2);
+    }
+    emit(s, head, row0);
+  }
 }
 
 template <int FMT, int D>
-int launch_attention(const AttArgs& a, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.n_tokens) * a.group / kAttRows + a.n_requests),
-                  static_cast<unsigned>(a.heads));
-  if (a.n_requests > 0) {
-    LaunchScope scope(TWELL_KERNEL_KV_ATTENTION, s);
-    if (launch_pdl(attention_kernel<FMT, D>, grid, dim3(kAttThreads), 0, s, a) != cudaSuccess) return TWELL_ERR_CUDA;
+__global__ void __launch_bounds__(kAttThreads, 3)
+    attention_kernel(const AttArgs a, float* partial, Piece* pieces, int whole) {
+  using R = Ring<D>;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  uint8_t* const ring_all = dyn;
+  int64_t* const start = reinterpret_cast<int64_t*>(dyn + kAttWarps * R::kWarp);
+  __shared__ int64_t warp_sum[kAttWarps];
+  grid_dependency_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, quad = lane & 3;
+  uint8_t* const ring = ring_all + warp * R::kWarp;
+  scan_requests(a, start, warp_sum);
+  // at least a unit for each CTA that works, so that every CTA between a cut
+  // segment's first and last has a part of it
+  const int64_t cta = blockIdx.x, n_ctas = min(static_cast<int64_t>(gridDim.x), start[a.n_requests]);
+  const int64_t end = cta < n_ctas ? cut_at(a, start, cta + 1, n_ctas, whole) : 0;
+  int64_t pos = cta < n_ctas ? cut_at(a, start, cta, n_ctas, whole) : 0;
+  if (tid == 0) pieces[cta].last_cta = -1;
+  // requests without cached tokens, and tokens of no request
+  for (int r = blockIdx.x; r < a.n_requests; r += gridDim.x) {
+    const Request q = request(a, r);
+    if (q.len == 0)
+      for (int t = 0; t < q.n_rows / a.group; ++t) zero_row<D>(a, q.t0 + t, tid, kAttThreads);
   }
-  LaunchScope scope(TWELL_KERNEL_KV_ATTENTION, s);
-  return launch_pdl(attention_rest_kernel<D>, dim3(16), dim3(kAttThreads), 0, s, a) == cudaSuccess ? TWELL_OK
-                                                                                                   : TWELL_ERR_CUDA;
+  for (int t = min(max(a.cu_q[a.n_requests], 0), a.n_tokens) + blockIdx.x; t < a.n_tokens; t += gridDim.x)
+    zero_row<D>(a, t, tid, kAttThreads);
+
+  int turn = 0;  // of the warps at whole segments
+  while (pos < end) {
+    const int r = request_at(start, a.n_requests, pos);
+    const Request q = request(a, r);
+    const int units = units_of(q), blocks = row_blocks_of(q);
+    const int64_t seg0 = (pos - start[r]) / units;
+    const int unit0 = static_cast<int>((pos - start[r]) % units);
+    Stream st;
+    st.table = a.block_table + static_cast<int64_t>(r) * a.max_blocks;
+    st.len = q.len;
+    if (unit0 == 0 && units <= kWarpUnits && end - pos >= units) {
+      // short segments that lie whole in this piece: each warp takes every fourth
+      const int64_t left = static_cast<int64_t>(blocks) * a.heads - seg0;
+      const int count = static_cast<int>(min(left, (end - pos) / units));
+      st.j_first = 0;
+      st.j_stride = kAttGroup;
+      st.n_steps = (q.len + kAttGroup - 1) / kAttGroup;
+      st.seg = static_cast<int>(seg0) + ((warp - turn) & (kAttWarps - 1));
+      st.seg_end = static_cast<int>(seg0) + count;
+      st.blocks = blocks;
+      turn += count;
+      pos += static_cast<int64_t>(count) * units;
+      run_stream<FMT, D>(a, st, q, ring, [&](TileState<D>& s, int head, int row0) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int row = row0 + g + 8 * half;
+          if (row >= q.n_rows) continue;
+#pragma unroll
+          for (int i0 = 0; i0 < 2 * (D / 8); i0 += 8) {
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = s.acc[(i0 + i) % (D / 8)][2 * half + (i0 + i) / (D / 8)];
+            store_row<D>(a, q.t0, row, head, (D / 8) * 2 * quad + i0, s.m[half], s.n[half], s.sum[half], o);
+          }
+        }
+      });
+      continue;
+    }
+    const int n_units = static_cast<int>(min(static_cast<int64_t>(units - unit0), end - pos));
+    pos += n_units;
+    st.j_first = unit0 * kUnit + warp * kAttGroup;
+    st.j_stride = kUnit;
+    const int seen = min(n_units * kUnit, q.len - unit0 * kUnit) - warp * kAttGroup;
+    st.n_steps = seen > 0 ? (seen + kUnit - 1) / kUnit : 0;
+    st.seg = static_cast<int>(seg0);
+    st.seg_end = st.seg + 1;
+    st.blocks = blocks;
+    // the four warps' results of the tile, joined in warp order; they take the ring's place
+    run_stream<FMT, D>(a, st, q, ring, [&](TileState<D>& s, int, int row0) {
+      float* const mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int row = g + 8 * half;
+        if (row0 + row < q.n_rows) {
+          float* const at = mine + row * (D + 4);
+          if (quad == 0) at[D] = s.m[half], at[D + 1] = s.n[half], at[D + 2] = s.sum[half];
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            at[(D / 8) * (2 * quad) + i] = s.acc[i][2 * half];
+            at[(D / 8) * (2 * quad + 1) + i] = s.acc[i][2 * half + 1];
+          }
+        }
+      }
+    });
+    __syncthreads();
+    const int head = st.seg / blocks, row0 = st.seg % blocks * kAttRows;
+    constexpr int kLanes = D / 8;
+    const bool complete = n_units == units, goes_on = unit0 + n_units < units;
+    // a cut segment's part: slot 1 where it starts here, slot 0 where it came from the CTA before
+    float* const out = partial + (2 * cta + (unit0 == 0 ? 1 : 0)) * partial_floats<D>();
+    if (unit0 == 0 && goes_on && tid == 0) {
+      // cuts inside a segment that may be cut are where the even split puts
+      // them, so the CTA of its last unit follows from the split alone
+      const int64_t seg_end = pos + (units - n_units);
+      pieces[cta] = {q.t0, q.n_rows, row0, head,
+                     static_cast<int32_t>((seg_end * n_ctas - 1) / start[a.n_requests]), {0, 0, 0}};
+    }
+    for (int row = tid / kLanes; row < min(kAttRows, q.n_rows - row0); row += kAttThreads / kLanes) {
+      const int d0 = (tid % kLanes) * 8;
+      float m = -INFINITY, n = -INFINITY, sum = 0.0f, o[8] = {};
+#pragma unroll
+      for (int w = 0; w < kAttWarps; ++w) {
+        const float* at = reinterpret_cast<const float*>(ring_all + w * R::kWarp) + row * (D + 4);
+        m = fmaxf(m, at[D]);
+        n = fmaxf(n, at[D + 1]);
+      }
+      if (m > -INFINITY) {
+#pragma unroll
+        for (int w = 0; w < kAttWarps; ++w) {
+          const float* at = reinterpret_cast<const float*>(ring_all + w * R::kWarp) + row * (D + 4);
+          sum += at[D + 2] * exp2_fast(at[D] - m);
+          const float f = exp2_fast(at[D + 1] - n);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] += at[d0 + i] * f;
+        }
+      }
+      if (complete) {
+        store_row<D>(a, q.t0, row0 + row, head, d0, m, n, sum, o);
+      } else {
+        float* const to = out + row * (D + 4);
+        *reinterpret_cast<float4*>(to + d0) = make_float4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<float4*>(to + d0 + 4) = make_float4(o[4], o[5], o[6], o[7]);
+        if (d0 == 0) *reinterpret_cast<float4*>(to + D) = make_float4(m, n, sum, 0.0f);
+      }
+    }
+    __syncthreads();  // the ring is free again
+  }
+}
+
+// Adds a cut segment's parts in the order of its units: one CTA for each CTA
+// of attention_kernel, idle unless a segment starts there and goes on.
+template <int D>
+__global__ void __launch_bounds__(kAttThreads) join_kernel(const AttArgs a, const float* partial, const Piece* pieces) {
+  grid_dependency_wait();
+  const int cta = blockIdx.x, tid = threadIdx.x;
+  const Piece p = pieces[cta];
+  if (p.last_cta <= cta) return;
+  constexpr int kLanes = D / 8;
+  const int d0 = (tid % kLanes) * 8;
+  const auto part = [&](int c, int row) {
+    return partial + (2 * static_cast<int64_t>(c) + (c == cta ? 1 : 0)) * partial_floats<D>() + row * (D + 4);
+  };
+  for (int row = tid / kLanes; row < min(kAttRows, p.n_rows - p.row0); row += kAttThreads / kLanes) {
+    float m = -INFINITY, n = -INFINITY, sum = 0.0f, o[8] = {};
+#pragma unroll 4
+    for (int c = cta; c <= p.last_cta; ++c) {
+      const float* const at = part(c, row);
+      m = fmaxf(m, at[D]);
+      n = fmaxf(n, at[D + 1]);
+    }
+    if (m > -INFINITY) {
+#pragma unroll 4
+      for (int c = cta; c <= p.last_cta; ++c) {
+        const float* const at = part(c, row);
+        const float4 st = *reinterpret_cast<const float4*>(at + D), lo = *reinterpret_cast<const float4*>(at + d0),
+                     hi = *reinterpret_cast<const float4*>(at + d0 + 4);
+        sum += st.z * exp2_fast(st.x - m);
+        const float f = exp2_fast(st.y - n);
+        o[0] += lo.x * f, o[1] += lo.y * f, o[2] += lo.z * f, o[3] += lo.w * f;
+        o[4] += hi.x * f, o[5] += hi.y * f, o[6] += hi.z * f, o[7] += hi.w * f;
+      }
+    }
+    store_row<D>(a, p.t0, p.row0 + row, p.head, d0, m, n, sum, o);
+  }
+}
+
+template <int FMT, int D>
+int launch_attention(const AttArgs& a, int max_kv_len, int max_q_len, void* workspace, cudaStream_t s) {
+  float* const partial = static_cast<float*>(workspace);
+  Piece* const pieces = reinterpret_cast<Piece*>(partial + 2 * kMaxCtas * partial_floats<D>());
+  const size_t smem = kAttWarps * Ring<D>::kWarp + sizeof(int64_t) * (static_cast<size_t>(a.n_requests) + 1);
+  const void* fn = reinterpret_cast<const void*>(attention_kernel<FMT, D>);
+  KV_TRY(set_max_dynamic_smem(fn, static_cast<int>(kAttWarps * Ring<D>::kWarp + 8 * (kAttMaxRequests + 1))));
+  const int resident = resident_ctas_per_sm(fn, kAttThreads, smem);
+  if (resident < 1) return TWELL_ERR_CUDA;
+  // no more CTAs than the units that the caller's bounds allow
+  const int64_t blocks = (static_cast<int64_t>(max_q_len) * a.group + kAttRows - 1) / kAttRows;
+  const int64_t units = (static_cast<int64_t>(max_kv_len) + kUnit - 1) / kUnit;
+  const int64_t most = std::max<int64_t>(1, a.n_requests * a.heads * std::max<int64_t>(1, blocks * units));
+  const int ctas = static_cast<int>(
+      std::min<int64_t>(most, std::min(kMaxCtas, sm_count() * resident)));
+  const bool whole = units <= kWholeUnits;
+  {
+    LaunchScope scope(TWELL_KERNEL_KV_ATTENTION, s);
+    if (launch_pdl(attention_kernel<FMT, D>, dim3(ctas), dim3(kAttThreads), smem, s, a, partial, pieces,
+                   static_cast<int>(whole)) != cudaSuccess)
+      return TWELL_ERR_CUDA;
+  }
+  if (whole || ctas == 1) return TWELL_OK;
+  LaunchScope scope(TWELL_KERNEL_KV_JOIN, s);
+  return launch_pdl(join_kernel<D>, dim3(ctas - 1), dim3(kAttThreads), 0, s, a, static_cast<const float*>(partial),
+                    static_cast<const Piece*>(pieces)) == cudaSuccess
+             ? TWELL_OK
+             : TWELL_ERR_CUDA;
 }
 
 }  // namespace
@@ -389,7 +711,8 @@ extern "C" TWELL_API size_t twell_kv_attention_workspace_bytes(int32_t n_tokens,
   if (n_tokens < 0 || n_requests < 0 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads != 0 ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  return 256;
+  return (2 * kMaxCtas * static_cast<size_t>(kAttRows) * (head_dim + 4) * sizeof(float) + kMaxCtas * sizeof(Piece) + 255) /
+         256 * 256;
 }
 
 extern "C" TWELL_API int twell_kv_attention(const uint16_t* Q, int64_t ldq, const twell_kv_t* cache,
@@ -449,7 +772,7 @@ extern "C" TWELL_API int twell_kv_attention(const uint16_t* Q, int64_t ldq, cons
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cache->format == TWELL_KV_E4M3)
-    return cache->head_dim == 64 ? launch_attention<TWELL_KV_E4M3, 64>(a, s)
-                                 : launch_attention<TWELL_KV_E4M3, 128>(a, s);
-  return cache->head_dim == 64 ? launch_attention<TWELL_KV_INT8, 64>(a, s) : launch_attention<TWELL_KV_INT8, 128>(a, s);
+    return cache->head_dim == 64 ? launch_attention<TWELL_KV_E4M3, 64>(a, max_kv_len, max_q_len, workspace, s)
+                                 : launch_attention<TWELL_KV_E4M3, 128>(a, max_kv_len, max_q_len, workspace, s);
+  return cache->head_dim == 64 ? launch_attention<TWELL_KV_INT8, 64>(a, max_kv_len, max_q_len, workspace, s) : launch_attention<TWELL_KV_INT8, 128>(a, max_kv_len, max_q_len, workspace, s);
 }
