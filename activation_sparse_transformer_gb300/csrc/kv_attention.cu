@@ -13,12 +13,16 @@
 // largest l + log2 s_v, both per row, so that neither the sum of p nor the
 // fp16 weights leave their range whatever the pages' scales are.
 //
-// The reduction index of an mma may be permuted as long as both operands
-// agree, and so may the columns of its result.  K's lanes therefore take 16
-// consecutive bytes of one token (two loads for D = 128) and Q is gathered to
-// match; V's lanes take the same 16 (D = 128) or 8 bytes of four tokens, whose
-// bytes are paired to fp16 registers, and the output columns come out in runs.
-// No transposition and no shared memory lies between the cache and the mma.
+// The products are computed transposed, S^T = K Q^T and O^T = V^T P^T, with the
+// cached tokens (or the dims) on the 16-wide side of the mma and the rows on the
+// 8-wide one: a decode step has 1 to 8 rows for a key head, and half the mma's,
+// exponentials and registers of the other orientation.  The reduction index of an
+// mma may be permuted as long as both operands agree, and so may the rows of
+// its result.  K's lanes therefore take 16 consecutive bytes of one token (two
+// loads for D = 128) and Q is gathered to match; V's lanes take the same 16 (D =
+// 128) or 8 bytes of four tokens, whose bytes are paired to fp16 registers, and the output's
+// dims come out in runs.  No transposition lies between the cache and the mma;
+// P's 8 x 8 blocks are turned by movmatrix.
 #include <algorithm>
 
 #include "kv_internal.h"
@@ -28,8 +32,10 @@ namespace {
 
 constexpr int kAttWarps = 4;
 constexpr int kAttThreads = 32 * kAttWarps;
-constexpr int kAttRows = 16;    // rows of a tile
-constexpr int kAttGroup = 16;   // cached tokens of one warp step, all of one page
+constexpr int kMaxTiles = 2;    // a row block is 1 or 2 tiles of 8 rows
+constexpr int kMaxRows = 8 * kMaxTiles;
+constexpr int kAttGroup = 16;   // cached tokens of one mma, all of one page
+constexpr int kAttStep = 2 * kAttGroup;  // cached tokens of one warp step
 constexpr int kAttMaxRequests = 4096;
 // The references m and n are moved only when a new value passes them by this
 // much (as powers of two): weights up to 2^8 stay well inside fp16.
@@ -90,48 +96,65 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& p01, uint32_t
   }
 }
 
-// One tile's running state in a warp: rows g = lane / 4 and g + 8.
-template <int D>
+// One row block's running state in a warp: rows 8 t + 2 quad and + 1 of its
+// tiles t, whose statistics the 8 lanes of a quad column share.
+template <int D, int NT>
 struct TileState {
-  float acc[D / 8][4];   // n-tile i: dims (D / 8) * 2q + i and (D / 8) * (2q + 1) + i of both rows
-  float m[2], n[2], sum[2];
+  float acc[NT][D / 16][4];   // i: dims (D / 8) g + 2 i (both rows), then + 1 (both rows)
+  float m[NT][2], n[NT][2];              // the references (0 before the first step)
+  float top_m[NT][2], top_n[NT][2];      // what a value must pass to move them
+  float sum[NT][2];
 };
 
-template <int D>
-__device__ __forceinline__ void reset(TileState<D>& s) {
+template <int D, int NT>
+__device__ __forceinline__ void reset(TileState<D, NT>& s) {
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i)
+  for (int t = 0; t < NT; ++t) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s.acc[i][j] = 0.0f;
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    s.m[i] = s.n[i] = -INFINITY;
-    s.sum[i] = 0.0f;
+      for (int j = 0; j < 4; ++j) s.acc[t][i][j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s.m[t][i] = s.n[t][i] = s.sum[t][i] = 0.0f;
+      s.top_m[t][i] = s.top_n[t][i] = -INFINITY;
+    }
   }
 }
 
-// Rows of the tile as fp16 fragments.  A row enters as q 2^-k with its largest
+// The block's rows as fp16 fragments.  A row enters as q 2^-k with its largest
 // magnitude in [1, 2): exact in fp16 for components above 2^-14 and off by at
 // most 2^-25 below, which is less than the fp32 sum's own rounding.  factor
-// returns c log2(e) 2^k.
-template <int D>
+// returns c log2(e) 2^k of rows 2 quad and 2 quad + 1.
+template <int D, int NT>
+struct RawQ {
+  uint4 w[NT][D / 32];
+};
+
+template <int D, int NT>
 __device__ __forceinline__ void load_q(const AttArgs& a, int64_t t0, int n_rows, int row0, int head,
-                                       uint32_t (&qa)[D / 16][4], float (&factor)[2]) {
+                                       RawQ<D, NT>& raw) {
   const int lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int row = row0 + g + 8 * half;
-    const bool on = row < n_rows;
-    const int token = row / a.group;
+  for (int t = 0; t < NT; ++t) {
+    const int row = row0 + 8 * t + g, token = row / a.group;
     const uint16_t* src = a.q + (t0 + token) * a.ldq + (static_cast<int64_t>(head) * a.group + row % a.group) * D;
-    uint4 w[D / 32];  // 16 dims each D / 64: two uint4
 #pragma unroll
     for (int i = 0; i < D / 64; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        w[2 * i + j] = on ? __ldg(reinterpret_cast<const uint4*>(src + 64 * i + 16 * quad + 8 * j))
-                          : make_uint4(0, 0, 0, 0);
-    const uint32_t* u = &w[0].x;
+        raw.w[t][2 * i + j] = row < n_rows ? __ldg(reinterpret_cast<const uint4*>(src + 64 * i + 16 * quad + 8 * j))
+                                           : make_uint4(0, 0, 0, 0);
+  }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void convert_q(const AttArgs& a, const RawQ<D, NT>& raw, uint32_t (&qb)[NT][D / 16][2],
+                                          float (&factor)[NT][2]) {
+  const int quad = threadIdx.x & 3;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const uint32_t* u = &raw.w[t][0].x;
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(u[i])), fabsf(bf16_hi(u[i]))));
@@ -139,90 +162,153 @@ __device__ __forceinline__ void load_q(const AttArgs& a, int64_t t0, int n_rows,
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const int k = min(max((__float_as_int(amax) >> 23) - 127, -126), 126);
     const float inv = __int_as_float((127 - k) << 23);
-    factor[half] = a.scale_log2 * __int_as_float((127 + k) << 23);
-    // word i of the 16-byte code vector holds dims 4 i .. 4 i + 3 = u[2 i], u[2 i + 1]
+    const float f = a.scale_log2 * __int_as_float((127 + k) << 23);
+    factor[t][0] = __shfl_sync(0xffffffffu, f, 8 * quad);
+    factor[t][1] = __shfl_sync(0xffffffffu, f, 8 * quad + 4);
+    // word j of a lane's code vectors holds dims 4 j .. 4 j + 3 = u[2 j], u[2 j + 1]
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-        qa[j][half + 2 * p] = pack_f16(bf16_lo(u[2 * j + p]) * inv, bf16_hi(u[2 * j + p]) * inv);
+      for (int p = 0; p < 2; ++p) qb[t][j][p] = pack_f16(bf16_lo(u[2 * j + p]) * inv, bf16_hi(u[2 * j + p]) * inv);
   }
 }
 
-// One warp step: 16 cached tokens [j0, j0 + 16) whose codes are in kw and vw.
-// limit: tokens each row sees; mask: some row sees not all of the 16.
-template <int FMT, int D>
-__device__ __forceinline__ void step16(TileState<D>& s, const uint32_t (&qa)[D / 16][4], const float (&factor)[2],
-                                       const uint32_t (&kw)[2][D / 16], const uint32_t (&vw)[4][D / 32], float ks,
-                                       float vs, int j0, const int (&limit)[2], bool mask) {
-  const int quad = threadIdx.x & 3;
-  float x[2][4] = {};
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// One warp step: the 32 cached tokens [j0, j0 + 32), two groups of 16 that may
+// lie in two pages, from a stage of the ring: keys of both groups, then values.
+// limit: tokens each row sees; least: the smallest of them; len: the request's tokens.
+template <int FMT, int D, int NT>
+__device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)[NT][D / 16][2],
+                                       const float (&factor)[NT][2], const uint8_t* stage, const float (&ks)[2],
+                                       const float (&vs)[2], int j0, const int (&limit)[NT][2], int least, int len) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
+  float x[2][NT][4];
 #pragma unroll
-  for (int j = 0; j < D / 16; ++j)
+  for (int h = 0; h < 2; ++h) {
+    uint32_t kw[2][D / 16];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      uint32_t b0, b1;
-      codes_to_f16<FMT>(kw[nt][j], b0, b1);
-      mma_f16(x[nt], qa[j], b0, b1);
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+        *reinterpret_cast<uint4*>(&kw[r][4 * i]) =
+            *reinterpret_cast<const uint4*>(stage + (16 * h + 8 * r + g) * D + 64 * i + 16 * quad);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[h][t][i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      uint32_t ka[4];
+      codes_to_f16<FMT>(kw[0][j], ka[0], ka[2]);
+      codes_to_f16<FMT>(kw[1][j], ka[1], ka[3]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mma_f16(x[h][t], ka, qb[t][j][0], qb[t][j][1]);
     }
-  const float lvs = fmaxf(log2_fast(vs), -200.0f);  // a scale of zero stands for zeros
-  float top[2];
+  }
+  const bool mask = j0 + kAttStep > least;
+  float lvs[2];
+  bool move = false;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const float f = factor[half] * ks;
+  for (int h = 0; h < 2; ++h) {
+    lvs[h] = fmaxf(log2_fast(vs[h]), -200.0f);  // a scale of zero stands for zeros
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float& v = x[nt][2 * half + c];
-        v *= f;
-        if (mask && j0 + nt * 8 + 2 * quad + c >= limit[half]) v = -INFINITY;
+        const float f = factor[t][c] * ks[h];
+        x[h][t][c] *= f;
+        x[h][t][2 + c] *= f;
+        if (mask) {
+          if (j0 + 16 * h + g >= limit[t][c]) x[h][t][c] = -INFINITY;
+          if (j0 + 16 * h + g + 8 >= limit[t][c]) x[h][t][2 + c] = -INFINITY;
+        }
+        const float v = fmaxf(x[h][t][c], x[h][t][2 + c]);
+        move |= v > s.top_m[t][c] || v + lvs[h] > s.top_n[t][c];
       }
-    top[half] = fmaxf(fmaxf(x[0][2 * half], x[0][2 * half + 1]), fmaxf(x[1][2 * half], x[1][2 * half + 1]));
-    top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 1));
-    top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 2));
   }
-  const bool move = top[0] > s.m[0] + kLazy || top[1] > s.m[1] + kLazy || top[0] + lvs > s.n[0] + kLazy ||
-                    top[1] + lvs > s.n[1] + kLazy;
   if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const float m = fmaxf(s.m[half], top[half]), n = fmaxf(s.n[half], top[half] + lvs);
-      // a row that has seen nothing yet keeps sums of zero: no factor of inf - inf
-      if (m > -INFINITY) s.sum[half] *= exp2_fast(s.m[half] - m);
-      const float f = n > -INFINITY ? exp2_fast(s.n[half] - n) : 1.0f;
-      s.m[half] = m;
-      s.n[half] = n;
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        s.acc[i][2 * half] *= f;
-        s.acc[i][2 * half + 1] *= f;
+      for (int c = 0; c < 2; ++c) {
+        float m = fmaxf(fmaxf(x[0][t][c], x[0][t][2 + c]), fmaxf(x[1][t][c], x[1][t][2 + c]));
+        float n = fmaxf(fmaxf(x[0][t][c], x[0][t][2 + c]) + lvs[0], fmaxf(x[1][t][c], x[1][t][2 + c]) + lvs[1]);
+#pragma unroll
+        for (int d = 4; d <= 16; d *= 2) {
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+          n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
+        }
+        if (m == -INFINITY) continue;  // the row has seen nothing yet, or nothing here
+        // the references only grow; before the first value they are 0 and so are the sums
+        m = fmaxf(m, s.top_m[t][c] - kLazy);
+        n = fmaxf(n, s.top_n[t][c] - kLazy);
+        const bool none = s.sum[t][c] == 0.0f;
+        const float f = none ? 0.0f : exp2_fast(s.n[t][c] - n);
+        s.sum[t][c] *= none ? 0.0f : exp2_fast(s.m[t][c] - m);
+        s.m[t][c] = m;
+        s.n[t][c] = n;
+        s.top_m[t][c] = m + kLazy;
+        s.top_n[t][c] = n + kLazy;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          s.acc[t][i][c] *= f;
+          s.acc[t][i][2 + c] *= f;
+        }
       }
-    }
-  }
-  uint32_t pa[4];
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const float m = s.m[half] > -INFINITY ? s.m[half] : 0.0f;
-    const float n = s.n[half] > -INFINITY ? s.n[half] : 0.0f;
-    const float c = exp2_fast(fminf(m + lvs - n, 100.0f));
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const float p0 = exp2_fast(x[nt][2 * half] - m), p1 = exp2_fast(x[nt][2 * half + 1] - m);
-      s.sum[half] += p0 + p1;
-      pa[half + 2 * nt] = pack_f16(p0 * c, p1 * c);
-    }
   }
 #pragma unroll
-  for (int w = 0; w < D / 32; ++w) {
-    // bytes of two neighbouring tokens side by side, then to fp16 pairs
-    uint32_t b0[4], b1[4];
-    codes_to_f16<FMT>(__byte_perm(vw[0][w], vw[1][w], 0x5140), b0[0], b0[1]);
-    codes_to_f16<FMT>(__byte_perm(vw[0][w], vw[1][w], 0x7362), b0[2], b0[3]);
-    codes_to_f16<FMT>(__byte_perm(vw[2][w], vw[3][w], 0x5140), b1[0], b1[1]);
-    codes_to_f16<FMT>(__byte_perm(vw[2][w], vw[3][w], 0x7362), b1[2], b1[3]);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pb[NT][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mma_f16(s.acc[4 * w + i], pa, b0[i], b1[i]);
+    for (int t = 0; t < NT; ++t) {
+      float w[4];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float f = exp2_fast(fminf(s.m[t][c] - s.n[t][c] + lvs[h], 100.0f));
+        const float p0 = exp2_fast(x[h][t][c] - s.m[t][c]), p1 = exp2_fast(x[h][t][2 + c] - s.m[t][c]);
+        s.sum[t][c] += p0 + p1;
+        w[c] = p0 * f;
+        w[2 + c] = p1 * f;
+      }
+      pb[t][0] = transpose8(pack_f16(w[0], w[1]));
+      pb[t][1] = transpose8(pack_f16(w[2], w[3]));
+    }
+    uint32_t vw[4][D / 32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* src = stage + (kAttStep + 16 * h + (i >> 1) * 8 + 2 * quad + (i & 1)) * D + (D / 8) * g;
+      if constexpr (D == 128)
+        *reinterpret_cast<uint4*>(vw[i]) = *reinterpret_cast<const uint4*>(src);
+      else
+        *reinterpret_cast<uint2*>(vw[i]) = *reinterpret_cast<const uint2*>(src);
+    }
+    if (j0 + kAttStep > len) {
+      // past the request's tokens the page (or the stage) may hold anything,
+      // and 0 * NaN is not 0: zeros in its place
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w)
+          if (j0 + 16 * h + (i >> 1) * 8 + 2 * quad + (i & 1) >= len) vw[i][w] = 0;
+    }
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      // bytes of two neighbouring tokens side by side, then to fp16 pairs
+      uint32_t va[2][4];
+      codes_to_f16<FMT>(__byte_perm(vw[0][w], vw[1][w], 0x5140), va[0][0], va[0][1]);
+      codes_to_f16<FMT>(__byte_perm(vw[0][w], vw[1][w], 0x7362), va[1][0], va[1][1]);
+      codes_to_f16<FMT>(__byte_perm(vw[2][w], vw[3][w], 0x5140), va[0][2], va[0][3]);
+      codes_to_f16<FMT>(__byte_perm(vw[2][w], vw[3][w], 0x7362), va[1][2], va[1][3]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_f16(s.acc[t][2 * w + i], va[i], pb[t][0], pb[t][1]);
+    }
   }
 }
 
@@ -254,25 +340,25 @@ __device__ __forceinline__ void zero_row(const AttArgs& a, int64_t t, int tid, i
 
 // ------------------------------------------------------------ work split
 // A segment is one tile of 16 rows of one key head with all its cached tokens,
-// in units of 64 of them.  The segments of all requests, laid end to end, are
+// in units of 128 of them.  The segments of all requests, laid end to end, are
 // cut into as many equal pieces as CTAs run, so the lengths of the requests
 // do not matter for the balance.  A piece's cut segments leave partial results in the
 // workspace (two a CTA: of the segment it starts in the middle of, and of the
 // one it ends in the middle of), which join_kernel adds in order.
-constexpr int kUnit = kAttGroup * kAttWarps;  // cached tokens of a unit: 16 a warp
+constexpr int kUnit = kAttStep * kAttWarps;  // cached tokens of a unit: a step of each warp
 constexpr int kMaxCtas = 608;
 // Segments of up to this many units are never cut: their join would cost more
 // than the imbalance of leaving them whole.
-constexpr int kWholeUnits = 4;
+constexpr int kWholeUnits = 2;
 // Whole segments of up to this many units (512 tokens) go to single warps.
-constexpr int kWarpUnits = 8;
+constexpr int kWarpUnits = 4;
 
 struct Piece {   // of a segment that goes on in the next CTA, for join_kernel
   int32_t t0, n_rows, row0, head, last_cta, pad[3];
 };
 
 template <int D>
-constexpr size_t partial_floats() { return static_cast<size_t>(kAttRows) * (D + 4); }
+constexpr size_t partial_floats() { return static_cast<size_t>(kMaxRows) * (D + 4); }
 
 __device__ __forceinline__ int visible_len(const AttArgs& a, int r) {
   const int64_t room = static_cast<int64_t>(a.max_blocks) << a.page_shift;
@@ -289,9 +375,13 @@ __device__ __forceinline__ Request request(const AttArgs& a, int r) {
 }
 
 __device__ __forceinline__ int units_of(const Request& q) { return (q.len + kUnit - 1) / kUnit; }
-__device__ __forceinline__ int row_blocks_of(const Request& q) { return (q.n_rows + kAttRows - 1) / kAttRows; }
+template <int NT>
+__device__ __forceinline__ int row_blocks_of(const Request& q) {
+  return (q.n_rows + 8 * NT - 1) / (8 * NT);
+}
 
 // start[r] = units of the requests before r, start[n_requests] = all; by the whole CTA.
+template <int NT>
 __device__ __forceinline__ void scan_requests(const AttArgs& a, int64_t* start, int64_t* warp_sum) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.n_requests + kAttThreads - 1) / kAttThreads;
@@ -299,7 +389,7 @@ __device__ __forceinline__ void scan_requests(const AttArgs& a, int64_t* start, 
   int64_t mine = 0;
   for (int r = r0; r < r1; ++r) {
     const Request q = request(a, r);
-    const int64_t w = static_cast<int64_t>(units_of(q)) * row_blocks_of(q) * a.heads;
+    const int64_t w = static_cast<int64_t>(units_of(q)) * row_blocks_of<NT>(q) * a.heads;
     start[r] = w;
     mine += w;
   }
@@ -349,156 +439,167 @@ __device__ __forceinline__ int64_t cut_at(const AttArgs& a, const int64_t* start
   return whole || units <= kWholeUnits ? u - in : u;
 }
 
+// A warp's own ring of stages in shared memory: a step's keys, then its values,
+// each D bytes a token as in the cache.
 template <int D>
 struct Ring {
-  static constexpr int kStages = 4;
-  static constexpr int kK = kAttGroup * D, kStage = 2 * kK + 16;  // bytes: keys, values, two scales
-  static constexpr int kWarp = kStages * kStage;
+  static constexpr int kStages = D == 128 ? 2 : 3;
+  static constexpr int kGroup = kAttGroup * D, kStage = 4 * kGroup, kWarp = kStages * kStage;
   static_assert(kWarp >= static_cast<int>(partial_floats<D>() * 4), "a warp's results take the ring's place");
+  uint8_t* data;
+  uint64_t* full;   // [kStages] mbarriers, two arrivals each: one a group
+  volatile int* abort;
+  int slot;         // the stage of the next step
+  uint32_t phases;  // bit i: the parity that full[i] completes next
 };
 
-template <int kBytes>
-__device__ __forceinline__ void copy_async(void* dst, const void* src, bool on) {
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(kBytes),
-                 "r"(on ? kBytes : 0)
-                 : "memory");
-}
-
 // One warp's way through the segments seg, seg + 4, ... < seg_end of a request
-// (row blocks of a head, then the next head): n_steps steps of 16 cached
+// (row blocks of a head, then the next head): n_steps steps of 32 cached
 // tokens each, j_stride tokens apart from j_first on.
 struct Stream {
   const int32_t* table;
   int len, j_first, j_stride, n_steps, seg, seg_end, blocks;
 };
 
-// The copies run kStages - 1 steps ahead of the arithmetic, over the ends of
-// segments too.  Several segments need n_steps <= 32 (their page numbers stay
-// in one register a lane).
-template <int FMT, int D, typename Emit>
-__device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, const Request& q, uint8_t* ring,
+// The copies (bulk copies of 16 D bytes, the keys and the values of a group) run
+// kStages - 1 steps ahead of the arithmetic, over the ends of segments too.  Lane l
+// looks after the groups l, l + 32, ... of a segment: it holds the page's
+// place and scales and issues the copies.  Several segments need at most 32 groups.
+template <int FMT, int D, int NT, typename Emit>
+__device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, const Request& q, Ring<D>& ring,
                                            Emit emit) {
   using R = Ring<D>;
-  const int lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
+  if (st.seg >= st.seg_end) return;
+  const int lane = threadIdx.x & 31, quad = lane & 3;
   const int page_mask = (1 << a.page_shift) - 1;
-  // page numbers of 32 steps at a time, one a lane, and the next 32 behind them
-  const auto pages_from = [&](int step) {
-    int page = 0;
-    if (step + lane < st.n_steps) {
-      page = st.table[(st.j_first + (step + lane) * st.j_stride) >> a.page_shift];
+  const int64_t head_bytes = static_cast<int64_t>(D) << a.page_shift;
+  struct Batch {
+    int64_t cell;   // of head 0
+    int offset;     // bytes inside a page's head
+    bool on;        // there is such a group
+    float ks, vs;
+  };
+  const auto scales_of = [&](Batch& b, int head) {
+    if (b.on) {
+      b.ks = __ldg(a.k_scale + b.cell + head);
+      b.vs = __ldg(a.v_scale + b.cell + head);
+    }
+  };
+  const auto batch_from = [&](int step, int head) {
+    Batch b = {0, 0, false, 0.0f, 0.0f};
+    const int mine = step + lane / 2;
+    const int j = st.j_first + mine * st.j_stride + (lane & 1) * kAttGroup;
+    if (mine < st.n_steps && j < st.len) {
+      int page = st.table[j >> a.page_shift];
       if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.n_pages)) {
         report_error(a.status, TWELL_ERR_BAD_FORMAT);
         page = 0;
       }
+      b.cell = static_cast<int64_t>(page) * a.heads;
+      b.offset = (j & page_mask) * D;
+      b.on = true;
     }
-    return page;
+    scales_of(b, head);
+    return b;
   };
-  int pages = 0, pages_next = 0;
-  if (st.seg < st.seg_end) {
-    pages = pages_from(0);
-    if (st.n_steps > 32) pages_next = pages_from(32);
-  }
-  int f_seg = st.seg, f_step = 0, f_slot = 0;  // the next copy
+  int head = st.seg / st.blocks;
+  Batch now = batch_from(0, head), ahead = now;  // of the arithmetic's steps and the next ones
+  if (st.n_steps > 16) ahead = batch_from(16, head);
+  Batch copies = now;
+  int f_seg = st.seg, f_head = head, f_step = 0, f_slot = ring.slot;
   const auto fetch = [&]() {
-    if (f_seg < st.seg_end && st.n_steps > 0) {
-      if (f_step > 0 && (f_step & 31) == 0) {
-        pages = pages_next;
-        if (f_step + 32 < st.n_steps) pages_next = pages_from(f_step + 32);
+    if (f_seg >= st.seg_end || st.n_steps == 0) return;
+    if (f_step > 0 && (f_step & 15) == 0) copies = ahead;
+    if (lane / 2 == (f_step & 15)) {
+      uint64_t* const bar = ring.full + f_slot;
+      if (copies.on) {
+        uint8_t* const stage = ring.data + f_slot * R::kStage + (lane & 1) * R::kGroup;
+        const int64_t at = (copies.cell + f_head) * head_bytes + copies.offset;
+        mbar_arrive_expect_tx(bar, 2 * R::kGroup);
+        bulk_load(stage, a.k + at, R::kGroup, bar);
+        bulk_load(stage + 2 * R::kGroup, a.v + at, R::kGroup, bar);
+      } else {
+        mbar_arrive(bar);
       }
-      const int page = __shfl_sync(0xffffffffu, pages, f_step & 31);
-      uint8_t* const stage = ring + f_slot * R::kStage;
-      const int j0 = st.j_first + f_step * st.j_stride;
-      const int64_t cell = static_cast<int64_t>(page) * a.heads + f_seg / st.blocks;
-      const int64_t at = ((cell << a.page_shift) + (j0 & page_mask)) * D;
-      // lane l's bytes of each load lie together: it reads back what it copied
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-          copy_async<16>(stage + ((nt * (D / 64) + i) * 32 + lane) * 16,
-                         a.k + at + (nt * 8 + g) * D + 64 * i + 16 * quad, true);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int token = (i >> 1) * 8 + 2 * quad + (i & 1);
-        // past the request's tokens the page may hold anything, and 0 * NaN is
-        // not 0: zeros in its place
-        copy_async<D / 8>(stage + R::kK + (i * 32 + lane) * (D / 8), a.v + at + token * D + (D / 8) * g,
-                          j0 + token < st.len);
-      }
-      if (lane < 2) copy_async<4>(stage + 2 * R::kK + 4 * lane, (lane == 0 ? a.k_scale : a.v_scale) + cell, true);
-      if (++f_step == st.n_steps) f_step = 0, f_seg += kAttWarps;
     }
     f_slot = f_slot + 1 == R::kStages ? 0 : f_slot + 1;
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++f_step == st.n_steps) {
+      f_step = 0;
+      f_seg += kAttWarps;
+      f_head = f_seg / st.blocks;
+    }
   };
 #pragma unroll
   for (int i = 0; i < R::kStages - 1; ++i) fetch();
-  int slot = 0;
+  RawQ<D, NT> raw;
+  load_q<D, NT>(a, q.t0, q.n_rows, st.seg % st.blocks * (8 * NT), head, raw);
+  int limit[NT][2], least = st.len;
   for (int seg = st.seg; seg < st.seg_end; seg += kAttWarps) {
-    const int head = seg / st.blocks, row0 = seg % st.blocks * kAttRows;
-    // what each row sees; rows past the last see everything and are not stored
-    int limit[2], least = INT32_MAX;
+    const int row0 = (seg - head * st.blocks) * (8 * NT);
+    const int next_head = (seg + kAttWarps) / st.blocks;
+    // what each row sees; rows past the last see everything and are not stored.
+    // The same in every head, so only several row blocks need it again.
+    if (seg == st.seg || st.blocks > 1) {
+      least = st.len;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int row = row0 + g + 8 * half;
-      limit[half] = INT32_MAX;
-      if (row < q.n_rows) {
-        const int p = a.positions[q.t0 + row / a.group];
-        limit[half] = max(0, min(p < INT32_MAX ? p + 1 : p, q.len));
-        least = min(least, limit[half]);
-      }
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int row = row0 + 8 * t + 2 * quad + c;
+          limit[t][c] = INT32_MAX;
+          if (row < q.n_rows) {
+            const int p = a.positions[q.t0 + row / a.group];
+            limit[t][c] = max(0, min(p < INT32_MAX ? p + 1 : p, q.len));
+            least = min(least, limit[t][c]);
+          }
+        }
+      least = min(least, __shfl_xor_sync(0xffffffffu, least, 1));
+      least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
     }
-#pragma unroll
-    for (int d = 16; d >= 4; d /= 2) least = min(least, __shfl_xor_sync(0xffffffffu, least, d));
-    least = min(least, st.len);
-    uint32_t qa[D / 16][4];
-    float factor[2];
-    load_q<D>(a, q.t0, q.n_rows, row0, head, qa, factor);
-    TileState<D> s;
+    uint32_t qb[NT][D / 16][2];
+    float factor[NT][2];
+    convert_q<D, NT>(a, raw, qb, factor);
+    if (seg != st.seg) now = ahead;
+    if (seg + kAttWarps < st.seg_end) {
+      // the next segment's rows and scales, a segment ahead
+      load_q<D, NT>(a, q.t0, q.n_rows, (seg + kAttWarps - next_head * st.blocks) * (8 * NT), next_head, raw);
+      scales_of(ahead, next_head);
+    }
+    TileState<D, NT> s;
     reset(s);
     for (int step = 0; step < st.n_steps; ++step) {
-      __syncwarp();  // the scales that fetch replaces have been read by all lanes
-      fetch();
-      asm volatile("cp.async.wait_group %0;" ::"n"(R::kStages - 1) : "memory");
-      __syncwarp();  // the scales came in by two lanes
-      const uint8_t* const stage = ring + slot * R::kStage;
-      slot = slot + 1 == R::kStages ? 0 : slot + 1;
-      const int j0 = st.j_first + step * st.j_stride;
-      uint32_t kw[2][D / 16], vw[4][D / 32];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-          *reinterpret_cast<uint4*>(&kw[nt][4 * i]) =
-              *reinterpret_cast<const uint4*>(stage + ((nt * (D / 64) + i) * 32 + lane) * 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint8_t* src = stage + R::kK + (i * 32 + lane) * (D / 8);
-        if constexpr (D == 128)
-          *reinterpret_cast<uint4*>(vw[i]) = *reinterpret_cast<const uint4*>(src);
-        else
-          *reinterpret_cast<uint2*>(vw[i]) = *reinterpret_cast<const uint2*>(src);
+      if (step > 0 && (step & 15) == 0) {
+        now = ahead;
+        if (step + 16 < st.n_steps) ahead = batch_from(step + 16, head);
       }
-      const float2 scales = *reinterpret_cast<const float2*>(stage + 2 * R::kK);
-      step16<FMT, D>(s, qa, factor, kw, vw, scales.x, scales.y, j0, limit, j0 + kAttGroup > least);
+      __syncwarp();  // all lanes have read the stage that fetch fills again
+      fetch();
+      if (!mbar_wait(ring.full + ring.slot, (ring.phases >> ring.slot) & 1u, kWaitLimitNs, ring.abort))
+        report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
+      ring.phases ^= 1u << ring.slot;
+      const uint8_t* const stage = ring.data + ring.slot * R::kStage;
+      ring.slot = ring.slot + 1 == R::kStages ? 0 : ring.slot + 1;
+      const int from = 2 * (step & 15);
+      const float ks[2] = {__shfl_sync(0xffffffffu, now.ks, from), __shfl_sync(0xffffffffu, now.ks, from + 1)};
+      const float vs[2] = {__shfl_sync(0xffffffffu, now.vs, from), __shfl_sync(0xffffffffu, now.vs, from + 1)};
+      step32<FMT, D, NT>(s, qb, factor, stage, ks, vs, st.j_first + step * st.j_stride, limit, least, st.len);
     }
-    if (seg + kAttWarps >= st.seg_end) asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      s.sum[half] += __shfl_xor_sync(0xffffffffu, s.sum[half], 1);
-      s.sum[half] += __shfl_xor_sync(0xffffffffu, s.sum[half], 2);
-    }
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int d = 4; d <= 16; d *= 2) s.sum[t][c] += __shfl_xor_sync(0xffffffffu, s.sum[t][c], d);
+        if (s.sum[t][c] == 0.0f) s.m[t][c] = s.n[t][c] = -INFINITY;  // nothing seen
+      }
     emit(s, head, row0);
+    head = next_head;
   }
 }
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(kAttThreads, 3)
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D == 64 ? 3 : 2)
     attention_kernel(const AttArgs a, float* partial, Piece* pieces, int whole) {
   using R = Ring<D>;
   extern __shared__ __align__(16) uint8_t dyn[];
@@ -507,8 +608,13 @@ __global__ void __launch_bounds__(kAttThreads, 3)
   __shared__ int64_t warp_sum[kAttWarps];
   grid_dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, quad = lane & 3;
-  uint8_t* const ring = ring_all + warp * R::kWarp;
-  scan_requests(a, start, warp_sum);
+  __shared__ uint64_t full[kAttWarps][R::kStages];
+  __shared__ int abort_flag;
+  Ring<D> ring = {ring_all + warp * R::kWarp, full[warp], &abort_flag, 0, 0};
+  if (tid == 0) abort_flag = 0;
+  if (lane < R::kStages) mbar_init(full[warp] + lane, 2);
+  mbar_fence_init();
+  scan_requests<NT>(a, start, warp_sum);
   // at least a unit for each CTA that works, so that every CTA between a cut
   // segment's first and last has a part of it
   const int64_t cta = blockIdx.x, n_ctas = min(static_cast<int64_t>(gridDim.x), start[a.n_requests]);
@@ -528,7 +634,7 @@ __global__ void __launch_bounds__(kAttThreads, 3)
   while (pos < end) {
     const int r = request_at(start, a.n_requests, pos);
     const Request q = request(a, r);
-    const int units = units_of(q), blocks = row_blocks_of(q);
+    const int units = units_of(q), blocks = row_blocks_of<NT>(q);
     const int64_t seg0 = (pos - start[r]) / units;
     const int unit0 = static_cast<int>((pos - start[r]) % units);
     Stream st;
@@ -539,57 +645,57 @@ __global__ void __launch_bounds__(kAttThreads, 3)
       const int64_t left = static_cast<int64_t>(blocks) * a.heads - seg0;
       const int count = static_cast<int>(min(left, (end - pos) / units));
       st.j_first = 0;
-      st.j_stride = kAttGroup;
-      st.n_steps = (q.len + kAttGroup - 1) / kAttGroup;
+      st.j_stride = kAttStep;
+      st.n_steps = (q.len + kAttStep - 1) / kAttStep;
       st.seg = static_cast<int>(seg0) + ((warp - turn) & (kAttWarps - 1));
       st.seg_end = static_cast<int>(seg0) + count;
       st.blocks = blocks;
       turn += count;
       pos += static_cast<int64_t>(count) * units;
-      run_stream<FMT, D>(a, st, q, ring, [&](TileState<D>& s, int head, int row0) {
+      run_stream<FMT, D, NT>(a, st, q, ring, [&](TileState<D, NT>& s, int head, int row0) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int row = row0 + g + 8 * half;
-          if (row >= q.n_rows) continue;
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i0 = 0; i0 < 2 * (D / 8); i0 += 8) {
-            float o[8];
+          for (int c = 0; c < 2; ++c) {
+            const int row = row0 + 8 * t + 2 * quad + c;
+            if (row >= q.n_rows) continue;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = s.acc[(i0 + i) % (D / 8)][2 * half + (i0 + i) / (D / 8)];
-            store_row<D>(a, q.t0, row, head, (D / 8) * 2 * quad + i0, s.m[half], s.n[half], s.sum[half], o);
+            for (int i0 = 0; i0 < D / 8; i0 += 8) {
+              float o[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] = s.acc[t][(i0 + i) / 2][2 * (i & 1) + c];
+              store_row<D>(a, q.t0, row, head, (D / 8) * g + i0, s.m[t][c], s.n[t][c], s.sum[t][c], o);
+            }
           }
-        }
       });
       continue;
     }
     const int n_units = static_cast<int>(min(static_cast<int64_t>(units - unit0), end - pos));
     pos += n_units;
-    st.j_first = unit0 * kUnit + warp * kAttGroup;
+    st.j_first = unit0 * kUnit + warp * kAttStep;
     st.j_stride = kUnit;
-    const int seen = min(n_units * kUnit, q.len - unit0 * kUnit) - warp * kAttGroup;
+    const int seen = min(n_units * kUnit, q.len - unit0 * kUnit) - warp * kAttStep;
     st.n_steps = seen > 0 ? (seen + kUnit - 1) / kUnit : 0;
     st.seg = static_cast<int>(seg0);
     st.seg_end = st.seg + 1;
     st.blocks = blocks;
     // the four warps' results of the tile, joined in warp order; they take the ring's place
-    run_stream<FMT, D>(a, st, q, ring, [&](TileState<D>& s, int, int row0) {
-      float* const mine = reinterpret_cast<float*>(ring);
+    run_stream<FMT, D, NT>(a, st, q, ring, [&](TileState<D, NT>& s, int, int row0) {
+      float* const mine = reinterpret_cast<float*>(ring.data);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int row = g + 8 * half;
-        if (row0 + row < q.n_rows) {
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int row = 8 * t + 2 * quad + c;
+          if (row0 + row >= q.n_rows) continue;
           float* const at = mine + row * (D + 4);
-          if (quad == 0) at[D] = s.m[half], at[D + 1] = s.n[half], at[D + 2] = s.sum[half];
+          if (g == 0) at[D] = s.m[t][c], at[D + 1] = s.n[t][c], at[D + 2] = s.sum[t][c];
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            at[(D / 8) * (2 * quad) + i] = s.acc[i][2 * half];
-            at[(D / 8) * (2 * quad + 1) + i] = s.acc[i][2 * half + 1];
-          }
+          for (int i = 0; i < D / 8; ++i) at[(D / 8) * g + i] = s.acc[t][i / 2][2 * (i & 1) + c];
         }
-      }
     });
     __syncthreads();
-    const int head = st.seg / blocks, row0 = st.seg % blocks * kAttRows;
+    const int head = st.seg / blocks, row0 = st.seg % blocks * (8 * NT);
     constexpr int kLanes = D / 8;
     const bool complete = n_units == units, goes_on = unit0 + n_units < units;
     // a cut segment's part: slot 1 where it starts here, slot 0 where it came from the CTA before
@@ -601,7 +707,7 @@ __global__ void __launch_bounds__(kAttThreads, 3)
       pieces[cta] = {q.t0, q.n_rows, row0, head,
                      static_cast<int32_t>((seg_end * n_ctas - 1) / start[a.n_requests]), {0, 0, 0}};
     }
-    for (int row = tid / kLanes; row < min(kAttRows, q.n_rows - row0); row += kAttThreads / kLanes) {
+    for (int row = tid / kLanes; row < min(8 * NT, q.n_rows - row0); row += kAttThreads / kLanes) {
       const int d0 = (tid % kLanes) * 8;
       float m = -INFINITY, n = -INFINITY, sum = 0.0f, o[8] = {};
 #pragma unroll
@@ -629,13 +735,14 @@ __global__ void __launch_bounds__(kAttThreads, 3)
         if (d0 == 0) *reinterpret_cast<float4*>(to + D) = make_float4(m, n, sum, 0.0f);
       }
     }
-    __syncthreads();  // the ring is free again
+    fence_async_shared();  // the results' place is the copies' again
+    __syncthreads();
   }
 }
 
 // Adds a cut segment's parts in the order of its units: one CTA for each CTA
 // of attention_kernel, idle unless a segment starts there and goes on.
-template <int D>
+template <int D, int NT>
 __global__ void __launch_bounds__(kAttThreads) join_kernel(const AttArgs a, const float* partial, const Piece* pieces) {
   grid_dependency_wait();
   const int cta = blockIdx.x, tid = threadIdx.x;
@@ -646,7 +753,7 @@ __global__ void __launch_bounds__(kAttThreads) join_kernel(const AttArgs a, cons
   const auto part = [&](int c, int row) {
     return partial + (2 * static_cast<int64_t>(c) + (c == cta ? 1 : 0)) * partial_floats<D>() + row * (D + 4);
   };
-  for (int row = tid / kLanes; row < min(kAttRows, p.n_rows - p.row0); row += kAttThreads / kLanes) {
+  for (int row = tid / kLanes; row < min(8 * NT, p.n_rows - p.row0); row += kAttThreads / kLanes) {
     float m = -INFINITY, n = -INFINITY, sum = 0.0f, o[8] = {};
 #pragma unroll 4
     for (int c = cta; c <= p.last_cta; ++c) {
@@ -670,17 +777,17 @@ __global__ void __launch_bounds__(kAttThreads) join_kernel(const AttArgs a, cons
   }
 }
 
-template <int FMT, int D>
+template <int FMT, int D, int NT>
 int launch_attention(const AttArgs& a, int max_kv_len, int max_q_len, void* workspace, cudaStream_t s) {
   float* const partial = static_cast<float*>(workspace);
   Piece* const pieces = reinterpret_cast<Piece*>(partial + 2 * kMaxCtas * partial_floats<D>());
   const size_t smem = kAttWarps * Ring<D>::kWarp + sizeof(int64_t) * (static_cast<size_t>(a.n_requests) + 1);
-  const void* fn = reinterpret_cast<const void*>(attention_kernel<FMT, D>);
+  const void* fn = reinterpret_cast<const void*>(attention_kernel<FMT, D, NT>);
   KV_TRY(set_max_dynamic_smem(fn, static_cast<int>(kAttWarps * Ring<D>::kWarp + 8 * (kAttMaxRequests + 1))));
   const int resident = resident_ctas_per_sm(fn, kAttThreads, smem);
   if (resident < 1) return TWELL_ERR_CUDA;
   // no more CTAs than the units that the caller's bounds allow
-  const int64_t blocks = (static_cast<int64_t>(max_q_len) * a.group + kAttRows - 1) / kAttRows;
+  const int64_t blocks = (static_cast<int64_t>(max_q_len) * a.group + 8 * NT - 1) / (8 * NT);
   const int64_t units = (static_cast<int64_t>(max_kv_len) + kUnit - 1) / kUnit;
   const int64_t most = std::max<int64_t>(1, a.n_requests * a.heads * std::max<int64_t>(1, blocks * units));
   const int ctas = static_cast<int>(
@@ -688,16 +795,28 @@ int launch_attention(const AttArgs& a, int max_kv_len, int max_q_len, void* work
   const bool whole = units <= kWholeUnits;
   {
     LaunchScope scope(TWELL_KERNEL_KV_ATTENTION, s);
-    if (launch_pdl(attention_kernel<FMT, D>, dim3(ctas), dim3(kAttThreads), smem, s, a, partial, pieces,
+    if (launch_pdl(attention_kernel<FMT, D, NT>, dim3(ctas), dim3(kAttThreads), smem, s, a, partial, pieces,
                    static_cast<int>(whole)) != cudaSuccess)
       return TWELL_ERR_CUDA;
   }
   if (whole || ctas == 1) return TWELL_OK;
   LaunchScope scope(TWELL_KERNEL_KV_JOIN, s);
-  return launch_pdl(join_kernel<D>, dim3(ctas - 1), dim3(kAttThreads), 0, s, a, static_cast<const float*>(partial),
+  return launch_pdl(join_kernel<D, NT>, dim3(ctas - 1), dim3(kAttThreads), 0, s, a, static_cast<const float*>(partial),
                     static_cast<const Piece*>(pieces)) == cudaSuccess
              ? TWELL_OK
              : TWELL_ERR_CUDA;
+}
+
+template <int FMT>
+int launch_dim(const AttArgs& a, int dim, int max_kv_len, int max_q_len, void* workspace, cudaStream_t s) {
+  // row blocks of 8 where every request has 8 rows or fewer, else of 16: the
+  // codes' conversion is then shared by twice the rows
+  const bool small = static_cast<int64_t>(std::max(max_q_len, 1)) * a.group <= 8;
+  if (dim == 64)
+    return small ? launch_attention<FMT, 64, 1>(a, max_kv_len, max_q_len, workspace, s)
+                 : launch_attention<FMT, 64, 2>(a, max_kv_len, max_q_len, workspace, s);
+  return small ? launch_attention<FMT, 128, 1>(a, max_kv_len, max_q_len, workspace, s)
+               : launch_attention<FMT, 128, 2>(a, max_kv_len, max_q_len, workspace, s);
 }
 
 }  // namespace
@@ -711,7 +830,7 @@ extern "C" TWELL_API size_t twell_kv_attention_workspace_bytes(int32_t n_tokens,
   if (n_tokens < 0 || n_requests < 0 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads != 0 ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  return (2 * kMaxCtas * static_cast<size_t>(kAttRows) * (head_dim + 4) * sizeof(float) + kMaxCtas * sizeof(Piece) + 255) /
+  return (2 * kMaxCtas * static_cast<size_t>(kMaxRows) * (head_dim + 4) * sizeof(float) + kMaxCtas * sizeof(Piece) + 255) /
          256 * 256;
 }
 
@@ -771,8 +890,6 @@ extern "C" TWELL_API int twell_kv_attention(const uint16_t* Q, int64_t ldq, cons
   a.n_pages = cache->n_pages;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cache->format == TWELL_KV_E4M3)
-    return cache->head_dim == 64 ? launch_attention<TWELL_KV_E4M3, 64>(a, max_kv_len, max_q_len, workspace, s)
-                                 : launch_attention<TWELL_KV_E4M3, 128>(a, max_kv_len, max_q_len, workspace, s);
-  return cache->head_dim == 64 ? launch_attention<TWELL_KV_INT8, 64>(a, max_kv_len, max_q_len, workspace, s) : launch_attention<TWELL_KV_INT8, 128>(a, max_kv_len, max_q_len, workspace, s);
+  return cache->format == TWELL_KV_E4M3 ? launch_dim<TWELL_KV_E4M3>(a, cache->head_dim, max_kv_len, max_q_len, workspace, s)
+                                        : launch_dim<TWELL_KV_INT8>(a, cache->head_dim, max_kv_len, max_q_len, workspace, s);
 }
