@@ -25,7 +25,7 @@
 // P's 8 x 8 blocks are turned by movmatrix.
 #include <algorithm>
 
-#include "kv_internal.h"
+#include "kv_attention.h"
 
 namespace twell {
 namespace {
@@ -41,59 +41,10 @@ constexpr int kAttMaxRequests = 4096;
 // much (as powers of two): weights up to 2^8 stay well inside fp16.
 constexpr float kLazy = 8.0f;
 
-struct AttArgs {
-  const uint16_t* q;
-  int64_t ldq;
-  const uint8_t *k, *v;
-  const float *k_scale, *v_scale;
-  const int32_t *block_table, *cu_q, *positions, *kv_lens;
-  uint16_t* o;
-  int64_t ldo;
-  float* lse;
-  int32_t* status;
-  int max_blocks, n_tokens, n_requests, q_heads, heads, group, page_shift, n_pages;
-  float scale_log2;  // softmax_scale * log2(e)
-};
-
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float log2_fast(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-// Four codes of one word to two fp16 pairs: (byte 0, byte 1) and (byte 2, byte 3).
-template <int FMT>
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& p01, uint32_t& p23) {
-  if (FMT == TWELL_KV_E4M3) {
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(p01), "=r"(p23)
-        : "r"(w));
-  } else {
-    // 0x6400 | u is the fp16 number 1024 + u: with u = code + 128, minus 1152
-    const uint32_t u = w ^ 0x80808080u;
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p01) : "r"(a), "r"(0x64806480u));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p23) : "r"(b), "r"(0x64806480u));
-  }
 }
 
 // One row block's running state in a warp: rows 8 t + 2 quad and + 1 of its
@@ -360,20 +311,6 @@ struct Piece {   // of a segment that goes on in the next CTA, for join_kernel
 template <int D>
 constexpr size_t partial_floats() { return static_cast<size_t>(kMaxRows) * (D + 4); }
 
-__device__ __forceinline__ int visible_len(const AttArgs& a, int r) {
-  const int64_t room = static_cast<int64_t>(a.max_blocks) << a.page_shift;
-  return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(a.kv_lens[r]), room)));
-}
-
-struct Request {
-  int t0, n_rows, len;
-};
-
-__device__ __forceinline__ Request request(const AttArgs& a, int r) {
-  const int t0 = min(max(a.cu_q[r], 0), a.n_tokens), t1 = min(max(a.cu_q[r + 1], t0), a.n_tokens);
-  return {t0, (t1 - t0) * a.group, visible_len(a, r)};
-}
-
 __device__ __forceinline__ int units_of(const Request& q) { return (q.len + kUnit - 1) / kUnit; }
 template <int NT>
 __device__ __forceinline__ int row_blocks_of(const Request& q) {
@@ -389,7 +326,8 @@ __device__ __forceinline__ void scan_requests(const AttArgs& a, int64_t* start, 
   int64_t mine = 0;
   for (int r = r0; r < r1; ++r) {
     const Request q = request(a, r);
-    const int64_t w = static_cast<int64_t>(units_of(q)) * row_blocks_of<NT>(q) * a.heads;
+    const int64_t w =
+        q.n_rows > a.chunk_rows ? 0 : static_cast<int64_t>(units_of(q)) * row_blocks_of<NT>(q) * a.heads;
     start[r] = w;
     mine += w;
   }
@@ -624,7 +562,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D =
   // requests without cached tokens, and tokens of no request
   for (int r = blockIdx.x; r < a.n_requests; r += gridDim.x) {
     const Request q = request(a, r);
-    if (q.len == 0)
+    if (q.len == 0 && q.n_rows <= a.chunk_rows)
       for (int t = 0; t < q.n_rows / a.group; ++t) zero_row<D>(a, q.t0 + t, tid, kAttThreads);
   }
   for (int t = min(max(a.cu_q[a.n_requests], 0), a.n_tokens) + blockIdx.x; t < a.n_tokens; t += gridDim.x)
@@ -889,7 +827,12 @@ extern "C" TWELL_API int twell_kv_attention(const uint16_t* Q, int64_t ldq, cons
   a.page_shift = __builtin_ctz(cache->page_size);
   a.n_pages = cache->n_pages;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.chunk_rows = INT32_MAX;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (n_requests > 0 && static_cast<int64_t>(max_q_len) * a.group > kChunkRows) {
+    a.chunk_rows = kChunkRows;
+    KV_TRY(launch_chunk_attention(a, cache->format, cache->head_dim, s));
+  }
   return cache->format == TWELL_KV_E4M3 ? launch_dim<TWELL_KV_E4M3>(a, cache->head_dim, max_kv_len, max_q_len, workspace, s)
                                         : launch_dim<TWELL_KV_INT8>(a, cache->head_dim, max_kv_len, max_q_len, workspace, s);
 }

@@ -1,0 +1,79 @@
+// Shared by the two kernels of the attention over the 8-bit cache
+// (kv_attention.cu: few rows a request; kv_chunk.cu: many).
+#pragma once
+
+#include "kv_internal.h"
+
+namespace twell {
+
+struct AttArgs {
+  const uint16_t* q;
+  int64_t ldq;
+  const uint8_t *k, *v;
+  const float *k_scale, *v_scale;
+  const int32_t *block_table, *cu_q, *positions, *kv_lens;
+  uint16_t* o;
+  int64_t ldo;
+  float* lse;
+  int32_t* status;
+  int max_blocks, n_tokens, n_requests, q_heads, heads, group, page_shift, n_pages;
+  float scale_log2;  // softmax_scale * log2(e)
+  int chunk_rows;    // requests of more rows than this go to chunk_attention
+};
+
+// Requests of more than this many rows (tokens times query heads of a key head)
+// fill tcgen05's 128 rows well enough to pay for the fp16 copy of the cache
+// that its operands need; a.chunk_rows is this, or INT32_MAX when no request is that large.
+constexpr int kChunkRows = 64;
+int launch_chunk_attention(const AttArgs& a, int format, int dim, cudaStream_t s);
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four codes of one word to two fp16 pairs: (byte 0, byte 1) and (byte 2, byte 3).
+template <int FMT>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& p01, uint32_t& p23) {
+  if (FMT == TWELL_KV_E4M3) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(p01), "=r"(p23)
+        : "r"(w));
+  } else {
+    // 0x6400 | u is the fp16 number 1024 + u: with u = code + 128, minus 1152
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p01) : "r"(a), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(p23) : "r"(b), "r"(0x64806480u));
+  }
+}
+
+__device__ __forceinline__ int visible_len(const AttArgs& a, int r) {
+  const int64_t room = static_cast<int64_t>(a.max_blocks) << a.page_shift;
+  return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(a.kv_lens[r]), room)));
+}
+
+struct Request {
+  int t0, n_rows, len;
+};
+
+__device__ __forceinline__ Request request(const AttArgs& a, int r) {
+  const int t0 = min(max(a.cu_q[r], 0), a.n_tokens), t1 = min(max(a.cu_q[r + 1], t0), a.n_tokens);
+  return {t0, (t1 - t0) * a.group, visible_len(a, r)};
+}
+
+}  // namespace twell

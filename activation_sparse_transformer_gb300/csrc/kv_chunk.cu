@@ -1,0 +1,474 @@
+// Attention over the 8-bit cache for requests with many rows (prompt chunks) on
+// the 5th-generation tensor cores.
+//
+// One CTA takes 256 rows (token, query head) of one request and key head, as
+// two tiles of 128 rows, and walks over the cached tokens 128 at a time.
+// Thirteen warps work on it:
+//   warps 0-3, 4-7  softmax of tile 0 and 1, one thread a row
+//   warps 8-11      codes -> fp16 operands in shared memory, shared by both tiles
+//   warp 12         issues the mma's
+// For tile X and step t:  S_X = Q_X K_t^T (tcgen05, fp32 in TMEM);  w = 2^(S f_j +
+// log2 s_v - n) -> fp16 in TMEM over S;  O_X += w V_t (A from TMEM).  f_j is
+// the row's factor times the key scale and s_v the value scale of the token's
+// page; n follows the row's largest exponent lazily (when it is passed by 8, O
+// is rescaled).  The softmax's own sum needs w / s_v: it is taken per 16
+// tokens, which share a page.  While one tile is in its softmax the tensor cores work on
+// the other.
+//
+// 4 D flops for each (row, token): tensor cores bound it, then the exponentials
+// and the shared memory that feeds both operands of S.
+#include "kv_attention.h"
+
+namespace twell {
+namespace {
+
+constexpr int kTileRows = 128;
+constexpr int kBlockRows = 2 * kTileRows;
+constexpr int kTokens = 128;   // cached tokens of a step
+constexpr int kGroups = kTokens / 16;
+constexpr int kThreads = 13 * 32;
+constexpr float kLazy = 8.0f;
+
+template <int D>
+struct ChunkSmem {
+  static constexpr uint32_t kBlk = kTileRows * 128;        // 128 rows of 64 fp16, 128-byte swizzled
+  static constexpr uint32_t kQ = (D / 64) * kBlk;          // one tile
+  static constexpr uint32_t kK = (D / 64) * kBlk, kV = kK;
+  static constexpr uint32_t kKAt = 2 * kQ, kVAt = kKAt + 2 * kK, kScaleAt = kVAt + 2 * kV;
+  static constexpr uint32_t kBarAt = kScaleAt + 4 * 3 * kGroups * 4;
+  static constexpr uint32_t kBytes = kBarAt + 256;
+};
+
+// D[tmem] (+)= A * B^T, fp16 inputs, fp32 accumulation: A from shared memory ...
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// ... or from TMEM (two fp16 a column, row = lane).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  uint32_t lo[16], hi[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) lo[i] = r[i], hi[i] = r[16 + i];
+  tmem_st16(taddr, lo);
+  tmem_st16(taddr + 16, hi);
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+struct Barriers {
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], scale_full[4], s_full[2], p_full[2], o_done[2], drain;
+  uint32_t tmem;
+  int abort;
+  int most;
+};
+static_assert(sizeof(Barriers) <= 256, "barrier region");
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
+  using L = ChunkSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  grid_dependency_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int head = blockIdx.y;
+  // row blocks: request r has room for floor(cu[r + 1] G / 256) - floor(cu[r] G / 256) + 1;
+  // the last ones, which see the most, come first
+  const int64_t x = gridDim.x - 1 - blockIdx.x;
+  const auto first_block = [&](int i) {
+    return static_cast<int64_t>(min(max(a.cu_q[i], 0), a.n_tokens)) * a.group / kBlockRows + i;
+  };
+  const int r = warp_upper(a.n_requests, x, first_block);
+  const Request q = request(a, r);
+  const int row0 = static_cast<int>(x - first_block(r)) * kBlockRows;
+  if (q.n_rows <= a.chunk_rows || row0 >= q.n_rows) return;
+
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* const scales = reinterpret_cast<float*>(smem + L::kScaleAt);  // [4][key, log2 value, 1 / value][8]
+  Barriers& bar = *reinterpret_cast<Barriers*>(smem + L::kBarAt);
+  volatile int* const abort = &bar.abort;
+  const int n_tiles = q.n_rows - row0 > kTileRows ? 2 : 1;
+
+  if (tid == 0) {
+    mbar_init(&bar.q_full, kTileRows * n_tiles);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.k_full[i], 128);
+      mbar_init(&bar.v_full[i], 128);
+      mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.v_empty[i], 1);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], kTileRows);
+      mbar_init(&bar.o_done[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&bar.scale_full[i], 1);
+    mbar_init(&bar.drain, 1);
+    bar.abort = 0;
+    bar.most = 0;
+    mbar_fence_init();
+  }
+  if (warp == 12) tmem_alloc(&bar.tmem, 512);
+  __syncthreads();
+  // what each row sees, and the most that any row of the block does
+  int limit = 0;
+  const int row = row0 + tid;
+  if (tid < kBlockRows) {
+    if (row < q.n_rows) {
+      const int p = a.positions[q.t0 + row / a.group];
+      limit = max(0, min(p < INT32_MAX ? p + 1 : p, q.len));
+    }
+    int most = limit;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+    if (lane == 0) atomicMax(&bar.most, most);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const int most = bar.most, n_steps = (most + kTokens - 1) / kTokens;
+  const uint32_t tmem = bar.tmem;
+  const uint64_t limit_ns = kWaitLimitNs;
+  bool ok = true;
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    const int t_id = warp >> 2, r_in = tid & 127;
+    if (t_id < n_tiles) {
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t s_tm = tmem + lanes + t_id * 128, o_tm = tmem + lanes + 256 + t_id * D;
+      const int token = row / a.group, h = head * a.group + row % a.group;
+      float factor;
+      {
+        // the row as fp16, 2^-k q with its largest magnitude in [1, 2), in the
+        // swizzled layout of a K-major operand
+        uint4 w[D / 8];
+        const uint16_t* src = a.q + static_cast<int64_t>(q.t0 + token) * a.ldq + static_cast<int64_t>(h) * D;
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          w[i] = row < q.n_rows ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+          const uint32_t* u = &w[i].x;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(u[j])), fabsf(bf16_hi(u[j]))));
+        }
+        const int k = min(max((__float_as_int(amax) >> 23) - 127, -126), 126);
+        const float inv = __int_as_float((127 - k) << 23);
+        factor = a.scale_log2 * __int_as_float((127 + k) << 23);
+        uint8_t* const dst = smem + t_id * L::kQ + r_in * 128;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t* u = &w[i].x;
+          uint32_t f[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f[j] = pack_f16(bf16_lo(u[j]) * inv, bf16_hi(u[j]) * inv);
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * L::kBlk + (((i & 7) ^ (r_in & 7)) << 4)) =
+              make_uint4(f[0], f[1], f[2], f[3]);
+        }
+        fence_async_shared();
+        mbar_arrive(&bar.q_full);
+      }
+      float n = 0.0f, pass = -INFINITY, sum = 0.0f;  // the reference, what must be passed to move it, the sum
+      for (int t = 0; t < n_steps; ++t) {
+        ok = mbar_wait(&bar.s_full[t_id], t & 1, limit_ns, abort) &&
+             mbar_wait(&bar.scale_full[t & 3], (t >> 2) & 1, limit_ns, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const float* const sc = scales + (t & 3) * 3 * kGroups;
+        const int left = limit - t * kTokens;  // tokens of the step that the row sees
+        const bool mask = left < kTokens;
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tmem_ld32(s_tm + 32 * c, v);
+          tmem_ld_wait();
+          if (mask) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= left) v[i] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float m = __uint_as_float(v[16 * g]);
+#pragma unroll
+            for (int i = 1; i < 16; ++i) m = fmaxf(m, __uint_as_float(v[16 * g + i]));
+            const float e = fmaf(m, factor * sc[2 * c + g], sc[kGroups + 2 * c + g]);
+            top = fmaxf(top, m > -INFINITY ? e : -INFINITY);
+          }
+        }
+        const bool move = top > pass;
+        if (__any_sync(0xffffffffu, move)) {
+          // O holds the steps before this one: their mma's were waited for before this S was issued
+          float f = 1.0f;
+          if (move) {
+            f = sum == 0.0f ? 0.0f : exp2_fast(n - top);
+            sum *= f;
+            n = top;
+            pass = top + kLazy;
+          }
+          if (t > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(o_tm + 32 * c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+              tmem_st32(o_tm + 32 * c, v);
+            }
+          }
+        }
+        // w = 2^(S f + log2 s_v - n): fp16 over the columns of S already read
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32], p[16];
+          tmem_ld32(s_tm + 32 * c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const float f = factor * sc[2 * c + g], off = sc[kGroups + 2 * c + g] - n;
+            float part = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              float e[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float y = fmaf(__uint_as_float(v[16 * g + i + j]), f, off);
+                if (mask && 32 * c + 16 * g + i + j >= left) y = -INFINITY;
+                e[j] = exp2_fast(y);
+                part += e[j];
+              }
+              p[8 * g + i / 2] = pack_f16(e[0], e[1]);
+            }
+            sum = fmaf(part, sc[2 * kGroups + 2 * c + g], sum);
+          }
+          tmem_st16(s_tm + 16 * c, p);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bar.p_full[t_id]);
+      }
+      // the finished row
+      if (ok && n_steps > 0) ok = mbar_wait(&bar.o_done[t_id], (n_steps - 1) & 1, limit_ns, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
+      } else {
+        tc_fence_after();
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint16_t* const dst = a.o + static_cast<int64_t>(q.t0 + token) * a.ldo + static_cast<int64_t>(h) * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32] = {};
+          if (n_steps > 0) {
+            tmem_ld32(o_tm + 32 * c, v);
+            tmem_ld_wait();
+          }
+          if (row >= q.n_rows) continue;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              // a row that sees nothing divides by no sum: zeros
+              const float lo = sum != 0.0f ? __uint_as_float(v[8 * i + 2 * j]) * inv : 0.0f;
+              const float hi = sum != 0.0f ? __uint_as_float(v[8 * i + 2 * j + 1]) * inv : 0.0f;
+              w[j] = static_cast<uint32_t>(float_to_bf16_bits(lo)) | (static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16);
+            }
+            reinterpret_cast<uint4*>(dst + 32 * c)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (a.lse && row < q.n_rows)
+          a.lse[static_cast<int64_t>(q.t0 + token) * a.q_heads + h] =
+              sum != 0.0f ? (n + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+      }
+    }
+  } else if (warp < 12) {
+    // ---------------------------------------------------------------- codes to operands
+    constexpr int kLanes = D / 16;                 // lanes of a token, 16 codes each
+    constexpr int kPass = 128 / kLanes;            // tokens of a pass of the four warps
+    constexpr int kPasses = kTokens / kPass;
+    const int dw = warp - 8, tok = (tid - 256) / kLanes, cc = lane % kLanes;
+    const int blk = cc >> 2, even = (2 * cc) & 7;
+    const int page_mask = (1 << a.page_shift) - 1;
+    const int32_t* const table = a.block_table + static_cast<int64_t>(r) * a.max_blocks;
+    // lane l < 8: the page of the step's l-th group of 16 tokens
+    const auto pages_of = [&](int t) {
+      const int64_t j = static_cast<int64_t>(t) * kTokens + lane * 16;
+      int page = 0;
+      if (lane < kGroups && j < q.len) {
+        page = table[j >> a.page_shift];
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.n_pages)) {
+          report_error(a.status, TWELL_ERR_BAD_FORMAT);
+          page = 0;
+        }
+      }
+      return page;
+    };
+    const auto load = [&](const uint8_t* codes, int t, int pages, uint4 (&w)[kPasses]) {
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int tk = i * kPass + tok, j = t * kTokens + tk;
+        const int64_t page = __shfl_sync(0xffffffffu, pages, tk >> 4);
+        // past the request's tokens a page may hold anything: zeros
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (j < q.len)
+          w[i] = __ldg(reinterpret_cast<const uint4*>(
+              codes + (((page * a.heads + head) << a.page_shift) + (j & page_mask)) * D + 16 * cc));
+      }
+    };
+    const auto store = [&](uint8_t* dst, uint32_t half, const uint4 (&w)[kPasses]) {
+      // half: bytes between the two 64-token halves of a value tile (a key tile has its tokens in one run)
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int tk = i * kPass + tok;
+        uint32_t f[8];
+        codes_to_f16<FMT>(w[i].x, f[0], f[1]);
+        codes_to_f16<FMT>(w[i].y, f[2], f[3]);
+        codes_to_f16<FMT>(w[i].z, f[4], f[5]);
+        codes_to_f16<FMT>(w[i].w, f[6], f[7]);
+        uint8_t* const at = half ? dst + (tk >> 6) * half + blk * 8192 + (tk & 63) * 128
+                                 : dst + blk * L::kBlk + tk * 128;
+        // the lanes of the second 64 dims start with the odd piece: no bank meets another
+        const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]), hi = make_uint4(f[4], f[5], f[6], f[7]);
+        *reinterpret_cast<uint4*>(at + (((even + blk) ^ (tk & 7)) << 4)) = blk ? hi : lo;
+        *reinterpret_cast<uint4*>(at + (((even + 1 - blk) ^ (tk & 7)) << 4)) = blk ? lo : hi;
+      }
+      fence_async_shared();
+    };
+    uint4 kw[kPasses], vw[kPasses];
+    int pages = pages_of(0);
+    if (n_steps > 0) {
+      load(a.k, 0, pages, kw);
+      load(a.v, 0, pages, vw);
+    }
+    for (int t = 0; t < n_steps; ++t) {
+      const int st = t & 1;
+      const int next = pages_of(t + 1);
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.k_empty[st], ((t >> 1) & 1) ^ 1, limit_ns, abort));
+      if (!ok) break;
+      if (dw == 0) {
+        // a slot of four: the step four before has been through both softmaxes
+        if (lane < kGroups) {
+          const bool on = t * kTokens + lane * 16 < q.len;
+          const int64_t cell = static_cast<int64_t>(pages) * a.heads + head;
+          const float ks = on ? a.k_scale[cell] : 1.0f, vs = on ? a.v_scale[cell] : 1.0f;
+          float* const sc = scales + (t & 3) * 3 * kGroups + lane;
+          sc[0] = ks;
+          sc[kGroups] = fmaxf(log2_fast(vs), -200.0f);
+          sc[2 * kGroups] = 1.0f / vs;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.scale_full[t & 3]);
+      }
+      store(smem + L::kKAt + st * L::kK, 0, kw);
+      mbar_arrive(&bar.k_full[st]);
+      if (t + 1 < n_steps) load(a.k, t + 1, next, kw);
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.v_empty[st], ((t >> 1) & 1) ^ 1, limit_ns, abort));
+      if (!ok) break;
+      store(smem + L::kVAt + st * L::kV, (D / 64) * 8192, vw);
+      mbar_arrive(&bar.v_full[st]);
+      if (t + 1 < n_steps) load(a.v, t + 1, next, vw);
+      pages = next;
+    }
+    if (!ok) report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
+  } else if (lane == 0 && n_steps > 0) {
+    // ---------------------------------------------------------------- mma's
+    constexpr uint32_t kShape = (1u << 4) | (8u << 24);  // fp32 result, fp16 operands, 128 rows
+    constexpr uint32_t kIdescS = kShape | ((kTokens >> 3) << 17);
+    constexpr uint32_t kIdescO = kShape | (static_cast<uint32_t>(D >> 3) << 17) | (1u << 16);  // V: dims run fastest
+    bool issued = false;
+    const auto scores = [&](int t, int x_id) {
+      const uint64_t qd = smem_desc_sw128(smem_u32(smem + x_id * L::kQ));
+      const uint64_t kd = smem_desc_sw128(smem_u32(smem + L::kKAt + (t & 1) * L::kK));
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t step = (k >> 2) * (L::kBlk >> 4) + 2 * (k & 3);
+        mma_ss(tmem + x_id * 128, qd + step, kd + step, kIdescS, k > 0);
+      }
+      mma_commit(&bar.s_full[x_id]);
+    };
+    const auto values = [&](int t, int x_id) {
+      const uint64_t vd = smem_desc_sw128_nmajor(smem_u32(smem + L::kVAt + (t & 1) * L::kV), 8192);
+#pragma unroll
+      for (int k = 0; k < kTokens / 16; ++k)
+        mma_ts(tmem + 256 + x_id * D, tmem + x_id * 128 + 8 * k,
+               vd + (k >> 2) * ((D / 64) * 8192 >> 4) + 128 * (k & 3), kIdescO, t > 0 || k > 0);
+      mma_commit(&bar.o_done[x_id]);
+    };
+    ok = mbar_wait(&bar.q_full, 0, limit_ns, abort);
+    for (int t = 0; ok && t <= n_steps; ++t) {
+      if (t < n_steps) ok = mbar_wait(&bar.k_full[t & 1], (t >> 1) & 1, limit_ns, abort);
+      for (int x_id = 0; ok && x_id < n_tiles; ++x_id) {
+        if (t > 0) {
+          // O of the step before; its weights lie over S, so the next S waits for it
+          ok = (x_id > 0 || mbar_wait(&bar.v_full[(t - 1) & 1], ((t - 1) >> 1) & 1, limit_ns, abort)) &&
+               mbar_wait(&bar.p_full[x_id], (t - 1) & 1, limit_ns, abort);
+          if (!ok) break;
+          tc_fence_after();
+          values(t - 1, x_id);
+          issued = true;
+          if (x_id == n_tiles - 1) mma_commit(&bar.v_empty[(t - 1) & 1]);
+          if (t < n_steps) ok = mbar_wait(&bar.o_done[x_id], (t - 1) & 1, limit_ns, abort);
+          if (!ok) break;
+        }
+        if (t < n_steps) {
+          tc_fence_after();
+          scores(t, x_id);
+          issued = true;
+          if (x_id == n_tiles - 1) mma_commit(&bar.k_empty[t & 1]);
+        }
+      }
+    }
+    if (!ok) {
+      report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
+      if (issued) {
+        // wait for the mma's already issued before TMEM is released
+        mma_commit(&bar.drain);
+        volatile int never = 0;
+        mbar_wait(&bar.drain, 0, 10000000ull, &never);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int FMT, int D>
+int launch(const AttArgs& a, cudaStream_t s) {
+  constexpr size_t smem = ChunkSmem<D>::kBytes + 1024;
+  KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(chunk_kernel<FMT, D>), static_cast<int>(smem)));
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.n_tokens) * a.group / kBlockRows + a.n_requests),
+                  static_cast<unsigned>(a.heads));
+  LaunchScope scope(TWELL_KERNEL_KV_ATTENTION, s);
+  return launch_pdl(chunk_kernel<FMT, D>, grid, dim3(kThreads), smem, s, a) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_chunk_attention(const AttArgs& a, int format, int dim, cudaStream_t s) {
+  if (format == TWELL_KV_E4M3) return dim == 64 ? launch<TWELL_KV_E4M3, 64>(a, s) : launch<TWELL_KV_E4M3, 128>(a, s);
+  return dim == 64 ? launch<TWELL_KV_INT8, 64>(a, s) : launch<TWELL_KV_INT8, 128>(a, s);
+}
+
+}  // namespace twell
