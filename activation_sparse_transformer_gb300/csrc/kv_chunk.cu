@@ -3,10 +3,10 @@
 //
 // One CTA takes 256 rows (token, query head) of one request and key head, as
 // two tiles of 128 rows, and walks over the cached tokens 128 at a time.
-// Thirteen warps work on it:
+// Four warpgroups work on it:
 //   warps 0-3, 4-7  softmax of tile 0 and 1, one thread a row
 //   warps 8-11      codes -> fp16 operands in shared memory, shared by both tiles
-//   warp 12         issues the mma's
+//   warp 12         issues the mma's (13-15 only lend their registers)
 // For tile X and step t:  S_X = Q_X K_t^T (tcgen05, fp32 in TMEM);  w = 2^(S f_j +
 // log2 s_v - n) -> fp16 in TMEM over S;  O_X += w V_t (A from TMEM).  f_j is
 // the row's factor times the key scale and s_v the value scale of the token's
@@ -17,6 +17,8 @@
 //
 // 4 D flops for each (row, token): tensor cores bound it, then the exponentials
 // and the shared memory that feeds both operands of S.
+#include <cfloat>
+
 #include "kv_attention.h"
 
 namespace twell {
@@ -26,7 +28,11 @@ constexpr int kTileRows = 128;
 constexpr int kBlockRows = 2 * kTileRows;
 constexpr int kTokens = 128;   // cached tokens of a step
 constexpr int kGroups = kTokens / 16;
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 16 * 32;
+// Registers a thread of each warpgroup (softmax 0, softmax 1, operands, mma's):
+// together the 4 x 128 that the launch gives.
+constexpr int kRegsSoftmax = 176, kRegsOperands = 112, kRegsMma = 48;
+static_assert(2 * kRegsSoftmax + kRegsOperands + kRegsMma == 4 * 128, "register split");
 constexpr float kLazy = 8.0f;
 
 template <int D>
@@ -64,14 +70,31 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  uint32_t lo[16], hi[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) lo[i] = r[i], hi[i] = r[16 + i];
-  tmem_st16(taddr, lo);
-  tmem_st16(taddr + 16, hi);
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Two fp32 lanes of one instruction.
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float f, float c) {
+  asm("{\n\t.reg .b64 v, m, k;\n\tmov.b64 v, {%2, %3};\n\tmov.b64 m, {%4, %4};\n\tmov.b64 k, {%5, %5};\n\t"
+      "fma.rn.f32x2 v, v, m, k;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(f), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\t"
+      "add.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
 
 struct Barriers {
   uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], scale_full[4], s_full[2], p_full[2], o_done[2], drain;
@@ -147,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
+    more_registers<kRegsSoftmax>();
     const int t_id = warp >> 2, r_in = tid & 127;
     if (t_id < n_tiles) {
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -190,27 +214,32 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
         if (!ok) break;
         tc_fence_after();
         const float* const sc = scales + (t & 3) * 3 * kGroups;
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, v[c]);
+        float ks[kGroups], lvs[kGroups], ivs[kGroups];
+#pragma unroll
+        for (int i = 0; i < kGroups; i += 4) {
+          *reinterpret_cast<float4*>(ks + i) = *reinterpret_cast<const float4*>(sc + i);
+          *reinterpret_cast<float4*>(lvs + i) = *reinterpret_cast<const float4*>(sc + kGroups + i);
+          *reinterpret_cast<float4*>(ivs + i) = *reinterpret_cast<const float4*>(sc + 2 * kGroups + i);
+        }
+        tmem_ld_wait();
         const int left = limit - t * kTokens;  // tokens of the step that the row sees
-        const bool mask = left < kTokens;
+        if (left < kTokens) {
+#pragma unroll
+          for (int i = 0; i < kTokens; ++i)
+            if (i >= left) v[i / 32][i % 32] = 0xFF800000u;
+        }
         float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tmem_ld32(s_tm + 32 * c, v);
-          tmem_ld_wait();
-          if (mask) {
+        for (int g = 0; g < kGroups; ++g) {
+          const uint32_t* const u = &v[g / 2][16 * (g % 2)];
+          float m = __uint_as_float(u[0]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= left) v[i] = 0xFF800000u;
-          }
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            float m = __uint_as_float(v[16 * g]);
-#pragma unroll
-            for (int i = 1; i < 16; ++i) m = fmaxf(m, __uint_as_float(v[16 * g + i]));
-            const float e = fmaf(m, factor * sc[2 * c + g], sc[kGroups + 2 * c + g]);
-            top = fmaxf(top, m > -INFINITY ? e : -INFINITY);
-          }
+          for (int i = 1; i < 16; ++i) m = fmaxf(m, __uint_as_float(u[i]));
+          ks[g] *= factor;
+          top = fmaxf(top, fmaf(m, ks[g], lvs[g]));
         }
         const bool move = top > pass;
         if (__any_sync(0xffffffffu, move)) {
@@ -224,39 +253,35 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
           }
           if (t > 0) {
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t v[32];
-              tmem_ld32(o_tm + 32 * c, v);
+            for (int c = 0; c < D / 8; ++c) {
+              uint32_t o[8];
+              tmem_ld8(o_tm + 8 * c, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-              tmem_st32(o_tm + 32 * c, v);
+              for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st8(o_tm + 8 * c, o);
             }
           }
         }
-        // w = 2^(S f + log2 s_v - n): fp16 over the columns of S already read
+        // w = 2^(S f + log2 s_v - n): fp16 over the columns of S
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t v[32], p[16];
-          tmem_ld32(s_tm + 32 * c, v);
-          tmem_ld_wait();
+          uint32_t p[16];
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float f = factor * sc[2 * c + g], off = sc[kGroups + 2 * c + g] - n;
-            float part = 0.0f;
+          for (int g = 2 * c; g < 2 * c + 2; ++g) {
+            const uint32_t* const u = &v[c][16 * (g % 2)];
+            const float off = lvs[g] - n;
+            float part[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-              float e[2];
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                float y = fmaf(__uint_as_float(v[16 * g + i + j]), f, off);
-                if (mask && 32 * c + 16 * g + i + j >= left) y = -INFINITY;
-                e[j] = exp2_fast(y);
-                part += e[j];
-              }
-              p[8 * g + i / 2] = pack_f16(e[0], e[1]);
+              float e0, e1;
+              fma2(e0, e1, __uint_as_float(u[i]), __uint_as_float(u[i + 1]), ks[g], off);
+              e0 = exp2_fast(e0);
+              e1 = exp2_fast(e1);
+              add2(part[0], part[1], e0, e1);
+              p[8 * (g % 2) + i / 2] = pack_f16(e0, e1);
             }
-            sum = fmaf(part, sc[2 * kGroups + 2 * c + g], sum);
+            sum = fmaf(part[0] + part[1], ivs[g], sum);
           }
           tmem_st16(s_tm + 16 * c, p);
         }
@@ -301,11 +326,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
     }
   } else if (warp < 12) {
     // ---------------------------------------------------------------- codes to operands
+    fewer_registers<kRegsOperands>();
     constexpr int kLanes = D / 16;                 // lanes of a token, 16 codes each
     constexpr int kPass = 128 / kLanes;            // tokens of a pass of the four warps
     constexpr int kPasses = kTokens / kPass;
-    const int dw = warp - 8, tok = (tid - 256) / kLanes, cc = lane % kLanes;
-    const int blk = cc >> 2, even = (2 * cc) & 7;
+    // 8 lanes that store together hold 64 dims of two neighbouring tokens: their
+    // swizzled 16-byte pieces lie in different banks
+    const int dw = warp - 8, blk = D == 128 ? lane >> 4 : 0, cc = blk * 4 + (lane & 3), even = 2 * (lane & 3);
+    const int tok = dw * (32 / kLanes) + (D == 128 ? (lane >> 2) & 3 : lane >> 2);
     const int page_mask = (1 << a.page_shift) - 1;
     const int32_t* const table = a.block_table + static_cast<int64_t>(r) * a.max_blocks;
     // lane l < 8: the page of the step's l-th group of 16 tokens
@@ -345,10 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
         codes_to_f16<FMT>(w[i].w, f[6], f[7]);
         uint8_t* const at = half ? dst + (tk >> 6) * half + blk * 8192 + (tk & 63) * 128
                                  : dst + blk * L::kBlk + tk * 128;
-        // the lanes of the second 64 dims start with the odd piece: no bank meets another
-        const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]), hi = make_uint4(f[4], f[5], f[6], f[7]);
-        *reinterpret_cast<uint4*>(at + (((even + blk) ^ (tk & 7)) << 4)) = blk ? hi : lo;
-        *reinterpret_cast<uint4*>(at + (((even + 1 - blk) ^ (tk & 7)) << 4)) = blk ? lo : hi;
+        *reinterpret_cast<uint4*>(at + ((even ^ (tk & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<uint4*>(at + (((even + 1) ^ (tk & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
       }
       fence_async_shared();
     };
@@ -370,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
           const int64_t cell = static_cast<int64_t>(pages) * a.heads + head;
           const float ks = on ? a.k_scale[cell] : 1.0f, vs = on ? a.v_scale[cell] : 1.0f;
           float* const sc = scales + (t & 3) * 3 * kGroups + lane;
-          sc[0] = ks;
+          sc[0] = fmaxf(ks, FLT_MIN);  // a masked S of -inf stays so
           sc[kGroups] = fmaxf(log2_fast(vs), -200.0f);
           sc[2 * kGroups] = 1.0f / vs;
         }
@@ -388,61 +414,64 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
       pages = next;
     }
     if (!ok) report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
-  } else if (lane == 0 && n_steps > 0) {
+  } else {
     // ---------------------------------------------------------------- mma's
-    constexpr uint32_t kShape = (1u << 4) | (8u << 24);  // fp32 result, fp16 operands, 128 rows
-    constexpr uint32_t kIdescS = kShape | ((kTokens >> 3) << 17);
-    constexpr uint32_t kIdescO = kShape | (static_cast<uint32_t>(D >> 3) << 17) | (1u << 16);  // V: dims run fastest
-    bool issued = false;
-    const auto scores = [&](int t, int x_id) {
-      const uint64_t qd = smem_desc_sw128(smem_u32(smem + x_id * L::kQ));
-      const uint64_t kd = smem_desc_sw128(smem_u32(smem + L::kKAt + (t & 1) * L::kK));
+    fewer_registers<kRegsMma>();
+    if (warp == 12 && lane == 0 && n_steps > 0) {
+      constexpr uint32_t kShape = (1u << 4) | (8u << 24);  // fp32 result, fp16 operands, 128 rows
+      constexpr uint32_t kIdescS = kShape | ((kTokens >> 3) << 17);
+      constexpr uint32_t kIdescO = kShape | (static_cast<uint32_t>(D >> 3) << 17) | (1u << 16);  // V: dims run fastest
+      bool issued = false;
+      const auto scores = [&](int t, int x_id) {
+        const uint64_t qd = smem_desc_sw128(smem_u32(smem + x_id * L::kQ));
+        const uint64_t kd = smem_desc_sw128(smem_u32(smem + L::kKAt + (t & 1) * L::kK));
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint64_t step = (k >> 2) * (L::kBlk >> 4) + 2 * (k & 3);
-        mma_ss(tmem + x_id * 128, qd + step, kd + step, kIdescS, k > 0);
-      }
-      mma_commit(&bar.s_full[x_id]);
-    };
-    const auto values = [&](int t, int x_id) {
-      const uint64_t vd = smem_desc_sw128_nmajor(smem_u32(smem + L::kVAt + (t & 1) * L::kV), 8192);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t step = (k >> 2) * (L::kBlk >> 4) + 2 * (k & 3);
+          mma_ss(tmem + x_id * 128, qd + step, kd + step, kIdescS, k > 0);
+        }
+        mma_commit(&bar.s_full[x_id]);
+      };
+      const auto values = [&](int t, int x_id) {
+        const uint64_t vd = smem_desc_sw128_nmajor(smem_u32(smem + L::kVAt + (t & 1) * L::kV), 8192);
 #pragma unroll
-      for (int k = 0; k < kTokens / 16; ++k)
-        mma_ts(tmem + 256 + x_id * D, tmem + x_id * 128 + 8 * k,
-               vd + (k >> 2) * ((D / 64) * 8192 >> 4) + 128 * (k & 3), kIdescO, t > 0 || k > 0);
-      mma_commit(&bar.o_done[x_id]);
-    };
-    ok = mbar_wait(&bar.q_full, 0, limit_ns, abort);
-    for (int t = 0; ok && t <= n_steps; ++t) {
-      if (t < n_steps) ok = mbar_wait(&bar.k_full[t & 1], (t >> 1) & 1, limit_ns, abort);
-      for (int x_id = 0; ok && x_id < n_tiles; ++x_id) {
-        if (t > 0) {
-          // O of the step before; its weights lie over S, so the next S waits for it
-          ok = (x_id > 0 || mbar_wait(&bar.v_full[(t - 1) & 1], ((t - 1) >> 1) & 1, limit_ns, abort)) &&
-               mbar_wait(&bar.p_full[x_id], (t - 1) & 1, limit_ns, abort);
-          if (!ok) break;
-          tc_fence_after();
-          values(t - 1, x_id);
-          issued = true;
-          if (x_id == n_tiles - 1) mma_commit(&bar.v_empty[(t - 1) & 1]);
-          if (t < n_steps) ok = mbar_wait(&bar.o_done[x_id], (t - 1) & 1, limit_ns, abort);
-          if (!ok) break;
-        }
-        if (t < n_steps) {
-          tc_fence_after();
-          scores(t, x_id);
-          issued = true;
-          if (x_id == n_tiles - 1) mma_commit(&bar.k_empty[t & 1]);
+        for (int k = 0; k < kTokens / 16; ++k)
+          mma_ts(tmem + 256 + x_id * D, tmem + x_id * 128 + 8 * k,
+                 vd + (k >> 2) * ((D / 64) * 8192 >> 4) + 128 * (k & 3), kIdescO, t > 0 || k > 0);
+        mma_commit(&bar.o_done[x_id]);
+      };
+      ok = mbar_wait(&bar.q_full, 0, limit_ns, abort);
+      for (int t = 0; ok && t <= n_steps; ++t) {
+        if (t < n_steps) ok = mbar_wait(&bar.k_full[t & 1], (t >> 1) & 1, limit_ns, abort);
+        for (int x_id = 0; ok && x_id < n_tiles; ++x_id) {
+          if (t > 0) {
+            // O of the step before; its weights lie over S, so the next S waits for it
+            ok = (x_id > 0 || mbar_wait(&bar.v_full[(t - 1) & 1], ((t - 1) >> 1) & 1, limit_ns, abort)) &&
+                 mbar_wait(&bar.p_full[x_id], (t - 1) & 1, limit_ns, abort);
+            if (!ok) break;
+            tc_fence_after();
+            values(t - 1, x_id);
+            issued = true;
+            if (x_id == n_tiles - 1) mma_commit(&bar.v_empty[(t - 1) & 1]);
+            if (t < n_steps) ok = mbar_wait(&bar.o_done[x_id], (t - 1) & 1, limit_ns, abort);
+            if (!ok) break;
+          }
+          if (t < n_steps) {
+            tc_fence_after();
+            scores(t, x_id);
+            issued = true;
+            if (x_id == n_tiles - 1) mma_commit(&bar.k_empty[t & 1]);
+          }
         }
       }
-    }
-    if (!ok) {
-      report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
-      if (issued) {
-        // wait for the mma's already issued before TMEM is released
-        mma_commit(&bar.drain);
-        volatile int never = 0;
-        mbar_wait(&bar.drain, 0, 10000000ull, &never);
+      if (!ok) {
+        report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
+        if (issued) {
+          // wait for the mma's already issued before TMEM is released
+          mma_commit(&bar.drain);
+          volatile int never = 0;
+          mbar_wait(&bar.drain, 0, 10000000ull, &never);
+        }
       }
     }
   }
