@@ -6,7 +6,8 @@
 // Four warpgroups work on it:
 //   warps 0-3, 4-7  softmax of tile 0 and 1, one thread a row
 //   warps 8-11      codes -> fp16 operands in shared memory, shared by both tiles
-//   warp 12         issues the mma's (13-15 only lend their registers)
+//   warp 12         issues the mma's
+//   warp 13         copies the codes to shared memory a step ahead
 // For tile X and step t:  S_X = Q_X K_t^T (tcgen05, fp32 in TMEM);  w = 2^(S f_j +
 // log2 s_v - n) -> fp16 in TMEM over S;  O_X += w V_t (A from TMEM).  f_j is
 // the row's factor times the key scale and s_v the value scale of the token's
@@ -31,7 +32,7 @@ constexpr int kGroups = kTokens / 16;
 constexpr int kThreads = 16 * 32;
 // Registers a thread of each warpgroup (softmax 0, softmax 1, operands, mma's):
 // together the 4 x 128 that the launch gives.
-constexpr int kRegsSoftmax = 176, kRegsOperands = 112, kRegsMma = 48;
+constexpr int kRegsSoftmax = 184, kRegsOperands = 88, kRegsMma = 56;
 static_assert(2 * kRegsSoftmax + kRegsOperands + kRegsMma == 4 * 128, "register split");
 constexpr float kLazy = 8.0f;
 
@@ -40,25 +41,44 @@ struct ChunkSmem {
   static constexpr uint32_t kBlk = kTileRows * 128;        // 128 rows of 64 fp16, 128-byte swizzled
   static constexpr uint32_t kQ = (D / 64) * kBlk;          // one tile
   static constexpr uint32_t kK = (D / 64) * kBlk, kV = kK;
-  static constexpr uint32_t kKAt = 2 * kQ, kVAt = kKAt + 2 * kK, kScaleAt = kVAt + 2 * kV;
+  static constexpr uint32_t kKAt = 2 * kQ, kVAt = kKAt + 2 * kK;
+  static constexpr uint32_t kRawAt = kVAt + 2 * kV, kRaw = kTokens * D;  // codes of a step's keys, of its values
+  static constexpr uint32_t kScaleAt = kRawAt + 2 * kRaw;
   static constexpr uint32_t kBarAt = kScaleAt + 4 * 3 * kGroups * 4;
   static constexpr uint32_t kBytes = kBarAt + 256;
 };
 
+// The issuing warp stays converged and one elected lane issues: the operands
+// then sit in uniform registers, without a move for each of them (an issue
+// from a lane's own branch took as long as the mma itself).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
 // D[tmem] (+)= A * B^T, fp16 inputs, fp32 accumulation: A from shared memory ...
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
 // ... or from TMEM (two fp16 a column, row = lane).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(leader)
       : "memory");
 }
 
@@ -97,6 +117,7 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
 }
 
 struct Barriers {
+  uint64_t raw_full[2], raw_empty[2];  // keys' codes, values' codes
   uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], scale_full[4], s_full[2], p_full[2], o_done[2], drain;
   uint32_t tmem;
   int abort;
@@ -109,7 +130,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
   using L = ChunkSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   grid_dependency_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, for the compiler too
   const int head = blockIdx.y;
   // row blocks: request r has room for floor(cu[r + 1] G / 256) - floor(cu[r] G / 256) + 1;
   // the last ones, which see the most, come first
@@ -131,6 +153,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
   if (tid == 0) {
     mbar_init(&bar.q_full, kTileRows * n_tiles);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.raw_full[i], kGroups);
+      mbar_init(&bar.raw_empty[i], 128);
       mbar_init(&bar.k_full[i], 128);
       mbar_init(&bar.v_full[i], 128);
       mbar_init(&bar.k_empty[i], 1);
@@ -139,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
       mbar_init(&bar.p_full[i], kTileRows);
       mbar_init(&bar.o_done[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&bar.scale_full[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&bar.scale_full[i], kGroups);
     mbar_init(&bar.drain, 1);
     bar.abort = 0;
     bar.most = 0;
@@ -164,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
   __syncthreads();
   tc_fence_after();
   const int most = bar.most, n_steps = (most + kTokens - 1) / kTokens;
-  const uint32_t tmem = bar.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
   const uint64_t limit_ns = kWaitLimitNs;
   bool ok = true;
 
@@ -330,39 +354,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
     constexpr int kLanes = D / 16;                 // lanes of a token, 16 codes each
     constexpr int kPass = 128 / kLanes;            // tokens of a pass of the four warps
     constexpr int kPasses = kTokens / kPass;
-    // 8 lanes that store together hold 64 dims of two neighbouring tokens: their
-    // swizzled 16-byte pieces lie in different banks
-    const int dw = warp - 8, blk = D == 128 ? lane >> 4 : 0, cc = blk * 4 + (lane & 3), even = 2 * (lane & 3);
-    const int tok = dw * (32 / kLanes) + (D == 128 ? (lane >> 2) & 3 : lane >> 2);
-    const int page_mask = (1 << a.page_shift) - 1;
-    const int32_t* const table = a.block_table + static_cast<int64_t>(r) * a.max_blocks;
-    // lane l < 8: the page of the step's l-th group of 16 tokens
-    const auto pages_of = [&](int t) {
-      const int64_t j = static_cast<int64_t>(t) * kTokens + lane * 16;
-      int page = 0;
-      if (lane < kGroups && j < q.len) {
-        page = table[j >> a.page_shift];
-        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.n_pages)) {
-          report_error(a.status, TWELL_ERR_BAD_FORMAT);
-          page = 0;
-        }
-      }
-      return page;
-    };
-    const auto load = [&](const uint8_t* codes, int t, int pages, uint4 (&w)[kPasses]) {
+    // The 8 lanes that access shared memory together hold 64 dims each of two
+    // neighbouring tokens, the first 64 of one and the last 64 of the other: neither
+    // the codes (128 bytes a token) nor the swizzled fp16 pieces share a bank.
+    const int dw = warp - 8, half = (lane >> 2) & 1, oct = lane >> 3;
+    const int blk = D == 128 ? half ^ (oct & 1) : 0, even = 2 * (lane & 3);
+    const int tok = dw * (32 / kLanes) + (D == 128 ? (oct >> 1) * 2 + half : lane >> 2);
+    const auto load = [&](int v, int t, uint4 (&w)[kPasses]) {
+      const uint8_t* const raw = smem + L::kRawAt + v * L::kRaw + blk * 64 + (lane & 3) * 16;
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const int tk = i * kPass + tok, j = t * kTokens + tk;
-        const int64_t page = __shfl_sync(0xffffffffu, pages, tk >> 4);
+      for (int i = 0; i < kPasses; ++i) w[i] = *reinterpret_cast<const uint4*>(raw + (i * kPass + tok) * D);
+      if ((t + 1) * kTokens > q.len) {
         // past the request's tokens a page may hold anything: zeros
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (j < q.len)
-          w[i] = __ldg(reinterpret_cast<const uint4*>(
-              codes + (((page * a.heads + head) << a.page_shift) + (j & page_mask)) * D + 16 * cc));
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i)
+          if (t * kTokens + i * kPass + tok >= q.len) w[i] = make_uint4(0, 0, 0, 0);
       }
     };
-    const auto store = [&](uint8_t* dst, uint32_t half, const uint4 (&w)[kPasses]) {
-      // half: bytes between the two 64-token halves of a value tile (a key tile has its tokens in one run)
+    const auto store = [&](uint8_t* dst, uint32_t halves, const uint4 (&w)[kPasses]) {
+      // halves: bytes between the two 64-token halves of a value tile (a key tile has its tokens in one run)
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
         const int tk = i * kPass + tok;
@@ -371,53 +381,41 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
         codes_to_f16<FMT>(w[i].y, f[2], f[3]);
         codes_to_f16<FMT>(w[i].z, f[4], f[5]);
         codes_to_f16<FMT>(w[i].w, f[6], f[7]);
-        uint8_t* const at = half ? dst + (tk >> 6) * half + blk * 8192 + (tk & 63) * 128
-                                 : dst + blk * L::kBlk + tk * 128;
+        uint8_t* const at = halves ? dst + (tk >> 6) * halves + blk * 8192 + (tk & 63) * 128
+                                   : dst + blk * L::kBlk + tk * 128;
         *reinterpret_cast<uint4*>(at + ((even ^ (tk & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
         *reinterpret_cast<uint4*>(at + (((even + 1) ^ (tk & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
       }
       fence_async_shared();
     };
-    uint4 kw[kPasses], vw[kPasses];
-    int pages = pages_of(0);
-    if (n_steps > 0) {
-      load(a.k, 0, pages, kw);
-      load(a.v, 0, pages, vw);
-    }
     for (int t = 0; t < n_steps; ++t) {
       const int st = t & 1;
-      const int next = pages_of(t + 1);
-      ok = __all_sync(0xffffffffu, mbar_wait(&bar.k_empty[st], ((t >> 1) & 1) ^ 1, limit_ns, abort));
-      if (!ok) break;
-      if (dw == 0) {
-        // a slot of four: the step four before has been through both softmaxes
-        if (lane < kGroups) {
-          const bool on = t * kTokens + lane * 16 < q.len;
-          const int64_t cell = static_cast<int64_t>(pages) * a.heads + head;
-          const float ks = on ? a.k_scale[cell] : 1.0f, vs = on ? a.v_scale[cell] : 1.0f;
-          float* const sc = scales + (t & 3) * 3 * kGroups + lane;
-          sc[0] = fmaxf(ks, FLT_MIN);  // a masked S of -inf stays so
-          sc[kGroups] = fmaxf(log2_fast(vs), -200.0f);
-          sc[2 * kGroups] = 1.0f / vs;
+      uint4 w[kPasses];
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bar.raw_full[v], t & 1, limit_ns, abort));
+        if (!ok) break;
+        load(v, t, w);
+        mbar_arrive(&bar.raw_empty[v]);
+        ok = __all_sync(0xffffffffu, mbar_wait(v ? &bar.v_empty[st] : &bar.k_empty[st], ((t >> 1) & 1) ^ 1, limit_ns,
+                                               abort));
+        if (!ok) break;
+        if (v == 0) {
+          store(smem + L::kKAt + st * L::kK, 0, w);
+          mbar_arrive(&bar.k_full[st]);
+        } else {
+          store(smem + L::kVAt + st * L::kV, (D / 64) * 8192, w);
+          mbar_arrive(&bar.v_full[st]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.scale_full[t & 3]);
       }
-      store(smem + L::kKAt + st * L::kK, 0, kw);
-      mbar_arrive(&bar.k_full[st]);
-      if (t + 1 < n_steps) load(a.k, t + 1, next, kw);
-      ok = __all_sync(0xffffffffu, mbar_wait(&bar.v_empty[st], ((t >> 1) & 1) ^ 1, limit_ns, abort));
       if (!ok) break;
-      store(smem + L::kVAt + st * L::kV, (D / 64) * 8192, vw);
-      mbar_arrive(&bar.v_full[st]);
-      if (t + 1 < n_steps) load(a.v, t + 1, next, vw);
-      pages = next;
     }
     if (!ok) report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
   } else {
     // ---------------------------------------------------------------- mma's
     fewer_registers<kRegsMma>();
-    if (warp == 12 && lane == 0 && n_steps > 0) {
+    if (warp == 12 && n_steps > 0) {
+      const uint32_t leader = elect_one();
       constexpr uint32_t kShape = (1u << 4) | (8u << 24);  // fp32 result, fp16 operands, 128 rows
       constexpr uint32_t kIdescS = kShape | ((kTokens >> 3) << 17);
       constexpr uint32_t kIdescO = kShape | (static_cast<uint32_t>(D >> 3) << 17) | (1u << 16);  // V: dims run fastest
@@ -428,17 +426,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint64_t step = (k >> 2) * (L::kBlk >> 4) + 2 * (k & 3);
-          mma_ss(tmem + x_id * 128, qd + step, kd + step, kIdescS, k > 0);
+          mma_ss(leader, tmem + x_id * 128, qd + step, kd + step, kIdescS, k > 0);
         }
-        mma_commit(&bar.s_full[x_id]);
+        commit(leader, &bar.s_full[x_id]);
       };
       const auto values = [&](int t, int x_id) {
         const uint64_t vd = smem_desc_sw128_nmajor(smem_u32(smem + L::kVAt + (t & 1) * L::kV), 8192);
 #pragma unroll
         for (int k = 0; k < kTokens / 16; ++k)
-          mma_ts(tmem + 256 + x_id * D, tmem + x_id * 128 + 8 * k,
+          mma_ts(leader, tmem + 256 + x_id * D, tmem + x_id * 128 + 8 * k,
                  vd + (k >> 2) * ((D / 64) * 8192 >> 4) + 128 * (k & 3), kIdescO, t > 0 || k > 0);
-        mma_commit(&bar.o_done[x_id]);
+        commit(leader, &bar.o_done[x_id]);
       };
       ok = mbar_wait(&bar.q_full, 0, limit_ns, abort);
       for (int t = 0; ok && t <= n_steps; ++t) {
@@ -452,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
             tc_fence_after();
             values(t - 1, x_id);
             issued = true;
-            if (x_id == n_tiles - 1) mma_commit(&bar.v_empty[(t - 1) & 1]);
+            if (x_id == n_tiles - 1) commit(leader, &bar.v_empty[(t - 1) & 1]);
             if (t < n_steps) ok = mbar_wait(&bar.o_done[x_id], (t - 1) & 1, limit_ns, abort);
             if (!ok) break;
           }
@@ -460,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
             tc_fence_after();
             scores(t, x_id);
             issued = true;
-            if (x_id == n_tiles - 1) mma_commit(&bar.k_empty[t & 1]);
+            if (x_id == n_tiles - 1) commit(leader, &bar.k_empty[t & 1]);
           }
         }
       }
@@ -468,9 +466,66 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
         report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
         if (issued) {
           // wait for the mma's already issued before TMEM is released
-          mma_commit(&bar.drain);
+          commit(leader, &bar.drain);
           volatile int never = 0;
           mbar_wait(&bar.drain, 0, 10000000ull, &never);
+        }
+      }
+    } else if (warp == 13 && lane < kGroups) {
+      // lane l: the l-th group of 16 tokens of every step, which lies in one page
+      constexpr uint32_t kGroupBytes = 16 * D;
+      const int page_mask = (1 << a.page_shift) - 1;
+      const int32_t* const table = a.block_table + static_cast<int64_t>(r) * a.max_blocks;
+      const auto page_at = [&](int t) {
+        const int64_t j = static_cast<int64_t>(t) * kTokens + lane * 16;
+        int page = -1;
+        if (j < q.len) {
+          page = table[j >> a.page_shift];
+          if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.n_pages)) {
+            report_error(a.status, TWELL_ERR_BAD_FORMAT);
+            page = 0;
+          }
+        }
+        return page;
+      };
+      constexpr uint32_t kMine = (1u << kGroups) - 1;
+      int page = page_at(0), next = n_steps > 1 ? page_at(1) : -1, issued = 0;
+      for (int t = 0; t < n_steps; ++t) {
+        const int after = t + 2 < n_steps ? page_at(t + 2) : -1;
+        const int64_t cell = static_cast<int64_t>(max(page, 0)) * a.heads + head;
+        const int64_t at = ((cell << a.page_shift) + ((t * kTokens + lane * 16) & page_mask)) * D;
+        const float ks = page >= 0 ? a.k_scale[cell] : 1.0f, vs = page >= 0 ? a.v_scale[cell] : 1.0f;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          ok = __all_sync(kMine, mbar_wait(&bar.raw_empty[v], (t & 1) ^ 1, limit_ns, abort));
+          if (!ok) break;
+          if (page >= 0) {
+            mbar_arrive_expect_tx(&bar.raw_full[v], kGroupBytes);
+            bulk_load(smem + L::kRawAt + v * L::kRaw + lane * kGroupBytes, (v ? a.v : a.k) + at, kGroupBytes,
+                      &bar.raw_full[v]);
+          } else {
+            mbar_arrive(&bar.raw_full[v]);
+          }
+          issued = t + 1;
+        }
+        if (!ok) break;
+        // The step's scales, in a slot of four: the keys' codes of step t - 1 have been
+        // taken up, after the values of t - 2 were put in place, which waited for the
+        // mma's of t - 4: both softmaxes are through with that step's scales.
+        float* const sc = scales + (t & 3) * 3 * kGroups + lane;
+        sc[0] = fmaxf(ks, FLT_MIN);  // a masked S of -inf stays so
+        sc[kGroups] = fmaxf(log2_fast(vs), -200.0f);
+        sc[2 * kGroups] = 1.0f / vs;
+        mbar_arrive(&bar.scale_full[t & 3]);
+        page = next;
+        next = after;
+      }
+      if (!ok) {
+        report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
+        // let the copies already in flight land before the CTA leaves
+        for (int v = 0; v < 2 && issued > 0; ++v) {
+          volatile int never = 0;
+          mbar_wait(&bar.raw_full[v], (issued - 1) & 1, 10000000ull, &never);
         }
       }
     }
