@@ -457,39 +457,66 @@ def twell_profile_read(kernel) -> tuple:
 
 # ---------------------------------------------------------------- decode step
 KV_E4M3, KV_INT8 = 0, 1
+_torch = None
+_raw_stream = None
 
 
-def _need_type(t, dtype, n: int, name: str) -> None:
-    """A contiguous device tensor of dtype with at least n elements."""
+def _setup():
+    """torch, imported at the first call, and the current stream's handle without
+    the Stream object around it (these calls are as short as the kernels they start)."""
+    global _torch, _raw_stream
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _raw_stream = ((lambda: get(torch._C._cuda_getDevice())) if get is not None
+                   else (lambda: torch.cuda.current_stream().cuda_stream))
+    _torch = torch
+    return torch
+
+
+def _on(stream) -> int:
+    return _raw_stream() if stream is None else int(stream.cuda_stream)
+
+
+def _arg(t, dtype, n: int, name: str) -> int:
+    """The address of a contiguous tensor of dtype with at least n elements; that
+    it is on the device is looked at last, by _on_device."""
     if t.dtype != dtype:
         raise ValueError(f"{name}: {t.dtype}, the call takes {dtype}")
     if t.numel() < n:
         raise ValueError(f"{name}: {t.numel()} elements, the call needs {n}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor")
+    return t.data_ptr()
 
 
-def _need_rows(t, dtype, tail: tuple, name: str) -> int:
-    """The distance between the tokens of a device tensor [tokens, *tail], which
+def _on_device(*tensors) -> None:
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("tensors passed to libtwell must be CUDA tensors")
+
+
+def _maybe(t, dtype, n: int, name: str):
+    return None if t is None else _arg(t, dtype, n, name)
+
+
+def _need_rows(t, dtype, heads: int, dim: int, name: str) -> int:
+    """The distance between the tokens of a device tensor [tokens, heads, dim], which
     may be a slice of wider rows but holds each token in one piece."""
     if t.dtype != dtype:
         raise ValueError(f"{name}: {t.dtype}, the call takes {dtype}")
-    if not t.is_cuda:
-        raise ValueError("tensors passed to libtwell must be CUDA tensors")
-    if tuple(t.shape[1:]) != tail:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, the call takes [tokens, {', '.join(map(str, tail))}]")
-    step, ok = 1, True
-    for size, stride in zip(reversed(tail), reversed(t.stride()[1:])):
-        ok = ok and (stride == step or size == 1)
-        step *= size
-    if not ok:
-        raise ValueError(f"{name}: strides {t.stride()}, a token's {step} elements must lie together")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), step)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name}: shape {tuple(shape)}, the call takes [tokens, {heads}, {dim}]")
+    if (stride[2] != 1 and dim > 1) or (stride[1] != dim and heads > 1):
+        raise ValueError(f"{name}: strides {tuple(stride)}, a token's {heads * dim} elements must lie together")
+    return stride[0] if shape[0] > 1 else max(stride[0], heads * dim)
 
 
-@dataclass
+@dataclass(frozen=True)
 class KVCache:
     """An 8-bit paged cache: k and v [n_pages, n_heads, page_size, head_dim] of
     torch.float8_e4m3fn or torch.int8, k_scale and v_scale [n_pages, n_heads]
-    float32, status int32.  The buffers stay the caller's."""
+    float32, status int32.  The buffers stay the caller's and the same ones."""
     k: "object"
     v: "object"
     k_scale: "object"
@@ -497,30 +524,33 @@ class KVCache:
     status: "object"
 
     def __post_init__(self):
-        import torch
+        torch = _torch or _setup()
         formats = {torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_INT8}
         if self.k.dtype not in formats or self.v.dtype != self.k.dtype:
             raise ValueError(f"k, v: {self.k.dtype}, {self.v.dtype}; a cache holds float8_e4m3fn or int8")
         if self.k.dim() != 4 or self.v.shape != self.k.shape:
             raise ValueError(f"k, v: shapes {tuple(self.k.shape)}, {tuple(self.v.shape)}")
-        self.n_pages, self.n_heads, self.page_size, self.head_dim = self.k.shape
+        keep = dict(zip(("n_pages", "n_heads", "page_size", "head_dim"), self.k.shape), format=formats[self.k.dtype],
+                    _struct=None)
         for t, name in ((self.k_scale, "k_scale"), (self.v_scale, "v_scale")):
-            _need_type(t, torch.float32, self.n_pages * self.n_heads, name)
-        _need_type(self.status, torch.int32, 1, "status")
-        self.format = formats[self.k.dtype]
-        self._struct = None
+            if t.dtype != torch.float32 or t.numel() < keep["n_pages"] * keep["n_heads"]:
+                raise ValueError(f"{name}: {t.numel()} elements of {t.dtype}, a cache needs [n_pages, n_heads] float32")
+        if self.status.dtype != torch.int32 or self.status.numel() < 1:
+            raise ValueError("status: an int32 tensor")
+        for name, value in keep.items():
+            object.__setattr__(self, name, value)
 
     def struct(self):
         if self._struct is None:
-            self._struct = ctypes.pointer(twell_kv_t(
+            object.__setattr__(self, "_struct", ctypes.pointer(twell_kv_t(
                 self.n_pages, self.page_size, self.n_heads, self.head_dim, self.format, 0, _ptr(self.k),
-                _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale), _ptr(self.status)))
+                _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale), _ptr(self.status))))
         return self._struct
 
 
 def alloc_kv_cache(n_pages: int, page_size: int, n_heads: int, head_dim: int, fmt: int = KV_E4M3,
                    device="cuda") -> KVCache:
-    import torch
+    torch = _torch or _setup()
     shape, dt = (n_pages, n_heads, page_size, head_dim), (torch.float8_e4m3fn if fmt == KV_E4M3 else torch.int8)
     return KVCache(k=torch.empty(shape, dtype=dt, device=device), v=torch.empty(shape, dtype=dt, device=device),
                    k_scale=torch.zeros(shape[:2], dtype=torch.float32, device=device),
@@ -528,10 +558,11 @@ def alloc_kv_cache(n_pages: int, page_size: int, n_heads: int, head_dim: int, fm
                    status=torch.zeros((4,), dtype=torch.int32, device=device))
 
 
-@dataclass
+@dataclass(frozen=True)
 class KVPlan:
     """What twell_kv_plan writes: kv_lens [R], cu_q [R + 1], slots [n_tokens]
-    int64, positions [n_tokens], pool [2] (for the next step's plan), status."""
+    int64, positions [n_tokens], pool [2] (for the next step's plan), status.
+    The buffers stay the same ones."""
     kv_lens: "object"
     cu_q: "object"
     slots: "object"
@@ -539,9 +570,22 @@ class KVPlan:
     pool: "object"
     status: "object"
 
+    def _outputs(self) -> tuple:
+        """(requests, tokens, addresses in the call's order), checked once."""
+        kept = self.__dict__.get("_kept")
+        if kept is None:
+            i32, R, n = _torch.int32, self.kv_lens.numel(), self.slots.numel()
+            kept = (R, n, (_arg(self.pool, i32, 2, "plan.pool"), _arg(self.kv_lens, i32, R, "plan.kv_lens"),
+                           _arg(self.cu_q, i32, R + 1, "plan.cu_q"),
+                           _arg(self.slots, _torch.int64, n, "plan.slots"),
+                           _arg(self.positions, i32, n, "plan.positions")), _arg(self.status, i32, 1, "plan.status"))
+            _on_device(self.pool, self.kv_lens, self.cu_q, self.slots, self.positions, self.status)
+            object.__setattr__(self, "_kept", kept)
+        return kept
+
 
 def alloc_kv_plan(n_requests: int, n_tokens: int, device="cuda") -> KVPlan:
-    import torch
+    torch = _torch or _setup()
     i32 = lambda n: torch.zeros((n,), dtype=torch.int32, device=device)  # noqa: E731
     return KVPlan(kv_lens=i32(n_requests), cu_q=i32(n_requests + 1),
                   slots=torch.zeros((n_tokens,), dtype=torch.int64, device=device), positions=i32(n_tokens),
@@ -550,48 +594,49 @@ def alloc_kv_plan(n_requests: int, n_tokens: int, device="cuda") -> KVPlan:
 
 def alloc_page_ring(n_pages: int, device="cuda") -> tuple:
     """(ring, pool) of a cache whose pages are all free."""
-    import torch
+    torch = _torch or _setup()
     return (torch.arange(n_pages, dtype=torch.int32, device=device),
             torch.tensor([0, n_pages], dtype=torch.int32, device=device))
 
 
-def twell_kv_plan(kv_lens, new_tokens, block_table, ring, pool, page_size: int, plan: KVPlan, stream=None) -> None:
-    """Block tables and slot maps of one step; the pages are ring.numel()."""
-    import torch
-    R, n_tokens = kv_lens.numel(), plan.slots.numel()
+def _table(block_table, R: int) -> tuple:
     if block_table.dim() != 2:
         raise ValueError("block_table: the call takes [requests, blocks]")
     width = block_table.shape[1]
-    i32 = torch.int32
-    _need_type(kv_lens, i32, R, "kv_lens")
-    _need_type(new_tokens, i32, R, "new_tokens")
-    _need_type(block_table, i32, R * width, "block_table")
-    _need_type(ring, i32, 1, "ring")
-    _need_type(pool, i32, 2, "pool")
-    _need_type(plan.kv_lens, i32, R, "plan.kv_lens")
-    _need_type(plan.cu_q, i32, R + 1, "plan.cu_q")
-    _need_type(plan.slots, torch.int64, n_tokens, "plan.slots")
-    _need_type(plan.positions, i32, n_tokens, "plan.positions")
-    _need_type(plan.pool, i32, 2, "plan.pool")
-    _need_type(plan.status, i32, 1, "plan.status")
-    _check(load_library().twell_kv_plan(_ptr(kv_lens), _ptr(new_tokens), R, page_size, ring.numel(), width,
-                                        _ptr(block_table), _ptr(ring), _ptr(pool), _ptr(plan.pool),
-                                        _ptr(plan.kv_lens), _ptr(plan.cu_q), _ptr(plan.slots), _ptr(plan.positions),
-                                        n_tokens, _ptr(plan.status), _stream(stream)), "twell_kv_plan")
+    return _arg(block_table, _torch.int32, R * width, "block_table"), width
+
+
+def twell_kv_plan(kv_lens, new_tokens, block_table, ring, pool, page_size: int, plan: KVPlan, stream=None) -> None:
+    """Block tables and slot maps of one step; the pages are ring.numel()."""
+    i32 = (_torch or _setup()).int32
+    R = kv_lens.numel()
+    lens_p, new_p = _arg(kv_lens, i32, R, "kv_lens"), _arg(new_tokens, i32, R, "new_tokens")
+    table, width = _table(block_table, R)
+    ring_p, pool_p = _arg(ring, i32, 1, "ring"), _arg(pool, i32, 2, "pool")
+    _on_device(kv_lens, new_tokens, block_table, ring, pool)
+    rows, n_tokens, out, status = plan._outputs()
+    if rows != R:
+        raise ValueError(f"plan: {rows} requests, kv_lens has {R}")
+    rc = load_library().twell_kv_plan(lens_p, new_p, R, page_size, ring.numel(), width, table, ring_p,
+                                      pool_p, *out, n_tokens, status, _on(stream))
+    if rc:
+        _check(rc, "twell_kv_plan")
 
 
 def twell_kv_append(K, V, cu_q, slots, cache: KVCache, stream=None) -> None:
     """Keys and values [n_tokens, n_heads, head_dim] bf16 into the cache's slots."""
-    import torch
-    tail = (cache.n_heads, cache.head_dim)
-    ldk, ldv = _need_rows(K, torch.bfloat16, tail, "K"), _need_rows(V, torch.bfloat16, tail, "V")
-    n, R = K.shape[0], cu_q.numel() - 1
+    torch = _torch or _setup()
+    ldk = _need_rows(K, torch.bfloat16, cache.n_heads, cache.head_dim, "K")
+    ldv = _need_rows(V, torch.bfloat16, cache.n_heads, cache.head_dim, "V")
+    n = K.shape[0]
     if V.shape[0] != n:
         raise ValueError(f"V: {V.shape[0]} tokens, K has {n}")
-    _need_type(cu_q, torch.int32, 1, "cu_q")
-    _need_type(slots, torch.int64, n, "slots")
-    _check(load_library().twell_kv_append(K.data_ptr(), ldk, V.data_ptr(), ldv, _ptr(cu_q), _ptr(slots), n, R,
-                                          cache.struct(), _stream(stream)), "twell_kv_append")
+    cu, at = _arg(cu_q, torch.int32, 1, "cu_q"), _arg(slots, torch.int64, n, "slots")
+    _on_device(K, V, cu_q, slots)
+    rc = load_library().twell_kv_append(K.data_ptr(), ldk, V.data_ptr(), ldv, cu, at, n, cu_q.numel() - 1,
+                                        cache.struct(), _on(stream))
+    if rc:
+        _check(rc, "twell_kv_append")
 
 
 def kv_attention_workspace_bytes(n_tokens, n_requests, n_q_heads, n_kv_heads, head_dim) -> int:
@@ -603,82 +648,81 @@ def twell_kv_attention(Q, cache: KVCache, block_table, cu_q, positions, kv_lens,
                        softmax_scale: float, O, workspace, lse=None, stream=None) -> None:
     """O [n_tokens, n_q_heads, head_dim] bf16 = attention of Q over the cache;
     lse [n_tokens, n_q_heads] float32 when given."""
-    import torch
+    torch = _torch or _setup()
     n, heads = Q.shape[0], Q.shape[1]
-    tail = (heads, cache.head_dim)
-    ldq, ldo = _need_rows(Q, torch.bfloat16, tail, "Q"), _need_rows(O, torch.bfloat16, tail, "O")
+    ldq = _need_rows(Q, torch.bfloat16, heads, cache.head_dim, "Q")
+    ldo = _need_rows(O, torch.bfloat16, heads, cache.head_dim, "O")
     if O.shape[0] != n:
         raise ValueError(f"O: {O.shape[0]} tokens, Q has {n}")
-    R = kv_lens.numel()
-    if block_table.dim() != 2:
-        raise ValueError("block_table: the call takes [requests, blocks]")
-    width = block_table.shape[1]
-    _need_type(block_table, torch.int32, R * width, "block_table")
-    _need_type(cu_q, torch.int32, R + 1, "cu_q")
-    _need_type(positions, torch.int32, n, "positions")
-    _need_type(kv_lens, torch.int32, R, "kv_lens")
-    if lse is not None:
-        _need_type(lse, torch.float32, n * heads, "lse")
-    _check(load_library().twell_kv_attention(Q.data_ptr(), ldq, cache.struct(), _ptr(block_table), width, _ptr(cu_q),
-                                             _ptr(positions), _ptr(kv_lens), n, R, heads, max_kv_len, max_q_len,
-                                             softmax_scale, O.data_ptr(), ldo, _ptr(lse), _ptr(workspace),
-                                             workspace.numel() * workspace.element_size(), _stream(stream)),
-           "twell_kv_attention")
+    i32, R = torch.int32, kv_lens.numel()
+    table, width = _table(block_table, R)
+    args = (_arg(cu_q, i32, R + 1, "cu_q"), _arg(positions, i32, n, "positions"), _arg(kv_lens, i32, R, "kv_lens"))
+    lse_p = _maybe(lse, torch.float32, n * heads, "lse")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor")
+    _on_device(Q, O, block_table, cu_q, positions, kv_lens, lse, workspace)
+    rc = load_library().twell_kv_attention(
+        Q.data_ptr(), ldq, cache.struct(), table, width, *args, n, R, heads, max_kv_len, max_q_len, softmax_scale,
+        O.data_ptr(), ldo, lse_p, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _on(stream))
+    if rc:
+        _check(rc, "twell_kv_attention")
 
 
 def twell_kv_read_status(cache: KVCache, stream=None) -> int:
-    return int(load_library().twell_kv_read_status(cache.struct(), _stream(stream)))
+    _torch or _setup()
+    return int(load_library().twell_kv_read_status(cache.struct(), _on(stream)))
 
 
 def _logits(t, name: str) -> tuple:
     """(dtype code, rows, vocabulary, distance between rows) of a logits tensor."""
-    import torch
-    codes = {torch.bfloat16: 0, torch.float32: 1}
-    if t.dtype not in codes or t.dim() != 2:
-        raise ValueError(f"{name}: {t.dtype} of {t.dim()} dimensions, the call takes [rows, vocab] of bfloat16 or float32")
-    if not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: a CUDA tensor whose rows are contiguous")
-    return codes[t.dtype], t.shape[0], t.shape[1], max(t.stride(0), t.shape[1]) if t.shape[0] < 2 else t.stride(0)
+    code = 0 if t.dtype == _torch.bfloat16 else 1 if t.dtype == _torch.float32 else -1
+    shape = t.shape
+    if code < 0 or len(shape) != 2:
+        raise ValueError(f"{name}: {t.dtype} of {len(shape)} dimensions, the call takes [rows, vocab] of bfloat16 or "
+                         "float32")
+    stride = t.stride()
+    if shape[1] > 1 and stride[1] != 1:
+        raise ValueError(f"{name}: a tensor whose rows are contiguous")
+    return code, shape[0], shape[1], max(stride[0], shape[1]) if shape[0] < 2 else stride[0]
 
 
 def twell_logprobs(logits, targets, inv_temperature: float, logprob, entropy, lse, top_logprob=None, top_index=None,
                    stream=None) -> None:
     """logprob, entropy, lse [rows] float32 (None: not wanted; targets and logprob
     together) and the top_logprob.shape[1] best alternatives [rows, k]."""
-    import torch
+    torch = _torch or _setup()
+    f32, i32 = torch.float32, torch.int32
     code, rows, vocab, ld = _logits(logits, "logits")
-    for t, name in ((logprob, "logprob"), (entropy, "entropy"), (lse, "lse")):
-        if t is not None:
-            _need_type(t, torch.float32, rows, name)
-    if targets is not None:
-        _need_type(targets, torch.int32, rows, "targets")
-    k = 0
+    k, top, index = 0, None, None
     if top_logprob is not None or top_index is not None:
         if top_logprob is None or top_index is None:
             raise ValueError("top_logprob, top_index: give both or neither")
         k = top_logprob.shape[1]
-        _need_type(top_logprob, torch.float32, rows * k, "top_logprob")
-        _need_type(top_index, torch.int32, rows * k, "top_index")
-    _check(load_library().twell_logprobs(logits.data_ptr(), code, ld, rows, vocab, _ptr(targets), inv_temperature,
-                                         _ptr(logprob), _ptr(entropy), _ptr(lse), k, _ptr(top_logprob),
-                                         _ptr(top_index), _stream(stream)), "twell_logprobs")
+        top = _arg(top_logprob, f32, rows * k, "top_logprob")
+        index = _arg(top_index, i32, rows * k, "top_index")
+    _on_device(logits, targets, logprob, entropy, lse, top_logprob, top_index)
+    rc = load_library().twell_logprobs(logits.data_ptr(), code, ld, rows, vocab, _maybe(targets, i32, rows, "targets"),
+                                       inv_temperature, _maybe(logprob, f32, rows, "logprob"),
+                                       _maybe(entropy, f32, rows, "entropy"), _maybe(lse, f32, rows, "lse"), k, top,
+                                       index, _on(stream))
+    if rc:
+        _check(rc, "twell_logprobs")
 
 
 def twell_logprobs_bwd(logits, targets, inv_temperature: float, lse, entropy, d_logprob, d_entropy, d_logits,
                        stream=None) -> None:
     """d_logits (type of logits; may be logits itself) from the upstream gradients
     of logprob and entropy; targets with d_logprob, or entropy with d_entropy, may be None."""
-    import torch
+    torch = _torch or _setup()
+    f32 = torch.float32
     code, rows, vocab, ld = _logits(logits, "logits")
     code_d, rows_d, vocab_d, ldd = _logits(d_logits, "d_logits")
     if (code_d, rows_d, vocab_d) != (code, rows, vocab):
         raise ValueError("d_logits: type and shape are those of logits")
-    for t, name in ((lse, "lse"), (entropy, "entropy"), (d_logprob, "d_logprob"), (d_entropy, "d_entropy")):
-        if t is not None:
-            _need_type(t, torch.float32, rows, name)
-    if targets is not None:
-        _need_type(targets, torch.int32, rows, "targets")
-    _check(load_library().twell_logprobs_bwd(logits.data_ptr(), code, ld, rows, vocab, _ptr(targets),
-                                             inv_temperature, _ptr(lse), _ptr(entropy), _ptr(d_logprob),
-                                             _ptr(d_entropy), d_logits.data_ptr(), ldd, _stream(stream)),
-           "twell_logprobs_bwd")
+    _on_device(logits, targets, lse, entropy, d_logprob, d_entropy, d_logits)
+    rc = load_library().twell_logprobs_bwd(
+        logits.data_ptr(), code, ld, rows, vocab, _maybe(targets, torch.int32, rows, "targets"), inv_temperature,
+        _arg(lse, f32, rows, "lse"), _maybe(entropy, f32, rows, "entropy"), _maybe(d_logprob, f32, rows, "d_logprob"),
+        _maybe(d_entropy, f32, rows, "d_entropy"), d_logits.data_ptr(), ldd, _on(stream))
+    if rc:
+        _check(rc, "twell_logprobs_bwd")
