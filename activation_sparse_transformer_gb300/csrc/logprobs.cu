@@ -1,16 +1,19 @@
 // Log probabilities of given tokens with entropy and best alternatives
 // (twell_logprobs) and their gradient (twell_logprobs_bwd).
 //
-// With x = logits / T, m = max x, S = sum exp(x - m), U = sum exp(x - m) (x - m):
-//   lse = m + log S,  logprob = (x_t - m) - log S,  entropy = log S - U / S.
+// In base 2, with y = logits log2(e) / T, m = max y, S = sum 2^(y - m),
+// U = sum 2^(y - m) (y - m):
+//   lse = ln2 (m + log2 S),  logprob = ln2 ((y_t - m) - log2 S),
+//   entropy = ln2 (log2 S - U / S).
 // A row is read from memory once: a CTA (or a cluster of 2 to 8 for long rows
 // and few of them) copies its slice to shared memory with asynchronous 16-byte
 // copies, finds the maximum there and then sums with it, so no running maximum has
 // to be corrected; slices are joined through distributed shared memory.  HBM
-// bounds many rows; few rows are bound by the latency of one slice.
+// bounds many rows, with the instructions of an element next (5 of them, two
+// elements an instruction where there is one); few rows are bound by the latency of one slice.
 //
-// The k largest: the k-th largest of the 256 threads' own maxima is a lower bound
-// of the k-th largest value, and hardly more than k values reach it.  Those are
+// The k largest: the k-th largest of 64 groups' own maxima is a lower bound of
+// the k-th largest value, and hardly more than k values reach it.  Those are
 // collected and ranked by counting.  Keys are (value, index) pairs in one
 // 64-bit word, so equal values go by index and no two keys are equal.
 #include <cooperative_groups.h>
@@ -25,13 +28,13 @@ namespace cg = cooperative_groups;
 namespace twell {
 namespace {
 
-constexpr int kLpThreads = 256;
-constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kBwdThreads = 256;
+constexpr int kGroups = 64;    // of the k largest's bound: with k = 20 about 24 values reach it
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
 constexpr int kCandidates = 1024;
 constexpr int kMaxVocab = 400000;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -52,7 +55,17 @@ struct Elem<float> {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
   static __device__ __forceinline__ float store(float x) { return x; }
-  static __device__ __forceinline__ float lowest() { return -INFINITY; }
+  struct Range {
+    float hi = -INFINITY, lo = INFINITY;
+    __device__ __forceinline__ void add(const uint4& w) {
+      float f[4];
+      unpack(w, f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) hi = fmaxf(hi, f[i]), lo = fminf(lo, f[i]);
+    }
+    __device__ __forceinline__ float high() const { return hi; }
+    __device__ __forceinline__ float low() const { return lo; }
+  };
 };
 template <>
 struct Elem<uint16_t> {
@@ -71,7 +84,19 @@ struct Elem<uint16_t> {
     return make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
   }
   static __device__ __forceinline__ uint16_t store(float x) { return float_to_bf16_bits(x); }
-  static __device__ __forceinline__ uint16_t lowest() { return 0xFF80u; }
+  struct Range {  // of the two elements of a word at once
+    uint32_t hi = 0xFF80FF80u, lo = 0x7F807F80u;
+    __device__ __forceinline__ void add(const uint4& w) {
+      const uint32_t* u = &w.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        asm("max.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(u[i]));
+        asm("min.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(u[i]));
+      }
+    }
+    __device__ __forceinline__ float high() const { return fmaxf(bf16_lo(hi), bf16_hi(hi)); }
+    __device__ __forceinline__ float low() const { return fminf(bf16_lo(lo), bf16_hi(lo)); }
+  };
 };
 
 struct LogprobsArgs {
@@ -93,7 +118,7 @@ struct Stat {
 // Stats relative to a common maximum; an empty part has s = u = 0.
 __device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
   const float m = fmaxf(a.m, b.m);
-  const float ea = ex2((a.m - m) * kLog2e), eb = ex2((b.m - m) * kLog2e);
+  const float ea = ex2(a.m - m), eb = ex2(b.m - m);
   return {m, a.s * ea + b.s * eb, ea * (a.u + a.s * (a.m - m)) + eb * (b.u + b.s * (b.m - m))};
 }
 
@@ -111,68 +136,110 @@ __device__ __forceinline__ int key_index(uint64_t k) {
   return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k));
 }
 
+template <int NT>
 struct LpShared {
-  uint64_t thread_key[kLpThreads];   // then: the cluster's lists
+  uint64_t key[kMaxCluster * kMaxTop];  // the groups' maxima, then the cluster's lists
   uint64_t candidates[kCandidates];
   uint64_t best[kMaxTop];
   uint64_t bound;
   Stat stat;
-  float warp_m[kLpWarps];
-  Stat warp_stat[kLpWarps];
-  uint64_t warp_key[kLpWarps];
+  float warp_hi[NT / 32], warp_lo[NT / 32];
+  float2 warp_sum[NT / 32];
+  uint64_t warp_key[NT / 32];
   int count;
 };
 
-// The top_k best keys of the CTA's slice to sh.best, in order, 0 behind the last.
+// The part of a row that a CTA holds: whole 16-byte chunks [c0, c1) of
+// `chunks`, and the elements before and behind them.
 template <typename T>
-__device__ void slice_top(LpShared& sh, const uint4* chunks, int n_chunks, int index0, int slice_n, float inv_t, int k,
-                          uint64_t mine) {
+struct Slice {
+  const uint4* chunks;
+  int lead, n, c0, c1;  // element i of the slice is element lead + i of the chunks
+  __device__ __forceinline__ const T* elems() const { return reinterpret_cast<const T*>(chunks); }
+  // position of the e-th element outside the whole chunks; there are edges() < 2 * kVec of them
+  __device__ __forceinline__ int head() const { return c1 > c0 ? c0 * Elem<T>::kVec - lead : n; }
+  __device__ __forceinline__ int edges() const { return c1 > c0 ? head() + (lead + n - c1 * Elem<T>::kVec) : n; }
+  __device__ __forceinline__ int edge(int e) const { return e < head() ? e : c1 * Elem<T>::kVec - lead + (e - head()); }
+};
+
+// Number of keys in list[0, n) above `mine`, counted by kShare neighbouring
+// threads together (kShare <= 32); all of them get it.
+template <int kShare>
+__device__ __forceinline__ int rank_in(const uint64_t* list, int n, uint64_t mine) {
+  int better = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x % kShare; i < n; i += kShare) better += list[i] > mine;
+#pragma unroll
+  for (int d = 1; d < kShare; d *= 2) better += __shfl_xor_sync(0xffffffffu, better, d);
+  return better;
+}
+
+// The top_k best keys of the slice to sh.best, in order, 0 behind the last.
+// best, at: this thread's largest logit and its place (-1: it has none).
+template <typename T, int NT>
+__device__ void slice_top(LpShared<NT>& sh, const Slice<T>& sl, float inv_t, int k, float best, int at) {
   using E = Elem<T>;
+  constexpr int kShare = NT / kGroups;
   const int tid = threadIdx.x;
-  sh.thread_key[tid] = mine;
+  uint64_t mine = at >= 0 ? key_of(best * inv_t, at) : 0;
+#pragma unroll
+  for (int d = 1; d < kShare; d *= 2) {
+    const uint64_t o = __shfl_xor_sync(0xffffffffu, mine, d);
+    mine = o > mine ? o : mine;
+  }
+  if (tid % kShare == 0) sh.key[tid / kShare] = mine;
   if (tid < kMaxTop) sh.best[tid] = 0;
   if (tid == 0) {
     sh.count = 0;
-    sh.bound = 1;  // every key is larger: fewer than k threads have one
+    sh.bound = 1;  // every key is larger: fewer than k groups have one
   }
   __syncthreads();
-  int better = 0;
-  for (int i = 0; i < kLpThreads; ++i) better += sh.thread_key[i] > mine;
+  const int better = rank_in<kShare>(sh.key, kGroups, mine);
   if (better == k - 1 && mine) sh.bound = mine;
   __syncthreads();
   const uint64_t bound = sh.bound;
-  const auto each = [&](auto&& f) {
-    for (int j = tid; j < n_chunks; j += kLpThreads) {
+  // f for every element of a chunk whose largest one is at least `from`
+  const auto each = [&](float from, auto&& f) {
+    for (int j = sl.c0 + tid; j < sl.c1; j += NT) {
+      typename E::Range r;
+      r.add(sl.chunks[j]);
+      if (r.high() * inv_t < from) continue;
       float x[E::kVec];
-      E::unpack(chunks[j], x);
+      E::unpack(sl.chunks[j], x);
 #pragma unroll
-      for (int i = 0; i < E::kVec; ++i) {
-        const int at = j * E::kVec + i - index0;
-        if (at >= 0 && at < slice_n) f(key_of(x[i] * inv_t, at));
-      }
+      for (int i = 0; i < E::kVec; ++i) f(x[i] * inv_t, j * E::kVec + i - sl.lead);
+    }
+    if (tid < sl.edges()) {
+      const int i = sl.edge(tid);
+      f(E::load(sl.elems() + sl.lead + i) * inv_t, i);
     }
   };
-  each([&](uint64_t key) {
-    if (key >= bound) {
-      const int at = atomicAdd(&sh.count, 1);
-      if (at < kCandidates) sh.candidates[at] = key;
+  const float least = bound > 1 ? key_value(bound) : -INFINITY;
+  each(least, [&](float v, int i) {
+    if (v >= least) {
+      const uint64_t key = key_of(v, i);
+      if (key >= bound) {
+        const int c = atomicAdd(&sh.count, 1);
+        if (c < kCandidates) sh.candidates[c] = key;
+      }
     }
   });
   __syncthreads();
   if (sh.count <= kCandidates) {
     const int n = sh.count;
-    for (int c = tid; c < n; c += kLpThreads) {
+    for (int c = tid; c < n; c += NT) {
       const uint64_t key = sh.candidates[c];
       int rank = 0;
       for (int i = 0; i < n; ++i) rank += sh.candidates[i] > key;
       if (rank < k) sh.best[rank] = key;
     }
   } else {
-    // rare: a few threads own most of the largest values; take them one by one
+    // rare: a few groups own most of the largest values; take them one by one
     uint64_t last = ~0ull;
     for (int i = 0; i < k; ++i) {
       uint64_t top = 0;
-      each([&](uint64_t key) {
+      each(-INFINITY, [&](float v, int index) {
+        const uint64_t key = key_of(v, index);
         if (key < last && key > top) top = key;
       });
 #pragma unroll
@@ -182,8 +249,7 @@ __device__ void slice_top(LpShared& sh, const uint4* chunks, int n_chunks, int i
       }
       if ((tid & 31) == 0) sh.warp_key[tid / 32] = top;
       __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kLpWarps; ++w) top = sh.warp_key[w] > top ? sh.warp_key[w] : top;
+      for (int w = 0; w < NT / 32; ++w) top = sh.warp_key[w] > top ? sh.warp_key[w] : top;
       if (tid == 0) sh.best[i] = top;
       last = top;
       __syncthreads();
@@ -192,94 +258,132 @@ __device__ void slice_top(LpShared& sh, const uint4* chunks, int n_chunks, int i
   __syncthreads();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs a) {
+// (a, b) += ... of two elements in one instruction each.
+__device__ __forceinline__ void sum2(float2& s, float2& u, float x0, float x1, float c, float m, float& e0, float& e1) {
+  float d0, d1;
+  asm("{\n\t.reg .b64 x, c, m;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 c, {%4, %4};\n\tmov.b64 m, {%5, %5};\n\t"
+      "fma.rn.f32x2 x, x, c, m;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(x0), "f"(x1), "f"(c), "f"(-m));
+  e0 = ex2(d0);
+  e1 = ex2(d1);
+  asm("{\n\t.reg .b64 s, u, e, d;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 u, {%2, %3};\n\tmov.b64 e, {%4, %5};\n\t"
+      "mov.b64 d, {%6, %7};\n\tadd.rn.f32x2 s, s, e;\n\tfma.rn.f32x2 u, e, d, u;\n\t"
+      "mov.b64 {%0, %1}, s;\n\tmov.b64 {%2, %3}, u;\n\t}"
+      : "+f"(s.x), "+f"(s.y), "+f"(u.x), "+f"(u.y)
+      : "f"(e0), "f"(e1), "f"(d0), "f"(d1));
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a) {
   using E = Elem<T>;
   extern __shared__ uint4 chunks[];
-  __shared__ LpShared sh;
+  __shared__ LpShared<NT> sh;
   grid_dependency_wait();
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, ranks = cluster.num_blocks(), rank = cluster.block_rank();
   const int64_t row = blockIdx.x / ranks;
   const T* const src = static_cast<const T*>(a.logits) + row * a.ld;
   const int beg = min(rank * a.slice, a.vocab), n = min(a.slice, a.vocab - beg);
-  // the slice with the 16-byte pieces it touches; the pieces' other elements
-  // are replaced by -inf, and the last, cut piece comes in by elements
+  // the slice with the 16-byte pieces it touches; the last, cut piece comes in by elements
   const T* const from = src + beg;
   const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(from) & 15) / sizeof(T));
-  const int n_chunks = n > 0 ? (lead + n + E::kVec - 1) / E::kVec : 0, whole = (lead + n) / E::kVec;
+  const int whole = n > 0 ? (lead + n) / E::kVec : 0;
   const uint4* const g = reinterpret_cast<const uint4*>(from - lead);
-  for (int j = tid; j < whole && n > 0; j += kLpThreads)
+  for (int j = tid; j < whole; j += NT)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(chunks + j)), "l"(g + j) : "memory");
-  T* const elems = reinterpret_cast<T*>(chunks);
-  for (int i = whole * E::kVec + tid; i < n_chunks * E::kVec; i += kLpThreads)
-    elems[i] = i >= lead && i < lead + n ? from[i - lead] : E::lowest();
+  for (int i = max(whole * E::kVec, lead) + tid; i < lead + n; i += NT) reinterpret_cast<T*>(chunks)[i] = from[i - lead];
+  const Slice<T> sl = {chunks, lead, n, lead > 0 ? 1 : 0, whole};
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  if (whole > 0 && tid < lead) elems[tid] = E::lowest();
-  if (lead) __syncthreads();
 
-  float m = -FLT_MAX;
-  uint64_t mine = 0;
+  // the largest logit (with its place, for the alternatives) and the smallest
+  float hi = -INFINITY, lo = INFINITY;
+  int at = -1;
   if (a.top_k > 0) {
-    float best = -INFINITY;
-    int at = INT_MAX;
-    for (int j = tid; j < n_chunks; j += kLpThreads) {
-      float x[E::kVec];
-      E::unpack(chunks[j], x);
-#pragma unroll
-      for (int i = 0; i < E::kVec; ++i) {
-        const float v = x[i] * a.inv_temperature;
-        const int index = j * E::kVec + i - lead;
-        if (v > best || (at == INT_MAX && index >= 0 && index < n)) best = v, at = index;
-      }
+    for (int j = sl.c0 + tid; j < sl.c1; j += NT) {
+      typename E::Range r;
+      r.add(chunks[j]);
+      lo = fminf(lo, r.low());
+      if (r.high() > hi || at < 0) hi = r.high(), at = j;
     }
-    if (at != INT_MAX) mine = key_of(best, at);
-    m = fmaxf(m, best);
+    if (at >= 0) {
+      // the first element of that chunk that is its largest (none where all are NaN)
+      float x[E::kVec];
+      E::unpack(chunks[at], x);
+      int i = 0;
+#pragma unroll
+      for (int k = E::kVec - 1; k >= 0; --k)
+        if (x[k] == hi) i = k;
+      at = at * E::kVec + i - lead;
+    }
   } else {
-    float best = -INFINITY;
-    for (int j = tid; j < n_chunks; j += kLpThreads) {
-      float x[E::kVec];
-      E::unpack(chunks[j], x);
-#pragma unroll
-      for (int i = 0; i < E::kVec; ++i) best = fmaxf(best, x[i]);
-    }
-    m = fmaxf(m, best * a.inv_temperature);
+    typename E::Range r;
+    for (int j = sl.c0 + tid; j < sl.c1; j += NT) r.add(chunks[j]);
+    hi = r.high();
+    lo = r.low();
   }
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  if ((tid & 31) == 0) sh.warp_m[tid / 32] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kLpWarps; ++w) m = fmaxf(m, sh.warp_m[w]);
-
-  float s = 0.0f, u = 0.0f;
-  for (int j = tid; j < n_chunks; j += kLpThreads) {
-    float x[E::kVec];
-    E::unpack(chunks[j], x);
-#pragma unroll
-    for (int i = 0; i < E::kVec; ++i) {
-      // the product rounded as m's was: fused, a row of -1e30 would be far from its own maximum
-      const float d = __fmul_rn(x[i], a.inv_temperature) - m;
-      const float e = ex2(d * kLog2e);
-      s += e;
-      u = fmaf(e, fmaxf(d, -1000.0f), u);  // a masked token adds 0, not 0 * inf
-    }
+  if (tid < sl.edges()) {
+    const int i = sl.edge(tid);
+    const float x = E::load(sl.elems() + lead + i);
+    if (x > hi || at < 0) at = i;
+    hi = fmaxf(hi, x);
+    lo = fminf(lo, x);
   }
+  float m = hi;
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) {
-    s += __shfl_xor_sync(0xffffffffu, s, d);
-    u += __shfl_xor_sync(0xffffffffu, u, d);
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
   }
-  if ((tid & 31) == 0) sh.warp_stat[tid / 32] = {m, s, u};
+  if ((tid & 31) == 0) sh.warp_hi[tid / 32] = m, sh.warp_lo[tid / 32] = lo;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) m = fmaxf(m, sh.warp_hi[w]), lo = fminf(lo, sh.warp_lo[w]);
+  const float c = a.inv_temperature * kLog2e;
+  m = fmaxf(__fmul_rn(m, c), -FLT_MAX);
+
+  float2 s = {0.0f, 0.0f}, u = {0.0f, 0.0f};
+  // masked tokens (2^-inf * -inf is no number) and logits so large that the
+  // rounding of m counts are summed one by one, with products rounded as m's was
+  const bool plain = lo > -INFINITY && fabsf(m) < 1.0e6f && c < 1.0e6f;
+  const auto add = [&](float x) {
+    const float d = plain ? fmaf(x, c, -m) : __fmul_rn(x, c) - m, e = ex2(d);
+    s.x += e;
+    u.x = fmaf(e, fmaxf(d, -2000.0f), u.x);
+  };
+  if (plain) {
+    for (int j = sl.c0 + tid; j < sl.c1; j += NT) {
+      float x[E::kVec], e0, e1;
+      E::unpack(chunks[j], x);
+#pragma unroll
+      for (int i = 0; i < E::kVec; i += 2) sum2(s, u, x[i], x[i + 1], c, m, e0, e1);
+    }
+  } else {
+    for (int j = sl.c0 + tid; j < sl.c1; j += NT) {
+      float x[E::kVec];
+      E::unpack(chunks[j], x);
+#pragma unroll
+      for (int i = 0; i < E::kVec; ++i) add(x[i]);
+    }
+  }
+  if (tid < sl.edges()) add(E::load(sl.elems() + lead + sl.edge(tid)));
+  s.x += s.y;
+  u.x += u.y;
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) {
+    s.x += __shfl_xor_sync(0xffffffffu, s.x, d);
+    u.x += __shfl_xor_sync(0xffffffffu, u.x, d);
+  }
+  if ((tid & 31) == 0) sh.warp_sum[tid / 32] = make_float2(s.x, u.x);
   __syncthreads();
   if (tid == 0) {
     Stat all = {m, 0.0f, 0.0f};
 #pragma unroll
-    for (int w = 0; w < kLpWarps; ++w) all.s += sh.warp_stat[w].s, all.u += sh.warp_stat[w].u;
+    for (int w = 0; w < NT / 32; ++w) all.s += sh.warp_sum[w].x, all.u += sh.warp_sum[w].y;
     sh.stat = all;
   }
-  if (a.top_k > 0) slice_top<T>(sh, chunks, n_chunks, lead, n, a.inv_temperature, a.top_k, mine);
+  if (a.top_k > 0) slice_top<T, NT>(sh, sl, a.inv_temperature, a.top_k, hi, at);
   if (ranks > 1) {
     cluster.sync();
     if (rank == 0) {
@@ -288,18 +392,18 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
         for (int i = 1; i < ranks; ++i) all = join(all, *cluster.map_shared_rank(&sh.stat, i));
         sh.stat = all;
       }
-      // the ranks' lists, indexes made those of the row, ranked together
-      const int of = tid / kMaxTop, i = tid % kMaxTop;
-      uint64_t key = 0;
-      if (of < ranks && i < a.top_k) {
-        key = cluster.map_shared_rank(&sh, of)->best[i];
-        if (key) key -= static_cast<uint64_t>(of) * a.slice;
-      }
       if (a.top_k > 0) {
-        sh.thread_key[tid] = key;
+        // the ranks' lists, indexes made those of the row, ranked together
+        constexpr int kShare = NT / (kMaxCluster * kMaxTop);
+        const int entry = tid / kShare, of = entry / a.top_k, i = entry % a.top_k, n_keys = ranks * a.top_k;
+        uint64_t key = 0;
+        if (entry < n_keys) {
+          key = cluster.map_shared_rank(&sh, of)->best[i];
+          if (key) key -= static_cast<uint64_t>(of) * a.slice;
+          if (tid % kShare == 0) sh.key[entry] = key;
+        }
         __syncthreads();
-        int better = 0;
-        for (int j = 0; j < kLpThreads; ++j) better += sh.thread_key[j] > key;
+        const int better = rank_in<kShare>(sh.key, n_keys, key);
         __syncthreads();
         if (key && better < a.top_k) sh.best[better] = key;
       }
@@ -310,26 +414,24 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const LogprobsArgs
   __syncthreads();
   const Stat st = sh.stat;
   const bool broken = isnan(st.s), empty = !broken && st.s == 0.0f;
-  const float log_s = logf(st.s);
+  const float log_s = log2f(st.s);
   const float nan = __int_as_float(0x7FC00000);
+  const auto logprob_of = [&](int i) {
+    const float x = E::load(src + i), d = fabsf(st.m) < 1.0e6f ? fmaf(x, c, -st.m) : __fmul_rn(x, c) - st.m;
+    return broken ? nan : empty ? -INFINITY : (d - log_s) * kLn2;
+  };
   if (tid == 0) {
-    if (a.lse) a.lse[row] = broken ? nan : empty ? -INFINITY : st.m + log_s;
-    if (a.entropy) a.entropy[row] = broken ? nan : empty ? 0.0f : log_s - st.u / st.s;
+    if (a.lse) a.lse[row] = broken ? nan : empty ? -INFINITY : (st.m + log_s) * kLn2;
+    if (a.entropy) a.entropy[row] = broken ? nan : empty ? 0.0f : (log_s - st.u / st.s) * kLn2;
     if (a.targets) {
       const int t = a.targets[row];
-      float lp = 0.0f;
-      if (t >= 0 && t < a.vocab) {
-        const float x = E::load(src + t) * a.inv_temperature;
-        lp = broken ? nan : empty ? -INFINITY : (x - st.m) - log_s;
-      }
-      a.logprob[row] = lp;
+      a.logprob[row] = t >= 0 && t < a.vocab ? logprob_of(t) : 0.0f;
     }
   }
   if (tid < a.top_k) {
-    const uint64_t key = sh.best[tid];
-    const float x = key_value(key);
-    a.top_logprob[row * a.top_k + tid] = broken ? nan : empty ? -INFINITY : (x - st.m) - log_s;
-    a.top_index[row * a.top_k + tid] = broken ? -1 : key_index(key);
+    const int i = key_index(sh.best[tid]);
+    a.top_logprob[row * a.top_k + tid] = logprob_of(broken ? 0 : i);
+    a.top_index[row * a.top_k + tid] = broken ? -1 : i;
   }
 }
 
@@ -346,7 +448,7 @@ struct BwdArgs {
 // One CTA writes one slice of a row.  Reads and writes every element once:
 // HBM bounds it.  The row's four numbers are loaded once per CTA.
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) logprobs_bwd_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const BwdArgs a) {
   using E = Elem<T>;
   grid_dependency_wait();
   const int64_t row = blockIdx.x / a.slices;
@@ -377,19 +479,19 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_bwd_kernel(const BwdArgs 
   const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(from) & 15);
   const bool together = off == (reinterpret_cast<uintptr_t>(to) & 15);
   const int head = together ? min(n, static_cast<int>((16 - off) % 16 / sizeof(T))) : n;
-  for (int i = tid; i < head; i += kLpThreads) to[i] = E::store(grad(E::load(from + i), i));
+  for (int i = tid; i < head; i += kBwdThreads) to[i] = E::store(grad(E::load(from + i), i));
   const int n_vec = (n - head) / E::kVec;
   const uint4* const v = reinterpret_cast<const uint4*>(from + head);
   uint4* const w = reinterpret_cast<uint4*>(to + head);
 #pragma unroll 4
-  for (int j = tid; j < n_vec; j += kLpThreads) {
+  for (int j = tid; j < n_vec; j += kBwdThreads) {
     float x[E::kVec];
     E::unpack(v[j], x);
 #pragma unroll
     for (int i = 0; i < E::kVec; ++i) x[i] = grad(x[i], head + j * E::kVec + i);
     w[j] = E::pack(x);
   }
-  for (int i = head + n_vec * E::kVec + tid; i < n; i += kLpThreads) to[i] = E::store(grad(E::load(from + i), i));
+  for (int i = head + n_vec * E::kVec + tid; i < n; i += kBwdThreads) to[i] = E::store(grad(E::load(from + i), i));
 }
 
 // Cluster width and slice of the forward pass.  A slice above 72 KB would leave
@@ -404,40 +506,51 @@ int choose_cluster(int n_rows, int64_t row_bytes) {
   return c;
 }
 
-template <typename T>
-int launch_logprobs(LogprobsArgs a, int n_rows, cudaStream_t s) {
-  const int c = choose_cluster(n_rows, static_cast<int64_t>(a.vocab) * sizeof(T));
-  a.slice = ((a.vocab + c - 1) / c + 7) / 8 * 8;
+template <typename T, int NT>
+int launch_rows(const LogprobsArgs& a, int n_rows, int cluster, cudaStream_t s) {
   const size_t smem = (static_cast<size_t>(a.slice) * sizeof(T) + 15) / 16 * 16 + 16;
   constexpr int kMaxSlice = ((kMaxVocab + kMaxCluster - 1) / kMaxCluster + 7) / 8 * 8;
-  KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(logprobs_kernel<T>),
+  KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(logprobs_kernel<T, NT>),
                               static_cast<int>(kMaxSlice * sizeof(T) + 32)));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(n_rows) * c);
-  cfg.blockDim = dim3(kLpThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(n_rows) * cluster);
+  cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = c;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   LaunchScope scope(TWELL_KERNEL_LOGPROBS, s);
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, a) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, NT>, a) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+}
+
+template <typename T>
+int launch_logprobs(LogprobsArgs a, int n_rows, cudaStream_t s) {
+  const int c = choose_cluster(n_rows, static_cast<int64_t>(a.vocab) * sizeof(T));
+  a.slice = ((a.vocab + c - 1) / c + 7) / 8 * 8;
+  // one CTA or less an SM: its threads are all there are to hide the latencies
+  if (static_cast<int64_t>(n_rows) * c <= sm_count() && static_cast<int64_t>(a.slice) * sizeof(T) > 16 * 1024)
+    return launch_rows<T, 1024>(a, n_rows, c, s);
+  return launch_rows<T, 256>(a, n_rows, c, s);
 }
 
 template <typename T>
 int launch_logprobs_bwd(BwdArgs a, int n_rows, cudaStream_t s) {
-  // whole rows of up to 32768 elements; longer ones, or few, in slices of 8192
-  a.slice = a.vocab <= 32768 && n_rows >= 4 * sm_count() ? (a.vocab + 7) / 8 * 8 : 8192;
+  // slices of 32768 elements where there is work for all SMs several times over,
+  // down to 2048 where there is not
+  const int64_t share = static_cast<int64_t>(n_rows) * a.vocab / (8 * sm_count());
+  a.slice = static_cast<int>(share > 32768 ? 32768 : share < 2048 ? 2048 : share) / 8 * 8;
+  if (a.slice > a.vocab) a.slice = (a.vocab + 7) / 8 * 8;
   a.slices = (a.vocab + a.slice - 1) / a.slice;
   if (static_cast<int64_t>(n_rows) * a.slices > INT_MAX) return TWELL_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(n_rows) * a.slices);
   LaunchScope scope(TWELL_KERNEL_LOGPROBS_BWD, s);
-  return launch_pdl(logprobs_bwd_kernel<T>, grid, dim3(kLpThreads), 0, s, a) == cudaSuccess ? TWELL_OK
+  return launch_pdl(logprobs_bwd_kernel<T>, grid, dim3(kBwdThreads), 0, s, a) == cudaSuccess ? TWELL_OK
                                                                                             : TWELL_ERR_CUDA;
 }
 
