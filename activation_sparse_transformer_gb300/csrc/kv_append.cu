@@ -1,12 +1,13 @@
 // Keys and values of a step into the 8-bit paged cache (twell_kv_append).
 //
 // A run is the tokens of one request that fall into one page.  One CTA takes
-// one run of one head of K or of V: it reads the run's 2-byte values once into
-// registers, takes their largest magnitude, sets the scale 2^e from its bits and
+// one run and some heads of K or of V, one head after the other: it reads the
+// run's 2-byte values of a head once into registers (while the head before is being
+// encoded), takes their largest magnitude, sets the scale 2^e from its bits and
 // writes the codes.  Reads 2 bytes and writes 1 byte per value, so HBM bounds
-// long runs and the launch plus three dependent latencies (request, slot, values)
-// bound single tokens.  The tokens of a run lie ld apart, each with 2 D bytes
-// in one piece: 16-byte loads, D / 8 lanes a token.
+// long runs; the launch and three dependent latencies (request, slot, values)
+// bound single tokens, which get a CTA for each head.  The tokens of a run lie ld
+// apart, each with 2 D bytes in one piece: 16-byte loads, D / 8 lanes a token.
 #include <cuda_bf16.h>
 
 #include "kv_internal.h"
@@ -14,7 +15,9 @@
 namespace twell {
 namespace {
 
-constexpr int kAppendThreads = 128;
+// Threads for a full page's run: four 16-byte loads each, which leaves the registers for
+// several CTAs on an SM (with 128 threads whatever the page, pages of 128 tokens took 198 us instead of 78).
+constexpr int append_threads(int page, int dim) { return page * dim / 32 < 128 ? 128 : page * dim / 32; }
 constexpr int kMinExponent = -100;
 
 struct AppendArgs {
@@ -26,6 +29,7 @@ struct AppendArgs {
   const int64_t* slots;
   int32_t* status;
   int n_tokens, n_requests, n_pages, heads;
+  int heads_per_cta;
 };
 
 // Least e with amax <= q 2^e (q = 448 = 1.75 * 2^8 or 127 = 1.984375 * 2^6),
@@ -48,7 +52,9 @@ __device__ __forceinline__ uint32_t encode2(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
     return c;
   }
-  return (static_cast<uint32_t>(__float2int_rn(lo)) & 0xFFu) | ((static_cast<uint32_t>(__float2int_rn(hi)) & 0xFFu) << 8);
+  // 1.5 * 2^23 + x has x rounded to the nearest integer in its low bits
+  const uint32_t l = __float_as_uint(lo + 12582912.0f), h = __float_as_uint(hi + 12582912.0f);
+  return __byte_perm(l, h, 0x7740) & 0xFFFFu;
 }
 
 template <int FMT>
@@ -79,11 +85,12 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w, bool* bad) {
 }
 
 template <int FMT, int D, int P>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(append_threads(P, D)) append_kernel(const AppendArgs a) {
+  constexpr int kThreads = append_threads(P, D);
   constexpr int kLanes = D / 8;                       // lanes of one token, 8 values each
-  constexpr int kRows = kAppendThreads / kLanes;      // tokens of one pass
+  constexpr int kRows = kThreads / kLanes;      // tokens of one pass
   constexpr int kPasses = (P + kRows - 1) / kRows;
-  __shared__ float warp_max[kAppendThreads / 32];
+  __shared__ float warp_max[2][kThreads / 32];
   grid_dependency_wait();
   const int tid = threadIdx.x;
   // run x of the grid: request r has room for floor(cu[r + 1] / P) -
@@ -107,90 +114,111 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     if (tid == 0) report_error(a.status, TWELL_ERR_BAD_FORMAT);
     return;
   }
-  const int head = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
+  const int head0 = blockIdx.y * a.heads_per_cta, head1 = min(a.heads, head0 + a.heads_per_cta);
   const int lane_col = (tid % kLanes) * 8, row0 = tid / kLanes;
-  const uint16_t* src = (is_v ? a.v : a.k) + static_cast<int64_t>(head) * D + lane_col;
   const int64_t ld = is_v ? a.ldv : a.ldk;
+  const uint16_t* const src = (is_v ? a.v : a.k) + beg * ld + lane_col;
+  float* const scales = (is_v ? a.v_scale : a.k_scale) + page * a.heads;
+  uint8_t* const codes = (is_v ? a.v_codes : a.k_codes) + page * a.heads * (P * D);
   const int n = end - beg;
-
-  uint4 w[kPasses];
+  const auto load = [&](int head, uint4 (&w)[kPasses]) {
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int t = row0 + i * kRows;
-    w[i] = t < n ? __ldg(reinterpret_cast<const uint4*>(src + (beg + t) * ld)) : make_uint4(0, 0, 0, 0);
-  }
-  const int64_t cell = page * a.heads + head;
-  float* const scale_at = (is_v ? a.v_scale : a.k_scale) + cell;
-  const float was = first > 0 ? *scale_at : 0.0f;
-  bool bad = false;
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    uint32_t* q = &w[i].x;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      q[j] = finite2(q[j], &bad);
-      amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q[j])), fabsf(bf16_hi(q[j]))));
+    for (int i = 0; i < kPasses; ++i) {
+      const int t = row0 + i * kRows;
+      w[i] = t < n ? __ldg(reinterpret_cast<const uint4*>(src + t * ld + static_cast<int64_t>(head) * D))
+                   : make_uint4(0, 0, 0, 0);
     }
-  }
+  };
+  uint4 next[kPasses];
+  load(head0, next);
+  float next_was = first > 0 ? scales[head0] : 0.0f;
+  for (int head = head0; head < head1; ++head) {
+    uint4 w[kPasses];
 #pragma unroll
-  for (int d = 16; d > 0; d /= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-  if ((tid & 31) == 0) warp_max[tid / 32] = amax;
-  if (bad) report_error(a.status, TWELL_ERR_NOT_FINITE);
-  __syncthreads();
+    for (int i = 0; i < kPasses; ++i) w[i] = next[i];
+    const float was = next_was;
+    if (head + 1 < head1) {
+      load(head + 1, next);
+      if (first > 0) next_was = scales[head + 1];
+    }
+    bool bad = false;
+    float amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kAppendThreads / 32; ++i) amax = fmaxf(amax, warp_max[i]);
-  const int e = scale_exponent<FMT>(amax);
-  const float own = two_to(e);
-  const float scale = fmaxf(own, was);
-  uint8_t* const dst = (is_v ? a.v_codes : a.k_codes) + cell * (P * D);
-  // earlier tokens of the page move to the larger scale
-  if (first > 0 && scale > was) {
-    const float ratio = was / scale;
-    for (int t = row0; t < first; t += kRows) {
-      uint2* at = reinterpret_cast<uint2*>(dst + t * D + lane_col);
-      uint2 c = *at;
-      uint32_t* q = &c.x;
+    for (int i = 0; i < kPasses; ++i) {
+      uint32_t* q = &w[i].x;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float2 lo = decode2<FMT>(q[j] & 0xFFFFu), hi = decode2<FMT>(q[j] >> 16);
-        q[j] = encode2<FMT>(lo.x * ratio, lo.y * ratio) | (encode2<FMT>(hi.x * ratio, hi.y * ratio) << 16);
+      for (int j = 0; j < 4; ++j) {
+        q[j] = finite2(q[j], &bad);
+        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q[j])), fabsf(bf16_hi(q[j]))));
       }
-      *at = c;
     }
-  }
-  // 1 / scale is exact for a power of two; another scale (a cache written by
-  // someone else) divides
-  const bool pow2 = (__float_as_uint(scale) & 0x7FFFFFu) == 0;
-  const float inv = 1.0f / scale;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int t = row0 + i * kRows;
-    if (t >= n) continue;
-    const uint32_t* q = &w[i].x;
-    uint32_t c[4];
+    for (int d = 16; d > 0; d /= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    float* const maxima = warp_max[(head - head0) & 1];  // two, so that one barrier a head is enough
+    if ((tid & 31) == 0) maxima[tid / 32] = amax;
+    if (bad) report_error(a.status, TWELL_ERR_NOT_FINITE);
+    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float lo = bf16_lo(q[j]), hi = bf16_hi(q[j]);
-      c[j] = pow2 ? encode2<FMT>(lo * inv, hi * inv) : encode2<FMT>(lo / scale, hi / scale);
+    for (int i = 0; i < kThreads / 32; ++i) amax = fmaxf(amax, maxima[i]);
+    const float scale = fmaxf(two_to(scale_exponent<FMT>(amax)), was);
+    uint8_t* const dst = codes + static_cast<int64_t>(head) * (P * D);
+    // earlier tokens of the page move to the larger scale
+    if (first > 0 && scale > was) {
+      const float ratio = was / scale;
+      for (int t = row0; t < first; t += kRows) {
+        uint2* at = reinterpret_cast<uint2*>(dst + t * D + lane_col);
+        uint2 c = *at;
+        uint32_t* q = &c.x;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 lo = decode2<FMT>(q[j] & 0xFFFFu), hi = decode2<FMT>(q[j] >> 16);
+          q[j] = encode2<FMT>(lo.x * ratio, lo.y * ratio) | (encode2<FMT>(hi.x * ratio, hi.y * ratio) << 16);
+        }
+        *at = c;
+      }
     }
-    *reinterpret_cast<uint2*>(dst + (first + t) * D + lane_col) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    // 1 / scale is exact for a power of two; another scale (a cache written by
+    // someone else) divides
+    const bool pow2 = (__float_as_uint(scale) & 0x7FFFFFu) == 0;
+    const float inv = 1.0f / scale;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int t = row0 + i * kRows;
+      if (t >= n) continue;
+      const uint32_t* q = &w[i].x;
+      uint32_t c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float lo = bf16_lo(q[j]), hi = bf16_hi(q[j]);
+        if (pow2) lo *= inv, hi *= inv;
+        else lo /= scale, hi /= scale;
+        c[j] = encode2<FMT>(lo, hi);
+      }
+      *reinterpret_cast<uint2*>(dst + (first + t) * D + lane_col) =
+          make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    }
+    if (tid == 0 && scale != was) scales[head] = scale;
   }
-  if (tid == 0 && scale != was) *scale_at = scale;
 }
 
 template <int FMT, int D>
-int launch_append(const AppendArgs& a, int page, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.n_tokens / page + 2 * static_cast<int64_t>(a.n_requests)),
-                  static_cast<unsigned>(a.heads), 2);
+int launch_append(AppendArgs a, int page, cudaStream_t s) {
+  // heads one after the other once every SM has CTAs enough: 24 prompts of up to
+  // 4000 tokens, 8 heads of 128, int8: 87 us with a CTA for each head, 78.7 so
+  // (4.3 TB/s; 84 with four times as many CTAs)
+  const int64_t runs = a.n_tokens / page + 2 * static_cast<int64_t>(a.n_requests);
+  while (a.heads_per_cta < a.heads && runs * 2 * (a.heads / (2 * a.heads_per_cta)) >= 6 * sm_count())
+    a.heads_per_cta *= 2;
+  const dim3 grid(static_cast<unsigned>(runs),
+                  static_cast<unsigned>((a.heads + a.heads_per_cta - 1) / a.heads_per_cta), 2);
   LaunchScope scope(TWELL_KERNEL_KV_APPEND, s);
   cudaError_t e = cudaErrorInvalidValue;
   switch (page) {
-    case 16: e = launch_pdl(append_kernel<FMT, D, 16>, grid, dim3(kAppendThreads), 0, s, a); break;
-    case 32: e = launch_pdl(append_kernel<FMT, D, 32>, grid, dim3(kAppendThreads), 0, s, a); break;
-    case 64: e = launch_pdl(append_kernel<FMT, D, 64>, grid, dim3(kAppendThreads), 0, s, a); break;
-    case 128: e = launch_pdl(append_kernel<FMT, D, 128>, grid, dim3(kAppendThreads), 0, s, a); break;
+    case 16: e = launch_pdl(append_kernel<FMT, D, 16>, grid, dim3(append_threads(16, D)), 0, s, a); break;
+    case 32: e = launch_pdl(append_kernel<FMT, D, 32>, grid, dim3(append_threads(32, D)), 0, s, a); break;
+    case 64: e = launch_pdl(append_kernel<FMT, D, 64>, grid, dim3(append_threads(64, D)), 0, s, a); break;
+    case 128: e = launch_pdl(append_kernel<FMT, D, 128>, grid, dim3(append_threads(128, D)), 0, s, a); break;
   }
   return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }
@@ -217,7 +245,7 @@ extern "C" TWELL_API int twell_kv_append(const uint16_t* K, int64_t ldk, const u
   if (!device_is_sm103()) return TWELL_ERR_NO_DEVICE;
   if (n_tokens == 0 || n_requests == 0) return TWELL_OK;
   const AppendArgs a{K, V, ldk, ldv, cache->k, cache->v, cache->k_scale, cache->v_scale, cu_q, slots,
-                     cache->status, n_tokens, n_requests, cache->n_pages, cache->n_heads};
+                     cache->status, n_tokens, n_requests, cache->n_pages, cache->n_heads, 1};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cache->format == TWELL_KV_E4M3)
     return cache->head_dim == 64 ? launch_append<TWELL_KV_E4M3, 64>(a, cache->page_size, s)

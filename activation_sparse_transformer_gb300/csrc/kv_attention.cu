@@ -7,11 +7,12 @@
 // 16 rows of an mma tile, so each cached byte is read once for all of them.
 // Per 16 cached tokens a warp computes
 //   S = Q K^T                 fp16 x fp16 -> fp32, codes exact in fp16
-//   l = S (c log2(e) 2^k s_k) (2^k: the row's own factor, see load_q)
-//   p = 2^(l - m),  w = p s_v 2^-n  ->  fp16,  O += w V
-// in one pass with running references: m follows the largest l and n the
-// largest l + log2 s_v, both per row, so that neither the sum of p nor the
-// fp16 weights leave their range whatever the pages' scales are.
+//   l = S (c log2(e) 2^k s_k) + log2 s_v   (2^k: the row's own factor, see convert_q)
+//   w = 2^(l - n)  ->  fp16,  O += w V,  sum += w / s_v
+// in one pass.  n is the row's reference: it follows the largest l, that is,
+// the largest weight that a code is multiplied with, so the fp16 weights stay in their
+// range whatever the pages' scales are; the sum is fp32 and may differ from O's
+// scale by as much as the scales do (pages 2^100 apart are told apart still).
 //
 // The products are computed transposed, S^T = K Q^T and O^T = V^T P^T, with the
 // cached tokens (or the dims) on the 16-wide side of the mma and the rows on the
@@ -24,6 +25,7 @@
 // dims come out in runs.  No transposition lies between the cache and the mma;
 // P's 8 x 8 blocks are turned by movmatrix.
 #include <algorithm>
+#include <cfloat>
 
 #include "kv_attention.h"
 
@@ -37,8 +39,8 @@ constexpr int kMaxRows = 8 * kMaxTiles;
 constexpr int kAttGroup = 16;   // cached tokens of one mma, all of one page
 constexpr int kAttStep = 2 * kAttGroup;  // cached tokens of one warp step
 constexpr int kAttMaxRequests = 4096;
-// The references m and n are moved only when a new value passes them by this
-// much (as powers of two): weights up to 2^8 stay well inside fp16.
+// The reference n is moved only when a new value passes it by this much (as a
+// power of two): weights up to 2^8 stay well inside fp16.
 constexpr float kLazy = 8.0f;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -52,9 +54,9 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
 template <int D, int NT>
 struct TileState {
   float acc[NT][D / 16][4];   // i: dims (D / 8) g + 2 i (both rows), then + 1 (both rows)
-  float m[NT][2], n[NT][2];              // the references (0 before the first step)
-  float top_m[NT][2], top_n[NT][2];      // what a value must pass to move them
-  float sum[NT][2];
+  float n[NT][2];     // the reference (0 before the first step)
+  float pass[NT][2];  // what an exponent must pass to move it
+  float sum[NT][2];   // sum of 2^(l - n)
 };
 
 template <int D, int NT>
@@ -67,8 +69,8 @@ __device__ __forceinline__ void reset(TileState<D, NT>& s) {
       for (int j = 0; j < 4; ++j) s.acc[t][i][j] = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      s.m[t][i] = s.n[t][i] = s.sum[t][i] = 0.0f;
-      s.top_m[t][i] = s.top_n[t][i] = -INFINITY;
+      s.n[t][i] = s.sum[t][i] = 0.0f;
+      s.pass[t][i] = -INFINITY;
     }
   }
 }
@@ -136,7 +138,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 template <int FMT, int D, int NT>
 __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)[NT][D / 16][2],
                                        const float (&factor)[NT][2], const uint8_t* stage, const float (&ks)[2],
-                                       const float (&vs)[2], int j0, const int (&limit)[NT][2], int least, int len) {
+                                       const float (&lvs)[2], const float (&ivs)[2], int j0, const int (&limit)[NT][2], int least, int len) {
   const int lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
   float x[2][NT][4];
 #pragma unroll
@@ -162,24 +164,21 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
     }
   }
   const bool mask = j0 + kAttStep > least;
-  float lvs[2];
   bool move = false;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    lvs[h] = fmaxf(log2_fast(vs[h]), -200.0f);  // a scale of zero stands for zeros
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float f = factor[t][c] * ks[h];
-        x[h][t][c] *= f;
-        x[h][t][2 + c] *= f;
+        const float f = fmaxf(factor[t][c] * ks[h], FLT_MIN);  // a masked -inf stays so
         if (mask) {
           if (j0 + 16 * h + g >= limit[t][c]) x[h][t][c] = -INFINITY;
           if (j0 + 16 * h + g + 8 >= limit[t][c]) x[h][t][2 + c] = -INFINITY;
         }
-        const float v = fmaxf(x[h][t][c], x[h][t][2 + c]);
-        move |= v > s.top_m[t][c] || v + lvs[h] > s.top_n[t][c];
+        x[h][t][c] = fmaf(x[h][t][c], f, lvs[h]);
+        x[h][t][2 + c] = fmaf(x[h][t][2 + c], f, lvs[h]);
+        move |= fmaxf(x[h][t][c], x[h][t][2 + c]) > s.pass[t][c];
       }
   }
   if (__any_sync(0xffffffffu, move)) {
@@ -187,24 +186,16 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float m = fmaxf(fmaxf(x[0][t][c], x[0][t][2 + c]), fmaxf(x[1][t][c], x[1][t][2 + c]));
-        float n = fmaxf(fmaxf(x[0][t][c], x[0][t][2 + c]) + lvs[0], fmaxf(x[1][t][c], x[1][t][2 + c]) + lvs[1]);
+        float n = fmaxf(fmaxf(x[0][t][c], x[0][t][2 + c]), fmaxf(x[1][t][c], x[1][t][2 + c]));
 #pragma unroll
-        for (int d = 4; d <= 16; d *= 2) {
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-          n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
-        }
-        if (m == -INFINITY) continue;  // the row has seen nothing yet, or nothing here
-        // the references only grow; before the first value they are 0 and so are the sums
-        m = fmaxf(m, s.top_m[t][c] - kLazy);
-        n = fmaxf(n, s.top_n[t][c] - kLazy);
-        const bool none = s.sum[t][c] == 0.0f;
-        const float f = none ? 0.0f : exp2_fast(s.n[t][c] - n);
-        s.sum[t][c] *= none ? 0.0f : exp2_fast(s.m[t][c] - m);
-        s.m[t][c] = m;
+        for (int d = 4; d <= 16; d *= 2) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
+        if (n == -INFINITY) continue;  // nothing seen here
+        // the reference only grows; before the first value it is 0 and so is the sum
+        n = fmaxf(n, s.pass[t][c] - kLazy);
+        const float f = s.sum[t][c] == 0.0f ? 0.0f : exp2_fast(s.n[t][c] - n);
+        s.sum[t][c] *= f;
         s.n[t][c] = n;
-        s.top_m[t][c] = m + kLazy;
-        s.top_n[t][c] = n + kLazy;
+        s.pass[t][c] = n + kLazy;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           s.acc[t][i][c] *= f;
@@ -220,11 +211,9 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
       float w[4];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float f = exp2_fast(fminf(s.m[t][c] - s.n[t][c] + lvs[h], 100.0f));
-        const float p0 = exp2_fast(x[h][t][c] - s.m[t][c]), p1 = exp2_fast(x[h][t][2 + c] - s.m[t][c]);
-        s.sum[t][c] += p0 + p1;
-        w[c] = p0 * f;
-        w[2 + c] = p1 * f;
+        w[c] = exp2_fast(x[h][t][c] - s.n[t][c]);
+        w[2 + c] = exp2_fast(x[h][t][2 + c] - s.n[t][c]);
+        s.sum[t][c] = fmaf(w[c] + w[2 + c], ivs[h], s.sum[t][c]);
       }
       pb[t][0] = transpose8(pack_f16(w[0], w[1]));
       pb[t][1] = transpose8(pack_f16(w[2], w[3]));
@@ -263,11 +252,13 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
   }
 }
 
-// Eight dims of one finished row: o 2^(n - m) / sum, rounded once, and the row's lse.
+// Eight dims of one finished row: o / sum, rounded once, and the row's lse.
+// n = -inf: the row has seen nothing.
 template <int D>
-__device__ __forceinline__ void store_row(const AttArgs& a, int t0, int row, int head, int d0, float m, float n,
-                                          float sum, const float (&o)[8]) {
-  const float f = m > -INFINITY ? exp2_fast(n - m) / sum : 0.0f;
+__device__ __forceinline__ void store_row(const AttArgs& a, int t0, int row, int head, int d0, float n, float sum,
+                                          const float (&o)[8]) {
+  const bool seen = n > -INFINITY;
+  const float f = seen ? 1.0f / sum : 0.0f;
   const int64_t token = t0 + row / a.group;
   const int h = head * a.group + row % a.group;
   uint32_t out[4];
@@ -277,8 +268,7 @@ __device__ __forceinline__ void store_row(const AttArgs& a, int t0, int row, int
              (static_cast<uint32_t>(float_to_bf16_bits(o[2 * i + 1] * f)) << 16);
   *reinterpret_cast<uint4*>(a.o + token * a.ldo + static_cast<int64_t>(h) * D + d0) =
       make_uint4(out[0], out[1], out[2], out[3]);
-  if (a.lse && d0 == 0)
-    a.lse[token * a.q_heads + h] = m > -INFINITY ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+  if (a.lse && d0 == 0) a.lse[token * a.q_heads + h] = seen ? (n + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
 template <int D>
@@ -290,17 +280,21 @@ __device__ __forceinline__ void zero_row(const AttArgs& a, int64_t t, int tid, i
 }
 
 // ------------------------------------------------------------ work split
-// A segment is one tile of 16 rows of one key head with all its cached tokens,
-// in units of 128 of them.  The segments of all requests, laid end to end, are
-// cut into as many equal pieces as CTAs run, so the lengths of the requests
-// do not matter for the balance.  A piece's cut segments leave partial results in the
-// workspace (two a CTA: of the segment it starts in the middle of, and of the
-// one it ends in the middle of), which join_kernel adds in order.
+// A segment is one row block of one key head with all its cached tokens, in
+// units of 128 of them.  The segments of all requests, laid end to end, are
+// cut into as many equal pieces as CTAs run, so the lengths of the requests do
+// not matter for the balance; every CTA sums up the requests itself (a few loads a
+// thread) rather than wait for another kernel.  A piece's cut segments leave partial results in the workspace (two a CTA: of the
+// segment it starts in the middle of, and of the one it ends in the middle of), which
+// join_kernel adds in order.  (Adding them in the CTA that finishes last costs more:
+// one CTA's loads have to bring in all parts, 19.6 against 16.8 us for 16 requests of up to 1000 tokens.)
 constexpr int kUnit = kAttStep * kAttWarps;  // cached tokens of a unit: a step of each warp
 constexpr int kMaxCtas = 608;
+constexpr int kMaxSmem = 224 * 1024;  // dynamic, of a CTA
 // Segments of up to this many units are never cut: their join would cost more
 // than the imbalance of leaving them whole.
 constexpr int kWholeUnits = 2;
+constexpr int kNoJoinUnits = 8;  // see launch_attention
 // Whole segments of up to this many units (512 tokens) go to single warps.
 constexpr int kWarpUnits = 4;
 
@@ -317,9 +311,22 @@ __device__ __forceinline__ int row_blocks_of(const Request& q) {
   return (q.n_rows + 8 * NT - 1) / (8 * NT);
 }
 
+// How the segments are dealt out.
+enum Split {
+  kCut,    // equal units, segments cut
+  kWhole,  // equal units, the cuts moved to segments' starts: no join
+  kEach    // every segment to a CTA of its own (there are CTAs enough): no join
+};
+
+// What a segment counts for in the split.
+__device__ __forceinline__ int span_of(const Request& q, int split) {
+  const int units = units_of(q);
+  return split == kEach ? min(units, 1) : units;
+}
+
 // start[r] = units of the requests before r, start[n_requests] = all; by the whole CTA.
 template <int NT>
-__device__ __forceinline__ void scan_requests(const AttArgs& a, int64_t* start, int64_t* warp_sum) {
+__device__ __forceinline__ void scan_requests(const AttArgs& a, int64_t* start, int64_t* warp_sum, int split) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.n_requests + kAttThreads - 1) / kAttThreads;
   const int r0 = min(a.n_requests, tid * per), r1 = min(a.n_requests, r0 + per);
@@ -327,7 +334,7 @@ __device__ __forceinline__ void scan_requests(const AttArgs& a, int64_t* start, 
   for (int r = r0; r < r1; ++r) {
     const Request q = request(a, r);
     const int64_t w =
-        q.n_rows > a.chunk_rows ? 0 : static_cast<int64_t>(units_of(q)) * row_blocks_of<NT>(q) * a.heads;
+        q.n_rows > a.chunk_rows ? 0 : static_cast<int64_t>(span_of(q, split)) * row_blocks_of<NT>(q) * a.heads;
     start[r] = w;
     mine += w;
   }
@@ -367,25 +374,27 @@ __device__ __forceinline__ int request_at(const int64_t* start, int n, int64_t u
 
 // Cut b of n_cuts over all units: moved to its segment's start where the segment stays whole.
 __device__ __forceinline__ int64_t cut_at(const AttArgs& a, const int64_t* start, int64_t b, int64_t n_cuts,
-                                          bool whole) {
+                                          int split) {
   const int64_t all = start[a.n_requests];
   const int64_t u = b * all / n_cuts;
   if (b == 0 || u >= all) return b == 0 ? 0 : all;
   const int r = request_at(start, a.n_requests, u);
+  if (split == kEach) return u;
   const int units = units_of(request(a, r));
-  const int64_t in = (u - start[r]) % units;
-  return whole || units <= kWholeUnits ? u - in : u;
+  return split == kWhole || units <= kWholeUnits ? u - (u - start[r]) % units : u;
 }
 
 // A warp's own ring of stages in shared memory: a step's keys, then its values,
 // each D bytes a token as in the cache.
 template <int D>
 struct Ring {
-  static constexpr int kStages = D == 128 ? 2 : 3;
-  static constexpr int kGroup = kAttGroup * D, kStage = 4 * kGroup, kWarp = kStages * kStage;
-  static_assert(kWarp >= static_cast<int>(partial_floats<D>() * 4), "a warp's results take the ring's place");
+  // with as many CTAs on an SM as its registers allow, and with one
+  static constexpr int kLeast = D == 128 ? 2 : 3, kMost = D == 128 ? 6 : 12;
+  static constexpr int kGroup = kAttGroup * D, kStage = 4 * kGroup;
+  static_assert(kLeast * kStage >= static_cast<int>(partial_floats<D>() * 4), "a warp's results take the ring's place");
+  int stages;
   uint8_t* data;
-  uint64_t* full;   // [kStages] mbarriers, two arrivals each: one a group
+  uint64_t* full;   // [stages] mbarriers, two arrivals each: one a group
   volatile int* abort;
   int slot;         // the stage of the next step
   uint32_t phases;  // bit i: the parity that full[i] completes next
@@ -400,7 +409,7 @@ struct Stream {
 };
 
 // The copies (bulk copies of 16 D bytes, the keys and the values of a group) run
-// kStages - 1 steps ahead of the arithmetic, over the ends of segments too.  Lane l
+// a ring less one step ahead of the arithmetic, over the ends of segments too.  Lane l
 // looks after the groups l, l + 32, ... of a segment: it holds the page's
 // place and scales and issues the copies.  Several segments need at most 32 groups.
 template <int FMT, int D, int NT, typename Emit>
@@ -415,16 +424,18 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
     int64_t cell;   // of head 0
     int offset;     // bytes inside a page's head
     bool on;        // there is such a group
-    float ks, vs;
+    float ks, lvs, ivs;  // key scale, log2 and inverse of the value scale
   };
   const auto scales_of = [&](Batch& b, int head) {
     if (b.on) {
+      const float vs = __ldg(a.v_scale + b.cell + head);
       b.ks = __ldg(a.k_scale + b.cell + head);
-      b.vs = __ldg(a.v_scale + b.cell + head);
+      b.lvs = fmaxf(log2_fast(vs), -200.0f);
+      b.ivs = 1.0f / vs;
     }
   };
   const auto batch_from = [&](int step, int head) {
-    Batch b = {0, 0, false, 0.0f, 0.0f};
+    Batch b = {0, 0, false, 1.0f, 0.0f, 1.0f};
     const int mine = step + lane / 2;
     const int j = st.j_first + mine * st.j_stride + (lane & 1) * kAttGroup;
     if (mine < st.n_steps && j < st.len) {
@@ -460,15 +471,15 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
         mbar_arrive(bar);
       }
     }
-    f_slot = f_slot + 1 == R::kStages ? 0 : f_slot + 1;
+    f_slot = f_slot + 1 == ring.stages ? 0 : f_slot + 1;
     if (++f_step == st.n_steps) {
       f_step = 0;
       f_seg += kAttWarps;
       f_head = f_seg / st.blocks;
     }
   };
-#pragma unroll
-  for (int i = 0; i < R::kStages - 1; ++i) fetch();
+#pragma unroll 1
+  for (int i = 0; i < ring.stages - 1; ++i) fetch();
   RawQ<D, NT> raw;
   load_q<D, NT>(a, q.t0, q.n_rows, st.seg % st.blocks * (8 * NT), head, raw);
   int limit[NT][2], least = st.len;
@@ -516,11 +527,12 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
         report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
       ring.phases ^= 1u << ring.slot;
       const uint8_t* const stage = ring.data + ring.slot * R::kStage;
-      ring.slot = ring.slot + 1 == R::kStages ? 0 : ring.slot + 1;
+      ring.slot = ring.slot + 1 == ring.stages ? 0 : ring.slot + 1;
       const int from = 2 * (step & 15);
       const float ks[2] = {__shfl_sync(0xffffffffu, now.ks, from), __shfl_sync(0xffffffffu, now.ks, from + 1)};
-      const float vs[2] = {__shfl_sync(0xffffffffu, now.vs, from), __shfl_sync(0xffffffffu, now.vs, from + 1)};
-      step32<FMT, D, NT>(s, qb, factor, stage, ks, vs, st.j_first + step * st.j_stride, limit, least, st.len);
+      const float lvs[2] = {__shfl_sync(0xffffffffu, now.lvs, from), __shfl_sync(0xffffffffu, now.lvs, from + 1)};
+      const float ivs[2] = {__shfl_sync(0xffffffffu, now.ivs, from), __shfl_sync(0xffffffffu, now.ivs, from + 1)};
+      step32<FMT, D, NT>(s, qb, factor, stage, ks, lvs, ivs, st.j_first + step * st.j_stride, limit, least, st.len);
     }
     __syncwarp();
 #pragma unroll
@@ -529,7 +541,7 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int d = 4; d <= 16; d *= 2) s.sum[t][c] += __shfl_xor_sync(0xffffffffu, s.sum[t][c], d);
-        if (s.sum[t][c] == 0.0f) s.m[t][c] = s.n[t][c] = -INFINITY;  // nothing seen
+        if (s.sum[t][c] == 0.0f) s.n[t][c] = -INFINITY;  // nothing seen
       }
     emit(s, head, row0);
     head = next_head;
@@ -538,26 +550,27 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
 
 template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D == 64 ? 3 : 2)
-    attention_kernel(const AttArgs a, float* partial, Piece* pieces, int whole) {
+    attention_kernel(const AttArgs a, float* partial, Piece* pieces, int split, int stages) {
   using R = Ring<D>;
-  extern __shared__ __align__(16) uint8_t dyn[];
-  uint8_t* const ring_all = dyn;
-  int64_t* const start = reinterpret_cast<int64_t*>(dyn + kAttWarps * R::kWarp);
+  extern __shared__ __align__(16) uint8_t ring_all[];
+  const int ring_bytes = stages * R::kStage;  // of a warp
+  int64_t* const start = reinterpret_cast<int64_t*>(ring_all + kAttWarps * ring_bytes);
   __shared__ int64_t warp_sum[kAttWarps];
-  grid_dependency_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, quad = lane & 3;
-  __shared__ uint64_t full[kAttWarps][R::kStages];
+  __shared__ uint64_t full[kAttWarps][R::kMost];
   __shared__ int abort_flag;
-  Ring<D> ring = {ring_all + warp * R::kWarp, full[warp], &abort_flag, 0, 0};
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, quad = lane & 3;
+  Ring<D> ring = {stages, ring_all + warp * ring_bytes, full[warp], &abort_flag, 0, 0};
   if (tid == 0) abort_flag = 0;
-  if (lane < R::kStages) mbar_init(full[warp] + lane, 2);
+  if (lane < stages) mbar_init(full[warp] + lane, 2);
   mbar_fence_init();
-  scan_requests<NT>(a, start, warp_sum);
+  grid_dependency_wait();
+  scan_requests<NT>(a, start, warp_sum, split);
+  const int64_t all = start[a.n_requests];
   // at least a unit for each CTA that works, so that every CTA between a cut
   // segment's first and last has a part of it
-  const int64_t cta = blockIdx.x, n_ctas = min(static_cast<int64_t>(gridDim.x), start[a.n_requests]);
-  const int64_t end = cta < n_ctas ? cut_at(a, start, cta + 1, n_ctas, whole) : 0;
-  int64_t pos = cta < n_ctas ? cut_at(a, start, cta, n_ctas, whole) : 0;
+  const int64_t cta = blockIdx.x, n_ctas = min(static_cast<int64_t>(gridDim.x), all);
+  const int64_t end = cta < n_ctas ? cut_at(a, start, cta + 1, n_ctas, split) : 0;
+  int64_t pos = cta < n_ctas ? cut_at(a, start, cta, n_ctas, split) : 0;
   if (tid == 0) pieces[cta].last_cta = -1;
   // requests without cached tokens, and tokens of no request
   for (int r = blockIdx.x; r < a.n_requests; r += gridDim.x) {
@@ -573,15 +586,16 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D =
     const int r = request_at(start, a.n_requests, pos);
     const Request q = request(a, r);
     const int units = units_of(q), blocks = row_blocks_of<NT>(q);
-    const int64_t seg0 = (pos - start[r]) / units;
-    const int unit0 = static_cast<int>((pos - start[r]) % units);
+    const int span = split == kEach ? 1 : units;
+    const int64_t seg0 = (pos - start[r]) / span;
+    const int unit0 = static_cast<int>((pos - start[r]) % span);
     Stream st;
     st.table = a.block_table + static_cast<int64_t>(r) * a.max_blocks;
     st.len = q.len;
-    if (unit0 == 0 && units <= kWarpUnits && end - pos >= units) {
+    const int64_t left = static_cast<int64_t>(blocks) * a.heads - seg0;
+    const int count = static_cast<int>(min(left, (end - pos) / span));
+    if (unit0 == 0 && units <= kWarpUnits && count >= kAttWarps) {
       // short segments that lie whole in this piece: each warp takes every fourth
-      const int64_t left = static_cast<int64_t>(blocks) * a.heads - seg0;
-      const int count = static_cast<int>(min(left, (end - pos) / units));
       st.j_first = 0;
       st.j_stride = kAttStep;
       st.n_steps = (q.len + kAttStep - 1) / kAttStep;
@@ -589,7 +603,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D =
       st.seg_end = static_cast<int>(seg0) + count;
       st.blocks = blocks;
       turn += count;
-      pos += static_cast<int64_t>(count) * units;
+      pos += static_cast<int64_t>(count) * span;
       run_stream<FMT, D, NT>(a, st, q, ring, [&](TileState<D, NT>& s, int head, int row0) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -602,14 +616,15 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D =
               float o[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) o[i] = s.acc[t][(i0 + i) / 2][2 * (i & 1) + c];
-              store_row<D>(a, q.t0, row, head, (D / 8) * g + i0, s.m[t][c], s.n[t][c], s.sum[t][c], o);
+              store_row<D>(a, q.t0, row, head, (D / 8) * g + i0, s.n[t][c], s.sum[t][c], o);
             }
           }
       });
       continue;
     }
-    const int n_units = static_cast<int>(min(static_cast<int64_t>(units - unit0), end - pos));
-    pos += n_units;
+    const int n_units =
+        split == kEach ? units : static_cast<int>(min(static_cast<int64_t>(units - unit0), end - pos));
+    pos += split == kEach ? 1 : n_units;
     st.j_first = unit0 * kUnit + warp * kAttStep;
     st.j_stride = kUnit;
     const int seen = min(n_units * kUnit, q.len - unit0 * kUnit) - warp * kAttStep;
@@ -627,7 +642,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D =
           const int row = 8 * t + 2 * quad + c;
           if (row0 + row >= q.n_rows) continue;
           float* const at = mine + row * (D + 4);
-          if (g == 0) at[D] = s.m[t][c], at[D + 1] = s.n[t][c], at[D + 2] = s.sum[t][c];
+          if (g == 0) at[D] = s.n[t][c], at[D + 1] = s.sum[t][c];
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) at[(D / 8) * g + i] = s.acc[t][i / 2][2 * (i & 1) + c];
         }
@@ -635,42 +650,38 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D =
     __syncthreads();
     const int head = st.seg / blocks, row0 = st.seg % blocks * (8 * NT);
     constexpr int kLanes = D / 8;
-    const bool complete = n_units == units, goes_on = unit0 + n_units < units;
+    const bool complete = n_units == units;
     // a cut segment's part: slot 1 where it starts here, slot 0 where it came from the CTA before
     float* const out = partial + (2 * cta + (unit0 == 0 ? 1 : 0)) * partial_floats<D>();
-    if (unit0 == 0 && goes_on && tid == 0) {
+    if (unit0 == 0 && !complete && tid == 0) {
       // cuts inside a segment that may be cut are where the even split puts
       // them, so the CTA of its last unit follows from the split alone
       const int64_t seg_end = pos + (units - n_units);
-      pieces[cta] = {q.t0, q.n_rows, row0, head,
-                     static_cast<int32_t>((seg_end * n_ctas - 1) / start[a.n_requests]), {0, 0, 0}};
+      pieces[cta] = {q.t0, q.n_rows, row0, head, static_cast<int32_t>((seg_end * n_ctas - 1) / all), {0, 0, 0}};
     }
     for (int row = tid / kLanes; row < min(8 * NT, q.n_rows - row0); row += kAttThreads / kLanes) {
       const int d0 = (tid % kLanes) * 8;
-      float m = -INFINITY, n = -INFINITY, sum = 0.0f, o[8] = {};
+      float n = -INFINITY, sum = 0.0f, o[8] = {};
 #pragma unroll
-      for (int w = 0; w < kAttWarps; ++w) {
-        const float* at = reinterpret_cast<const float*>(ring_all + w * R::kWarp) + row * (D + 4);
-        m = fmaxf(m, at[D]);
-        n = fmaxf(n, at[D + 1]);
-      }
-      if (m > -INFINITY) {
+      for (int w = 0; w < kAttWarps; ++w)
+        n = fmaxf(n, reinterpret_cast<const float*>(ring_all + w * ring_bytes)[row * (D + 4) + D]);
+      if (n > -INFINITY) {
 #pragma unroll
         for (int w = 0; w < kAttWarps; ++w) {
-          const float* at = reinterpret_cast<const float*>(ring_all + w * R::kWarp) + row * (D + 4);
-          sum += at[D + 2] * exp2_fast(at[D] - m);
-          const float f = exp2_fast(at[D + 1] - n);
+          const float* at = reinterpret_cast<const float*>(ring_all + w * ring_bytes) + row * (D + 4);
+          const float f = exp2_fast(at[D] - n);
+          sum += at[D + 1] * f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] += at[d0 + i] * f;
         }
       }
       if (complete) {
-        store_row<D>(a, q.t0, row0 + row, head, d0, m, n, sum, o);
+        store_row<D>(a, q.t0, row0 + row, head, d0, n, sum, o);
       } else {
         float* const to = out + row * (D + 4);
         *reinterpret_cast<float4*>(to + d0) = make_float4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<float4*>(to + d0 + 4) = make_float4(o[4], o[5], o[6], o[7]);
-        if (d0 == 0) *reinterpret_cast<float4*>(to + D) = make_float4(m, n, sum, 0.0f);
+        if (d0 == 0) *reinterpret_cast<float4*>(to + D) = make_float4(n, sum, 0.0f, 0.0f);
       }
     }
     fence_async_shared();  // the results' place is the copies' again
@@ -678,69 +689,114 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D =
   }
 }
 
-// Adds a cut segment's parts in the order of its units: one CTA for each CTA
-// of attention_kernel, idle unless a segment starts there and goes on.
+// Adds a cut segment's parts: a CTA for each row of a segment that starts in one
+// CTA of attention_kernel and goes on in others.  Teams of D / 8 lanes take the
+// parts in turn, eight loads of each lane in flight, and are added in order.
+constexpr int kTeams = 16;
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttThreads) join_kernel(const AttArgs a, const float* partial, const Piece* pieces) {
+__global__ void __launch_bounds__(kTeams * D / 8) join_kernel(const AttArgs a, const float* partial, const Piece* pieces) {
+  constexpr int kLanes = D / 8, kMost = 8;
+  __shared__ float sh_o[kTeams][D + 4], sh_n[kTeams], sh_sum[kTeams];
   grid_dependency_wait();
-  const int cta = blockIdx.x, tid = threadIdx.x;
+  const int cta = blockIdx.x, row = blockIdx.y, tid = threadIdx.x;
   const Piece p = pieces[cta];
-  if (p.last_cta <= cta) return;
-  constexpr int kLanes = D / 8;
-  const int d0 = (tid % kLanes) * 8;
-  const auto part = [&](int c, int row) {
-    return partial + (2 * static_cast<int64_t>(c) + (c == cta ? 1 : 0)) * partial_floats<D>() + row * (D + 4);
-  };
-  for (int row = tid / kLanes; row < min(8 * NT, p.n_rows - p.row0); row += kAttThreads / kLanes) {
-    float m = -INFINITY, n = -INFINITY, sum = 0.0f, o[8] = {};
-#pragma unroll 4
-    for (int c = cta; c <= p.last_cta; ++c) {
-      const float* const at = part(c, row);
-      m = fmaxf(m, at[D]);
-      n = fmaxf(n, at[D + 1]);
-    }
-    if (m > -INFINITY) {
-#pragma unroll 4
-      for (int c = cta; c <= p.last_cta; ++c) {
-        const float* const at = part(c, row);
-        const float4 st = *reinterpret_cast<const float4*>(at + D), lo = *reinterpret_cast<const float4*>(at + d0),
-                     hi = *reinterpret_cast<const float4*>(at + d0 + 4);
-        sum += st.z * exp2_fast(st.x - m);
-        const float f = exp2_fast(st.y - n);
-        o[0] += lo.x * f, o[1] += lo.y * f, o[2] += lo.z * f, o[3] += lo.w * f;
-        o[4] += hi.x * f, o[5] += hi.y * f, o[6] += hi.z * f, o[7] += hi.w * f;
+  if (p.last_cta <= cta || p.row0 + row >= p.n_rows) return;
+  const int team = tid / kLanes, d0 = (tid % kLanes) * 8;
+  float n = -INFINITY, sum = 0.0f, o[8] = {};
+  for (int c0 = cta + team; c0 <= p.last_cta; c0 += kTeams * kMost) {
+    float4 lo[kMost], hi[kMost];
+    float2 st[kMost];
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const int c = c0 + i * kTeams;
+      st[i] = make_float2(-INFINITY, 0.0f);
+      lo[i] = hi[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (c <= p.last_cta) {
+        const float* const at =
+            partial + (2 * static_cast<int64_t>(c) + (c == cta ? 1 : 0)) * partial_floats<D>() + row * (D + 4);
+        st[i] = *reinterpret_cast<const float2*>(at + D);
+        lo[i] = *reinterpret_cast<const float4*>(at + d0);
+        hi[i] = *reinterpret_cast<const float4*>(at + d0 + 4);
       }
     }
-    store_row<D>(a, p.t0, p.row0 + row, p.head, d0, m, n, sum, o);
+    float m = n;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) m = fmaxf(m, st[i].x);
+    if (m == -INFINITY) continue;
+    const float f0 = exp2_fast(n - m);
+    n = m;
+    sum *= f0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= f0;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const float f = exp2_fast(st[i].x - m);
+      sum += st[i].y * f;
+      o[0] += lo[i].x * f, o[1] += lo[i].y * f, o[2] += lo[i].z * f, o[3] += lo[i].w * f;
+      o[4] += hi[i].x * f, o[5] += hi[i].y * f, o[6] += hi[i].z * f, o[7] += hi[i].w * f;
+    }
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sh_o[team][d0 + i] = o[i];
+  if (d0 == 0) sh_n[team] = n, sh_sum[team] = sum;
+  __syncthreads();
+  if (team > 0) return;
+  n = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kTeams; ++w) n = fmaxf(n, sh_n[w]);
+  sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+  if (n > -INFINITY) {
+#pragma unroll
+    for (int w = 0; w < kTeams; ++w) {
+      const float f = exp2_fast(sh_n[w] - n);
+      sum += sh_sum[w] * f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] += sh_o[w][d0 + i] * f;
+    }
+  }
+  store_row<D>(a, p.t0, p.row0 + row, p.head, d0, n, sum, o);
 }
 
 template <int FMT, int D, int NT>
 int launch_attention(const AttArgs& a, int max_kv_len, int max_q_len, void* workspace, cudaStream_t s) {
   float* const partial = static_cast<float*>(workspace);
   Piece* const pieces = reinterpret_cast<Piece*>(partial + 2 * kMaxCtas * partial_floats<D>());
-  const size_t smem = kAttWarps * Ring<D>::kWarp + sizeof(int64_t) * (static_cast<size_t>(a.n_requests) + 1);
+  constexpr size_t kStageBytes = kAttWarps * Ring<D>::kStage;
+  const size_t sums = sizeof(int64_t) * (static_cast<size_t>(a.n_requests) + 1);
   const void* fn = reinterpret_cast<const void*>(attention_kernel<FMT, D, NT>);
-  KV_TRY(set_max_dynamic_smem(fn, static_cast<int>(kAttWarps * Ring<D>::kWarp + 8 * (kAttMaxRequests + 1))));
-  const int resident = resident_ctas_per_sm(fn, kAttThreads, smem);
+  KV_TRY(set_max_dynamic_smem(fn, kMaxSmem));
+  const int resident = resident_ctas_per_sm(fn, kAttThreads, Ring<D>::kLeast * kStageBytes + sums);
   if (resident < 1) return TWELL_ERR_CUDA;
   // no more CTAs than the units that the caller's bounds allow
   const int64_t blocks = (static_cast<int64_t>(max_q_len) * a.group + 8 * NT - 1) / (8 * NT);
   const int64_t units = (static_cast<int64_t>(max_kv_len) + kUnit - 1) / kUnit;
-  const int64_t most = std::max<int64_t>(1, a.n_requests * a.heads * std::max<int64_t>(1, blocks * units));
-  const int ctas = static_cast<int>(
-      std::min<int64_t>(most, std::min(kMaxCtas, sm_count() * resident)));
-  const bool whole = units <= kWholeUnits;
+  // Cutting saves what a segment is longer than the even share, at 0.5 us a
+  // unit; the join costs 4 to 5 us.  So short caches are not cut at all; and
+  // where their segments are no more than the SMs, each has one to itself, with
+  // all its shared memory for copies ahead (16 requests of up to 1000 tokens, 8 key heads: cut
+  // 19.7 us, moved cuts 18.7, each its own 14.0; 256 requests: 90, 80, 89).
+  const int64_t segments = a.n_requests * a.heads * std::max<int64_t>(1, blocks);
+  const int split = units > kNoJoinUnits ? kCut : segments <= sm_count() ? kEach : kWhole;
+  const int64_t most = std::max<int64_t>(1, split == kEach ? segments : segments * std::max<int64_t>(1, units));
+  const int ctas = static_cast<int>(std::min<int64_t>(most, std::min(kMaxCtas, sm_count() * resident)));
+  // where fewer CTAs share an SM each has more of its shared memory: more copies ahead
+  const int share = (ctas + sm_count() - 1) / sm_count();
+  const int stages = std::min<int>(Ring<D>::kMost, std::max<int>(Ring<D>::kLeast, static_cast<int>(
+      (kMaxSmem / share - static_cast<int>(sums) - 2048) / static_cast<int>(kStageBytes))));
+  const size_t smem = stages * kStageBytes + sums;
   {
     LaunchScope scope(TWELL_KERNEL_KV_ATTENTION, s);
     if (launch_pdl(attention_kernel<FMT, D, NT>, dim3(ctas), dim3(kAttThreads), smem, s, a, partial, pieces,
-                   static_cast<int>(whole)) != cudaSuccess)
+                   split, stages) != cudaSuccess)
       return TWELL_ERR_CUDA;
   }
-  if (whole || ctas == 1) return TWELL_OK;
+  if (split != kCut || ctas == 1) return TWELL_OK;
+  const int rows = static_cast<int>(std::min<int64_t>(8 * NT, static_cast<int64_t>(a.n_tokens) * a.group));
   LaunchScope scope(TWELL_KERNEL_KV_JOIN, s);
-  return launch_pdl(join_kernel<D, NT>, dim3(ctas - 1), dim3(kAttThreads), 0, s, a, static_cast<const float*>(partial),
-                    static_cast<const Piece*>(pieces)) == cudaSuccess
+  return launch_pdl(join_kernel<D, NT>, dim3(ctas - 1, rows), dim3(kTeams * D / 8), 0, s, a,
+                    static_cast<const float*>(partial), static_cast<const Piece*>(pieces)) == cudaSuccess
              ? TWELL_OK
              : TWELL_ERR_CUDA;
 }

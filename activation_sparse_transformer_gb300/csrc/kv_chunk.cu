@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
           float m = __uint_as_float(u[0]);
 #pragma unroll
           for (int i = 1; i < 16; ++i) m = fmaxf(m, __uint_as_float(u[i]));
-          ks[g] *= factor;
+          ks[g] = fmaxf(ks[g] * factor, FLT_MIN);  // a masked -inf stays so
           top = fmaxf(top, fmaf(m, ks[g], lvs[g]));
         }
         const bool move = top > pass;
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
         // taken up, after the values of t - 2 were put in place, which waited for the
         // mma's of t - 4: both softmaxes are through with that step's scales.
         float* const sc = scales + (t & 3) * 3 * kGroups + lane;
-        sc[0] = fmaxf(ks, FLT_MIN);  // a masked S of -inf stays so
+        sc[0] = ks;
         sc[kGroups] = fmaxf(log2_fast(vs), -200.0f);
         sc[2 * kGroups] = 1.0f / vs;
         mbar_arrive(&bar.scale_full[t & 3]);

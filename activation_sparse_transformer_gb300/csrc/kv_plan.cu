@@ -16,13 +16,13 @@
 namespace twell {
 namespace {
 
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxRequests = 16384;
 
 struct PlanArgs {
   const int32_t* kv_lens;
   const int32_t* new_tokens;
-  int n_requests, page, n_pages, max_blocks;
+  int n_requests, page_shift, n_pages, max_blocks;
   int32_t* block_table;
   int32_t* ring;
   const int32_t* pool;
@@ -48,8 +48,14 @@ __device__ __forceinline__ Sums shfl_up(const Sums& a, int d) {
           __shfl_up_sync(0xffffffffu, a.back, d)};
 }
 
-__device__ __forceinline__ int blocks_of(int64_t tokens, int page) {
-  return static_cast<int>((tokens + page - 1) / page);
+__device__ __forceinline__ int blocks_of(int64_t tokens, int page_shift) {
+  return static_cast<int>((tokens + (1 << page_shift) - 1) >> page_shift);
+}
+
+// i mod n for 0 <= i < 2 n, without a division.
+__device__ __forceinline__ int wrap(int64_t i, int n) {
+  if (i >= n) i -= n;
+  return static_cast<int>(i);
 }
 
 // What one request asks for.  One that wants more blocks than its table has
@@ -57,9 +63,9 @@ __device__ __forceinline__ int blocks_of(int64_t tokens, int page) {
 // the running sum passes the free pages (or the tokens' capacity) every later
 // one with a need is refused too: the accepted ones' pages are one run.
 __device__ __forceinline__ Sums asks(const PlanArgs& a, int len, int add) {
-  const int have = blocks_of(len, a.page);
+  const int have = blocks_of(len, a.page_shift);
   if (add < 0) return {0, 0, min(have, a.max_blocks)};
-  const int upto = blocks_of(static_cast<int64_t>(len) + add, a.page);
+  const int upto = blocks_of(static_cast<int64_t>(len) + add, a.page_shift);
   return {add, upto > a.max_blocks ? 0 : upto - have, 0};
 }
 
@@ -104,7 +110,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     const int len = max(a.kv_lens[r], 0), add = a.new_tokens[r];
     const Sums s = asks(a, len, add), upto = run + s;
     const bool no = add > 0 && ((s.need > 0 && upto.need > free_pages) ||
-                                blocks_of(static_cast<int64_t>(len) + add, a.page) > a.max_blocks ||
+                                blocks_of(static_cast<int64_t>(len) + add, a.page_shift) > a.max_blocks ||
                                 upto.tokens > cap);
     cu[r] = static_cast<int32_t>(min(run.tokens, static_cast<int64_t>(cap)));
     base[r] = add < 0 ? -2 - static_cast<int>(run.back) : no ? -1 : static_cast<int>(run.need);
@@ -124,7 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   __syncthreads();
   if (first_cta && tid == 0) {
     a.cu_q[R] = cu[R];
-    a.pool_out[0] = static_cast<int32_t>((static_cast<int64_t>(head) + taken_all) % a.n_pages);
+    a.pool_out[0] = wrap(static_cast<int64_t>(head) + taken_all, a.n_pages);
     a.pool_out[1] = free_pages - taken_all + static_cast<int32_t>(all.back);
     *a.status = refused_any ? TWELL_ERR_CACHE_FULL : TWELL_OK;
   }
@@ -141,30 +147,29 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
         else hi = mid - 1;
       }
       if (base[lo] >= 0) {
-        const int len = max(a.kv_lens[lo], 0), have = blocks_of(len, a.page);
+        const int len = max(a.kv_lens[lo], 0), have = blocks_of(len, a.page_shift);
         pos = len + (t - cu[lo]);
-        const int block = pos / a.page;
+        const int block = pos >> a.page_shift, in = pos & ((1 << a.page_shift) - 1);
         int32_t* const entry = a.block_table + static_cast<int64_t>(lo) * a.max_blocks + block;
         int page;
         if (block < have) {
           page = *entry;
         } else {
-          page = a.ring[(static_cast<int64_t>(head) + base[lo] + (block - have)) % a.n_pages];
-          if (pos % a.page == 0) *entry = page;
+          page = a.ring[wrap(static_cast<int64_t>(head) + base[lo] + (block - have), a.n_pages)];
+          if (in == 0) *entry = page;
         }
-        slot = static_cast<int64_t>(page) * a.page + pos % a.page;
+        slot = static_cast<int64_t>(page) * (1 << a.page_shift) + in;
       }
     }
     a.slots[t] = slot;
     a.positions[t] = pos;
   }
-  // pages of finished requests, a warp per request
-  const int warps = gridDim.x * (kPlanThreads / 32);
-  for (int r = blockIdx.x * (kPlanThreads / 32) + warp; r < R; r += warps) {
+  // pages of finished requests, a CTA per request
+  for (int r = blockIdx.x; r < R; r += gridDim.x) {
     if (base[r] > -2) continue;
-    const int back = min(blocks_of(max(a.kv_lens[r], 0), a.page), a.max_blocks);
+    const int back = min(blocks_of(max(a.kv_lens[r], 0), a.page_shift), a.max_blocks);
     const int64_t to = static_cast<int64_t>(head) + free_pages + (-2 - base[r]);
-    for (int j = lane; j < back; j += 32)
+    for (int j = tid; j < back; j += kPlanThreads)
       a.ring[(to + j) % a.n_pages] = a.block_table[static_cast<int64_t>(r) * a.max_blocks + j];
   }
 }
@@ -199,13 +204,15 @@ extern "C" TWELL_API int twell_kv_plan(const int32_t* kv_lens, const int32_t* ne
     KV_TRY(check_array(positions, 4));
   }
   if (!device_is_sm103()) return TWELL_ERR_NO_DEVICE;
-  const PlanArgs a{kv_lens, new_tokens, n_requests, page_size, n_pages, max_blocks, block_table, ring, pool,
+  const PlanArgs a{kv_lens, new_tokens, n_requests, __builtin_ctz(page_size), n_pages, max_blocks, block_table, ring, pool,
                    pool_out, kv_lens_out, cu_q, slots, positions, n_tokens, status};
   const size_t smem = sizeof(int32_t) * (2 * static_cast<size_t>(n_requests) + 1);
   KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(plan_kernel),
                               sizeof(int32_t) * (2 * kPlanMaxRequests + 1)));
   // every CTA repeats the sums, so no more CTAs than one wave
-  const int want = (n_tokens + kPlanThreads - 1) / kPlanThreads;
+  // (finished requests take a CTA each in turn, so some for those too)
+  const int tokens = (n_tokens + kPlanThreads - 1) / kPlanThreads, requests = (n_requests + 15) / 16;
+  const int want = tokens > requests ? tokens : requests;
   const int grid = want < 1 ? 1 : want < 2 * sm_count() ? want : 2 * sm_count();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   LaunchScope scope(TWELL_KERNEL_KV_PLAN, s);

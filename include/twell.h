@@ -356,7 +356,8 @@ enum {
 
 /* A paged cache of keys and values in 8 bits.  A key is code * k_scale of its
  * page and head (a value likewise); twell_kv_append writes powers of two as
- * scales, the attention takes any positive finite ones.  The struct lives in
+ * scales, the attention takes any positive finite ones (value scales of one
+ * request within 2^100 of each other).  The struct lives in
  * host memory; the pointers are device pointers to caller-owned memory. */
 typedef struct twell_kv_t {
   int32_t n_pages;    /* >= 1 */
@@ -565,7 +566,7 @@ enum {
   TWELL_KERNEL_KV_PLAN = 15,     /* block tables and slot maps of a step */
   TWELL_KERNEL_KV_APPEND = 16,   /* keys and values into the 8-bit cache */
   TWELL_KERNEL_KV_ATTENTION = 17, /* attention over the cache */
-  TWELL_KERNEL_KV_JOIN = 18,     /* join of the split caches' partial results */
+  TWELL_KERNEL_KV_JOIN = 18,     /* join of the cut caches' partial results */
   TWELL_KERNEL_LOGPROBS = 19,    /* log probabilities, entropy, best alternatives */
   TWELL_KERNEL_LOGPROBS_BWD = 20, /* their gradient */
   TWELL_KERNEL_COUNT = 21

@@ -358,6 +358,27 @@ def test_attention_scales_far_apart(tw, fmt):
     check_attention(q, kc, ks, vc, vs, table, cu, positions, lens, 4, 0.125, o, lse)
 
 
+@pytest.mark.parametrize("new", [1, 5, 90])
+def test_attention_zero_and_tiny_queries_under_a_mask(tw, new):
+    """A row of zeros weighs all it sees alike, and what it does not see not at
+    all; rows of the smallest numbers, keys of the smallest scales."""
+    r = np.random.RandomState(new)
+    page, lens = 16, np.array([150])
+    cache, kc, ks, vc, vs = make_cache(tw, "e4m3", 12, page, 1, 64, 2)
+    import torch
+    ks = np.exp2(np.where(r.rand(*ks.shape) < 0.5, -100, -7)).astype(np.float64)
+    cache.k_scale.copy_(dev(ks).float())
+    table = layout(r, lens, page, 12, 11)
+    x = r.randn(new, 4, 64)
+    x[:, 0] = 0
+    x[:, 1] *= 2.0 ** -120
+    x[:, 2, 1:] = 0
+    q = dev(x).to(torch.bfloat16)
+    cu, positions = np.array([0, new], np.int32), np.arange(150 - new, 150).astype(np.int32)
+    o, lse = run_attention(tw, cache, q, table, cu, positions, lens, max_q=new)
+    check_attention(q, kc, ks, vc, vs, table, cu, positions, lens, 4, 0.125, o, lse)
+
+
 def test_attention_page_outside_the_cache_is_reported(tw):
     import torch
     cache, *_ = make_cache(tw, "int8", 3, 16, 1, 64, 4)
