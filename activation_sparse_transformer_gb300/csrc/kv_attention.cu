@@ -252,25 +252,6 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
   }
 }
 
-// Eight dims of one finished row: o / sum, rounded once, and the row's lse.
-// n = -inf: the row has seen nothing.
-template <int D>
-__device__ __forceinline__ void store_row(const AttArgs& a, int t0, int row, int head, int d0, float n, float sum,
-                                          const float (&o)[8]) {
-  const bool seen = n > -INFINITY;
-  const float f = seen ? 1.0f / sum : 0.0f;
-  const int64_t token = t0 + row / a.group;
-  const int h = head * a.group + row % a.group;
-  uint32_t out[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    out[i] = static_cast<uint32_t>(float_to_bf16_bits(o[2 * i] * f)) |
-             (static_cast<uint32_t>(float_to_bf16_bits(o[2 * i + 1] * f)) << 16);
-  *reinterpret_cast<uint4*>(a.o + token * a.ldo + static_cast<int64_t>(h) * D + d0) =
-      make_uint4(out[0], out[1], out[2], out[3]);
-  if (a.lse && d0 == 0) a.lse[token * a.q_heads + h] = seen ? (n + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-}
-
 template <int D>
 __device__ __forceinline__ void zero_row(const AttArgs& a, int64_t t, int tid, int n_threads) {
   for (int i = tid; i < a.q_heads * (D / 8); i += n_threads)
@@ -813,6 +794,11 @@ int launch_dim(const AttArgs& a, int dim, int max_kv_len, int max_q_len, void* w
                : launch_attention<FMT, 128, 2>(a, max_kv_len, max_q_len, workspace, s);
 }
 
+size_t decode_workspace_bytes(int dim) {
+  return (2 * kMaxCtas * static_cast<size_t>(kMaxRows) * (dim + 4) * sizeof(float) + kMaxCtas * sizeof(Piece) + 255) /
+         256 * 256;
+}
+
 }  // namespace
 }  // namespace twell
 
@@ -824,8 +810,8 @@ extern "C" TWELL_API size_t twell_kv_attention_workspace_bytes(int32_t n_tokens,
   if (n_tokens < 0 || n_requests < 0 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads != 0 ||
       (head_dim != 64 && head_dim != 128))
     return 0;
-  return (2 * kMaxCtas * static_cast<size_t>(kMaxRows) * (head_dim + 4) * sizeof(float) + kMaxCtas * sizeof(Piece) + 255) /
-         256 * 256;
+  const int64_t rows = static_cast<int64_t>(n_tokens) * (n_q_heads / n_kv_heads);
+  return decode_workspace_bytes(head_dim) + (chunk_workspace_bytes(rows, head_dim) + 255) / 256 * 256;
 }
 
 extern "C" TWELL_API int twell_kv_attention(const uint16_t* Q, int64_t ldq, const twell_kv_t* cache,
@@ -887,7 +873,8 @@ extern "C" TWELL_API int twell_kv_attention(const uint16_t* Q, int64_t ldq, cons
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (n_requests > 0 && static_cast<int64_t>(max_q_len) * a.group > kChunkRows) {
     a.chunk_rows = kChunkRows;
-    KV_TRY(launch_chunk_attention(a, cache->format, cache->head_dim, s));
+    KV_TRY(launch_chunk_attention(a, cache->format, cache->head_dim, max_kv_len,
+                                  static_cast<uint8_t*>(workspace) + decode_workspace_bytes(cache->head_dim), s));
   }
   return cache->format == TWELL_KV_E4M3 ? launch_dim<TWELL_KV_E4M3>(a, cache->head_dim, max_kv_len, max_q_len, workspace, s)
                                         : launch_dim<TWELL_KV_INT8>(a, cache->head_dim, max_kv_len, max_q_len, workspace, s);

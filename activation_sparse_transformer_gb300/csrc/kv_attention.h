@@ -25,7 +25,8 @@ struct AttArgs {
 // fill tcgen05's 128 rows well enough to pay for the fp16 copy of the cache
 // that its operands need; a.chunk_rows is this, or INT32_MAX when no request is that large.
 constexpr int kChunkRows = 64;
-int launch_chunk_attention(const AttArgs& a, int format, int dim, cudaStream_t s);
+int launch_chunk_attention(const AttArgs& a, int format, int dim, int max_kv_len, void* workspace, cudaStream_t s);
+size_t chunk_workspace_bytes(int64_t rows, int dim);  // for so many rows in all
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -74,6 +75,25 @@ struct Request {
 __device__ __forceinline__ Request request(const AttArgs& a, int r) {
   const int t0 = min(max(a.cu_q[r], 0), a.n_tokens), t1 = min(max(a.cu_q[r + 1], t0), a.n_tokens);
   return {t0, (t1 - t0) * a.group, visible_len(a, r)};
+}
+
+// Eight dims of one finished row: o / sum, rounded once, and the row's lse.
+// n = -inf: the row has seen nothing.
+template <int D>
+__device__ __forceinline__ void store_row(const AttArgs& a, int t0, int row, int head, int d0, float n, float sum,
+                                          const float (&o)[8]) {
+  const bool seen = n > -INFINITY;
+  const float f = seen ? 1.0f / sum : 0.0f;
+  const int64_t token = t0 + row / a.group;
+  const int h = head * a.group + row % a.group;
+  uint32_t out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    out[i] = static_cast<uint32_t>(float_to_bf16_bits(o[2 * i] * f)) |
+             (static_cast<uint32_t>(float_to_bf16_bits(o[2 * i + 1] * f)) << 16);
+  *reinterpret_cast<uint4*>(a.o + token * a.ldo + static_cast<int64_t>(h) * D + d0) =
+      make_uint4(out[0], out[1], out[2], out[3]);
+  if (a.lse && d0 == 0) a.lse[token * a.q_heads + h] = seen ? (n + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace twell

@@ -18,6 +18,12 @@
 //
 // 4 D flops for each (row, token): tensor cores bound it, then the exponentials
 // and the shared memory that feeds both operands of S.
+//
+// 4 chunks of 556 to 966 tokens at the end of 5668 to 8192, 32 / 8 heads of 128, e4m3: 357 us,
+// 925 TFLOP/s (a step 2.4 us, its mma's alone 1.1).  Taking the blocks as they come,
+// uncut, 380; longest first, uncut, 381 (376 blocks are 2.5 waves); longest first with the last wave
+// cut 357.  One chunk of 541 tokens at the end of 32768: 534 -> 462 us with up to 4 waves of parts.
+#include <algorithm>
 #include <cfloat>
 
 #include "kv_attention.h"
@@ -35,6 +41,10 @@ constexpr int kThreads = 16 * 32;
 constexpr int kRegsSoftmax = 184, kRegsOperands = 88, kRegsMma = 56;
 static_assert(2 * kRegsSoftmax + kRegsOperands + kRegsMma == 4 * 128, "register split");
 constexpr float kLazy = 8.0f;
+constexpr int kMaxWaves = 4, kMaxParts = kMaxWaves * 152;  // CTAs that leave parts of rows
+constexpr int kJoinSteps = 8;
+template <int D>
+constexpr int kPartFloats = D + 4;  // of a row: the sums over the values, the reference, the sum
 
 template <int D>
 struct ChunkSmem {
@@ -45,7 +55,7 @@ struct ChunkSmem {
   static constexpr uint32_t kRawAt = kVAt + 2 * kV, kRaw = kTokens * D;  // codes of a step's keys, of its values
   static constexpr uint32_t kScaleAt = kRawAt + 2 * kRaw;
   static constexpr uint32_t kBarAt = kScaleAt + 4 * 3 * kGroups * 4;
-  static constexpr uint32_t kBytes = kBarAt + 256;
+  static constexpr uint32_t kBytes = kBarAt + 512;
 };
 
 // The issuing warp stays converged and one elected lane issues: the operands
@@ -116,38 +126,154 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
       : "f"(a), "f"(b));
 }
 
+// ------------------------------------------------------------ order of the blocks
+// The row blocks of all requests with many rows, by the cached tokens that their last
+// row sees (128 a step, as positions at the cache's end give it), the longest first and
+// then in request order: CTAs start in this order, so the short blocks fill up what the
+// long ones leave.
+// Each CTA looks up the block of its rank by bisection over the number of steps; counts have a closed form in a request.
+// What is left for chunk_join_kernel: the place of a block's rows.
+struct Item {
+  int32_t t0, n_rows, row0, head, n_parts;
+};
+
+struct Order {
+  int sums[2][16];
+  int request, block;
+};
+
+__device__ __forceinline__ int blocks_of(const AttArgs& a, const Request& q) {
+  return q.n_rows > a.chunk_rows ? (q.n_rows + kBlockRows - 1) / kBlockRows : 0;
+}
+// Blocks of q whose last row sees at least min_tokens: all but the first ones.
+__device__ __forceinline__ int blocks_from(const AttArgs& a, const Request& q, int64_t min_tokens) {
+  const int blocks = blocks_of(a, q);
+  if (min_tokens <= 0) return blocks;
+  if (q.len < min_tokens) return 0;
+  const int64_t before = q.n_rows - (q.len - min_tokens + 1) * a.group;
+  return before <= 0 ? blocks : blocks - static_cast<int>(min(static_cast<int64_t>(blocks), before / kBlockRows));
+}
+// The sum of v over the CTA, in every thread; turn alternates between calls.
+__device__ __forceinline__ int cta_sum(Order& o, int turn, int v) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  if ((threadIdx.x & 31) == 0) o.sums[turn & 1][threadIdx.x >> 5] = v;
+  __syncthreads();
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; w += 4) {
+    const int4 x = *reinterpret_cast<const int4*>(&o.sums[turn & 1][w]);
+    all += x.x + x.y + x.z + x.w;
+  }
+  return all;
+}
+// Waves of parts: each takes a CTA's start, which is little beside 32 steps.
+__host__ __device__ inline int max_waves(int max_steps) {
+  return max_steps < 64 ? 1 : max_steps < 32 * kMaxWaves ? max_steps / 32 : kMaxWaves;
+}
+// What CTA x of chunk_kernel does.
+struct Work {
+  int request, row0, head, part, n_parts, slot;  // slot: among the blocks that are cut
+};
+// By the whole CTA: false when there is nothing left for it.
+__device__ __forceinline__ bool work_at(const AttArgs& a, int n_sms, int max_steps, Order& o, Item* items, Work& w) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.n_requests + kThreads - 1) / kThreads;
+  const int r0 = min(a.n_requests, tid * per), r1 = min(a.n_requests, r0 + per);
+  const Request first = r0 < r1 ? request(a, r0) : Request{0, 0, 0};
+  const auto count = [&](int steps) {
+    const int64_t least = static_cast<int64_t>(steps - 1) * kTokens + 1;  // tokens of that many steps
+    int c = r0 < r1 ? blocks_from(a, first, least) : 0;
+    for (int r = r0 + 1; r < r1; ++r) c += blocks_from(a, request(a, r), least);
+    return c;
+  };
+  int turn = 0;
+  const int items_in_all = cta_sum(o, turn++, count(0)) * a.heads;
+  // One item (block, head) for each SM in turn, whole; the rest, fewer than there are SMs, are cut into as
+  // many parts as fill the SMs once (or a few times, which pays for long caches), if
+  // that gains more than the join takes: about 8 steps, as 3 are what a CTA takes beside its steps.
+  const int whole = items_in_all / n_sms * n_sms, rest = items_in_all - whole;
+  int n_parts = 1, cost = max_steps + 3 - kJoinSteps;
+  for (int waves = 1; rest > 0 && waves <= max_waves(max_steps); ++waves) {
+    const int p = waves * n_sms / rest;
+    const int c = waves * ((max_steps + p - 1) / p + 3);
+    if (p > 1 && c < cost) n_parts = p, cost = c;
+  }
+  if (blockIdx.x == 0)  // what is not cut is not joined
+    for (int i = tid + (n_parts > 1 ? rest : 0); i < n_sms; i += kThreads) items[i] = {0, 0, 0, 0, 0};
+  const int x = blockIdx.x, y = x - whole;
+  if (y >= rest * n_parts) return false;
+  w.slot = y >= 0 ? y / n_parts : 0;
+  w.part = y >= 0 ? y % n_parts : 0;
+  w.n_parts = y >= 0 ? n_parts : 1;
+  const int item = y >= 0 ? whole + w.slot : x;
+  const int rank = item / a.heads;
+  w.head = item % a.heads;
+  // the most steps that more than rank blocks take: those with max_steps or more count as one
+  int lo = 0, hi = max_steps;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo + 1) / 2;
+    if (cta_sum(o, turn++, count(mid)) > rank) lo = mid;
+    else hi = mid - 1;
+  }
+  const bool open = lo == max_steps;  // no block is ranked by more steps
+  const int above = open ? 0 : count(lo + 1), mine = count(lo) - above;
+  int left = rank - cta_sum(o, turn++, above);  // among the blocks of lo steps
+  int inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += x;
+  }
+  if (lane == 31) o.sums[turn & 1][warp] = inc;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) left -= o.sums[turn & 1][w];
+  left -= inc - mine;
+  if (left >= 0 && left < mine) {
+    for (int r = r0; r < r1; ++r) {
+      const Request q = request(a, r);
+      const int out = open ? 0 : blocks_from(a, q, static_cast<int64_t>(lo) * kTokens + 1);
+      const int in = blocks_from(a, q, static_cast<int64_t>(lo - 1) * kTokens + 1) - out;
+      if (left < in) {
+        o.request = r;
+        o.block = blocks_of(a, q) - out - in + left;
+        break;
+      }
+      left -= in;
+    }
+  }
+  __syncthreads();
+  w.request = __shfl_sync(0xffffffffu, o.request, 0);
+  w.row0 = __shfl_sync(0xffffffffu, o.block, 0) * kBlockRows;
+  return true;
+}
+
 struct Barriers {
   uint64_t raw_full[2], raw_empty[2];  // keys' codes, values' codes
   uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], scale_full[4], s_full[2], p_full[2], o_done[2], drain;
   uint32_t tmem;
   int abort;
   int most;
+  alignas(16) Order order;
 };
-static_assert(sizeof(Barriers) <= 256, "barrier region");
+static_assert(sizeof(Barriers) <= 512, "barrier region");
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a, int n_sms, int max_steps, float* partial, Item* items) {
   using L = ChunkSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   grid_dependency_wait();
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, for the compiler too
-  const int head = blockIdx.y;
-  // row blocks: request r has room for floor(cu[r + 1] G / 256) - floor(cu[r] G / 256) + 1;
-  // the last ones, which see the most, come first
-  const int64_t x = gridDim.x - 1 - blockIdx.x;
-  const auto first_block = [&](int i) {
-    return static_cast<int64_t>(min(max(a.cu_q[i], 0), a.n_tokens)) * a.group / kBlockRows + i;
-  };
-  const int r = warp_upper(a.n_requests, x, first_block);
-  const Request q = request(a, r);
-  const int row0 = static_cast<int>(x - first_block(r)) * kBlockRows;
-  if (q.n_rows <= a.chunk_rows || row0 >= q.n_rows) return;
-
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* const scales = reinterpret_cast<float*>(smem + L::kScaleAt);  // [4][key, log2 value, 1 / value][8]
   Barriers& bar = *reinterpret_cast<Barriers*>(smem + L::kBarAt);
   volatile int* const abort = &bar.abort;
+  Work work;
+  if (!work_at(a, n_sms, max_steps, bar.order, items, work)) return;
+  const int r = work.request, row0 = work.row0, head = work.head;
+  const Request q = request(a, r);
+  if (work.n_parts > 1 && work.part == 0 && tid == 0)
+    items[work.slot] = {q.t0, q.n_rows, row0, head, work.n_parts};
   const int n_tiles = q.n_rows - row0 > kTileRows ? 2 : 1;
 
   if (tid == 0) {
@@ -187,7 +313,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const int most = bar.most, n_steps = (most + kTokens - 1) / kTokens;
+  const int all_steps = (bar.most + kTokens - 1) / kTokens;
+  const int first = static_cast<int>(static_cast<int64_t>(all_steps) * work.part / work.n_parts);
+  const int n_steps = static_cast<int>(static_cast<int64_t>(all_steps) * (work.part + 1) / work.n_parts) - first;
+  const int j0 = first * kTokens;  // the part's first token
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
   const uint64_t limit_ns = kWaitLimitNs;
   bool ok = true;
@@ -249,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
           *reinterpret_cast<float4*>(ivs + i) = *reinterpret_cast<const float4*>(sc + 2 * kGroups + i);
         }
         tmem_ld_wait();
-        const int left = limit - t * kTokens;  // tokens of the step that the row sees
-        if (left < kTokens) {
+        const int left = limit - j0 - t * kTokens;  // tokens of the step that the row sees
+        if (left < kTokens) {  // may be negative
 #pragma unroll
           for (int i = 0; i < kTokens; ++i)
             if (i >= left) v[i / 32][i % 32] = 0xFF800000u;
@@ -320,8 +449,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
         report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
       } else {
         tc_fence_after();
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const bool whole = work.n_parts == 1;
+        // a row that sees nothing divides by no sum: zeros
+        const float inv = sum == 0.0f ? 0.0f : whole ? 1.0f / sum : 1.0f;
         uint16_t* const dst = a.o + static_cast<int64_t>(q.t0 + token) * a.ldo + static_cast<int64_t>(h) * D;
+        float* const to = partial + (static_cast<int64_t>(work.slot * work.n_parts + work.part) * kBlockRows + tid) * kPartFloats<D>;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32] = {};
@@ -331,19 +463,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
           }
           if (row >= q.n_rows) continue;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+          for (int i = 0; i < 32; ++i) v[i] = sum != 0.0f ? __float_as_uint(__uint_as_float(v[i]) * inv) : 0u;
+          if (whole) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              // a row that sees nothing divides by no sum: zeros
-              const float lo = sum != 0.0f ? __uint_as_float(v[8 * i + 2 * j]) * inv : 0.0f;
-              const float hi = sum != 0.0f ? __uint_as_float(v[8 * i + 2 * j + 1]) * inv : 0.0f;
-              w[j] = static_cast<uint32_t>(float_to_bf16_bits(lo)) | (static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                w[j] = static_cast<uint32_t>(float_to_bf16_bits(__uint_as_float(v[8 * i + 2 * j]))) |
+                       (static_cast<uint32_t>(float_to_bf16_bits(__uint_as_float(v[8 * i + 2 * j + 1]))) << 16);
+              reinterpret_cast<uint4*>(dst + 32 * c)[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            reinterpret_cast<uint4*>(dst + 32 * c)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<uint4*>(to + 32 * c)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
-        if (a.lse && row < q.n_rows)
+        if (!whole && row < q.n_rows)
+          *reinterpret_cast<float4*>(to + D) = make_float4(sum != 0.0f ? n : -INFINITY, sum, 0.0f, 0.0f);
+        if (whole && a.lse && row < q.n_rows)
           a.lse[static_cast<int64_t>(q.t0 + token) * a.q_heads + h] =
               sum != 0.0f ? (n + log2f(sum)) * 0.69314718055994531f : -INFINITY;
       }
@@ -364,11 +503,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
       const uint8_t* const raw = smem + L::kRawAt + v * L::kRaw + blk * 64 + (lane & 3) * 16;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) w[i] = *reinterpret_cast<const uint4*>(raw + (i * kPass + tok) * D);
-      if ((t + 1) * kTokens > q.len) {
+      if (j0 + (t + 1) * kTokens > q.len) {
         // past the request's tokens a page may hold anything: zeros
 #pragma unroll
         for (int i = 0; i < kPasses; ++i)
-          if (t * kTokens + i * kPass + tok >= q.len) w[i] = make_uint4(0, 0, 0, 0);
+          if (j0 + t * kTokens + i * kPass + tok >= q.len) w[i] = make_uint4(0, 0, 0, 0);
       }
     };
     const auto store = [&](uint8_t* dst, uint32_t halves, const uint4 (&w)[kPasses]) {
@@ -477,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
       const int page_mask = (1 << a.page_shift) - 1;
       const int32_t* const table = a.block_table + static_cast<int64_t>(r) * a.max_blocks;
       const auto page_at = [&](int t) {
-        const int64_t j = static_cast<int64_t>(t) * kTokens + lane * 16;
+        const int64_t j = static_cast<int64_t>(first + t) * kTokens + lane * 16;
         int page = -1;
         if (j < q.len) {
           page = table[j >> a.page_shift];
@@ -538,21 +677,98 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a) {
   }
 }
 
+// Adds the parts of a block's rows, in order: D / 8 lanes a row.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const AttArgs a, const float* partial,
+                                                                  const Item* items) {
+  constexpr int kLanes = D / 8, kMost = 4;
+  grid_dependency_wait();
+  const Item p = items[blockIdx.x];
+  const int n_parts = p.n_parts;
+  const int in = blockIdx.y * (kJoinThreads / kLanes) + threadIdx.x / kLanes, d0 = threadIdx.x % kLanes * 8;
+  if (p.row0 + in >= p.n_rows) return;
+  const int64_t stride = static_cast<int64_t>(kBlockRows) * kPartFloats<D>;
+  const float* const from = partial + blockIdx.x * n_parts * stride + in * kPartFloats<D>;
+  float n = -INFINITY, sum = 0.0f, o[8] = {};
+  for (int c0 = 0; c0 < n_parts; c0 += kMost) {
+    float4 lo[kMost], hi[kMost];
+    float2 st[kMost];
+    float m = n;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      st[i] = make_float2(-INFINITY, 0.0f);
+      lo[i] = hi[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (c0 + i < n_parts) {
+        const float* const at = from + (c0 + i) * stride;
+        st[i] = *reinterpret_cast<const float2*>(at + D);
+        lo[i] = *reinterpret_cast<const float4*>(at + d0);
+        hi[i] = *reinterpret_cast<const float4*>(at + d0 + 4);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) m = fmaxf(m, st[i].x);
+    if (m == -INFINITY) continue;
+    const float f0 = exp2_fast(n - m);
+    n = m;
+    sum *= f0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= f0;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const float f = exp2_fast(st[i].x - m);
+      sum += st[i].y * f;
+      o[0] += lo[i].x * f, o[1] += lo[i].y * f, o[2] += lo[i].z * f, o[3] += lo[i].w * f;
+      o[4] += hi[i].x * f, o[5] += hi[i].y * f, o[6] += hi[i].z * f, o[7] += hi[i].w * f;
+    }
+  }
+  store_row<D>(a, p.t0, p.row0 + in, p.head, d0, n, sum, o);
+}
+
+// Row blocks that n_tokens tokens can come to.
+int64_t most_blocks(const AttArgs& a) {
+  const int64_t rows = static_cast<int64_t>(a.n_tokens) * a.group;
+  return rows / kBlockRows + std::min<int64_t>(a.n_requests, rows / (kChunkRows + 1));
+}
+
 template <int FMT, int D>
-int launch(const AttArgs& a, cudaStream_t s) {
+int launch(const AttArgs& a, int max_kv_len, void* workspace, cudaStream_t s) {
   constexpr size_t smem = ChunkSmem<D>::kBytes + 1024;
   KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(chunk_kernel<FMT, D>), static_cast<int>(smem)));
-  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.n_tokens) * a.group / kBlockRows + a.n_requests),
-                  static_cast<unsigned>(a.heads));
-  LaunchScope scope(TWELL_KERNEL_KV_ATTENTION, s);
-  return launch_pdl(chunk_kernel<FMT, D>, grid, dim3(kThreads), smem, s, a) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+  float* const partial = static_cast<float*>(workspace);
+  Item* const items = reinterpret_cast<Item*>(partial + static_cast<size_t>(kMaxParts) * kBlockRows * kPartFloats<D>);
+  const int64_t most = most_blocks(a) * a.heads, sms = std::min(sm_count(), kMaxParts / kMaxWaves);
+  if (most == 0) return TWELL_OK;  // no request can have that many rows
+  const int max_steps = static_cast<int>((static_cast<int64_t>(max_kv_len) + kTokens - 1) / kTokens);
+  // whole items and the parts of the rest, see work_at
+  const int64_t ctas = (most / sms + max_waves(max_steps)) * sms;
+  {
+    LaunchScope scope(TWELL_KERNEL_KV_ATTENTION, s);
+    if (launch_pdl(chunk_kernel<FMT, D>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), smem, s, a,
+                   static_cast<int>(sms), max_steps, partial, items) != cudaSuccess)
+      return TWELL_ERR_CUDA;
+  }
+  if (max_steps <= kJoinSteps + 1) return TWELL_OK;  // too short for any to be cut: a part's step and 3 are no gain
+  LaunchScope scope(TWELL_KERNEL_KV_JOIN, s);
+  return launch_pdl(chunk_join_kernel<D>, dim3(static_cast<unsigned>(sms), kBlockRows / (kJoinThreads / (D / 8))),
+                    dim3(kJoinThreads), 0, s, a, static_cast<const float*>(partial),
+                    static_cast<const Item*>(items)) == cudaSuccess
+             ? TWELL_OK
+             : TWELL_ERR_CUDA;
 }
 
 }  // namespace
 
-int launch_chunk_attention(const AttArgs& a, int format, int dim, cudaStream_t s) {
-  if (format == TWELL_KV_E4M3) return dim == 64 ? launch<TWELL_KV_E4M3, 64>(a, s) : launch<TWELL_KV_E4M3, 128>(a, s);
-  return dim == 64 ? launch<TWELL_KV_INT8, 64>(a, s) : launch<TWELL_KV_INT8, 128>(a, s);
+size_t chunk_workspace_bytes(int64_t rows, int dim) {
+  if (rows <= kChunkRows) return 0;
+  return static_cast<size_t>(kMaxParts) * (static_cast<size_t>(kBlockRows) * (dim + 4) * sizeof(float) + sizeof(Item));
+}
+
+int launch_chunk_attention(const AttArgs& a, int format, int dim, int max_kv_len, void* workspace, cudaStream_t s) {
+  const auto fn = format == TWELL_KV_E4M3 ? dim == 64 ? launch<TWELL_KV_E4M3, 64> : launch<TWELL_KV_E4M3, 128>
+                  : dim == 64             ? launch<TWELL_KV_INT8, 64>
+                                          : launch<TWELL_KV_INT8, 128>;
+  return fn(a, max_kv_len, workspace, s);
 }
 
 }  // namespace twell

@@ -338,6 +338,46 @@ def test_attention_rows_that_see_nothing_or_less(tw):
     assert (host(o)[4:8] == 0).all() and (host(lse)[4:8] == -np.inf).all()
 
 
+@pytest.mark.parametrize("fmt,dim", [("e4m3", 128), ("int8", 64)])
+def test_attention_chunks_over_cut_caches(tw, fmt, dim):
+    """Chunks whose caches are cut into parts: rows that see nothing, that see the
+    first part only, that end at parts' borders, and a cache that ends in a part's first page."""
+    import torch
+    r = np.random.RandomState(dim)
+    page, lens, new = 128, np.array([20000, 700, 8193, 129]), np.array([70, 40, 100, 33])
+    n_pages = int(sum(-(-lens // page)))
+    cache, kc, ks, vc, vs = make_cache(tw, fmt, n_pages, page, 2, dim, 8)
+    table = layout(r, lens, page, n_pages, int(max(-(-lens // page))))
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    positions = np.concatenate([np.arange(a - b, a) for a, b in zip(lens, new)]).astype(np.int32)
+    positions[:16] = [-1, 0, 1, 127, 128, 255, 511, 639, 640, 5000, 9999, 10000, 14999, 19998, 19999, 30000]
+    positions[cu[2]:cu[2] + 40] = -1    # most of a tile sees nothing
+    q = dev(r.randn(int(cu[-1]), 8, dim) * 1.3).to(torch.bfloat16)
+    o, lse = run_attention(tw, cache, q, table, cu, positions, lens, max_q=100)
+    assert tw.twell_kv_read_status(cache) == 0
+    check_attention(q, kc, ks, vc, vs, table, cu, positions, lens, 4, dim ** -0.5, o, lse)
+    o2, lse2 = run_attention(tw, cache, q, table, cu, positions, lens, max_q=100)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_attention_many_chunks_and_single_tokens(tw):
+    """1100 requests: chunks of every length among single tokens and idle requests, each in its place."""
+    import torch
+    r = np.random.RandomState(5)
+    page, n = 16, 1100
+    new = np.where(r.rand(n) < 0.3, r.randint(9, 80, n), r.randint(0, 2, n))
+    lens = np.where(new > 0, new + r.randint(0, 300, n), 0)
+    n_pages = int(sum(-(-lens // page)))
+    cache, kc, ks, vc, vs = make_cache(tw, "e4m3", n_pages, page, 1, 64, 6)
+    table = layout(r, lens, page, n_pages, int(max(-(-lens // page))))
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    positions = np.concatenate([np.arange(a - b, a) for a, b in zip(lens, new)]).astype(np.int32)
+    q = dev(r.randn(int(cu[-1]), 8, 64) * 1.3).to(torch.bfloat16)
+    o, lse = run_attention(tw, cache, q, table, cu, positions, lens, max_q=80)
+    assert tw.twell_kv_read_status(cache) == 0
+    check_attention(q, kc, ks, vc, vs, table, cu, positions, lens, 8, 0.125, o, lse)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 def test_attention_scales_far_apart(tw, fmt):
     """Value scales from 2^-60 to 2^40 and key scales that make some pages' logits
