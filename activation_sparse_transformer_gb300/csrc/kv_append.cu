@@ -57,6 +57,27 @@ __device__ __forceinline__ uint32_t encode2(float lo, float hi) {
   return __byte_perm(l, h, 0x7740) & 0xFFFFu;
 }
 
+// Four codes of two words of bf16 pairs times inv, a power of two: the products are
+// exact, so that the fused addition rounds to the integer as the separate one does.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(uint32_t w0, uint32_t w1, float inv) {
+  const auto fma2 = [](uint32_t w, float m, float c) {  // both halves of a word by one instruction
+    uint2 r;
+    asm("{\n\t.reg .b64 v, m, c;\n\tmov.b64 v, {%2, %3};\n\tmov.b64 m, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+        "fma.rn.f32x2 v, v, m, c;\n\tmov.b64 {%0, %1}, v;\n\t}"
+        : "=r"(r.x), "=r"(r.y)
+        : "r"(w << 16), "r"(w & 0xFFFF0000u), "f"(m), "f"(c));
+    return r;
+  };
+  if (FMT == TWELL_KV_E4M3) {
+    const uint2 a = fma2(w0, inv, -0.0f), b = fma2(w1, inv, -0.0f);
+    return encode2<FMT>(__uint_as_float(a.x), __uint_as_float(a.y)) |
+           (encode2<FMT>(__uint_as_float(b.x), __uint_as_float(b.y)) << 16);
+  }
+  const uint2 a = fma2(w0, inv, 12582912.0f), b = fma2(w1, inv, 12582912.0f);
+  return __byte_perm(__byte_perm(a.x, a.y, 0x0040), __byte_perm(b.x, b.y, 0x0040), 0x5410);
+}
+
 template <int FMT>
 __device__ __forceinline__ float2 decode2(uint32_t codes) {
   if (FMT == TWELL_KV_E4M3) {
@@ -90,7 +111,7 @@ __global__ void __launch_bounds__(append_threads(P, D)) append_kernel(const Appe
   constexpr int kLanes = D / 8;                       // lanes of one token, 8 values each
   constexpr int kRows = kThreads / kLanes;      // tokens of one pass
   constexpr int kPasses = (P + kRows - 1) / kRows;
-  __shared__ float warp_max[2][kThreads / 32];
+  __shared__ uint32_t warp_max[2][kThreads / 32];
   grid_dependency_wait();
   const int tid = threadIdx.x;
   // run x of the grid: request r has room for floor(cu[r + 1] / P) -
@@ -142,25 +163,35 @@ __global__ void __launch_bounds__(append_threads(P, D)) append_kernel(const Appe
       load(head + 1, next);
       if (first > 0) next_was = scales[head + 1];
     }
-    bool bad = false;
-    float amax = 0.0f;
+    // the largest magnitude by the bits, which order as the magnitudes do, two at a time
+    uint32_t both = 0;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      uint32_t* q = &w[i].x;
+      const uint32_t* q = &w[i].x;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        q[j] = finite2(q[j], &bad);
-        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(q[j])), fabsf(bf16_hi(q[j]))));
-      }
+      for (int j = 0; j < 4; ++j) both = __vmaxu2(both, q[j] & 0x7FFF7FFFu);
     }
+    if (max(both & 0xFFFFu, both >> 16) >= 0x7F80u) {  // an infinity or a NaN: rare
+      bool bad = false;
+      both = 0;
 #pragma unroll
-    for (int d = 16; d > 0; d /= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-    float* const maxima = warp_max[(head - head0) & 1];  // two, so that one barrier a head is enough
-    if ((tid & 31) == 0) maxima[tid / 32] = amax;
-    if (bad) report_error(a.status, TWELL_ERR_NOT_FINITE);
+      for (int i = 0; i < kPasses; ++i) {
+        uint32_t* q = &w[i].x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          q[j] = finite2(q[j], &bad);
+          both = __vmaxu2(both, q[j] & 0x7FFF7FFFu);
+        }
+      }
+      report_error(a.status, TWELL_ERR_NOT_FINITE);
+    }
+    uint32_t most = __reduce_max_sync(0xffffffffu, max(both & 0xFFFFu, both >> 16));
+    uint32_t* const maxima = warp_max[(head - head0) & 1];  // two, so that one barrier a head is enough
+    if ((tid & 31) == 0) maxima[tid / 32] = most;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) amax = fmaxf(amax, maxima[i]);
+    for (int i = 0; i < kThreads / 32; ++i) most = max(most, maxima[i]);
+    const float amax = __uint_as_float(most << 16);
     const float scale = fmaxf(two_to(scale_exponent<FMT>(amax)), was);
     uint8_t* const dst = codes + static_cast<int64_t>(head) * (P * D);
     // earlier tokens of the page move to the larger scale
@@ -187,16 +218,14 @@ __global__ void __launch_bounds__(append_threads(P, D)) append_kernel(const Appe
       const int t = row0 + i * kRows;
       if (t >= n) continue;
       const uint32_t* q = &w[i].x;
-      uint32_t c[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float lo = bf16_lo(q[j]), hi = bf16_hi(q[j]);
-        if (pow2) lo *= inv, hi *= inv;
-        else lo /= scale, hi /= scale;
-        c[j] = encode2<FMT>(lo, hi);
+      uint2 c;
+      if (pow2) {
+        c = make_uint2(encode4<FMT>(q[0], q[1], inv), encode4<FMT>(q[2], q[3], inv));
+      } else {
+        const auto divided = [&](uint32_t v) { return encode2<FMT>(bf16_lo(v) / scale, bf16_hi(v) / scale); };
+        c = make_uint2(divided(q[0]) | (divided(q[1]) << 16), divided(q[2]) | (divided(q[3]) << 16));
       }
-      *reinterpret_cast<uint2*>(dst + (first + t) * D + lane_col) =
-          make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+      *reinterpret_cast<uint2*>(dst + (first + t) * D + lane_col) = c;
     }
     if (tid == 0 && scale != was) scales[head] = scale;
   }

@@ -34,6 +34,7 @@ namespace {
 constexpr int kTileRows = 128;
 constexpr int kBlockRows = 2 * kTileRows;
 constexpr int kTokens = 128;   // cached tokens of a step
+constexpr int kRuns = 2;        // weights handed over in so many runs of tokens
 constexpr int kGroups = kTokens / 16;
 constexpr int kThreads = 16 * 32;
 // Registers a thread of each warpgroup (softmax 0, softmax 1, operands, mma's):
@@ -249,7 +250,7 @@ __device__ __forceinline__ bool work_at(const AttArgs& a, int n_sms, int max_ste
 
 struct Barriers {
   uint64_t raw_full[2], raw_empty[2];  // keys' codes, values' codes
-  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], scale_full[4], s_full[2], p_full[2], o_done[2], drain;
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], scale_full[4], s_full[2], p_full[2][kRuns], o_done[2], drain;
   uint32_t tmem;
   int abort;
   int most;
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a, int
       mbar_init(&bar.k_empty[i], 1);
       mbar_init(&bar.v_empty[i], 1);
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], kTileRows);
+      for (int j = 0; j < kRuns; ++j) mbar_init(&bar.p_full[i][j], kTileRows);
       mbar_init(&bar.o_done[i], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&bar.scale_full[i], kGroups);
@@ -437,10 +438,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a, int
             sum = fmaf(part[0] + part[1], ivs[g], sum);
           }
           tmem_st16(s_tm + 16 * c, p);
+          if ((c + 1) % (4 / kRuns) == 0) {
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&bar.p_full[t_id][c / (4 / kRuns)]);
+          }
         }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&bar.p_full[t_id]);
       }
       // the finished row
       if (ok && n_steps > 0) ok = mbar_wait(&bar.o_done[t_id], (n_steps - 1) & 1, limit_ns, abort);
@@ -569,13 +572,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a, int
         }
         commit(leader, &bar.s_full[x_id]);
       };
-      const auto values = [&](int t, int x_id) {
+      const auto values = [&](int t, int x_id, int run) {
         const uint64_t vd = smem_desc_sw128_nmajor(smem_u32(smem + L::kVAt + (t & 1) * L::kV), 8192);
 #pragma unroll
-        for (int k = 0; k < kTokens / 16; ++k)
+        for (int i = 0; i < kTokens / 16 / kRuns; ++i) {
+          const int k = run * (kTokens / 16 / kRuns) + i;
           mma_ts(leader, tmem + 256 + x_id * D, tmem + x_id * 128 + 8 * k,
                  vd + (k >> 2) * ((D / 64) * 8192 >> 4) + 128 * (k & 3), kIdescO, t > 0 || k > 0);
-        commit(leader, &bar.o_done[x_id]);
+        }
+        if (run == kRuns - 1) commit(leader, &bar.o_done[x_id]);
       };
       ok = mbar_wait(&bar.q_full, 0, limit_ns, abort);
       for (int t = 0; ok && t <= n_steps; ++t) {
@@ -583,12 +588,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a, int
         for (int x_id = 0; ok && x_id < n_tiles; ++x_id) {
           if (t > 0) {
             // O of the step before; its weights lie over S, so the next S waits for it
-            ok = (x_id > 0 || mbar_wait(&bar.v_full[(t - 1) & 1], ((t - 1) >> 1) & 1, limit_ns, abort)) &&
-                 mbar_wait(&bar.p_full[x_id], (t - 1) & 1, limit_ns, abort);
+            ok = x_id > 0 || mbar_wait(&bar.v_full[(t - 1) & 1], ((t - 1) >> 1) & 1, limit_ns, abort);
+#pragma unroll
+            for (int run = 0; run < kRuns; ++run) {
+              ok = ok && mbar_wait(&bar.p_full[x_id][run], (t - 1) & 1, limit_ns, abort);
+              if (!ok) break;
+              tc_fence_after();
+              values(t - 1, x_id, run);
+              issued = true;
+            }
             if (!ok) break;
-            tc_fence_after();
-            values(t - 1, x_id);
-            issued = true;
             if (x_id == n_tiles - 1) commit(leader, &bar.v_empty[(t - 1) & 1]);
             if (t < n_steps) ok = mbar_wait(&bar.o_done[x_id], (t - 1) & 1, limit_ns, abort);
             if (!ok) break;
