@@ -5,7 +5,8 @@
 // U = sum 2^(y - m) (y - m):
 //   lse = ln2 (m + log2 S),  logprob = ln2 ((y_t - m) - log2 S),
 //   entropy = ln2 (log2 S - U / S).
-// A row is read from memory once: a CTA (or a cluster of 2 to 8 for long rows
+// A row is read from memory once.  Many rows without alternatives are summed as they are read
+// (logprobs_rows_kernel).  Else a CTA (or a cluster of 2 to 8 for long rows
 // and few of them) copies its slice to shared memory with asynchronous 16-byte
 // copies, finds the maximum there and then sums with it, so no running maximum has
 // to be corrected; slices are joined through distributed shared memory.  HBM
@@ -20,6 +21,7 @@
 
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 #include "kv_internal.h"
 
@@ -118,8 +120,9 @@ struct Stat {
 // Stats relative to a common maximum; an empty part has s = u = 0.
 __device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
   const float m = fmaxf(a.m, b.m);
-  const float ea = ex2(a.m - m), eb = ex2(b.m - m);
-  return {m, a.s * ea + b.s * eb, ea * (a.u + a.s * (a.m - m)) + eb * (b.u + b.s * (b.m - m))};
+  const float da = fmaxf(a.m - m, -2000.0f), db = fmaxf(b.m - m, -2000.0f);  // finite: 0 * da is 0
+  const float ea = ex2(da), eb = ex2(db);
+  return {m, a.s * ea + b.s * eb, ea * (a.u + a.s * da) + eb * (b.u + b.s * db)};
 }
 
 // (value, index) as one word, larger = better: higher value, then lower index.
@@ -258,6 +261,13 @@ __device__ void slice_top(LpShared<NT>& sh, const Slice<T>& sl, float inv_t, int
   __syncthreads();
 }
 
+// May a row whose smallest logit is lo and whose maximum is m be summed two elements at a
+// time?  Masked tokens (2^-inf * -inf is no number, be they -inf or so low that the product is) and logits
+// so large that the rounding of m counts are summed one by one, with products rounded as m's was.
+__device__ __forceinline__ bool short_sums(float lo, float m, float c) {
+  return __fmul_rn(lo, c) > -FLT_MAX && fabsf(m) < 1.0e6f && c < 1.0e6f;
+}
+
 // (a, b) += ... of two elements in one instruction each.
 __device__ __forceinline__ void sum2(float2& s, float2& u, float x0, float x1, float c, float m, float& e0, float& e1) {
   float d0, d1;
@@ -272,6 +282,20 @@ __device__ __forceinline__ void sum2(float2& s, float2& u, float x0, float x1, f
       "mov.b64 {%0, %1}, s;\n\tmov.b64 {%2, %3}, u;\n\t}"
       : "+f"(s.x), "+f"(s.y), "+f"(u.x), "+f"(u.y)
       : "f"(e0), "f"(e1), "f"(d0), "f"(d1));
+}
+
+// A row's results from its statistics; a NaN or +inf among the logits makes all of them NaN.
+__device__ __forceinline__ float logprob_of(const LogprobsArgs& a, const Stat& st, float x) {
+  const float c = a.inv_temperature * kLog2e;
+  const float d = fabsf(st.m) < 1.0e6f ? fmaf(x, c, -st.m) : __fmul_rn(x, c) - st.m;
+  return isnan(st.s) ? __int_as_float(0x7FC00000) : st.s == 0.0f ? -INFINITY : (d - log2f(st.s)) * kLn2;
+}
+__device__ __forceinline__ void store_row(const LogprobsArgs& a, int64_t row, const Stat& st, int target, float x) {
+  const float nan = __int_as_float(0x7FC00000), log_s = log2f(st.s);
+  const bool broken = isnan(st.s), empty = !broken && st.s == 0.0f;
+  if (a.lse) a.lse[row] = broken ? nan : empty ? -INFINITY : (st.m + log_s) * kLn2;
+  if (a.entropy) a.entropy[row] = broken ? nan : empty ? 0.0f : (log_s - st.u / st.s) * kLn2;
+  if (a.targets) a.logprob[row] = target >= 0 && target < a.vocab ? logprob_of(a, st, x) : 0.0f;
 }
 
 template <typename T, int NT>
@@ -344,9 +368,7 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a) {
   m = fmaxf(__fmul_rn(m, c), -FLT_MAX);
 
   float2 s = {0.0f, 0.0f}, u = {0.0f, 0.0f};
-  // masked tokens (2^-inf * -inf is no number) and logits so large that the
-  // rounding of m counts are summed one by one, with products rounded as m's was
-  const bool plain = lo > -INFINITY && fabsf(m) < 1.0e6f && c < 1.0e6f;
+  const bool plain = short_sums(lo, m, c);
   const auto add = [&](float x) {
     const float d = plain ? fmaf(x, c, -m) : __fmul_rn(x, c) - m, e = ex2(d);
     s.x += e;
@@ -413,49 +435,136 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a) {
   if (rank != 0) return;
   __syncthreads();
   const Stat st = sh.stat;
-  const bool broken = isnan(st.s), empty = !broken && st.s == 0.0f;
-  const float log_s = log2f(st.s);
-  const float nan = __int_as_float(0x7FC00000);
-  const auto logprob_of = [&](int i) {
-    const float x = E::load(src + i), d = fabsf(st.m) < 1.0e6f ? fmaf(x, c, -st.m) : __fmul_rn(x, c) - st.m;
-    return broken ? nan : empty ? -INFINITY : (d - log_s) * kLn2;
-  };
   if (tid == 0) {
-    if (a.lse) a.lse[row] = broken ? nan : empty ? -INFINITY : (st.m + log_s) * kLn2;
-    if (a.entropy) a.entropy[row] = broken ? nan : empty ? 0.0f : (log_s - st.u / st.s) * kLn2;
-    if (a.targets) {
-      const int t = a.targets[row];
-      a.logprob[row] = t >= 0 && t < a.vocab ? logprob_of(t) : 0.0f;
-    }
+    const int t = a.targets ? a.targets[row] : -1;
+    store_row(a, row, st, t, t >= 0 && t < a.vocab ? E::load(src + t) : 0.0f);
   }
   if (tid < a.top_k) {
     const int i = key_index(sh.best[tid]);
-    a.top_logprob[row * a.top_k + tid] = logprob_of(broken ? 0 : i);
+    const bool broken = isnan(st.s);
+    a.top_logprob[row * a.top_k + tid] = logprob_of(a, st, E::load(src + (broken ? 0 : i)));
     a.top_index[row * a.top_k + tid] = broken ? -1 : i;
   }
+}
+
+// The same without alternatives, for many rows: nothing is read twice, so nothing needs
+// to be kept.  NT threads take a row, each with a maximum of its own that follows what it
+// reads, kBatch 16-byte loads at a time; their sums are brought to the row's maximum at the end.
+// The next rows' loads run under a row's sums, where a staged row's CTA waits for all of its
+// copies first: 8192 x 32768 bf16 81.8 us (6.6 TB/s), staged 101; fp32 147 (7.3 TB/s), staged 212.
+constexpr int kRowsThreads = 256, kBatch = 4;
+// From 2 rows an SM on (320 x 131072 fp32: 34 us, staged in clusters 40).
+constexpr int kManyRows = 2;
+template <typename T, int NT>
+__global__ void __launch_bounds__(kRowsThreads) logprobs_rows_kernel(const LogprobsArgs a, int n_rows) {
+  using E = Elem<T>;
+  __shared__ Stat sh[kRowsThreads / 32];
+  grid_dependency_wait();
+  const int t = threadIdx.x % NT;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRowsThreads / NT) + threadIdx.x / NT;
+  if (row >= n_rows) return;  // whole warps, and whole CTAs where a row has several
+  const T* const src = static_cast<const T*>(a.logits) + row * a.ld;
+  int target = -1;
+  float x_target = 0.0f;
+  if (t == 0 && a.targets) {
+    target = a.targets[row];
+    if (target >= 0 && target < a.vocab) x_target = E::load(src + target);
+  }
+  const float c = a.inv_temperature * kLog2e;
+  float m = -FLT_MAX;
+  float2 s = {0.0f, 0.0f}, u = {0.0f, 0.0f};
+  // moves the reference up to y, and tells if what goes with it may be summed the short way
+  const auto meet = [&](float hi, float lo) {
+    const float y = __fmul_rn(hi, c);
+    if (y > m) {
+      const float d = fmaxf(m - y, -2000.0f), f = ex2(d);
+      u.x = f * fmaf(s.x, d, u.x), u.y = f * fmaf(s.y, d, u.y);
+      s.x *= f, s.y *= f;
+      m = y;
+    }
+    return short_sums(lo, m, c);
+  };
+  const auto add = [&](float x) {  // with the product rounded as m's was, and for masked tokens
+    const float d = __fmul_rn(x, c) - m, e = ex2(d);
+    s.x += e;
+    u.x = fmaf(e, fmaxf(d, -2000.0f), u.x);
+  };
+  const auto batch = [&](const uint4* w, auto n) {
+    typename E::Range r;
+#pragma unroll
+    for (int i = 0; i < n.value; ++i) r.add(w[i]);
+    const bool plain = meet(r.high(), r.low());
+#pragma unroll
+    for (int i = 0; i < n.value; ++i) {
+      float x[E::kVec], e0, e1;
+      E::unpack(w[i], x);
+      if (plain) {
+#pragma unroll
+        for (int k = 0; k < E::kVec; k += 2) sum2(s, u, x[k], x[k + 1], c, m, e0, e1);
+      } else {
+#pragma unroll
+        for (int k = 0; k < E::kVec; ++k) add(x[k]);
+      }
+    }
+  };
+  // elements up to a 16-byte boundary, whole pieces, the elements behind them
+  const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
+  const int head = min(a.vocab, (16 - off) % 16 / static_cast<int>(sizeof(T)));
+  const int n_vec = (a.vocab - head) / E::kVec, behind = head + n_vec * E::kVec;
+  const uint4* const v = reinterpret_cast<const uint4*>(src + head);
+  int j = t;
+  const auto batches = [&](auto n) {
+    for (; j + (n.value - 1) * NT < n_vec; j += n.value * NT) {
+      uint4 w[n.value];
+#pragma unroll
+      for (int i = 0; i < n.value; ++i) w[i] = __ldg(v + j + i * NT);
+      batch(w, n);
+    }
+  };
+  batches(std::integral_constant<int, kBatch>{});
+  batches(std::integral_constant<int, kBatch / 2>{});
+  batches(std::integral_constant<int, 1>{});
+  if (t < head + a.vocab - behind) {
+    const float x = E::load(src + (t < head ? t : behind + t - head));
+    meet(x, x);
+    add(x);
+  }
+  Stat st = {m, s.x + s.y, u.x + u.y};
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2)
+    st = join(st, {__shfl_xor_sync(0xffffffffu, st.m, d), __shfl_xor_sync(0xffffffffu, st.s, d),
+                   __shfl_xor_sync(0xffffffffu, st.u, d)});
+  if (NT > 32) {
+    if (t % 32 == 0) sh[t / 32] = st;
+    __syncthreads();
+    if (t == 0)
+      for (int w = 1; w < NT / 32; ++w) st = join(st, sh[w]);
+  }
+  if (t == 0) store_row(a, row, st, target, x_target);
 }
 
 struct BwdArgs {
   const void* logits;
   void* d_logits;
   int64_t ld, ldd;
-  int vocab, slice, slices;
+  int vocab, slice;
   const int32_t* targets;
   float inv_temperature;
   const float *lse, *entropy, *d_logprob, *d_entropy;
 };
 
-// One CTA writes one slice of a row.  Reads and writes every element once:
-// HBM bounds it.  The row's four numbers are loaded once per CTA.
-template <typename T>
-__global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const BwdArgs a) {
+// NT threads, a CTA or a warp of it, write one slice of a row.  Reads and writes every
+// element once: HBM bounds it.  The row's four numbers are loaded once by each thread.
+template <typename T, int NT>
+__global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const BwdArgs a, int n_rows) {
   using E = Elem<T>;
   grid_dependency_wait();
-  const int64_t row = blockIdx.x / a.slices;
-  const int tid = threadIdx.x;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kBwdThreads / NT) + threadIdx.x / NT;
+  if (row >= n_rows) return;
+  const int tid = threadIdx.x % NT;
   const T* const src = static_cast<const T*>(a.logits) + row * a.ld;
   T* const dst = static_cast<T*>(a.d_logits) + row * a.ldd;
-  const int beg = (blockIdx.x % a.slices) * a.slice, n = min(a.slice, a.vocab - beg);
+  const int beg = blockIdx.y * a.slice, n = min(a.slice, a.vocab - beg);
   const float lse = a.lse[row], inv_t = a.inv_temperature;
   int target = a.targets ? a.targets[row] : -1;
   if (target < 0 || target >= a.vocab) target = -1;
@@ -479,19 +588,19 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const BwdArgs
   const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(from) & 15);
   const bool together = off == (reinterpret_cast<uintptr_t>(to) & 15);
   const int head = together ? min(n, static_cast<int>((16 - off) % 16 / sizeof(T))) : n;
-  for (int i = tid; i < head; i += kBwdThreads) to[i] = E::store(grad(E::load(from + i), i));
+  for (int i = tid; i < head; i += NT) to[i] = E::store(grad(E::load(from + i), i));
   const int n_vec = (n - head) / E::kVec;
   const uint4* const v = reinterpret_cast<const uint4*>(from + head);
   uint4* const w = reinterpret_cast<uint4*>(to + head);
 #pragma unroll 4
-  for (int j = tid; j < n_vec; j += kBwdThreads) {
+  for (int j = tid; j < n_vec; j += NT) {
     float x[E::kVec];
     E::unpack(v[j], x);
 #pragma unroll
     for (int i = 0; i < E::kVec; ++i) x[i] = grad(x[i], head + j * E::kVec + i);
     w[j] = E::pack(x);
   }
-  for (int i = head + n_vec * E::kVec + tid; i < n; i += kBwdThreads) to[i] = E::store(grad(E::load(from + i), i));
+  for (int i = head + n_vec * E::kVec + tid; i < n; i += NT) to[i] = E::store(grad(E::load(from + i), i));
 }
 
 // Cluster width and slice of the forward pass.  A slice above 72 KB would leave
@@ -504,6 +613,13 @@ int choose_cluster(int n_rows, int64_t row_bytes) {
                              (static_cast<int64_t>(n_rows) * c < 2 * sm_count() && row_bytes / c > 16 * 1024)))
     c *= 2;
   return c;
+}
+
+// A warp a row for short rows, if every SM gets 8 of them (bf16, 8192 rows of 1000: 7.4 us, with a
+// CTA a row 16.6; of 8000: 29.4 and 36.4; 1400 of 8000: 8.1 and 7.1; 700 of 3000: 4.2 and 3.3).
+template <typename T>
+bool warp_rows(int n_rows, int vocab) {
+  return vocab * sizeof(T) <= 16384 && n_rows >= 8 * sm_count();
 }
 
 template <typename T, int NT>
@@ -531,6 +647,15 @@ int launch_rows(const LogprobsArgs& a, int n_rows, int cluster, cudaStream_t s) 
 
 template <typename T>
 int launch_logprobs(LogprobsArgs a, int n_rows, cudaStream_t s) {
+  const bool warps = warp_rows<T>(n_rows, a.vocab);
+  if (a.top_k == 0 && (warps || n_rows >= kManyRows * sm_count())) {
+    LaunchScope scope(TWELL_KERNEL_LOGPROBS, s);
+    const int grid = warps ? (n_rows + kRowsThreads / 32 - 1) / (kRowsThreads / 32) : n_rows;
+    return launch_pdl(warps ? logprobs_rows_kernel<T, 32> : logprobs_rows_kernel<T, kRowsThreads>, dim3(grid),
+                      dim3(kRowsThreads), 0, s, a, n_rows) == cudaSuccess
+               ? TWELL_OK
+               : TWELL_ERR_CUDA;
+  }
   const int c = choose_cluster(n_rows, static_cast<int64_t>(a.vocab) * sizeof(T));
   a.slice = ((a.vocab + c - 1) / c + 7) / 8 * 8;
   // one CTA or less an SM: its threads are all there are to hide the latencies
@@ -546,12 +671,17 @@ int launch_logprobs_bwd(BwdArgs a, int n_rows, cudaStream_t s) {
   const int64_t share = static_cast<int64_t>(n_rows) * a.vocab / (8 * sm_count());
   a.slice = static_cast<int>(share > 32768 ? 32768 : share < 2048 ? 2048 : share) / 8 * 8;
   if (a.slice > a.vocab) a.slice = (a.vocab + 7) / 8 * 8;
-  a.slices = (a.vocab + a.slice - 1) / a.slice;
-  if (static_cast<int64_t>(n_rows) * a.slices > INT_MAX) return TWELL_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(n_rows) * a.slices);
+  // a warp a row where that is 4 KB or less and every SM gets 16 (bf16, 8192 rows of 1000: 12.5 us,
+  // with a CTA a row 14.9; 100000 of 100: 41 and 140)
+  const bool warps = a.vocab * sizeof(T) <= 4096 && n_rows >= 16 * sm_count();
+  if (warps) a.slice = a.vocab;
+  const dim3 grid(warps ? (n_rows + kBwdThreads / 32 - 1) / (kBwdThreads / 32) : n_rows,
+                  (a.vocab + a.slice - 1) / a.slice);
   LaunchScope scope(TWELL_KERNEL_LOGPROBS_BWD, s);
-  return launch_pdl(logprobs_bwd_kernel<T>, grid, dim3(kBwdThreads), 0, s, a) == cudaSuccess ? TWELL_OK
-                                                                                            : TWELL_ERR_CUDA;
+  return launch_pdl(warps ? logprobs_bwd_kernel<T, 32> : logprobs_bwd_kernel<T, kBwdThreads>, grid,
+                    dim3(kBwdThreads), 0, s, a, n_rows) == cudaSuccess
+             ? TWELL_OK
+             : TWELL_ERR_CUDA;
 }
 
 int check_logits(const void* logits, int dtype, int64_t ld, int n_rows, int vocab, float inv_temperature) {
@@ -610,7 +740,7 @@ extern "C" TWELL_API int twell_logprobs_bwd(const void* logits, int32_t dtype, i
   }
   if (!device_is_sm103()) return TWELL_ERR_NO_DEVICE;
   if (n_rows == 0) return TWELL_OK;
-  const BwdArgs a{logits, d_logits, ld, ldd, vocab, 0, 0, targets, inv_temperature, lse, entropy, d_logprob, d_entropy};
+  const BwdArgs a{logits, d_logits, ld, ldd, vocab, 0, targets, inv_temperature, lse, entropy, d_logprob, d_entropy};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return dtype == TWELL_BF16 ? launch_logprobs_bwd<uint16_t>(a, n_rows, s) : launch_logprobs_bwd<float>(a, n_rows, s);
 }

@@ -554,6 +554,47 @@ def test_logprobs_match_definition(tw, n, vocab, dtype, ld, k, inv_t):
                 near(got[3][i][j], top[j], tol + 2 * U32 * (abs(top[j]) if np.isfinite(top[j]) else 0), "top")
 
 
+@pytest.mark.parametrize("n,vocab,dtype,ld,inv_t", [
+    (2000, 333, "bfloat16", 335, 0.9), (1300, 4096, "float32", 4099, 1.0), (1217, 8192, "bfloat16", 8192, 1.0),
+    (1300, 7, "float32", 7, 1.1), (400, 30011, "bfloat16", 30013, 1.3), (310, 33000, "float32", 33001, 1.0)])
+def test_logprobs_of_many_rows_match_definition(tw, n, vocab, dtype, ld, inv_t):
+    """Rows that are summed as they are read, by a warp or by a CTA."""
+    test_logprobs_match_definition(tw, n, vocab, dtype, ld, 0, inv_t)
+
+
+@pytest.mark.parametrize("n,vocab", [(3, 5000), (3, 100001), (400, 20000), (1300, 500)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("inv_t", [1.0, 3.0])
+def test_logprobs_masked_by_the_lowest_value(tw, n, vocab, dtype, inv_t):
+    """Tokens masked by their type's lowest value weigh nothing in sums and gradient, though their
+    product with the inverse temperature may be no number's; rows that are all so masked are uniform."""
+    import torch
+    r = np.random.RandomState(vocab)
+    t = getattr(torch, dtype)
+    x = dev(r.randn(n, vocab) * 2).to(t)
+    masked = dev(r.rand(n, vocab)) < 0.3
+    masked[1] = True
+    masked[1, 3] = masked[0, 0] = False
+    x[masked] = torch.finfo(t).min
+    targets = np.full(n, 3, np.int32)
+    targets[0] = 0
+    lp, en, lse, *_ = [None if v is None else host(v) for v in run_logprobs(tw, x, dev(targets), inv_t, 0)]
+    live = x.masked_fill(masked, float("-inf"))
+    xs = host(live.float() * torch.tensor(inv_t, dtype=torch.float32, device="cuda"))
+    d = torch.empty_like(x)
+    ones = torch.ones(n, device="cuda")
+    tw.twell_logprobs_bwd(x, dev(targets), inv_t, dev(lse.astype(np.float32)), dev(en.astype(np.float32)), ones, ones, d)
+    assert (d[masked & (torch.arange(vocab, device="cuda") != dev(targets)[:, None])] == 0).all()
+    assert torch.isfinite(d).all()
+    tol = 2.0 ** -21 + 2 * (vocab / 256 + 40) * U32 + 4 * U32 * 90 + 6 * U32 * 10 * inv_t
+    for i in list(range(3)) + list(range(3, n, 97)):
+        want_lp, want_en, want_lse, *_ = ref.logprobs(xs[i], int(targets[i]), 0)
+        assert abs(lse[i] - want_lse) <= tol + 2 * U32 * abs(want_lse), i
+        assert abs(en[i] - want_en) <= (tol + 2 * U32) * (want_en + 2) * 2, i
+        if np.isfinite(want_lp):
+            assert abs(lp[i] - want_lp) <= tol + 2 * U32 * abs(want_lp), i
+
+
 def test_logprobs_best_values_crowded_in_one_place(tw):
     """The largest values all in the columns of one thread, rising and falling
     rows: more candidates than the quick selection holds."""
@@ -624,6 +665,12 @@ def test_logprobs_gradient_matches_formula(tw, n, vocab, dtype, ld, inv_t, both)
     assert torch.equal(view.nan_to_num(5.0), out.nan_to_num(5.0))
     if ld > vocab:
         assert (x[:, vocab:] == 3.0).all()
+
+
+@pytest.mark.parametrize("n,vocab,dtype,ld,inv_t", [
+    (2500, 333, "bfloat16", 335, 0.9), (2432, 1024, "float32", 1025, 1.0), (3000, 7, "float32", 7, 1.1)])
+def test_logprobs_gradient_of_many_short_rows(tw, n, vocab, dtype, ld, inv_t):
+    test_logprobs_gradient_matches_formula(tw, n, vocab, dtype, ld, inv_t, True)
 
 
 def test_logprobs_gradient_matches_differences(tw):
