@@ -22,6 +22,7 @@
 #include <cfloat>
 #include <climits>
 #include <type_traits>
+#include <utility>
 
 #include "kv_internal.h"
 
@@ -35,6 +36,7 @@ constexpr int kGroups = 64;    // of the k largest's bound: with k = 20 about 24
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
 constexpr int kCandidates = 1024;
+constexpr int kRankLanes = 8;  // threads that rank a key together
 constexpr int kMaxVocab = 400000;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
@@ -145,7 +147,7 @@ struct LpShared {
   uint64_t candidates[kCandidates];
   uint64_t best[kMaxTop];
   uint64_t bound;
-  Stat stat;
+  Stat stat, whole;  // of the slice, of the row
   float warp_hi[NT / 32], warp_lo[NT / 32];
   float2 warp_sum[NT / 32];
   uint64_t warp_key[NT / 32];
@@ -230,11 +232,11 @@ __device__ void slice_top(LpShared<NT>& sh, const Slice<T>& sl, float inv_t, int
   __syncthreads();
   if (sh.count <= kCandidates) {
     const int n = sh.count;
-    for (int c = tid; c < n; c += NT) {
-      const uint64_t key = sh.candidates[c];
-      int rank = 0;
-      for (int i = 0; i < n; ++i) rank += sh.candidates[i] > key;
-      if (rank < k) sh.best[rank] = key;
+    for (int c0 = 0; c0 < n; c0 += NT / kRankLanes) {
+      const int c = c0 + tid / kRankLanes;
+      const uint64_t key = c < n ? sh.candidates[c] : 0;
+      const int rank = rank_in<kRankLanes>(sh.candidates, n, key);
+      if (c < n && rank < k) sh.best[rank] = key;
     }
   } else {
     // rare: a few groups own most of the largest values; take them one by one
@@ -298,10 +300,25 @@ __device__ __forceinline__ void store_row(const LogprobsArgs& a, int64_t row, co
   if (a.targets) a.logprob[row] = target >= 0 && target < a.vocab ? logprob_of(a, st, x) : 0.0f;
 }
 
+template <typename T>
+__device__ __forceinline__ void store_target(const LogprobsArgs& a, int64_t row, const Stat& st, const T* src) {
+  const int t = a.targets ? a.targets[row] : -1;
+  store_row(a, row, st, t, t >= 0 && t < a.vocab ? Elem<T>::load(src + t) : 0.0f);
+}
+// The i-th best of a row.
+template <typename T>
+__device__ __forceinline__ void store_top(const LogprobsArgs& a, int64_t row, int i, const Stat& st, uint64_t key,
+                                          const T* src) {
+  const bool broken = isnan(st.s);
+  a.top_logprob[row * a.top_k + i] = logprob_of(a, st, Elem<T>::load(src + (broken ? 0 : key_index(key))));
+  a.top_index[row * a.top_k + i] = broken ? -1 : key_index(key);
+}
+
 template <typename T, int NT>
 __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a) {
   using E = Elem<T>;
-  extern __shared__ uint4 chunks[];
+  // copies to another place within 128 bytes cost up to a sixth (8192 x 32768 with 5 alternatives 172 us, so 153)
+  extern __shared__ __align__(128) uint4 chunks[];
   __shared__ LpShared<NT> sh;
   grid_dependency_wait();
   cg::cluster_group cluster = cg::this_cluster();
@@ -406,45 +423,43 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a) {
     sh.stat = all;
   }
   if (a.top_k > 0) slice_top<T, NT>(sh, sl, a.inv_temperature, a.top_k, hi, at);
-  if (ranks > 1) {
-    cluster.sync();
-    if (rank == 0) {
-      if (tid == 0) {
-        Stat all = sh.stat;
-        for (int i = 1; i < ranks; ++i) all = join(all, *cluster.map_shared_rank(&sh.stat, i));
-        sh.stat = all;
-      }
-      if (a.top_k > 0) {
-        // the ranks' lists, indexes made those of the row, ranked together
-        constexpr int kShare = NT / (kMaxCluster * kMaxTop);
-        const int entry = tid / kShare, of = entry / a.top_k, i = entry % a.top_k, n_keys = ranks * a.top_k;
-        uint64_t key = 0;
-        if (entry < n_keys) {
-          key = cluster.map_shared_rank(&sh, of)->best[i];
-          if (key) key -= static_cast<uint64_t>(of) * a.slice;
-          if (tid % kShare == 0) sh.key[entry] = key;
-        }
-        __syncthreads();
-        const int better = rank_in<kShare>(sh.key, n_keys, key);
-        __syncthreads();
-        if (key && better < a.top_k) sh.best[better] = key;
-      }
-    }
-    cluster.sync();  // the other ranks' shared memory is read above
+  if (ranks == 1) {
+    __syncthreads();
+    const Stat st = sh.stat;
+    if (tid == 0) store_target(a, row, st, src);
+    if (tid < a.top_k) store_top(a, row, tid, st, sh.best[tid], src);
+    return;
   }
-  if (rank != 0) return;
+  cluster.sync();
+  // every rank takes all statistics and lists, and places the keys of its own list
+  const int n_keys = ranks * a.top_k;
+  if (tid < 32 && (rank == 0 || n_keys > 0)) {
+    Stat st = {-FLT_MAX, 0.0f, 0.0f};
+    if (tid < ranks) st = *cluster.map_shared_rank(&sh.stat, tid);
+#pragma unroll
+    for (int d = 1; d < kMaxCluster; d *= 2)
+      st = join(st, {__shfl_xor_sync(0xffffffffu, st.m, d), __shfl_xor_sync(0xffffffffu, st.s, d),
+                     __shfl_xor_sync(0xffffffffu, st.u, d)});
+    if (tid == 0) sh.whole = st;
+  }
+  for (int e = tid - 32; e < n_keys; e += NT - 32) {
+    if (e < 0) break;  // the first warp is at the statistics
+    const int of = e / a.top_k;
+    const uint64_t key = cluster.map_shared_rank(&sh, of)->best[e % a.top_k];
+    sh.key[e] = key ? key - static_cast<uint64_t>(of) * a.slice : 0;  // indexes of the row
+  }
+  auto last = cluster.barrier_arrive();  // no rank leaves before the others have read its shared memory
   __syncthreads();
-  const Stat st = sh.stat;
-  if (tid == 0) {
-    const int t = a.targets ? a.targets[row] : -1;
-    store_row(a, row, st, t, t >= 0 && t < a.vocab ? E::load(src + t) : 0.0f);
+  if (rank == 0 && tid == 0) store_target(a, row, sh.whole, src);
+  for (int i0 = 0; i0 < a.top_k; i0 += NT / kRankLanes) {
+    const int i = i0 + tid / kRankLanes;
+    const uint64_t key = i < a.top_k ? sh.key[rank * a.top_k + i] : 0;
+    const int better = rank_in<kRankLanes>(sh.key, n_keys, key);
+    if (tid % kRankLanes != 0 || i >= a.top_k) continue;
+    const Stat st = sh.whole;
+    if (isnan(st.s) ? rank == 0 : key && better < a.top_k) store_top(a, row, isnan(st.s) ? i : better, st, key, src);
   }
-  if (tid < a.top_k) {
-    const int i = key_index(sh.best[tid]);
-    const bool broken = isnan(st.s);
-    a.top_logprob[row * a.top_k + tid] = logprob_of(a, st, E::load(src + (broken ? 0 : i)));
-    a.top_index[row * a.top_k + tid] = broken ? -1 : i;
-  }
+  cluster.barrier_wait(std::move(last));
 }
 
 // The same without alternatives, for many rows: nothing is read twice, so nothing needs
@@ -658,9 +673,11 @@ int launch_logprobs(LogprobsArgs a, int n_rows, cudaStream_t s) {
   }
   const int c = choose_cluster(n_rows, static_cast<int64_t>(a.vocab) * sizeof(T));
   a.slice = ((a.vocab + c - 1) / c + 7) / 8 * 8;
-  // one CTA or less an SM: its threads are all there are to hide the latencies
+  // One CTA or less an SM: its threads are all there are to hide the latencies, but two must fit, as the
+  // SMs of a GPC need not be a multiple of a cluster (16 x 131072 fp32 with 20 alternatives: 9.0 us;
+  // with 1024 threads, one of 16 clusters late, 15.6; with 256 9.1.  1 row: 7.3, 8.3 and 7.9).
   if (static_cast<int64_t>(n_rows) * c <= sm_count() && static_cast<int64_t>(a.slice) * sizeof(T) > 16 * 1024)
-    return launch_rows<T, 1024>(a, n_rows, c, s);
+    return launch_rows<T, 512>(a, n_rows, c, s);
   return launch_rows<T, 256>(a, n_rows, c, s);
 }
 
