@@ -33,7 +33,7 @@ namespace twell {
 namespace {
 
 constexpr int kAttWarps = 4;
-constexpr int kAttThreads = 32 * kAttWarps;
+constexpr int kWideWarps = 8;  // of a CTA that has an SM to itself
 constexpr int kMaxTiles = 2;    // a row block is 1 or 2 tiles of 8 rows
 constexpr int kMaxRows = 8 * kMaxTiles;
 constexpr int kAttGroup = 16;   // cached tokens of one mma, all of one page
@@ -275,7 +275,6 @@ constexpr int kMaxSmem = 224 * 1024;  // dynamic, of a CTA
 // Segments of up to this many units are never cut: their join would cost more
 // than the imbalance of leaving them whole.
 constexpr int kWholeUnits = 2;
-constexpr int kNoJoinUnits = 8;  // see launch_attention
 // Whole segments of up to this many units (512 tokens) go to single warps.
 constexpr int kWarpUnits = 4;
 
@@ -286,7 +285,8 @@ struct Piece {   // of a segment that goes on in the next CTA, for join_kernel
 template <int D>
 constexpr size_t partial_floats() { return static_cast<size_t>(kMaxRows) * (D + 4); }
 
-__device__ __forceinline__ int units_of(const Request& q) { return (q.len + kUnit - 1) / kUnit; }
+template <int W>
+__device__ __forceinline__ int units_of(const Request& q) { return (q.len + (kAttStep * W) - 1) / (kAttStep * W); }
 template <int NT>
 __device__ __forceinline__ int row_blocks_of(const Request& q) {
   return (q.n_rows + 8 * NT - 1) / (8 * NT);
@@ -300,22 +300,23 @@ enum Split {
 };
 
 // What a segment counts for in the split.
+template <int W>
 __device__ __forceinline__ int span_of(const Request& q, int split) {
-  const int units = units_of(q);
+  const int units = units_of<W>(q);
   return split == kEach ? min(units, 1) : units;
 }
 
 // start[r] = units of the requests before r, start[n_requests] = all; by the whole CTA.
-template <int NT>
+template <int NT, int W>
 __device__ __forceinline__ void scan_requests(const AttArgs& a, int64_t* start, int64_t* warp_sum, int split) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.n_requests + kAttThreads - 1) / kAttThreads;
+  const int per = (a.n_requests + (32 * W) - 1) / (32 * W);
   const int r0 = min(a.n_requests, tid * per), r1 = min(a.n_requests, r0 + per);
   int64_t mine = 0;
   for (int r = r0; r < r1; ++r) {
     const Request q = request(a, r);
     const int64_t w =
-        q.n_rows > a.chunk_rows ? 0 : static_cast<int64_t>(span_of(q, split)) * row_blocks_of<NT>(q) * a.heads;
+        q.n_rows > a.chunk_rows ? 0 : static_cast<int64_t>(span_of<W>(q, split)) * row_blocks_of<NT>(q) * a.heads;
     start[r] = w;
     mine += w;
   }
@@ -329,7 +330,7 @@ __device__ __forceinline__ void scan_requests(const AttArgs& a, int64_t* start, 
   __syncthreads();
   int64_t run = inc - mine, all = 0;
 #pragma unroll
-  for (int w = 0; w < kAttWarps; ++w) {
+  for (int w = 0; w < W; ++w) {
     if (w < warp) run += warp_sum[w];
     all += warp_sum[w];
   }
@@ -354,6 +355,7 @@ __device__ __forceinline__ int request_at(const int64_t* start, int n, int64_t u
 }
 
 // Cut b of n_cuts over all units: moved to its segment's start where the segment stays whole.
+template <int W>
 __device__ __forceinline__ int64_t cut_at(const AttArgs& a, const int64_t* start, int64_t b, int64_t n_cuts,
                                           int split) {
   const int64_t all = start[a.n_requests];
@@ -361,7 +363,7 @@ __device__ __forceinline__ int64_t cut_at(const AttArgs& a, const int64_t* start
   if (b == 0 || u >= all) return b == 0 ? 0 : all;
   const int r = request_at(start, a.n_requests, u);
   if (split == kEach) return u;
-  const int units = units_of(request(a, r));
+  const int units = units_of<W>(request(a, r));
   return split == kWhole || units <= kWholeUnits ? u - (u - start[r]) % units : u;
 }
 
@@ -393,7 +395,7 @@ struct Stream {
 // a ring less one step ahead of the arithmetic, over the ends of segments too.  Lane l
 // looks after the groups l, l + 32, ... of a segment: it holds the page's
 // place and scales and issues the copies.  Several segments need at most 32 groups.
-template <int FMT, int D, int NT, typename Emit>
+template <int FMT, int D, int NT, int W, typename Emit>
 __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, const Request& q, Ring<D>& ring,
                                            Emit emit) {
   using R = Ring<D>;
@@ -455,7 +457,7 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
     f_slot = f_slot + 1 == ring.stages ? 0 : f_slot + 1;
     if (++f_step == st.n_steps) {
       f_step = 0;
-      f_seg += kAttWarps;
+      f_seg += W;
       f_head = f_seg / st.blocks;
     }
   };
@@ -464,9 +466,9 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
   RawQ<D, NT> raw;
   load_q<D, NT>(a, q.t0, q.n_rows, st.seg % st.blocks * (8 * NT), head, raw);
   int limit[NT][2], least = st.len;
-  for (int seg = st.seg; seg < st.seg_end; seg += kAttWarps) {
+  for (int seg = st.seg; seg < st.seg_end; seg += W) {
     const int row0 = (seg - head * st.blocks) * (8 * NT);
-    const int next_head = (seg + kAttWarps) / st.blocks;
+    const int next_head = (seg + W) / st.blocks;
     // what each row sees; rows past the last see everything and are not stored.
     // The same in every head, so only several row blocks need it again.
     if (seg == st.seg || st.blocks > 1) {
@@ -490,9 +492,9 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
     float factor[NT][2];
     convert_q<D, NT>(a, raw, qb, factor);
     if (seg != st.seg) now = ahead;
-    if (seg + kAttWarps < st.seg_end) {
+    if (seg + W < st.seg_end) {
       // the next segment's rows and scales, a segment ahead
-      load_q<D, NT>(a, q.t0, q.n_rows, (seg + kAttWarps - next_head * st.blocks) * (8 * NT), next_head, raw);
+      load_q<D, NT>(a, q.t0, q.n_rows, (seg + W - next_head * st.blocks) * (8 * NT), next_head, raw);
       scales_of(ahead, next_head);
     }
     TileState<D, NT> s;
@@ -529,15 +531,16 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
   }
 }
 
-template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D == 64 ? 3 : 2)
-    attention_kernel(const AttArgs a, float* partial, Piece* pieces, int split, int stages) {
+template <int FMT, int D, int NT, int W>
+__global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT == 1 ? (D == 64 ? 4 : 3) : D == 64 ? 3 : 2)
+    attention_kernel(const AttArgs a, float* partial, Piece* pieces, int given_split, int stages) {
+  const int split = W > kAttWarps ? kEach : given_split;
   using R = Ring<D>;
   extern __shared__ __align__(16) uint8_t ring_all[];
   const int ring_bytes = stages * R::kStage;  // of a warp
-  int64_t* const start = reinterpret_cast<int64_t*>(ring_all + kAttWarps * ring_bytes);
-  __shared__ int64_t warp_sum[kAttWarps];
-  __shared__ uint64_t full[kAttWarps][R::kMost];
+  int64_t* const start = reinterpret_cast<int64_t*>(ring_all + W * ring_bytes);
+  __shared__ int64_t warp_sum[W];
+  __shared__ uint64_t full[W][R::kMost];
   __shared__ int abort_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, quad = lane & 3;
   Ring<D> ring = {stages, ring_all + warp * ring_bytes, full[warp], &abort_flag, 0, 0};
@@ -545,28 +548,28 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D =
   if (lane < stages) mbar_init(full[warp] + lane, 2);
   mbar_fence_init();
   grid_dependency_wait();
-  scan_requests<NT>(a, start, warp_sum, split);
+  scan_requests<NT, W>(a, start, warp_sum, split);
   const int64_t all = start[a.n_requests];
   // at least a unit for each CTA that works, so that every CTA between a cut
   // segment's first and last has a part of it
   const int64_t cta = blockIdx.x, n_ctas = min(static_cast<int64_t>(gridDim.x), all);
-  const int64_t end = cta < n_ctas ? cut_at(a, start, cta + 1, n_ctas, split) : 0;
-  int64_t pos = cta < n_ctas ? cut_at(a, start, cta, n_ctas, split) : 0;
+  const int64_t end = cta < n_ctas ? cut_at<W>(a, start, cta + 1, n_ctas, split) : 0;
+  int64_t pos = cta < n_ctas ? cut_at<W>(a, start, cta, n_ctas, split) : 0;
   if (tid == 0) pieces[cta].last_cta = -1;
   // requests without cached tokens, and tokens of no request
   for (int r = blockIdx.x; r < a.n_requests; r += gridDim.x) {
     const Request q = request(a, r);
     if (q.len == 0 && q.n_rows <= a.chunk_rows)
-      for (int t = 0; t < q.n_rows / a.group; ++t) zero_row<D>(a, q.t0 + t, tid, kAttThreads);
+      for (int t = 0; t < q.n_rows / a.group; ++t) zero_row<D>(a, q.t0 + t, tid, (32 * W));
   }
   for (int t = min(max(a.cu_q[a.n_requests], 0), a.n_tokens) + blockIdx.x; t < a.n_tokens; t += gridDim.x)
-    zero_row<D>(a, t, tid, kAttThreads);
+    zero_row<D>(a, t, tid, (32 * W));
 
   int turn = 0;  // of the warps at whole segments
   while (pos < end) {
     const int r = request_at(start, a.n_requests, pos);
     const Request q = request(a, r);
-    const int units = units_of(q), blocks = row_blocks_of<NT>(q);
+    const int units = units_of<W>(q), blocks = row_blocks_of<NT>(q);
     const int span = split == kEach ? 1 : units;
     const int64_t seg0 = (pos - start[r]) / span;
     const int unit0 = static_cast<int>((pos - start[r]) % span);
@@ -575,17 +578,17 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D =
     st.len = q.len;
     const int64_t left = static_cast<int64_t>(blocks) * a.heads - seg0;
     const int count = static_cast<int>(min(left, (end - pos) / span));
-    if (unit0 == 0 && units <= kWarpUnits && count >= kAttWarps) {
+    if (unit0 == 0 && units <= kWarpUnits && count >= W) {
       // short segments that lie whole in this piece: each warp takes every fourth
       st.j_first = 0;
       st.j_stride = kAttStep;
       st.n_steps = (q.len + kAttStep - 1) / kAttStep;
-      st.seg = static_cast<int>(seg0) + ((warp - turn) & (kAttWarps - 1));
+      st.seg = static_cast<int>(seg0) + ((warp - turn) & (W - 1));
       st.seg_end = static_cast<int>(seg0) + count;
       st.blocks = blocks;
       turn += count;
       pos += static_cast<int64_t>(count) * span;
-      run_stream<FMT, D, NT>(a, st, q, ring, [&](TileState<D, NT>& s, int head, int row0) {
+      run_stream<FMT, D, NT, W>(a, st, q, ring, [&](TileState<D, NT>& s, int head, int row0) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -606,15 +609,15 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D =
     const int n_units =
         split == kEach ? units : static_cast<int>(min(static_cast<int64_t>(units - unit0), end - pos));
     pos += split == kEach ? 1 : n_units;
-    st.j_first = unit0 * kUnit + warp * kAttStep;
-    st.j_stride = kUnit;
-    const int seen = min(n_units * kUnit, q.len - unit0 * kUnit) - warp * kAttStep;
-    st.n_steps = seen > 0 ? (seen + kUnit - 1) / kUnit : 0;
+    st.j_first = unit0 * (kAttStep * W) + warp * kAttStep;
+    st.j_stride = (kAttStep * W);
+    const int seen = min(n_units * (kAttStep * W), q.len - unit0 * (kAttStep * W)) - warp * kAttStep;
+    st.n_steps = seen > 0 ? (seen + (kAttStep * W) - 1) / (kAttStep * W) : 0;
     st.seg = static_cast<int>(seg0);
     st.seg_end = st.seg + 1;
     st.blocks = blocks;
     // the four warps' results of the tile, joined in warp order; they take the ring's place
-    run_stream<FMT, D, NT>(a, st, q, ring, [&](TileState<D, NT>& s, int, int row0) {
+    run_stream<FMT, D, NT, W>(a, st, q, ring, [&](TileState<D, NT>& s, int, int row0) {
       float* const mine = reinterpret_cast<float*>(ring.data);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -640,15 +643,15 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? (D == 64 ? 4 : 3) : D =
       const int64_t seg_end = pos + (units - n_units);
       pieces[cta] = {q.t0, q.n_rows, row0, head, static_cast<int32_t>((seg_end * n_ctas - 1) / all), {0, 0, 0}};
     }
-    for (int row = tid / kLanes; row < min(8 * NT, q.n_rows - row0); row += kAttThreads / kLanes) {
+    for (int row = tid / kLanes; row < min(8 * NT, q.n_rows - row0); row += 32 * W / kLanes) {
       const int d0 = (tid % kLanes) * 8;
       float n = -INFINITY, sum = 0.0f, o[8] = {};
 #pragma unroll
-      for (int w = 0; w < kAttWarps; ++w)
+      for (int w = 0; w < W; ++w)
         n = fmaxf(n, reinterpret_cast<const float*>(ring_all + w * ring_bytes)[row * (D + 4) + D]);
       if (n > -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < kAttWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
           const float* at = reinterpret_cast<const float*>(ring_all + w * ring_bytes) + row * (D + 4);
           const float f = exp2_fast(at[D] - n);
           sum += at[D + 1] * f;
@@ -744,33 +747,39 @@ template <int FMT, int D, int NT>
 int launch_attention(const AttArgs& a, int max_kv_len, int max_q_len, void* workspace, cudaStream_t s) {
   float* const partial = static_cast<float*>(workspace);
   Piece* const pieces = reinterpret_cast<Piece*>(partial + 2 * kMaxCtas * partial_floats<D>());
-  constexpr size_t kStageBytes = kAttWarps * Ring<D>::kStage;
   const size_t sums = sizeof(int64_t) * (static_cast<size_t>(a.n_requests) + 1);
-  const void* fn = reinterpret_cast<const void*>(attention_kernel<FMT, D, NT>);
-  KV_TRY(set_max_dynamic_smem(fn, kMaxSmem));
-  const int resident = resident_ctas_per_sm(fn, kAttThreads, Ring<D>::kLeast * kStageBytes + sums);
-  if (resident < 1) return TWELL_ERR_CUDA;
   // no more CTAs than the units that the caller's bounds allow
   const int64_t blocks = (static_cast<int64_t>(max_q_len) * a.group + 8 * NT - 1) / (8 * NT);
   const int64_t units = (static_cast<int64_t>(max_kv_len) + kUnit - 1) / kUnit;
-  // Cutting saves what a segment is longer than the even share, at 0.5 us a
-  // unit; the join costs 4 to 5 us.  So short caches are not cut at all; and
-  // where their segments are no more than the SMs, each has one to itself, with
-  // all its shared memory for copies ahead (16 requests of up to 1000 tokens, 8 key heads: cut
-  // 19.7 us, moved cuts 18.7, each its own 14.0; 256 requests: 90, 80, 89).
+  // Cutting evens out the CTAs' loads and costs the join and the search for the cuts.  A
+  // segment with an SM to itself takes 5.7 us and 0.57 more a unit (8 warps share its steps), cut segments
+  // 8 to 18 us and, by how many there are, 0.07 to 0.44 a unit: about even at units = segments / 2
+  // (heads of 128, 128 segments of up to 1000 tokens: 10.8 us, cut 20; of 4000 26.1 and 32.2, of 9000
+  // 49 and 50; 32 segments of 1500: 12.8 and 13.1, of 4000 24.1 and 18.1; 8 of 4000: 23.8 and 10.6).
+  // More segments than SMs: whole ones are better up to 16 units (256 segments of 1500 tokens 26.0, cut 30.1;
+  // of 2500 38.3 and 36.7), and up to 32 where there are so many that they even out
+  // (8000 of up to 4001 143 and 146); beyond, one long segment among short ones would be all a CTA's work.
   const int64_t segments = a.n_requests * a.heads * std::max<int64_t>(1, blocks);
-  const int split = units > kNoJoinUnits ? kCut : segments <= sm_count() ? kEach : kWhole;
+  const int64_t sms = sm_count();
+  const int split = segments <= sms ? 2 * units <= std::max<int64_t>(8, segments) ? kEach : kCut
+                    : units <= (segments >= 8 * sms ? 32 : 16) ? kWhole : kCut;
+  const int warps = split == kEach ? kWideWarps : kAttWarps;
+  const auto kernel = split == kEach ? attention_kernel<FMT, D, NT, kWideWarps> : attention_kernel<FMT, D, NT, kAttWarps>;
+  const void* fn = reinterpret_cast<const void*>(kernel);
+  KV_TRY(set_max_dynamic_smem(fn, kMaxSmem));
+  const int stage_bytes = warps * Ring<D>::kStage;
+  const int resident = resident_ctas_per_sm(fn, 32 * warps, Ring<D>::kLeast * stage_bytes + sums);
+  if (resident < 1) return TWELL_ERR_CUDA;
   const int64_t most = std::max<int64_t>(1, split == kEach ? segments : segments * std::max<int64_t>(1, units));
   const int ctas = static_cast<int>(std::min<int64_t>(most, std::min(kMaxCtas, sm_count() * resident)));
   // where fewer CTAs share an SM each has more of its shared memory: more copies ahead
   const int share = (ctas + sm_count() - 1) / sm_count();
   const int stages = std::min<int>(Ring<D>::kMost, std::max<int>(Ring<D>::kLeast, static_cast<int>(
-      (kMaxSmem / share - static_cast<int>(sums) - 2048) / static_cast<int>(kStageBytes))));
-  const size_t smem = stages * kStageBytes + sums;
+      (kMaxSmem / share - static_cast<int>(sums) - 2048) / stage_bytes)));
+  const size_t smem = static_cast<size_t>(stages) * stage_bytes + sums;
   {
     LaunchScope scope(TWELL_KERNEL_KV_ATTENTION, s);
-    if (launch_pdl(attention_kernel<FMT, D, NT>, dim3(ctas), dim3(kAttThreads), smem, s, a, partial, pieces,
-                   split, stages) != cudaSuccess)
+    if (launch_pdl(kernel, dim3(ctas), dim3(32 * warps), smem, s, a, partial, pieces, split, stages) != cudaSuccess)
       return TWELL_ERR_CUDA;
   }
   if (split != kCut || ctas == 1) return TWELL_OK;
