@@ -6,7 +6,7 @@
 // encoded), takes their largest magnitude, sets the scale 2^e from its bits and
 // writes the codes.  Reads 2 bytes and writes 1 byte per value, so HBM bounds
 // long runs; the launch and three dependent latencies (request, slot, values)
-// bound single tokens, which get a CTA for each head.  The tokens of a run lie ld
+// bound single tokens (16 of them 2.8 us), which get a CTA for each head.  The tokens of a run lie ld
 // apart, each with 2 D bytes in one piece: 16-byte loads, D / 8 lanes a token.
 #include <cuda_bf16.h>
 
@@ -16,7 +16,7 @@ namespace twell {
 namespace {
 
 // Threads for a full page's run: four 16-byte loads each, which leaves the registers for
-// several CTAs on an SM (with 128 threads whatever the page, pages of 128 tokens took 198 us instead of 78).
+// several CTAs on an SM (pages of 128 tokens: 55.3 us; with 128 threads, eight loads each, 57.5).
 constexpr int append_threads(int page, int dim) { return page * dim / 32 < 128 ? 128 : page * dim / 32; }
 constexpr int kMinExponent = -100;
 
@@ -233,9 +233,9 @@ __global__ void __launch_bounds__(append_threads(P, D)) append_kernel(const Appe
 
 template <int FMT, int D>
 int launch_append(AppendArgs a, int page, cudaStream_t s) {
-  // heads one after the other once every SM has CTAs enough: 24 prompts of up to
-  // 4000 tokens, 8 heads of 128, int8: 87 us with a CTA for each head, 78.7 so
-  // (4.3 TB/s; 84 with four times as many CTAs)
+  // heads one after the other, a head's loads under the encoding of the one before, once every SM has CTAs enough:
+  // 24 prompts of up to 4000 tokens, 8 heads of 128, int8: 55.4 us (6.1 TB/s); with a
+  // CTA for each head 70, with twice as many CTAs 55.7 (pages of 64: 56.7 and 59.6)
   const int64_t runs = a.n_tokens / page + 2 * static_cast<int64_t>(a.n_requests);
   while (a.heads_per_cta < a.heads && runs * 2 * (a.heads / (2 * a.heads_per_cta)) >= 6 * sm_count())
     a.heads_per_cta *= 2;

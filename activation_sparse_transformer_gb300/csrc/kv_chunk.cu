@@ -19,10 +19,10 @@
 // 4 D flops for each (row, token): tensor cores bound it, then the exponentials
 // and the shared memory that feeds both operands of S.
 //
-// 4 chunks of 556 to 966 tokens at the end of 5668 to 8192, 32 / 8 heads of 128, e4m3: 357 us,
-// 925 TFLOP/s (a step 2.4 us, its mma's alone 1.1).  Taking the blocks as they come,
+// 4 chunks of 556 to 966 tokens at the end of 5668 to 8192, 32 / 8 heads of 128, e4m3: 355 us,
+// 930 TFLOP/s (a step 2.4 us, its mma's alone 1.1).  Taking the blocks as they come,
 // uncut, 380; longest first, uncut, 381 (376 blocks are 2.5 waves); longest first with the last wave
-// cut 357.  One chunk of 541 tokens at the end of 32768: 534 -> 462 us with up to 4 waves of parts.
+// cut 355.  One chunk of 541 tokens at the end of 32768: 534 -> 462 us with up to 4 waves of parts.
 #include <algorithm>
 #include <cfloat>
 
@@ -34,7 +34,7 @@ namespace {
 constexpr int kTileRows = 128;
 constexpr int kBlockRows = 2 * kTileRows;
 constexpr int kTokens = 128;   // cached tokens of a step
-constexpr int kRuns = 2;        // weights handed over in so many runs of tokens
+constexpr int kRuns = 2;       // a step's weights are handed over in so many runs (heads of 64: 277 us; in one 285, in four 292)
 constexpr int kGroups = kTokens / 16;
 constexpr int kThreads = 16 * 32;
 // Registers a thread of each warpgroup (softmax 0, softmax 1, operands, mma's):

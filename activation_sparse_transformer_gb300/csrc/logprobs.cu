@@ -12,6 +12,7 @@
 // to be corrected; slices are joined through distributed shared memory.  HBM
 // bounds many rows, with the instructions of an element next (5 of them, two
 // elements an instruction where there is one); few rows are bound by the latency of one slice.
+// 8192 x 32768 bf16: 82 us, its gradient 164 (6.6 TB/s both); with 5 alternatives 153; 16 x 131072 fp32 with 20: 9 us.
 //
 // The k largest: the k-th largest of 64 groups' own maxima is a lower bound of
 // the k-th largest value, and hardly more than k values reach it.  Those are
