@@ -679,6 +679,11 @@ int launch_logprobs(LogprobsArgs a, int n_rows, cudaStream_t s) {
   // with 1024 threads, one of 16 clusters late, 15.6; with 256 9.1.  1 row: 7.3, 8.3 and 7.9).
   if (static_cast<int64_t>(n_rows) * c <= sm_count() && static_cast<int64_t>(a.slice) * sizeof(T) > 16 * 1024)
     return launch_rows<T, 512>(a, n_rows, c, s);
+  // A slice's 16-byte pieces go to the threads in turn, and a group's maximum needs a piece: with
+  // few pieces a group has to be one thread for enough groups to have one (6614 rows of 500 bf16 with 20 alternatives:
+  // 33 us, with 256 threads and no bound 382).  Fewer pieces than alternatives give no bound either way.
+  const int chunks = a.slice / Elem<T>::kVec;
+  if (chunks >= a.top_k && chunks < 6 * a.top_k) return launch_rows<T, 64>(a, n_rows, c, s);
   return launch_rows<T, 256>(a, n_rows, c, s);
 }
 

@@ -562,6 +562,14 @@ def test_logprobs_of_many_rows_match_definition(tw, n, vocab, dtype, ld, inv_t):
     test_logprobs_match_definition(tw, n, vocab, dtype, ld, 0, inv_t)
 
 
+@pytest.mark.parametrize("n,vocab,dtype,ld,k", [
+    (60, 500, "bfloat16", 503, 20), (60, 170, "bfloat16", 170, 20), (60, 140, "bfloat16", 141, 20),
+    (60, 300, "float32", 301, 32), (60, 957, "bfloat16", 957, 20), (60, 40, "float32", 40, 32)])
+def test_logprobs_alternatives_of_small_vocabularies(tw, n, vocab, dtype, ld, k):
+    """About as many 16-byte pieces as alternatives: with and without a bound of the k largest."""
+    test_logprobs_match_definition(tw, n, vocab, dtype, ld, k, 1.0)
+
+
 @pytest.mark.parametrize("n,vocab", [(3, 5000), (3, 100001), (400, 20000), (1300, 500)])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("inv_t", [1.0, 3.0])
