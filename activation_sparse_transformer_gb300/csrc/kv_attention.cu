@@ -410,7 +410,7 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
   const int64_t head_bytes = static_cast<int64_t>(D) << a.page_shift;
   struct Batch {
     int64_t cell;   // of head 0
-    int offset;     // bytes inside a page's head
+    int64_t at;     // its place in head 0, in bytes
     bool on;        // there is such a group
     float ks, lvs, ivs;  // key scale, log2 and inverse of the value scale
   };
@@ -433,7 +433,7 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
         page = 0;
       }
       b.cell = static_cast<int64_t>(page) * a.heads;
-      b.offset = (j & page_mask) * D;
+      b.at = b.cell * head_bytes + (j & page_mask) * D;
       b.on = true;
     }
     scales_of(b, head);
@@ -443,7 +443,8 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
   Batch now = batch_from(0, head), ahead = now;  // of the arithmetic's steps and the next ones
   if (st.n_steps > 16) ahead = batch_from(16, head);
   Batch copies = now;
-  int f_seg = st.seg, f_head = head, f_step = 0, f_slot = ring.slot;
+  int f_seg = st.seg, f_step = 0, f_slot = ring.slot;
+  int64_t f_base = head * head_bytes;  // of the head that is being fetched
   const auto fetch = [&]() {
     if (f_seg >= st.seg_end || st.n_steps == 0) return;
     if (f_step > 0 && (f_step & 15) == 0) copies = ahead;
@@ -451,7 +452,7 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
       uint64_t* const bar = ring.full + f_slot;
       if (copies.on) {
         uint8_t* const stage = ring.data + f_slot * R::kStage + (lane & 1) * R::kGroup;
-        const int64_t at = (copies.cell + f_head) * head_bytes + copies.offset;
+        const int64_t at = copies.at + f_base;
         mbar_arrive_expect_tx(bar, 2 * R::kGroup);
         bulk_load(stage, a.k + at, R::kGroup, bar);
         bulk_load(stage + 2 * R::kGroup, a.v + at, R::kGroup, bar);
@@ -463,7 +464,7 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
     if (++f_step == st.n_steps) {
       f_step = 0;
       f_seg += W;
-      f_head = f_seg / st.blocks;
+      f_base = f_seg / st.blocks * head_bytes;
     }
   };
 #pragma unroll 1
