@@ -54,20 +54,30 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// One row block's running state in a warp: rows 8 t + 2 quad and + 1 of its
+// A row block: NT = 1 or 2 tiles of 8 rows, or (0) 4 rows in every other column of a tile.
+template <int NT>
+constexpr int kTiles = NT == 0 ? 1 : NT;
+template <int NT>
+constexpr int kCols = NT == 0 ? 1 : 2;  // of a tile, in a lane
+template <int NT>
+constexpr int kRows = NT == 0 ? 4 : 8 * NT;
+template <int NT>
+__device__ __forceinline__ int row_in(int t, int quad, int c) { return NT == 0 ? quad : 8 * t + 2 * quad + c; }
+
+// One row block's running state in a warp: rows row_in(t, quad, c) of its
 // tiles t, whose statistics the 8 lanes of a quad column share.
 template <int D, int NT>
 struct TileState {
-  float acc[NT][D / 16][4];   // i: dims (D / 8) g + 2 i (both rows), then + 1 (both rows)
-  float n[NT][2];     // the reference (0 before the first step)
-  float pass[NT][2];  // what an exponent must pass to move it
-  float sum[NT][2];   // sum of 2^(l - n)
+  float acc[kTiles<NT>][D / 16][4];   // i: dims (D / 8) g + 2 i (both rows), then + 1 (both rows)
+  float n[kTiles<NT>][2];     // the reference (0 before the first step)
+  float pass[kTiles<NT>][2];  // what an exponent must pass to move it
+  float sum[kTiles<NT>][2];   // sum of 2^(l - n)
 };
 
 template <int D, int NT>
 __device__ __forceinline__ void reset(TileState<D, NT>& s) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
+  for (int t = 0; t < kTiles<NT>; ++t) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -86,7 +96,7 @@ __device__ __forceinline__ void reset(TileState<D, NT>& s) {
 // returns c log2(e) 2^k of rows 2 quad and 2 quad + 1.
 template <int D, int NT>
 struct RawQ {
-  uint4 w[NT][D / 32];
+  uint4 w[kTiles<NT>][D / 32];
 };
 
 template <int D, int NT>
@@ -94,24 +104,25 @@ __device__ __forceinline__ void load_q(const AttArgs& a, int64_t t0, int n_rows,
                                        RawQ<D, NT>& raw) {
   const int lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int row = row0 + 8 * t + g, token = row / a.group;
+  for (int t = 0; t < kTiles<NT>; ++t) {
+    const int row = NT == 0 ? row0 + g / 2 : row0 + 8 * t + g, token = row / a.group;
+    const bool on = row < n_rows && (NT > 0 || g % 2 == 0);
     const uint16_t* src = a.q + (t0 + token) * a.ldq + (static_cast<int64_t>(head) * a.group + row % a.group) * D;
 #pragma unroll
     for (int i = 0; i < D / 64; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        raw.w[t][2 * i + j] = row < n_rows ? __ldg(reinterpret_cast<const uint4*>(src + 64 * i + 16 * quad + 8 * j))
+        raw.w[t][2 * i + j] = on ? __ldg(reinterpret_cast<const uint4*>(src + 64 * i + 16 * quad + 8 * j))
                                            : make_uint4(0, 0, 0, 0);
   }
 }
 
 template <int D, int NT>
-__device__ __forceinline__ void convert_q(const AttArgs& a, const RawQ<D, NT>& raw, uint32_t (&qb)[NT][D / 16][2],
-                                          float (&factor)[NT][2]) {
+__device__ __forceinline__ void convert_q(const AttArgs& a, const RawQ<D, NT>& raw, uint32_t (&qb)[kTiles<NT>][D / 16][2],
+                                          float (&factor)[kTiles<NT>][2]) {
   const int quad = threadIdx.x & 3;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
+  for (int t = 0; t < kTiles<NT>; ++t) {
     const uint32_t* u = &raw.w[t][0].x;
     float amax = 0.0f;
 #pragma unroll
@@ -122,7 +133,7 @@ __device__ __forceinline__ void convert_q(const AttArgs& a, const RawQ<D, NT>& r
     const float inv = __int_as_float((127 - k) << 23);
     const float f = a.scale_log2 * __int_as_float((127 + k) << 23);
     factor[t][0] = __shfl_sync(0xffffffffu, f, 8 * quad);
-    factor[t][1] = __shfl_sync(0xffffffffu, f, 8 * quad + 4);
+    if (NT > 0) factor[t][1] = __shfl_sync(0xffffffffu, f, 8 * quad + 4);
     // word j of a lane's code vectors holds dims 4 j .. 4 j + 3 = u[2 j], u[2 j + 1]
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
@@ -141,11 +152,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // lie in two pages, from a stage of the ring: keys of both groups, then values.
 // limit: tokens each row sees; least: the smallest of them; len: the request's tokens.
 template <int FMT, int D, int NT>
-__device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)[NT][D / 16][2],
-                                       const float (&factor)[NT][2], const uint8_t* stage, const float (&ks)[2],
-                                       const float (&lvs)[2], const float (&ivs)[2], int j0, const int (&limit)[NT][2], int least, int len) {
+__device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)[kTiles<NT>][D / 16][2],
+                                       const float (&factor)[kTiles<NT>][2], const uint8_t* stage, const float (&ks)[2],
+                                       const float (&lvs)[2], const float (&ivs)[2], int j0, const int (&limit)[kTiles<NT>][2], int least, int len) {
   const int lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
-  float x[2][NT][4];
+  float x[2][kTiles<NT>][4];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t kw[2][D / 16];
@@ -156,7 +167,7 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
         *reinterpret_cast<uint4*>(&kw[r][4 * i]) =
             *reinterpret_cast<const uint4*>(stage + (16 * h + 8 * r + g) * D + 64 * i + 16 * quad);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < kTiles<NT>; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[h][t][i] = 0.0f;
 #pragma unroll
@@ -165,7 +176,7 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
       codes_to_f16<FMT>(kw[0][j], ka[0], ka[2]);
       codes_to_f16<FMT>(kw[1][j], ka[1], ka[3]);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) mma_f16(x[h][t], ka, qb[t][j][0], qb[t][j][1]);
+      for (int t = 0; t < kTiles<NT>; ++t) mma_f16(x[h][t], ka, qb[t][j][0], qb[t][j][1]);
     }
   }
   const bool mask = j0 + kAttStep > least;
@@ -173,9 +184,9 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < kTiles<NT>; ++t)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < kCols<NT>; ++c) {
         const float f = fmaxf(factor[t][c] * ks[h], FLT_MIN);  // a masked -inf stays so
         if (mask) {
           if (j0 + 16 * h + g >= limit[t][c]) x[h][t][c] = -INFINITY;
@@ -188,9 +199,9 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
   }
   if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < kTiles<NT>; ++t)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < kCols<NT>; ++c) {
         float n = fmaxf(fmaxf(x[0][t][c], x[0][t][2 + c]), fmaxf(x[1][t][c], x[1][t][2 + c]));
 #pragma unroll
         for (int d = 4; d <= 16; d *= 2) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
@@ -210,12 +221,12 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t pb[NT][2];
+    uint32_t pb[kTiles<NT>][2];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float w[4];
+    for (int t = 0; t < kTiles<NT>; ++t) {
+      float w[4] = {};
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < kCols<NT>; ++c) {
         w[c] = exp2_fast(x[h][t][c] - s.n[t][c]);
         w[2 + c] = exp2_fast(x[h][t][2 + c] - s.n[t][c]);
         s.sum[t][c] = fmaf(w[c] + w[2 + c], ivs[h], s.sum[t][c]);
@@ -252,7 +263,7 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma_f16(s.acc[t][2 * w + i], va[i], pb[t][0], pb[t][1]);
+        for (int t = 0; t < kTiles<NT>; ++t) mma_f16(s.acc[t][2 * w + i], va[i], pb[t][0], pb[t][1]);
     }
   }
 }
@@ -294,7 +305,7 @@ template <int W>
 __device__ __forceinline__ int units_of(const Request& q) { return (q.len + (kAttStep * W) - 1) / (kAttStep * W); }
 template <int NT>
 __device__ __forceinline__ int row_blocks_of(const Request& q) {
-  return (q.n_rows + 8 * NT - 1) / (8 * NT);
+  return (q.n_rows + kRows<NT> - 1) / kRows<NT>;
 }
 
 // How the segments are dealt out.
@@ -470,20 +481,20 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
 #pragma unroll 1
   for (int i = 0; i < ring.stages - 1; ++i) fetch();
   RawQ<D, NT> raw;
-  load_q<D, NT>(a, q.t0, q.n_rows, st.seg % st.blocks * (8 * NT), head, raw);
-  int limit[NT][2], least = st.len;
+  load_q<D, NT>(a, q.t0, q.n_rows, st.seg % st.blocks * kRows<NT>, head, raw);
+  int limit[kTiles<NT>][2], least = st.len;
   for (int seg = st.seg; seg < st.seg_end; seg += W) {
-    const int row0 = (seg - head * st.blocks) * (8 * NT);
+    const int row0 = (seg - head * st.blocks) * kRows<NT>;
     const int next_head = (seg + W) / st.blocks;
     // what each row sees; rows past the last see everything and are not stored.
     // The same in every head, so only several row blocks need it again.
     if (seg == st.seg || st.blocks > 1) {
       least = st.len;
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < kTiles<NT>; ++t)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int row = row0 + 8 * t + 2 * quad + c;
+        for (int c = 0; c < kCols<NT>; ++c) {
+          const int row = row0 + row_in<NT>(t, quad, c);
           limit[t][c] = INT32_MAX;
           if (row < q.n_rows) {
             const int p = a.positions[q.t0 + row / a.group];
@@ -494,13 +505,13 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
       least = min(least, __shfl_xor_sync(0xffffffffu, least, 1));
       least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
     }
-    uint32_t qb[NT][D / 16][2];
-    float factor[NT][2];
+    uint32_t qb[kTiles<NT>][D / 16][2];
+    float factor[kTiles<NT>][2];
     convert_q<D, NT>(a, raw, qb, factor);
     if (seg != st.seg) now = ahead;
     if (seg + W < st.seg_end) {
       // the next segment's rows and scales, a segment ahead
-      load_q<D, NT>(a, q.t0, q.n_rows, (seg + W - next_head * st.blocks) * (8 * NT), next_head, raw);
+      load_q<D, NT>(a, q.t0, q.n_rows, (seg + W - next_head * st.blocks) * kRows<NT>, next_head, raw);
       scales_of(ahead, next_head);
     }
     TileState<D, NT> s;
@@ -525,9 +536,9 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
     }
     __syncwarp();
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < kTiles<NT>; ++t)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < kCols<NT>; ++c) {
 #pragma unroll
         for (int d = 4; d <= 16; d *= 2) s.sum[t][c] += __shfl_xor_sync(0xffffffffu, s.sum[t][c], d);
         if (s.sum[t][c] == 0.0f) s.n[t][c] = -INFINITY;  // nothing seen
@@ -538,7 +549,7 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
 }
 
 template <int FMT, int D, int NT, int W>
-__global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT == 1 ? (D == 64 ? 4 : 3) : D == 64 ? 3 : 2)
+__global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT <= 1 ? (D == 64 ? 4 : 3) : D == 64 ? 3 : 2)
     attention_kernel(const AttArgs a, float* partial, Piece* pieces, int given_split, int stages) {
   const int split = W > kAttWarps ? kEach : given_split;
   using R = Ring<D>;
@@ -596,10 +607,10 @@ __global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT == 1 ? (D == 64
       pos += static_cast<int64_t>(count) * span;
       run_stream<FMT, D, NT, W>(a, st, q, ring, [&](TileState<D, NT>& s, int head, int row0) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < kTiles<NT>; ++t)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int row = row0 + 8 * t + 2 * quad + c;
+          for (int c = 0; c < kCols<NT>; ++c) {
+            const int row = row0 + row_in<NT>(t, quad, c);
             if (row >= q.n_rows) continue;
 #pragma unroll
             for (int i0 = 0; i0 < D / 8; i0 += 8) {
@@ -626,10 +637,10 @@ __global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT == 1 ? (D == 64
     run_stream<FMT, D, NT, W>(a, st, q, ring, [&](TileState<D, NT>& s, int, int row0) {
       float* const mine = reinterpret_cast<float*>(ring.data);
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < kTiles<NT>; ++t)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int row = 8 * t + 2 * quad + c;
+        for (int c = 0; c < kCols<NT>; ++c) {
+          const int row = row_in<NT>(t, quad, c);
           if (row0 + row >= q.n_rows) continue;
           float* const at = mine + row * (D + 4);
           if (g == 0) at[D] = s.n[t][c], at[D + 1] = s.sum[t][c];
@@ -638,7 +649,7 @@ __global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT == 1 ? (D == 64
         }
     });
     __syncthreads();
-    const int head = st.seg / blocks, row0 = st.seg % blocks * (8 * NT);
+    const int head = st.seg / blocks, row0 = st.seg % blocks * kRows<NT>;
     constexpr int kLanes = D / 8;
     const bool complete = n_units == units;
     // a cut segment's part: slot 1 where it starts here, slot 0 where it came from the CTA before
@@ -649,7 +660,7 @@ __global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT == 1 ? (D == 64
       const int64_t seg_end = pos + (units - n_units);
       pieces[cta] = {q.t0, q.n_rows, row0, head, static_cast<int32_t>((seg_end * n_ctas - 1) / all), {0, 0, 0}};
     }
-    for (int row = tid / kLanes; row < min(8 * NT, q.n_rows - row0); row += 32 * W / kLanes) {
+    for (int row = tid / kLanes; row < min(kRows<NT>, q.n_rows - row0); row += 32 * W / kLanes) {
       const int d0 = (tid % kLanes) * 8;
       float n = -INFINITY, sum = 0.0f, o[8] = {};
 #pragma unroll
@@ -755,7 +766,7 @@ int launch_attention(const AttArgs& a, int max_kv_len, int max_q_len, void* work
   Piece* const pieces = reinterpret_cast<Piece*>(partial + 2 * kMaxCtas * partial_floats<D>());
   const size_t sums = sizeof(int64_t) * (static_cast<size_t>(a.n_requests) + 1);
   // no more CTAs than the units that the caller's bounds allow
-  const int64_t blocks = (static_cast<int64_t>(max_q_len) * a.group + 8 * NT - 1) / (8 * NT);
+  const int64_t blocks = (static_cast<int64_t>(max_q_len) * a.group + kRows<NT> - 1) / kRows<NT>;
   const int64_t units = (static_cast<int64_t>(max_kv_len) + kUnit - 1) / kUnit;
   // Cutting evens out the CTAs' loads and costs the join and the search for the cuts.  A
   // segment with an SM to itself takes 5.7 us and 0.57 more a unit (8 warps share its steps), cut segments
@@ -789,7 +800,7 @@ int launch_attention(const AttArgs& a, int max_kv_len, int max_q_len, void* work
       return TWELL_ERR_CUDA;
   }
   if (split != kCut || ctas == 1) return TWELL_OK;
-  const int rows = static_cast<int>(std::min<int64_t>(8 * NT, static_cast<int64_t>(a.n_tokens) * a.group));
+  const int rows = static_cast<int>(std::min<int64_t>(kRows<NT>, static_cast<int64_t>(a.n_tokens) * a.group));
   LaunchScope scope(TWELL_KERNEL_KV_JOIN, s);
   return launch_pdl(join_kernel<D, NT>, dim3(ctas - 1, rows), dim3(kTeams * D / 8), 0, s, a,
                     static_cast<const float*>(partial), static_cast<const Piece*>(pieces)) == cudaSuccess
@@ -799,14 +810,17 @@ int launch_attention(const AttArgs& a, int max_kv_len, int max_q_len, void* work
 
 template <int FMT>
 int launch_dim(const AttArgs& a, int dim, int max_kv_len, int max_q_len, void* workspace, cudaStream_t s) {
-  // row blocks of 8 where every request has 8 rows or fewer, else of 16: the
-  // codes' conversion is then shared by twice the rows
-  const bool small = static_cast<int64_t>(std::max(max_q_len, 1)) * a.group <= 8;
-  if (dim == 64)
-    return small ? launch_attention<FMT, 64, 1>(a, max_kv_len, max_q_len, workspace, s)
-                 : launch_attention<FMT, 64, 2>(a, max_kv_len, max_q_len, workspace, s);
-  return small ? launch_attention<FMT, 128, 1>(a, max_kv_len, max_q_len, workspace, s)
-               : launch_attention<FMT, 128, 2>(a, max_kv_len, max_q_len, workspace, s);
+  // Row blocks of 16 where a request has more than 8 rows: the codes' conversion is then shared by
+  // twice the rows.  Blocks of 4 where none has more: a lane's second column stays empty
+  // and half the exponentials go (250 ragged requests with a row each 143 -> 136 us, 4 x 131072 tokens with 4 134 -> 130).
+  const int64_t rows = static_cast<int64_t>(std::max(max_q_len, 1)) * a.group;
+  const auto fn = dim == 64 ? rows <= 4   ? launch_attention<FMT, 64, 0>
+                              : rows <= 8 ? launch_attention<FMT, 64, 1>
+                                          : launch_attention<FMT, 64, 2>
+                  : rows <= 4 ? launch_attention<FMT, 128, 0>
+                  : rows <= 8 ? launch_attention<FMT, 128, 1>
+                              : launch_attention<FMT, 128, 2>;
+  return fn(a, max_kv_len, max_q_len, workspace, s);
 }
 
 size_t decode_workspace_bytes(int dim) {
