@@ -26,9 +26,9 @@
 // P's 8 x 8 blocks are turned by movmatrix.
 //
 // Each cached byte is read once, so HBM bounds long caches: 4 x 65536 to 131072 tokens, 8 key heads of 128, e4m3:
-// 133 to 136 us, 5.7 TB/s.  Heads with one query row each and 64 dims are bound by the
-// instructions of a step, 535 for 32 tokens, a third of them conversions: 250 ragged requests, int8, 143 us, 4.0 TB/s.
-// Short caches are bound by the latencies in a row (lengths, table, codes, softmax): 16 x 1000 tokens 10.8 us.
+// 130 us, 5.9 TB/s.  Heads with one query row each and 64 dims are bound by the
+// instructions of a step, 475 for 32 tokens, a third of them conversions: 250 ragged requests, int8, 136 us, 4.2 TB/s.
+// Short caches are bound by the latencies in a row (lengths, table, codes, softmax): 16 x 1000 tokens 10.3 us.
 #include <algorithm>
 #include <cfloat>
 
