@@ -154,7 +154,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 template <int FMT, int D, int NT>
 __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)[kTiles<NT>][D / 16][2],
                                        const float (&factor)[kTiles<NT>][2], const uint8_t* stage, const float (&ks)[2],
-                                       const float (&lvs)[2], const float (&ivs)[2], int j0, const int (&limit)[kTiles<NT>][2], int least, int len) {
+                                       const float (&lvs)[2], const float (&ivs)[2], int j0,
+                                       const int (&limit)[kTiles<NT>][2], int least, int len) {
   const int lane = threadIdx.x & 31, g = lane >> 2, quad = lane & 3;
   float x[2][kTiles<NT>][4];
 #pragma unroll
@@ -284,7 +285,8 @@ __device__ __forceinline__ void zero_row(const AttArgs& a, int64_t t, int tid, i
 // thread) rather than wait for another kernel.  A piece's cut segments leave partial
 // results in the workspace (two a CTA: of the segment it starts in the middle of, and of
 // the one it ends in the middle of), which join_kernel adds in order.  (Adding them in the CTA
-// that finishes last costs more: one CTA's loads have to bring in all parts.)  Short segments are not cut, see launch_attention.
+// that finishes last costs more: one CTA's loads have to bring in all parts.)  Short
+// segments are not cut, see launch_attention.
 constexpr int kUnit = kAttStep * kAttWarps;  // cached tokens of a unit: a step of each warp
 constexpr int kMaxCtas = 608;
 constexpr int kMaxSmem = 224 * 1024;  // dynamic, of a CTA
@@ -771,7 +773,7 @@ int launch_attention(const AttArgs& a, int max_kv_len, int max_q_len, void* work
   // Cutting evens out the CTAs' loads and costs the join and the search for the cuts.  A
   // segment with an SM to itself takes 5.7 us and 0.57 more a unit (8 warps share its steps), cut segments
   // 8 to 18 us and, by how many there are, 0.07 to 0.44 a unit: about even at units = segments / 2
-  // (heads of 128, 128 segments of up to 1000 tokens: 10.8 us, cut 20; of 4000 26.1 and 32.2, of 9000
+  // (heads of 128, blocks of 8 rows, 128 segments of up to 1000 tokens: 10.8 us, cut 20; of 4000 26.1 and 32.2, of 9000
   // 49 and 50; 32 segments of 1500: 12.8 and 13.1, of 4000 24.1 and 18.1; 8 of 4000: 23.8 and 10.6).
   // More segments than SMs: whole ones are better up to 16 units (256 segments of 1500 tokens 26.0, cut 30.1;
   // of 2500 38.3 and 36.7), and up to 32 where there are so many that they even out

@@ -34,7 +34,8 @@ namespace {
 constexpr int kTileRows = 128;
 constexpr int kBlockRows = 2 * kTileRows;
 constexpr int kTokens = 128;   // cached tokens of a step
-constexpr int kRuns = 2;       // a step's weights are handed over in so many runs (heads of 64: 277 us; in one 285, in four 292)
+// A step's weights are handed over in so many runs (heads of 64: 277 us; in one 285, in four 292).
+constexpr int kRuns = 2;
 constexpr int kGroups = kTokens / 16;
 constexpr int kThreads = 16 * 32;
 // Registers a thread of each warpgroup (softmax 0, softmax 1, operands, mma's):
@@ -259,7 +260,8 @@ struct Barriers {
 static_assert(sizeof(Barriers) <= 512, "barrier region");
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a, int n_sms, int max_steps, float* partial, Item* items) {
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const AttArgs a, int n_sms, int max_steps, float* partial, Item* items) {
   using L = ChunkSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   grid_dependency_wait();
@@ -456,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const AttArgs a, int
         // a row that sees nothing divides by no sum: zeros
         const float inv = sum == 0.0f ? 0.0f : whole ? 1.0f / sum : 1.0f;
         uint16_t* const dst = a.o + static_cast<int64_t>(q.t0 + token) * a.ldo + static_cast<int64_t>(h) * D;
-        float* const to = partial + (static_cast<int64_t>(work.slot * work.n_parts + work.part) * kBlockRows + tid) * kPartFloats<D>;
+        float* const to =
+            partial + (static_cast<int64_t>(work.slot * work.n_parts + work.part) * kBlockRows + tid) * kPartFloats<D>;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32] = {};
