@@ -445,8 +445,9 @@ TWELL_API int twell_kv_append(const uint16_t* K, int64_t ldk, const uint16_t* V,
  * (exact for components above 2^-13 of the row's largest); probabilities are rounded to fp16,
  * every sum and the softmax's statistics are fp32.  Long caches are split
  * over the GPU and joined in a fixed order: the same call gives the same bits.
- * workspace: device, >= twell_kv_attention_workspace_bytes(...) bytes, 256-byte
- * aligned, contents need no initialisation.  A page number outside the cache
+ * workspace: device, >= twell_kv_attention_workspace_bytes(...) bytes (10 MB; 93 MB
+ * where the tokens may hold a chunk, more than 64 rows of one key head, for the
+ * parts of cut caches), 256-byte aligned, contents need no initialisation.  A page number outside the cache
  * reads page 0 and reports TWELL_ERR_BAD_FORMAT in cache->status.
  * n_requests <= 4096. */
 TWELL_API int twell_kv_attention(const uint16_t* Q, int64_t ldq, const twell_kv_t* cache, const int32_t* block_table,
