@@ -293,8 +293,9 @@ constexpr int kMaxSmem = 224 * 1024;  // dynamic, of a CTA
 // Segments of up to this many units are never cut: their join would cost more
 // than the imbalance of leaving them whole.
 constexpr int kWholeUnits = 2;
-// Whole segments of up to this many units (512 tokens) go to single warps.
-constexpr int kWarpUnits = 4;
+// Segments of up to this many steps (512 tokens) go to single warps: the groups that
+// the 32 lanes of run_stream look after, which it loads once for all of a warp's segments.
+constexpr int kWarpSteps = 16;
 
 struct Piece {   // of a segment that goes on in the next CTA, for join_kernel
   int32_t t0, n_rows, row0, head, last_cta, pad[3];
@@ -401,7 +402,7 @@ struct Ring {
   uint32_t phases;  // bit i: the parity that full[i] completes next
 };
 
-// One warp's way through the segments seg, seg + 4, ... < seg_end of a request
+// One warp's way through the segments seg, seg + W, ... < seg_end of a request
 // (row blocks of a head, then the next head): n_steps steps of 32 cached
 // tokens each, j_stride tokens apart from j_first on.
 struct Stream {
@@ -412,7 +413,8 @@ struct Stream {
 // The copies (bulk copies of 16 D bytes, the keys and the values of a group) run
 // a ring less one step ahead of the arithmetic, over the ends of segments too.  Lane l
 // looks after the groups l, l + 32, ... of a segment: it holds the page's
-// place and scales and issues the copies.  Several segments need at most 32 groups.
+// place and scales and issues the copies.  Only a stream of one segment may have more than 32 groups
+// (kWarpSteps steps): the places of the first 32 are not loaded again for the next segment.
 template <int FMT, int D, int NT, int W, typename Emit>
 __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, const Request& q, Ring<D>& ring,
                                            Emit emit) {
@@ -597,11 +599,12 @@ __global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT <= 1 ? (D == 64
     st.len = q.len;
     const int64_t left = static_cast<int64_t>(blocks) * a.heads - seg0;
     const int count = static_cast<int>(min(left, (end - pos) / span));
-    if (unit0 == 0 && units <= kWarpUnits && count >= W) {
-      // short segments that lie whole in this piece: each warp takes every fourth
+    const int steps = (q.len + kAttStep - 1) / kAttStep;
+    if (unit0 == 0 && steps <= kWarpSteps && count >= W) {
+      // short segments that lie whole in this piece: each warp takes every W-th
       st.j_first = 0;
       st.j_stride = kAttStep;
-      st.n_steps = (q.len + kAttStep - 1) / kAttStep;
+      st.n_steps = steps;
       st.seg = static_cast<int>(seg0) + ((warp - turn) & (W - 1));
       st.seg_end = static_cast<int>(seg0) + count;
       st.blocks = blocks;
@@ -635,7 +638,7 @@ __global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT <= 1 ? (D == 64
     st.seg = static_cast<int>(seg0);
     st.seg_end = st.seg + 1;
     st.blocks = blocks;
-    // the four warps' results of the tile, joined in warp order; they take the ring's place
+    // the warps' results of the tile, joined in warp order; they take the ring's place
     run_stream<FMT, D, NT, W>(a, st, q, ring, [&](TileState<D, NT>& s, int, int row0) {
       float* const mine = reinterpret_cast<float*>(ring.data);
 #pragma unroll
