@@ -207,9 +207,10 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
 #pragma unroll
         for (int d = 4; d <= 16; d *= 2) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
         if (n == -INFINITY) continue;  // nothing seen here
-        // the reference only grows; before the first value it is 0 and so is the sum
+        // The reference only grows; before the first value it is 0 and nothing has been added.  (Not
+        // told by the sum: that is of this lane's tokens, acc of all tokens for this lane's dims.)
         n = fmaxf(n, s.pass[t][c] - kLazy);
-        const float f = s.sum[t][c] == 0.0f ? 0.0f : exp2_fast(s.n[t][c] - n);
+        const float f = s.pass[t][c] == -INFINITY ? 0.0f : exp2_fast(s.n[t][c] - n);
         s.sum[t][c] *= f;
         s.n[t][c] = n;
         s.pass[t][c] = n + kLazy;

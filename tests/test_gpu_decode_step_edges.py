@@ -42,3 +42,38 @@ def test_attention_more_tokens_than_the_bound(tw, fmt, page, heads, group, dim, 
         check_attention(q, kc, ks, vc, vs, table, cu, positions, lens, group, dim ** -0.5, o, lse)
 
 
+def one_dim_cache(tw, fmt, page, dim, logits, values):
+    """One request of one head whose token j has the logit q[0] * logits[j] and the value values[j] in
+    every dim, all of them codes as they are (scale 1); returns (cache, table)."""
+    n = len(logits)
+    pages = -(-n // page)
+    cache = tw.alloc_kv_cache(pages, page, 1, dim, tw.KV_E4M3 if fmt == "e4m3" else tw.KV_INT8, "cuda")
+    k, v = np.zeros((pages * page, dim)), np.zeros((pages * page, dim))
+    k[:n, 0], v[:n] = logits, np.asarray(values)[:, None]
+    for codes, scale, x in ((cache.k, cache.k_scale, k), (cache.v, cache.v_scale, v)):
+        codes.copy_(dev(x.reshape(pages, 1, page, dim)).to(codes.dtype))
+        assert np.array_equal(host(codes.float()).reshape(-1, dim), x)
+        scale.fill_(1.0)
+    return cache, np.arange(pages, dtype=np.int32)[None]
+
+
+@pytest.mark.parametrize("fmt,dim", [("e4m3", 64), ("int8", 128)])
+@pytest.mark.parametrize("rows", [1, 4, 8, 16, 40])
+@pytest.mark.parametrize("bound", [300, 1 << 20])
+def test_attention_keeps_what_a_larger_logit_follows(tw, fmt, dim, rows, bound):
+    """Token 0 outweighs its neighbours by e^96, and a later one outweighs it by e^7: what
+    token 0 brought stays in every dim.  o = 64 e^-7 / (1 + e^-7): its terms are exact but for the weight,
+    which is rounded to fp16 after an exponential good to 2^-20."""
+    import torch
+    logits, values = np.full(300, -96.0), np.zeros(300)
+    logits[0], values[0], logits[260] = 0.0, 64.0, 7.0
+    cache, table = one_dim_cache(tw, fmt, 16, dim, logits, values)
+    q = torch.zeros((1, rows, dim), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1.0
+    o, lse = run_attention(tw, cache, q, table, np.array([0, 1], np.int32), np.array([299], np.int32), [300],
+                           max_kv=bound, scale=1.0)
+    want = 64 * np.exp(-7.0) / (1 + np.exp(-7.0))
+    assert (np.abs(host(o) - want) <= want * (UBF + U16 + 2.0 ** -19)).all()
+    assert (np.abs(host(lse) - (7 + np.log1p(np.exp(-7.0)))) <= 2.0 ** -19 + 4 * U32 * 7).all()
+
+
