@@ -9,7 +9,7 @@
 //   S = Q K^T                 fp16 x fp16 -> fp32, codes exact in fp16
 //   l = S (c log2(e) 2^k s_k) + log2 s_v   (2^k: the row's own factor, see convert_q)
 //   w = 2^(l - n)  ->  fp16,  O += w V,  sum += w / s_v
-// in one pass.  n is the row's reference: it follows the largest l, that is,
+// in one pass.  n is the row's reference: it follows the largest l (kRoom below it), that is,
 // the largest weight that a code is multiplied with, so the fp16 weights stay in their
 // range whatever the pages' scales are; the sum is fp32 and may differ from O's
 // scale by as much as the scales do (pages 2^100 apart are told apart still).
@@ -44,9 +44,6 @@ constexpr int kMaxRows = 8 * kMaxTiles;
 constexpr int kAttGroup = 16;   // cached tokens of one mma, all of one page
 constexpr int kAttStep = 2 * kAttGroup;  // cached tokens of one warp step
 constexpr int kAttMaxRequests = 4096;
-// The reference n is moved only when a new value passes it by this much (as a
-// power of two): weights up to 2^8 stay well inside fp16.
-constexpr float kLazy = 8.0f;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -69,9 +66,9 @@ __device__ __forceinline__ int row_in(int t, int quad, int c) { return NT == 0 ?
 template <int D, int NT>
 struct TileState {
   float acc[kTiles<NT>][D / 16][4];   // i: dims (D / 8) g + 2 i (both rows), then + 1 (both rows)
-  float n[kTiles<NT>][2];     // the reference (0 before the first step)
+  float n[kTiles<NT>][2];     // the reference (0 before the first value)
   float pass[kTiles<NT>][2];  // what an exponent must pass to move it
-  float sum[kTiles<NT>][2];   // sum of 2^(l - n)
+  float sum[kTiles<NT>][2];   // sum of 2^(l - n - kRoom) / s_v
 };
 
 template <int D, int NT>
@@ -210,9 +207,9 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
         // The reference only grows; before the first value it is 0 and nothing has been added.  (Not
         // told by the sum: that is of this lane's tokens, acc of all tokens for this lane's dims.)
         n = fmaxf(n, s.pass[t][c] - kLazy);
-        const float f = s.pass[t][c] == -INFINITY ? 0.0f : exp2_fast(s.n[t][c] - n);
+        const float f = s.pass[t][c] == -INFINITY ? 0.0f : exp2_fast(s.n[t][c] + kRoom - n);
         s.sum[t][c] *= f;
-        s.n[t][c] = n;
+        s.n[t][c] = n - kRoom;
         s.pass[t][c] = n + kLazy;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -428,14 +425,14 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
     int64_t cell;   // of head 0
     int64_t at;     // its place in head 0, in bytes
     bool on;        // there is such a group
-    float ks, lvs, ivs;  // key scale, log2 and inverse of the value scale
+    float ks, lvs, ivs;  // key scale, log2 of the value scale, 2^-kRoom over it
   };
   const auto scales_of = [&](Batch& b, int head) {
     if (b.on) {
       const float vs = __ldg(a.v_scale + b.cell + head);
       b.ks = __ldg(a.k_scale + b.cell + head);
       b.lvs = fmaxf(log2_fast(vs), -200.0f);
-      b.ivs = 1.0f / vs;
+      b.ivs = kUnroom / vs;
     }
   };
   const auto batch_from = [&](int step, int head) {

@@ -28,6 +28,13 @@ constexpr int kChunkRows = 64;
 int launch_chunk_attention(const AttArgs& a, int format, int dim, int max_kv_len, void* workspace, cudaStream_t s);
 size_t chunk_workspace_bytes(int64_t rows, int dim);  // for so many rows in all
 
+// Weights are 2^(l - n) in fp16.  A row's reference n stands kRoom below the largest l that it was
+// set by, and moves when an l passes that one by kLazy: the largest weights lie between 2^kRoom and
+// 2^(kRoom + kLazy) = 2^15, below fp16's 65504, and a weight is off by 2^-32 of the largest at most where fp16
+// cannot hold it to 2^-11 of itself (below 2^-21 of the largest; with n at the largest l 2^-25, which over
+// 131072 tokens came to 2^-8 of the result).  The sums of weights are taken without the factor 2^kRoom.
+constexpr float kLazy = 8.0f, kRoom = 7.0f, kUnroom = 1.0f / 128;
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -77,13 +84,13 @@ __device__ __forceinline__ Request request(const AttArgs& a, int r) {
   return {t0, (t1 - t0) * a.group, visible_len(a, r)};
 }
 
-// Eight dims of one finished row: o / sum, rounded once, and the row's lse.
-// n = -inf: the row has seen nothing.
+// Eight dims of one finished row: o / sum, rounded once, and the row's lse.  o has the
+// weights' factor 2^kRoom, sum has not.  n = -inf: the row has seen nothing.
 template <int D>
 __device__ __forceinline__ void store_row(const AttArgs& a, int t0, int row, int head, int d0, float n, float sum,
                                           const float (&o)[8]) {
   const bool seen = n > -INFINITY;
-  const float f = seen ? 1.0f / sum : 0.0f;
+  const float f = seen ? kUnroom / sum : 0.0f;
   const int64_t token = t0 + row / a.group;
   const int h = head * a.group + row % a.group;
   uint32_t out[4];
@@ -93,7 +100,7 @@ __device__ __forceinline__ void store_row(const AttArgs& a, int t0, int row, int
              (static_cast<uint32_t>(float_to_bf16_bits(o[2 * i + 1] * f)) << 16);
   *reinterpret_cast<uint4*>(a.o + token * a.ldo + static_cast<int64_t>(h) * D + d0) =
       make_uint4(out[0], out[1], out[2], out[3]);
-  if (a.lse && d0 == 0) a.lse[token * a.q_heads + h] = seen ? (n + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+  if (a.lse && d0 == 0) a.lse[token * a.q_heads + h] = seen ? (n + kRoom + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace twell

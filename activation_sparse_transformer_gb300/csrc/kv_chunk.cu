@@ -11,7 +11,7 @@
 // For tile X and step t:  S_X = Q_X K_t^T (tcgen05, fp32 in TMEM);  w = 2^(S f_j +
 // log2 s_v - n) -> fp16 in TMEM over S;  O_X += w V_t (A from TMEM).  f_j is
 // the row's factor times the key scale and s_v the value scale of the token's
-// page; n follows the row's largest exponent lazily (when it is passed by 8, O
+// page; n follows the row's largest exponent lazily (kRoom below it; when it is passed by 8, O
 // is rescaled).  The softmax's own sum needs w / s_v: it is taken per 16
 // tokens, which share a page.  While one tile is in its softmax the tensor cores work on
 // the other.
@@ -42,7 +42,6 @@ constexpr int kThreads = 16 * 32;
 // together the 4 x 128 that the launch gives.
 constexpr int kRegsSoftmax = 184, kRegsOperands = 88, kRegsMma = 56;
 static_assert(2 * kRegsSoftmax + kRegsOperands + kRegsMma == 4 * 128, "register split");
-constexpr float kLazy = 8.0f;
 constexpr int kMaxWaves = 4, kMaxParts = kMaxWaves * 152;  // CTAs that leave parts of rows
 constexpr int kJoinSteps = 8;
 template <int D>
@@ -268,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, for the compiler too
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* const scales = reinterpret_cast<float*>(smem + L::kScaleAt);  // [4][key, log2 value, 1 / value][8]
+  float* const scales = reinterpret_cast<float*>(smem + L::kScaleAt);  // [4][key, log2 value, 2^-kRoom / value][8]
   Barriers& bar = *reinterpret_cast<Barriers*>(smem + L::kBarAt);
   volatile int* const abort = &bar.abort;
   Work work;
@@ -402,9 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           // O holds the steps before this one: their mma's were waited for before this S was issued
           float f = 1.0f;
           if (move) {
-            f = sum == 0.0f ? 0.0f : exp2_fast(n - top);
+            f = sum == 0.0f ? 0.0f : exp2_fast(n + kRoom - top);
             sum *= f;
-            n = top;
+            n = top - kRoom;
             pass = top + kLazy;
           }
           if (t > 0) {
@@ -456,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const bool whole = work.n_parts == 1;
         // a row that sees nothing divides by no sum: zeros
-        const float inv = sum == 0.0f ? 0.0f : whole ? 1.0f / sum : 1.0f;
+        const float inv = sum == 0.0f ? 0.0f : whole ? kUnroom / sum : 1.0f;
         uint16_t* const dst = a.o + static_cast<int64_t>(q.t0 + token) * a.ldo + static_cast<int64_t>(h) * D;
         float* const to =
             partial + (static_cast<int64_t>(work.slot * work.n_parts + work.part) * kBlockRows + tid) * kPartFloats<D>;
@@ -490,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float4*>(to + D) = make_float4(sum != 0.0f ? n : -INFINITY, sum, 0.0f, 0.0f);
         if (whole && a.lse && row < q.n_rows)
           a.lse[static_cast<int64_t>(q.t0 + token) * a.q_heads + h] =
-              sum != 0.0f ? (n + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+              sum != 0.0f ? (n + kRoom + log2f(sum)) * 0.69314718055994531f : -INFINITY;
       }
     }
   } else if (warp < 12) {
@@ -666,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* const sc = scales + (t & 3) * 3 * kGroups + lane;
         sc[0] = ks;
         sc[kGroups] = fmaxf(log2_fast(vs), -200.0f);
-        sc[2 * kGroups] = 1.0f / vs;
+        sc[2 * kGroups] = kUnroom / vs;
         mbar_arrive(&bar.scale_full[t & 3]);
         page = next;
         next = after;

@@ -77,3 +77,25 @@ def test_attention_keeps_what_a_larger_logit_follows(tw, fmt, dim, rows, bound):
     assert (np.abs(host(lse) - (7 + np.log1p(np.exp(-7.0)))) <= 2.0 ** -19 + 4 * U32 * 7).all()
 
 
+@pytest.mark.parametrize("fmt,dim,new", [("e4m3", 128, 70), ("int8", 64, 70), ("e4m3", 64, 1), ("int8", 128, 4)])
+@pytest.mark.parametrize("bound", [1, 30000])
+def test_attention_of_many_small_weights(tw, fmt, dim, new, bound):
+    """One token outweighs each of the others by e^18 and has the value 0, they have the
+    value 1: o is their weights' sum, N e^-18 / (1 + N e^-18).  A weight in fp16 is off by 2^-25 of
+    fp16's 1 where it is below 2^-14, and the largest weight stands at 2^7 or above: N 2^-32 in all.
+    (A short bound keeps the cache in one piece, where they all meet the one large weight.)"""
+    import torch
+    n = 30000
+    logits, values = np.zeros(n), np.ones(n)
+    logits[0], values[0] = 18.0, 0.0
+    cache, table = one_dim_cache(tw, fmt, 128, dim, logits, values)
+    q = torch.zeros((new, 1, dim), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1.0
+    positions = np.arange(n - new, n).astype(np.int32)
+    o, _ = run_attention(tw, cache, q, table, np.array([0, new], np.int32), positions, [n], max_q=new, max_kv=bound,
+                         scale=1.0)
+    tail = positions * np.exp(-18.0)
+    want = (tail / (1 + tail))[:, None, None]
+    assert (np.abs(host(o) - want) <= want * (UBF + U16 + 2.0 ** -19 + 2 * n * U32) + n * 2.0 ** -32).all()
+
+
