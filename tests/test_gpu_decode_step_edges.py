@@ -99,3 +99,38 @@ def test_attention_of_many_small_weights(tw, fmt, dim, new, bound):
     assert (np.abs(host(o) - want) <= want * (UBF + U16 + 2.0 ** -19 + 2 * n * U32) + n * 2.0 ** -32).all()
 
 
+@pytest.mark.parametrize("fmt,dim", [("e4m3", 64), ("int8", 128)])
+@pytest.mark.parametrize("length,new", [(150, 90), (9000, 1), (9000, 12), (20000, 70)])
+def test_attention_scales_far_apart_in_chunks_and_parts(tw, fmt, dim, length, new):
+    """Value scales from 2^-60 to 2^40 in the chunk kernel and where caches are cut and their parts
+    joined: neither weights nor sums nor the parts' references may leave their range.  Bounds as in
+    check_attention, and 2^-32 of the row's largest weight for each weight in fp16: it shows where the tokens
+    of large weights hold the code 0."""
+    import torch
+    r = np.random.RandomState(length + new)
+    page, lens = 64, np.array([length])
+    n_pages = -(-length // page)
+    cache, kc, ks, vc, vs = make_cache(tw, fmt, n_pages, page, 1, dim, 2)
+    vs = np.exp2(r.randint(-60, 41, vs.shape)).astype(np.float64)
+    ks = np.exp2(r.randint(-14, -3, ks.shape)).astype(np.float64)
+    cache.v_scale.copy_(dev(vs).float())
+    cache.k_scale.copy_(dev(ks).float())
+    table = layout(r, lens, page, n_pages, n_pages)
+    q = dev(r.randn(new, 4, dim) * np.array([1e-3, 1, 3, 30])[None, :, None]).to(torch.bfloat16)
+    cu, positions = np.array([0, new], np.int32), np.arange(length - new, length).astype(np.int32)
+    o, lse = run_attention(tw, cache, q, table, cu, positions, lens, max_q=new)
+    pages = table[0]
+    k = (kc[pages, 0] * ks[pages, 0, None, None]).reshape(-1, dim)[:length]
+    v = (vc[pages, 0] * vs[pages, 0, None, None]).reshape(-1, dim)[:length]
+    rows, limit = host(q).reshape(-1, dim), np.repeat(positions + 1, 4)
+    want, want_lse, spread, most = ref.attention(rows, k, v, dim ** -0.5, limit)
+    depth = 2 * 2 * dim * U32 * most + 2.0 ** -20 + 2 * length * U32
+    s_v = np.repeat(vs[pages, 0], page)[:length]
+    for i, (got, got_lse) in enumerate(zip(host(o).reshape(-1, dim), host(lse).reshape(-1))):
+        p = np.exp(dim ** -0.5 * (k[:limit[i]] @ rows[i]) - want_lse[i])
+        tiny = length * 2.0 ** -32 * (p * s_v[:limit[i]]).max() * ref.QMAX[fmt]
+        tol = UBF * np.abs(want[i]) * (1 + 2.0 ** -6) + (U16 + depth) * spread[i] + tiny + 1e-30
+        assert (np.abs(got - want[i]) <= tol).all(), (i, (np.abs(got - want[i]) / tol).max())
+        assert abs(got_lse - want_lse[i]) <= depth + 4 * U32 * abs(want_lse[i]), i
+
+
