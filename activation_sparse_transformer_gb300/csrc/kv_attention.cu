@@ -228,7 +228,8 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
       for (int c = 0; c < kCols<NT>; ++c) {
         w[c] = exp2_fast(x[h][t][c] - s.n[t][c]);
         w[2 + c] = exp2_fast(x[h][t][2 + c] - s.n[t][c]);
-        s.sum[t][c] = fmaf(w[c] + w[2 + c], ivs[h], s.sum[t][c]);
+        const float both = w[c] + w[2 + c];
+        if (both != 0.0f) s.sum[t][c] = fmaf(both, ivs[h], s.sum[t][c]);  // a page that is not seen may have any scale
       }
       pb[t][0] = transpose8(pack_f16(w[0], w[1]));
       pb[t][1] = transpose8(pack_f16(w[2], w[3]));
@@ -242,14 +243,38 @@ __device__ __forceinline__ void step32(TileState<D, NT>& s, const uint32_t (&qb)
       else
         *reinterpret_cast<uint2*>(vw[i]) = *reinterpret_cast<const uint2*>(src);
     }
-    if (j0 + kAttStep > len) {
-      // past the request's tokens the page (or the stage) may hold anything,
-      // and 0 * NaN is not 0: zeros in its place
+    if (mask) {
+      // Past the request's tokens the page (or the stage) may hold anything, and so may a token
+      // that not all rows see, but 0 * NaN is not 0: zeros in their place, and NaN
+      // for the rows that do see such a token.
+      uint32_t bad = 0;  // tokens of the group with a NaN among their codes
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        const int token = (i >> 1) * 8 + 2 * quad + (i & 1);
+        uint32_t nan = 0;
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w)
-          if (j0 + 16 * h + (i >> 1) * 8 + 2 * quad + (i & 1) >= len) vw[i][w] = 0;
+        for (int w = 0; w < D / 32; ++w) {
+          if (j0 + 16 * h + token >= len) vw[i][w] = 0;
+          if (FMT == TWELL_KV_E4M3) nan |= nan_codes(vw[i][w]);
+        }
+        if (nan) bad |= 1u << token;
+      }
+      if (FMT == TWELL_KV_E4M3) bad = __reduce_or_sync(0xffffffffu, bad);
+      if (bad) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w)
+            if (bad >> ((i >> 1) * 8 + 2 * quad + (i & 1)) & 1) vw[i][w] = 0;
+#pragma unroll
+        for (int t = 0; t < kTiles<NT>; ++t)
+#pragma unroll
+          for (int c = 0; c < kCols<NT>; ++c)
+            if (limit[t][c] >= j0 + 16 * h + __ffs(bad)) {
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) s.acc[t][i][c] = s.acc[t][i][2 + c] = __int_as_float(0x7FC00000);
+            }
+      }
     }
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
@@ -431,7 +456,7 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
     if (b.on) {
       const float vs = __ldg(a.v_scale + b.cell + head);
       b.ks = __ldg(a.k_scale + b.cell + head);
-      b.lvs = fmaxf(log2_fast(vs), -200.0f);
+      b.lvs = log2_scale(vs);
       b.ivs = kUnroom / vs;
     }
   };

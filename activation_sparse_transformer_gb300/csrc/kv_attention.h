@@ -70,6 +70,13 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& p01, uint32_t
   }
 }
 
+// Bits where a byte of w is e4m3's NaN, 0x7F or 0xFF.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// log2 of a value scale.  Always a number: a page that a row does not see may have any
+// scale, and a masked -inf has to stay so when it is added.
+__device__ __forceinline__ float log2_scale(float vs) { return fminf(fmaxf(log2_fast(vs), -200.0f), 200.0f); }
+
 __device__ __forceinline__ int visible_len(const AttArgs& a, int r) {
   const int64_t room = static_cast<int64_t>(a.max_blocks) << a.page_shift;
   return static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(a.kv_lens[r]), room)));

@@ -253,7 +253,8 @@ struct Barriers {
   uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], scale_full[4], s_full[2], p_full[2][kRuns], o_done[2], drain;
   uint32_t tmem;
   int abort;
-  int most;
+  int most, least;  // tokens that the rows of the block see
+  int nan_at;       // the first token with NaN among its value's codes that not all rows see
   alignas(16) Order order;
 };
 static_assert(sizeof(Barriers) <= 512, "barrier region");
@@ -295,11 +296,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar.drain, 1);
     bar.abort = 0;
     bar.most = 0;
+    bar.least = bar.nan_at = INT32_MAX;
     mbar_fence_init();
   }
   if (warp == 12) tmem_alloc(&bar.tmem, 512);
   __syncthreads();
-  // what each row sees, and the most that any row of the block does
+  // what each row sees, and the most and the least that a row of the block does
   int limit = 0;
   const int row = row0 + tid;
   if (tid < kBlockRows) {
@@ -307,10 +309,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int p = a.positions[q.t0 + row / a.group];
       limit = max(0, min(p < INT32_MAX ? p + 1 : p, q.len));
     }
-    int most = limit;
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-    if (lane == 0) atomicMax(&bar.most, most);
+    const int most = __reduce_max_sync(0xffffffffu, limit);
+    const int least = __reduce_min_sync(0xffffffffu, row < q.n_rows ? limit : INT32_MAX);
+    if (lane == 0) atomicMax(&bar.most, most), atomicMin(&bar.least, least);
   }
   tc_fence_before();
   __syncthreads();
@@ -436,7 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               add2(part[0], part[1], e0, e1);
               p[8 * (g % 2) + i / 2] = pack_f16(e0, e1);
             }
-            sum = fmaf(part[0] + part[1], ivs[g], sum);
+            const float both = part[0] + part[1];
+            if (both != 0.0f) sum = fmaf(both, ivs[g], sum);  // a page that is not seen may have any scale
           }
           tmem_st16(s_tm + 16 * c, p);
           if ((c + 1) % (4 / kRuns) == 0) {
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const bool whole = work.n_parts == 1;
         // a row that sees nothing divides by no sum: zeros
-        const float inv = sum == 0.0f ? 0.0f : whole ? kUnroom / sum : 1.0f;
+        const float inv = limit > bar.nan_at ? __int_as_float(0x7FC00000) : sum == 0.0f ? 0.0f : whole ? kUnroom / sum : 1.0f;
         uint16_t* const dst = a.o + static_cast<int64_t>(q.t0 + token) * a.ldo + static_cast<int64_t>(h) * D;
         float* const to =
             partial + (static_cast<int64_t>(work.slot * work.n_parts + work.part) * kBlockRows + tid) * kPartFloats<D>;
@@ -504,15 +506,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int dw = warp - 8, half = (lane >> 2) & 1, oct = lane >> 3;
     const int blk = D == 128 ? half ^ (oct & 1) : 0, even = 2 * (lane & 3);
     const int tok = dw * (32 / kLanes) + (D == 128 ? (oct >> 1) * 2 + half : lane >> 2);
+    const int least = bar.least;
     const auto load = [&](int v, int t, uint4 (&w)[kPasses]) {
       const uint8_t* const raw = smem + L::kRawAt + v * L::kRaw + blk * 64 + (lane & 3) * 16;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) w[i] = *reinterpret_cast<const uint4*>(raw + (i * kPass + tok) * D);
-      if (j0 + (t + 1) * kTokens > q.len) {
-        // past the request's tokens a page may hold anything: zeros
+      if (j0 + (t + 1) * kTokens > least) {
+        // Past the request's tokens a page may hold anything, and so may the value of a token that
+        // not all rows see, but 0 * NaN is not 0: zeros, and NaN at the end for the rows that see such a token.
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i)
-          if (j0 + t * kTokens + i * kPass + tok >= q.len) w[i] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kPasses; ++i) {
+          const int j = j0 + t * kTokens + i * kPass + tok;
+          if (j >= q.len) w[i] = make_uint4(0, 0, 0, 0);
+          if (FMT == TWELL_KV_E4M3 && v == 1 &&
+              (nan_codes(w[i].x) | nan_codes(w[i].y) | nan_codes(w[i].z) | nan_codes(w[i].w))) {
+            atomicMin(&bar.nan_at, j);
+            w[i] = make_uint4(0, 0, 0, 0);
+          }
+        }
       }
     };
     const auto store = [&](uint8_t* dst, uint32_t halves, const uint4 (&w)[kPasses]) {
@@ -664,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // mma's of t - 4: both softmaxes are through with that step's scales.
         float* const sc = scales + (t & 3) * 3 * kGroups + lane;
         sc[0] = ks;
-        sc[kGroups] = fmaxf(log2_fast(vs), -200.0f);
+        sc[kGroups] = log2_scale(vs);
         sc[2 * kGroups] = kUnroom / vs;
         mbar_arrive(&bar.scale_full[t & 3]);
         page = next;

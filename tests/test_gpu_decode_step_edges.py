@@ -134,3 +134,68 @@ def test_attention_scales_far_apart_in_chunks_and_parts(tw, fmt, dim, length, ne
         assert abs(got_lse - want_lse[i]) <= depth + 4 * U32 * abs(want_lse[i]), i
 
 
+HIDDEN = [  # page, group, dim, length, positions: the rows of one request
+    (16, 4, 64, 300, [100]),                            # a single token and pages that are to be written yet
+    (64, 1, 128, 700, [9]),
+    (32, 8, 128, 90, [3, 40, 41, 42]),                  # several tokens that see different parts of a page
+    (16, 2, 64, 900, list(range(880, 900))),
+    (128, 4, 128, 1500, list(range(700, 760))),         # a chunk
+    (16, 1, 64, 300, list(range(180, 260)) + [-1, 5]),
+    (128, 1, 128, 20000, list(range(9950, 10050))),     # a chunk whose cache is cut into parts
+    (64, 1, 64, 9000, [4000, 4001]),                    # single rows whose cache is cut
+]
+
+
+@pytest.mark.parametrize("page,group,dim,length,positions", HIDDEN)
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("scale", [0.0, float("nan"), float("inf")])
+def test_attention_of_hidden_tokens_that_are_no_numbers(tw, page, group, dim, length, positions, fmt, scale):
+    """kv_lens beyond the rows' positions: what no row sees (codes of NaN, scales that were never
+    written) leaves no trace."""
+    import torch
+    r = np.random.RandomState(length)
+    lens, n_pages = np.array([length]), -(-length // page)
+    cache, kc, ks, vc, vs = make_cache(tw, fmt, n_pages, page, 2, dim, 3)
+    table = layout(r, lens, page, n_pages, n_pages)
+    first = max(positions) + 1   # the first token that nobody sees
+    for c in (cache.k, cache.v):
+        raw = c.view(torch.uint8)
+        for j in range(first // page, n_pages):
+            raw[int(table[0, j]), :, max(first - j * page, 0):] = 0x7F if fmt == "e4m3" else 0x80
+    for s in (cache.k_scale, cache.v_scale):
+        for j in range(-(-first // page), n_pages):
+            s[int(table[0, j])] = scale
+    positions = np.array(positions, np.int32)
+    cu = np.array([0, len(positions)], np.int32)
+    q = dev(r.randn(len(positions), 2 * group, dim) * 1.3).to(torch.bfloat16)
+    o, lse = run_attention(tw, cache, q, table, cu, positions, lens, max_q=len(positions))
+    ks[~np.isin(np.arange(n_pages), table[0, :-(-first // page)])] = 1.0
+    vs[~np.isin(np.arange(n_pages), table[0, :-(-first // page)])] = 1.0
+    check_attention(q, kc, ks, vc, vs, table, cu, positions, lens, group, dim ** -0.5, o, lse)
+
+
+@pytest.mark.parametrize("page,group,dim,length,positions", HIDDEN[2:])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_attention_of_a_nan_code_that_some_rows_see(tw, page, group, dim, length, positions, what):
+    """One NaN among the codes of a token: rows that end before it are as without it, the
+    others are no numbers in that dim (a key's: in all dims)."""
+    import torch
+    r = np.random.RandomState(length + 1)
+    lens, n_pages = np.array([length]), -(-length // page)
+    cache, kc, ks, vc, vs = make_cache(tw, "e4m3", n_pages, page, 2, dim, 3)
+    table = layout(r, lens, page, n_pages, n_pages)
+    positions = np.array(positions, np.int32)
+    at = int(positions[len(positions) // 2])   # half of the rows see it
+    getattr(cache, what).view(torch.uint8)[int(table[0, at // page]), :, at % page, dim - 5] = 0xFF
+    cu = np.array([0, len(positions)], np.int32)
+    q = dev(r.randn(len(positions), 2 * group, dim) * 1.3).to(torch.bfloat16)
+    o, lse = run_attention(tw, cache, q, table, cu, positions, lens, max_q=len(positions))
+    sees = positions >= at
+    assert sees.any() and not sees.all()
+    assert np.isnan(host(o)[sees][..., dim - 5]).all()
+    assert what == "v" or np.isnan(host(o)[sees]).all()
+    for i in np.flatnonzero(~sees):
+        check_attention(q[i:i + 1], kc, ks, vc, vs, table, np.array([0, 1]), positions[i:i + 1], lens, group,
+                        dim ** -0.5, o[i:i + 1], lse[i:i + 1])
+
+
