@@ -120,6 +120,12 @@ struct Stat {
   float m, s, u;
 };
 
+// A row whose scaled maximum is so far from zero that y's rounding counts, or that y is no number
+// where x = logits / T is one (a row masked by its type's lowest value): summed again, from
+// memory, by the definition's own x (far_stat), and answered in natural units.
+constexpr float kFar = 1.0e6f;
+__device__ __forceinline__ bool is_far(float m) { return !(fabsf(m) < kFar); }
+
 // Stats relative to a common maximum; an empty part has s = u = 0.
 __device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
   const float m = fmaxf(a.m, b.m);
@@ -264,11 +270,46 @@ __device__ void slice_top(LpShared<NT>& sh, const Slice<T>& sl, float inv_t, int
   __syncthreads();
 }
 
+// f over the elements of a row by NT threads, t the thread's number among them.
+template <typename T, int NT, typename F>
+__device__ __forceinline__ void each_of_row(const T* src, int vocab, int t, F f) {
+  for (int i = t; i < vocab; i += NT) f(Elem<T>::load(src + i), i);
+}
+// v of all NT threads (a warp, or a CTA with a place for each of its warps), joined by f.
+template <int NT, typename V, typename F>
+__device__ __forceinline__ V team_join(V v, V* place, F f) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) v = f(v, __shfl_xor_sync(0xffffffffu, v, d));
+  if (NT == 32) return v;
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) place[threadIdx.x / 32] = v;
+  __syncthreads();
+  v = place[0];
+  for (int w = 1; w < NT / 32; ++w) v = f(v, place[w]);
+  return v;
+}
+// The statistics of a far row in all its threads: m the largest x (not times log2 e), s and u as
+// always, sums of 2^d and 2^d d with d = (x - m) log2 e.  Two more reads of the row: rare.
+template <typename T, int NT>
+__device__ __forceinline__ Stat far_stat(const T* src, int vocab, float inv_t, int t, float* place) {
+  const auto sum = [](float a, float b) { return a + b; };
+  float m = -INFINITY, s = 0.0f, u = 0.0f;
+  each_of_row<T, NT>(src, vocab, t, [&](float x, int) { m = fmaxf(m, __fmul_rn(x, inv_t)); });
+  m = fmaxf(team_join<NT>(m, place, [](float a, float b) { return fmaxf(a, b); }), -FLT_MAX);
+  each_of_row<T, NT>(src, vocab, t, [&](float x, int) {
+    const float d = (__fmul_rn(x, inv_t) - m) * kLog2e, e = ex2(d);
+    s += e;
+    u = fmaf(e, fmaxf(d, -2000.0f), u);
+  });
+  s = team_join<NT>(s, place, sum);
+  return {m, s, team_join<NT>(u, place, sum)};
+}
+
 // May a row whose smallest logit is lo and whose maximum is m be summed two elements at a
 // time?  Masked tokens (2^-inf * -inf is no number, be they -inf or so low that the product is) and logits
 // so large that the rounding of m counts are summed one by one, with products rounded as m's was.
 __device__ __forceinline__ bool short_sums(float lo, float m, float c) {
-  return __fmul_rn(lo, c) > -FLT_MAX && fabsf(m) < 1.0e6f && c < 1.0e6f;
+  return __fmul_rn(lo, c) > -FLT_MAX && !is_far(m) && c < 1.0e6f;
 }
 
 // (a, b) += ... of two elements in one instruction each.
@@ -287,31 +328,47 @@ __device__ __forceinline__ void sum2(float2& s, float2& u, float x0, float x1, f
       : "f"(e0), "f"(e1), "f"(d0), "f"(d1));
 }
 
-// A row's results from its statistics; a NaN or +inf among the logits makes all of them NaN.
-__device__ __forceinline__ float logprob_of(const LogprobsArgs& a, const Stat& st, float x) {
-  const float c = a.inv_temperature * kLog2e;
-  const float d = fabsf(st.m) < 1.0e6f ? fmaf(x, c, -st.m) : __fmul_rn(x, c) - st.m;
-  return isnan(st.s) ? __int_as_float(0x7FC00000) : st.s == 0.0f ? -INFINITY : (d - log2f(st.s)) * kLn2;
+// A row's results from its statistics (FAR: those of far_stat); a NaN or +inf among the
+// scaled logits makes all of them NaN.
+template <bool FAR>
+__device__ __forceinline__ float lse_of(const Stat& st, float log_s) {
+  return isnan(st.s) ? __int_as_float(0x7FC00000) : st.s == 0.0f ? -INFINITY
+         : FAR       ? fmaf(log_s, kLn2, st.m) : (st.m + log_s) * kLn2;
 }
-__device__ __forceinline__ void store_row(const LogprobsArgs& a, int64_t row, const Stat& st, int target, float x) {
-  const float nan = __int_as_float(0x7FC00000), log_s = log2f(st.s);
-  const bool broken = isnan(st.s), empty = !broken && st.s == 0.0f;
-  if (a.lse) a.lse[row] = broken ? nan : empty ? -INFINITY : (st.m + log_s) * kLn2;
-  if (a.entropy) a.entropy[row] = broken ? nan : empty ? 0.0f : (log_s - st.u / st.s) * kLn2;
-  if (a.targets) a.logprob[row] = target >= 0 && target < a.vocab ? logprob_of(a, st, x) : 0.0f;
+template <bool FAR>
+__device__ __forceinline__ float logprob_of(const LogprobsArgs& a, const Stat& st, float logit) {
+  const float log_s = log2f(st.s);
+  float y;
+  if (FAR) {
+    y = __fmul_rn(logit, a.inv_temperature) - st.m - log_s * kLn2;
+  } else {
+    const float d = fmaf(logit, a.inv_temperature * kLog2e, -st.m);
+    y = (d - log_s) * kLn2;
+    // a masked token's d may be no number's
+    if (d < -kFar) y = __fmul_rn(logit, a.inv_temperature) - lse_of<FAR>(st, log_s);
+  }
+  return isnan(st.s) ? __int_as_float(0x7FC00000) : st.s == 0.0f ? -INFINITY : y;
+}
+template <bool FAR>
+__device__ __forceinline__ void store_row(const LogprobsArgs& a, int64_t row, const Stat& st, int target, float logit) {
+  const float log_s = log2f(st.s);
+  if (a.lse) a.lse[row] = lse_of<FAR>(st, log_s);
+  if (a.entropy)
+    a.entropy[row] = isnan(st.s) ? __int_as_float(0x7FC00000) : st.s == 0.0f ? 0.0f : (log_s - st.u / st.s) * kLn2;
+  if (a.targets) a.logprob[row] = target >= 0 && target < a.vocab ? logprob_of<FAR>(a, st, logit) : 0.0f;
 }
 
-template <typename T>
+template <bool FAR, typename T>
 __device__ __forceinline__ void store_target(const LogprobsArgs& a, int64_t row, const Stat& st, const T* src) {
   const int t = a.targets ? a.targets[row] : -1;
-  store_row(a, row, st, t, t >= 0 && t < a.vocab ? Elem<T>::load(src + t) : 0.0f);
+  store_row<FAR>(a, row, st, t, t >= 0 && t < a.vocab ? Elem<T>::load(src + t) : 0.0f);
 }
 // The i-th best of a row.
-template <typename T>
+template <bool FAR, typename T>
 __device__ __forceinline__ void store_top(const LogprobsArgs& a, int64_t row, int i, const Stat& st, uint64_t key,
                                           const T* src) {
   const bool broken = isnan(st.s);
-  a.top_logprob[row * a.top_k + i] = logprob_of(a, st, Elem<T>::load(src + (broken ? 0 : key_index(key))));
+  a.top_logprob[row * a.top_k + i] = logprob_of<FAR>(a, st, Elem<T>::load(src + (broken ? 0 : key_index(key))));
   a.top_index[row * a.top_k + i] = broken ? -1 : key_index(key);
 }
 
@@ -427,8 +484,12 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a) {
   if (ranks == 1) {
     __syncthreads();
     const Stat st = sh.stat;
-    if (tid == 0) store_target(a, row, st, src);
-    if (tid < a.top_k) store_top(a, row, tid, st, sh.best[tid], src);
+    const auto store = [&](const Stat& st, auto far) {
+      if (tid == 0) store_target<far.value>(a, row, st, src);
+      if (tid < a.top_k) store_top<far.value>(a, row, tid, st, sh.best[tid], src);
+    };
+    if (is_far(st.m)) store(far_stat<T, NT>(src, a.vocab, a.inv_temperature, tid, sh.warp_hi), std::true_type{});
+    else store(st, std::false_type{});
     return;
   }
   cluster.sync();
@@ -451,15 +512,23 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a) {
   }
   auto last = cluster.barrier_arrive();  // no rank leaves before the others have read its shared memory
   __syncthreads();
-  if (rank == 0 && tid == 0) store_target(a, row, sh.whole, src);
-  for (int i0 = 0; i0 < a.top_k; i0 += NT / kRankLanes) {
-    const int i = i0 + tid / kRankLanes;
-    const uint64_t key = i < a.top_k ? sh.key[rank * a.top_k + i] : 0;
-    const int better = rank_in<kRankLanes>(sh.key, n_keys, key);
-    if (tid % kRankLanes != 0 || i >= a.top_k) continue;
-    const Stat st = sh.whole;
-    if (isnan(st.s) ? rank == 0 : key && better < a.top_k) store_top(a, row, isnan(st.s) ? i : better, st, key, src);
+  if (rank > 0 && n_keys == 0) {  // has placed what it has, without the row's statistics
+    cluster.barrier_wait(std::move(last));
+    return;
   }
+  const auto store = [&](const Stat& st, auto far) {
+    if (rank == 0 && tid == 0) store_target<far.value>(a, row, st, src);
+    for (int i0 = 0; i0 < a.top_k; i0 += NT / kRankLanes) {
+      const int i = i0 + tid / kRankLanes;
+      const uint64_t key = i < a.top_k ? sh.key[rank * a.top_k + i] : 0;
+      const int better = rank_in<kRankLanes>(sh.key, n_keys, key);
+      if (tid % kRankLanes != 0 || i >= a.top_k) continue;
+      if (isnan(st.s) ? rank == 0 : key && better < a.top_k)
+        store_top<far.value>(a, row, isnan(st.s) ? i : better, st, key, src);
+    }
+  };
+  if (is_far(sh.whole.m)) store(far_stat<T, NT>(src, a.vocab, a.inv_temperature, tid, sh.warp_hi), std::true_type{});
+  else store(sh.whole, std::false_type{});
   cluster.barrier_wait(std::move(last));
 }
 
@@ -471,8 +540,9 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a) {
 constexpr int kRowsThreads = 256, kBatch = 4;
 // From 2 rows an SM on (320 x 131072 fp32: 34 us, staged in clusters 40).
 constexpr int kManyRows = 2;
+// (Six CTAs an SM where one takes a row: far_stat's registers alone would leave five, 85.9 us.)
 template <typename T, int NT>
-__global__ void __launch_bounds__(kRowsThreads) logprobs_rows_kernel(const LogprobsArgs a, int n_rows) {
+__global__ void __launch_bounds__(kRowsThreads, NT == 32 ? 5 : 6) logprobs_rows_kernel(const LogprobsArgs a, int n_rows) {
   using E = Elem<T>;
   __shared__ Stat sh[kRowsThreads / 32];
   grid_dependency_wait();
@@ -553,10 +623,16 @@ __global__ void __launch_bounds__(kRowsThreads) logprobs_rows_kernel(const Logpr
   if (NT > 32) {
     if (t % 32 == 0) sh[t / 32] = st;
     __syncthreads();
+    if (t >= 32) return;
     if (t == 0)
       for (int w = 1; w < NT / 32; ++w) st = join(st, sh[w]);
   }
-  if (t == 0) store_row(a, row, st, target, x_target);
+  if (is_far(__shfl_sync(0xffffffffu, st.m, 0))) {
+    st = far_stat<T, 32>(src, a.vocab, a.inv_temperature, t, nullptr);
+    if (t == 0) store_row<true>(a, row, st, target, x_target);
+  } else if (t == 0) {
+    store_row<false>(a, row, st, target, x_target);
+  }
 }
 
 struct BwdArgs {

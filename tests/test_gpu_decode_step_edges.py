@@ -199,3 +199,75 @@ def test_attention_of_a_nan_code_that_some_rows_see(tw, page, group, dim, length
                         dim ** -0.5, o[i:i + 1], lse[i:i + 1])
 
 
+# ---------------------------------------------------------------- log probabilities
+def far_rows(r, n, vocab, t):
+    """Rows of t at the ends of its range: all at its lowest value; all there but for masked ones; one
+    at its largest and the rest spread over it all; far from zero with small distances; ordinary ones."""
+    import torch
+    low, high = torch.finfo(t).min, torch.finfo(t).max
+    x = r.randn(n, vocab) * 2
+    for i in range(n):
+        if i % 6 == 0:
+            x[i] = low
+        elif i % 6 == 1:
+            x[i] = np.where(np.arange(vocab) % 3 == 1, -np.inf, low)
+        elif i % 6 == 2:
+            x[i] = low + (high / 2 - low / 2) * r.rand(vocab) * 1.9
+            x[i, vocab // 2] = high
+        elif i % 6 == 3:
+            x[i] = np.round(4 * r.randn(vocab)) + 3e6      # a quarter is the distance of fp32 there
+        elif i % 6 == 4:
+            x[i] = -1e9 - 64 * r.randint(0, 3, vocab)      # 64 is
+    return dev(x).to(t)
+
+
+def far_reference(x, target, k):
+    """ref.logprobs for rows without NaN and +inf, by distances from the maximum: lse itself, in 64
+    bits too, is too coarse at 1e38."""
+    has, order = 0 <= target < len(x), sorted(range(len(x)), key=lambda j: (-x[j], j))[:k]
+    m = x.max()
+    if m == -np.inf:
+        return (-np.inf if has else 0.0), 0.0, -np.inf, np.full(k, -np.inf), np.array(order)
+    logp = (x - m) - np.log(np.exp(x - m).sum())
+    p = np.exp(logp)
+    return (logp[target] if has else 0.0, -(p[p > 0] * logp[p > 0]).sum(), m + np.log(np.exp(x - m).sum()),
+            logp[order], np.array(order))
+
+
+FAR = [(12, 700), (12, 40000), (7, 131072), (400, 30000), (1300, 500), (1300, 40)]
+
+
+@pytest.mark.parametrize("n,vocab", FAR)
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("inv_t", [1.0, 0.5])
+@pytest.mark.parametrize("k", [0, 5])
+def test_logprobs_at_the_ends_of_the_type(tw, n, vocab, dtype, inv_t, k):
+    """x = logits * inv_t is finite there though its product with log2 e is not, or is too coarse.
+    Distances from the largest x are exact or one rounding; a result of size S is rounded to 2^-24 S,
+    and of distances that are no more than 90 the bounds are the ordinary ones."""
+    import torch
+    t = getattr(torch, dtype)
+    r = np.random.RandomState(vocab)
+    x = far_rows(r, n, vocab, t)
+    targets = r.randint(-1, vocab + 1, n).astype(np.int32)
+    got = [None if v is None else host(v) for v in run_logprobs(tw, x, dev(targets), inv_t, k)]
+    xs = host(x.float() * torch.tensor(inv_t, dtype=torch.float32, device="cuda"))
+    tol = 2.0 ** -21 + 2 * (vocab / 256 + 40) * U32 + 4 * U32 * 90
+
+    def near(a, b, what):
+        if np.abs(b) <= float(torch.finfo(torch.float32).max):
+            assert abs(a - b) <= tol + 4 * U32 * abs(b), what
+        else:   # no number of the results' type
+            assert a == np.copysign(np.inf, b), what
+
+    for i in list(range(min(n, 12))) + list(range(12, n, 61)):
+        lp, en, lse, top, index = far_reference(xs[i], int(targets[i]), k)
+        near(got[2][i], lse, (i, "lse"))
+        near(got[0][i], lp, (i, "logprob"))
+        assert abs(got[1][i] - en) <= 4 * (tol + 2 * U32) * (en + 2), (i, "entropy", got[1][i], en)
+        if k:
+            assert np.array_equal(got[4][i], index), i
+            for j in range(k):
+                near(got[3][i][j], top[j], (i, "top"))
+
+
