@@ -645,11 +645,30 @@ struct BwdArgs {
   const float *lse, *entropy, *d_logprob, *d_entropy;
 };
 
+// From here on lse, in fp32, tells p to 2^-10 of itself or less (2^-24 |lse|), which a bf16 result shows; at
+// 1e38 it does not tell a row's sum from its maximum.  The row is then summed again, and its
+// gradient taken by distances from its maximum: by one team, as another slice's CTA may have
+// overwritten the logits (d_logits may be the logits) before they are read.
+constexpr float kFarLse = 16384.0f;
+template <typename T, int NT>
+__device__ __noinline__ void far_gradient(const T* src, T* dst, int vocab, float inv_t, int t, float* place, int target,
+                                          float g, float gh, float entropy) {
+  const Stat st = far_stat<T, NT>(src, vocab, inv_t, t, place);
+  const float log_sum = log2f(st.s) * kLn2, base = fmaf(gh, entropy, g);
+  each_of_row<T, NT>(src, vocab, t, [&](float x, int i) {
+    const float logp = __fmul_rn(x, inv_t) - st.m - log_sum, p = ex2(logp * kLog2e);
+    float d = p == 0.0f ? 0.0f : -p * fmaf(gh, logp, base);
+    if (i == target) d += g;
+    dst[i] = Elem<T>::store(d);
+  });
+}
+
 // NT threads, a CTA or a warp of it, write one slice of a row.  Reads and writes every
 // element once: HBM bounds it.  The row's four numbers are loaded once by each thread.
 template <typename T, int NT>
 __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const BwdArgs a, int n_rows) {
   using E = Elem<T>;
+  __shared__ float place[kBwdThreads / 32];
   grid_dependency_wait();
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kBwdThreads / NT) + threadIdx.x / NT;
   if (row >= n_rows) return;
@@ -665,6 +684,11 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const BwdArgs
   // -p (g + gh (log p + H)) + g [j = t], all times 1 / T
   const float base = a.entropy ? fmaf(gh, a.entropy[row], g) : g;
   const bool empty = lse == -INFINITY;
+  if (fabsf(lse) >= kFarLse && fabsf(lse) < INFINITY) {
+    if (blockIdx.y == 0)
+      far_gradient<T, NT>(src, dst, a.vocab, inv_t, tid, place, target, g, gh, a.entropy ? a.entropy[row] : 0.0f);
+    return;
+  }
   target -= beg;
   const auto grad = [&](float x, int at) {
     const float logp = __fmul_rn(x, inv_t) - lse;

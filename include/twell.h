@@ -487,6 +487,8 @@ TWELL_API int twell_logprobs(const void* logits, int32_t dtype, int64_t ld, int3
  * left (lse, entropy) and the upstream gradients of logprob and entropy:
  *   d_logits_j = inv_temperature * (d_logprob (1[j = target] - p_j)
  *                                   - d_entropy p_j (log p_j + entropy))
+ * p = exp(x - lse), or where |lse| is 16384 or more (fp32 then tells it too coarsely)
+ * the softmax of the logits themselves.
  * A row without a target takes d_logprob as 0; p_j = 0 gives 0; a row of -inf
  * only gives zeros.  d_logits: type dtype, ldd >= vocab apart, base 16-byte
  * aligned; it may be the logits themselves (with ldd == ld).  targets with

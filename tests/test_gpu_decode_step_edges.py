@@ -271,3 +271,39 @@ def test_logprobs_at_the_ends_of_the_type(tw, n, vocab, dtype, inv_t, k):
                 near(got[3][i][j], top[j], (i, "top"))
 
 
+@pytest.mark.parametrize("n,vocab", [(12, 700), (12, 40000), (6, 131072), (2500, 200)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("inv_t", [1.0, 0.5])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_logprobs_gradient_at_the_ends_of_the_type(tw, n, vocab, dtype, inv_t, in_place):
+    """There lse, in 32 bits, does not tell a row's sum from its maximum: p is still the softmax.  Bounds as for
+    ordinary rows: p is off by 2^-20 and the sum's roundings of itself, the result by its type's."""
+    import torch
+    t = getattr(torch, dtype)
+    r = np.random.RandomState(vocab)
+    x = far_rows(r, n, vocab, t)
+    kept = x.clone()
+    targets = r.randint(-1, vocab + 1, n).astype(np.int32)
+    _, entropy, lse, *_ = run_logprobs(tw, x, dev(targets), inv_t, 0)
+    g, gh = r.randn(n).astype(np.float32), r.randn(n).astype(np.float32)
+    out = x if in_place else torch.empty_like(x)
+    tw.twell_logprobs_bwd(x, dev(targets), inv_t, lse, entropy, dev(g), dev(gh), out)
+    xs, got = host(kept.float() * torch.tensor(inv_t, dtype=torch.float32, device="cuda")), host(out)
+    ulp = UBF if dtype == "bfloat16" else U32
+    for i in list(range(min(n, 12))) + list(range(12, n, 61)):
+        _, en, *_ = far_reference(xs[i], -1, 0)
+        m = xs[i].max()
+        logp = (xs[i] - m) - np.log(np.exp(xs[i] - m).sum())
+        p = np.exp(logp)
+        has = 0 <= targets[i] < vocab
+        w = -float(gh[i]) * (np.where(p > 0, logp, 0) + en)
+        want = p * w - (p * g[i] if has else 0)
+        size = p * (np.abs(w) + abs(float(gh[i])) * (np.abs(np.where(p > 0, logp, 0)) + en + 1) + abs(g[i]))
+        if has:
+            want[targets[i]] += g[i]
+        want, size = want * inv_t, size * inv_t
+        rel = 2.0 ** -20 + (vocab / 256 + 40) * 2 * U32 + 8 * U32 * 90
+        tol = rel * size + 2 * U32 * np.abs(want) + ulp * np.abs(want) * (1 + 2 * rel) + 1e-37
+        assert (np.abs(got[i] - want) <= tol + ulp * rel * size).all(), (i, (np.abs(got[i] - want) / tol).max())
+
+
