@@ -62,7 +62,7 @@ EXPORTED = [
     "twell_bwd_tiles_workspace_bytes", "twell_gated_ffn_fwd_train", "twell_gated_ffn_bwd",
     "twell_gated_bwd_workspace_bytes", "twell_gated_bwd_tiles_workspace_bytes",
     "twell_kv_plan", "twell_kv_append", "twell_kv_attention", "twell_kv_attention_workspace_bytes",
-    "twell_kv_read_status", "twell_logprobs", "twell_logprobs_bwd",
+    "twell_kv_read_status", "twell_logprobs", "twell_logprobs_bwd", "twell_selftest_kv_attention_stall",
 ]
 
 
@@ -139,6 +139,8 @@ def load_library() -> ctypes.CDLL:
         "twell_kv_append": (ctypes.c_int, [P, I64, P, I64, P, P, I32, I32, KV, P]),
         "twell_kv_attention": (ctypes.c_int, [P, I64, KV, P, I32, P, P, P, I32, I32, I32, I32, I32, ctypes.c_float, P,
                                               I64, P, P, SZ, P]),
+        "twell_selftest_kv_attention_stall": (ctypes.c_int, [P, I64, KV, P, I32, P, P, P, I32, I32, I32, I32, I32,
+                                                             ctypes.c_float, P, I64, P, P, SZ, ctypes.c_uint64, P]),
         "twell_kv_attention_workspace_bytes": (SZ, [I32, I32, I32, I32, I32]),
         "twell_kv_read_status": (ctypes.c_int, [KV, P]),
         "twell_logprobs": (ctypes.c_int, [P, I32, I64, I32, I32, P, ctypes.c_float, P, P, P, I32, P, P, P]),

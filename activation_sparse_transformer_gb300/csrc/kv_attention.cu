@@ -438,11 +438,12 @@ struct Stream {
 // looks after the groups l, l + 32, ... of a segment: it holds the page's
 // place and scales and issues the copies.  Only a stream of one segment may have more than 32 groups
 // (kWarpSteps steps): the places of the first 32 are not loaded again for the next segment.
+// False when a wait expired: the segment has no result, and no copy is in flight any more.
 template <int FMT, int D, int NT, int W, typename Emit>
-__device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, const Request& q, Ring<D>& ring,
+__device__ __forceinline__ bool run_stream(const AttArgs& a, const Stream& st, const Request& q, Ring<D>& ring,
                                            Emit emit) {
   using R = Ring<D>;
-  if (st.seg >= st.seg_end) return;
+  if (st.seg >= st.seg_end) return true;
   const int lane = threadIdx.x & 31, quad = lane & 3;
   const int page_mask = (1 << a.page_shift) - 1;
   const int64_t head_bytes = static_cast<int64_t>(D) << a.page_shift;
@@ -550,8 +551,18 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
       }
       __syncwarp();  // all lanes have read the stage that fetch fills again
       fetch();
-      if (!mbar_wait(ring.full + ring.slot, (ring.phases >> ring.slot) & 1u, kWaitLimitNs, ring.abort))
-        report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(ring.full + ring.slot, (ring.phases >> ring.slot) & 1u, a.wait_ns, ring.abort))) {
+        if (lane == 0) report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
+        // let the copies already in flight land: the stages from this one up to the next to be fetched
+        int slot = ring.slot;
+        do {
+          volatile int never = 0;
+          mbar_wait(ring.full + slot, (ring.phases >> slot) & 1u, kDrainNs, &never);
+          slot = slot + 1 == ring.stages ? 0 : slot + 1;
+        } while (slot != f_slot);
+        return false;
+      }
       ring.phases ^= 1u << ring.slot;
       const uint8_t* const stage = ring.data + ring.slot * R::kStage;
       ring.slot = ring.slot + 1 == ring.stages ? 0 : ring.slot + 1;
@@ -573,6 +584,7 @@ __device__ __forceinline__ void run_stream(const AttArgs& a, const Stream& st, c
     emit(s, head, row0);
     head = next_head;
   }
+  return true;
 }
 
 template <int FMT, int D, int NT, int W>
@@ -589,7 +601,7 @@ __global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT <= 1 ? (D == 64
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, quad = lane & 3;
   Ring<D> ring = {stages, ring_all + warp * ring_bytes, full[warp], &abort_flag, 0, 0};
   if (tid == 0) abort_flag = 0;
-  if (lane < stages) mbar_init(full[warp] + lane, 2);
+  if (lane < stages) mbar_init(full[warp] + lane, lane == 0 ? 2 + a.stall : 2);
   mbar_fence_init();
   grid_dependency_wait();
   scan_requests<NT, W>(a, start, warp_sum, split);
@@ -610,6 +622,7 @@ __global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT <= 1 ? (D == 64
     zero_row<D>(a, t, tid, (32 * W));
 
   int turn = 0;  // of the warps at whole segments
+  bool ok = true;  // no wait of this warp has expired
   while (pos < end) {
     const int r = request_at(start, a.n_requests, pos);
     const Request q = request(a, r);
@@ -633,7 +646,7 @@ __global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT <= 1 ? (D == 64
       st.blocks = blocks;
       turn += count;
       pos += static_cast<int64_t>(count) * span;
-      run_stream<FMT, D, NT, W>(a, st, q, ring, [&](TileState<D, NT>& s, int head, int row0) {
+      ok = ok && run_stream<FMT, D, NT, W>(a, st, q, ring, [&](TileState<D, NT>& s, int head, int row0) {
 #pragma unroll
         for (int t = 0; t < kTiles<NT>; ++t)
 #pragma unroll
@@ -662,7 +675,7 @@ __global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT <= 1 ? (D == 64
     st.seg_end = st.seg + 1;
     st.blocks = blocks;
     // the warps' results of the tile, joined in warp order; they take the ring's place
-    run_stream<FMT, D, NT, W>(a, st, q, ring, [&](TileState<D, NT>& s, int, int row0) {
+    ok = ok && run_stream<FMT, D, NT, W>(a, st, q, ring, [&](TileState<D, NT>& s, int, int row0) {
       float* const mine = reinterpret_cast<float*>(ring.data);
 #pragma unroll
       for (int t = 0; t < kTiles<NT>; ++t)
@@ -676,7 +689,7 @@ __global__ void __launch_bounds__(32 * W, W > kAttWarps ? 1 : NT <= 1 ? (D == 64
           for (int i = 0; i < D / 8; ++i) at[(D / 8) * g + i] = s.acc[t][i / 2][2 * (i & 1) + c];
         }
     });
-    __syncthreads();
+    if (__syncthreads_or(!ok)) return;
     const int head = st.seg / blocks, row0 = st.seg % blocks * kRows<NT>;
     constexpr int kLanes = D / 8;
     const bool complete = n_units == units;
@@ -871,13 +884,13 @@ extern "C" TWELL_API size_t twell_kv_attention_workspace_bytes(int32_t n_tokens,
   return decode_workspace_bytes(head_dim) + (chunk_workspace_bytes(rows, head_dim) + 255) / 256 * 256;
 }
 
-extern "C" TWELL_API int twell_kv_attention(const uint16_t* Q, int64_t ldq, const twell_kv_t* cache,
-                                            const int32_t* block_table, int32_t max_blocks, const int32_t* cu_q,
-                                            const int32_t* positions, const int32_t* kv_lens, int32_t n_tokens,
-                                            int32_t n_requests, int32_t n_q_heads, int32_t max_kv_len,
-                                            int32_t max_q_len, float softmax_scale, uint16_t* O, int64_t ldo,
-                                            float* lse, void* workspace, size_t workspace_bytes,
-                                            twell_stream_t stream) {
+namespace {
+
+int kv_attention(const uint16_t* Q, int64_t ldq, const twell_kv_t* cache, const int32_t* block_table,
+                 int32_t max_blocks, const int32_t* cu_q, const int32_t* positions, const int32_t* kv_lens,
+                 int32_t n_tokens, int32_t n_requests, int32_t n_q_heads, int32_t max_kv_len, int32_t max_q_len,
+                 float softmax_scale, uint16_t* O, int64_t ldo, float* lse, void* workspace, size_t workspace_bytes,
+                 twell_stream_t stream, int stall, uint64_t wait_ns) {
   KV_TRY(check_kv(cache));
   if (n_tokens < 0 || n_requests < 0 || max_blocks < 0 || max_kv_len < 0 || max_q_len < 0)
     return TWELL_ERR_INVALID_ARG;
@@ -927,6 +940,8 @@ extern "C" TWELL_API int twell_kv_attention(const uint16_t* Q, int64_t ldq, cons
   a.n_pages = cache->n_pages;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.chunk_rows = INT32_MAX;
+  a.stall = stall;
+  a.wait_ns = wait_ns;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (n_requests > 0 && static_cast<int64_t>(max_q_len) * a.group > kChunkRows) {
     a.chunk_rows = kChunkRows;
@@ -935,4 +950,29 @@ extern "C" TWELL_API int twell_kv_attention(const uint16_t* Q, int64_t ldq, cons
   }
   return cache->format == TWELL_KV_E4M3 ? launch_dim<TWELL_KV_E4M3>(a, cache->head_dim, max_kv_len, max_q_len, workspace, s)
                                         : launch_dim<TWELL_KV_INT8>(a, cache->head_dim, max_kv_len, max_q_len, workspace, s);
+}
+
+}  // namespace
+
+extern "C" TWELL_API int twell_kv_attention(const uint16_t* Q, int64_t ldq, const twell_kv_t* cache,
+                                            const int32_t* block_table, int32_t max_blocks, const int32_t* cu_q,
+                                            const int32_t* positions, const int32_t* kv_lens, int32_t n_tokens,
+                                            int32_t n_requests, int32_t n_q_heads, int32_t max_kv_len,
+                                            int32_t max_q_len, float softmax_scale, uint16_t* O, int64_t ldo,
+                                            float* lse, void* workspace, size_t workspace_bytes,
+                                            twell_stream_t stream) {
+  return kv_attention(Q, ldq, cache, block_table, max_blocks, cu_q, positions, kv_lens, n_tokens, n_requests, n_q_heads,
+                      max_kv_len, max_q_len, softmax_scale, O, ldo, lse, workspace, workspace_bytes, stream, 0,
+                      kWaitLimitNs);
+}
+
+extern "C" TWELL_API int twell_selftest_kv_attention_stall(
+    const uint16_t* Q, int64_t ldq, const twell_kv_t* cache, const int32_t* block_table, int32_t max_blocks,
+    const int32_t* cu_q, const int32_t* positions, const int32_t* kv_lens, int32_t n_tokens, int32_t n_requests,
+    int32_t n_q_heads, int32_t max_kv_len, int32_t max_q_len, float softmax_scale, uint16_t* O, int64_t ldo, float* lse,
+    void* workspace, size_t workspace_bytes, uint64_t limit_ns, twell_stream_t stream) {
+  if (limit_ns < 100000ull || limit_ns > 1000000000ull) return TWELL_ERR_INVALID_ARG;
+  return kv_attention(Q, ldq, cache, block_table, max_blocks, cu_q, positions, kv_lens, n_tokens, n_requests, n_q_heads,
+                      max_kv_len, max_q_len, softmax_scale, O, ldo, lse, workspace, workspace_bytes, stream, 1,
+                      limit_ns);
 }

@@ -19,12 +19,16 @@ struct AttArgs {
   int max_blocks, n_tokens, n_requests, q_heads, heads, group, page_shift, n_pages;
   float scale_log2;  // softmax_scale * log2(e)
   int chunk_rows;    // requests of more rows than this go to chunk_attention
+  int stall;         // self-test: arrivals that a barrier of each CTA's copies waits for in vain (else 0)
+  uint64_t wait_ns;  // limit of each wait
 };
 
 // Requests of more than this many rows (tokens times query heads of a key head)
 // fill tcgen05's 128 rows well enough to pay for the fp16 copy of the cache
 // that its operands need; a.chunk_rows is this, or INT32_MAX when no request is that large.
 constexpr int kChunkRows = 64;
+// After an expired wait: how long a CTA waits for its own copies in flight before it leaves.
+constexpr uint64_t kDrainNs = 10000000ull;
 int launch_chunk_attention(const AttArgs& a, int format, int dim, int max_kv_len, void* workspace, cudaStream_t s);
 size_t chunk_workspace_bytes(int64_t rows, int dim);  // for so many rows in all
 

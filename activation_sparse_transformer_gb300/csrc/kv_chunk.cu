@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     mbar_init(&bar.q_full, kTileRows * n_tiles);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.raw_full[i], kGroups);
+      mbar_init(&bar.raw_full[i], i == 0 ? kGroups + a.stall : kGroups);
       mbar_init(&bar.raw_empty[i], 128);
       mbar_init(&bar.k_full[i], 128);
       mbar_init(&bar.v_full[i], 128);
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_steps = static_cast<int>(static_cast<int64_t>(all_steps) * (work.part + 1) / work.n_parts) - first;
   const int j0 = first * kTokens;  // the part's first token
   const uint32_t tmem = __shfl_sync(0xffffffffu, bar.tmem, 0);
-  const uint64_t limit_ns = kWaitLimitNs;
+  const uint64_t limit_ns = a.wait_ns;
   bool ok = true;
 
   if (warp < 8) {
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // wait for the mma's already issued before TMEM is released
           commit(leader, &bar.drain);
           volatile int never = 0;
-          mbar_wait(&bar.drain, 0, 10000000ull, &never);
+          mbar_wait(&bar.drain, 0, kDrainNs, &never);
         }
       }
     } else if (warp == 13 && lane < kGroups) {
@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // let the copies already in flight land before the CTA leaves
         for (int v = 0; v < 2 && issued > 0; ++v) {
           volatile int never = 0;
-          mbar_wait(&bar.raw_full[v], (issued - 1) & 1, 10000000ull, &never);
+          mbar_wait(&bar.raw_full[v], (issued - 1) & 1, kDrainNs, &never);
         }
       }
     }

@@ -512,6 +512,17 @@ TWELL_API int twell_read_status(const twell_t* layout, twell_stream_t stream);
  * 0 < limit_ns <= 10 s.  Asynchronous on `stream`. */
 TWELL_API int twell_selftest_wait_timeout(int32_t* status, uint64_t limit_ns, twell_stream_t stream);
 
+/* The same for the attention over the cache: twell_kv_attention with waits of at most
+ * limit_ns (0.1 ms to 1 s), in which one barrier of each CTA's copies waits for an arrival that never
+ * comes.  The call ends with TWELL_ERR_WAIT_TIMEOUT in cache->status and without results. */
+TWELL_API int twell_selftest_kv_attention_stall(const uint16_t* Q, int64_t ldq, const twell_kv_t* cache,
+                                                const int32_t* block_table, int32_t max_blocks, const int32_t* cu_q,
+                                                const int32_t* positions, const int32_t* kv_lens, int32_t n_tokens,
+                                                int32_t n_requests, int32_t n_q_heads, int32_t max_kv_len,
+                                                int32_t max_q_len, float softmax_scale, uint16_t* O, int64_t ldo,
+                                                float* lse, void* workspace, size_t workspace_bytes,
+                                                uint64_t limit_ns, twell_stream_t stream);
+
 /* Device check of a packed layout against the format rules at the top of this
  * file: a debugging aid for layouts built outside twell_pack / twell_ffn_fwd
  * (the gathers trust stored indices and slot numbers, and read out of bounds

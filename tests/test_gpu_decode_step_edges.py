@@ -199,6 +199,44 @@ def test_attention_of_a_nan_code_that_some_rows_see(tw, page, group, dim, length
                         dim ** -0.5, o[i:i + 1], lse[i:i + 1])
 
 
+@pytest.mark.parametrize("fmt,dim,group,lens,new", [
+    ("e4m3", 128, 4, [1000] * 16, 1),           # segments with a CTA each
+    ("int8", 64, 1, [9000, 20000], 1),          # cut segments
+    ("int8", 64, 1, [100 + 3 * i for i in range(120)], 1),   # short segments, one a warp
+    ("e4m3", 128, 2, [3000] * 40, 1),           # whole segments, several a CTA
+    ("e4m3", 64, 4, [700, 20000], 90),          # chunks, whole and in parts
+    ("int8", 128, 4, [100], 40)])               # a chunk of one step
+def test_attention_whose_copies_do_not_arrive(tw, fmt, dim, group, lens, new):
+    """A barrier that one arrival is missing from: the waits expire (here after 1 ms), every CTA lets
+    its copies land and leaves, the status tells, and the next call is right."""
+    import torch
+    r = np.random.RandomState(dim)
+    page, lens, heads = 16, np.array(lens), 4
+    n_pages = int(sum(-(-lens // page)))
+    cache, kc, ks, vc, vs = make_cache(tw, fmt, n_pages, page, heads, dim, 5)
+    table = layout(r, lens, page, n_pages, int(max(-(-lens // page))))
+    cu = (np.arange(len(lens) + 1) * new).astype(np.int32)
+    positions = np.concatenate([np.arange(n - new, n) for n in lens]).astype(np.int32)
+    n, q_heads = len(positions), heads * group
+    q = dev(r.randn(n, q_heads, dim)).to(torch.bfloat16)
+    o = torch.empty_like(q)
+    ws = torch.empty(tw.kv_attention_workspace_bytes(n, len(lens), q_heads, heads, dim), dtype=torch.uint8,
+                     device="cuda")
+    d = [dev(x) for x in (table, cu, positions, lens.astype(np.int32))]
+    ld = q_heads * dim
+    args = (q.data_ptr(), ld, cache.struct(), d[0].data_ptr(), table.shape[1], d[1].data_ptr(), d[2].data_ptr(),
+            d[3].data_ptr(), n, len(lens), q_heads, int(max(lens)), new, dim ** -0.5, o.data_ptr(), ld, None,
+            ws.data_ptr(), ws.numel())
+    stall = tw.load_library().twell_selftest_kv_attention_stall
+    assert stall(*args, 0, None) == -1 and stall(*args, 2_000_000_000, None) == -1
+    assert stall(*args, 1_000_000, torch.cuda.current_stream().cuda_stream) == 0
+    assert tw.twell_kv_read_status(cache) == -7
+    cache.status.zero_()
+    o, lse = run_attention(tw, cache, q, table, cu, positions, lens, max_q=new)
+    assert tw.twell_kv_read_status(cache) == 0
+    check_attention(q, kc, ks, vc, vs, table, cu, positions, lens, group, dim ** -0.5, o, lse)
+
+
 # ---------------------------------------------------------------- log probabilities
 def far_rows(r, n, vocab, t):
     """Rows of t at the ends of its range: all at its lowest value; all there but for masked ones; one
