@@ -518,7 +518,7 @@ def _need_rows(t, dtype, heads: int, dim: int, name: str) -> int:
 class KVCache:
     """An 8-bit paged cache: k and v [n_pages, n_heads, page_size, head_dim] of
     torch.float8_e4m3fn or torch.int8, k_scale and v_scale [n_pages, n_heads]
-    float32, status int32.  The buffers stay the caller's and the same ones."""
+    float32, status int32.  The buffers stay the caller's."""
     k: "object"
     v: "object"
     k_scale: "object"
@@ -526,6 +526,9 @@ class KVCache:
     status: "object"
 
     def __post_init__(self):
+        self._check()
+
+    def _check(self):
         torch = _torch or _setup()
         formats = {torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_INT8}
         if self.k.dtype not in formats or self.v.dtype != self.k.dtype:
@@ -533,7 +536,7 @@ class KVCache:
         if self.k.dim() != 4 or self.v.shape != self.k.shape:
             raise ValueError(f"k, v: shapes {tuple(self.k.shape)}, {tuple(self.v.shape)}")
         keep = dict(zip(("n_pages", "n_heads", "page_size", "head_dim"), self.k.shape), format=formats[self.k.dtype],
-                    _struct=None)
+                    _struct=None, _at=None)
         for t, name in ((self.k_scale, "k_scale"), (self.v_scale, "v_scale")):
             if t.dtype != torch.float32 or t.numel() < keep["n_pages"] * keep["n_heads"]:
                 raise ValueError(f"{name}: {t.numel()} elements of {t.dtype}, a cache needs [n_pages, n_heads] float32")
@@ -543,10 +546,18 @@ class KVCache:
             object.__setattr__(self, name, value)
 
     def struct(self):
-        if self._struct is None:
+        # looked at anew when a buffer has moved (set_, resize_): the storage is where it is now
+        at = (self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+              self.status.data_ptr())
+        if at != self._at:
+            pages = (self.n_heads, self.page_size, self.head_dim)
+            self._check()
+            if (self.n_heads, self.page_size, self.head_dim) != pages:
+                raise ValueError(f"k, v: pages of {tuple(self.k.shape[1:])}, the cache was made of pages of {pages}")
             object.__setattr__(self, "_struct", ctypes.pointer(twell_kv_t(
                 self.n_pages, self.page_size, self.n_heads, self.head_dim, self.format, 0, _ptr(self.k),
                 _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale), _ptr(self.status))))
+            object.__setattr__(self, "_at", at)
         return self._struct
 
 
@@ -563,8 +574,7 @@ def alloc_kv_cache(n_pages: int, page_size: int, n_heads: int, head_dim: int, fm
 @dataclass(frozen=True)
 class KVPlan:
     """What twell_kv_plan writes: kv_lens [R], cu_q [R + 1], slots [n_tokens]
-    int64, positions [n_tokens], pool [2] (for the next step's plan), status.
-    The buffers stay the same ones."""
+    int64, positions [n_tokens], pool [2] (for the next step's plan), status."""
     kv_lens: "object"
     cu_q: "object"
     slots: "object"
@@ -573,14 +583,17 @@ class KVPlan:
     status: "object"
 
     def _outputs(self) -> tuple:
-        """(requests, tokens, addresses in the call's order), checked once."""
+        """(requests, tokens, addresses in the call's order, status), checked when a buffer has moved."""
+        at = (self.kv_lens.data_ptr(), self.cu_q.data_ptr(), self.slots.data_ptr(), self.positions.data_ptr(),
+              self.pool.data_ptr(), self.status.data_ptr())
         kept = self.__dict__.get("_kept")
-        if kept is None:
+        if kept is None or kept[4] != at:
             i32, R, n = _torch.int32, self.kv_lens.numel(), self.slots.numel()
             kept = (R, n, (_arg(self.pool, i32, 2, "plan.pool"), _arg(self.kv_lens, i32, R, "plan.kv_lens"),
                            _arg(self.cu_q, i32, R + 1, "plan.cu_q"),
                            _arg(self.slots, _torch.int64, n, "plan.slots"),
-                           _arg(self.positions, i32, n, "plan.positions")), _arg(self.status, i32, 1, "plan.status"))
+                           _arg(self.positions, i32, n, "plan.positions")), _arg(self.status, i32, 1, "plan.status"),
+                    at)
             _on_device(self.pool, self.kv_lens, self.cu_q, self.slots, self.positions, self.status)
             object.__setattr__(self, "_kept", kept)
         return kept
@@ -616,7 +629,7 @@ def twell_kv_plan(kv_lens, new_tokens, block_table, ring, pool, page_size: int, 
     table, width = _table(block_table, R)
     ring_p, pool_p = _arg(ring, i32, 1, "ring"), _arg(pool, i32, 2, "pool")
     _on_device(kv_lens, new_tokens, block_table, ring, pool)
-    rows, n_tokens, out, status = plan._outputs()
+    rows, n_tokens, out, status, _ = plan._outputs()
     if rows != R:
         raise ValueError(f"plan: {rows} requests, kv_lens has {R}")
     rc = load_library().twell_kv_plan(lens_p, new_p, R, page_size, ring.numel(), width, table, ring_p,

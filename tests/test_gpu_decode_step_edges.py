@@ -345,3 +345,42 @@ def test_logprobs_gradient_at_the_ends_of_the_type(tw, n, vocab, dtype, inv_t, i
         assert (np.abs(got[i] - want) <= tol + ulp * rel * size).all(), (i, (np.abs(got[i] - want) / tol).max())
 
 
+# ---------------------------------------------------------------- buffers
+def test_buffers_that_moved_are_used_where_they_are(tw):
+    """A plan's or a cache's tensor that was given other storage after the first call: the next
+    call works on the new one, and checks it."""
+    import torch
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    plan = tw.alloc_kv_plan(2, 3)
+    ring, pool = tw.alloc_page_ring(4)
+    table = torch.zeros((2, 2), dtype=torch.int32, device="cuda")
+    args = (i32([0, 0]), i32([1, 2]), table, ring, pool, 16, plan)
+    tw.twell_kv_plan(*args)
+    old = plan.slots.clone(), plan.slots.view_as(plan.slots)   # the view keeps the old storage
+    plan.slots.set_(torch.full((3,), 77, dtype=torch.int64, device="cuda"))
+    old[1].fill_(-5)
+    tw.twell_kv_plan(*args)
+    assert torch.equal(plan.slots, old[0]) and (old[1] == -5).all()
+    plan.positions.set_(torch.zeros(2, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="positions"):
+        tw.twell_kv_plan(*args)
+
+    cache = tw.alloc_kv_cache(2, 16, 1, 64, tw.KV_INT8)
+    x = torch.ones((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    cu, slots = i32([0, 1]), torch.zeros(1, dtype=torch.int64, device="cuda")
+    tw.twell_kv_append(x, x, cu, slots, cache)
+    code = cache.k[0, 0, 0].clone()
+    before = cache.k.view_as(cache.k)
+    cache.k.set_(torch.zeros_like(cache.k))
+    before.fill_(3)
+    tw.twell_kv_append(x, x, cu, slots, cache)
+    assert torch.equal(cache.k[0, 0, 0], code) and (before == 3).all()
+    cache.v.set_(torch.zeros((1, 1, 16, 64), dtype=torch.int8, device="cuda"))
+    with pytest.raises(ValueError, match="k, v"):
+        tw.twell_kv_append(x, x, cu, slots, cache)
+    for t in (cache.k, cache.v):
+        t.set_(torch.zeros((2, 2, 16, 64), dtype=torch.int8, device="cuda"))
+    for t in (cache.k_scale, cache.v_scale):
+        t.set_(torch.zeros((2, 2), device="cuda"))
+    with pytest.raises(ValueError, match="k, v"):   # K and V have one head
+        tw.twell_kv_append(x, x, cu, slots, cache)
