@@ -664,6 +664,8 @@ def twell_kv_attention(Q, cache: KVCache, block_table, cu_q, positions, kv_lens,
     """O [n_tokens, n_q_heads, head_dim] bf16 = attention of Q over the cache;
     lse [n_tokens, n_q_heads] float32 when given."""
     torch = _torch or _setup()
+    if Q.dim() != 3:
+        raise ValueError(f"Q: shape {tuple(Q.shape)}, the call takes [tokens, heads, {cache.head_dim}]")
     n, heads = Q.shape[0], Q.shape[1]
     ldq = _need_rows(Q, torch.bfloat16, heads, cache.head_dim, "Q")
     ldo = _need_rows(O, torch.bfloat16, heads, cache.head_dim, "O")
@@ -712,6 +714,9 @@ def twell_logprobs(logits, targets, inv_temperature: float, logprob, entropy, ls
     if top_logprob is not None or top_index is not None:
         if top_logprob is None or top_index is None:
             raise ValueError("top_logprob, top_index: give both or neither")
+        if top_logprob.dim() != 2 or top_index.dim() != 2 or top_logprob.shape[1] != top_index.shape[1]:
+            raise ValueError(f"top_logprob, top_index: shapes {tuple(top_logprob.shape)}, {tuple(top_index.shape)}, the "
+                             f"call takes [{rows}, k] twice")
         k = top_logprob.shape[1]
         top = _arg(top_logprob, f32, rows * k, "top_logprob")
         index = _arg(top_index, i32, rows * k, "top_index")

@@ -384,3 +384,20 @@ def test_buffers_that_moved_are_used_where_they_are(tw):
         t.set_(torch.zeros((2, 2), device="cuda"))
     with pytest.raises(ValueError, match="k, v"):   # K and V have one head
         tw.twell_kv_append(x, x, cu, slots, cache)
+
+
+def test_alternatives_and_queries_of_the_wrong_shape_are_refused(tw):
+    """The k best go to two [rows, k] matrices of the same k; queries have three dimensions."""
+    import torch
+    x = torch.zeros((4, 100), device="cuda")
+    lse = torch.empty(4, device="cuda")
+    f = lambda *s: torch.empty(s, device="cuda")  # noqa: E731
+    i = lambda *s: torch.empty(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    for top, index in ((f(4, 5), i(4, 6)), (f(4, 5), i(20)), (f(20), i(4, 5)), (f(3, 5), i(3, 5))):
+        with pytest.raises(ValueError, match="top_logprob"):
+            tw.twell_logprobs(x, None, 1.0, None, None, lse, top, index)
+    cache = tw.alloc_kv_cache(1, 16, 1, 64)
+    i32 = i(2)
+    for q in (torch.empty(64, device="cuda"), torch.empty((1, 64), device="cuda")):
+        with pytest.raises(ValueError, match="^Q: shape"):
+            tw.twell_kv_attention(q.bfloat16(), cache, i(1, 1), i32, i32, i(1), 1, 1, 0.1, q.bfloat16(), f(256))
