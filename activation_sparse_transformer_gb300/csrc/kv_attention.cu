@@ -25,10 +25,13 @@
 // dims come out in runs.  No transposition lies between the cache and the mma;
 // P's 8 x 8 blocks are turned by movmatrix.
 //
+// Below, W is a CTA's warps: 4, or 8 where a segment has an SM to itself.
+//
 // Each cached byte is read once, so HBM bounds long caches: 4 x 65536 to 131072 tokens, 8 key heads of 128, e4m3:
-// 130 us, 5.9 TB/s.  Heads with one query row each and 64 dims are bound by the
-// instructions of a step, 475 for 32 tokens, a third of them conversions: 250 ragged requests, int8, 136 us, 4.2 TB/s.
-// Short caches are bound by the latencies in a row (lengths, table, codes, softmax): 16 x 1000 tokens 10.3 us.
+// 133 us, 5.8 TB/s.  Heads with one query row each and 64 dims are bound by the chain of
+// dependent instructions of a warp's step (480 for 32 tokens, a third of them conversions; 54 % of the issue slots busy,
+// the largest stall their fixed latency): 250 ragged requests, int8, 137 us, 4.2 TB/s.
+// Short caches are bound by the latencies in a row (lengths, table, codes, softmax): 16 x 1000 tokens 10.5 us.
 #include <algorithm>
 #include <cfloat>
 
@@ -302,7 +305,7 @@ __device__ __forceinline__ void zero_row(const AttArgs& a, int64_t t, int tid, i
 
 // ------------------------------------------------------------ work split
 // A segment is one row block of one key head with all its cached tokens, in
-// units of 128 of them.  The segments of all requests, laid end to end, are
+// units of a step of each warp (32 W of them).  The segments of all requests, laid end to end, are
 // cut into as many equal pieces as CTAs run, so the lengths of the requests do
 // not matter for the balance; every CTA sums up the requests itself (a few loads a
 // thread) rather than wait for another kernel.  A piece's cut segments leave partial
@@ -310,7 +313,7 @@ __device__ __forceinline__ void zero_row(const AttArgs& a, int64_t t, int tid, i
 // the one it ends in the middle of), which join_kernel adds in order.  (Adding them in the CTA
 // that finishes last costs more: one CTA's loads have to bring in all parts.)  Short
 // segments are not cut, see launch_attention.
-constexpr int kUnit = kAttStep * kAttWarps;  // cached tokens of a unit: a step of each warp
+constexpr int kUnit = kAttStep * kAttWarps;  // cached tokens of a unit with 4 warps: a step of each
 constexpr int kMaxCtas = 608;
 constexpr int kMaxSmem = 224 * 1024;  // dynamic, of a CTA
 // Segments of up to this many units are never cut: their join would cost more
@@ -816,7 +819,8 @@ int launch_attention(const AttArgs& a, int max_kv_len, int max_q_len, void* work
   // 49 and 50; 32 segments of 1500: 12.8 and 13.1, of 4000 24.1 and 18.1; 8 of 4000: 23.8 and 10.6).
   // More segments than SMs: whole ones are better up to 16 units (256 segments of 1500 tokens 26.0, cut 30.1;
   // of 2500 38.3 and 36.7), and up to 32 where there are so many that they even out
-  // (8000 of up to 4001 143 and 146); beyond, one long segment among short ones would be all a CTA's work.
+  // (8000 of up to 4001, 32 units, 143 and 146: little, and the one size that was measured); beyond, one long segment
+  // among short ones would be all a CTA's work.  All but 16 x 1000 and 16 x 4000 measured with blocks of 8 rows.
   const int64_t segments = a.n_requests * a.heads * std::max<int64_t>(1, blocks);
   const int64_t sms = sm_count();
   const int split = segments <= sms ? 2 * units <= std::max<int64_t>(8, segments) ? kEach : kCut

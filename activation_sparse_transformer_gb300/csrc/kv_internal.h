@@ -47,8 +47,6 @@ inline int check_rows(const void* p, int64_t ld, int heads, int dim) {
   return ld >= static_cast<int64_t>(heads) * dim && ld % 8 == 0 ? TWELL_OK : TWELL_ERR_INVALID_ARG;
 }
 
-inline int launched() { return cudaGetLastError() == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA; }
-
 // The largest i in [0, n) with f(i) <= x, for a non-decreasing f with f(0) <=
 // x, found by a whole warp: 32 probes a round, so that a table of 1024 costs
 // two dependent loads instead of ten.

@@ -12,7 +12,7 @@
 // to be corrected; slices are joined through distributed shared memory.  HBM
 // bounds many rows, with the instructions of an element next (5 of them, two
 // elements an instruction where there is one); few rows are bound by the latency of one slice.
-// 8192 x 32768 bf16: 82 us, its gradient 164 (6.6 TB/s both); with 5 alternatives 153; 16 x 131072 fp32 with 20: 9 us.
+// 8192 x 32768 bf16: 83 us, its gradient 164 (6.5 TB/s both); with 5 alternatives 154; 16 x 131072 fp32 with 20: 9.2 us.
 //
 // The k largest: the k-th largest of 64 groups' own maxima is a lower bound of
 // the k-th largest value, and hardly more than k values reach it.  Those are
@@ -536,9 +536,9 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(const LogprobsArgs a) {
 // to be kept.  NT threads take a row, each with a maximum of its own that follows what it
 // reads, kBatch 16-byte loads at a time; their sums are brought to the row's maximum at the end.
 // The next rows' loads run under a row's sums, where a staged row's CTA waits for all of its
-// copies first: 8192 x 32768 bf16 81.8 us (6.6 TB/s), staged 101; fp32 147 (7.3 TB/s), staged 212.
+// copies first: 8192 x 32768 bf16 83.0 us (6.5 TB/s), staged 101; fp32 149 (7.2 TB/s), staged 212.
 constexpr int kRowsThreads = 256, kBatch = 4;
-// From 2 rows an SM on (320 x 131072 fp32: 34 us, staged in clusters 40).
+// From 2 rows an SM on (320 x 131072 fp32: 33 us, staged in clusters 40).
 constexpr int kManyRows = 2;
 // (Six CTAs an SM where one takes a row: far_stat's registers alone would leave five, 85.9 us.)
 template <typename T, int NT>

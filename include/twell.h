@@ -358,7 +358,8 @@ enum {
  * page and head (a value likewise); twell_kv_append writes powers of two as
  * scales, the attention takes any positive finite ones (value scales of one
  * request within 2^100 of each other).  The struct lives in
- * host memory; the pointers are device pointers to caller-owned memory. */
+ * host memory; the pointers are device pointers to caller-owned memory.
+ * (Positive finite: normal numbers, from 2^-126 on.) */
 typedef struct twell_kv_t {
   int32_t n_pages;    /* >= 1 */
   int32_t page_size;  /* tokens per page: 16, 32, 64 or 128 */
@@ -433,7 +434,9 @@ TWELL_API int twell_kv_append(const uint16_t* K, int64_t ldk, const uint16_t* V,
  *   L = min(positions[t] + 1, kv_lens[r], max_blocks * page_size)
  *   x_j = softmax_scale * (q . k_j),  o = sum_j softmax(x)_j v_j,  lse = log sum_j exp(x_j)
  * A row that sees nothing (L <= 0: an empty request, a refused one, a token past
- * cu_q[n_requests]) has o = 0 and lse = -inf.
+ * cu_q[n_requests]) has o = 0 and lse = -inf.  What a row does not see, positions from L on, may hold
+ * any codes and its pages any scales.  A row that sees a NaN code (e4m3; twell_kv_append writes
+ * none) is NaN, in that dim at least.
  *   Q, O   token t's head h at Q + t * ldq + h * head_dim (bf16), ldq and ldo as ldk
  *          above; lse [n_tokens][n_q_heads] fp32 or null
  *   n_q_heads  a multiple of cache->n_heads
@@ -442,7 +445,8 @@ TWELL_API int twell_kv_append(const uint16_t* K, int64_t ldk, const uint16_t* V,
  *          when a bound is exceeded.
  * The cache's codes enter the tensor cores exactly (as fp16, which holds every
  * e4m3 and int8 value); q enters as fp16 scaled by a power of two per row
- * (exact for components above 2^-13 of the row's largest); probabilities are rounded to fp16,
+ * (exact for components above 2^-13 of the row's largest); probabilities times their value scales are
+ * rounded to fp16: to 2^-11 of themselves, below 2^-21 of a row's largest to 2^-32 of that one;
  * every sum and the softmax's statistics are fp32.  Long caches are split
  * over the GPU and joined in a fixed order: the same call gives the same bits.
  * workspace: device, >= twell_kv_attention_workspace_bytes(...) bytes (10 MB; 93 MB
