@@ -50,7 +50,8 @@ KERNELS = {
     "up_pack": 0, "route": 1, "fb_assemble": 2, "spmm": 4, "fb_down": 5, "pack": 6,
     "check_format": 3, "unpack": 7, "sddmm": 8, "dx": 9, "dw": 10, "dense_gemm": 11, "aux": 12,
     "dw_fallback": 13, "dx_fallback": 14, "kv_plan": 15, "kv_append": 16, "kv_attention": 17,
-    "kv_join": 18, "logprobs": 19, "logprobs_bwd": 20,
+    "kv_join": 18, "logprobs": 19, "logprobs_bwd": 20, "block_norm": 21, "block_norm_bwd": 22,
+    "linear_logprobs": 23, "linear_logprobs_bwd": 24,
 }
 EXPORTED = [
     "twell_pack", "twell_unpack", "twell_ffn_fwd", "twell_fwd_workspace_bytes", "twell_ffn_bwd",
@@ -63,6 +64,7 @@ EXPORTED = [
     "twell_gated_bwd_workspace_bytes", "twell_gated_bwd_tiles_workspace_bytes",
     "twell_kv_plan", "twell_kv_append", "twell_kv_attention", "twell_kv_attention_workspace_bytes",
     "twell_kv_read_status", "twell_logprobs", "twell_logprobs_bwd", "twell_selftest_kv_attention_stall",
+    "twell_block_norm", "twell_block_norm_bwd", "twell_block_norm_bwd_workspace_bytes",
 ]
 
 
@@ -145,6 +147,12 @@ def load_library() -> ctypes.CDLL:
         "twell_kv_read_status": (ctypes.c_int, [KV, P]),
         "twell_logprobs": (ctypes.c_int, [P, I32, I64, I32, I32, P, ctypes.c_float, P, P, P, I32, P, P, P]),
         "twell_logprobs_bwd": (ctypes.c_int, [P, I32, I64, I32, I32, P, ctypes.c_float, P, P, P, P, P, I64, P]),
+        "twell_block_norm": (ctypes.c_int, [P, I32, I64, P, I64, I32, I32, P, P, P, I32, P] + [ctypes.c_float] * 3 +
+                             [P, I64, P, I64, P, P, P]),
+        "twell_block_norm_bwd": (ctypes.c_int, [P, I64, P, I32, I64, P, I64, P, I64, I32, I32, P, P, P, I32, P,
+                                                ctypes.c_float, ctypes.c_float, P, P, P, I64, P, I64, P, P, P, P, P,
+                                                SZ, P]),
+        "twell_block_norm_bwd_workspace_bytes": (SZ, [I32, I32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -746,3 +754,107 @@ def twell_logprobs_bwd(logits, targets, inv_temperature: float, lse, entropy, d_
         _maybe(d_entropy, f32, rows, "d_entropy"), d_logits.data_ptr(), ldd, _on(stream))
     if rc:
         _check(rc, "twell_logprobs_bwd")
+
+
+# ---------------------------------------------------------------- a training step around the layer
+def _matrix(t, dtypes, rows, dim, name: str) -> tuple:
+    """(address, distance between rows) of a device matrix [rows, dim] whose rows are contiguous
+    (rows, dim None: any); (None, 0) of None."""
+    if t is None:
+        return None, 0
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: {t.dtype}, the call takes {' or '.join(str(d) for d in dtypes)}")
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and (shape[0] != rows or shape[1] != dim)):
+        raise ValueError(f"{name}: shape {tuple(shape)}, the call takes [{'rows' if rows is None else rows}, "
+                         f"{'columns' if dim is None else dim}]")
+    stride = t.stride()
+    if stride[1] != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: a tensor whose rows are contiguous")
+    # a matrix of one row may have any stride
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else (shape[1] + 7) // 8 * 8)
+
+
+def _vectors(dim: int, **given) -> tuple:
+    """(type code, addresses) of the norm's weights: all bfloat16 or all float32."""
+    torch, dtype, out = _torch, None, []
+    for name, t in given.items():
+        if t is not None:
+            if t.dtype not in (torch.bfloat16, torch.float32):
+                raise ValueError(f"{name}: {t.dtype}, the call takes bfloat16 or float32")
+            if dtype is not None and t.dtype != dtype:
+                raise ValueError(f"{name}: {t.dtype}, the other weights are {dtype}")
+            dtype = t.dtype
+            if t.numel() != dim:
+                raise ValueError(f"{name}: {t.numel()} elements, the rows have {dim}")
+            out.append(_arg(t, dtype, dim, name))
+        else:
+            out.append(None)
+    return (1 if dtype == torch.float32 else 0), out
+
+
+def twell_block_norm(x, y, x_out=None, h=None, *, w_post=None, gate=None, w_pre=None, row_gate=None,
+                     skip_scale: float = 1.0, branch_scale: float = 1.0, eps: float = 1e-6, rstd_post=None,
+                     rstd_pre=None, stream=None) -> None:
+    """x_out [rows, d] (type of x; may be x itself) = skip_scale x + branch_scale row_gate gate u with u the
+    block's output y (bf16), normed if w_post is given; h (bf16) = the norm of x_out with w_pre.  y None: no block."""
+    torch = _torch or _setup()
+    bf = (torch.bfloat16,)
+    streams = (torch.bfloat16, torch.float32)
+    x_p, ldx = _matrix(x, streams, None, None, "x")
+    rows, dim = x.shape
+    y_p, ldy = _matrix(y, bf, rows, dim, "y")
+    o_p, ldo = _matrix(x_out, (x.dtype,), rows, dim, "x_out")
+    h_p, ldh = _matrix(h, bf, rows, dim, "h")
+    code, (post, gate_p, pre) = _vectors(dim, w_post=w_post, gate=gate, w_pre=w_pre)
+    per_row = [_maybe(t, torch.float32, rows, name) for t, name in ((row_gate, "row_gate"), (rstd_post, "rstd_post"),
+                                                                    (rstd_pre, "rstd_pre"))]
+    _on_device(x, y, x_out, h, w_post, gate, w_pre, row_gate, rstd_post, rstd_pre)
+    rc = load_library().twell_block_norm(x_p, 0 if x.dtype == torch.bfloat16 else 1, ldx, y_p, ldy, rows, dim, post,
+                                         gate_p, pre, code, per_row[0], skip_scale, branch_scale, eps, o_p, ldo, h_p,
+                                         ldh, per_row[1], per_row[2], _on(stream))
+    if rc:
+        _check(rc, "twell_block_norm")
+
+
+def block_norm_bwd_workspace_bytes(n_rows, d_model) -> int:
+    return int(load_library().twell_block_norm_bwd_workspace_bytes(n_rows, d_model))
+
+
+def twell_block_norm_bwd(dh, d_out, x_out, y, dx=None, dy=None, *, w_post=None, gate=None, w_pre=None, row_gate=None,
+                         skip_scale: float = 1.0, branch_scale: float = 1.0, rstd_post=None, rstd_pre=None,
+                         dw_post=None, dgate=None, dw_pre=None, drow_gate=None, workspace=None, stream=None) -> None:
+    """Gradients of twell_block_norm from those of h (dh, bf16) and x_out (d_out, its type): dx (may be
+    d_out itself), dy (bf16), and fp32 sums dw_post, dgate, dw_pre [d], drow_gate [rows]; None: not wanted."""
+    torch = _torch or _setup()
+    bf, streams = (torch.bfloat16,), (torch.bfloat16, torch.float32)
+    like = next((t for t in (d_out, x_out, dx) if t is not None), None)
+    if like is None:
+        raise ValueError("d_out, x_out, dx: give one at least")
+    _matrix(like, streams, None, None, "d_out, x_out, dx")
+    (rows, dim), own = like.shape, (like.dtype,)
+    dh_p, lddh = _matrix(dh, bf, rows, dim, "dh")
+    do_p, lddo = _matrix(d_out, own, rows, dim, "d_out")
+    o_p, ldo = _matrix(x_out, own, rows, dim, "x_out")
+    y_p, ldy = _matrix(y, bf, rows, dim, "y")
+    dx_p, lddx = _matrix(dx, own, rows, dim, "dx")
+    dy_p, lddy = _matrix(dy, bf, rows, dim, "dy")
+    code, (post, gate_p, pre) = _vectors(dim, w_post=w_post, gate=gate, w_pre=w_pre)
+    f32 = torch.float32
+    row_p, rstd1, rstd2, drow = (_maybe(t, f32, rows, name) for t, name in (
+        (row_gate, "row_gate"), (rstd_post, "rstd_post"), (rstd_pre, "rstd_pre"), (drow_gate, "drow_gate")))
+    dwo, dg, dwi = (_maybe(t, f32, dim, name) for t, name in ((dw_post, "dw_post"), (dgate, "dgate"),
+                                                              (dw_pre, "dw_pre")))
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous tensor")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _on_device(dh, d_out, x_out, y, dx, dy, w_post, gate, w_pre, row_gate, rstd_post, rstd_pre, dw_post, dgate, dw_pre,
+               drow_gate, workspace)
+    rc = load_library().twell_block_norm_bwd(dh_p, lddh, do_p, 0 if like.dtype == torch.bfloat16 else 1, lddo, o_p, ldo,
+                                             y_p, ldy, rows, dim, post, gate_p, pre, code, row_p, skip_scale,
+                                             branch_scale, rstd1, rstd2, dx_p, lddx, dy_p, lddy, dwo, dg, dwi, drow, ws,
+                                             ws_bytes, _on(stream))
+    if rc:
+        _check(rc, "twell_block_norm_bwd")

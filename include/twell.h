@@ -502,6 +502,56 @@ TWELL_API int twell_logprobs_bwd(const void* logits, int32_t dtype, int64_t ld, 
                                  const float* entropy, const float* d_logprob, const float* d_entropy,
                                  void* d_logits, int64_t ldd, twell_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A training step around the layer: the norms before and after a block with
+ * its gate and the residual sum (twell_block_norm), the log probabilities of
+ * tokens from hidden rows and output weights without the logits in memory
+ * (twell_linear_logprobs), and their gradients.  The same calls serve single tokens.
+ * Row matrices: ld elements between rows, ld >= the row's length and a multiple of 8, base
+ * 16-byte aligned; what is written overlaps nothing that is read, except where a call says so.
+ *
+ * The residual stream z that a block leaves and the next block's input h:
+ *   u = y rstd_post w_post,  rstd_post = (mean of y^2 + eps)^-1/2   (w_post null: u = y)
+ *   z = skip_scale x + branch_scale row_gate[n] gate u      (gate, row_gate null: 1)
+ *   h = z rstd_pre w_pre,    rstd_pre = (mean of z^2 + eps)^-1/2
+ *   x       [n_rows][d_model] of type dtype (TWELL_BF16 or TWELL_F32): the stream before the block
+ *   y       [n_rows][d_model] bf16: the block's output; null (with w_post, gate and row_gate): z = skip_scale x
+ *   w_post, gate, w_pre  [d_model] of type w_dtype, 16-byte aligned, each may be null
+ *   row_gate  [n_rows] fp32 or null
+ *   x_out   z in type dtype, or null; it may be x itself (with ldo == ldx)
+ *   h       bf16, of z before its rounding; given exactly when w_pre is
+ *   rstd_post, rstd_pre  [n_rows] fp32 for the backward, or null
+ * d_model a multiple of 8, at most 16384; eps > 0.  Squares are summed in fp32: magnitudes up to 1e17.
+ * One launch. */
+TWELL_API int twell_block_norm(const void* x, int32_t dtype, int64_t ldx, const uint16_t* y, int64_t ldy,
+                               int32_t n_rows, int32_t d_model, const void* w_post, const void* gate,
+                               const void* w_pre, int32_t w_dtype, const float* row_gate, float skip_scale,
+                               float branch_scale, float eps, void* x_out, int64_t ldo, uint16_t* h, int64_t ldh,
+                               float* rstd_post, float* rstd_pre, twell_stream_t stream);
+
+/* Gradient of twell_block_norm, from what that call took and left:
+ *   dh     [n_rows][d_model] bf16, gradient of h (with w_pre and rstd_pre, or null with both)
+ *   d_out  [n_rows][d_model] of type dtype, gradient of x_out from what reads it further on, or null
+ *   x_out  the forward's, needed with dh
+ *   dx     type dtype, or null; it may be d_out itself (with lddx == lddo)
+ *   dy     bf16, or null
+ *   dw_post, dgate, dw_pre  [d_model] fp32 sums over the rows, drow_gate [n_rows] fp32; each may be null
+ * With v = x_out rstd_pre, a = dh w_pre, s = y rstd_post (or y):
+ *   dz = d_out + rstd_pre (a - v mean(a v)),  dx = skip_scale dz,  dw_pre = sum_n dh v
+ *   t = branch_scale row_gate gate w_post dz,  dy = rstd_post (t - s mean(t s))  (w_post null: dy = t)
+ * and the branch's weights by the product rule.  The sums over rows are made in a fixed order: equal
+ * calls give equal bits.  With n_rows == 0 the vectors' gradients are set to zero.
+ * workspace: >= twell_block_norm_bwd_workspace_bytes(...), 256-byte aligned, needed with dw_post, dgate or dw_pre. */
+TWELL_API int twell_block_norm_bwd(const uint16_t* dh, int64_t lddh, const void* d_out, int32_t dtype, int64_t lddo,
+                                   const void* x_out, int64_t ldo, const uint16_t* y, int64_t ldy, int32_t n_rows,
+                                   int32_t d_model, const void* w_post, const void* gate, const void* w_pre,
+                                   int32_t w_dtype, const float* row_gate, float skip_scale, float branch_scale,
+                                   const float* rstd_post, const float* rstd_pre, void* dx, int64_t lddx,
+                                   uint16_t* dy, int64_t lddy, float* dw_post, float* dgate, float* dw_pre,
+                                   float* drow_gate, void* workspace, size_t workspace_bytes, twell_stream_t stream);
+
+TWELL_API size_t twell_block_norm_bwd_workspace_bytes(int32_t n_rows, int32_t d_model);
+
 /* Synchronises `stream`, then returns *layout->status if non-zero, else
  * TWELL_ERR_FALLBACK_OVERFLOW when *layout->n_fb exceeds the capacity (fb_cap
  * rows, or fb_cap * d_ff / tile dense tiles for the tile-granular variant),
@@ -587,7 +637,11 @@ enum {
   TWELL_KERNEL_KV_JOIN = 18,     /* join of the cut caches' partial results */
   TWELL_KERNEL_LOGPROBS = 19,    /* log probabilities, entropy, best alternatives */
   TWELL_KERNEL_LOGPROBS_BWD = 20, /* their gradient */
-  TWELL_KERNEL_COUNT = 21
+  TWELL_KERNEL_BLOCK_NORM = 21,  /* norms before and after a block, gate, residual sum */
+  TWELL_KERNEL_BLOCK_NORM_BWD = 22, /* their gradient */
+  TWELL_KERNEL_LINEAR_LOGPROBS = 23, /* log probabilities from hidden rows and output weights */
+  TWELL_KERNEL_LINEAR_LOGPROBS_BWD = 24, /* their gradient */
+  TWELL_KERNEL_COUNT = 25
 };
 TWELL_API int twell_profile_enable(int on);
 TWELL_API int twell_profile_reset(void);

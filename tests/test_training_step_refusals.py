@@ -1,0 +1,101 @@
+"""The training step's calls refuse bad arguments on the host, before any launch: the C ABI by its
+codes (aligned fake pointers, never dereferenced), the binding by type, shape, stride and size."""
+import ctypes
+
+import pytest
+
+P = ctypes.c_void_p
+A, B, C, D, E, F = (P(0x10000 * i) for i in range(1, 7))
+
+
+@pytest.fixture(scope="module")
+def tw():
+    import __graft_entry__ as g
+    g.build()
+    import activation_sparse_transformer_gb300 as m
+    return m
+
+
+@pytest.fixture(scope="module")
+def lib(tw):
+    return tw.load_library()
+
+
+NORM = dict(x=A, dtype=0, ldx=256, y=B, ldy=256, n=5, d=256, w_post=A, gate=A, w_pre=A, w_dtype=0, row_gate=A, skip=1.0,
+            branch=1.0, eps=1e-6, x_out=C, ldo=256, h=D, ldh=256, rstd_post=A, rstd_pre=A, stream=None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(x=None), -1), (dict(n=-1), -1), (dict(d=0), -1), (dict(d=-8), -1), (dict(dtype=2), -1), (dict(dtype=-1), -1),
+    (dict(w_dtype=2), -1), (dict(eps=0.0), -1), (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1),
+    (dict(eps=float("inf")), -1), (dict(skip=float("nan")), -1), (dict(branch=float("inf")), -1),
+    (dict(y=None), -1), (dict(y=None, w_post=None, gate=None, rstd_post=None), -1),     # a gate without a block
+    (dict(h=None), -1), (dict(w_pre=None), -1), (dict(w_pre=None, h=None), -1),         # rstd_pre without a norm
+    (dict(w_post=None), -1), (dict(x_out=None, h=None, w_pre=None, rstd_pre=None), -1),
+    (dict(ldx=248), -1), (dict(ldy=260), -1), (dict(ldo=255), -1), (dict(ldh=0), -1),
+    (dict(x_out=A, ldo=264), -1),                                                     # in place with another distance
+    (dict(d=260, ldx=264, ldy=264, ldo=264, ldh=264), -3),
+    (dict(d=16392, ldx=16392, ldy=16392, ldo=16392, ldh=16392), -3),
+    (dict(x=P(0x10008)), -2), (dict(y=P(0x10008)), -2), (dict(h=P(0x10004)), -2), (dict(gate=P(0x10002)), -2),
+    (dict(row_gate=P(0x10002)), -2), (dict(rstd_pre=P(0x10001)), -2)])
+def test_block_norm_refuses(lib, over, code):
+    assert lib.twell_block_norm(*{**NORM, **over}.values()) == code
+
+
+BWD = dict(dh=A, lddh=256, d_out=B, dtype=0, lddo=256, x_out=C, ldo=256, y=D, ldy=256, n=5, d=256, w_post=A, gate=A,
+           w_pre=A, w_dtype=0, row_gate=A, skip=1.0, branch=1.0, rstd_post=A, rstd_pre=A, dx=E, lddx=256, dy=F,
+           lddy=256, dw_post=A, dgate=A, dw_pre=A, drow_gate=A, ws=A, ws_bytes=1 << 40, stream=None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(dh=None), -1), (dict(w_pre=None), -1), (dict(rstd_pre=None), -1), (dict(x_out=None), -1),
+    (dict(dh=None, w_pre=None, rstd_pre=None), -1),                                   # dw_pre without a norm
+    (dict(dh=None, w_pre=None, rstd_pre=None, dw_pre=None, d_out=None), -1),
+    (dict(w_post=None), -1), (dict(rstd_post=None), -1), (dict(gate=None), -1), (dict(row_gate=None), -1),
+    (dict(y=None), -1), (dict(n=-1), -1), (dict(d=0), -1), (dict(dtype=5), -1), (dict(w_dtype=-1), -1),
+    (dict(skip=float("inf")), -1), (dict(branch=float("nan")), -1), (dict(lddh=248), -1), (dict(lddx=250), -1),
+    (dict(dx=B, lddx=264), -1), (dict(d=100, lddh=104), -3), (dict(dh=P(0x10008)), -2), (dict(dy=P(0x10008)), -2),
+    (dict(dw_pre=P(0x10002)), -2), (dict(w_post=P(0x10008)), -2), (dict(ws=None), -5), (dict(ws_bytes=100), -5),
+    (dict(ws=P(0x10010)), -2)])
+def test_block_norm_bwd_refuses(lib, over, code):
+    assert lib.twell_block_norm_bwd(*{**BWD, **over}.values()) == code
+
+
+def test_block_norm_workspace_is_host_arithmetic(tw):
+    assert tw.block_norm_bwd_workspace_bytes(100, 256) > 0
+    for bad in ((-1, 256), (10, 0), (10, 12), (10, 16392)):
+        assert tw.block_norm_bwd_workspace_bytes(*bad) == 0
+
+
+def test_binding_of_the_norms_checks(tw):
+    """CPU tensors: everything else is refused before they are."""
+    import torch
+    bf = torch.bfloat16
+    x, w = torch.zeros((4, 64), dtype=bf), torch.ones(64, dtype=bf)
+    with pytest.raises(ValueError, match="^x: torch.float16"):
+        tw.twell_block_norm(x.half(), x, x)
+    with pytest.raises(ValueError, match="^y: torch.float32"):
+        tw.twell_block_norm(x, x.float(), x)
+    with pytest.raises(ValueError, match="^y: shape"):
+        tw.twell_block_norm(x, x[:3], x)
+    with pytest.raises(ValueError, match="^x_out: torch.float32"):
+        tw.twell_block_norm(x, x, x.float())
+    with pytest.raises(ValueError, match="^h: a tensor whose rows"):
+        tw.twell_block_norm(x, x, x, torch.zeros((64, 4), dtype=bf).t(), w_pre=w)
+    with pytest.raises(ValueError, match="^w_pre: 63"):
+        tw.twell_block_norm(x, x, x, x, w_pre=w[:63])
+    with pytest.raises(ValueError, match="^w_pre: torch.float32, the other"):
+        tw.twell_block_norm(x, x, x, x, w_post=w, w_pre=w.float())
+    with pytest.raises(ValueError, match="^row_gate: 3"):
+        tw.twell_block_norm(x, x, x, row_gate=torch.zeros(3))
+    with pytest.raises(ValueError, match="CUDA"):
+        tw.twell_block_norm(x, x, x)
+    r = torch.zeros(4)
+    with pytest.raises(ValueError, match="^d_out, x_out, dx"):
+        tw.twell_block_norm_bwd(x, None, None, x)
+    with pytest.raises(ValueError, match="^dx: torch.float32"):
+        tw.twell_block_norm_bwd(x, x, x, x, x.float(), x, w_pre=w, rstd_pre=r)
+    with pytest.raises(ValueError, match="^dw_pre: torch.bfloat16"):
+        tw.twell_block_norm_bwd(x, x, x, x, x, x, w_pre=w, rstd_pre=r, dw_pre=w)
+    with pytest.raises(ValueError, match="CUDA"):
+        tw.twell_block_norm_bwd(x, x, x, x, x, x, w_pre=w, rstd_pre=r)
