@@ -65,6 +65,8 @@ EXPORTED = [
     "twell_kv_plan", "twell_kv_append", "twell_kv_attention", "twell_kv_attention_workspace_bytes",
     "twell_kv_read_status", "twell_logprobs", "twell_logprobs_bwd", "twell_selftest_kv_attention_stall",
     "twell_block_norm", "twell_block_norm_bwd", "twell_block_norm_bwd_workspace_bytes",
+    "twell_linear_logprobs", "twell_linear_logprobs_workspace_bytes", "twell_linear_logprobs_bwd",
+    "twell_linear_logprobs_bwd_workspace_bytes",
 ]
 
 
@@ -153,6 +155,12 @@ def load_library() -> ctypes.CDLL:
                                                 ctypes.c_float, ctypes.c_float, P, P, P, I64, P, I64, P, P, P, P, P,
                                                 SZ, P]),
         "twell_block_norm_bwd_workspace_bytes": (SZ, [I32, I32]),
+        "twell_linear_logprobs": (ctypes.c_int, [P, I64, P, I64, I32, I32, I32, P, ctypes.c_float, P, P, P, P, SZ, P,
+                                                 P]),
+        "twell_linear_logprobs_workspace_bytes": (SZ, [I32, I32, I32]),
+        "twell_linear_logprobs_bwd": (ctypes.c_int, [P, I64, P, I64, I32, I32, I32, P, ctypes.c_float, P, P, P, P, P,
+                                                     I64, P, I64, P, SZ, P, P]),
+        "twell_linear_logprobs_bwd_workspace_bytes": (SZ, [I32, I32, I32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -845,11 +853,7 @@ def twell_block_norm_bwd(dh, d_out, x_out, y, dx=None, dy=None, *, w_post=None, 
         (row_gate, "row_gate"), (rstd_post, "rstd_post"), (rstd_pre, "rstd_pre"), (drow_gate, "drow_gate")))
     dwo, dg, dwi = (_maybe(t, f32, dim, name) for t, name in ((dw_post, "dw_post"), (dgate, "dgate"),
                                                               (dw_pre, "dw_pre")))
-    ws, ws_bytes = None, 0
-    if workspace is not None:
-        if not workspace.is_contiguous():
-            raise ValueError("workspace: a contiguous tensor")
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    ws, ws_bytes = (None, 0) if workspace is None else _workspace(workspace)
     _on_device(dh, d_out, x_out, y, dx, dy, w_post, gate, w_pre, row_gate, rstd_post, rstd_pre, dw_post, dgate, dw_pre,
                drow_gate, workspace)
     rc = load_library().twell_block_norm_bwd(dh_p, lddh, do_p, 0 if like.dtype == torch.bfloat16 else 1, lddo, o_p, ldo,
@@ -858,3 +862,66 @@ def twell_block_norm_bwd(dh, d_out, x_out, y, dx=None, dy=None, *, w_post=None, 
                                              ws_bytes, _on(stream))
     if rc:
         _check(rc, "twell_block_norm_bwd")
+
+
+def linear_logprobs_workspace_bytes(n_rows, d_model, vocab) -> int:
+    return int(load_library().twell_linear_logprobs_workspace_bytes(n_rows, d_model, vocab))
+
+
+def linear_logprobs_bwd_workspace_bytes(n_rows, d_model, vocab) -> int:
+    return int(load_library().twell_linear_logprobs_bwd_workspace_bytes(n_rows, d_model, vocab))
+
+
+def _workspace(t) -> tuple:
+    if not t.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _linear(hidden, weight) -> tuple:
+    """(rows, d, vocab, address and distance of hidden, of weight)"""
+    bf = (_torch.bfloat16,)
+    h_p, ldh = _matrix(hidden, bf, None, None, "hidden")
+    rows, dim = hidden.shape
+    w_p, ldw = _matrix(weight, bf, None, None, "weight")
+    if weight.shape[1] != dim:
+        raise ValueError(f"weight: rows of {weight.shape[1]}, hidden has rows of {dim}")
+    return rows, dim, weight.shape[0], h_p, ldh, w_p, ldw
+
+
+def twell_linear_logprobs(hidden, weight, targets, inv_temperature: float, logprob, entropy, lse, workspace, status,
+                          stream=None) -> None:
+    """logprob, entropy, lse [rows] float32 (None: not wanted; targets and logprob together) of the logits
+    inv_temperature * hidden weight^T, hidden [rows, d] and weight [vocab, d] bf16, which are not stored."""
+    torch = _torch or _setup()
+    f32, i32 = torch.float32, torch.int32
+    rows, dim, vocab, h_p, ldh, w_p, ldw = _linear(hidden, weight)
+    outs = [_maybe(t, f32, rows, name) for t, name in ((logprob, "logprob"), (entropy, "entropy"), (lse, "lse"))]
+    t_p, st = _maybe(targets, i32, rows, "targets"), _arg(status, i32, 1, "status")
+    ws, ws_bytes = _workspace(workspace)
+    _on_device(hidden, weight, targets, logprob, entropy, lse, workspace, status)
+    rc = load_library().twell_linear_logprobs(h_p, ldh, w_p, ldw, rows, dim, vocab, t_p, inv_temperature, *outs, ws,
+                                              ws_bytes, st, _on(stream))
+    if rc:
+        _check(rc, "twell_linear_logprobs")
+
+
+def twell_linear_logprobs_bwd(hidden, weight, targets, inv_temperature: float, lse, entropy, d_logprob, d_entropy,
+                              d_hidden, d_weight, workspace, status, stream=None) -> None:
+    """d_hidden [rows, d] and d_weight [vocab, d] bf16 (either may be None) from the upstream gradients of
+    logprob and entropy; targets with d_logprob, or entropy with d_entropy, may be None."""
+    torch = _torch or _setup()
+    f32, i32, bf = torch.float32, torch.int32, (torch.bfloat16,)
+    rows, dim, vocab, h_p, ldh, w_p, ldw = _linear(hidden, weight)
+    dh_p, lddh = _matrix(d_hidden, bf, rows, dim, "d_hidden")
+    dw_p, lddw = _matrix(d_weight, bf, vocab, dim, "d_weight")
+    lse_p = _arg(lse, f32, rows, "lse")
+    ent, g, ge = (_maybe(t, f32, rows, name) for t, name in ((entropy, "entropy"), (d_logprob, "d_logprob"),
+                                                             (d_entropy, "d_entropy")))
+    t_p, st = _maybe(targets, i32, rows, "targets"), _arg(status, i32, 1, "status")
+    ws, ws_bytes = _workspace(workspace)
+    _on_device(hidden, weight, targets, lse, entropy, d_logprob, d_entropy, d_hidden, d_weight, workspace, status)
+    rc = load_library().twell_linear_logprobs_bwd(h_p, ldh, w_p, ldw, rows, dim, vocab, t_p, inv_temperature, lse_p,
+                                                  ent, g, ge, dh_p, lddh, dw_p, lddw, ws, ws_bytes, st, _on(stream))
+    if rc:
+        _check(rc, "twell_linear_logprobs_bwd")

@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtwell.so")
 SOURCES = ["api.cu", "gemm_tcgen05.cu", "fwd_kernels.cu", "pack_kernels.cu", "bwd_kernels.cu", "spmm.cu", "noalloc.cu",
            "selftest.cu", "kv_plan.cu", "kv_append.cu", "kv_attention.cu", "kv_chunk.cu", "logprobs.cu",
-           "block_norm.cu"]
+           "block_norm.cu", "linear_logprobs.cu"]
 HEADERS = ["sm103.cuh", "twell_internal.h", "kv_internal.h", "kv_attention.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

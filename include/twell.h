@@ -552,6 +552,45 @@ TWELL_API int twell_block_norm_bwd(const uint16_t* dh, int64_t lddh, const void*
 
 TWELL_API size_t twell_block_norm_bwd_workspace_bytes(int32_t n_rows, int32_t d_model);
 
+/* Log probabilities of tokens straight from hidden rows and output weights: twell_logprobs of
+ *   x = inv_temperature H W^T
+ * (bf16 products, fp32 sums) without x in memory.
+ *   H       [n_rows][d_model] bf16, W [vocab][d_model] bf16; d_model a multiple of 8
+ *   targets [n_rows] int32; a target outside [0, vocab) is none: logprob 0
+ *   logprob x_target - lse; entropy; lse = log sum exp x: [n_rows] fp32, each may be null
+ *           (targets and logprob together)
+ * A row with a NaN or an infinite logit gives NaN, a row of -inf only logprob -inf, entropy 0, lse -inf.
+ * workspace: >= twell_linear_logprobs_workspace_bytes(...), 256-byte aligned, needs no initialisation.
+ * status: device int32, zero at first: the first TWELL_ERR_* code a kernel met (an expired wait).
+ * Two launches. */
+TWELL_API int twell_linear_logprobs(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw, int32_t n_rows,
+                                    int32_t d_model, int32_t vocab, const int32_t* targets, float inv_temperature,
+                                    float* logprob, float* entropy, float* lse, void* workspace,
+                                    size_t workspace_bytes, int32_t* status, twell_stream_t stream);
+
+TWELL_API size_t twell_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t d_model, int32_t vocab);
+
+/* Gradient of twell_linear_logprobs with respect to H and W, from what that call left (lse,
+ * entropy) and the upstream gradients of logprob and entropy.  With p = exp(x - lse):
+ *   G_j = inv_temperature * (d_logprob (1[j = target] - p_j) - d_entropy p_j (log p_j + entropy))
+ *   dH = G W [n_rows][d_model] bf16,  dW = G^T H [vocab][d_model] bf16; either may be null
+ * G is made again in pieces of the vocabulary, rounded to bf16 (each entry off by at most 2^-8 of
+ * itself: why dW is bf16, too), and multiplied with fp32 sums that are rounded once.  A row without a
+ * target takes d_logprob as 0; a row whose lse is -inf gives zeros.  targets with d_logprob, or entropy with
+ * d_entropy, may be null: that term is left out.  fp32 tells lse to 2^-24 of itself: beyond |lse| =
+ * 16384 p is off by more than its rounding to bf16.  With n_rows == 0 dW is set to zero.
+ * workspace: >= twell_linear_logprobs_bwd_workspace_bytes(...), 256-byte aligned, needs no
+ * initialisation: two pieces of G (128 MB each, or 4096 columns where rows are many) and dH in
+ * fp32, much less where one piece is enough.  status as above. */
+TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw,
+                                        int32_t n_rows, int32_t d_model, int32_t vocab, const int32_t* targets,
+                                        float inv_temperature, const float* lse, const float* entropy,
+                                        const float* d_logprob, const float* d_entropy, uint16_t* dH, int64_t lddh,
+                                        uint16_t* dW, int64_t lddw, void* workspace, size_t workspace_bytes,
+                                        int32_t* status, twell_stream_t stream);
+
+TWELL_API size_t twell_linear_logprobs_bwd_workspace_bytes(int32_t n_rows, int32_t d_model, int32_t vocab);
+
 /* Synchronises `stream`, then returns *layout->status if non-zero, else
  * TWELL_ERR_FALLBACK_OVERFLOW when *layout->n_fb exceeds the capacity (fb_cap
  * rows, or fb_cap * d_ff / tile dense tiles for the tile-granular variant),

@@ -99,3 +99,64 @@ def test_binding_of_the_norms_checks(tw):
         tw.twell_block_norm_bwd(x, x, x, x, x, x, w_pre=w, rstd_pre=r, dw_pre=w)
     with pytest.raises(ValueError, match="CUDA"):
         tw.twell_block_norm_bwd(x, x, x, x, x, x, w_pre=w, rstd_pre=r)
+
+
+LIN = dict(H=A, ldh=256, W=B, ldw=256, n=5, d=256, vocab=1000, targets=C, inv_t=1.0, logprob=D, entropy=E, lse=F, ws=A,
+           ws_bytes=1 << 40, status=A, stream=None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(H=None), -1), (dict(W=None), -1), (dict(n=-1), -1), (dict(d=0), -1), (dict(vocab=0), -1), (dict(ldh=248), -1),
+    (dict(ldw=260), -1), (dict(inv_t=0.0), -1), (dict(inv_t=-1.0), -1), (dict(inv_t=float("nan")), -1),
+    (dict(inv_t=float("inf")), -1), (dict(targets=None), -1), (dict(logprob=None), -1), (dict(status=None), -1),
+    (dict(d=100, ldh=104), -3), (dict(H=P(0x10008)), -2), (dict(W=P(0x10008)), -2), (dict(lse=P(0x10002)), -2),
+    (dict(status=P(0x10002)), -2), (dict(ws=None), -5), (dict(ws_bytes=100), -5), (dict(ws=P(0x10010)), -2)])
+def test_linear_logprobs_refuse(lib, over, code):
+    assert lib.twell_linear_logprobs(*{**LIN, **over}.values()) == code
+
+
+LINB = dict(H=A, ldh=256, W=B, ldw=256, n=5, d=256, vocab=1000, targets=C, inv_t=1.0, lse=D, entropy=E, g=F, ge=A,
+            dH=C, lddh=256, dW=D, lddw=256, ws=A, ws_bytes=1 << 40, status=A, stream=None)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(H=None), -1), (dict(W=None), -1), (dict(lse=None), -1), (dict(targets=None), -1), (dict(g=None), -1),
+    (dict(entropy=None), -1), (dict(ge=None), -1), (dict(dH=None, dW=None), -1), (dict(lddh=248), -1),
+    (dict(lddw=257), -1), (dict(n=-1), -1), (dict(inv_t=0.0), -1), (dict(status=None), -1), (dict(d=100), -3),
+    (dict(dH=P(0x10008)), -2), (dict(dW=P(0x10008)), -2), (dict(g=P(0x10001)), -2), (dict(ws=None), -5),
+    (dict(ws_bytes=1000), -5), (dict(ws=P(0x10010)), -2)])
+def test_linear_logprobs_bwd_refuses(lib, over, code):
+    assert lib.twell_linear_logprobs_bwd(*{**LINB, **over}.values()) == code
+
+
+def test_linear_workspaces_are_host_arithmetic(tw):
+    assert tw.linear_logprobs_workspace_bytes(16, 4096, 131072) >= 16 * 4 * 3
+    assert tw.linear_logprobs_bwd_workspace_bytes(16, 4096, 131072) >= 16 * 131072 * 2
+    # pieces: far less than the logits
+    assert tw.linear_logprobs_bwd_workspace_bytes(65536, 4096, 131072) < 65536 * 131072 * 2 // 4
+    for f in (tw.linear_logprobs_workspace_bytes, tw.linear_logprobs_bwd_workspace_bytes):
+        for bad in ((-1, 64, 10), (1, 0, 10), (1, 12, 10), (1, 64, 0)):
+            assert f(*bad) == 0
+
+
+def test_binding_of_the_linear_calls_checks(tw):
+    import torch
+    bf, i32 = torch.bfloat16, torch.int32
+    h, w, f, t = torch.zeros((4, 64), dtype=bf), torch.zeros((10, 64), dtype=bf), torch.zeros(4), torch.zeros(4, dtype=i32)
+    ws, st = torch.zeros(256, dtype=torch.uint8), torch.zeros(1, dtype=i32)
+    with pytest.raises(ValueError, match="^hidden: torch.float32"):
+        tw.twell_linear_logprobs(h.float(), w, t, 1.0, f, f, f, ws, st)
+    with pytest.raises(ValueError, match="^weight: rows of 56"):
+        tw.twell_linear_logprobs(h, w[:, :56], t, 1.0, f, f, f, ws, st)
+    with pytest.raises(ValueError, match="^targets: torch.int64"):
+        tw.twell_linear_logprobs(h, w, t.long(), 1.0, f, f, f, ws, st)
+    with pytest.raises(ValueError, match="^lse: 3"):
+        tw.twell_linear_logprobs(h, w, t, 1.0, f, f, f[:3], ws, st)
+    with pytest.raises(ValueError, match="CUDA"):
+        tw.twell_linear_logprobs(h, w, t, 1.0, f, f, f, ws, st)
+    with pytest.raises(ValueError, match="^d_weight: shape"):
+        tw.twell_linear_logprobs_bwd(h, w, t, 1.0, f, f, f, f, h, w[:9], ws, st)
+    with pytest.raises(ValueError, match="^d_hidden: torch.float32"):
+        tw.twell_linear_logprobs_bwd(h, w, t, 1.0, f, f, f, f, h.float(), w, ws, st)
+    with pytest.raises(ValueError, match="CUDA"):
+        tw.twell_linear_logprobs_bwd(h, w, t, 1.0, f, f, f, f, h, w, ws, st)

@@ -1,7 +1,8 @@
 """Plain 64-bit definitions of the training step's operators for the tests, written from the
-formulas in numpy, sharing no code with the package.  Beside each result stands the sum of the
+formulas in numpy (the linear ones in torch), sharing no code with the package.  Beside each result stands the sum of the
 magnitudes that went into it, which the tests' error bounds are multiples of."""
 import numpy as np
+import torch
 
 
 def block_norm(x, y, w_post, gate, w_pre, row_gate, skip, branch, eps):
@@ -59,32 +60,37 @@ def block_norm_bwd(dh, d_out, z, y, w_post, gate, w_pre, row_gate, skip, branch,
     return out, size
 
 
-def linear_logprobs(h, w, targets, inv_t):
-    """(logprob, entropy, lse, scaled logits)"""
-    x = inv_t * (h @ w.T)
-    with np.errstate(over="ignore", invalid="ignore"):
-        m = x.max(1)
-        m0 = np.where(np.isinf(m), 0, m)
-        e = np.exp(x - m0[:, None])
-        total = e.sum(1)
-        lse = m0 + np.log(total)
-        shifted = np.where(e > 0, e * (x - m0[:, None]), 0).sum(1)
-        entropy = np.log(total) - shifted / total
-    has = (targets >= 0) & (targets < w.shape[0])
-    of = x[np.arange(len(x)), np.where(has, targets, 0)]
-    return np.where(has, of - lse, 0.0), entropy, lse, x
+def linear_logits(h, w, inv_t):
+    """(scaled logits, the magnitudes in them) of 64-bit torch tensors"""
+    return inv_t * (h @ w.T), inv_t * (h.abs() @ w.abs().T)
 
 
-def linear_logprobs_bwd(h, w, targets, inv_t, lse, entropy, g, ge):
-    """(d_hidden, d_weight, gradient of the unscaled logits)"""
-    x = inv_t * (h @ w.T)
+def linear_logprobs(x, targets):
+    """(logprob, entropy, lse) of scaled logits"""
+    m = x.amax(1)
+    m0 = torch.where(torch.isinf(m), 0.0, m)[:, None]
+    e = torch.exp(x - m0)
+    total = e.sum(1)
+    lse = m0[:, 0] + torch.log(total)
+    shifted = torch.where(e > 0, e * (x - m0), 0.0).sum(1)
+    entropy = torch.where(total > 0, torch.log(total) - shifted / total, 0.0)
+    has = (targets >= 0) & (targets < x.shape[1])
+    of = x.gather(1, torch.where(has, targets, 0).long()[:, None])[:, 0]
+    return torch.where(has, of - lse, 0.0), entropy, lse
+
+
+def linear_grad(x, targets, inv_t, lse, entropy, g, ge):
+    """(gradient of the unscaled logits, the magnitudes in it)"""
     logp = x - lse[:, None]
-    p = np.exp(logp)
-    has = (targets >= 0) & (targets < w.shape[0])
-    g = np.where(has, 0.0 if g is None else g, 0.0)
-    d = -p * g[:, None]
+    p = torch.exp(logp)
+    has = (targets >= 0) & (targets < x.shape[1])
+    g = torch.where(has, 0.0 if g is None else g, 0.0)
+    d, size = -p * g[:, None], p * g.abs()[:, None]
     if ge is not None:
-        d -= ge[:, None] * p * (logp + entropy[:, None])
-    d[np.arange(len(x))[has], targets[has]] += g[has]
-    d *= inv_t
-    return d @ w, d.T @ h, d
+        shift = torch.where(p > 0, logp + entropy[:, None], 0.0)
+        d = d - ge[:, None] * p * shift
+        size = size + ge.abs()[:, None] * p * (torch.where(p > 0, logp.abs(), 0.0) + entropy[:, None] + 1)
+    rows = torch.arange(len(x), device=x.device)[has]
+    d[rows, targets[has].long()] += g[has]
+    size[rows, targets[has].long()] += g[has].abs()
+    return inv_t * d, inv_t * size
