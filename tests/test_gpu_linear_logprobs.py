@@ -183,16 +183,19 @@ def check_backward(h, w, t, inv_t, lse, ent, g, ge, dh, dw):
     e = size.amax(1, keepdim=True) * d * 2.0 ** -23
     none = torch.full((n,), -1, device="cuda")
     G, big = ref.linear_grad(x, none if t is None else t, inv_t, up(lse), up(ent), up(g), up(ge))
-    off = 2.0 ** -8 * G.abs() + (2 * e + 2.0 ** -20 + 2.0 ** -22 * lse.double().abs()[:, None]) * big
-    for got, A, B, terms, what in ((dh, (G, off, big), wd, v, "d_hidden"), (dw, (G.T, off.T, big.T), hd, n, "d_weight")):
+    fp32 = (2 * e + 2.0 ** -20 + 2.0 ** -22 * lse.double().abs()[:, None]) * big
+    off = 2.0 ** -8 * G.abs() + fp32
+    for got, A, B, terms, what in ((dh, (G, off, big, fp32), wd, v, "d_hidden"),
+                                 (dw, (G.T, off.T, big.T, fp32.T), hd, n, "d_weight")):
         if got is None:
             continue
         want = A[0] @ B
         bound = A[1] @ B.abs() + terms * 2.0 ** -23 * (A[2] @ B.abs()) + 2.0 ** -8 * want.abs()
         close(got, want, bound + 1e-36, what)
-        norm = want.norm()
-        if norm > 0:  # two roundings to bf16, each 2^-9 on average at most
-            assert float((got.double() - want).norm() / norm) <= 2.0 ** -8, what
+        # as a whole: a result of one term is off by its two roundings to bf16, 2^-7 of itself; in a sum of many these
+        # add like random numbers, so that the norm of all of them is within that too.  Beside it stands what fp32 leaves
+        # where G's own terms cancel (a vocabulary of one token: p = 1, G = 0), the second part of G's bound
+        assert (got.double() - want).norm() <= 2.0 ** -7 * want.norm() + (A[3] @ B.abs()).norm(), what
 
 
 @pytest.mark.parametrize("n,d,v", SHAPES + [(400, 264, 2500), (70, 64, 12345)])
