@@ -12,9 +12,17 @@
 //   drow_gate = sum_c branch gate w_post dz s
 // so the two vectors of the branch share one sum over the rows.
 //
-// A row is held in registers by a group of threads, 8 elements a 16-byte load,
-// and is read once.  All sums are fp32: a thread's own elements in order, then
-// a tree over the group, so results do not depend on the launch.
+// A row is held in registers by a group of threads, 16 elements a thread, and is
+// read once.  One CTA an SM stays and takes rows in turn, several groups side by side;
+// each thread copies its own elements of the next rows into its own shared memory
+// asynchronously, which keeps enough bytes on the way without a barrier or a register.
+// Arithmetic goes two fp32 lanes an instruction: with one, instructions bound it (8192 x 2048 bf16: 31 us
+// forward, 54 backward).  The gradient's three sums of a row are taken together:
+//   sum t s / scale = sum w (d_out + r2 a) s - r2 c2 sum w v s,  c2 = mean(a v), w = gate w_post.
+// HBM bounds long calls (8192 x 2048 bf16: 25 us, 5.4 TB/s; gradient 41 us, 4.9 TB/s, 3 of it the sum over
+// the CTAs), the launch and a row's chain of two sums short ones (16 x 4096: 2.9 us).
+// All sums are fp32: a thread's own elements in order, then a tree over the group;
+// sums over the rows by groups, CTAs and then runs of CTAs in order, so equal calls give equal bits.
 #include <algorithm>
 
 #include "kv_internal.h"
@@ -23,7 +31,13 @@ namespace twell {
 namespace {
 
 constexpr int kMaxDim = 16384;
-constexpr int kMaxParts = 1024;  // partial sums of the weights' gradients
+constexpr int kMaxParts = 160;      // CTAs that leave sums of their rows
+constexpr int kMaxGroups = 20;      // rows of a CTA at a time
+constexpr int kMaxStages = 4;       // rows on the way to a thread
+constexpr int kSharedBytes = 208 * 1024;  // beside 15 KB for the sums
+constexpr int kWideDim = 8192;      // above, 1024 threads a row and its weights in no registers or shared memory
+constexpr int kThreads = 512, kBwdThreads = 512;  // of a CTA: what registers allow
+constexpr int kV = 2;               // 16-byte pieces of a row a thread has
 
 struct NormArgs {
   const void* x;
@@ -31,7 +45,7 @@ struct NormArgs {
   void* x_out;
   uint16_t* h;
   int64_t ldx, ldy, ldo, ldh;
-  int n_rows, dim, group;  // group: threads of a row
+  int n_rows, dim, group, stages;  // group: threads of a row
   const void *w_post, *gate, *w_pre;
   bool w_f32;
   const float* row_gate;
@@ -47,7 +61,7 @@ struct NormBwdArgs {
   void* dx;
   uint16_t* dy;
   int64_t lddh, lddo, ldz, ldy, lddx, lddy;
-  int n_rows, dim, group;
+  int n_rows, dim, group, stages;
   const void *w_post, *gate, *w_pre;
   bool w_f32;
   const float* row_gate;
@@ -58,225 +72,521 @@ struct NormBwdArgs {
   float* part;                 // [parts][2][dim]: sum dh v, then P
 };
 
-// 8 elements of a row at p + 8 i.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]);
-template <>
-__device__ __forceinline__ void load8<uint16_t>(const uint16_t* p, float (&f)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  f[0] = bf16_lo(w.x), f[1] = bf16_hi(w.x), f[2] = bf16_lo(w.y), f[3] = bf16_hi(w.y);
-  f[4] = bf16_lo(w.z), f[5] = bf16_hi(w.z), f[6] = bf16_lo(w.w), f[7] = bf16_hi(w.w);
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&f)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-}
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+// Two fp32 lanes, one instruction an operation.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
   return r;
 }
-__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8]) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+__device__ __forceinline__ float2 lanes(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
 }
-__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
-__device__ __forceinline__ void weight8(const void* p, bool f32, int at, float (&f)[8]) {
-  if (f32)
-    load8(static_cast<const float*>(p) + at, f);
-  else
-    load8(static_cast<const uint16_t*>(p) + at, f);
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float both(F2 a) {
+  const float2 f = lanes(a);
+  return f.x + f.y;
+}
+
+// A thread's 8 elements of a piece.
+struct Oct {
+  F2 v[4];
+};
+__device__ __forceinline__ Oct from_bf16(const uint4& w) {
+  return Oct{{pair(bf16_lo(w.x), bf16_hi(w.x)), pair(bf16_lo(w.y), bf16_hi(w.y)), pair(bf16_lo(w.z), bf16_hi(w.z)),
+              pair(bf16_lo(w.w), bf16_hi(w.w))}};
+}
+__device__ __forceinline__ Oct from_f32(const float4& a, const float4& b) {
+  return Oct{{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
+}
+__device__ __forceinline__ uint32_t bf16_word(F2 a) {
+  const float2 f = lanes(a);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
+  return r;
+}
+__device__ __forceinline__ float weight1(const void* p, bool f32, int c) {
+  return f32 ? static_cast<const float*>(p)[c] : bf16_bits_to_float(static_cast<const uint16_t*>(p)[c]);
+}
+
+// The sum of the warps' sums (zero past the group's warps).
+__device__ __forceinline__ float warp_sums(const float* scratch, int group) {
+  const float4* const at = reinterpret_cast<const float4*>(scratch);
+  float4 a = at[0];
+  if (group > 128) {  // more than 4 warps
+    const float4 b = at[1];
+    a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+    for (int k = 2; k * 128 < group; ++k) {
+      const float4 c = at[k];
+      a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
+    }
+  }
+  return (a.x + a.y) + (a.z + a.w);
 }
 
 // The sum over the group's threads, in every thread of it.  scratch: 32 floats of
-// the group's own, free again once the group has passed another such barrier.
+// the group's own, zero past its warps; free again once the group has passed another such barrier.
 __device__ __forceinline__ float group_sum(float v, int group, int id, int thread, float* scratch) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if (group == 32) return v;
-  const int lane = thread & 31;
-  if (lane == 0) scratch[thread >> 5] = v;
+  if ((thread & 31) == 0) scratch[thread >> 5] = v;
   asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(group) : "memory");
-  v = lane < (group >> 5) ? scratch[lane] : 0.0f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  return warp_sums(scratch, group);
 }
 
-constexpr int kMaxGroups = 8;  // rows of a CTA at a time (named barriers 1 to 8)
+// Three sums at once.  scratch: [3][32].
+__device__ __forceinline__ void group_sum3(float (&v)[3], int group, int id, int thread, float* scratch) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if (group == 32) return;
+  if ((thread & 31) == 0)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) scratch[k * 32 + (thread >> 5)] = v[k];
+  asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(group) : "memory");
+#pragma unroll
+  for (int k = 0; k < 3; ++k) v[k] = warp_sums(scratch + k * 32, group);
+}
 
-template <typename T, int V>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const NormArgs a) {
-  __shared__ float scratch[kMaxGroups][2][32];
-  grid_dependency_wait();
-  const int id = threadIdx.x / a.group, t = threadIdx.x % a.group;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / a.group) + id;
-  if (row >= a.n_rows) return;  // whole groups leave: barriers are a group's own
-  const float inv_dim = 1.0f / static_cast<float>(a.dim);
-  float z[V][8];
-  float scale = a.branch;
-  if (a.row_gate) scale *= a.row_gate[row];
-  if (a.y) {
-    float s = 0.0f;
+__device__ __forceinline__ void copy16(uint8_t* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint8_t* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest `stages - 1` groups of this thread's copies have landed.
+__device__ __forceinline__ void copies_wait(int stages) {
+  if (stages == 1)
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (stages == 2)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (stages == 3)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// Which columns a thread has.  A piece is 8 elements a thread: with a bf16 stream 8 in a
+// row, with fp32 two runs of 4, `group` runs apart, so that every access of a warp is one run of whole lines
+// (8 in a row of fp32 are two accesses of half of every line: 8192 x 2048, 42 us).
+// In shared memory a piece is 16 bytes a thread, or two planes of them in fp32, those of a CTA's threads side by
+// side (`pitch` bytes together).  Columns past the row are zero there and in the weights, so they add nothing.
+template <typename T>
+struct Layout {
+  static constexpr int kRuns = sizeof(T) / 2, kRun = 8 / kRuns;
+  static constexpr int kPieces = kRuns;  // 16-byte pieces of the stream's 8 elements
+  int dim, first, step;  // a run's column is first + its number * step
+
+  __device__ __forceinline__ int column(int i, int q) const { return first + (i * kRuns + q) * step; }
+  __device__ __forceinline__ bool on(int i, int q) const { return column(i, q) < dim; }
+
+  __device__ __forceinline__ void copy(uint8_t* at, int pitch, const T* row, int i) const {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (t + i * a.group) * 8;
-      if (c < a.dim) {
-        load8(a.y + row * a.ldy + c, z[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s = fmaf(z[i][e], z[i][e], s);
-      }
-    }
-    if (a.w_post) {
-      s = group_sum(s, a.group, id, t, scratch[id][0]);
-      const float r1 = 1.0f / sqrtf(fmaf(s, inv_dim, a.eps));
-      if (t == 0 && a.rstd_post) a.rstd_post[row] = r1;
-      scale *= r1;
-    }
+    for (int q = 0; q < kRuns; ++q)
+      if (on(i, q)) copy16(at + q * pitch, row + column(i, q));
   }
-  float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (t + i * a.group) * 8;
-    if (c >= a.dim) continue;
-    float x[8];
-    load8(static_cast<const T*>(a.x) + row * a.ldx + c, x);
-    if (a.y) {
-      float w[8];
-      if (a.w_post) {
-        weight8(a.w_post, a.w_f32, c, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[i][e] *= w[e];
-      }
-      if (a.gate) {
-        weight8(a.gate, a.w_f32, c, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[i][e] *= w[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[i][e] = fmaf(scale, z[i][e], a.skip * x[e]);
+  __device__ __forceinline__ void copy_bf16(uint8_t* at, const uint16_t* row, int i) const {
+    if constexpr (kRuns == 1) {
+      if (on(i, 0)) copy16(at, row + column(i, 0));
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[i][e] = a.skip * x[e];
+      for (int q = 0; q < kRuns; ++q)
+        if (on(i, q)) copy8(at + 8 * q, row + column(i, q));
     }
-    if (a.x_out) store8(static_cast<T*>(a.x_out) + row * a.ldo + c, z[i]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(z[i][e], z[i][e], s);
   }
-  if (!a.h) return;
-  s = group_sum(s, a.group, id, t, scratch[id][1]);
-  const float r2 = 1.0f / sqrtf(fmaf(s, inv_dim, a.eps));
-  if (t == 0 && a.rstd_pre) a.rstd_pre[row] = r2;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (t + i * a.group) * 8;
-    if (c >= a.dim) continue;
-    float w[8];
-    weight8(a.w_pre, a.w_f32, c, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) z[i][e] *= r2 * w[e];
-    store8(a.h + row * a.ldh + c, z[i]);
+  static __device__ __forceinline__ Oct read(const uint8_t* at, int pitch) {
+    if constexpr (kRuns == 1)
+      return read_bf16(at);
+    else
+      return from_f32(*reinterpret_cast<const float4*>(at), *reinterpret_cast<const float4*>(at + pitch));
   }
-}
+  static __device__ __forceinline__ Oct read_bf16(const uint8_t* at) {
+    return from_bf16(*reinterpret_cast<const uint4*>(at));
+  }
+  __device__ __forceinline__ void write(T* row, int i, const Oct& o) const {
+    if constexpr (kRuns == 1)
+      write_bf16(row, i, o);
+    else
+      write_f32(row, i, o);
+  }
+  __device__ __forceinline__ void write_bf16(uint16_t* row, int i, const Oct& o) const {
+    const uint4 w = make_uint4(bf16_word(o.v[0]), bf16_word(o.v[1]), bf16_word(o.v[2]), bf16_word(o.v[3]));
+    if constexpr (kRuns == 1) {
+      if (on(i, 0)) *reinterpret_cast<uint4*>(row + column(i, 0)) = w;
+    } else {
+      if (on(i, 0)) *reinterpret_cast<uint2*>(row + column(i, 0)) = make_uint2(w.x, w.y);
+      if (on(i, 1)) *reinterpret_cast<uint2*>(row + column(i, 1)) = make_uint2(w.z, w.w);
+    }
+  }
+  // fp32, wherever the runs are
+  __device__ __forceinline__ void write_f32(float* row, int i, const Oct& o) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 a = lanes(o.v[2 * h]), b = lanes(o.v[2 * h + 1]);
+      const int c = kRuns == 1 ? column(i, 0) + 4 * h : column(i, h);
+      if (c < dim) *reinterpret_cast<float4*>(row + c) = make_float4(a.x, a.y, b.x, b.y);
+    }
+  }
+  __device__ __forceinline__ Oct read_f32(const float* row, int i) const {  // of columns that are on, else 0
+    float4 f[2] = {};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = kRuns == 1 ? column(i, 0) + 4 * h : column(i, h);
+      if (c < dim) f[h] = *reinterpret_cast<const float4*>(row + c);
+    }
+    return from_f32(f[0], f[1]);
+  }
+};
 
-template <typename T, int V>
-__global__ void __launch_bounds__(1024) block_norm_bwd_kernel(const NormBwdArgs a) {
-  __shared__ float scratch[kMaxGroups][2][2][32];  // two sums of a row, rows in turn
+// The product of the branch's weights, and the next norm's weight, as fp32: in shared memory ([2]
+// planes of a thread's 16-byte pieces, read without conflicts), or read anew where rows are too wide for that.
+template <typename T, bool SHARED>
+struct Weights {
+  uint8_t* base;  // [branch, pre][piece][2][group] of 16 bytes
+  const void *post, *gate, *pre;
+  bool f32;
+  int group, thread;
+  Layout<T> at;
+
+  // a run of a vector as fp32 (1 without one)
+  __device__ __forceinline__ void run(const void* p, int c, float (&f)[Layout<T>::kRun]) const {
+    constexpr int R = Layout<T>::kRun;
+#pragma unroll
+    for (int e = 0; e < R; e += 4) {
+      float4 v = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+      if (p && f32) {
+        v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + e);
+      } else if (p) {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + c + e);
+        v = make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+      }
+      f[e] = v.x, f[e + 1] = v.y, f[e + 2] = v.z, f[e + 3] = v.w;
+    }
+  }
+  __device__ __forceinline__ Oct make(bool branch, int i) const {
+    constexpr int R = Layout<T>::kRun;
+    float f[8] = {};
+#pragma unroll
+    for (int q = 0; q < Layout<T>::kRuns; ++q) {
+      if (!at.on(i, q)) continue;
+      float x[R], y[R];
+      run(branch ? post : pre, at.column(i, q), x);
+      run(branch ? gate : nullptr, at.column(i, q), y);
+#pragma unroll
+      for (int e = 0; e < R; ++e) f[q * R + e] = x[e] * y[e];
+    }
+    return Oct{{pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7])}};
+  }
+  __device__ __forceinline__ ulonglong2* slot(bool branch, int i, int h) const {
+    return reinterpret_cast<ulonglong2*>(base) + (((branch ? 0 : kV) + i) * 2 + h) * group + thread;
+  }
+  // by the first group's threads, a barrier before the first use
+  __device__ __forceinline__ void fill() const {
+    if constexpr (SHARED) {
+#pragma unroll
+      for (int i = 0; i < 2 * kV; ++i) {
+        const Oct w = make(i < kV, i % kV);
+        *slot(i < kV, i % kV, 0) = make_ulonglong2(w.v[0], w.v[1]);
+        *slot(i < kV, i % kV, 1) = make_ulonglong2(w.v[2], w.v[3]);
+      }
+    }
+  }
+  __device__ __forceinline__ Oct get(bool branch, int i) const {
+    if constexpr (!SHARED) return make(branch, i);
+    const ulonglong2 a = *slot(branch, i, 0), b = *slot(branch, i, 1);
+    return Oct{{a.x, a.y, b.x, b.y}};
+  }
+};
+
+// What the two kernels set up alike.
+template <typename T, int NT>
+struct Setup {
+  static constexpr bool kShared = NT < 1024;
+  int groups, id, thread, pitch;
+  Layout<T> at;
+  Weights<T, kShared> weights;
+  uint8_t *ring, *mine;
+  __device__ __forceinline__ Setup(uint8_t* smem, int group, int dim, const void* post, const void* gate,
+                                   const void* pre, bool f32) {
+    groups = blockDim.x / group, id = threadIdx.x / group, thread = threadIdx.x % group;
+    pitch = blockDim.x * 16;
+    at = Layout<T>{dim, thread * Layout<T>::kRun, group * Layout<T>::kRun};
+    weights = Weights<T, kShared>{smem, post, gate, pre, f32, group, thread, at};
+    ring = smem + (kShared ? 2 * kV * 2 * 16 * group : 0);
+    mine = ring + threadIdx.x * 16;
+  }
+  // Zeros where no copy goes.
+  __device__ __forceinline__ void clear(int pieces) const {
+    if (at.on(kV - 1, Layout<T>::kRuns - 1)) return;
+    for (int p = 0; p < pieces; ++p) *reinterpret_cast<uint4*>(mine + p * pitch) = make_uint4(0, 0, 0, 0);
+  }
+};
+
+// A row for each group of threads in turn; Y: there is a block's output.
+template <typename T, int NT, bool Y>
+__global__ void __launch_bounds__(NT, 1) block_norm_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(16) float scratch[kMaxGroups][2][2][32];  // two sums of a row, rows in turn
+  for (int i = threadIdx.x; i < kMaxGroups * 128; i += blockDim.x) (&scratch[0][0][0][0])[i] = 0.0f;
   grid_dependency_wait();
-  const int id = threadIdx.x / a.group, t = threadIdx.x % a.group, groups = blockDim.x / a.group;
+  const Setup<T, NT> g(smem, a.group, a.dim, a.w_post, a.gate, a.w_pre, a.w_f32);
+  const Layout<T>& at = g.at;
+  constexpr int V = kV, kX = Layout<T>::kPieces, kPieces = kX + (Y ? 1 : 0);  // of x, of y
+  const int pitch = g.pitch, step = gridDim.x * g.groups;
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
-  float sum_pre[V][8] = {}, sum_branch[V][8] = {};
-  int turn = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * groups + id; row < a.n_rows;
-       row += static_cast<int64_t>(gridDim.x) * groups, turn ^= 1) {
-    float dz[V][8], v[V][8];
-    float r2 = 0.0f, c2 = 0.0f;
-    if (a.dh) {
-      r2 = a.rstd_pre[row];
+  g.clear(a.stages * V * kPieces);
+  int64_t row = static_cast<int64_t>(blockIdx.x) * g.groups + g.id, next = row;
+  auto copy = [&](uint8_t* to) {
+    if (next < a.n_rows) {
+      const T* const x = static_cast<const T*>(a.x) + next * a.ldx;
+      const uint16_t* const y = Y ? a.y + next * a.ldy : nullptr;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = (t + i * a.group) * 8;
-        if (c >= a.dim) continue;
-        float w[8];
-        load8(a.dh + row * a.lddh + c, dz[i]);
-        load8(static_cast<const T*>(a.z) + row * a.ldz + c, v[i]);
-        weight8(a.w_pre, a.w_f32, c, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[i][e] *= r2;
-          sum_pre[i][e] = fmaf(dz[i][e], v[i][e], sum_pre[i][e]);
-          dz[i][e] *= w[e];
-          c2 = fmaf(dz[i][e], v[i][e], c2);
-        }
+        at.copy(to + i * kPieces * pitch, pitch, x, i);
+        if (Y) at.copy_bf16(to + (i * kPieces + kX) * pitch, y, i);
       }
-      c2 = group_sum(c2, a.group, id, t, scratch[id][0][turn]) * inv_dim;
     }
-    const float scale = a.row_gate ? a.branch * a.row_gate[row] : a.branch;
-    const float r1 = a.rstd_post ? a.rstd_post[row] : 1.0f;
-    float c1 = 0.0f;  // sum t s / scale
+    copies_commit();
+    next += step;
+  };
+#pragma unroll 1
+  for (int s = 0; s < a.stages; ++s) copy(g.mine + s * V * kPieces * pitch);
+  float gate = a.branch;  // of a row, read a row ahead
+  if (Y && a.row_gate && row < a.n_rows) gate *= a.row_gate[row];
+  if (g.id == 0) g.weights.fill();
+  __syncthreads();
+  const F2 skip = pair(a.skip, a.skip);
+  uint8_t* from = g.mine;
+  int stage = 0, turn = 0;
+#pragma unroll 1
+  for (; row < a.n_rows; row += step, turn ^= 1) {
+    float scale = gate;
+    if (Y && a.row_gate && row + step < a.n_rows) gate = a.branch * a.row_gate[row + step];
+    copies_wait(a.stages);
+    Oct x[V], z[V];
+    F2 sum = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (t + i * a.group) * 8;
-      if (c >= a.dim) continue;
+      x[i] = at.read(from + i * kPieces * pitch, pitch);
+      if (!Y) continue;
+      z[i] = at.read_bf16(from + (i * kPieces + kX) * pitch);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dz[i][e] = a.dh ? r2 * (dz[i][e] - v[i][e] * c2) : 0.0f;
-      float w[8];
-      if (a.d_out) {
-        load8(static_cast<const T*>(a.d_out) + row * a.lddo + c, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dz[i][e] += w[e];
-      }
-      if (a.dx) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = a.skip * dz[i][e];
-        store8(static_cast<T*>(a.dx) + row * a.lddx + c, w);
-      }
-      if (!a.y) continue;
-      load8(a.y + row * a.ldy + c, v[i]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[i][e] *= r1;
-        sum_branch[i][e] = fmaf(scale * dz[i][e], v[i][e], sum_branch[i][e]);
-      }
-      if (a.w_post) {
-        weight8(a.w_post, a.w_f32, c, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dz[i][e] *= w[e];
-      }
-      if (a.gate) {
-        weight8(a.gate, a.w_f32, c, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dz[i][e] *= w[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) c1 = fmaf(dz[i][e], v[i][e], c1);
+      for (int k = 0; k < 4; ++k) sum = fma2(z[i].v[k], z[i].v[k], sum);
     }
-    if (!a.y) continue;
-    if (a.w_post || a.drow_gate) {
-      c1 = group_sum(c1, a.group, id, t, scratch[id][1][turn]);
-      if (t == 0 && a.drow_gate) a.drow_gate[row] = a.branch * c1;
+    copy(from);  // into what has just been read
+    from += V * kPieces * pitch;
+    if (++stage == a.stages) stage = 0, from = g.mine;
+    if (Y && a.w_post) {
+      const float s = group_sum(both(sum), a.group, g.id, g.thread, scratch[g.id][0][turn]);
+      const float r1 = rsqrtf(fmaf(s, inv_dim, a.eps));
+      if (g.thread == 0 && a.rstd_post) a.rstd_post[row] = r1;
+      scale *= r1;
     }
-    c1 = a.w_post ? c1 * inv_dim : 0.0f;
+    const F2 scale2 = pair(scale, scale);
+    sum = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (t + i * a.group) * 8;
-      if (c >= a.dim) continue;
+      Oct w;
+      if (Y) w = g.weights.get(true, i);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dz[i][e] = scale * (r1 * (dz[i][e] - v[i][e] * c1));
-      if (a.dy) store8(a.dy + row * a.lddy + c, dz[i]);
+      for (int k = 0; k < 4; ++k) {
+        const F2 xs = mul2(x[i].v[k], skip);
+        z[i].v[k] = Y ? fma2(mul2(z[i].v[k], w.v[k]), scale2, xs) : xs;
+        sum = fma2(z[i].v[k], z[i].v[k], sum);
+      }
+    }
+    if (a.x_out) {
+      T* const to = static_cast<T*>(a.x_out) + row * a.ldo;
+#pragma unroll
+      for (int i = 0; i < V; ++i) at.write(to, i, z[i]);
+    }
+    if (!a.h) continue;
+    const float s = group_sum(both(sum), a.group, g.id, g.thread, scratch[g.id][1][turn]);
+    const float r2 = rsqrtf(fmaf(s, inv_dim, a.eps));
+    if (g.thread == 0 && a.rstd_pre) a.rstd_pre[row] = r2;
+    const F2 r22 = pair(r2, r2);
+    uint16_t* const to = a.h + row * a.ldh;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const Oct w = g.weights.get(false, i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) z[i].v[k] = mul2(mul2(z[i].v[k], w.v[k]), r22);
+      at.write_bf16(to, i, z[i]);
     }
   }
-  float* const part = a.part + static_cast<int64_t>(blockIdx.x * groups + id) * 2 * a.dim;
+  copies_wait(1);
+}
+
+// Its gradient, dealt the same.  NORM: there is a norm behind (dh); Y: there is a block's output.
+template <typename T, int NT, bool NORM, bool Y>
+__global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(16) float scratch[kMaxGroups][2][3][32];  // three sums of a row, rows in turn
+  for (int i = threadIdx.x; i < kMaxGroups * 192; i += blockDim.x) (&scratch[0][0][0][0])[i] = 0.0f;
+  grid_dependency_wait();
+  const Setup<T, NT> g(smem, a.group, a.dim, a.w_post, a.gate, a.w_pre, a.w_f32);
+  const Layout<T>& at = g.at;
+  // of x_out, dh, y, d_out
+  constexpr int V = kV, kP = Layout<T>::kPieces, kDh = NORM ? kP : 0, kY = kDh + (NORM ? 1 : 0);
+  constexpr int kUp = kY + (Y ? 1 : 0), kPieces = kUp + kP;
+  const int pitch = g.pitch, step = gridDim.x * g.groups;
+  const float inv_dim = 1.0f / static_cast<float>(a.dim);
+  g.clear(a.stages * V * kPieces);
+  int64_t row = static_cast<int64_t>(blockIdx.x) * g.groups + g.id, next = row;
+  auto copy = [&](uint8_t* slot) {
+    if (next < a.n_rows) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = (t + i * a.group) * 8;
-    if (c >= a.dim) continue;
-    if (a.want_pre) store8(part + c, sum_pre[i]);
-    if (a.want_branch) store8(part + a.dim + c, sum_branch[i]);
+      for (int i = 0; i < V; ++i) {
+        uint8_t* const to = slot + i * kPieces * pitch;
+        if (NORM) {
+          at.copy(to, pitch, static_cast<const T*>(a.z) + next * a.ldz, i);
+          at.copy_bf16(to + kDh * pitch, a.dh + next * a.lddh, i);
+        }
+        if (Y) at.copy_bf16(to + kY * pitch, a.y + next * a.ldy, i);
+        if (a.d_out) at.copy(to + kUp * pitch, pitch, static_cast<const T*>(a.d_out) + next * a.lddo, i);
+      }
+    }
+    copies_commit();
+    next += step;
+  };
+#pragma unroll 1
+  for (int s = 0; s < a.stages; ++s) copy(g.mine + s * V * kPieces * pitch);
+  // a row's factors, read a row ahead
+  float r1 = 1.0f, r2 = 0.0f, scale = a.branch;
+  auto factors = [&](int64_t of) {
+    if (of >= a.n_rows) return;
+    if (NORM) r2 = a.rstd_pre[of];
+    if (Y && a.rstd_post) r1 = a.rstd_post[of];
+    if (Y && a.row_gate) scale = a.branch * a.row_gate[of];
+  };
+  factors(row);
+  if (g.id == 0) g.weights.fill();
+  __syncthreads();
+  Oct sum_pre[V] = {}, sum_branch[V] = {};
+  const F2 skip = pair(a.skip, a.skip);
+  uint8_t* slot = g.mine;
+  int stage = 0, turn = 0;
+#pragma unroll 1
+  for (; row < a.n_rows; row += step, turn ^= 1) {
+    const float now_r1 = r1, now_r2 = r2, now_scale = scale;
+    factors(row + step);
+    copies_wait(a.stages);
+    // e = d_out + r2 a, so that dz = e - r2 c2 v; the three sums of the row
+    Oct e[V], v[V];
+    F2 sum_av = 0, sum_es = 0, sum_vs = 0;
+    const F2 r12 = pair(now_r1, now_r1), r22 = pair(now_r2, now_r2);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint8_t* const from = slot + i * kPieces * pitch;
+      if (a.d_out) {
+        e[i] = at.read(from + kUp * pitch, pitch);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[i].v[k] = 0;
+      }
+      if (NORM) {
+        v[i] = at.read(from, pitch);
+        const Oct dh = at.read_bf16(from + kDh * pitch), w = g.weights.get(false, i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[i].v[k] = mul2(v[i].v[k], r22);
+          sum_pre[i].v[k] = fma2(dh.v[k], v[i].v[k], sum_pre[i].v[k]);
+          const F2 up = mul2(dh.v[k], w.v[k]);
+          sum_av = fma2(up, v[i].v[k], sum_av);
+          e[i].v[k] = fma2(up, r22, e[i].v[k]);
+        }
+      }
+      if (Y) {
+        const Oct y = at.read_bf16(from + kY * pitch), w = g.weights.get(true, i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const F2 ws = mul2(mul2(y.v[k], r12), w.v[k]);
+          sum_es = fma2(e[i].v[k], ws, sum_es);
+          if (NORM) sum_vs = fma2(v[i].v[k], ws, sum_vs);
+        }
+      }
+    }
+    float c2 = 0.0f, c1 = 0.0f;
+    if (NORM || (Y && (a.w_post || a.drow_gate))) {
+      float sums[3] = {both(sum_av), both(sum_es), both(sum_vs)};
+      group_sum3(sums, a.group, g.id, g.thread, scratch[g.id][turn][0]);
+      c2 = now_r2 * (inv_dim * sums[0]);
+      c1 = fmaf(-c2, sums[2], sums[1]);  // sum of gate w_post dz s
+      if (Y && g.thread == 0 && a.drow_gate) a.drow_gate[row] = a.branch * c1;
+      c1 = Y && a.w_post ? inv_dim * c1 : 0.0f;
+    }
+    const F2 minus_c2 = pair(-c2, -c2), minus_c1 = pair(-c1, -c1), scale2 = pair(now_scale, now_scale);
+    const F2 factor = pair(now_r1 * now_scale, now_r1 * now_scale);
+    T* const to_x = a.dx ? static_cast<T*>(a.dx) + row * a.lddx : nullptr;
+    uint16_t* const to_y = Y && a.dy ? a.dy + row * a.lddy : nullptr;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (NORM) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[i].v[k] = fma2(v[i].v[k], minus_c2, e[i].v[k]);  // dz
+      }
+      if (a.dx) {
+        Oct dx;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dx.v[k] = mul2(e[i].v[k], skip);
+        at.write(to_x, i, dx);
+      }
+      if (!Y) continue;
+      const Oct y = at.read_bf16(slot + (i * kPieces + kY) * pitch), w = g.weights.get(true, i);
+      Oct dy;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const F2 s = mul2(y.v[k], r12);
+        sum_branch[i].v[k] = fma2(mul2(e[i].v[k], scale2), s, sum_branch[i].v[k]);
+        dy.v[k] = mul2(fma2(s, minus_c1, mul2(e[i].v[k], w.v[k])), factor);
+      }
+      if (a.dy) at.write_bf16(to_y, i, dy);
+    }
+    copy(slot);  // into what has just been read
+    slot += V * kPieces * pitch;
+    if (++stage == a.stages) stage = 0, slot = g.mine;
+  }
+  copies_wait(1);
+  if (!a.want_pre && !a.want_branch) return;
+  // the groups' sums in order through shared memory, then the CTA's to the workspace
+  float* const sums = reinterpret_cast<float*>(g.ring);
+  float* const part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.dim;
+  for (int k = 0; k < g.groups; ++k) {
+    __syncthreads();  // also: every thread is through with the ring
+    if (g.id != k) continue;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (k > 0) {
+        const Oct p = at.read_f32(sums, i), q = at.read_f32(sums + a.dim, i);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          sum_pre[i].v[m] = add2(sum_pre[i].v[m], p.v[m]);
+          sum_branch[i].v[m] = add2(sum_branch[i].v[m], q.v[m]);
+        }
+      }
+      float* const to = k + 1 < g.groups ? sums : part;
+      if (NORM) at.write_f32(to, i, sum_pre[i]);
+      if (Y) at.write_f32(to + a.dim, i, sum_branch[i]);
+    }
   }
 }
 
@@ -288,59 +598,81 @@ struct NormSumArgs {
   float *dw_pre, *dw_post, *dgate;
 };
 
-__device__ __forceinline__ float weight1(const void* p, bool f32, int c) {
-  return f32 ? static_cast<const float*>(p)[c] : bf16_bits_to_float(static_cast<const uint16_t*>(p)[c]);
-}
-
-// The partial sums of 32 columns in order: 32 threads of columns by 8 runs of parts.
-__global__ void __launch_bounds__(256) block_norm_sum_kernel(const NormSumArgs a) {
-  __shared__ float s[2][8][32];
+// The CTAs' sums of 32 columns: a lane a column, 32 warps with 5 CTAs each (all their
+// loads at once: this kernel is one latency), joined in order.
+constexpr int kRun = kMaxParts / 32;
+__global__ void __launch_bounds__(1024) block_norm_sum_kernel(const NormSumArgs a) {
+  __shared__ float s[2][32][32];
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-  float pre = 0.0f, branch = 0.0f;
-  if (c < a.dim)
-    for (int p = run * a.parts / 8; p < (run + 1) * a.parts / 8; ++p) {
-      const float* const at = a.part + static_cast<int64_t>(p) * 2 * a.dim + c;
-      if (a.dw_pre) pre += at[0];
-      if (a.dw_post || a.dgate) branch += at[a.dim];
-    }
-  s[0][run][lane] = pre, s[1][run][lane] = branch;
+  const bool want_branch = a.dw_post || a.dgate;
+  float pre[kRun], branch[kRun];
+#pragma unroll
+  for (int k = 0; k < kRun; ++k) {
+    const int p = run * kRun + k;
+    const bool there = c < a.dim && p < a.parts;
+    const float* const at = a.part + static_cast<int64_t>(p) * 2 * a.dim + c;
+    pre[k] = there && a.dw_pre ? at[0] : 0.0f;
+    branch[k] = there && want_branch ? at[a.dim] : 0.0f;
+  }
+#pragma unroll
+  for (int k = 1; k < kRun; ++k) pre[0] += pre[k], branch[0] += branch[k];
+  s[0][run][lane] = pre[0], s[1][run][lane] = branch[0];
   __syncthreads();
   if (run > 0 || c >= a.dim) return;
-  for (int r = 1; r < 8; ++r) pre += s[0][r][lane], branch += s[1][r][lane];
-  if (a.dw_pre) a.dw_pre[c] = pre;
-  if (a.dw_post) a.dw_post[c] = a.gate ? branch * weight1(a.gate, a.w_f32, c) : branch;
-  if (a.dgate) a.dgate[c] = a.w_post ? branch * weight1(a.w_post, a.w_f32, c) : branch;
+  for (int r = 1; r < 32; ++r) pre[0] += s[0][r][lane], branch[0] += s[1][r][lane];
+  if (a.dw_pre) a.dw_pre[c] = pre[0];
+  if (a.dw_post) a.dw_post[c] = a.gate ? branch[0] * weight1(a.gate, a.w_f32, c) : branch[0];
+  if (a.dgate) a.dgate[c] = a.w_post ? branch[0] * weight1(a.w_post, a.w_f32, c) : branch[0];
 }
 
-// Threads of a row: 8 V elements a thread, whole warps.
-int group_of(int dim, int v) { return ((dim + 8 * v - 1) / (8 * v) + 31) / 32 * 32; }
-int groups_of(int group) { return std::max(1, std::min(kMaxGroups, 256 / group)); }
+// How a call's rows are dealt: threads of a row, rows of a CTA, CTAs, and rows on the way.
+struct Deal {
+  int group, groups, grid, stages, smem;
+};
+Deal deal(int n_rows, int dim, int threads, int pieces, int least_ring) {
+  Deal d;
+  const bool wide = dim > kWideDim;
+  d.group = ((dim + 8 * kV - 1) / (8 * kV) + 31) / 32 * 32;
+  d.groups = std::max(1, std::min(kMaxGroups, (wide ? 1024 : threads) / d.group));
+  // few rows are spread over the SMs, one to a CTA
+  d.groups = std::min(d.groups, std::max(1, (n_rows + sm_count() - 1) / sm_count()));
+  d.grid = std::max(1, std::min({(n_rows + d.groups - 1) / d.groups, sm_count(), kMaxParts}));
+  const int row = d.groups * d.group * kV * pieces * 16, weights = wide ? 0 : 2 * kV * 2 * 16 * d.group;
+  d.stages = std::max(1, std::min(kMaxStages, (kSharedBytes - weights) / row));
+  d.smem = weights + std::max(d.stages * row, least_ring);
+  return d;
+}
 
-int bwd_parts(int n_rows, int dim) {
-  const int groups = groups_of(group_of(dim, 2));
-  return std::max(1, std::min({(n_rows + groups - 1) / groups, 2 * sm_count(), kMaxParts / groups})) * groups;
+template <typename Args>
+int launch(void (*kernel)(Args), const Deal& d, const Args& a, int id, cudaStream_t s) {
+  KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kSharedBytes));
+  LaunchScope scope(id, s);
+  return launch_pdl(kernel, dim3(d.grid), dim3(d.groups * d.group), d.smem, s, a) == cudaSuccess ? TWELL_OK
+                                                                                                : TWELL_ERR_CUDA;
 }
 
 template <typename T>
 int launch_norm(NormArgs a, cudaStream_t s) {
-  a.group = group_of(a.dim, 2);
-  const int groups = groups_of(a.group);
-  LaunchScope scope(TWELL_KERNEL_BLOCK_NORM, s);
-  return launch_pdl(block_norm_kernel<T, 2>, dim3((a.n_rows + groups - 1) / groups), dim3(groups * a.group), 0, s,
-                    a) == cudaSuccess
-             ? TWELL_OK
-             : TWELL_ERR_CUDA;
+  const Deal d = deal(a.n_rows, a.dim, kThreads, Layout<T>::kPieces + (a.y ? 1 : 0), 0);
+  a.group = d.group, a.stages = d.stages;
+  const auto kernel = a.dim > kWideDim ? (a.y ? block_norm_kernel<T, 1024, true> : block_norm_kernel<T, 1024, false>)
+                                       : (a.y ? block_norm_kernel<T, kThreads, true> : block_norm_kernel<T, kThreads, false>);
+  return launch(kernel, d, a, TWELL_KERNEL_BLOCK_NORM, s);
+}
+
+template <typename T, int NT>
+auto bwd_kernel(const NormBwdArgs& a) {
+  if (a.dh) return a.y ? block_norm_bwd_kernel<T, NT, true, true> : block_norm_bwd_kernel<T, NT, true, false>;
+  return a.y ? block_norm_bwd_kernel<T, NT, false, true> : block_norm_bwd_kernel<T, NT, false, false>;
 }
 
 template <typename T>
-int launch_norm_bwd(NormBwdArgs a, int parts, cudaStream_t s) {
-  a.group = group_of(a.dim, 2);
-  const int groups = groups_of(a.group);
-  LaunchScope scope(TWELL_KERNEL_BLOCK_NORM_BWD, s);
-  return launch_pdl(block_norm_bwd_kernel<T, 2>, dim3(parts / groups), dim3(groups * a.group), 0, s, a) == cudaSuccess
-             ? TWELL_OK
-             : TWELL_ERR_CUDA;
+int launch_norm_bwd(NormBwdArgs a, int* parts, cudaStream_t s) {
+  const Deal d = deal(a.n_rows, a.dim, kBwdThreads, Layout<T>::kPieces * (a.dh ? 2 : 1) + (a.dh ? 1 : 0) + (a.y ? 1 : 0),
+                      2 * a.dim * 4);
+  a.group = d.group, a.stages = d.stages, *parts = d.grid;
+  return launch(a.dim > kWideDim ? bwd_kernel<T, 1024>(a) : bwd_kernel<T, kBwdThreads>(a), d, a, TWELL_KERNEL_BLOCK_NORM_BWD, s);
 }
 
 bool finite(float x) { return x - x == 0.0f; }
@@ -387,7 +719,7 @@ extern "C" TWELL_API int twell_block_norm(const void* x, int32_t dtype, int64_t 
   }
   if (!device_is_sm103()) return TWELL_ERR_NO_DEVICE;
   if (n_rows == 0) return TWELL_OK;
-  const NormArgs a{x,    y,      x_out, h,     ldx,  ldy,    ldo,   ldh, n_rows,    d_model, 0, w_post,
+  const NormArgs a{x,    y,      x_out, h,     ldx,  ldy,    ldo,   ldh, n_rows,    d_model, 0, 0, w_post,
                    gate, w_pre,  w_dtype == TWELL_F32, row_gate, skip_scale, branch_scale, eps, rstd_post, rstd_pre};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return dtype == TWELL_BF16 ? launch_norm<uint16_t>(a, s) : launch_norm<float>(a, s);
@@ -437,19 +769,19 @@ extern "C" TWELL_API int twell_block_norm_bwd(const uint16_t* dh, int64_t lddh, 
   }
   if (!device_is_sm103()) return TWELL_ERR_NO_DEVICE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int parts = n_rows > 0 ? bwd_parts(n_rows, d_model) : 0;
+  int parts = 0;
   if (n_rows > 0) {
     const NormBwdArgs a{dh,     d_out,   x_out, y,      dx,   dy,    lddh,  lddo,
-                        ldo,    ldy,     lddx,  lddy,   n_rows, d_model, 0, w_post, gate, w_pre,
+                        ldo,    ldy,     lddx,  lddy,   n_rows, d_model, 0, 0, w_post, gate, w_pre,
                         w_dtype == TWELL_F32, row_gate, skip_scale, branch_scale, rstd_post, rstd_pre,
                         drow_gate, dw_pre != nullptr, dw_post || dgate, static_cast<float*>(workspace)};
-    KV_TRY(dtype == TWELL_BF16 ? launch_norm_bwd<uint16_t>(a, parts, s) : launch_norm_bwd<float>(a, parts, s));
+    KV_TRY(dtype == TWELL_BF16 ? launch_norm_bwd<uint16_t>(a, &parts, s) : launch_norm_bwd<float>(a, &parts, s));
   }
   if (!sums) return TWELL_OK;
   const NormSumArgs a{static_cast<const float*>(workspace), parts, d_model, w_post, gate, w_dtype == TWELL_F32,
                       dw_pre, dw_post, dgate};
   LaunchScope scope(TWELL_KERNEL_BLOCK_NORM_BWD, s);
-  return launch_pdl(block_norm_sum_kernel, dim3((d_model + 31) / 32), dim3(256), 0, s, a) == cudaSuccess
+  return launch_pdl(block_norm_sum_kernel, dim3((d_model + 31) / 32), dim3(1024), 0, s, a) == cudaSuccess
              ? TWELL_OK
              : TWELL_ERR_CUDA;
 }
