@@ -17,6 +17,13 @@
 // operands by TMA into 128-byte swizzled stages, accumulators twice in TMEM, one
 // warp for the copies, one for the MMAs, eight for the epilogue.  The two gradient products read
 // G and H or W along their rows, so those operands go in M- or N-major.
+// A pair of CTAs shares a tile of 256 x 256 (each keeps half of either operand and half of the
+// rows' sums), which halves what shared memory feeds to the tensor cores; up to 128 rows there is
+// nothing for a second CTA, and a CTA takes 128 x 256 alone.
+//
+// The tensor cores cut off what does not fit when they add, one step in 16 products, so a
+// logit of d = 4096 would come out 4e-6 too near to zero.  The forward pass, whose results are
+// fp32, adds up runs of 256 products in registers instead, rounding to nearest, while the next run is multiplied.
 #include <algorithm>
 
 #include "kv_internal.h"
@@ -24,14 +31,24 @@
 namespace twell {
 namespace {
 
-constexpr int kBM = 128, kBN = 256, kBK = 64, kUmmaK = 16;
-constexpr int kStages = 4;
-constexpr int kThreads = 384, kEpiThreads = 256;
-constexpr uint32_t kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2;
-constexpr uint32_t kPipeBytes = kStages * (kABytes + kBBytes);
+constexpr int kBM = 128, kBN = 256, kBK = 64, kUmmaK = 16;  // kBM: rows of a CTA
+constexpr int kThreads = 384, kEpiWarps = 8;
+// Registers of the forward pass, whose epilogue holds 128 sums a thread.
+constexpr int kRegs = 168, kRegsRest = 56, kRegsEpilogue = 224;
+static_assert(128 * kRegsRest + 256 * kRegsEpilogue <= kThreads * kRegs, "register split");
+constexpr int kRun = 8;  // steps of K that the forward pass adds up in tensor memory
 constexpr uint32_t kBarBytes = 256;
 constexpr uint32_t kEpiBytes = 2 * 128 * 3 * sizeof(float);  // one half's sums, for the other half
-constexpr uint32_t kSmemBytes = 1024 + kPipeBytes + kBarBytes + kEpiBytes;
+
+// R CTAs to a tile.
+template <int R>
+struct Cfg {
+  static constexpr int kStages = R == 1 ? 4 : 6;
+  static constexpr uint32_t kABytes = kBM * kBK * 2, kBBytes = kBN / R * kBK * 2;  // of a CTA
+  static constexpr uint32_t kPipeBytes = kStages * (kABytes + kBBytes);
+  static constexpr uint32_t kSmemBytes = 1024 + kPipeBytes + kBarBytes + kEpiBytes;
+};
+constexpr int kBandWide = 64, kBandDh = 8, kBandDw = 8;
 constexpr int kMaxJobs = 3;
 constexpr int kPlanSms = 152;            // plans do not depend on the device, workspaces neither
 constexpr int64_t kPieceBytes = 1 << 27; // of G: what the L2 cache can hold
@@ -48,7 +65,7 @@ struct Job {
   int num_m, num_n, num_k;  // tiles, steps of K
   int ksplit;
   int col0;                 // first vocabulary column of the piece
-  int units;
+  int units, band;          // tiles, rows of tiles that are taken together
   int a_mn, b_mn;           // operand stored [K][M] / [K][N]
   int add, round;           // dH: earlier pieces have left sums; these are the last
 };
@@ -84,24 +101,93 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The shared memory of another CTA of the cluster.
+__device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The tensor-core operations of a CTA alone and of a pair, whose first CTA issues for both.
+template <int R>
+struct Tc;
+template <>
+struct Tc<1> {
+  static __device__ __forceinline__ void alloc(uint32_t* holder) { tmem_alloc(holder, 512); }
+  static __device__ __forceinline__ void dealloc(uint32_t base) { tmem_dealloc(base, 512); }
+  static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    mma_bf16(d, a, b, idesc, add);
+  }
+  static __device__ __forceinline__ void commit(uint64_t* bar) { mma_commit(bar); }
+  static __device__ __forceinline__ void sync() { __syncthreads(); }
+};
+template <>
+struct Tc<2> {
+  static __device__ __forceinline__ void alloc(uint32_t* holder) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(holder)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  static __device__ __forceinline__ void dealloc(uint32_t base) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(512) : "memory");
+  }
+  static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+  }
+  // arrives at the same barrier of both CTAs
+  static __device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  }
+  static __device__ __forceinline__ void sync() { cluster_sync(); }
+};
+
+// Two fp32 lanes of one instruction.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 lanes(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
-}
-
-// Element i of 32, by a tree of selections (an indexed array would go to local memory).
-__device__ __forceinline__ float pick(const uint32_t (&r)[32], int i) {
-  uint32_t a[16], b[8], c[4], d[2];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) a[k] = (i & 16) ? r[k + 16] : r[k];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) b[k] = (i & 8) ? a[k + 8] : a[k];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) c[k] = (i & 4) ? b[k + 4] : b[k];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) d[k] = (i & 2) ? c[k + 2] : c[k];
-  return __uint_as_float((i & 1) ? d[1] : d[0]);
 }
 
 // A row's running sums in base 2 relative to m (as y = acc c).
@@ -130,38 +216,63 @@ struct Tile {
   bool valid;        // the row exists
 };
 
+// A thread's share of a tile: its row's logits (unscaled) of half of the columns, two a word.
+struct Half {
+  F2 v[kBN / 4];
+};
+
+// Adds a run's sums to those of the runs before.
+__device__ __forceinline__ void add_run(Half& x, uint32_t taddr) {
+#pragma unroll
+  for (int k = 0; k < kBN / 2; k += 32) {
+    uint32_t r[32];
+    tmem_ld32(taddr + k, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      x.v[k / 2 + i] = add2(x.v[k / 2 + i], pair(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
+  }
+}
+
 // Sums of the tile's columns; both halves of a row are joined through shared memory.
-__device__ __forceinline__ void epilogue_sums(const Args& a, const Job& j, const Tile& t, int n_blk, float* shared,
-                                              int turn) {
+__device__ __forceinline__ void epilogue_sums(const Args& a, const Job& j, const Tile& t, int n_blk, Half& x,
+                                              float* shared, int turn) {
   const float c = a.inv_t * kLog2e;
   const int target = t.valid && a.targets ? a.targets[t.row] : -1;
-  Sums all;
-#pragma unroll 1
-  for (int k = t.half * (kBN / 2); k < (t.half + 1) * (kBN / 2); k += 32) {
-    uint32_t r[32];
-    tmem_ld32(t.taddr + k, r);
-    tmem_ld_wait();
-    const int col = t.col0 + k, left = j.n - col;
-    if (left <= 0) break;  // the same for all threads of the CTA
-    if (left < 32) {
+  const int col = t.col0 + t.half * (kBN / 2), left = j.n - col;
+  if (left < kBN / 2) {  // columns past the vocabulary
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i >= left) r[i] = 0xFF800000u;
+    for (int i = 0; i < kBN / 4; ++i) {
+      const float2 f = lanes(x.v[i]);
+      x.v[i] = pair(2 * i < left ? f.x : -INFINITY, 2 * i + 1 < left ? f.y : -INFINITY);
     }
-    if (target >= col && target < col + 32) a.of_target[t.row] = pick(r, target - col) * a.inv_t;
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(r[i]));
-    const float m = top * c, ref = m == -INFINITY ? 0.0f : m;
-    float s = 0.0f, u = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float y = fmaf(__uint_as_float(r[i]), c, -ref), e = ex2(y);
-      s += e;
-      u = fmaf(e, fmaxf(y, -1e30f), u);  // 0 for an entry of -inf
-    }
-    all.join(m, s, u);
   }
+  if (target >= col && target < col + min(left, kBN / 2)) {
+    F2 own = 0;
+#pragma unroll
+    for (int i = 0; i < kBN / 4; ++i)  // in asm: as C++ it becomes an indexed read, and x goes to local memory
+      asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %2, %3;\n\t@p mov.b64 %0, %1;\n\t}"
+          : "+l"(own)
+          : "l"(x.v[i]), "r"((target - col) / 2), "r"(i));
+    a.of_target[t.row] = ((target - col) & 1 ? lanes(own).y : lanes(own).x) * a.inv_t;
+  }
+  Sums all;
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kBN / 4; ++i) top = fmaxf(top, fmaxf(lanes(x.v[i]).x, lanes(x.v[i]).y));
+  all.m = top * c;
+  const float ref = all.m == -INFINITY ? 0.0f : all.m;
+  const F2 c2 = pair(c, c), minus = pair(-ref, -ref);
+  F2 s[2] = {0, 0}, u[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < kBN / 4; ++i) {
+    const float2 y = lanes(fma2(x.v[i], c2, minus));
+    const F2 e = pair(ex2(y.x), ex2(y.y));
+    s[i & 1] = add2(s[i & 1], e);
+    u[i & 1] = fma2(e, pair(fmaxf(y.x, -1e30f), fmaxf(y.y, -1e30f)), u[i & 1]);  // 0 for an entry of -inf
+  }
+  const float2 sums = lanes(add2(s[0], s[1])), shifted = lanes(add2(u[0], u[1]));
+  all.s = sums.x + sums.y, all.u = shifted.x + shifted.y;
   float* const at = shared + turn * 128 * 3 + (t.lg * 32 + (threadIdx.x & 31)) * 3;
   if (t.half == 1) at[0] = all.m, at[1] = all.s, at[2] = all.u;
   asm volatile("bar.sync %0, 64;" ::"r"(t.lg + 1) : "memory");
@@ -256,194 +367,245 @@ struct Unit {
   int job, m_blk, n_blk, ks, kb0, kb1;
 };
 
-// The u-th tile of the launch: jobs one after the other, m fastest, so that CTAs working side by
-// side share the columns' operand and all rows stay in L2.
+// The u-th tile of the launch: jobs one after the other; in a job K's ranges, then bands of rows
+// of tiles, in a band the rows fastest.
 __device__ __forceinline__ Unit unit_of(const Args& a, int u) {
   int i = 0;
   while (i + 1 < a.num_jobs && u >= a.job[i].units) u -= a.job[i++].units;
   const Job& j = a.job[i];
   Unit x;
   x.job = i;
-  x.m_blk = u % j.num_m;
-  u /= j.num_m;
-  x.n_blk = u % j.num_n;
-  x.ks = u / j.num_n;
+  x.ks = u / (j.num_m * j.num_n);
+  u -= x.ks * j.num_m * j.num_n;
+  const int band = u / (j.band * j.num_n), rows = min(j.band, j.num_m - band * j.band);
+  u -= band * j.band * j.num_n;
+  x.n_blk = u / rows;
+  x.m_blk = band * j.band + u - x.n_blk * rows;
   x.kb0 = static_cast<int>(static_cast<int64_t>(x.ks) * j.num_k / j.ksplit);
   x.kb1 = static_cast<int>(static_cast<int64_t>(x.ks + 1) * j.num_k / j.ksplit);
   return x;
 }
 
+// R CTAs a tile; SUMS: the forward pass (its one job), else the jobs of the backward pass.
+template <int R, bool SUMS>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
-  constexpr int S = kStages;
+  using C = Cfg<R>;
+  constexpr int S = C::kStages;
   grid_dependency_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const sA = smem;
-  uint8_t* const sB = smem + S * kABytes;
-  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + kPipeBytes);
+  uint8_t* const sB = smem + S * C::kABytes;
+  // of the first CTA: full, tempty (and its own of the others); of both: empty, tfull
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + C::kPipeBytes);
   uint64_t* const empty = full + S;
   uint64_t* const tfull = empty + S;
   uint64_t* const tempty = tfull + 2;
   uint64_t* const drain = tempty + 2;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* const abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* const issued = const_cast<int*>(abort) + 1;  // [S] parity of the last fill of each stage, -1: none
-  float* const epi = reinterpret_cast<float*>(smem + kPipeBytes + kBarBytes);
-  static_assert((2 * S + 5) * 8 + 8 + S * 4 <= static_cast<int>(kBarBytes), "barrier region");
+  float* const epi = reinterpret_cast<float*>(smem + C::kPipeBytes + kBarBytes);
+  static_assert((2 * S + 5) * 8 + 8 <= static_cast<int>(kBarBytes), "barrier region");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = R == 1 ? 0 : static_cast<int>(cluster_rank());
+  const int first = blockIdx.x / R, stride = gridDim.x / R;
   int units = 0;
   for (int i = 0; i < a.num_jobs; ++i) units += a.job[i].units;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], rank == 0 ? R : 1);  // the first CTA's own copies, and word of the second one's
       mbar_init(&empty[s], 1);
-      issued[s] = -1;
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], kEpiThreads);
+      mbar_init(&tempty[i], R * kEpiWarps);
     }
     mbar_init(drain, 1);
     *abort = 0;
     mbar_fence_init();
   }
   if (warp == 0 && lane < 2 * a.num_jobs) tma_prefetch_desc(lane & 1 ? &maps.b[lane >> 1] : &maps.a[lane >> 1]);
-  if (warp == 2) tmem_alloc(tmem_holder, 512);
+  __syncwarp();
+  if (warp == 2) Tc<R>::alloc(tmem_holder);
   tc_fence_before();
-  __syncthreads();
+  Tc<R>::sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const uint64_t limit = a.wait_limit_ns;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    if (SUMS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == 0 && lane == 0) {
       // ---------------- copies
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      for (int u = first; ok && u < units; u += stride) {
         const Unit x = unit_of(a, u);
         const Job& j = a.job[x.job];
         const CUtensorMap* const ma = &maps.a[x.job];
         const CUtensorMap* const mb = &maps.b[x.job];
+        const int m0 = (x.m_blk * R + rank) * kBM, n0 = x.n_blk * kBN + rank * (kBN / R);
         for (int kb = x.kb0; kb < x.kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, limit, abort)) {
             ok = false;
             break;
           }
-          uint8_t* const da = sA + stage * kABytes;
-          uint8_t* const db = sB + stage * kBBytes;
-          mbar_arrive_expect_tx(&full[stage], kABytes + kBBytes);
+          uint8_t* const da = sA + stage * C::kABytes;
+          uint8_t* const db = sB + stage * C::kBBytes;
+          mbar_arrive_expect_tx(&full[stage], C::kABytes + C::kBBytes);
+          uint64_t* const bar = &full[stage];
           if (j.a_mn) {  // [K][M]: boxes of 64 columns by 64 rows of K
 #pragma unroll
-            for (int q = 0; q < kBM / 64; ++q)
-              tma_load_2d(da + q * 8192, ma, &full[stage], x.m_blk * kBM + q * 64, kb * kBK);
+            for (int q = 0; q < kBM / 64; ++q) tma_load_2d(da + q * 8192, ma, bar, m0 + q * 64, kb * kBK);
           } else {
-            tma_load_2d(da, ma, &full[stage], kb * kBK, x.m_blk * kBM);
+            tma_load_2d(da, ma, bar, kb * kBK, m0);
           }
           if (j.b_mn) {
 #pragma unroll
-            for (int q = 0; q < kBN / 64; ++q)
-              tma_load_2d(db + q * 8192, mb, &full[stage], x.n_blk * kBN + q * 64, kb * kBK);
+            for (int q = 0; q < kBN / R / 64; ++q) tma_load_2d(db + q * 8192, mb, bar, n0 + q * 64, kb * kBK);
           } else {
-            tma_load_2d(db, mb, &full[stage], kb * kBK, x.n_blk * kBN);
+            tma_load_2d(db, mb, bar, kb * kBK, n0);
           }
-          issued[stage] = static_cast<int>(phase);
           if (++stage == S) stage = 0, phase ^= 1u;
         }
       }
       if (!ok) {
         report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
-        for (int s = 0; s < S; ++s)  // the copies in flight land before the CTA leaves
-          if (issued[s] >= 0) {
-            volatile int never = 0;
-            mbar_wait(&full[s], static_cast<uint32_t>(issued[s]), 10000000ull, &never);
-          }
+        // the copies in flight land before the CTA leaves
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 10000000ull) __nanosleep(1000);
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1 && lane == 0 && rank == 0) {
       // ---------------- products
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      for (int u = first; ok && u < units; u += stride) {
         const Unit x = unit_of(a, u);
         const Job& j = a.job[x.job];
-        const uint32_t idesc = idesc_bf16_f32(kBM, kBN) | (j.a_mn ? 1u << 15 : 0u) | (j.b_mn ? 1u << 16 : 0u);
+        const uint32_t idesc = idesc_bf16_f32(kBM * R, kBN) | (j.a_mn ? 1u << 15 : 0u) | (j.b_mn ? 1u << 16 : 0u);
         // a step of 16 along K: 32 bytes of a K-major row, 16 rows of 128 bytes of the others
         const uint64_t a_step = j.a_mn ? 128u : 2u, b_step = j.b_mn ? 128u : 2u;
-        if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, limit, abort)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kBN);
-        for (int kb = x.kb0; kb < x.kb1; ++kb) {
-          if (!mbar_wait(&full[stage], phase, limit, abort)) {
+        for (int k0 = x.kb0; ok && k0 < x.kb1;) {
+          const int k1 = SUMS ? min(k0 + kRun, x.kb1) : x.kb1;
+          if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, limit, abort)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t pa = smem_u32(sA + stage * kABytes), pb = smem_u32(sB + stage * kBBytes);
-          const uint64_t ad = j.a_mn ? smem_desc_sw128_nmajor(pa, 8192) : smem_desc_sw128(pa);
-          const uint64_t bd = j.b_mn ? smem_desc_sw128_nmajor(pb, 8192) : smem_desc_sw128(pb);
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kBN);
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait(&full[stage], phase, limit, abort)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t pa = smem_u32(sA + stage * C::kABytes), pb = smem_u32(sB + stage * C::kBBytes);
+            const uint64_t ad = j.a_mn ? smem_desc_sw128_nmajor(pa, 8192) : smem_desc_sw128(pa);
+            const uint64_t bd = j.b_mn ? smem_desc_sw128_nmajor(pb, 8192) : smem_desc_sw128(pb);
 #pragma unroll
-          for (int k = 0; k < kBK / kUmmaK; ++k)
-            mma_bf16(d, ad + k * a_step, bd + k * b_step, idesc, (kb > x.kb0 || k > 0) ? 1u : 0u);
-          mma_commit(&empty[stage]);
-          if (++stage == S) stage = 0, phase ^= 1u;
+            for (int k = 0; k < kBK / kUmmaK; ++k)
+              Tc<R>::mma(d, ad + k * a_step, bd + k * b_step, idesc, (kb > k0 || k > 0) ? 1u : 0u);
+            Tc<R>::commit(&empty[stage]);
+            if (++stage == S) stage = 0, phase ^= 1u;
+          }
+          if (!ok) break;
+          Tc<R>::commit(&tfull[acc]);
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
+          k0 = k1;
         }
-        if (!ok) break;
-        mma_commit(&tfull[acc]);
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
       }
       if (!ok) {
         report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
-        mma_commit(drain);  // the MMAs already issued end before TMEM is released
+        Tc<R>::commit(drain);  // the MMAs already issued end before TMEM is released
         volatile int never = 0;
         mbar_wait(drain, 0, 10000000ull, &never);
       }
     }
-  } else if (warp >= 4) {
+    if (R == 2 && warp == 3 && lane == 0 && rank == 1) {
+      // ---------------- word to the first CTA that the second one's copies have landed (counted there by the
+      // copies themselves, their many completions cross over one by one: 8192 x 2048 x 32768 in 712 us, not 630)
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = first; ok && u < units; u += stride) {
+        const Unit x = unit_of(a, u);
+        for (int kb = x.kb0; kb < x.kb1; ++kb) {
+          ok = mbar_wait(&full[stage], phase, limit, abort);
+          if (!ok) break;
+          arrive_at(map_rank(&full[stage], 0));
+          if (++stage == S) stage = 0, phase ^= 1u;
+        }
+      }
+      if (!ok) report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
+    }
+    __syncwarp();
+  } else {
     // ---------------- epilogue: thread = row of the tile (a TMEM lane), two warps share a row's columns
+    if (SUMS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpilogue));
     Tile t;
     t.lg = warp & 3;
     t.half = (warp - 4) >> 2;
-    int acc = 0;
+    int acc = 0, turn = 0;
     uint32_t acc_phase = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    bool ok = true;
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(t.lg * 32) << 16);
+    for (int u = first; ok && u < units; u += stride) {
       const Unit x = unit_of(a, u);
       const Job& j = a.job[x.job];
-      if (!mbar_wait(&tfull[acc], acc_phase, limit, abort)) {
-        report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
-        break;
-      }
-      tc_fence_after();
-      t.row = x.m_blk * kBM + t.lg * 32 + lane;
+      t.row = (x.m_blk * R + rank) * kBM + t.lg * 32 + lane;
       t.col0 = x.n_blk * kBN;
       t.valid = t.row < j.m;
-      t.taddr = tmem_base + (static_cast<uint32_t>(t.lg * 32) << 16) + static_cast<uint32_t>(acc * kBN);
-      if (j.type == kJobSums)
-        epilogue_sums(a, j, t, x.n_blk, epi, acc);
-      else if (j.type == kJobGrad)
-        epilogue_grad(a, j, t);
-      else
-        epilogue_store(a, j, t, x.ks);
-      tc_fence_before();
-      mbar_arrive(&tempty[acc]);
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
+      auto wait_full = [&]() {
+        ok = mbar_wait(&tfull[acc], acc_phase, limit, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
+        tc_fence_after();
+        t.taddr = lane_base + static_cast<uint32_t>(acc * kBN);
+        return ok;
+      };
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (R == 1)
+            mbar_arrive(&tempty[acc]);
+          else
+            arrive_at(map_rank(&tempty[acc], 0));
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      };
+      if constexpr (SUMS) {
+        Half sums = {};
+#pragma unroll 1
+        for (int k0 = x.kb0; k0 < x.kb1; k0 += kRun) {
+          if (!wait_full()) break;
+          add_run(sums, t.taddr + t.half * (kBN / 2));
+          release();
+        }
+        if (!ok) break;
+        epilogue_sums(a, j, t, x.n_blk, sums, epi, turn);
+        turn ^= 1;
+      } else {
+        if (!wait_full()) break;
+        if (j.type == kJobGrad)
+          epilogue_grad(a, j, t);
+        else
+          epilogue_store(a, j, t, x.ks);
+        release();
+      }
     }
   }
   tc_fence_before();
-  __syncthreads();
+  Tc<R>::sync();
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
+    Tc<R>::dealloc(tmem_base);
   }
 }
 
@@ -540,10 +702,14 @@ size_t fwd_bytes(int64_t n_rows, int64_t vocab) {
   return round_up(static_cast<size_t>(n_rows) * 4 * (3 * ceil_div(vocab, kBN) + 1), 256) + 256;
 }
 
+// CTAs to a tile: a pair from 129 rows on.
+int ctas_of(int n_rows) { return n_rows > kBM ? 2 : 1; }
+
 // A: [m][k], or [k][m] with mn; likewise B.  rows of either lie ld elements apart.
-int set_job(Maps* maps, Args* args, Job j, const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb, int k) {
+int set_job(Maps* maps, Args* args, int ctas, Job j, const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb,
+            int k) {
   const int i = args->num_jobs++;
-  j.num_m = ceil_div(j.m, kBM), j.num_n = ceil_div(j.n, kBN), j.num_k = ceil_div(k, kBK);
+  j.num_m = ceil_div(j.m, kBM * ctas), j.num_n = ceil_div(j.n, kBN), j.num_k = ceil_div(k, kBK);
   j.ksplit = std::min(j.ksplit, j.num_k);
   const int64_t units = static_cast<int64_t>(j.num_m) * j.num_n * j.ksplit;
   if (units > (1 << 29)) return TWELL_ERR_UNSUPPORTED;
@@ -554,18 +720,38 @@ int set_job(Maps* maps, Args* args, Job j, const uint16_t* A, int64_t lda, const
   else
     KV_TRY(encode_tmap_2d(&maps->a[i], A, k, j.m, lda * 2, kBK, kBM));
   if (j.b_mn) return encode_tmap_2d(&maps->b[i], B, j.n, k, ldb * 2, 64, kBK);
-  return encode_tmap_2d(&maps->b[i], B, k, j.n, ldb * 2, kBK, kBN);
+  return encode_tmap_2d(&maps->b[i], B, k, j.n, ldb * 2, kBK, kBN / ctas);
 }
 
-int launch_jobs(const Maps& maps, const Args& args, int kernel_id, cudaStream_t s) {
-  KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(linear_kernel), static_cast<int>(kSmemBytes)));
+template <int R, bool SUMS>
+int launch_jobs(const Maps& maps, const Args& args, cudaStream_t s) {
+  const auto kernel = linear_kernel<R, SUMS>;
+  constexpr uint32_t smem = Cfg<R>::kSmemBytes;
+  KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem)));
+  if (SUMS) {  // the split above waits for registers that only a launch with kRegs a thread has
+    static const int regs = [&] {
+      cudaFuncAttributes f;
+      return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs < kRegs) return TWELL_ERR_CUDA;
+  }
   int64_t units = 0;
   for (int i = 0; i < args.num_jobs; ++i) units += args.job[i].units;
-  const int grid = static_cast<int>(std::min<int64_t>(units, sm_count()));
-  LaunchScope scope(kernel_id, s);
-  return launch_pdl(linear_kernel, dim3(grid), dim3(kThreads), kSmemBytes, s, maps, args) == cudaSuccess
-             ? TWELL_OK
-             : TWELL_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units, sm_count() / R)) * R);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = R;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  LaunchScope scope(SUMS ? TWELL_KERNEL_LINEAR_LOGPROBS : TWELL_KERNEL_LINEAR_LOGPROBS_BWD, s);
+  return cudaLaunchKernelEx(&cfg, kernel, maps, args) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }
 
 int check_linear(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw, int n_rows, int d, int vocab,
@@ -619,9 +805,10 @@ extern "C" TWELL_API int twell_linear_logprobs(const uint16_t* H, int64_t ldh, c
   a.of_target = static_cast<float*>(workspace);
   a.part = a.of_target + n_rows;
   Job j = {};
-  j.type = kJobSums, j.m = n_rows, j.n = vocab, j.ksplit = 1;
-  KV_TRY(set_job(&maps, &a, j, H, ldh, W, ldw, d_model));
-  KV_TRY(launch_jobs(maps, a, TWELL_KERNEL_LINEAR_LOGPROBS, s));
+  j.type = kJobSums, j.band = kBandWide, j.m = n_rows, j.n = vocab, j.ksplit = 1;
+  const int ctas = ctas_of(n_rows);
+  KV_TRY(set_job(&maps, &a, ctas, j, H, ldh, W, ldw, d_model));
+  KV_TRY((ctas == 2 ? launch_jobs<2, true>(maps, a, s) : launch_jobs<1, true>(maps, a, s)));
   const JoinArgs join{a.part, a.of_target, a.job[0].num_n, n_rows, vocab, targets, logprob, entropy, lse};
   LaunchScope scope(TWELL_KERNEL_LINEAR_LOGPROBS, s);
   return launch_pdl(linear_join_kernel, dim3(ceil_div(n_rows, 32)), dim3(kJoinWarps * 32), 0, s, join) == cudaSuccess
@@ -673,6 +860,7 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
   base.dh_sum = reinterpret_cast<float*>(ws + plan.grad_bytes * (plan.pieces > 1 ? 2 : 1));
   base.dh = dH, base.lddh = lddh, base.dw = dW, base.lddw = lddw;
   base.status = status, base.wait_limit_ns = kWaitLimitNs;
+  const int ctas = ctas_of(n_rows);
   for (int p = 0; p <= plan.pieces; ++p) {
     Maps maps;
     Args a = base;
@@ -683,24 +871,24 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
       Job j = {};
       j.col0 = col0, j.add = p > 1, j.round = p == plan.pieces && plan.ksplit == 1;
       if (dH) {
-        j.type = kJobDHidden, j.m = n_rows, j.n = d_model, j.b_mn = 1;
+        j.type = kJobDHidden, j.band = kBandDh, j.m = n_rows, j.n = d_model, j.b_mn = 1;
         // the first piece fills all ranges' sums; a narrower last one adds to no more than it has steps
         j.ksplit = plan.ksplit;
-        KV_TRY(set_job(&maps, &a, j, G, plan.piece, Wp, ldw, width));
+        KV_TRY(set_job(&maps, &a, ctas, j, G, plan.piece, Wp, ldw, width));
       }
       if (dW) {
-        j.type = kJobDWeight, j.m = width, j.n = d_model, j.a_mn = j.b_mn = 1, j.ksplit = 1;
-        KV_TRY(set_job(&maps, &a, j, G, plan.piece, H, ldh, n_rows));
+        j.type = kJobDWeight, j.band = kBandDw, j.m = width, j.n = d_model, j.a_mn = j.b_mn = 1, j.ksplit = 1;
+        KV_TRY(set_job(&maps, &a, ctas, j, G, plan.piece, H, ldh, n_rows));
       }
     }
     if (p < plan.pieces) {  // G of piece p
       const int col0 = p * plan.piece;
       Job j = {};
-      j.type = kJobGrad, j.m = n_rows, j.n = std::min(plan.piece, vocab - col0), j.ksplit = 1, j.col0 = col0;
+      j.type = kJobGrad, j.band = kBandWide, j.m = n_rows, j.n = std::min(plan.piece, vocab - col0), j.ksplit = 1, j.col0 = col0;
       a.grad = buffer[p & 1];
-      KV_TRY(set_job(&maps, &a, j, H, ldh, W + static_cast<int64_t>(col0) * ldw, ldw, d_model));
+      KV_TRY(set_job(&maps, &a, ctas, j, H, ldh, W + static_cast<int64_t>(col0) * ldw, ldw, d_model));
     }
-    KV_TRY(launch_jobs(maps, a, TWELL_KERNEL_LINEAR_LOGPROBS_BWD, s));
+    KV_TRY((ctas == 2 ? launch_jobs<2, false>(maps, a, s) : launch_jobs<1, false>(maps, a, s)));
   }
   if (!dH || plan.ksplit == 1) return TWELL_OK;
   const ReduceArgs r{base.dh_sum, plan.ksplit, n_rows, d_model, dH, lddh};
