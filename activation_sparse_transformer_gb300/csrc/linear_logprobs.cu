@@ -31,24 +31,20 @@
 namespace twell {
 namespace {
 
-constexpr int kBM = 128, kBN = 256, kBK = 64, kUmmaK = 16;  // kBM: rows of a CTA
+constexpr int kBM = 128, kMinBN = 128, kMaxBN = 256, kBK = 64, kUmmaK = 16;  // kBM: rows of a CTA
 constexpr int kThreads = 384, kEpiWarps = 8;
 // Registers of the forward pass, whose epilogue holds 128 sums a thread.
 constexpr int kRegs = 168, kRegsRest = 56, kRegsEpilogue = 224;
 static_assert(128 * kRegsRest + 256 * kRegsEpilogue <= kThreads * kRegs, "register split");
 constexpr int kRun = 8;  // steps of K that the forward pass adds up in tensor memory
+constexpr int kMaxStages = 8;
+constexpr uint32_t kABytes = kBM * kBK * 2;
 constexpr uint32_t kBarBytes = 256;
-constexpr uint32_t kEpiBytes = 2 * 128 * 3 * sizeof(float);  // one half's sums, for the other half
-
-// R CTAs to a tile.
-template <int R>
-struct Cfg {
-  static constexpr int kStages = R == 1 ? 4 : 6;
-  static constexpr uint32_t kABytes = kBM * kBK * 2, kBBytes = kBN / R * kBK * 2;  // of a CTA
-  static constexpr uint32_t kPipeBytes = kStages * (kABytes + kBBytes);
-  static constexpr uint32_t kSmemBytes = 1024 + kPipeBytes + kBarBytes + kEpiBytes;
-};
-constexpr int kBandWide = 64, kBandDh = 8, kBandDw = 8;
+constexpr uint32_t kSumBytes = 2 * 128 * 3 * sizeof(float);  // forward: one half's sums, for the other half
+constexpr uint32_t kBoxBytes = 32 * 128;                     // backward: a box of 32 rows on its way out,
+constexpr uint32_t kOutBytes = kEpiWarps * 2 * kBoxBytes;    // two a warp
+constexpr uint32_t kMaxShared = 232448;
+constexpr int kBandWide = 64, kBandGradients = 8;
 constexpr int kMaxJobs = 3;
 constexpr int kPlanSms = 152;            // plans do not depend on the device, workspaces neither
 constexpr int64_t kPieceBytes = 1 << 27; // of G: what the L2 cache can hold
@@ -65,18 +61,21 @@ struct Job {
   int num_m, num_n, num_k;  // tiles, steps of K
   int ksplit;
   int col0;                 // first vocabulary column of the piece
+  int bn;                   // columns of a tile: 128 or 256, or 192 in the forward pass
   int units, band;          // tiles, rows of tiles that are taken together
+  int start, light0, light, extra;  // how the tiles are dealt, see Walk
   int a_mn, b_mn;           // operand stored [K][M] / [K][N]
   int add, round;           // dH: earlier pieces have left sums; these are the last
 };
 
 struct Maps {
-  CUtensorMap a[kMaxJobs], b[kMaxJobs];
+  CUtensorMap a[kMaxJobs], b[kMaxJobs], out[kMaxJobs];
 };
 
 struct Args {
   Job job[kMaxJobs];
   int num_jobs;
+  int stages, b_bytes;  // of the pipeline; of a stage's share of B
   int n_rows, d_model, vocab;
   const int32_t* targets;
   float inv_t;
@@ -85,12 +84,8 @@ struct Args {
   float* of_target;   // [n_rows] x of the target
   // backward
   const float *lse, *entropy, *g, *ge;
-  uint16_t* grad;     // G of the piece: [n_rows][ld_grad]
-  int64_t ld_grad;
-  float* dh_sum;      // [ksplit][n_rows][d_model]
-  uint16_t* dh;
-  uint16_t* dw;
-  int64_t lddh, lddw;
+  const float* dh_sum;  // [ksplit][sum_rows][d_model]
+  int sum_rows;         // n_rows, up to whole tiles
   int32_t* status;
   uint64_t wait_limit_ns;
 };
@@ -178,6 +173,11 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -218,13 +218,14 @@ struct Tile {
 
 // A thread's share of a tile: its row's logits (unscaled) of half of the columns, two a word.
 struct Half {
-  F2 v[kBN / 4];
+  F2 v[kMaxBN / 4];
 };
 
 // Adds a run's sums to those of the runs before.
-__device__ __forceinline__ void add_run(Half& x, uint32_t taddr) {
+__device__ __forceinline__ void add_run(Half& x, uint32_t taddr, int width) {
 #pragma unroll
-  for (int k = 0; k < kBN / 2; k += 32) {
+  for (int k = 0; k < kMaxBN / 2; k += 32) {
+    if (k >= width) break;
     uint32_t r[32];
     tmem_ld32(taddr + k, r);
     tmem_ld_wait();
@@ -239,18 +240,18 @@ __device__ __forceinline__ void epilogue_sums(const Args& a, const Job& j, const
                                               float* shared, int turn) {
   const float c = a.inv_t * kLog2e;
   const int target = t.valid && a.targets ? a.targets[t.row] : -1;
-  const int col = t.col0 + t.half * (kBN / 2), left = j.n - col;
-  if (left < kBN / 2) {  // columns past the vocabulary
+  const int col = t.col0 + t.half * (j.bn / 2), left = min(j.n - col, j.bn / 2);
+  if (left < kMaxBN / 2) {  // columns past the vocabulary or the tile
 #pragma unroll
-    for (int i = 0; i < kBN / 4; ++i) {
+    for (int i = 0; i < kMaxBN / 4; ++i) {
       const float2 f = lanes(x.v[i]);
       x.v[i] = pair(2 * i < left ? f.x : -INFINITY, 2 * i + 1 < left ? f.y : -INFINITY);
     }
   }
-  if (target >= col && target < col + min(left, kBN / 2)) {
+  if (target >= col && target < col + left) {
     F2 own = 0;
 #pragma unroll
-    for (int i = 0; i < kBN / 4; ++i)  // in asm: as C++ it becomes an indexed read, and x goes to local memory
+    for (int i = 0; i < kMaxBN / 4; ++i)  // in asm: as C++ it becomes an indexed read, and x goes to local memory
       asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %2, %3;\n\t@p mov.b64 %0, %1;\n\t}"
           : "+l"(own)
           : "l"(x.v[i]), "r"((target - col) / 2), "r"(i));
@@ -259,13 +260,13 @@ __device__ __forceinline__ void epilogue_sums(const Args& a, const Job& j, const
   Sums all;
   float top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kBN / 4; ++i) top = fmaxf(top, fmaxf(lanes(x.v[i]).x, lanes(x.v[i]).y));
+  for (int i = 0; i < kMaxBN / 4; ++i) top = fmaxf(top, fmaxf(lanes(x.v[i]).x, lanes(x.v[i]).y));
   all.m = top * c;
   const float ref = all.m == -INFINITY ? 0.0f : all.m;
   const F2 c2 = pair(c, c), minus = pair(-ref, -ref);
   F2 s[2] = {0, 0}, u[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < kBN / 4; ++i) {
+  for (int i = 0; i < kMaxBN / 4; ++i) {
     const float2 y = lanes(fma2(x.v[i], c2, minus));
     const F2 e = pair(ex2(y.x), ex2(y.y));
     s[i & 1] = add2(s[i & 1], e);
@@ -283,8 +284,44 @@ __device__ __forceinline__ void epilogue_sums(const Args& a, const Job& j, const
   out[0] = all.m, out[plane] = all.s, out[2 * plane] = all.u;
 }
 
+// Results leave through shared memory by TMA, a box of 32 rows of 128 bytes a time, so that memory gets whole
+// lines and edges are cut by the copy (a row's 64 bytes from each thread are half sectors, 16 bytes at
+// a time).  Two boxes a warp: one is filled while the other is read.
+struct Box {
+  uint8_t* base;  // this warp's two
+  int turn;
+  // the box to fill: its last copy has been read
+  __device__ __forceinline__ uint8_t* open() {
+    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
+    return base + (turn ^= 1) * kBoxBytes;
+  }
+  // 16-byte piece c of this thread's row, swizzled as the copy reads it
+  static __device__ __forceinline__ void put(uint8_t* box, int lane, int c, const uint4& w) {
+    *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) = w;
+  }
+  template <bool ADD>
+  static __device__ __forceinline__ void send(const uint8_t* box, const CUtensorMap* map, int x, int y) {
+    fence_async_shared();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      if (ADD)
+        asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                     "r"(smem_u32(box)), "r"(x), "r"(y)
+                     : "memory");
+      else
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                     "r"(smem_u32(box)), "r"(x), "r"(y)
+                     : "memory");
+    }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+};
+
 // G of the tile as bf16.
-__device__ __forceinline__ void epilogue_grad(const Args& a, const Job& j, const Tile& t) {
+__device__ __forceinline__ void epilogue_grad(const Args& a, const Job& j, const Tile& t, const CUtensorMap* map,
+                                              Box& out) {
+  const int lane = threadIdx.x & 31;
   float lse = 0.0f, a0 = 0.0f, a1 = 0.0f, g = 0.0f;
   int target = -1;
   if (t.valid) {
@@ -300,66 +337,92 @@ __device__ __forceinline__ void epilogue_grad(const Args& a, const Job& j, const
     }
     if (lse == -INFINITY) lse = 0.0f, a0 = 0.0f, a1 = 0.0f, g = 0.0f;  // a row of -inf only: zeros
   }
+  const F2 inv_t2 = pair(a.inv_t, a.inv_t), minus = pair(-lse, -lse), log2e = pair(kLog2e, kLog2e);
+  const F2 a02 = pair(a0, a0), a12 = pair(a1, a1);
+  const int from = t.half * (j.bn / 2);
 #pragma unroll 1
-  for (int k = t.half * (kBN / 2); k < (t.half + 1) * (kBN / 2); k += 32) {
-    uint32_t r[32];
-    tmem_ld32(t.taddr + k, r);
-    tmem_ld_wait();
+  for (int k = from; k < from + j.bn / 2; k += 64) {
     const int col = t.col0 + k;
     if (col >= j.n) break;
-    const int own = target - j.col0 - col;
-    uint32_t w[16];
+    uint8_t* const box = out.open();
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      float q[2];
+    for (int h = 0; h < 2; ++h) {
+      uint32_t r[32];
+      tmem_ld32(t.taddr + k + 32 * h, r);
+      tmem_ld_wait();
+      const int own = target - j.col0 - col - 32 * h;
+      const bool here = __any_sync(0xffffffffu, own >= 0 && own < 32);
+      uint32_t w[16];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float x = fmaf(__uint_as_float(r[i + e]), a.inv_t, -lse);
-        q[e] = ex2(x * kLog2e) * fmaf(a1, fmaxf(x, -1e30f), a0) + (own == i + e ? g : 0.0f);
+      for (int i = 0; i < 32; i += 2) {
+        const F2 x = fma2(pair(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), inv_t2, minus);
+        const float2 y = lanes(mul2(x, log2e)), xs = lanes(x);
+        const F2 q = mul2(pair(ex2(y.x), ex2(y.y)),
+                          fma2(a12, pair(fmaxf(xs.x, -1e30f), fmaxf(xs.y, -1e30f)), a02));
+        float2 f = lanes(q);
+        if (here) f.x += own == i ? g : 0.0f, f.y += own == i + 1 ? g : 0.0f;
+        w[i / 2] = bf16_pair(f.x, f.y);
       }
-      w[i / 2] = bf16_pair(q[0], q[1]);
-    }
-    if (!t.valid) continue;
-    // rows of G are a multiple of 256 columns apart: what lies past the piece is never read
-    uint4* const out = reinterpret_cast<uint4*>(a.grad + t.row * a.ld_grad + col);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) out[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+      for (int q = 0; q < 4; ++q)
+        Box::put(box, lane, 4 * h + q, make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
+    }
+    Box::send<false>(box, map, col, t.row - lane);
   }
 }
 
-// bf16 rows of a gradient; dH adds what earlier pieces left, and keeps fp32 until the last one.
-__device__ __forceinline__ void epilogue_store(const Args& a, const Job& j, const Tile& t, int ks) {
-  const bool dh = j.type == kJobDHidden;
-  float* const sum =
-      dh ? a.dh_sum + (static_cast<int64_t>(ks) * a.n_rows + t.row) * a.d_model + t.col0 : nullptr;
-  uint16_t* const out = dh ? a.dh + t.row * a.lddh + t.col0 : a.dw + (t.row + static_cast<int64_t>(j.col0)) * a.lddw + t.col0;
-  const bool add = dh && j.add, round = !dh || j.round;
+// A gradient's tile: bf16, or dH's sums in fp32 while pieces or ranges are still to be added.
+__device__ __forceinline__ void epilogue_store(const Args& a, const Job& j, const Tile& t, int ks,
+                                               const CUtensorMap* map, Box& out) {
+  const int lane = threadIdx.x & 31, from = t.half * (j.bn / 2);
+  if (!j.round) {
+    const int y = ks * a.sum_rows + t.row - lane;
 #pragma unroll 1
-  for (int k = t.half * (kBN / 2); k < (t.half + 1) * (kBN / 2); k += 32) {
-    uint32_t r[32];
-    tmem_ld32(t.taddr + k, r);
-    tmem_ld_wait();
-    if (t.col0 + k >= j.n) break;
-    if (!t.valid) continue;
+    for (int k = from; k < from + j.bn / 2; k += 32) {
+      if (t.col0 + k >= j.n) break;
+      uint32_t r[32];
+      tmem_ld32(t.taddr + k, r);
+      tmem_ld_wait();
+      uint8_t* const box = out.open();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (t.col0 + k + 8 * q >= j.n) break;
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(r[8 * q + e]);
-      float4* const at = reinterpret_cast<float4*>(sum + k + 8 * q);
-      if (add) {
-        const float4 x = at[0], y = at[1];
-        f[0] += x.x, f[1] += x.y, f[2] += x.z, f[3] += x.w, f[4] += y.x, f[5] += y.y, f[6] += y.z, f[7] += y.w;
-      }
-      if (round) {
-        *reinterpret_cast<uint4*>(out + k + 8 * q) =
-            make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
-      } else {
-        at[0] = make_float4(f[0], f[1], f[2], f[3]);
-        at[1] = make_float4(f[4], f[5], f[6], f[7]);
-      }
+      for (int q = 0; q < 8; ++q)
+        Box::put(box, lane, q, make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]));
+      if (j.add)
+        Box::send<true>(box, map, t.col0 + k, y);
+      else
+        Box::send<false>(box, map, t.col0 + k, y);
     }
+    return;
+  }
+#pragma unroll 1
+  for (int k = from; k < from + j.bn / 2; k += 64) {
+    if (t.col0 + k >= j.n) break;
+    uint8_t* const box = out.open();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t r[32];
+      tmem_ld32(t.taddr + k + 32 * h, r);
+      tmem_ld_wait();
+      if (j.add && t.valid) {  // what the earlier pieces left
+        const float* const sum = a.dh_sum + static_cast<int64_t>(t.row) * a.d_model + t.col0 + k + 32 * h;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (t.col0 + k + 32 * h + 4 * q >= j.n) break;
+          const float4 s = *reinterpret_cast<const float4*>(sum + 4 * q);
+          r[4 * q] = __float_as_uint(__uint_as_float(r[4 * q]) + s.x);
+          r[4 * q + 1] = __float_as_uint(__uint_as_float(r[4 * q + 1]) + s.y);
+          r[4 * q + 2] = __float_as_uint(__uint_as_float(r[4 * q + 2]) + s.z);
+          r[4 * q + 3] = __float_as_uint(__uint_as_float(r[4 * q + 3]) + s.w);
+        }
+      }
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = bf16_pair(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        Box::put(box, lane, 4 * h + q, make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
+    }
+    Box::send<false>(box, map, t.col0 + k, t.row - lane);
   }
 }
 
@@ -367,52 +430,68 @@ struct Unit {
   int job, m_blk, n_blk, ks, kb0, kb1;
 };
 
-// The u-th tile of the launch: jobs one after the other; in a job K's ranges, then bands of rows
-// of tiles, in a band the rows fastest.
-__device__ __forceinline__ Unit unit_of(const Args& a, int u) {
-  int i = 0;
-  while (i + 1 < a.num_jobs && u >= a.job[i].units) u -= a.job[i++].units;
-  const Job& j = a.job[i];
-  Unit x;
-  x.job = i;
-  x.ks = u / (j.num_m * j.num_n);
-  u -= x.ks * j.num_m * j.num_n;
-  const int band = u / (j.band * j.num_n), rows = min(j.band, j.num_m - band * j.band);
-  u -= band * j.band * j.num_n;
-  x.n_blk = u / rows;
-  x.m_blk = band * j.band + u - x.n_blk * rows;
-  x.kb0 = static_cast<int>(static_cast<int64_t>(x.ks) * j.num_k / j.ksplit);
-  x.kb1 = static_cast<int>(static_cast<int64_t>(x.ks + 1) * j.num_k / j.ksplit);
-  return x;
-}
+// The tiles of one CTA (or pair): jobs one after the other, in a job K's ranges, then bands of rows of tiles, in a
+// band the rows fastest.  Tiles are dealt in turn, beginning where the job before has ended; before
+// that a job of short tiles behind one of long ones gives `extra` rounds to those that had one long tile less
+// (`light` of them from light0 on).
+struct Walk {
+  int who, all;  // this CTA (or pair) of how many
+  int job = 0, k = 0;
+  __device__ __forceinline__ bool next(const Args& a, Unit& x) {
+    for (; job < a.num_jobs; ++job, k = 0) {
+      const Job& j = a.job[job];
+      const int q = who - j.light0;
+      if (k < j.extra && (q < 0 || q >= j.light)) k = j.extra;
+      int u;
+      if (k < j.extra) {
+        u = k * j.light + q;
+      } else {
+        int turn = who - j.start;
+        turn += turn < 0 ? all : 0;
+        u = j.extra * j.light + turn + (k - j.extra) * all;
+        if (u >= j.units) continue;
+      }
+      ++k;
+      x.job = job;
+      x.ks = u / (j.num_m * j.num_n);
+      u -= x.ks * j.num_m * j.num_n;
+      const int band = u / (j.band * j.num_n), rows = min(j.band, j.num_m - band * j.band);
+      u -= band * j.band * j.num_n;
+      x.n_blk = u / rows;
+      x.m_blk = band * j.band + u - x.n_blk * rows;
+      x.kb0 = static_cast<int>(static_cast<int64_t>(x.ks) * j.num_k / j.ksplit);
+      x.kb1 = static_cast<int>(static_cast<int64_t>(x.ks + 1) * j.num_k / j.ksplit);
+      return true;
+    }
+    return false;
+  }
+};
 
 // R CTAs a tile; SUMS: the forward pass (its one job), else the jobs of the backward pass.
 template <int R, bool SUMS>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
-  using C = Cfg<R>;
-  constexpr int S = C::kStages;
   grid_dependency_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int S = a.stages;
   uint8_t* const sA = smem;
-  uint8_t* const sB = smem + S * C::kABytes;
+  uint8_t* const sB = smem + S * kABytes;
+  uint8_t* const extra = sB + S * a.b_bytes;  // forward: sums, backward: boxes
   // of the first CTA: full, tempty (and its own of the others); of both: empty, tfull
-  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + C::kPipeBytes);
-  uint64_t* const empty = full + S;
-  uint64_t* const tfull = empty + S;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(extra + (SUMS ? kSumBytes : kOutBytes));
+  uint64_t* const empty = full + kMaxStages;
+  uint64_t* const tfull = empty + kMaxStages;
   uint64_t* const tempty = tfull + 2;
   uint64_t* const drain = tempty + 2;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* const abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  float* const epi = reinterpret_cast<float*>(smem + C::kPipeBytes + kBarBytes);
-  static_assert((2 * S + 5) * 8 + 8 <= static_cast<int>(kBarBytes), "barrier region");
+  static_assert((2 * kMaxStages + 5) * 8 + 8 <= static_cast<int>(kBarBytes), "barrier region");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = R == 1 ? 0 : static_cast<int>(cluster_rank());
-  const int first = blockIdx.x / R, stride = gridDim.x / R;
-  int units = 0;
-  for (int i = 0; i < a.num_jobs; ++i) units += a.job[i].units;
+  Walk walk{static_cast<int>(blockIdx.x) / R, static_cast<int>(gridDim.x) / R};
+  Unit x;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], rank == 0 ? R : 1);  // the first CTA's own copies, and word of the second one's
@@ -442,20 +521,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int u = first; ok && u < units; u += stride) {
-        const Unit x = unit_of(a, u);
+      while (ok && walk.next(a, x)) {
         const Job& j = a.job[x.job];
+        const uint32_t b_bytes = j.bn / R * kBK * 2;
         const CUtensorMap* const ma = &maps.a[x.job];
         const CUtensorMap* const mb = &maps.b[x.job];
-        const int m0 = (x.m_blk * R + rank) * kBM, n0 = x.n_blk * kBN + rank * (kBN / R);
+        const int m0 = (x.m_blk * R + rank) * kBM, n0 = x.n_blk * j.bn + rank * (j.bn / R);
         for (int kb = x.kb0; kb < x.kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, limit, abort)) {
             ok = false;
             break;
           }
-          uint8_t* const da = sA + stage * C::kABytes;
-          uint8_t* const db = sB + stage * C::kBBytes;
-          mbar_arrive_expect_tx(&full[stage], C::kABytes + C::kBBytes);
+          uint8_t* const da = sA + stage * kABytes;
+          uint8_t* const db = sB + stage * a.b_bytes;
+          mbar_arrive_expect_tx(&full[stage], kABytes + b_bytes);
           uint64_t* const bar = &full[stage];
           if (j.a_mn) {  // [K][M]: boxes of 64 columns by 64 rows of K
 #pragma unroll
@@ -464,8 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d(da, ma, bar, kb * kBK, m0);
           }
           if (j.b_mn) {
-#pragma unroll
-            for (int q = 0; q < kBN / R / 64; ++q) tma_load_2d(db + q * 8192, mb, bar, n0 + q * 64, kb * kBK);
+            for (int q = 0; q < j.bn / R / 64; ++q) tma_load_2d(db + q * 8192, mb, bar, n0 + q * 64, kb * kBK);
           } else {
             tma_load_2d(db, mb, bar, kb * kBK, n0);
           }
@@ -483,10 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int u = first; ok && u < units; u += stride) {
-        const Unit x = unit_of(a, u);
+      while (ok && walk.next(a, x)) {
         const Job& j = a.job[x.job];
-        const uint32_t idesc = idesc_bf16_f32(kBM * R, kBN) | (j.a_mn ? 1u << 15 : 0u) | (j.b_mn ? 1u << 16 : 0u);
+        const uint32_t idesc = idesc_bf16_f32(kBM * R, j.bn) | (j.a_mn ? 1u << 15 : 0u) | (j.b_mn ? 1u << 16 : 0u);
         // a step of 16 along K: 32 bytes of a K-major row, 16 rows of 128 bytes of the others
         const uint64_t a_step = j.a_mn ? 128u : 2u, b_step = j.b_mn ? 128u : 2u;
         for (int k0 = x.kb0; ok && k0 < x.kb1;) {
@@ -496,14 +573,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kBN);
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kMaxBN);
           for (int kb = k0; kb < k1; ++kb) {
             if (!mbar_wait(&full[stage], phase, limit, abort)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t pa = smem_u32(sA + stage * C::kABytes), pb = smem_u32(sB + stage * C::kBBytes);
+            const uint32_t pa = smem_u32(sA + stage * kABytes), pb = smem_u32(sB + stage * a.b_bytes);
             const uint64_t ad = j.a_mn ? smem_desc_sw128_nmajor(pa, 8192) : smem_desc_sw128(pa);
             const uint64_t bd = j.b_mn ? smem_desc_sw128_nmajor(pb, 8192) : smem_desc_sw128(pb);
 #pragma unroll
@@ -532,8 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int u = first; ok && u < units; u += stride) {
-        const Unit x = unit_of(a, u);
+      while (ok && walk.next(a, x)) {
         for (int kb = x.kb0; kb < x.kb1; ++kb) {
           ok = mbar_wait(&full[stage], phase, limit, abort);
           if (!ok) break;
@@ -554,18 +630,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_phase = 0;
     bool ok = true;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(t.lg * 32) << 16);
-    for (int u = first; ok && u < units; u += stride) {
-      const Unit x = unit_of(a, u);
+    Box out{extra + (warp - 4) * 2 * kBoxBytes, 0};
+    while (ok && walk.next(a, x)) {
       const Job& j = a.job[x.job];
       t.row = (x.m_blk * R + rank) * kBM + t.lg * 32 + lane;
-      t.col0 = x.n_blk * kBN;
+      t.col0 = x.n_blk * j.bn;
       t.valid = t.row < j.m;
       auto wait_full = [&]() {
         ok = mbar_wait(&tfull[acc], acc_phase, limit, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
         tc_fence_after();
-        t.taddr = lane_base + static_cast<uint32_t>(acc * kBN);
+        t.taddr = lane_base + static_cast<uint32_t>(acc * kMaxBN);
         return ok;
       };
       auto release = [&]() {
@@ -585,21 +661,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int k0 = x.kb0; k0 < x.kb1; k0 += kRun) {
           if (!wait_full()) break;
-          add_run(sums, t.taddr + t.half * (kBN / 2));
+          add_run(sums, t.taddr + t.half * (j.bn / 2), j.bn / 2);
           release();
         }
         if (!ok) break;
-        epilogue_sums(a, j, t, x.n_blk, sums, epi, turn);
+        epilogue_sums(a, j, t, x.n_blk, sums, reinterpret_cast<float*>(extra), turn);
         turn ^= 1;
       } else {
         if (!wait_full()) break;
-        if (j.type == kJobGrad)
-          epilogue_grad(a, j, t);
-        else
-          epilogue_store(a, j, t, x.ks);
+        if (t.row - lane < j.m) {  // else the warp's rows are all past the end
+          if (j.type == kJobGrad)
+            epilogue_grad(a, j, t, &maps.out[x.job], out);
+          else
+            epilogue_store(a, j, t, x.ks, &maps.out[x.job], out);
+        }
         release();
       }
     }
+    if (!SUMS) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // what leaves this CTA has left
   }
   tc_fence_before();
   Tc<R>::sync();
@@ -647,7 +726,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) linear_join_kernel(const Join
 
 struct ReduceArgs {
   const float* sum;
-  int ksplit, n_rows, dim;
+  int ksplit, n_rows, sum_rows, dim;
   uint16_t* out;
   int64_t ld;
 };
@@ -657,7 +736,7 @@ __global__ void __launch_bounds__(256) linear_reduce_kernel(const ReduceArgs a) 
   grid_dependency_wait();
   const int64_t vecs = a.dim / 8, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= vecs * a.n_rows) return;
-  const int64_t row = i / vecs, c = i % vecs * 8, plane = static_cast<int64_t>(a.n_rows) * a.dim;
+  const int64_t row = i / vecs, c = i % vecs * 8, plane = static_cast<int64_t>(a.sum_rows) * a.dim;
   const float* const at = a.sum + row * a.dim + c;
   float f[8] = {};
   for (int k = 0; k < a.ksplit; ++k) {
@@ -670,6 +749,9 @@ __global__ void __launch_bounds__(256) linear_reduce_kernel(const ReduceArgs a) 
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 size_t round_up(size_t x, size_t to) { return (x + to - 1) / to * to; }
+
+// Rows of dH's fp32 sums: whole tiles, as a tile leaves whole.
+int64_t sum_rows(int64_t n_rows) { return (n_rows + 255) / 256 * 256; }
 
 // How a backward call is cut.
 struct Plan {
@@ -687,29 +769,45 @@ Plan plan_bwd(int64_t n_rows, int64_t d, int64_t vocab) {
   // dH's tiles have long sums: where they are few, K is cut so that none takes longer than a
   // CTA's share of the two products
   const int64_t num_k = ceil_div(std::min<int64_t>(p.piece, vocab), kBK);
-  const int64_t dh = ceil_div(n_rows, kBM) * static_cast<int64_t>(ceil_div(d, kBN)) * num_k;
-  const int64_t dw = ceil_div(std::min<int64_t>(p.piece, vocab), kBM) * static_cast<int64_t>(ceil_div(d, kBN)) *
+  const int64_t dh = ceil_div(n_rows, kBM) * static_cast<int64_t>(ceil_div(d, kMaxBN)) * num_k;
+  const int64_t dw = ceil_div(std::min<int64_t>(p.piece, vocab), kBM) * static_cast<int64_t>(ceil_div(d, kMaxBN)) *
                      ceil_div(n_rows, kBK);
   const int64_t share = std::max<int64_t>(8, (dh + dw) / kPlanSms);
   p.ksplit = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({num_k, kMaxKSplit, ceil_div(num_k, share)})));
   p.grad_bytes = round_up(static_cast<size_t>(n_rows) * p.piece * 2, 256);
-  p.sum_bytes = p.pieces > 1 || p.ksplit > 1 ? round_up(static_cast<size_t>(p.ksplit) * n_rows * d * 4, 256) : 0;
+  p.sum_bytes = p.pieces > 1 || p.ksplit > 1 ? round_up(static_cast<size_t>(p.ksplit) * sum_rows(n_rows) * d * 4, 256) : 0;
   p.bytes = p.grad_bytes * (p.pieces > 1 ? 2 : 1) + p.sum_bytes + 256;
   return p;
 }
 
 size_t fwd_bytes(int64_t n_rows, int64_t vocab) {
-  return round_up(static_cast<size_t>(n_rows) * 4 * (3 * ceil_div(vocab, kBN) + 1), 256) + 256;
+  return round_up(static_cast<size_t>(n_rows) * 4 * (3 * ceil_div(vocab, kMinBN) + 1), 256) + 256;
 }
 
 // CTAs to a tile: a pair from 129 rows on.
 int ctas_of(int n_rows) { return n_rows > kBM ? 2 : 1; }
 
-// A: [m][k], or [k][m] with mn; likewise B.  rows of either lie ld elements apart.
+// CTAs (or pairs) that work at a time.
+int slots_of(int ctas) { return std::max(1, sm_count() / ctas); }
+
+// Columns of a tile, of those that are allowed: what leaves the least time in the last round where a
+// launch has this job alone (`alone`), or the least work past the edge.  A tile's rows are read
+// again for each, which makes narrow tiles dearer (24 columns' worth).
+int choose_bn(std::initializer_list<int> allowed, int64_t num_m, int n, int slots, bool alone) {
+  int best = 0;
+  int64_t least = 0;
+  for (int bn : allowed) {
+    const int64_t tiles = num_m * ceil_div(n, bn), cost = (alone ? ceil_div(tiles, slots) : tiles) * (bn + 24);
+    if (!best || cost < least) best = bn, least = cost;
+  }
+  return best;
+}
+
+// Adds a job.  A: [m][k], or [k][m] with a_mn; likewise B; their rows lie lda, ldb elements apart.
 int set_job(Maps* maps, Args* args, int ctas, Job j, const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb,
             int k) {
   const int i = args->num_jobs++;
-  j.num_m = ceil_div(j.m, kBM * ctas), j.num_n = ceil_div(j.n, kBN), j.num_k = ceil_div(k, kBK);
+  j.num_m = ceil_div(j.m, kBM * ctas), j.num_n = ceil_div(j.n, j.bn), j.num_k = ceil_div(k, kBK);
   j.ksplit = std::min(j.ksplit, j.num_k);
   const int64_t units = static_cast<int64_t>(j.num_m) * j.num_n * j.ksplit;
   if (units > (1 << 29)) return TWELL_ERR_UNSUPPORTED;
@@ -720,27 +818,49 @@ int set_job(Maps* maps, Args* args, int ctas, Job j, const uint16_t* A, int64_t 
   else
     KV_TRY(encode_tmap_2d(&maps->a[i], A, k, j.m, lda * 2, kBK, kBM));
   if (j.b_mn) return encode_tmap_2d(&maps->b[i], B, j.n, k, ldb * 2, 64, kBK);
-  return encode_tmap_2d(&maps->b[i], B, k, j.n, ldb * 2, kBK, kBN / ctas);
+  return encode_tmap_2d(&maps->b[i], B, k, j.n, ldb * 2, kBK, j.bn / ctas);
+}
+
+// Deals the jobs' tiles to the CTAs or pairs (see Walk); returns how many of those there are.
+int deal(Args* args, int slots) {
+  int64_t units = 0;
+  for (int i = 0; i < args->num_jobs; ++i) units += args->job[i].units;
+  const int all = static_cast<int>(std::min<int64_t>(units, slots));
+  int start = 0;
+  int64_t cost_before = 0;
+  for (int i = 0; i < args->num_jobs; ++i) {
+    Job& j = args->job[i];
+    const int64_t cost = std::max<int64_t>(1, static_cast<int64_t>(j.num_k) * j.bn / j.ksplit);
+    j.start = start, j.light0 = start, j.light = all - start;
+    j.extra = start > 0 ? static_cast<int>(std::min<int64_t>(cost_before / cost, j.units / j.light)) : 0;
+    if (j.extra < 2) j.extra = 0;  // a round more for some is what beginning there gives, too
+    start = static_cast<int>((start + j.units - static_cast<int64_t>(j.extra) * j.light) % all);
+    cost_before = cost;
+  }
+  return all;
 }
 
 template <int R, bool SUMS>
-int launch_jobs(const Maps& maps, const Args& args, cudaStream_t s) {
+int launch_jobs(const Maps& maps, Args args, cudaStream_t s) {
   const auto kernel = linear_kernel<R, SUMS>;
-  constexpr uint32_t smem = Cfg<R>::kSmemBytes;
-  KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(smem)));
-  if (SUMS) {  // the split above waits for registers that only a launch with kRegs a thread has
+  KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(kMaxShared)));
+  if (SUMS) {  // the split of the registers waits for as many as only a launch with kRegs a thread has
     static const int regs = [&] {
       cudaFuncAttributes f;
       return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
     }();
     if (regs < kRegs) return TWELL_ERR_CUDA;
   }
-  int64_t units = 0;
-  for (int i = 0; i < args.num_jobs; ++i) units += args.job[i].units;
+  int bn = 0;
+  for (int i = 0; i < args.num_jobs; ++i) bn = std::max(bn, args.job[i].bn);
+  args.b_bytes = bn / R * kBK * 2;
+  const uint32_t stage = kABytes + args.b_bytes, rest = 1024 + kBarBytes + (SUMS ? kSumBytes : kOutBytes);
+  args.stages = static_cast<int>(std::min<uint32_t>(kMaxStages, (kMaxShared - rest) / stage));
+  const int all = deal(&args, slots_of(R));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units, sm_count() / R)) * R);
+  cfg.gridDim = dim3(static_cast<unsigned>(all) * R);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = rest + args.stages * stage;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -807,6 +927,7 @@ extern "C" TWELL_API int twell_linear_logprobs(const uint16_t* H, int64_t ldh, c
   Job j = {};
   j.type = kJobSums, j.band = kBandWide, j.m = n_rows, j.n = vocab, j.ksplit = 1;
   const int ctas = ctas_of(n_rows);
+  j.bn = choose_bn({256, 192, 128}, ceil_div(n_rows, kBM * ctas), vocab, slots_of(ctas), true);
   KV_TRY(set_job(&maps, &a, ctas, j, H, ldh, W, ldw, d_model));
   KV_TRY((ctas == 2 ? launch_jobs<2, true>(maps, a, s) : launch_jobs<1, true>(maps, a, s)));
   const JoinArgs join{a.part, a.of_target, a.job[0].num_n, n_rows, vocab, targets, logprob, entropy, lse};
@@ -856,11 +977,10 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
   Args base = {};
   base.n_rows = n_rows, base.d_model = d_model, base.vocab = vocab, base.targets = targets;
   base.inv_t = inv_temperature, base.lse = lse, base.entropy = entropy, base.g = d_logprob, base.ge = d_entropy;
-  base.ld_grad = plan.piece;
-  base.dh_sum = reinterpret_cast<float*>(ws + plan.grad_bytes * (plan.pieces > 1 ? 2 : 1));
-  base.dh = dH, base.lddh = lddh, base.dw = dW, base.lddw = lddw;
+  float* const dh_sum = reinterpret_cast<float*>(ws + plan.grad_bytes * (plan.pieces > 1 ? 2 : 1));
+  base.dh_sum = dh_sum, base.sum_rows = static_cast<int>(sum_rows(n_rows));
   base.status = status, base.wait_limit_ns = kWaitLimitNs;
-  const int ctas = ctas_of(n_rows);
+  const int ctas = ctas_of(n_rows), slots = slots_of(ctas);
   for (int p = 0; p <= plan.pieces; ++p) {
     Maps maps;
     Args a = base;
@@ -869,29 +989,42 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
       const uint16_t* const G = buffer[(p - 1) & 1];
       const uint16_t* const Wp = W + static_cast<int64_t>(col0) * ldw;
       Job j = {};
-      j.col0 = col0, j.add = p > 1, j.round = p == plan.pieces && plan.ksplit == 1;
+      j.col0 = col0, j.band = kBandGradients, j.b_mn = 1;
+      j.bn = choose_bn({256, 128}, 1, d_model, slots, false);
       if (dH) {
-        j.type = kJobDHidden, j.band = kBandDh, j.m = n_rows, j.n = d_model, j.b_mn = 1;
+        j.type = kJobDHidden, j.m = n_rows, j.n = d_model, j.add = p > 1;
+        j.round = p == plan.pieces && plan.ksplit == 1;
         // the first piece fills all ranges' sums; a narrower last one adds to no more than it has steps
         j.ksplit = plan.ksplit;
+        if (j.round)
+          KV_TRY(encode_tmap_2d(&maps.out[a.num_jobs], dH, d_model, n_rows, lddh * 2, 64, 32));
+        else
+          KV_TRY(encode_tmap_2d_f32(&maps.out[a.num_jobs], dh_sum, d_model,
+                                    static_cast<uint64_t>(plan.ksplit) * base.sum_rows,
+                                    static_cast<uint64_t>(d_model) * 4, 32, 32));
         KV_TRY(set_job(&maps, &a, ctas, j, G, plan.piece, Wp, ldw, width));
       }
       if (dW) {
-        j.type = kJobDWeight, j.band = kBandDw, j.m = width, j.n = d_model, j.a_mn = j.b_mn = 1, j.ksplit = 1;
+        j.type = kJobDWeight, j.m = width, j.n = d_model, j.a_mn = 1, j.add = 0, j.round = 1, j.ksplit = 1;
+        KV_TRY(encode_tmap_2d(&maps.out[a.num_jobs], dW + static_cast<int64_t>(col0) * lddw, d_model, width, lddw * 2,
+                              64, 32));
         KV_TRY(set_job(&maps, &a, ctas, j, G, plan.piece, H, ldh, n_rows));
       }
     }
     if (p < plan.pieces) {  // G of piece p
       const int col0 = p * plan.piece;
       Job j = {};
-      j.type = kJobGrad, j.band = kBandWide, j.m = n_rows, j.n = std::min(plan.piece, vocab - col0), j.ksplit = 1, j.col0 = col0;
-      a.grad = buffer[p & 1];
+      j.type = kJobGrad, j.band = kBandWide, j.m = n_rows, j.n = std::min(plan.piece, vocab - col0), j.ksplit = 1;
+      j.col0 = col0;
+      j.bn = choose_bn({256, 128}, ceil_div(n_rows, kBM * ctas), j.n, slots, a.num_jobs == 0);
+      KV_TRY(encode_tmap_2d(&maps.out[a.num_jobs], buffer[p & 1], plan.piece, n_rows,
+                            static_cast<uint64_t>(plan.piece) * 2, 64, 32));
       KV_TRY(set_job(&maps, &a, ctas, j, H, ldh, W + static_cast<int64_t>(col0) * ldw, ldw, d_model));
     }
     KV_TRY((ctas == 2 ? launch_jobs<2, false>(maps, a, s) : launch_jobs<1, false>(maps, a, s)));
   }
   if (!dH || plan.ksplit == 1) return TWELL_OK;
-  const ReduceArgs r{base.dh_sum, plan.ksplit, n_rows, d_model, dH, lddh};
+  const ReduceArgs r{dh_sum, plan.ksplit, n_rows, base.sum_rows, d_model, dH, lddh};
   LaunchScope scope(TWELL_KERNEL_LINEAR_LOGPROBS_BWD, s);
   return launch_pdl(linear_reduce_kernel, dim3(ceil_div(static_cast<int64_t>(n_rows) * (d_model / 8), 256)), dim3(256),
                     0, s, r) == cudaSuccess

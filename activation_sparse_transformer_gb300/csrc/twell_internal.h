@@ -88,6 +88,8 @@ bool device_is_sm103();              // current device is compute capability 10.
 // row-major boxes (shared-memory slabs read by CUDA cores).
 int encode_tmap_2d(CUtensorMap* map, const void* base, uint64_t inner_elems, uint64_t rows,
                    uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows);
+int encode_tmap_2d_f32(CUtensorMap* map, const void* base, uint64_t inner_elems, uint64_t rows,
+                       uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows);  // the first kind, of fp32
 int encode_tmap_2d_plain(CUtensorMap* map, const void* base, uint64_t inner_elems, uint64_t rows,
                          uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows);
 
