@@ -114,6 +114,30 @@ __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// The issuing warps stay converged and one elected lane issues: the operands then sit in uniform registers,
+// without a move for each of them (issued from a lane's own branch, four MMAs and their commit took
+// 640 cycles of the 512 that they run: 8192 x 2048 x 32768 in 642 us without any copies).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void expect_bytes(uint32_t leader, uint64_t* bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(bytes), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void load_box(uint32_t leader, void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(leader)
+      : "memory");
+}
+
 // The tensor-core operations of a CTA alone and of a pair, whose first CTA issues for both.
 template <int R>
 struct Tc;
@@ -121,10 +145,21 @@ template <>
 struct Tc<1> {
   static __device__ __forceinline__ void alloc(uint32_t* holder) { tmem_alloc(holder, 512); }
   static __device__ __forceinline__ void dealloc(uint32_t base) { tmem_dealloc(base, 512); }
-  static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-    mma_bf16(d, a, b, idesc, add);
+  static __device__ __forceinline__ void mma(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(leader)
+        : "memory");
   }
-  static __device__ __forceinline__ void commit(uint64_t* bar) { mma_commit(bar); }
+  static __device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(leader)
+        : "memory");
+  }
   static __device__ __forceinline__ void sync() { __syncthreads(); }
 };
 template <>
@@ -137,20 +172,21 @@ struct Tc<2> {
   static __device__ __forceinline__ void dealloc(uint32_t base) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(512) : "memory");
   }
-  static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  static __device__ __forceinline__ void mma(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(leader)
         : "memory");
   }
   // arrives at the same barrier of both CTAs
-  static __device__ __forceinline__ void commit(uint64_t* bar) {
+  static __device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
             smem_u32(bar)),
-        "h"(static_cast<uint16_t>(3))
+        "h"(static_cast<uint16_t>(3)), "r"(leader)
         : "memory");
   }
   static __device__ __forceinline__ void sync() { cluster_sync(); }
@@ -516,8 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     if (SUMS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ---------------- copies
+      const uint32_t leader = elect_one();
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -534,18 +571,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           uint8_t* const da = sA + stage * kABytes;
           uint8_t* const db = sB + stage * a.b_bytes;
-          mbar_arrive_expect_tx(&full[stage], kABytes + b_bytes);
+          expect_bytes(leader, &full[stage], kABytes + b_bytes);
           uint64_t* const bar = &full[stage];
           if (j.a_mn) {  // [K][M]: boxes of 64 columns by 64 rows of K
 #pragma unroll
-            for (int q = 0; q < kBM / 64; ++q) tma_load_2d(da + q * 8192, ma, bar, m0 + q * 64, kb * kBK);
+            for (int q = 0; q < kBM / 64; ++q) load_box(leader, da + q * 8192, ma, bar, m0 + q * 64, kb * kBK);
           } else {
-            tma_load_2d(da, ma, bar, kb * kBK, m0);
+            load_box(leader, da, ma, bar, kb * kBK, m0);
           }
           if (j.b_mn) {
-            for (int q = 0; q < j.bn / R / 64; ++q) tma_load_2d(db + q * 8192, mb, bar, n0 + q * 64, kb * kBK);
+            for (int q = 0; q < j.bn / R / 64; ++q) load_box(leader, db + q * 8192, mb, bar, n0 + q * 64, kb * kBK);
           } else {
-            tma_load_2d(db, mb, bar, kb * kBK, n0);
+            load_box(leader, db, mb, bar, kb * kBK, n0);
           }
           if (++stage == S) stage = 0, phase ^= 1u;
         }
@@ -556,8 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < 10000000ull) __nanosleep(1000);
       }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
       // ---------------- products
+      const uint32_t leader = elect_one();
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -585,12 +623,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t bd = j.b_mn ? smem_desc_sw128_nmajor(pb, 8192) : smem_desc_sw128(pb);
 #pragma unroll
             for (int k = 0; k < kBK / kUmmaK; ++k)
-              Tc<R>::mma(d, ad + k * a_step, bd + k * b_step, idesc, (kb > k0 || k > 0) ? 1u : 0u);
-            Tc<R>::commit(&empty[stage]);
+              Tc<R>::mma(leader, d, ad + k * a_step, bd + k * b_step, idesc, (kb > k0 || k > 0) ? 1u : 0u);
+            Tc<R>::commit(leader, &empty[stage]);
             if (++stage == S) stage = 0, phase ^= 1u;
           }
           if (!ok) break;
-          Tc<R>::commit(&tfull[acc]);
+          Tc<R>::commit(leader, &tfull[acc]);
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1u;
           k0 = k1;
@@ -598,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) {
         report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
-        Tc<R>::commit(drain);  // the MMAs already issued end before TMEM is released
+        Tc<R>::commit(leader, drain);  // the MMAs already issued end before TMEM is released
         volatile int never = 0;
         mbar_wait(drain, 0, 10000000ull, &never);
       }
