@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Unit x;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], rank == 0 ? R : 1);  // the first CTA's own copies, and word of the second one's
+      mbar_init(&full[s], rank == 0 ? R + 1 : 2);  // A, B; of the first CTA also word of the second one's
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -552,38 +552,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     if (SUMS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == 0) {
-      // ---------------- copies
+    if (warp == 0 || warp == 2) {
+      // ---------------- copies: one warp brings A, the other B (one for both takes longer to issue them than they
+      // are multiplied)
       const uint32_t leader = elect_one();
+      const bool is_b = warp == 2;
+      uint8_t* const base = is_b ? sB : sA;
+      const uint32_t pitch = is_b ? a.b_bytes : kABytes;
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       while (ok && walk.next(a, x)) {
         const Job& j = a.job[x.job];
-        const uint32_t b_bytes = j.bn / R * kBK * 2;
-        const CUtensorMap* const ma = &maps.a[x.job];
-        const CUtensorMap* const mb = &maps.b[x.job];
-        const int m0 = (x.m_blk * R + rank) * kBM, n0 = x.n_blk * j.bn + rank * (j.bn / R);
-        for (int kb = x.kb0; kb < x.kb1; ++kb) {
+        const CUtensorMap* const map = is_b ? &maps.b[x.job] : &maps.a[x.job];
+        const int at = is_b ? x.n_blk * j.bn + rank * (j.bn / R) : (x.m_blk * R + rank) * kBM;
+        const bool mn = is_b ? j.b_mn : j.a_mn;  // [K][at]: boxes of 64 columns by 64 rows of K; else one of 64 columns of K
+        const int rows = is_b ? j.bn / R : kBM, boxes = mn ? rows / 64 : 1;
+        const uint32_t bytes = rows * kBK * 2;
+        const int dx = mn ? 0 : kBK, dy = mn ? kBK : 0;
+        int cx = mn ? at : x.kb0 * kBK, cy = mn ? x.kb0 * kBK : at;
+        for (int n = x.kb1 - x.kb0; n > 0; --n, cx += dx, cy += dy) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, limit, abort)) {
             ok = false;
             break;
           }
-          uint8_t* const da = sA + stage * kABytes;
-          uint8_t* const db = sB + stage * a.b_bytes;
-          expect_bytes(leader, &full[stage], kABytes + b_bytes);
-          uint64_t* const bar = &full[stage];
-          if (j.a_mn) {  // [K][M]: boxes of 64 columns by 64 rows of K
-#pragma unroll
-            for (int q = 0; q < kBM / 64; ++q) load_box(leader, da + q * 8192, ma, bar, m0 + q * 64, kb * kBK);
-          } else {
-            load_box(leader, da, ma, bar, kb * kBK, m0);
-          }
-          if (j.b_mn) {
-            for (int q = 0; q < j.bn / R / 64; ++q) load_box(leader, db + q * 8192, mb, bar, n0 + q * 64, kb * kBK);
-          } else {
-            load_box(leader, db, mb, bar, kb * kBK, n0);
-          }
+          uint8_t* const dst = base + stage * pitch;
+          expect_bytes(leader, &full[stage], bytes);
+          load_box(leader, dst, map, &full[stage], cx, cy);
+          for (int q = 1; q < boxes; ++q) load_box(leader, dst + q * 8192, map, &full[stage], cx + q * 64, cy);
           if (++stage == S) stage = 0, phase ^= 1u;
         }
       }
@@ -599,11 +595,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
+      const uint32_t a_stage = kABytes >> 4, b_stage = static_cast<uint32_t>(a.b_bytes) >> 4;
       while (ok && walk.next(a, x)) {
         const Job& j = a.job[x.job];
         const uint32_t idesc = idesc_bf16_f32(kBM * R, j.bn) | (j.a_mn ? 1u << 15 : 0u) | (j.b_mn ? 1u << 16 : 0u);
         // a step of 16 along K: 32 bytes of a K-major row, 16 rows of 128 bytes of the others
         const uint64_t a_step = j.a_mn ? 128u : 2u, b_step = j.b_mn ? 128u : 2u;
+        const uint64_t ad0 = j.a_mn ? smem_desc_sw128_nmajor(smem_u32(sA), 8192) : smem_desc_sw128(smem_u32(sA));
+        const uint64_t bd0 = j.b_mn ? smem_desc_sw128_nmajor(smem_u32(sB), 8192) : smem_desc_sw128(smem_u32(sB));
         for (int k0 = x.kb0; ok && k0 < x.kb1;) {
           const int k1 = SUMS ? min(k0 + kRun, x.kb1) : x.kb1;
           if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, limit, abort)) {
@@ -612,18 +611,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kMaxBN);
-          for (int kb = k0; kb < k1; ++kb) {
+          uint32_t add = 0;
+          for (int n = k1 - k0; n > 0; --n) {
             if (!mbar_wait(&full[stage], phase, limit, abort)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t pa = smem_u32(sA + stage * kABytes), pb = smem_u32(sB + stage * a.b_bytes);
-            const uint64_t ad = j.a_mn ? smem_desc_sw128_nmajor(pa, 8192) : smem_desc_sw128(pa);
-            const uint64_t bd = j.b_mn ? smem_desc_sw128_nmajor(pb, 8192) : smem_desc_sw128(pb);
+            const uint64_t ad = ad0 + stage * a_stage, bd = bd0 + stage * b_stage;
 #pragma unroll
-            for (int k = 0; k < kBK / kUmmaK; ++k)
-              Tc<R>::mma(leader, d, ad + k * a_step, bd + k * b_step, idesc, (kb > k0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < kBK / kUmmaK; ++k) {
+              Tc<R>::mma(leader, d, ad + k * a_step, bd + k * b_step, idesc, add);
+              add = 1;
+            }
             Tc<R>::commit(leader, &empty[stage]);
             if (++stage == S) stage = 0, phase ^= 1u;
           }
@@ -965,7 +965,7 @@ extern "C" TWELL_API int twell_linear_logprobs(const uint16_t* H, int64_t ldh, c
   Job j = {};
   j.type = kJobSums, j.band = kBandWide, j.m = n_rows, j.n = vocab, j.ksplit = 1;
   const int ctas = ctas_of(n_rows);
-  j.bn = choose_bn({256, 192, 128}, ceil_div(n_rows, kBM * ctas), vocab, slots_of(ctas), true);
+  j.bn = choose_bn({256}, ceil_div(n_rows, kBM * ctas), vocab, slots_of(ctas), true);
   KV_TRY(set_job(&maps, &a, ctas, j, H, ldh, W, ldw, d_model));
   KV_TRY((ctas == 2 ? launch_jobs<2, true>(maps, a, s) : launch_jobs<1, true>(maps, a, s)));
   const JoinArgs join{a.part, a.of_target, a.job[0].num_n, n_rows, vocab, targets, logprob, entropy, lse};
@@ -1028,7 +1028,7 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
       const uint16_t* const Wp = W + static_cast<int64_t>(col0) * ldw;
       Job j = {};
       j.col0 = col0, j.band = kBandGradients, j.b_mn = 1;
-      j.bn = choose_bn({256, 128}, 1, d_model, slots, false);
+      j.bn = choose_bn({256}, 1, d_model, slots, false);
       if (dH) {
         j.type = kJobDHidden, j.m = n_rows, j.n = d_model, j.add = p > 1;
         j.round = p == plan.pieces && plan.ksplit == 1;
@@ -1054,7 +1054,7 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
       Job j = {};
       j.type = kJobGrad, j.band = kBandWide, j.m = n_rows, j.n = std::min(plan.piece, vocab - col0), j.ksplit = 1;
       j.col0 = col0;
-      j.bn = choose_bn({256, 128}, ceil_div(n_rows, kBM * ctas), j.n, slots, a.num_jobs == 0);
+      j.bn = choose_bn({256}, ceil_div(n_rows, kBM * ctas), j.n, slots, a.num_jobs == 0);
       KV_TRY(encode_tmap_2d(&maps.out[a.num_jobs], buffer[p & 1], plan.piece, n_rows,
                             static_cast<uint64_t>(plan.piece) * 2, 64, 32));
       KV_TRY(set_job(&maps, &a, ctas, j, H, ldh, W + static_cast<int64_t>(col0) * ldw, ldw, d_model));
