@@ -765,40 +765,51 @@ def twell_logprobs_bwd(logits, targets, inv_temperature: float, lse, entropy, d_
 
 
 # ---------------------------------------------------------------- a training step around the layer
-def _matrix(t, dtypes, rows, dim, name: str) -> tuple:
-    """(address, distance between rows) of a device matrix [rows, dim] whose rows are contiguous
-    (rows, dim None: any); (None, 0) of None."""
+def _matrix(t, dtype, rows, dim, name: str) -> tuple:
+    """(address, distance between rows) of a matrix [rows, dim] whose rows are contiguous; (None, 0) of None."""
     if t is None:
         return None, 0
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: {t.dtype}, the call takes {' or '.join(str(d) for d in dtypes)}")
     shape = t.shape
-    if len(shape) != 2 or (rows is not None and (shape[0] != rows or shape[1] != dim)):
-        raise ValueError(f"{name}: shape {tuple(shape)}, the call takes [{'rows' if rows is None else rows}, "
-                         f"{'columns' if dim is None else dim}]")
-    stride = t.stride()
-    if stride[1] != 1 and shape[1] > 1:
+    if t.dtype == dtype and shape == (rows, dim):
+        stride = t.stride()
+        if stride[1] == 1 or dim == 1:
+            # a matrix of one row may have any stride
+            return t.data_ptr(), stride[0] if rows > 1 else (dim + 7) // 8 * 8
         raise ValueError(f"{name}: a tensor whose rows are contiguous")
-    # a matrix of one row may have any stride
-    return t.data_ptr(), (stride[0] if shape[0] > 1 else (shape[1] + 7) // 8 * 8)
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, the call takes {dtype}")
+    raise ValueError(f"{name}: shape {tuple(shape)}, the call takes [{rows}, {dim}]")
 
 
-def _vectors(dim: int, **given) -> tuple:
-    """(type code, addresses) of the norm's weights: all bfloat16 or all float32."""
-    torch, dtype, out = _torch, None, []
-    for name, t in given.items():
-        if t is not None:
-            if t.dtype not in (torch.bfloat16, torch.float32):
-                raise ValueError(f"{name}: {t.dtype}, the call takes bfloat16 or float32")
-            if dtype is not None and t.dtype != dtype:
-                raise ValueError(f"{name}: {t.dtype}, the other weights are {dtype}")
-            dtype = t.dtype
-            if t.numel() != dim:
-                raise ValueError(f"{name}: {t.numel()} elements, the rows have {dim}")
-            out.append(_arg(t, dtype, dim, name))
-        else:
+def _stream_of(t, name: str) -> tuple:
+    """(type, its code, rows, dim) of a residual stream."""
+    dtype, shape = t.dtype, t.shape
+    code = 0 if dtype == _torch.bfloat16 else 1 if dtype == _torch.float32 else -1
+    if code < 0 or len(shape) != 2:
+        raise ValueError(f"{name}: {dtype} of {len(shape)} dimensions, the call takes [rows, columns] of bfloat16 or "
+                         "float32")
+    return dtype, code, shape[0], shape[1]
+
+
+def _weights(dim: int, w_post, gate, w_pre) -> tuple:
+    """(type code, address of each) of the norm's weights: all bfloat16 or all float32."""
+    dtype, out = None, []
+    for t, name in ((w_post, "w_post"), (gate, "gate"), (w_pre, "w_pre")):
+        if t is None:
             out.append(None)
-    return (1 if dtype == torch.float32 else 0), out
+            continue
+        if dtype is None:
+            dtype = t.dtype
+            if dtype != _torch.bfloat16 and dtype != _torch.float32:
+                raise ValueError(f"{name}: {dtype}, the call takes bfloat16 or float32")
+        elif t.dtype != dtype:
+            raise ValueError(f"{name}: {t.dtype}, the other weights are {dtype}")
+        if t.numel() != dim:
+            raise ValueError(f"{name}: {t.numel()} elements, the rows have {dim}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: a contiguous tensor")
+        out.append(t.data_ptr())
+    return 1 if dtype is not None and dtype != _torch.bfloat16 else 0, out
 
 
 def twell_block_norm(x, y, x_out=None, h=None, *, w_post=None, gate=None, w_pre=None, row_gate=None,
@@ -807,20 +818,18 @@ def twell_block_norm(x, y, x_out=None, h=None, *, w_post=None, gate=None, w_pre=
     """x_out [rows, d] (type of x; may be x itself) = skip_scale x + branch_scale row_gate gate u with u the
     block's output y (bf16), normed if w_post is given; h (bf16) = the norm of x_out with w_pre.  y None: no block."""
     torch = _torch or _setup()
-    bf = (torch.bfloat16,)
-    streams = (torch.bfloat16, torch.float32)
-    x_p, ldx = _matrix(x, streams, None, None, "x")
-    rows, dim = x.shape
+    bf, f32 = torch.bfloat16, torch.float32
+    dtype, kind, rows, dim = _stream_of(x, "x")
+    x_p, ldx = _matrix(x, dtype, rows, dim, "x")
     y_p, ldy = _matrix(y, bf, rows, dim, "y")
-    o_p, ldo = _matrix(x_out, (x.dtype,), rows, dim, "x_out")
+    o_p, ldo = _matrix(x_out, dtype, rows, dim, "x_out")
     h_p, ldh = _matrix(h, bf, rows, dim, "h")
-    code, (post, gate_p, pre) = _vectors(dim, w_post=w_post, gate=gate, w_pre=w_pre)
-    per_row = [_maybe(t, torch.float32, rows, name) for t, name in ((row_gate, "row_gate"), (rstd_post, "rstd_post"),
-                                                                    (rstd_pre, "rstd_pre"))]
+    code, (post, gate_p, pre) = _weights(dim, w_post, gate, w_pre)
+    row_p = _maybe(row_gate, f32, rows, "row_gate")
+    r1, r2 = _maybe(rstd_post, f32, rows, "rstd_post"), _maybe(rstd_pre, f32, rows, "rstd_pre")
     _on_device(x, y, x_out, h, w_post, gate, w_pre, row_gate, rstd_post, rstd_pre)
-    rc = load_library().twell_block_norm(x_p, 0 if x.dtype == torch.bfloat16 else 1, ldx, y_p, ldy, rows, dim, post,
-                                         gate_p, pre, code, per_row[0], skip_scale, branch_scale, eps, o_p, ldo, h_p,
-                                         ldh, per_row[1], per_row[2], _on(stream))
+    rc = load_library().twell_block_norm(x_p, kind, ldx, y_p, ldy, rows, dim, post, gate_p, pre, code, row_p, skip_scale,
+                                         branch_scale, eps, o_p, ldo, h_p, ldh, r1, r2, _on(stream))
     if rc:
         _check(rc, "twell_block_norm")
 
@@ -835,28 +844,26 @@ def twell_block_norm_bwd(dh, d_out, x_out, y, dx=None, dy=None, *, w_post=None, 
     """Gradients of twell_block_norm from those of h (dh, bf16) and x_out (d_out, its type): dx (may be
     d_out itself), dy (bf16), and fp32 sums dw_post, dgate, dw_pre [d], drow_gate [rows]; None: not wanted."""
     torch = _torch or _setup()
-    bf, streams = (torch.bfloat16,), (torch.bfloat16, torch.float32)
-    like = next((t for t in (d_out, x_out, dx) if t is not None), None)
+    bf, f32 = torch.bfloat16, torch.float32
+    like = d_out if d_out is not None else x_out if x_out is not None else dx
     if like is None:
         raise ValueError("d_out, x_out, dx: give one at least")
-    _matrix(like, streams, None, None, "d_out, x_out, dx")
-    (rows, dim), own = like.shape, (like.dtype,)
+    dtype, kind, rows, dim = _stream_of(like, "d_out, x_out, dx")
     dh_p, lddh = _matrix(dh, bf, rows, dim, "dh")
-    do_p, lddo = _matrix(d_out, own, rows, dim, "d_out")
-    o_p, ldo = _matrix(x_out, own, rows, dim, "x_out")
+    do_p, lddo = _matrix(d_out, dtype, rows, dim, "d_out")
+    o_p, ldo = _matrix(x_out, dtype, rows, dim, "x_out")
     y_p, ldy = _matrix(y, bf, rows, dim, "y")
-    dx_p, lddx = _matrix(dx, own, rows, dim, "dx")
+    dx_p, lddx = _matrix(dx, dtype, rows, dim, "dx")
     dy_p, lddy = _matrix(dy, bf, rows, dim, "dy")
-    code, (post, gate_p, pre) = _vectors(dim, w_post=w_post, gate=gate, w_pre=w_pre)
-    f32 = torch.float32
-    row_p, rstd1, rstd2, drow = (_maybe(t, f32, rows, name) for t, name in (
-        (row_gate, "row_gate"), (rstd_post, "rstd_post"), (rstd_pre, "rstd_pre"), (drow_gate, "drow_gate")))
-    dwo, dg, dwi = (_maybe(t, f32, dim, name) for t, name in ((dw_post, "dw_post"), (dgate, "dgate"),
-                                                              (dw_pre, "dw_pre")))
+    code, (post, gate_p, pre) = _weights(dim, w_post, gate, w_pre)
+    row_p, drow = _maybe(row_gate, f32, rows, "row_gate"), _maybe(drow_gate, f32, rows, "drow_gate")
+    rstd1, rstd2 = _maybe(rstd_post, f32, rows, "rstd_post"), _maybe(rstd_pre, f32, rows, "rstd_pre")
+    dwo, dg, dwi = (_maybe(dw_post, f32, dim, "dw_post"), _maybe(dgate, f32, dim, "dgate"),
+                    _maybe(dw_pre, f32, dim, "dw_pre"))
     ws, ws_bytes = (None, 0) if workspace is None else _workspace(workspace)
     _on_device(dh, d_out, x_out, y, dx, dy, w_post, gate, w_pre, row_gate, rstd_post, rstd_pre, dw_post, dgate, dw_pre,
                drow_gate, workspace)
-    rc = load_library().twell_block_norm_bwd(dh_p, lddh, do_p, 0 if like.dtype == torch.bfloat16 else 1, lddo, o_p, ldo,
+    rc = load_library().twell_block_norm_bwd(dh_p, lddh, do_p, kind, lddo, o_p, ldo,
                                              y_p, ldy, rows, dim, post, gate_p, pre, code, row_p, skip_scale,
                                              branch_scale, rstd1, rstd2, dx_p, lddx, dy_p, lddy, dwo, dg, dwi, drow, ws,
                                              ws_bytes, _on(stream))
@@ -880,13 +887,14 @@ def _workspace(t) -> tuple:
 
 def _linear(hidden, weight) -> tuple:
     """(rows, d, vocab, address and distance of hidden, of weight)"""
-    bf = (_torch.bfloat16,)
-    h_p, ldh = _matrix(hidden, bf, None, None, "hidden")
-    rows, dim = hidden.shape
-    w_p, ldw = _matrix(weight, bf, None, None, "weight")
+    bf = _torch.bfloat16
+    for t, name in ((hidden, "hidden"), (weight, "weight")):
+        if t.dim() != 2:
+            raise ValueError(f"{name}: {t.dim()} dimensions, the call takes a matrix")
+    (rows, dim), vocab = hidden.shape, weight.shape[0]
     if weight.shape[1] != dim:
         raise ValueError(f"weight: rows of {weight.shape[1]}, hidden has rows of {dim}")
-    return rows, dim, weight.shape[0], h_p, ldh, w_p, ldw
+    return (rows, dim, vocab, *_matrix(hidden, bf, rows, dim, "hidden"), *_matrix(weight, bf, vocab, dim, "weight"))
 
 
 def twell_linear_logprobs(hidden, weight, targets, inv_temperature: float, logprob, entropy, lse, workspace, status,
@@ -896,7 +904,7 @@ def twell_linear_logprobs(hidden, weight, targets, inv_temperature: float, logpr
     torch = _torch or _setup()
     f32, i32 = torch.float32, torch.int32
     rows, dim, vocab, h_p, ldh, w_p, ldw = _linear(hidden, weight)
-    outs = [_maybe(t, f32, rows, name) for t, name in ((logprob, "logprob"), (entropy, "entropy"), (lse, "lse"))]
+    outs = (_maybe(logprob, f32, rows, "logprob"), _maybe(entropy, f32, rows, "entropy"), _maybe(lse, f32, rows, "lse"))
     t_p, st = _maybe(targets, i32, rows, "targets"), _arg(status, i32, 1, "status")
     ws, ws_bytes = _workspace(workspace)
     _on_device(hidden, weight, targets, logprob, entropy, lse, workspace, status)
@@ -911,13 +919,13 @@ def twell_linear_logprobs_bwd(hidden, weight, targets, inv_temperature: float, l
     """d_hidden [rows, d] and d_weight [vocab, d] bf16 (either may be None) from the upstream gradients of
     logprob and entropy; targets with d_logprob, or entropy with d_entropy, may be None."""
     torch = _torch or _setup()
-    f32, i32, bf = torch.float32, torch.int32, (torch.bfloat16,)
+    f32, i32, bf = torch.float32, torch.int32, torch.bfloat16
     rows, dim, vocab, h_p, ldh, w_p, ldw = _linear(hidden, weight)
     dh_p, lddh = _matrix(d_hidden, bf, rows, dim, "d_hidden")
     dw_p, lddw = _matrix(d_weight, bf, vocab, dim, "d_weight")
     lse_p = _arg(lse, f32, rows, "lse")
-    ent, g, ge = (_maybe(t, f32, rows, name) for t, name in ((entropy, "entropy"), (d_logprob, "d_logprob"),
-                                                             (d_entropy, "d_entropy")))
+    ent, g, ge = (_maybe(entropy, f32, rows, "entropy"), _maybe(d_logprob, f32, rows, "d_logprob"),
+                  _maybe(d_entropy, f32, rows, "d_entropy"))
     t_p, st = _maybe(targets, i32, rows, "targets"), _arg(status, i32, 1, "status")
     ws, ws_bytes = _workspace(workspace)
     _on_device(hidden, weight, targets, lse, entropy, d_logprob, d_entropy, d_hidden, d_weight, workspace, status)

@@ -31,25 +31,35 @@
 namespace twell {
 namespace {
 
-constexpr int kBM = 128, kMinBN = 128, kMaxBN = 256, kBK = 64, kUmmaK = 16;  // kBM: rows of a CTA
+// A tile: kBM rows a CTA, kBN columns.  A step of K takes 257 ns and 0.59 a column, so narrower tiles do not pay even
+// where they leave fewer CTAs idle in the last round (413 x 1032 x 50001: 192 columns 54 us, 128 73, 256 52).
+constexpr int kBM = 128, kBN = 256, kBK = 64, kUmmaK = 16;
 constexpr int kThreads = 384, kEpiWarps = 8;
 // Registers of the forward pass, whose epilogue holds 128 sums a thread.
 constexpr int kRegs = 168, kRegsRest = 56, kRegsEpilogue = 224;
 static_assert(128 * kRegsRest + 256 * kRegsEpilogue <= kThreads * kRegs, "register split");
 constexpr int kRun = 8;  // steps of K that the forward pass adds up in tensor memory
-constexpr int kMaxStages = 8;
 constexpr uint32_t kABytes = kBM * kBK * 2;
 constexpr uint32_t kBarBytes = 256;
 constexpr uint32_t kSumBytes = 2 * 128 * 3 * sizeof(float);  // forward: one half's sums, for the other half
 constexpr uint32_t kBoxBytes = 32 * 128;                     // backward: a box of 32 rows on its way out,
 constexpr uint32_t kOutBytes = kEpiWarps * 2 * kBoxBytes;    // two a warp
 constexpr uint32_t kMaxShared = 232448;
+// R CTAs to a tile; SUMS: the forward pass.  As many stages as there is room for.
+template <int R, bool SUMS>
+struct Cfg {
+  static constexpr uint32_t kBBytes = kBN / R * kBK * 2;  // of a CTA
+  static constexpr uint32_t kRest = 1024 + kBarBytes + (SUMS ? kSumBytes : kOutBytes);
+  static constexpr int kStages = static_cast<int>((kMaxShared - kRest) / (kABytes + kBBytes));
+  static constexpr uint32_t kShared = kRest + kStages * (kABytes + kBBytes);
+};
 constexpr int kBandWide = 64, kBandGradients = 8;
 constexpr int kMaxJobs = 3;
 constexpr int kPlanSms = 152;            // plans do not depend on the device, workspaces neither
 constexpr int64_t kPieceBytes = 1 << 27; // of G: what the L2 cache can hold
 constexpr int kMinPiece = 4096;          // columns; dH's sums are read and written once a piece
 constexpr int kMaxKSplit = 32;
+constexpr int kTileSteps = 5;            // of K, that a tile takes at least: until its results have left
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
 enum JobType { kJobSums, kJobGrad, kJobDHidden, kJobDWeight };
@@ -61,7 +71,6 @@ struct Job {
   int num_m, num_n, num_k;  // tiles, steps of K
   int ksplit;
   int col0;                 // first vocabulary column of the piece
-  int bn;                   // columns of a tile: 128 or 256, or 192 in the forward pass
   int units, band;          // tiles, rows of tiles that are taken together
   int start, light0, light, extra;  // how the tiles are dealt, see Walk
   int a_mn, b_mn;           // operand stored [K][M] / [K][N]
@@ -75,12 +84,11 @@ struct Maps {
 struct Args {
   Job job[kMaxJobs];
   int num_jobs;
-  int stages, b_bytes;  // of the pipeline; of a stage's share of B
   int n_rows, d_model, vocab;
   const int32_t* targets;
   float inv_t;
   // forward
-  float* part;        // [3][num_n][n_rows]: m, S, U
+  float4* part;       // [n_rows][num_n]: m, S, U
   float* of_target;   // [n_rows] x of the target
   // backward
   const float *lse, *entropy, *g, *ge;
@@ -254,14 +262,13 @@ struct Tile {
 
 // A thread's share of a tile: its row's logits (unscaled) of half of the columns, two a word.
 struct Half {
-  F2 v[kMaxBN / 4];
+  F2 v[kBN / 4];
 };
 
 // Adds a run's sums to those of the runs before.
-__device__ __forceinline__ void add_run(Half& x, uint32_t taddr, int width) {
+__device__ __forceinline__ void add_run(Half& x, uint32_t taddr) {
 #pragma unroll
-  for (int k = 0; k < kMaxBN / 2; k += 32) {
-    if (k >= width) break;
+  for (int k = 0; k < kBN / 2; k += 32) {
     uint32_t r[32];
     tmem_ld32(taddr + k, r);
     tmem_ld_wait();
@@ -276,10 +283,10 @@ __device__ __forceinline__ void epilogue_sums(const Args& a, const Job& j, const
                                               float* shared, int turn) {
   const float c = a.inv_t * kLog2e;
   const int target = t.valid && a.targets ? a.targets[t.row] : -1;
-  const int col = t.col0 + t.half * (j.bn / 2), left = min(j.n - col, j.bn / 2);
-  if (left < kMaxBN / 2) {  // columns past the vocabulary or the tile
+  const int col = t.col0 + t.half * (kBN / 2), left = min(j.n - col, kBN / 2);
+  if (left < kBN / 2) {  // columns past the vocabulary
 #pragma unroll
-    for (int i = 0; i < kMaxBN / 4; ++i) {
+    for (int i = 0; i < kBN / 4; ++i) {
       const float2 f = lanes(x.v[i]);
       x.v[i] = pair(2 * i < left ? f.x : -INFINITY, 2 * i + 1 < left ? f.y : -INFINITY);
     }
@@ -287,7 +294,7 @@ __device__ __forceinline__ void epilogue_sums(const Args& a, const Job& j, const
   if (target >= col && target < col + left) {
     F2 own = 0;
 #pragma unroll
-    for (int i = 0; i < kMaxBN / 4; ++i)  // in asm: as C++ it becomes an indexed read, and x goes to local memory
+    for (int i = 0; i < kBN / 4; ++i)  // in asm: as C++ it becomes an indexed read, and x goes to local memory
       asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %2, %3;\n\t@p mov.b64 %0, %1;\n\t}"
           : "+l"(own)
           : "l"(x.v[i]), "r"((target - col) / 2), "r"(i));
@@ -296,13 +303,13 @@ __device__ __forceinline__ void epilogue_sums(const Args& a, const Job& j, const
   Sums all;
   float top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kMaxBN / 4; ++i) top = fmaxf(top, fmaxf(lanes(x.v[i]).x, lanes(x.v[i]).y));
+  for (int i = 0; i < kBN / 4; ++i) top = fmaxf(top, fmaxf(lanes(x.v[i]).x, lanes(x.v[i]).y));
   all.m = top * c;
   const float ref = all.m == -INFINITY ? 0.0f : all.m;
   const F2 c2 = pair(c, c), minus = pair(-ref, -ref);
   F2 s[2] = {0, 0}, u[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < kMaxBN / 4; ++i) {
+  for (int i = 0; i < kBN / 4; ++i) {
     const float2 y = lanes(fma2(x.v[i], c2, minus));
     const F2 e = pair(ex2(y.x), ex2(y.y));
     s[i & 1] = add2(s[i & 1], e);
@@ -315,9 +322,7 @@ __device__ __forceinline__ void epilogue_sums(const Args& a, const Job& j, const
   asm volatile("bar.sync %0, 64;" ::"r"(t.lg + 1) : "memory");
   if (t.half == 1 || !t.valid) return;
   all.join(at[0], at[1], at[2]);
-  const int64_t plane = static_cast<int64_t>(j.num_n) * a.n_rows;
-  float* const out = a.part + static_cast<int64_t>(n_blk) * a.n_rows + t.row;
-  out[0] = all.m, out[plane] = all.s, out[2 * plane] = all.u;
+  a.part[static_cast<int64_t>(t.row) * j.num_n + n_blk] = make_float4(all.m, all.s, all.u, 0.0f);
 }
 
 // Results leave through shared memory by TMA, a box of 32 rows of 128 bytes a time, so that memory gets whole
@@ -375,9 +380,9 @@ __device__ __forceinline__ void epilogue_grad(const Args& a, const Job& j, const
   }
   const F2 inv_t2 = pair(a.inv_t, a.inv_t), minus = pair(-lse, -lse), log2e = pair(kLog2e, kLog2e);
   const F2 a02 = pair(a0, a0), a12 = pair(a1, a1);
-  const int from = t.half * (j.bn / 2);
+  const int from = t.half * (kBN / 2);
 #pragma unroll 1
-  for (int k = from; k < from + j.bn / 2; k += 64) {
+  for (int k = from; k < from + kBN / 2; k += 64) {
     const int col = t.col0 + k;
     if (col >= j.n) break;
     uint8_t* const box = out.open();
@@ -410,11 +415,11 @@ __device__ __forceinline__ void epilogue_grad(const Args& a, const Job& j, const
 // A gradient's tile: bf16, or dH's sums in fp32 while pieces or ranges are still to be added.
 __device__ __forceinline__ void epilogue_store(const Args& a, const Job& j, const Tile& t, int ks,
                                                const CUtensorMap* map, Box& out) {
-  const int lane = threadIdx.x & 31, from = t.half * (j.bn / 2);
+  const int lane = threadIdx.x & 31, from = t.half * (kBN / 2);
   if (!j.round) {
     const int y = ks * a.sum_rows + t.row - lane;
 #pragma unroll 1
-    for (int k = from; k < from + j.bn / 2; k += 32) {
+    for (int k = from; k < from + kBN / 2; k += 32) {
       if (t.col0 + k >= j.n) break;
       uint32_t r[32];
       tmem_ld32(t.taddr + k, r);
@@ -431,7 +436,7 @@ __device__ __forceinline__ void epilogue_store(const Args& a, const Job& j, cons
     return;
   }
 #pragma unroll 1
-  for (int k = from; k < from + j.bn / 2; k += 64) {
+  for (int k = from; k < from + kBN / 2; k += 64) {
     if (t.col0 + k >= j.n) break;
     uint8_t* const box = out.open();
 #pragma unroll
@@ -510,19 +515,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int S = a.stages;
+  using C = Cfg<R, SUMS>;
+  constexpr int S = C::kStages;
   uint8_t* const sA = smem;
   uint8_t* const sB = smem + S * kABytes;
-  uint8_t* const extra = sB + S * a.b_bytes;  // forward: sums, backward: boxes
+  uint8_t* const extra = sB + S * C::kBBytes;  // forward: sums, backward: boxes
   // of the first CTA: full, tempty (and its own of the others); of both: empty, tfull
   uint64_t* const full = reinterpret_cast<uint64_t*>(extra + (SUMS ? kSumBytes : kOutBytes));
-  uint64_t* const empty = full + kMaxStages;
-  uint64_t* const tfull = empty + kMaxStages;
+  uint64_t* const empty = full + S;
+  uint64_t* const tfull = empty + S;
   uint64_t* const tempty = tfull + 2;
   uint64_t* const drain = tempty + 2;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* const abort = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  static_assert((2 * kMaxStages + 5) * 8 + 8 <= static_cast<int>(kBarBytes), "barrier region");
+  static_assert((2 * S + 5) * 8 + 8 <= static_cast<int>(kBarBytes), "barrier region");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = R == 1 ? 0 : static_cast<int>(cluster_rank());
@@ -558,16 +564,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t leader = elect_one();
       const bool is_b = warp == 2;
       uint8_t* const base = is_b ? sB : sA;
-      const uint32_t pitch = is_b ? a.b_bytes : kABytes;
+      const uint32_t pitch = is_b ? C::kBBytes : kABytes;
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       while (ok && walk.next(a, x)) {
         const Job& j = a.job[x.job];
         const CUtensorMap* const map = is_b ? &maps.b[x.job] : &maps.a[x.job];
-        const int at = is_b ? x.n_blk * j.bn + rank * (j.bn / R) : (x.m_blk * R + rank) * kBM;
+        const int at = is_b ? x.n_blk * kBN + rank * (kBN / R) : (x.m_blk * R + rank) * kBM;
         const bool mn = is_b ? j.b_mn : j.a_mn;  // [K][at]: boxes of 64 columns by 64 rows of K; else one of 64 columns of K
-        const int rows = is_b ? j.bn / R : kBM, boxes = mn ? rows / 64 : 1;
+        const int rows = is_b ? kBN / R : kBM, boxes = mn ? rows / 64 : 1;
         const uint32_t bytes = rows * kBK * 2;
         const int dx = mn ? 0 : kBK, dy = mn ? kBK : 0;
         int cx = mn ? at : x.kb0 * kBK, cy = mn ? x.kb0 * kBK : at;
@@ -595,10 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      const uint32_t a_stage = kABytes >> 4, b_stage = static_cast<uint32_t>(a.b_bytes) >> 4;
+      const uint32_t a_stage = kABytes >> 4, b_stage = C::kBBytes >> 4;
       while (ok && walk.next(a, x)) {
         const Job& j = a.job[x.job];
-        const uint32_t idesc = idesc_bf16_f32(kBM * R, j.bn) | (j.a_mn ? 1u << 15 : 0u) | (j.b_mn ? 1u << 16 : 0u);
+        const uint32_t idesc = idesc_bf16_f32(kBM * R, kBN) | (j.a_mn ? 1u << 15 : 0u) | (j.b_mn ? 1u << 16 : 0u);
         // a step of 16 along K: 32 bytes of a K-major row, 16 rows of 128 bytes of the others
         const uint64_t a_step = j.a_mn ? 128u : 2u, b_step = j.b_mn ? 128u : 2u;
         const uint64_t ad0 = j.a_mn ? smem_desc_sw128_nmajor(smem_u32(sA), 8192) : smem_desc_sw128(smem_u32(sA));
@@ -610,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kMaxBN);
+          const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kBN);
           uint32_t add = 0;
           for (int n = k1 - k0; n > 0; --n) {
             if (!mbar_wait(&full[stage], phase, limit, abort)) {
@@ -672,14 +678,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && walk.next(a, x)) {
       const Job& j = a.job[x.job];
       t.row = (x.m_blk * R + rank) * kBM + t.lg * 32 + lane;
-      t.col0 = x.n_blk * j.bn;
+      t.col0 = x.n_blk * kBN;
       t.valid = t.row < j.m;
       auto wait_full = [&]() {
         ok = mbar_wait(&tfull[acc], acc_phase, limit, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
         tc_fence_after();
-        t.taddr = lane_base + static_cast<uint32_t>(acc * kMaxBN);
+        t.taddr = lane_base + static_cast<uint32_t>(acc * kBN);
         return ok;
       };
       auto release = [&]() {
@@ -699,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int k0 = x.kb0; k0 < x.kb1; k0 += kRun) {
           if (!wait_full()) break;
-          add_run(sums, t.taddr + t.half * (j.bn / 2), j.bn / 2);
+          add_run(sums, t.taddr + t.half * (kBN / 2));
           release();
         }
         if (!ok) break;
@@ -727,38 +733,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 struct JoinArgs {
-  const float *part, *of_target;
+  const float4* part;
+  const float* of_target;
   int num_n, n_rows, vocab;
   const int32_t* targets;
   float *logprob, *entropy, *lse;
 };
 
-// The tiles' sums of 32 rows: a lane a row, the warps take tiles in turn and are joined in order.
-constexpr int kJoinWarps = 16;
-__global__ void __launch_bounds__(kJoinWarps * 32) linear_join_kernel(const JoinArgs a) {
-  __shared__ float sh[kJoinWarps][3][32];
+// The tiles' sums of a row: a warp a row, each lane tiles in turn, then lanes by halves.
+__global__ void __launch_bounds__(32) linear_join_kernel(const JoinArgs a) {
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x * 32 + lane;
-  Sums all;
-  if (row < a.n_rows) {
-    const int64_t plane = static_cast<int64_t>(a.num_n) * a.n_rows;
+  const int lane = threadIdx.x;
+  for (int row = blockIdx.x; row < a.n_rows; row += gridDim.x) {
+    const float4* const at = a.part + static_cast<int64_t>(row) * a.num_n;
+    Sums all;
 #pragma unroll 4
-    for (int k = warp; k < a.num_n; k += kJoinWarps) {
-      const float* const at = a.part + static_cast<int64_t>(k) * a.n_rows + row;
-      all.join(at[0], at[plane], at[2 * plane]);
+    for (int k = lane; k < a.num_n; k += 32) {
+      const float4 p = at[k];
+      all.join(p.x, p.y, p.z);
     }
-  }
-  sh[warp][0][lane] = all.m, sh[warp][1][lane] = all.s, sh[warp][2][lane] = all.u;
-  __syncthreads();
-  if (warp > 0 || row >= a.n_rows) return;
-  for (int w = 1; w < kJoinWarps; ++w) all.join(sh[w][0][lane], sh[w][1][lane], sh[w][2][lane]);
-  const float log_s = log2f(all.s), lse = kLn2 * (all.m + log_s);
-  if (a.lse) a.lse[row] = lse;
-  if (a.entropy) a.entropy[row] = all.s == 0.0f ? 0.0f : kLn2 * (log_s - all.u / all.s);
-  if (a.logprob) {
-    const int t = a.targets[row];
-    // a row of -inf only: -inf, as all its log probabilities
-    a.logprob[row] = t < 0 || t >= a.vocab ? 0.0f : all.s == 0.0f ? -INFINITY : a.of_target[row] - lse;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      // both lanes of a pair join the lower one's sums first, so that all come to the same bits
+      const float m = __shfl_xor_sync(0xffffffffu, all.m, o), s = __shfl_xor_sync(0xffffffffu, all.s, o),
+                  u = __shfl_xor_sync(0xffffffffu, all.u, o);
+      Sums low = all, high;
+      high.m = m, high.s = s, high.u = u;
+      if (lane & o) low = high, high = all;
+      low.join(high.m, high.s, high.u);
+      all = low;
+    }
+    if (lane > 0) continue;
+    const float log_s = log2f(all.s), lse = kLn2 * (all.m + log_s);
+    if (a.lse) a.lse[row] = lse;
+    if (a.entropy) a.entropy[row] = all.s == 0.0f ? 0.0f : kLn2 * (log_s - all.u / all.s);
+    if (a.logprob) {
+      const int t = a.targets[row];
+      // a row of -inf only: -inf, as all its log probabilities
+      a.logprob[row] = t < 0 || t >= a.vocab ? 0.0f : all.s == 0.0f ? -INFINITY : a.of_target[row] - lse;
+    }
   }
 }
 
@@ -769,24 +782,30 @@ struct ReduceArgs {
   int64_t ld;
 };
 
-// dH from the sums of K's ranges, added in order; 8 elements a thread.
+// dH from the sums of K's ranges, added in order, 8 of them on the way at a time; 4 elements a thread.
 __global__ void __launch_bounds__(256) linear_reduce_kernel(const ReduceArgs a) {
   grid_dependency_wait();
-  const int64_t vecs = a.dim / 8, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t vecs = a.dim / 4, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= vecs * a.n_rows) return;
-  const int64_t row = i / vecs, c = i % vecs * 8, plane = static_cast<int64_t>(a.sum_rows) * a.dim;
+  const int64_t row = i / vecs, c = i % vecs * 4, plane = static_cast<int64_t>(a.sum_rows) * a.dim;
   const float* const at = a.sum + row * a.dim + c;
-  float f[8] = {};
-  for (int k = 0; k < a.ksplit; ++k) {
-    const float4 x = *reinterpret_cast<const float4*>(at + k * plane), y = *reinterpret_cast<const float4*>(at + k * plane + 4);
-    f[0] += x.x, f[1] += x.y, f[2] += x.z, f[3] += x.w, f[4] += y.x, f[5] += y.y, f[6] += y.z, f[7] += y.w;
+  float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int k = 0; k < a.ksplit; k += 8) {
+    float4 x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      x[e] = k + e < a.ksplit ? *reinterpret_cast<const float4*>(at + (k + e) * plane) : make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f.x += x[e].x, f.y += x[e].y, f.z += x[e].z, f.w += x[e].w;
   }
-  *reinterpret_cast<uint4*>(a.out + row * a.ld + c) =
-      make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+  *reinterpret_cast<uint2*>(a.out + row * a.ld + c) = make_uint2(bf16_pair(f.x, f.y), bf16_pair(f.z, f.w));
 }
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 size_t round_up(size_t x, size_t to) { return (x + to - 1) / to * to; }
+
+// CTAs to a tile: a pair from 129 rows on.
+int ctas_of(int64_t n_rows) { return n_rows > kBM ? 2 : 1; }
 
 // Rows of dH's fp32 sums: whole tiles, as a tile leaves whole.
 int64_t sum_rows(int64_t n_rows) { return (n_rows + 255) / 256 * 256; }
@@ -804,14 +823,14 @@ Plan plan_bwd(int64_t n_rows, int64_t d, int64_t vocab) {
   p.pieces = ceil_div(vocab, most);
   p.piece = ceil_div(ceil_div(vocab, p.pieces), 256) * 256;
   p.pieces = ceil_div(vocab, p.piece);
-  // dH's tiles have long sums: where they are few, K is cut so that none takes longer than a
-  // CTA's share of the two products
+  // dH's tiles have long sums: where there are fewer than CTAs (or pairs), K is cut so that all have one.
+  // A CTA asks for 57 to 83 GB/s alone, so all of them are needed even where the other product could fill
+  // them (16 x 4096 x 131072: 612 us with three ranges, dH's 48 CTAs the last to end).
+  const int ctas = ctas_of(n_rows);
+  const int64_t tiles = ceil_div(n_rows, kBM * ctas) * static_cast<int64_t>(ceil_div(d, kBN));
   const int64_t num_k = ceil_div(std::min<int64_t>(p.piece, vocab), kBK);
-  const int64_t dh = ceil_div(n_rows, kBM) * static_cast<int64_t>(ceil_div(d, kMaxBN)) * num_k;
-  const int64_t dw = ceil_div(std::min<int64_t>(p.piece, vocab), kBM) * static_cast<int64_t>(ceil_div(d, kMaxBN)) *
-                     ceil_div(n_rows, kBK);
-  const int64_t share = std::max<int64_t>(8, (dh + dw) / kPlanSms);
-  p.ksplit = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({num_k, kMaxKSplit, ceil_div(num_k, share)})));
+  p.ksplit = static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>({kMaxKSplit, num_k / 8, kPlanSms / ctas / tiles})));
   p.grad_bytes = round_up(static_cast<size_t>(n_rows) * p.piece * 2, 256);
   p.sum_bytes = p.pieces > 1 || p.ksplit > 1 ? round_up(static_cast<size_t>(p.ksplit) * sum_rows(n_rows) * d * 4, 256) : 0;
   p.bytes = p.grad_bytes * (p.pieces > 1 ? 2 : 1) + p.sum_bytes + 256;
@@ -819,33 +838,17 @@ Plan plan_bwd(int64_t n_rows, int64_t d, int64_t vocab) {
 }
 
 size_t fwd_bytes(int64_t n_rows, int64_t vocab) {
-  return round_up(static_cast<size_t>(n_rows) * 4 * (3 * ceil_div(vocab, kMinBN) + 1), 256) + 256;
+  return round_up(static_cast<size_t>(n_rows) * 4 * (4 * ceil_div(vocab, kBN) + 1), 256) + 512;
 }
-
-// CTAs to a tile: a pair from 129 rows on.
-int ctas_of(int n_rows) { return n_rows > kBM ? 2 : 1; }
 
 // CTAs (or pairs) that work at a time.
 int slots_of(int ctas) { return std::max(1, sm_count() / ctas); }
-
-// Columns of a tile, of those that are allowed: what leaves the least time in the last round where a
-// launch has this job alone (`alone`), or the least work past the edge.  A tile's rows are read
-// again for each, which makes narrow tiles dearer (24 columns' worth).
-int choose_bn(std::initializer_list<int> allowed, int64_t num_m, int n, int slots, bool alone) {
-  int best = 0;
-  int64_t least = 0;
-  for (int bn : allowed) {
-    const int64_t tiles = num_m * ceil_div(n, bn), cost = (alone ? ceil_div(tiles, slots) : tiles) * (bn + 24);
-    if (!best || cost < least) best = bn, least = cost;
-  }
-  return best;
-}
 
 // Adds a job.  A: [m][k], or [k][m] with a_mn; likewise B; their rows lie lda, ldb elements apart.
 int set_job(Maps* maps, Args* args, int ctas, Job j, const uint16_t* A, int64_t lda, const uint16_t* B, int64_t ldb,
             int k) {
   const int i = args->num_jobs++;
-  j.num_m = ceil_div(j.m, kBM * ctas), j.num_n = ceil_div(j.n, j.bn), j.num_k = ceil_div(k, kBK);
+  j.num_m = ceil_div(j.m, kBM * ctas), j.num_n = ceil_div(j.n, kBN), j.num_k = ceil_div(k, kBK);
   j.ksplit = std::min(j.ksplit, j.num_k);
   const int64_t units = static_cast<int64_t>(j.num_m) * j.num_n * j.ksplit;
   if (units > (1 << 29)) return TWELL_ERR_UNSUPPORTED;
@@ -856,7 +859,7 @@ int set_job(Maps* maps, Args* args, int ctas, Job j, const uint16_t* A, int64_t 
   else
     KV_TRY(encode_tmap_2d(&maps->a[i], A, k, j.m, lda * 2, kBK, kBM));
   if (j.b_mn) return encode_tmap_2d(&maps->b[i], B, j.n, k, ldb * 2, 64, kBK);
-  return encode_tmap_2d(&maps->b[i], B, k, j.n, ldb * 2, kBK, j.bn / ctas);
+  return encode_tmap_2d(&maps->b[i], B, k, j.n, ldb * 2, kBK, kBN / ctas);
 }
 
 // Deals the jobs' tiles to the CTAs or pairs (see Walk); returns how many of those there are.
@@ -868,7 +871,7 @@ int deal(Args* args, int slots) {
   int64_t cost_before = 0;
   for (int i = 0; i < args->num_jobs; ++i) {
     Job& j = args->job[i];
-    const int64_t cost = std::max<int64_t>(1, static_cast<int64_t>(j.num_k) * j.bn / j.ksplit);
+    const int64_t cost = std::max(kTileSteps, j.num_k / j.ksplit);
     j.start = start, j.light0 = start, j.light = all - start;
     j.extra = start > 0 ? static_cast<int>(std::min<int64_t>(cost_before / cost, j.units / j.light)) : 0;
     if (j.extra < 2) j.extra = 0;  // a round more for some is what beginning there gives, too
@@ -881,7 +884,7 @@ int deal(Args* args, int slots) {
 template <int R, bool SUMS>
 int launch_jobs(const Maps& maps, Args args, cudaStream_t s) {
   const auto kernel = linear_kernel<R, SUMS>;
-  KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(kMaxShared)));
+  KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(Cfg<R, SUMS>::kShared)));
   if (SUMS) {  // the split of the registers waits for as many as only a launch with kRegs a thread has
     static const int regs = [&] {
       cudaFuncAttributes f;
@@ -889,16 +892,11 @@ int launch_jobs(const Maps& maps, Args args, cudaStream_t s) {
     }();
     if (regs < kRegs) return TWELL_ERR_CUDA;
   }
-  int bn = 0;
-  for (int i = 0; i < args.num_jobs; ++i) bn = std::max(bn, args.job[i].bn);
-  args.b_bytes = bn / R * kBK * 2;
-  const uint32_t stage = kABytes + args.b_bytes, rest = 1024 + kBarBytes + (SUMS ? kSumBytes : kOutBytes);
-  args.stages = static_cast<int>(std::min<uint32_t>(kMaxStages, (kMaxShared - rest) / stage));
   const int all = deal(&args, slots_of(R));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(all) * R);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = rest + args.stages * stage;
+  cfg.dynamicSmemBytes = Cfg<R, SUMS>::kShared;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -961,16 +959,15 @@ extern "C" TWELL_API int twell_linear_logprobs(const uint16_t* H, int64_t ldh, c
   a.n_rows = n_rows, a.d_model = d_model, a.vocab = vocab, a.targets = targets, a.inv_t = inv_temperature;
   a.status = status, a.wait_limit_ns = kWaitLimitNs;
   a.of_target = static_cast<float*>(workspace);
-  a.part = a.of_target + n_rows;
+  a.part = reinterpret_cast<float4*>(static_cast<uint8_t*>(workspace) + round_up(static_cast<size_t>(n_rows) * 4, 256));
   Job j = {};
   j.type = kJobSums, j.band = kBandWide, j.m = n_rows, j.n = vocab, j.ksplit = 1;
   const int ctas = ctas_of(n_rows);
-  j.bn = choose_bn({256}, ceil_div(n_rows, kBM * ctas), vocab, slots_of(ctas), true);
   KV_TRY(set_job(&maps, &a, ctas, j, H, ldh, W, ldw, d_model));
   KV_TRY((ctas == 2 ? launch_jobs<2, true>(maps, a, s) : launch_jobs<1, true>(maps, a, s)));
   const JoinArgs join{a.part, a.of_target, a.job[0].num_n, n_rows, vocab, targets, logprob, entropy, lse};
   LaunchScope scope(TWELL_KERNEL_LINEAR_LOGPROBS, s);
-  return launch_pdl(linear_join_kernel, dim3(ceil_div(n_rows, 32)), dim3(kJoinWarps * 32), 0, s, join) == cudaSuccess
+  return launch_pdl(linear_join_kernel, dim3(std::min(n_rows, 24 * sm_count())), dim3(32), 0, s, join) == cudaSuccess
              ? TWELL_OK
              : TWELL_ERR_CUDA;
 }
@@ -1018,7 +1015,7 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
   float* const dh_sum = reinterpret_cast<float*>(ws + plan.grad_bytes * (plan.pieces > 1 ? 2 : 1));
   base.dh_sum = dh_sum, base.sum_rows = static_cast<int>(sum_rows(n_rows));
   base.status = status, base.wait_limit_ns = kWaitLimitNs;
-  const int ctas = ctas_of(n_rows), slots = slots_of(ctas);
+  const int ctas = ctas_of(n_rows);
   for (int p = 0; p <= plan.pieces; ++p) {
     Maps maps;
     Args a = base;
@@ -1028,7 +1025,6 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
       const uint16_t* const Wp = W + static_cast<int64_t>(col0) * ldw;
       Job j = {};
       j.col0 = col0, j.band = kBandGradients, j.b_mn = 1;
-      j.bn = choose_bn({256}, 1, d_model, slots, false);
       if (dH) {
         j.type = kJobDHidden, j.m = n_rows, j.n = d_model, j.add = p > 1;
         j.round = p == plan.pieces && plan.ksplit == 1;
@@ -1054,7 +1050,6 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
       Job j = {};
       j.type = kJobGrad, j.band = kBandWide, j.m = n_rows, j.n = std::min(plan.piece, vocab - col0), j.ksplit = 1;
       j.col0 = col0;
-      j.bn = choose_bn({256}, ceil_div(n_rows, kBM * ctas), j.n, slots, a.num_jobs == 0);
       KV_TRY(encode_tmap_2d(&maps.out[a.num_jobs], buffer[p & 1], plan.piece, n_rows,
                             static_cast<uint64_t>(plan.piece) * 2, 64, 32));
       KV_TRY(set_job(&maps, &a, ctas, j, H, ldh, W + static_cast<int64_t>(col0) * ldw, ldw, d_model));
@@ -1064,7 +1059,7 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
   if (!dH || plan.ksplit == 1) return TWELL_OK;
   const ReduceArgs r{dh_sum, plan.ksplit, n_rows, base.sum_rows, d_model, dH, lddh};
   LaunchScope scope(TWELL_KERNEL_LINEAR_LOGPROBS_BWD, s);
-  return launch_pdl(linear_reduce_kernel, dim3(ceil_div(static_cast<int64_t>(n_rows) * (d_model / 8), 256)), dim3(256),
+  return launch_pdl(linear_reduce_kernel, dim3(ceil_div(static_cast<int64_t>(n_rows) * (d_model / 4), 256)), dim3(256),
                     0, s, r) == cudaSuccess
              ? TWELL_OK
              : TWELL_ERR_CUDA;
