@@ -12,17 +12,22 @@
 //   drow_gate = sum_c branch gate w_post dz s
 // so the two vectors of the branch share one sum over the rows.
 //
-// A row is held in registers by a group of threads, 16 elements a thread, and is
-// read once.  One CTA an SM stays and takes rows in turn, several groups side by side;
-// each thread copies its own elements of the next rows into its own shared memory
-// asynchronously, which keeps enough bytes on the way without a barrier or a register.
-// Arithmetic goes two fp32 lanes an instruction: with one, instructions bound it (8192 x 2048 bf16: 31 us
-// forward, 54 backward).  The gradient's three sums of a row are taken together:
+// A row is taken by a group of threads, 16 elements a thread, and is read from memory once; up to 256
+// columns several rows share a warp.  One CTA an SM stays and takes rows in turn, several groups side by
+// side; each thread copies its own elements of the next rows into its own shared memory
+// asynchronously, which keeps enough bytes on the way without a barrier or a register, and reads
+// them from there once for each pass over the row.  Arithmetic goes two fp32 lanes an
+// instruction: with one, instructions bound it (8192 x 2048 bf16: 31 us forward, 54 backward).  The
+// gradient's three sums of a row are taken together:
 //   sum t s / scale = sum w (d_out + r2 a) s - r2 c2 sum w v s,  c2 = mean(a v), w = gate w_post.
-// HBM bounds long calls (8192 x 2048 bf16: 25 us, 5.4 TB/s; gradient 41 us, 4.9 TB/s, 3 of it the sum over
-// the CTAs), the launch and a row's chain of two sums short ones (16 x 4096: 2.9 us).
-// All sums are fp32: a thread's own elements in order, then a tree over the group;
-// sums over the rows by groups, CTAs and then runs of CTAs in order, so equal calls give equal bits.
+// HBM bounds long calls (16384 x 2048 bf16: 48 us, 5.6 TB/s; gradient 71 us, 5.7 TB/s; 8192 rows 26 and 41, where
+// starting and the sum over the CTAs are 5 and 8 of it), the launch and a row's chain of two sums short
+// ones (16 x 4096: 2.8 us).  The gradient keeps its sums over the rows in registers, so its CTAs have 512
+// threads (with 640 or 768 they spill: 54 and 65 us), and rows of 4104 to 8191 columns leave it one group
+// an SM (8000 x 4104: 116 us, 3.4 TB/s; forward, 1024 threads, 53).  Above 8192 columns the weights are read anew
+// for each row (2048 x 16384: 88 us, gradient 205).
+// All sums are fp32: a thread's own elements in order, then a tree over the group; sums over the
+// rows by groups, CTAs and then runs of CTAs in order, so equal calls give equal bits.
 #include <algorithm>
 
 #include "kv_internal.h"
@@ -32,12 +37,12 @@ namespace {
 
 constexpr int kMaxDim = 16384;
 constexpr int kMaxParts = 160;      // CTAs that leave sums of their rows
-constexpr int kMaxGroups = 20;      // rows of a CTA at a time
+constexpr int kMaxBarriers = 15;    // groups of more than a warp in a CTA
 constexpr int kMaxStages = 4;       // rows on the way to a thread
-constexpr int kSharedBytes = 208 * 1024;  // beside 15 KB for the sums
-constexpr int kWideDim = 8192;      // above, 1024 threads a row and its weights in no registers or shared memory
-constexpr int kThreads = 512, kBwdThreads = 512;  // of a CTA: what registers allow
-constexpr int kV = 2;               // 16-byte pieces of a row a thread has
+constexpr int kSharedBytes = 208 * 1024;  // beside 12 KB for the sums
+constexpr int kV = 2;               // pieces of 8 elements a thread
+constexpr int kThreads = 1024, kBwdThreads = 512;  // of a CTA: what registers allow
+constexpr int kWide = 8192;         // above, 1024 threads a row and its weights read anew for each
 
 struct NormArgs {
   const void* x;
@@ -140,30 +145,43 @@ __device__ __forceinline__ float warp_sums(const float* scratch, int group) {
   return (a.x + a.y) + (a.z + a.w);
 }
 
-// The sum over the group's threads, in every thread of it.  scratch: 32 floats of
+// The sum over the group's threads, in every thread of it (SUB: a part of a warp).  scratch: 32 floats of
 // the group's own, zero past its warps; free again once the group has passed another such barrier.
+template <bool SUB>
 __device__ __forceinline__ float group_sum(float v, int group, int id, int thread, float* scratch) {
+  if constexpr (SUB) {
+    for (int o = group >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  } else {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (group == 32) return v;
-  if ((thread & 31) == 0) scratch[thread >> 5] = v;
-  asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(group) : "memory");
-  return warp_sums(scratch, group);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (group == 32) return v;
+    if ((thread & 31) == 0) scratch[thread >> 5] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(group) : "memory");
+    return warp_sums(scratch, group);
+  }
 }
 
 // Three sums at once.  scratch: [3][32].
+template <bool SUB>
 __device__ __forceinline__ void group_sum3(float (&v)[3], int group, int id, int thread, float* scratch) {
+  if constexpr (SUB) {
+    for (int o = group >> 1; o > 0; o >>= 1)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+      for (int k = 0; k < 3; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  } else {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if (group == 32) return;
-  if ((thread & 31) == 0)
+    for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-    for (int k = 0; k < 3; ++k) scratch[k * 32 + (thread >> 5)] = v[k];
-  asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(group) : "memory");
+      for (int k = 0; k < 3; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    if (group == 32) return;
+    if ((thread & 31) == 0)
 #pragma unroll
-  for (int k = 0; k < 3; ++k) v[k] = warp_sums(scratch + k * 32, group);
+      for (int k = 0; k < 3; ++k) scratch[k * 32 + (thread >> 5)] = v[k];
+    asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(group) : "memory");
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] = warp_sums(scratch + k * 32, group);
+  }
 }
 
 __device__ __forceinline__ void copy16(uint8_t* dst, const void* src) {
@@ -261,6 +279,7 @@ struct Layout {
 // planes of a thread's 16-byte pieces, read without conflicts), or read anew where rows are too wide for that.
 template <typename T, bool SHARED>
 struct Weights {
+  static constexpr int V = kV;
   uint8_t* base;  // [branch, pre][piece][2][group] of 16 bytes
   const void *post, *gate, *pre;
   bool f32;
@@ -297,16 +316,16 @@ struct Weights {
     return Oct{{pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7])}};
   }
   __device__ __forceinline__ ulonglong2* slot(bool branch, int i, int h) const {
-    return reinterpret_cast<ulonglong2*>(base) + (((branch ? 0 : kV) + i) * 2 + h) * group + thread;
+    return reinterpret_cast<ulonglong2*>(base) + (((branch ? 0 : V) + i) * 2 + h) * group + thread;
   }
   // by the first group's threads, a barrier before the first use
   __device__ __forceinline__ void fill() const {
     if constexpr (SHARED) {
 #pragma unroll
-      for (int i = 0; i < 2 * kV; ++i) {
-        const Oct w = make(i < kV, i % kV);
-        *slot(i < kV, i % kV, 0) = make_ulonglong2(w.v[0], w.v[1]);
-        *slot(i < kV, i % kV, 1) = make_ulonglong2(w.v[2], w.v[3]);
+      for (int i = 0; i < 2 * V; ++i) {
+        const Oct w = make(i < V, i % V);
+        *slot(i < V, i % V, 0) = make_ulonglong2(w.v[0], w.v[1]);
+        *slot(i < V, i % V, 1) = make_ulonglong2(w.v[2], w.v[3]);
       }
     }
   }
@@ -318,39 +337,43 @@ struct Weights {
 };
 
 // What the two kernels set up alike.
-template <typename T, int NT>
+template <typename T, bool SHARED, bool SUB>
 struct Setup {
-  static constexpr bool kShared = NT < 1024;
-  int groups, id, thread, pitch;
+  static constexpr int V = kV;
+  static constexpr bool kShared = SHARED;
+  int groups, id, thread, pitch, rows;  // rows: of a warp
   Layout<T> at;
   Weights<T, kShared> weights;
   uint8_t *ring, *mine;
   __device__ __forceinline__ Setup(uint8_t* smem, int group, int dim, const void* post, const void* gate,
                                    const void* pre, bool f32) {
     groups = blockDim.x / group, id = threadIdx.x / group, thread = threadIdx.x % group;
-    pitch = blockDim.x * 16;
+    pitch = blockDim.x * 16, rows = SUB ? 32 / group : 1;
     at = Layout<T>{dim, thread * Layout<T>::kRun, group * Layout<T>::kRun};
     weights = Weights<T, kShared>{smem, post, gate, pre, f32, group, thread, at};
-    ring = smem + (kShared ? 2 * kV * 2 * 16 * group : 0);
+    ring = smem + (kShared ? 2 * V * 2 * 16 * group : 0);
     mine = ring + threadIdx.x * 16;
   }
+  // the row of this warp's first group: loops go by it, so that a warp stays together
+  __device__ __forceinline__ int64_t first_row(int64_t row) const { return SUB ? row - id % rows : row; }
   // Zeros where no copy goes.
   __device__ __forceinline__ void clear(int pieces) const {
-    if (at.on(kV - 1, Layout<T>::kRuns - 1)) return;
+    if (at.on(V - 1, Layout<T>::kRuns - 1)) return;
     for (int p = 0; p < pieces; ++p) *reinterpret_cast<uint4*>(mine + p * pitch) = make_uint4(0, 0, 0, 0);
   }
 };
 
 // A row for each group of threads in turn; Y: there is a block's output.
-template <typename T, int NT, bool Y>
+template <typename T, int NT, bool SHARED, bool SUB, bool Y>
 __global__ void __launch_bounds__(NT, 1) block_norm_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ __align__(16) float scratch[kMaxGroups][2][2][32];  // two sums of a row, rows in turn
-  for (int i = threadIdx.x; i < kMaxGroups * 128; i += blockDim.x) (&scratch[0][0][0][0])[i] = 0.0f;
+  __shared__ __align__(16) float scratch[kMaxBarriers][2][2][32];  // two sums of a row, rows in turn
+  for (int i = threadIdx.x; i < kMaxBarriers * 128; i += blockDim.x) (&scratch[0][0][0][0])[i] = 0.0f;
   grid_dependency_wait();
-  const Setup<T, NT> g(smem, a.group, a.dim, a.w_post, a.gate, a.w_pre, a.w_f32);
+  constexpr int V = kV;
+  const Setup<T, SHARED, SUB> g(smem, a.group, a.dim, a.w_post, a.gate, a.w_pre, a.w_f32);
   const Layout<T>& at = g.at;
-  constexpr int V = kV, kX = Layout<T>::kPieces, kPieces = kX + (Y ? 1 : 0);  // of x, of y
+  constexpr int kX = Layout<T>::kPieces, kPieces = kX + (Y ? 1 : 0);  // of x, of y
   const int pitch = g.pitch, step = gridDim.x * g.groups;
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
   g.clear(a.stages * V * kPieces);
@@ -377,52 +400,53 @@ __global__ void __launch_bounds__(NT, 1) block_norm_kernel(const NormArgs a) {
   const F2 skip = pair(a.skip, a.skip);
   uint8_t* from = g.mine;
   int stage = 0, turn = 0;
+  const int own = a.group > 32 ? g.id : 0;  // smaller groups use no scratch
 #pragma unroll 1
-  for (; row < a.n_rows; row += step, turn ^= 1) {
+  for (; g.first_row(row) < a.n_rows; row += step, turn ^= 1) {
+    const bool live = !SUB || row < a.n_rows;
     float scale = gate;
     if (Y && a.row_gate && row + step < a.n_rows) gate = a.branch * a.row_gate[row + step];
     copies_wait(a.stages);
-    Oct x[V], z[V];
     F2 sum = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      x[i] = at.read(from + i * kPieces * pitch, pitch);
-      if (!Y) continue;
-      z[i] = at.read_bf16(from + (i * kPieces + kX) * pitch);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) sum = fma2(z[i].v[k], z[i].v[k], sum);
-    }
-    copy(from);  // into what has just been read
-    from += V * kPieces * pitch;
-    if (++stage == a.stages) stage = 0, from = g.mine;
     if (Y && a.w_post) {
-      const float s = group_sum(both(sum), a.group, g.id, g.thread, scratch[g.id][0][turn]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const Oct y = at.read_bf16(from + (i * kPieces + kX) * pitch);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum = fma2(y.v[k], y.v[k], sum);
+      }
+      const float s = group_sum<SUB>(both(sum), a.group, g.id, g.thread, scratch[own][0][turn]);
       const float r1 = rsqrtf(fmaf(s, inv_dim, a.eps));
-      if (g.thread == 0 && a.rstd_post) a.rstd_post[row] = r1;
+      if (live && g.thread == 0 && a.rstd_post) a.rstd_post[row] = r1;
       scale *= r1;
     }
+    Oct z[V];
     const F2 scale2 = pair(scale, scale);
     sum = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      Oct w;
-      if (Y) w = g.weights.get(true, i);
+      const Oct x = at.read(from + i * kPieces * pitch, pitch);
+      Oct y, w;
+      if (Y) y = at.read_bf16(from + (i * kPieces + kX) * pitch), w = g.weights.get(true, i);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const F2 xs = mul2(x[i].v[k], skip);
-        z[i].v[k] = Y ? fma2(mul2(z[i].v[k], w.v[k]), scale2, xs) : xs;
+        const F2 xs = mul2(x.v[k], skip);
+        z[i].v[k] = Y ? fma2(mul2(y.v[k], w.v[k]), scale2, xs) : xs;
         sum = fma2(z[i].v[k], z[i].v[k], sum);
       }
     }
-    if (a.x_out) {
+    copy(from);  // into what has just been read
+    from += V * kPieces * pitch;
+    if (++stage == a.stages) stage = 0, from = g.mine;
+    if (a.x_out && live) {
       T* const to = static_cast<T*>(a.x_out) + row * a.ldo;
 #pragma unroll
       for (int i = 0; i < V; ++i) at.write(to, i, z[i]);
     }
     if (!a.h) continue;
-    const float s = group_sum(both(sum), a.group, g.id, g.thread, scratch[g.id][1][turn]);
+    const float s = group_sum<SUB>(both(sum), a.group, g.id, g.thread, scratch[own][1][turn]);
     const float r2 = rsqrtf(fmaf(s, inv_dim, a.eps));
-    if (g.thread == 0 && a.rstd_pre) a.rstd_pre[row] = r2;
+    if (live && g.thread == 0 && a.rstd_pre) a.rstd_pre[row] = r2;
     const F2 r22 = pair(r2, r2);
     uint16_t* const to = a.h + row * a.ldh;
 #pragma unroll
@@ -430,23 +454,24 @@ __global__ void __launch_bounds__(NT, 1) block_norm_kernel(const NormArgs a) {
       const Oct w = g.weights.get(false, i);
 #pragma unroll
       for (int k = 0; k < 4; ++k) z[i].v[k] = mul2(mul2(z[i].v[k], w.v[k]), r22);
-      at.write_bf16(to, i, z[i]);
+      if (live) at.write_bf16(to, i, z[i]);
     }
   }
   copies_wait(1);
 }
 
 // Its gradient, dealt the same.  NORM: there is a norm behind (dh); Y: there is a block's output.
-template <typename T, int NT, bool NORM, bool Y>
+template <typename T, int NT, bool SHARED, bool SUB, bool NORM, bool Y>
 __global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ __align__(16) float scratch[kMaxGroups][2][3][32];  // three sums of a row, rows in turn
-  for (int i = threadIdx.x; i < kMaxGroups * 192; i += blockDim.x) (&scratch[0][0][0][0])[i] = 0.0f;
+  __shared__ __align__(16) float scratch[kMaxBarriers][2][3][32];  // three sums of a row, rows in turn
+  for (int i = threadIdx.x; i < kMaxBarriers * 192; i += blockDim.x) (&scratch[0][0][0][0])[i] = 0.0f;
   grid_dependency_wait();
-  const Setup<T, NT> g(smem, a.group, a.dim, a.w_post, a.gate, a.w_pre, a.w_f32);
+  constexpr int V = kV;
+  const Setup<T, SHARED, SUB> g(smem, a.group, a.dim, a.w_post, a.gate, a.w_pre, a.w_f32);
   const Layout<T>& at = g.at;
   // of x_out, dh, y, d_out
-  constexpr int V = kV, kP = Layout<T>::kPieces, kDh = NORM ? kP : 0, kY = kDh + (NORM ? 1 : 0);
+  constexpr int kP = Layout<T>::kPieces, kDh = NORM ? kP : 0, kY = kDh + (NORM ? 1 : 0);
   constexpr int kUp = kY + (Y ? 1 : 0), kPieces = kUp + kP;
   const int pitch = g.pitch, step = gridDim.x * g.groups;
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
@@ -485,11 +510,16 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs
   const F2 skip = pair(a.skip, a.skip);
   uint8_t* slot = g.mine;
   int stage = 0, turn = 0;
+  const int own = a.group > 32 ? g.id : 0;  // smaller groups use no scratch
 #pragma unroll 1
-  for (; row < a.n_rows; row += step, turn ^= 1) {
+  for (; g.first_row(row) < a.n_rows; row += step, turn ^= 1) {
+    const bool live = !SUB || row < a.n_rows;
     const float now_r1 = r1, now_r2 = r2, now_scale = scale;
     factors(row + step);
     copies_wait(a.stages);
+    if (SUB && !live) {  // past the last row: zeros, which add nothing to the sums over the rows
+      for (int p = 0; p < V * kPieces; ++p) *reinterpret_cast<uint4*>(slot + p * pitch) = make_uint4(0, 0, 0, 0);
+    }
     // e = d_out + r2 a, so that dz = e - r2 c2 v; the three sums of the row
     Oct e[V], v[V];
     F2 sum_av = 0, sum_es = 0, sum_vs = 0;
@@ -528,10 +558,10 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs
     float c2 = 0.0f, c1 = 0.0f;
     if (NORM || (Y && (a.w_post || a.drow_gate))) {
       float sums[3] = {both(sum_av), both(sum_es), both(sum_vs)};
-      group_sum3(sums, a.group, g.id, g.thread, scratch[g.id][turn][0]);
+      group_sum3<SUB>(sums, a.group, g.id, g.thread, scratch[own][turn][0]);
       c2 = now_r2 * (inv_dim * sums[0]);
       c1 = fmaf(-c2, sums[2], sums[1]);  // sum of gate w_post dz s
-      if (Y && g.thread == 0 && a.drow_gate) a.drow_gate[row] = a.branch * c1;
+      if (Y && live && g.thread == 0 && a.drow_gate) a.drow_gate[row] = a.branch * c1;
       c1 = Y && a.w_post ? inv_dim * c1 : 0.0f;
     }
     const F2 minus_c2 = pair(-c2, -c2), minus_c1 = pair(-c1, -c1), scale2 = pair(now_scale, now_scale);
@@ -548,7 +578,7 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs
         Oct dx;
 #pragma unroll
         for (int k = 0; k < 4; ++k) dx.v[k] = mul2(e[i].v[k], skip);
-        at.write(to_x, i, dx);
+        if (live) at.write(to_x, i, dx);
       }
       if (!Y) continue;
       const Oct y = at.read_bf16(slot + (i * kPieces + kY) * pitch), w = g.weights.get(true, i);
@@ -559,7 +589,7 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs
         sum_branch[i].v[k] = fma2(mul2(e[i].v[k], scale2), s, sum_branch[i].v[k]);
         dy.v[k] = mul2(fma2(s, minus_c1, mul2(e[i].v[k], w.v[k])), factor);
       }
-      if (a.dy) at.write_bf16(to_y, i, dy);
+      if (a.dy && live) at.write_bf16(to_y, i, dy);
     }
     copy(slot);  // into what has just been read
     slot += V * kPieces * pitch;
@@ -567,12 +597,23 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs
   }
   copies_wait(1);
   if (!a.want_pre && !a.want_branch) return;
-  // the groups' sums in order through shared memory, then the CTA's to the workspace
+  // the groups of a warp, then the groups (or warps) in order through shared memory, then the CTA's to the workspace
+  for (int o = a.group; SUB && o < 32; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        sum_pre[i].v[m] = add2(sum_pre[i].v[m], __shfl_xor_sync(0xffffffffu, sum_pre[i].v[m], o));
+        sum_branch[i].v[m] = add2(sum_branch[i].v[m], __shfl_xor_sync(0xffffffffu, sum_branch[i].v[m], o));
+      }
+  }
+  const int parts = g.groups / g.rows, part_id = g.id / g.rows;
+  const bool writes = g.id % g.rows == 0;
   float* const sums = reinterpret_cast<float*>(g.ring);
   float* const part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.dim;
-  for (int k = 0; k < g.groups; ++k) {
+  for (int k = 0; k < parts; ++k) {
     __syncthreads();  // also: every thread is through with the ring
-    if (g.id != k) continue;
+    if (part_id != k || !writes) continue;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (k > 0) {
@@ -583,7 +624,7 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs
           sum_branch[i].v[m] = add2(sum_branch[i].v[m], q.v[m]);
         }
       }
-      float* const to = k + 1 < g.groups ? sums : part;
+      float* const to = k + 1 < parts ? sums : part;
       if (NORM) at.write_f32(to, i, sum_pre[i]);
       if (Y) at.write_f32(to + a.dim, i, sum_branch[i]);
     }
@@ -632,13 +673,15 @@ struct Deal {
 };
 Deal deal(int n_rows, int dim, int threads, int pieces, int least_ring) {
   Deal d;
-  const bool wide = dim > kWideDim;
-  d.group = ((dim + 8 * kV - 1) / (8 * kV) + 31) / 32 * 32;
-  d.groups = std::max(1, std::min(kMaxGroups, (wide ? 1024 : threads) / d.group));
-  // few rows are spread over the SMs, one to a CTA
-  d.groups = std::min(d.groups, std::max(1, (n_rows + sm_count() - 1) / sm_count()));
+  const int need = (dim + 8 * kV - 1) / (8 * kV);
+  d.group = need > 32 ? (need + 31) / 32 * 32 : 1;
+  while (d.group < need) d.group *= 2;  // within a warp: a power of two
+  // few rows are spread over the SMs, one to a CTA (or a warp's)
+  d.groups = std::max(1, std::min(threads / d.group, (n_rows + sm_count() - 1) / sm_count()));
+  if (d.group < 32) d.groups = (d.groups + 32 / d.group - 1) / (32 / d.group) * (32 / d.group);
+  if (d.group > 32) d.groups = std::min(d.groups, kMaxBarriers);
   d.grid = std::max(1, std::min({(n_rows + d.groups - 1) / d.groups, sm_count(), kMaxParts}));
-  const int row = d.groups * d.group * kV * pieces * 16, weights = wide ? 0 : 2 * kV * 2 * 16 * d.group;
+  const int row = d.groups * d.group * kV * pieces * 16, weights = dim > kWide ? 0 : 2 * kV * 2 * 16 * d.group;
   d.stages = std::max(1, std::min(kMaxStages, (kSharedBytes - weights) / row));
   d.smem = weights + std::max(d.stages * row, least_ring);
   return d;
@@ -652,27 +695,34 @@ int launch(void (*kernel)(Args), const Deal& d, const Args& a, int id, cudaStrea
                                                                                                 : TWELL_ERR_CUDA;
 }
 
-template <typename T>
-int launch_norm(NormArgs a, cudaStream_t s) {
-  const Deal d = deal(a.n_rows, a.dim, kThreads, Layout<T>::kPieces + (a.y ? 1 : 0), 0);
-  a.group = d.group, a.stages = d.stages;
-  const auto kernel = a.dim > kWideDim ? (a.y ? block_norm_kernel<T, 1024, true> : block_norm_kernel<T, 1024, false>)
-                                       : (a.y ? block_norm_kernel<T, kThreads, true> : block_norm_kernel<T, kThreads, false>);
-  return launch(kernel, d, a, TWELL_KERNEL_BLOCK_NORM, s);
+template <typename T, int NT, bool SHARED, bool SUB>
+auto fwd_kernel(const NormArgs& a) {
+  return a.y ? block_norm_kernel<T, NT, SHARED, SUB, true> : block_norm_kernel<T, NT, SHARED, SUB, false>;
 }
 
-template <typename T, int NT>
+template <typename T>
+int launch_norm(NormArgs a, cudaStream_t s) {
+  const Deal d = deal(a.n_rows, a.dim, a.dim > kWide ? 1024 : kThreads, Layout<T>::kPieces + (a.y ? 1 : 0), 0);
+  a.group = d.group, a.stages = d.stages;
+  return launch(d.group < 32 ? fwd_kernel<T, kThreads, true, true>(a)
+                : a.dim > kWide ? fwd_kernel<T, 1024, false, false>(a) : fwd_kernel<T, kThreads, true, false>(a),
+                d, a, TWELL_KERNEL_BLOCK_NORM, s);
+}
+
+template <typename T, int NT, bool SHARED, bool SUB>
 auto bwd_kernel(const NormBwdArgs& a) {
-  if (a.dh) return a.y ? block_norm_bwd_kernel<T, NT, true, true> : block_norm_bwd_kernel<T, NT, true, false>;
-  return a.y ? block_norm_bwd_kernel<T, NT, false, true> : block_norm_bwd_kernel<T, NT, false, false>;
+  if (a.dh) return a.y ? block_norm_bwd_kernel<T, NT, SHARED, SUB, true, true> : block_norm_bwd_kernel<T, NT, SHARED, SUB, true, false>;
+  return a.y ? block_norm_bwd_kernel<T, NT, SHARED, SUB, false, true> : block_norm_bwd_kernel<T, NT, SHARED, SUB, false, false>;
 }
 
 template <typename T>
 int launch_norm_bwd(NormBwdArgs a, int* parts, cudaStream_t s) {
-  const Deal d = deal(a.n_rows, a.dim, kBwdThreads, Layout<T>::kPieces * (a.dh ? 2 : 1) + (a.dh ? 1 : 0) + (a.y ? 1 : 0),
-                      2 * a.dim * 4);
+  const Deal d = deal(a.n_rows, a.dim, a.dim > kWide ? 1024 : kBwdThreads,
+                      Layout<T>::kPieces * (a.dh ? 2 : 1) + (a.dh ? 1 : 0) + (a.y ? 1 : 0), 2 * a.dim * 4);
   a.group = d.group, a.stages = d.stages, *parts = d.grid;
-  return launch(a.dim > kWideDim ? bwd_kernel<T, 1024>(a) : bwd_kernel<T, kBwdThreads>(a), d, a, TWELL_KERNEL_BLOCK_NORM_BWD, s);
+  return launch(d.group < 32 ? bwd_kernel<T, kBwdThreads, true, true>(a)
+                : a.dim > kWide ? bwd_kernel<T, 1024, false, false>(a) : bwd_kernel<T, kBwdThreads, true, false>(a),
+                d, a, TWELL_KERNEL_BLOCK_NORM_BWD, s);
 }
 
 bool finite(float x) { return x - x == 0.0f; }

@@ -104,7 +104,8 @@ def test_forward_parts(tw, rows, dim, stream, flags):
 
 
 @pytest.mark.parametrize("rows,dim", [(1, 16384), (2, 16376), (1, 64), (5, 72), (2, 248), (9, 256), (17, 512), (300, 520),
-                                      (1000, 2048), (4097, 64), (64, 8200), (152, 4096), (2431, 1024)])
+                                      (1000, 2048), (4097, 64), (64, 8200), (152, 4096), (2431, 1024), (700, 8), (5001, 24),
+                                      (301, 40), (90, 5008), (33, 8192)])
 def test_forward_sizes(tw, rows, dim):
     i = make(rows, dim, torch.bfloat16, "ypgrn", 2)
     check_forward(i, run(tw, i, 1.0, 1.0), 1.0, 1.0)
@@ -202,7 +203,8 @@ def test_backward_parts(tw, rows, dim, stream, flags):
 
 
 @pytest.mark.parametrize("rows,dim", [(1, 16384), (2, 16376), (1, 64), (5, 72), (2, 248), (300, 520), (1000, 2048),
-                                      (4097, 64), (400, 8200), (2431, 1024), (20000, 128)])
+                                      (4097, 64), (400, 8200), (2431, 1024), (20000, 128), (700, 8),
+                                      (5001, 24), (301, 40), (200, 5008), (155, 8192)])
 def test_backward_sizes(tw, rows, dim):
     i = make(rows, dim, torch.bfloat16, "ypgrn", 13)
     check_backward(*backward(tw, i, 1.0, 1.0, 14)[:3], rows)
