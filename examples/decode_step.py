@@ -5,8 +5,10 @@ by one, then the gradient of their log probabilities.
 Every step runs, on the current stream and without a synchronisation,
 
     twell_kv_plan       which cache pages the step's tokens go to
+    twell_block_norm    the first norm
     per layer:  projections (torch), twell_kv_append, twell_kv_attention,
-                output projection (torch), twell_ffn_fwd (the sparse layer)
+                output projection (torch), twell_block_norm (residual sum and next norm),
+                twell_ffn_fwd (the sparse layer), twell_block_norm
     twell_logprobs      log probability, entropy and best alternatives of the answer
 
 for requests of different lengths in one batch: their prompts in the first step,
@@ -49,6 +51,7 @@ class Decoder:
         self.ring, self.pool = tw.alloc_page_ring(n_pages)
         self.table = torch.zeros((max_requests, blocks), dtype=torch.int32, device="cuda")
         self.lens = torch.zeros((max_requests,), dtype=torch.int32, device="cuda")
+        self.norm = torch.ones(D_MODEL, device="cuda").bfloat16()
         self.max_len = max_len
 
     def ffn(self, x, layer):
@@ -65,21 +68,21 @@ class Decoder:
         n, requests = tokens.numel(), self.lens.numel()
         plan = tw.alloc_kv_plan(requests, n)
         tw.twell_kv_plan(self.lens, new, self.table, self.ring, self.pool, PAGE, plan)
-        norm = lambda t: torch.nn.functional.rms_norm(t.float(), (D_MODEL,)).bfloat16()  # noqa: E731
         x = self.embed[tokens]
+        hidden = torch.empty_like(x)
+        tw.twell_block_norm(x, None, None, hidden, w_pre=self.norm)
         o = torch.empty((n, Q_HEADS, HEAD_DIM), dtype=torch.bfloat16, device="cuda")
         ws = torch.empty(tw.kv_attention_workspace_bytes(n, requests, Q_HEADS, KV_HEADS, HEAD_DIM), dtype=torch.uint8,
                          device="cuda")
         for layer, cache in zip(self.layers, self.caches):
-            qkv = (norm(x) @ layer["qkv"].T).view(n, Q_HEADS + 2 * KV_HEADS, HEAD_DIM)
+            qkv = (hidden @ layer["qkv"].T).view(n, Q_HEADS + 2 * KV_HEADS, HEAD_DIM)
             q, k, v = qkv.split((Q_HEADS, KV_HEADS, KV_HEADS), 1)
             tw.twell_kv_append(k, v, plan.cu_q, plan.slots, cache)
             tw.twell_kv_attention(q, cache, self.table, plan.cu_q, plan.positions, plan.kv_lens, self.max_len,
                                   max_new, HEAD_DIM ** -0.5, o, ws)
-            x = x + o.view(n, -1) @ layer["out"].T
-            x = x + self.ffn(norm(x), layer)
+            tw.twell_block_norm(x, o.view(n, -1) @ layer["out"].T, x, hidden, w_pre=self.norm)
+            tw.twell_block_norm(x, self.ffn(hidden, layer), x, hidden, w_pre=self.norm)
         self.lens, self.pool = plan.kv_lens, plan.pool
-        hidden = norm(x)
         return hidden @ self.unembed.T, hidden, plan
 
     def status(self) -> list:
