@@ -66,7 +66,7 @@ EXPORTED = [
     "twell_kv_read_status", "twell_logprobs", "twell_logprobs_bwd", "twell_selftest_kv_attention_stall",
     "twell_block_norm", "twell_block_norm_bwd", "twell_block_norm_bwd_workspace_bytes",
     "twell_linear_logprobs", "twell_linear_logprobs_workspace_bytes", "twell_linear_logprobs_bwd",
-    "twell_linear_logprobs_bwd_workspace_bytes",
+    "twell_linear_logprobs_bwd_workspace_bytes", "twell_selftest_linear_stall",
 ]
 
 
@@ -161,6 +161,7 @@ def load_library() -> ctypes.CDLL:
         "twell_linear_logprobs_bwd": (ctypes.c_int, [P, I64, P, I64, I32, I32, I32, P, ctypes.c_float, P, P, P, P, P,
                                                      I64, P, I64, P, SZ, P, P]),
         "twell_linear_logprobs_bwd_workspace_bytes": (SZ, [I32, I32, I32]),
+        "twell_selftest_linear_stall": (ctypes.c_int, [P, I64, P, I64, I32, I32, I32, P, SZ, P, ctypes.c_uint64, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

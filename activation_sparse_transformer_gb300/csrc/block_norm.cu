@@ -734,6 +734,17 @@ int check_matrix(const void* p, int64_t ld, int dim, bool needed) {
   return ld >= dim && ld % 8 == 0 ? TWELL_OK : TWELL_ERR_INVALID_ARG;
 }
 
+// No output lies where an input or another output does (null: none).
+bool apart(std::initializer_list<const void*> outputs, std::initializer_list<const void*> inputs) {
+  for (const void* const* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const void* const* p = outputs.begin(); p != o; ++p)
+      if (*o && *o == *p) return false;
+    for (const void* p : inputs)
+      if (*o && *o == p) return false;
+  }
+  return true;
+}
+
 int check_sizes(int n_rows, int dim, int dtype, int w_dtype) {
   if (n_rows < 0 || dim < 1) return TWELL_ERR_INVALID_ARG;
   if (dtype != TWELL_BF16 && dtype != TWELL_F32) return TWELL_ERR_INVALID_ARG;
@@ -762,6 +773,7 @@ extern "C" TWELL_API int twell_block_norm(const void* x, int32_t dtype, int64_t 
     KV_TRY(check_matrix(x_out, ldo, d_model, false));
     KV_TRY(check_matrix(h, ldh, d_model, false));
     if (x_out == x && ldo != ldx) return TWELL_ERR_INVALID_ARG;
+    if (!apart({x_out, h}, {y}) || h == x) return TWELL_ERR_INVALID_ARG;
     for (const void* p : {w_post, gate, w_pre})
       if (!aligned_to(p, 16)) return TWELL_ERR_MISALIGNED;
     for (const float* p : {row_gate, static_cast<const float*>(rstd_post), static_cast<const float*>(rstd_pre)})
@@ -810,6 +822,7 @@ extern "C" TWELL_API int twell_block_norm_bwd(const uint16_t* dh, int64_t lddh, 
     KV_TRY(check_matrix(dx, lddx, d_model, false));
     KV_TRY(check_matrix(dy, lddy, d_model, false));
     if (dx && dx == d_out && lddx != lddo) return TWELL_ERR_INVALID_ARG;
+    if (!apart({dx, dy}, {dh, x_out, y}) || (dy && dy == d_out)) return TWELL_ERR_INVALID_ARG;
   }
   const bool sums = dw_post || dgate || dw_pre;
   if (sums) {

@@ -14,8 +14,8 @@
 // of one piece together with G of the next one, which needs a buffer of its own.
 //
 // All products are tiles of one persistent kernel on the 5th-generation tensor cores:
-// operands by TMA into 128-byte swizzled stages, accumulators twice in TMEM, one
-// warp for the copies, one for the MMAs, eight for the epilogue.  The two gradient products read
+// operands by TMA into 128-byte swizzled stages, accumulators twice in TMEM, a
+// warp for each operand's copies, one for the MMAs, eight for the epilogue.  The two gradient products read
 // G and H or W along their rows, so those operands go in M- or N-major.
 // A pair of CTAs shares a tile of 256 x 256 (each keeps half of either operand and half of the
 // rows' sums), which halves what shared memory feeds to the tensor cores; up to 128 rows there is
@@ -23,7 +23,7 @@
 //
 // The tensor cores cut off what does not fit when they add, one step in 16 products, so a
 // logit of d = 4096 would come out 4e-6 too near to zero.  The forward pass, whose results are
-// fp32, adds up runs of 256 products in registers instead, rounding to nearest, while the next run is multiplied.
+// fp32, adds up runs of 512 products in registers instead (all at once: off by four times as much, 2 % faster), rounding to nearest, while the next run is multiplied.
 #include <algorithm>
 
 #include "kv_internal.h"
@@ -35,13 +35,11 @@ namespace {
 // where they leave fewer CTAs idle in the last round (413 x 1032 x 50001: 192 columns 54 us, 128 73, 256 52).
 constexpr int kBM = 128, kBN = 256, kBK = 64, kUmmaK = 16;
 constexpr int kThreads = 384, kEpiWarps = 8;
-// Registers of the forward pass, whose epilogue holds 128 sums a thread.
-constexpr int kRegs = 168, kRegsRest = 56, kRegsEpilogue = 224;
-static_assert(128 * kRegsRest + 256 * kRegsEpilogue <= kThreads * kRegs, "register split");
 constexpr int kRun = 8;  // steps of K that the forward pass adds up in tensor memory
 constexpr uint32_t kABytes = kBM * kBK * 2;
 constexpr uint32_t kBarBytes = 256;
-constexpr uint32_t kSumBytes = 2 * 128 * 3 * sizeof(float);  // forward: one half's sums, for the other half
+constexpr int kSlots = 4;                                    // forward: one half's sums, for the other half
+constexpr uint32_t kSumBytes = kSlots * 128 * sizeof(float4);
 constexpr uint32_t kBoxBytes = 32 * 128;                     // backward: a box of 32 rows on its way out,
 constexpr uint32_t kOutBytes = kEpiWarps * 2 * kBoxBytes;    // two a warp
 constexpr uint32_t kMaxShared = 232448;
@@ -55,6 +53,7 @@ struct Cfg {
 };
 constexpr int kBandWide = 64, kBandGradients = 8;
 constexpr int kMaxJobs = 3;
+constexpr int kMaxSize = 1 << 30;        // rows, columns: indexes of whole tiles fit in 32 bits
 constexpr int kPlanSms = 152;            // plans do not depend on the device, workspaces neither
 constexpr int64_t kPieceBytes = 1 << 27; // of G: what the L2 cache can hold
 constexpr int kMinPiece = 4096;          // columns; dH's sums are read and written once a piece
@@ -96,6 +95,7 @@ struct Args {
   int sum_rows;         // n_rows, up to whole tiles
   int32_t* status;
   uint64_t wait_limit_ns;
+  int stall;  // arrivals that every stage waits for in vain (the self-test)
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -278,9 +278,12 @@ __device__ __forceinline__ void add_run(Half& x, uint32_t taddr) {
   }
 }
 
-// Sums of the tile's columns; both halves of a row are joined through shared memory.
-__device__ __forceinline__ void epilogue_sums(const Args& a, const Job& j, const Tile& t, int n_blk, Half& x,
-                                              float* shared, int turn) {
+// Sums of the tile's columns.  A row's right half hands its sums to the left one through shared memory, with the
+// number of the tile (turn, from 1 on) as word that they are there: a wait that can expire, as a barrier of both
+// could not.  The right half is at most two tiles ahead (it cannot get an accumulator that the left one has not read), so
+// four places in turn are enough.
+__device__ __forceinline__ bool epilogue_sums(const Args& a, const Job& j, const Tile& t, int n_blk, Half& x,
+                                              float4* shared, int turn, volatile int* abort) {
   const float c = a.inv_t * kLog2e;
   const int target = t.valid && a.targets ? a.targets[t.row] : -1;
   const int col = t.col0 + t.half * (kBN / 2), left = min(j.n - col, kBN / 2);
@@ -317,12 +320,27 @@ __device__ __forceinline__ void epilogue_sums(const Args& a, const Job& j, const
   }
   const float2 sums = lanes(add2(s[0], s[1])), shifted = lanes(add2(u[0], u[1]));
   all.s = sums.x + sums.y, all.u = shifted.x + shifted.y;
-  float* const at = shared + turn * 128 * 3 + (t.lg * 32 + (threadIdx.x & 31)) * 3;
-  if (t.half == 1) at[0] = all.m, at[1] = all.s, at[2] = all.u;
-  asm volatile("bar.sync %0, 64;" ::"r"(t.lg + 1) : "memory");
-  if (t.half == 1 || !t.valid) return;
+  volatile float* const at =
+      reinterpret_cast<volatile float*>(shared + (turn % kSlots) * 128 + t.lg * 32 + (threadIdx.x & 31));
+  if (t.half == 1) {
+    at[0] = all.m, at[1] = all.s, at[2] = all.u;
+    __threadfence_block();
+    at[3] = __int_as_float(turn);
+    return true;
+  }
+  const uint64_t t0 = global_timer_ns();
+  while (__float_as_int(at[3]) != turn) {
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > a.wait_limit_ns) {
+      *abort = 1;
+      return false;
+    }
+  }
+  __threadfence_block();
+  if (!t.valid) return true;
   all.join(at[0], at[1], at[2]);
   a.part[static_cast<int64_t>(t.row) * j.num_n + n_blk] = make_float4(all.m, all.s, all.u, 0.0f);
+  return true;
 }
 
 // Results leave through shared memory by TMA, a box of 32 rows of 128 bytes a time, so that memory gets whole
@@ -536,7 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Unit x;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], rank == 0 ? R + 1 : 2);  // A, B; of the first CTA also word of the second one's
+      // A, B; of the first CTA also word of the second one's
+      mbar_init(&full[s], (rank == 0 ? R + 1 : 2) + a.stall);
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -547,6 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort = 0;
     mbar_fence_init();
   }
+  if (SUMS)  // no tile has been there yet
+    for (int i = threadIdx.x; i < kSlots * 128; i += kThreads) reinterpret_cast<float4*>(extra)[i].w = __int_as_float(0);
   if (warp == 0 && lane < 2 * a.num_jobs) tma_prefetch_desc(lane & 1 ? &maps.b[lane >> 1] : &maps.a[lane >> 1]);
   __syncwarp();
   if (warp == 2) Tc<R>::alloc(tmem_holder);
@@ -557,7 +578,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint64_t limit = a.wait_limit_ns;
 
   if (warp < 4) {
-    if (SUMS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == 0 || warp == 2) {
       // ---------------- copies: one warp brings A, the other B (one for both takes longer to issue them than they
       // are multiplied)
@@ -666,7 +686,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ---------------- epilogue: thread = row of the tile (a TMEM lane), two warps share a row's columns
-    if (SUMS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpilogue));
     Tile t;
     t.lg = warp & 3;
     t.half = (warp - 4) >> 2;
@@ -703,14 +722,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (SUMS) {
         Half sums = {};
 #pragma unroll 1
-        for (int k0 = x.kb0; k0 < x.kb1; k0 += kRun) {
+        for (int k = 0; k < j.num_k; k += kRun) {
           if (!wait_full()) break;
           add_run(sums, t.taddr + t.half * (kBN / 2));
           release();
         }
         if (!ok) break;
-        epilogue_sums(a, j, t, x.n_blk, sums, reinterpret_cast<float*>(extra), turn);
-        turn ^= 1;
+        ok = __all_sync(0xffffffffu, epilogue_sums(a, j, t, x.n_blk, sums, reinterpret_cast<float4*>(extra), ++turn, abort));
+        if (!ok) report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
       } else {
         if (!wait_full()) break;
         if (t.row - lane < j.m) {  // else the warp's rows are all past the end
@@ -830,7 +849,7 @@ Plan plan_bwd(int64_t n_rows, int64_t d, int64_t vocab) {
   const int64_t tiles = ceil_div(n_rows, kBM * ctas) * static_cast<int64_t>(ceil_div(d, kBN));
   const int64_t num_k = ceil_div(std::min<int64_t>(p.piece, vocab), kBK);
   p.ksplit = static_cast<int>(
-      std::max<int64_t>(1, std::min<int64_t>({kMaxKSplit, num_k / 8, kPlanSms / ctas / tiles})));
+      std::max<int64_t>(1, std::min<int64_t>({kMaxKSplit, num_k / 8, kPlanSms / ctas / std::max<int64_t>(1, tiles)})));
   p.grad_bytes = round_up(static_cast<size_t>(n_rows) * p.piece * 2, 256);
   p.sum_bytes = p.pieces > 1 || p.ksplit > 1 ? round_up(static_cast<size_t>(p.ksplit) * sum_rows(n_rows) * d * 4, 256) : 0;
   p.bytes = p.grad_bytes * (p.pieces > 1 ? 2 : 1) + p.sum_bytes + 256;
@@ -885,13 +904,6 @@ template <int R, bool SUMS>
 int launch_jobs(const Maps& maps, Args args, cudaStream_t s) {
   const auto kernel = linear_kernel<R, SUMS>;
   KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(Cfg<R, SUMS>::kShared)));
-  if (SUMS) {  // the split of the registers waits for as many as only a launch with kRegs a thread has
-    static const int regs = [&] {
-      cudaFuncAttributes f;
-      return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
-    }();
-    if (regs < kRegs) return TWELL_ERR_CUDA;
-  }
   const int all = deal(&args, slots_of(R));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(all) * R);
@@ -913,8 +925,8 @@ int launch_jobs(const Maps& maps, Args args, cudaStream_t s) {
 int check_linear(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw, int n_rows, int d, int vocab,
                  float inv_t) {
   if (n_rows < 0 || d < 1 || vocab < 1) return TWELL_ERR_INVALID_ARG;
-  if (!(inv_t > 0.0f) || inv_t > 3.0e38f) return TWELL_ERR_INVALID_ARG;
-  if (d % 8 != 0) return TWELL_ERR_UNSUPPORTED;
+  if (!(inv_t > 0.0f) || inv_t > 2.0e38f) return TWELL_ERR_INVALID_ARG;  // times log2(e) it is finite
+  if (d % 8 != 0 || std::max({n_rows, d, vocab}) > kMaxSize) return TWELL_ERR_UNSUPPORTED;
   if (ldw < d || ldw % 8 != 0) return TWELL_ERR_INVALID_ARG;
   KV_TRY(check_array(W, 16));
   if (n_rows == 0) return TWELL_OK;
@@ -934,15 +946,16 @@ int check_vectors(std::initializer_list<const void*> ps) {
 using namespace twell;
 
 extern "C" TWELL_API size_t twell_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t d_model, int32_t vocab) {
-  if (n_rows < 0 || d_model < 8 || d_model % 8 != 0 || vocab < 1) return 0;
+  if (n_rows < 0 || d_model < 8 || d_model % 8 != 0 || vocab < 1 || std::max({n_rows, d_model, vocab}) > kMaxSize) return 0;
   return fwd_bytes(n_rows, vocab);
 }
 
-extern "C" TWELL_API int twell_linear_logprobs(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw,
-                                               int32_t n_rows, int32_t d_model, int32_t vocab, const int32_t* targets,
-                                               float inv_temperature, float* logprob, float* entropy, float* lse,
-                                               void* workspace, size_t workspace_bytes, int32_t* status,
-                                               twell_stream_t stream) {
+namespace {
+
+int linear_logprobs(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw, int n_rows, int d_model, int vocab,
+                    const int32_t* targets, float inv_temperature, float* logprob, float* entropy, float* lse,
+                    void* workspace, size_t workspace_bytes, int32_t* status, uint64_t limit_ns, int stall,
+                    cudaStream_t s) {
   KV_TRY(check_linear(H, ldh, W, ldw, n_rows, d_model, vocab, inv_temperature));
   KV_TRY(check_array(status, 4));
   if (n_rows > 0) {
@@ -953,11 +966,10 @@ extern "C" TWELL_API int twell_linear_logprobs(const uint16_t* H, int64_t ldh, c
   }
   if (!device_is_sm103()) return TWELL_ERR_NO_DEVICE;
   if (n_rows == 0) return TWELL_OK;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   Maps maps;
   Args a = {};
   a.n_rows = n_rows, a.d_model = d_model, a.vocab = vocab, a.targets = targets, a.inv_t = inv_temperature;
-  a.status = status, a.wait_limit_ns = kWaitLimitNs;
+  a.status = status, a.wait_limit_ns = limit_ns, a.stall = stall;
   a.of_target = static_cast<float*>(workspace);
   a.part = reinterpret_cast<float4*>(static_cast<uint8_t*>(workspace) + round_up(static_cast<size_t>(n_rows) * 4, 256));
   Job j = {};
@@ -972,9 +984,29 @@ extern "C" TWELL_API int twell_linear_logprobs(const uint16_t* H, int64_t ldh, c
              : TWELL_ERR_CUDA;
 }
 
+}  // namespace
+
+extern "C" TWELL_API int twell_linear_logprobs(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw,
+                                               int32_t n_rows, int32_t d_model, int32_t vocab, const int32_t* targets,
+                                               float inv_temperature, float* logprob, float* entropy, float* lse,
+                                               void* workspace, size_t workspace_bytes, int32_t* status,
+                                               twell_stream_t stream) {
+  return linear_logprobs(H, ldh, W, ldw, n_rows, d_model, vocab, targets, inv_temperature, logprob, entropy, lse,
+                         workspace, workspace_bytes, status, kWaitLimitNs, 0, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" TWELL_API int twell_selftest_linear_stall(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw,
+                                                     int32_t n_rows, int32_t d_model, int32_t vocab, void* workspace,
+                                                     size_t workspace_bytes, int32_t* status, uint64_t limit_ns,
+                                                     twell_stream_t stream) {
+  if (limit_ns < 100000ull || limit_ns > 1000000000ull) return TWELL_ERR_INVALID_ARG;
+  return linear_logprobs(H, ldh, W, ldw, n_rows, d_model, vocab, nullptr, 1.0f, nullptr, nullptr, nullptr, workspace,
+                         workspace_bytes, status, limit_ns, 1, reinterpret_cast<cudaStream_t>(stream));
+}
+
 extern "C" TWELL_API size_t twell_linear_logprobs_bwd_workspace_bytes(int32_t n_rows, int32_t d_model,
                                                                       int32_t vocab) {
-  if (n_rows < 0 || d_model < 8 || d_model % 8 != 0 || vocab < 1) return 0;
+  if (n_rows < 0 || d_model < 8 || d_model % 8 != 0 || vocab < 1 || std::max({n_rows, d_model, vocab}) > kMaxSize) return 0;
   return plan_bwd(n_rows, d_model, vocab).bytes;
 }
 
@@ -994,6 +1026,7 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
     KV_TRY(check_array(lse, 4));
     if (!targets != !d_logprob || !entropy != !d_entropy) return TWELL_ERR_INVALID_ARG;
     if (!dH && !dW) return TWELL_ERR_INVALID_ARG;
+    if ((dH && dH == H) || (dW && dW == W) || (dH && (dH == W || dH == dW)) || (dW && dW == H)) return TWELL_ERR_INVALID_ARG;
     if (dH && (lddh < d_model || lddh % 8 != 0)) return TWELL_ERR_INVALID_ARG;
     if (!aligned_to(dH, 16)) return TWELL_ERR_MISALIGNED;
     KV_TRY(check_vectors({targets, entropy, d_logprob, d_entropy}));

@@ -581,7 +581,7 @@ TWELL_API size_t twell_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t d
  * 16384 p is off by more than its rounding to bf16.  With n_rows == 0 dW is set to zero.
  * workspace: >= twell_linear_logprobs_bwd_workspace_bytes(...), 256-byte aligned, needs no
  * initialisation: two pieces of G (128 MB each, or 4096 columns where rows are many) and dH in
- * fp32, much less where one piece is enough.  status as above. */
+ * fp32, much less where one piece is enough.  status as above.  Nothing is written over H or W. */
 TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw,
                                         int32_t n_rows, int32_t d_model, int32_t vocab, const int32_t* targets,
                                         float inv_temperature, const float* lse, const float* entropy,
@@ -615,6 +615,14 @@ TWELL_API int twell_selftest_kv_attention_stall(const uint16_t* Q, int64_t ldq, 
                                                 int32_t max_q_len, float softmax_scale, uint16_t* O, int64_t ldo,
                                                 float* lse, void* workspace, size_t workspace_bytes,
                                                 uint64_t limit_ns, twell_stream_t stream);
+
+/* The same for the log probabilities from hidden rows: twell_linear_logprobs without outputs and with
+ * waits of at most limit_ns (0.1 ms to 1 s), in which every stage of the pipeline waits for an arrival that never
+ * comes.  The call ends with TWELL_ERR_WAIT_TIMEOUT in *status. */
+TWELL_API int twell_selftest_linear_stall(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw,
+                                          int32_t n_rows, int32_t d_model, int32_t vocab, void* workspace,
+                                          size_t workspace_bytes, int32_t* status, uint64_t limit_ns,
+                                          twell_stream_t stream);
 
 /* Device check of a packed layout against the format rules at the top of this
  * file: a debugging aid for layouts built outside twell_pack / twell_ffn_fwd

@@ -348,3 +348,18 @@ def test_gradient_against_differences(tw):
         numeric = (ends[0] - ends[1]) / 2e-5
         scale = float((got.double() * way).abs().sum())
         assert abs(float((got.double() * way).sum()) - numeric) <= 2.0 ** -7 * scale + 1e-6 * abs(numeric)
+
+
+@pytest.mark.parametrize("n", [40, 300])  # a CTA to a tile, and a pair
+def test_an_expired_wait_is_reported(tw, n):
+    """Every stage waits for an arrival that never comes: the call ends, says so, and the next one is sound."""
+    h, w, t = make(n, 128, 2000, 23)
+    ws = torch.empty(tw.linear_logprobs_workspace_bytes(n, 128, 2000), dtype=torch.uint8, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lib = tw.load_library()
+    rc = lib.twell_selftest_linear_stall(h.data_ptr(), 128, w.data_ptr(), 128, n, 128, 2000, ws.data_ptr(), ws.numel(),
+                                         st.data_ptr(), 1_000_000, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    torch.cuda.synchronize()
+    assert int(st) == -7
+    check_forward(tw, h, w, t, 1.0)

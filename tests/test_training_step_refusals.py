@@ -33,6 +33,7 @@ NORM = dict(x=A, dtype=0, ldx=256, y=B, ldy=256, n=5, d=256, w_post=A, gate=A, w
     (dict(h=None), -1), (dict(w_pre=None), -1), (dict(w_pre=None, h=None), -1),         # rstd_pre without a norm
     (dict(w_post=None), -1), (dict(x_out=None, h=None, w_pre=None, rstd_pre=None), -1),
     (dict(ldx=248), -1), (dict(ldy=260), -1), (dict(ldo=255), -1), (dict(ldh=0), -1),
+    (dict(h=A), -1), (dict(h=B), -1), (dict(h=C), -1), (dict(x_out=B), -1),             # over what is read, or each other
     (dict(x_out=A, ldo=264), -1),                                                     # in place with another distance
     (dict(d=260, ldx=264, ldy=264, ldo=264, ldh=264), -3),
     (dict(d=16392, ldx=16392, ldy=16392, ldo=16392, ldh=16392), -3),
@@ -54,7 +55,8 @@ BWD = dict(dh=A, lddh=256, d_out=B, dtype=0, lddo=256, x_out=C, ldo=256, y=D, ld
     (dict(w_post=None), -1), (dict(rstd_post=None), -1), (dict(gate=None), -1), (dict(row_gate=None), -1),
     (dict(y=None), -1), (dict(n=-1), -1), (dict(d=0), -1), (dict(dtype=5), -1), (dict(w_dtype=-1), -1),
     (dict(skip=float("inf")), -1), (dict(branch=float("nan")), -1), (dict(lddh=248), -1), (dict(lddx=250), -1),
-    (dict(dx=B, lddx=264), -1), (dict(d=100, lddh=104), -3), (dict(dh=P(0x10008)), -2), (dict(dy=P(0x10008)), -2),
+    (dict(dx=B, lddx=264), -1), (dict(dx=A), -1), (dict(dx=C), -1), (dict(dx=F), -1), (dict(dy=A), -1), (dict(dy=B), -1),
+    (dict(dy=D), -1), (dict(d=100, lddh=104), -3), (dict(dh=P(0x10008)), -2), (dict(dy=P(0x10008)), -2),
     (dict(dw_pre=P(0x10002)), -2), (dict(w_post=P(0x10008)), -2), (dict(ws=None), -5), (dict(ws_bytes=100), -5),
     (dict(ws=P(0x10010)), -2)])
 def test_block_norm_bwd_refuses(lib, over, code):
@@ -108,8 +110,8 @@ LIN = dict(H=A, ldh=256, W=B, ldw=256, n=5, d=256, vocab=1000, targets=C, inv_t=
 @pytest.mark.parametrize("over,code", [
     (dict(H=None), -1), (dict(W=None), -1), (dict(n=-1), -1), (dict(d=0), -1), (dict(vocab=0), -1), (dict(ldh=248), -1),
     (dict(ldw=260), -1), (dict(inv_t=0.0), -1), (dict(inv_t=-1.0), -1), (dict(inv_t=float("nan")), -1),
-    (dict(inv_t=float("inf")), -1), (dict(targets=None), -1), (dict(logprob=None), -1), (dict(status=None), -1),
-    (dict(d=100, ldh=104), -3), (dict(H=P(0x10008)), -2), (dict(W=P(0x10008)), -2), (dict(lse=P(0x10002)), -2),
+    (dict(inv_t=float("inf")), -1), (dict(inv_t=2.5e38), -1), (dict(targets=None), -1), (dict(logprob=None), -1),
+    (dict(status=None), -1), (dict(d=100, ldh=104), -3), (dict(n=(1 << 30) + 1), -3), (dict(vocab=(1 << 30) + 1), -3), (dict(H=P(0x10008)), -2), (dict(W=P(0x10008)), -2), (dict(lse=P(0x10002)), -2),
     (dict(status=P(0x10002)), -2), (dict(ws=None), -5), (dict(ws_bytes=100), -5), (dict(ws=P(0x10010)), -2)])
 def test_linear_logprobs_refuse(lib, over, code):
     assert lib.twell_linear_logprobs(*{**LIN, **over}.values()) == code
@@ -121,7 +123,9 @@ LINB = dict(H=A, ldh=256, W=B, ldw=256, n=5, d=256, vocab=1000, targets=C, inv_t
 
 @pytest.mark.parametrize("over,code", [
     (dict(H=None), -1), (dict(W=None), -1), (dict(lse=None), -1), (dict(targets=None), -1), (dict(g=None), -1),
-    (dict(entropy=None), -1), (dict(ge=None), -1), (dict(dH=None, dW=None), -1), (dict(lddh=248), -1),
+    (dict(entropy=None), -1), (dict(ge=None), -1), (dict(dH=None, dW=None), -1),
+    (dict(dH=A), -1), (dict(dW=B), -1), (dict(dH=B), -1), (dict(dW=A), -1), (dict(dW=C), -1),   # over what is read, or each other
+ (dict(lddh=248), -1),
     (dict(lddw=257), -1), (dict(n=-1), -1), (dict(inv_t=0.0), -1), (dict(status=None), -1), (dict(d=100), -3),
     (dict(dH=P(0x10008)), -2), (dict(dW=P(0x10008)), -2), (dict(g=P(0x10001)), -2), (dict(ws=None), -5),
     (dict(ws_bytes=1000), -5), (dict(ws=P(0x10010)), -2)])
@@ -130,12 +134,13 @@ def test_linear_logprobs_bwd_refuses(lib, over, code):
 
 
 def test_linear_workspaces_are_host_arithmetic(tw):
+    assert tw.linear_logprobs_workspace_bytes(0, 64, 10) > 0 and tw.linear_logprobs_bwd_workspace_bytes(0, 64, 10) > 0
     assert tw.linear_logprobs_workspace_bytes(16, 4096, 131072) >= 16 * 4 * 3
     assert tw.linear_logprobs_bwd_workspace_bytes(16, 4096, 131072) >= 16 * 131072 * 2
     # pieces: far less than the logits
     assert tw.linear_logprobs_bwd_workspace_bytes(65536, 4096, 131072) < 65536 * 131072 * 2 // 4
     for f in (tw.linear_logprobs_workspace_bytes, tw.linear_logprobs_bwd_workspace_bytes):
-        for bad in ((-1, 64, 10), (1, 0, 10), (1, 12, 10), (1, 64, 0)):
+        for bad in ((-1, 64, 10), (1, 0, 10), (1, 12, 10), (1, 64, 0), ((1 << 30) + 1, 64, 10), (1, 64, (1 << 30) + 1)):
             assert f(*bad) == 0
 
 
@@ -160,3 +165,11 @@ def test_binding_of_the_linear_calls_checks(tw):
         tw.twell_linear_logprobs_bwd(h, w, t, 1.0, f, f, f, f, h.float(), w, ws, st)
     with pytest.raises(ValueError, match="CUDA"):
         tw.twell_linear_logprobs_bwd(h, w, t, 1.0, f, f, f, f, h, w, ws, st)
+
+
+@pytest.mark.parametrize("over,code", [(dict(limit=0), -1), (dict(limit=2_000_000_000), -1), (dict(H=None), -1),
+                                       (dict(status=None), -1), (dict(ws=None), -5)])
+def test_linear_selftest_refuses(lib, over, code):
+    a = dict(H=A, ldh=256, W=B, ldw=256, n=5, d=256, vocab=1000, ws=A, ws_bytes=1 << 40, status=A, limit=1_000_000,
+             stream=None)
+    assert lib.twell_selftest_linear_stall(*{**a, **over}.values()) == code
