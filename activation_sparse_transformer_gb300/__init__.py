@@ -34,6 +34,15 @@ runs it whole):
     ...                                                          # the sparse layer, the output projection
     tw.twell_logprobs(logits, targets, 1.0, logprob, entropy, lse, top_logprob, top_index)
     tw.twell_logprobs_bwd(logits, targets, 1.0, lse, entropy, d_logprob, d_entropy, d_logits)
+
+A training step around the layer (examples/training_step.py runs it whole): the norms before and after a
+block with its gate and the residual sum, the log probabilities without logits in memory, and back:
+
+    tw.twell_block_norm(x, y, x_out, h, w_post=w_post, gate=gate, w_pre=w_next, rstd_post=r1, rstd_pre=r2)
+    tw.twell_linear_logprobs(h, W, targets, 1.0, logprob, entropy, lse, workspace, status)
+    tw.twell_linear_logprobs_bwd(h, W, targets, 1.0, lse, entropy, d_logprob, d_entropy, d_h, d_W, workspace, status)
+    tw.twell_block_norm_bwd(d_h, d_out, x_out, y, d_x, d_y, w_post=w_post, gate=gate, w_pre=w_next, rstd_post=r1,
+                            rstd_pre=r2, dw_post=dw_post, dgate=dgate, dw_pre=dw_next, workspace=workspace)
 """
 from __future__ import annotations
 
