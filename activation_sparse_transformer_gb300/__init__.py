@@ -779,16 +779,24 @@ def _matrix(t, dtype, rows, dim, name: str) -> tuple:
     """(address, distance between rows) of a matrix [rows, dim] whose rows are contiguous; (None, 0) of None."""
     if t is None:
         return None, 0
-    shape = t.shape
-    if t.dtype == dtype and shape == (rows, dim):
-        stride = t.stride()
-        if stride[1] == 1 or dim == 1:
+    if t.dtype == dtype and t.shape == (rows, dim):
+        ld, one = t.stride()
+        if one == 1 or dim == 1:
             # a matrix of one row may have any stride
-            return t.data_ptr(), stride[0] if rows > 1 else (dim + 7) // 8 * 8
+            return t.data_ptr(), ld if rows > 1 else (dim + 7) // 8 * 8
         raise ValueError(f"{name}: a tensor whose rows are contiguous")
     if t.dtype != dtype:
         raise ValueError(f"{name}: {t.dtype}, the call takes {dtype}")
-    raise ValueError(f"{name}: shape {tuple(shape)}, the call takes [{rows}, {dim}]")
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, the call takes [{rows}, {dim}]")
+
+
+def _row(t, dtype, n: int, name: str):
+    """_maybe for calls that are as short as what they start: one look at what is as it should be."""
+    if t is None:
+        return None
+    if t.dtype == dtype and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    return _arg(t, dtype, n, name)
 
 
 def _stream_of(t, name: str) -> tuple:
@@ -803,23 +811,26 @@ def _stream_of(t, name: str) -> tuple:
 
 def _weights(dim: int, w_post, gate, w_pre) -> tuple:
     """(type code, address of each) of the norm's weights: all bfloat16 or all float32."""
-    dtype, out = None, []
-    for t, name in ((w_post, "w_post"), (gate, "gate"), (w_pre, "w_pre")):
-        if t is None:
-            out.append(None)
-            continue
-        if dtype is None:
-            dtype = t.dtype
-            if dtype != _torch.bfloat16 and dtype != _torch.float32:
-                raise ValueError(f"{name}: {dtype}, the call takes bfloat16 or float32")
-        elif t.dtype != dtype:
-            raise ValueError(f"{name}: {t.dtype}, the other weights are {dtype}")
-        if t.numel() != dim:
-            raise ValueError(f"{name}: {t.numel()} elements, the rows have {dim}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: a contiguous tensor")
-        out.append(t.data_ptr())
-    return 1 if dtype is not None and dtype != _torch.bfloat16 else 0, out
+    first = w_post if w_post is not None else gate if gate is not None else w_pre
+    if first is None:
+        return 0, None, None, None
+    dtype = first.dtype
+    if dtype != _torch.bfloat16 and dtype != _torch.float32:
+        raise ValueError(f"w_post, gate, w_pre: {dtype}, the call takes bfloat16 or float32")
+    return (0 if dtype == _torch.bfloat16 else 1, _weight(w_post, dtype, dim, "w_post"), _weight(gate, dtype, dim, "gate"),
+            _weight(w_pre, dtype, dim, "w_pre"))
+
+
+def _weight(t, dtype, dim: int, name: str):
+    if t is None:
+        return None
+    if t.dtype == dtype and t.numel() == dim and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, the other weights are {dtype}")
+    if t.numel() != dim:
+        raise ValueError(f"{name}: {t.numel()} elements, the rows have {dim}")
+    raise ValueError(f"{name}: a contiguous tensor")
 
 
 def twell_block_norm(x, y, x_out=None, h=None, *, w_post=None, gate=None, w_pre=None, row_gate=None,
@@ -834,10 +845,14 @@ def twell_block_norm(x, y, x_out=None, h=None, *, w_post=None, gate=None, w_pre=
     y_p, ldy = _matrix(y, bf, rows, dim, "y")
     o_p, ldo = _matrix(x_out, dtype, rows, dim, "x_out")
     h_p, ldh = _matrix(h, bf, rows, dim, "h")
-    code, (post, gate_p, pre) = _weights(dim, w_post, gate, w_pre)
-    row_p = _maybe(row_gate, f32, rows, "row_gate")
-    r1, r2 = _maybe(rstd_post, f32, rows, "rstd_post"), _maybe(rstd_pre, f32, rows, "rstd_pre")
-    _on_device(x, y, x_out, h, w_post, gate, w_pre, row_gate, rstd_post, rstd_pre)
+    code, post, gate_p, pre = _weights(dim, w_post, gate, w_pre)
+    row_p = _row(row_gate, f32, rows, "row_gate")
+    r1, r2 = _row(rstd_post, f32, rows, "rstd_post"), _row(rstd_pre, f32, rows, "rstd_pre")
+    if not (x.is_cuda and (y is None or y.is_cuda) and (x_out is None or x_out.is_cuda) and (h is None or h.is_cuda)
+            and (w_post is None or w_post.is_cuda) and (gate is None or gate.is_cuda) and (w_pre is None or w_pre.is_cuda)
+            and (row_gate is None or row_gate.is_cuda) and (rstd_post is None or rstd_post.is_cuda)
+            and (rstd_pre is None or rstd_pre.is_cuda)):
+        raise ValueError("tensors passed to libtwell must be CUDA tensors")
     rc = load_library().twell_block_norm(x_p, kind, ldx, y_p, ldy, rows, dim, post, gate_p, pre, code, row_p, skip_scale,
                                          branch_scale, eps, o_p, ldo, h_p, ldh, r1, r2, _on(stream))
     if rc:
@@ -865,11 +880,11 @@ def twell_block_norm_bwd(dh, d_out, x_out, y, dx=None, dy=None, *, w_post=None, 
     y_p, ldy = _matrix(y, bf, rows, dim, "y")
     dx_p, lddx = _matrix(dx, dtype, rows, dim, "dx")
     dy_p, lddy = _matrix(dy, bf, rows, dim, "dy")
-    code, (post, gate_p, pre) = _weights(dim, w_post, gate, w_pre)
-    row_p, drow = _maybe(row_gate, f32, rows, "row_gate"), _maybe(drow_gate, f32, rows, "drow_gate")
-    rstd1, rstd2 = _maybe(rstd_post, f32, rows, "rstd_post"), _maybe(rstd_pre, f32, rows, "rstd_pre")
-    dwo, dg, dwi = (_maybe(dw_post, f32, dim, "dw_post"), _maybe(dgate, f32, dim, "dgate"),
-                    _maybe(dw_pre, f32, dim, "dw_pre"))
+    code, post, gate_p, pre = _weights(dim, w_post, gate, w_pre)
+    row_p, drow = _row(row_gate, f32, rows, "row_gate"), _row(drow_gate, f32, rows, "drow_gate")
+    rstd1, rstd2 = _row(rstd_post, f32, rows, "rstd_post"), _row(rstd_pre, f32, rows, "rstd_pre")
+    dwo, dg, dwi = (_row(dw_post, f32, dim, "dw_post"), _row(dgate, f32, dim, "dgate"),
+                    _row(dw_pre, f32, dim, "dw_pre"))
     ws, ws_bytes = (None, 0) if workspace is None else _workspace(workspace)
     _on_device(dh, d_out, x_out, y, dx, dy, w_post, gate, w_pre, row_gate, rstd_post, rstd_pre, dw_post, dgate, dw_pre,
                drow_gate, workspace)
@@ -914,8 +929,8 @@ def twell_linear_logprobs(hidden, weight, targets, inv_temperature: float, logpr
     torch = _torch or _setup()
     f32, i32 = torch.float32, torch.int32
     rows, dim, vocab, h_p, ldh, w_p, ldw = _linear(hidden, weight)
-    outs = (_maybe(logprob, f32, rows, "logprob"), _maybe(entropy, f32, rows, "entropy"), _maybe(lse, f32, rows, "lse"))
-    t_p, st = _maybe(targets, i32, rows, "targets"), _arg(status, i32, 1, "status")
+    outs = (_row(logprob, f32, rows, "logprob"), _row(entropy, f32, rows, "entropy"), _row(lse, f32, rows, "lse"))
+    t_p, st = _row(targets, i32, rows, "targets"), _arg(status, i32, 1, "status")
     ws, ws_bytes = _workspace(workspace)
     _on_device(hidden, weight, targets, logprob, entropy, lse, workspace, status)
     rc = load_library().twell_linear_logprobs(h_p, ldh, w_p, ldw, rows, dim, vocab, t_p, inv_temperature, *outs, ws,
@@ -934,9 +949,9 @@ def twell_linear_logprobs_bwd(hidden, weight, targets, inv_temperature: float, l
     dh_p, lddh = _matrix(d_hidden, bf, rows, dim, "d_hidden")
     dw_p, lddw = _matrix(d_weight, bf, vocab, dim, "d_weight")
     lse_p = _arg(lse, f32, rows, "lse")
-    ent, g, ge = (_maybe(entropy, f32, rows, "entropy"), _maybe(d_logprob, f32, rows, "d_logprob"),
-                  _maybe(d_entropy, f32, rows, "d_entropy"))
-    t_p, st = _maybe(targets, i32, rows, "targets"), _arg(status, i32, 1, "status")
+    ent, g, ge = (_row(entropy, f32, rows, "entropy"), _row(d_logprob, f32, rows, "d_logprob"),
+                  _row(d_entropy, f32, rows, "d_entropy"))
+    t_p, st = _row(targets, i32, rows, "targets"), _arg(status, i32, 1, "status")
     ws, ws_bytes = _workspace(workspace)
     _on_device(hidden, weight, targets, lse, entropy, d_logprob, d_entropy, d_hidden, d_weight, workspace, status)
     rc = load_library().twell_linear_logprobs_bwd(h_p, ldh, w_p, ldw, rows, dim, vocab, t_p, inv_temperature, lse_p,

@@ -574,6 +574,7 @@ TWELL_API size_t twell_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t d
  * entropy) and the upstream gradients of logprob and entropy.  With p = exp(x - lse):
  *   G_j = inv_temperature * (d_logprob (1[j = target] - p_j) - d_entropy p_j (log p_j + entropy))
  *   dH = G W [n_rows][d_model] bf16,  dW = G^T H [vocab][d_model] bf16; either may be null
+ * A p_j below 2^-126, less than any normal number of 32 bits, counts as zero.
  * G is made again in pieces of the vocabulary, rounded to bf16 (each entry off by at most 2^-8 of
  * itself: why dW is bf16, too), and multiplied with fp32 sums that are rounded once.  A row without a
  * target takes d_logprob as 0; a row whose lse is -inf gives zeros.  targets with d_logprob, or entropy with
