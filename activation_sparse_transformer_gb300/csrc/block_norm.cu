@@ -24,8 +24,8 @@
 // starting and the sum over the CTAs are 5 and 8 of it), the launch and a row's chain of two sums short
 // ones (16 x 4096: 2.8 us).  The gradient keeps its sums over the rows in registers, so its CTAs have 512
 // threads (with 640 or 768 they spill: 54 and 65 us), and rows of 4104 to 8191 columns leave it one group
-// an SM (8000 x 4104: 116 us, 3.4 TB/s; forward, 1024 threads, 53).  Above 8192 columns the weights are read anew
-// for each row (2048 x 16384: 88 us, gradient 205).
+// an SM (8000 x 4104: 116 us, 3.4 TB/s; forward, 1024 threads, 53).  Above 8192 columns two CTAs share a row
+// and its sums, through each other's shared memory (2048 x 16384: 80 us, gradient 108).
 // All sums are fp32: a thread's own elements in order, then a tree over the group; sums over the
 // rows by groups, CTAs and then runs of CTAs in order, so equal calls give equal bits.
 #include <algorithm>
@@ -42,7 +42,11 @@ constexpr int kMaxStages = 4;       // rows on the way to a thread
 constexpr int kSharedBytes = 208 * 1024;  // beside 12 KB for the sums
 constexpr int kV = 2;               // pieces of 8 elements a thread
 constexpr int kThreads = 1024, kBwdThreads = 512;  // of a CTA: what registers allow
-constexpr int kWide = 8192;         // above, 1024 threads a row and its weights read anew for each
+// Above, two CTAs share a row, so that its weights and the sums over the rows stay where they are (read anew for
+// each row and with spills, 2048 x 16384 took 88 us, the gradient 206; now 80 and 108).  A barrier of the pair is
+// dearer than one of a CTA's, so narrower rows stay in one (4096 x 8192: 49 us, in two 77; gradient 81 and 101; 8176 x 4104 53
+// and 92; 119 and 127).
+constexpr int kWide = 8192;
 
 struct NormArgs {
   const void* x;
@@ -145,43 +149,51 @@ __device__ __forceinline__ float warp_sums(const float* scratch, int group) {
   return (a.x + a.y) + (a.z + a.w);
 }
 
-// The sum over the group's threads, in every thread of it (SUB: a part of a warp).  scratch: 32 floats of
-// the group's own, zero past its warps; free again once the group has passed another such barrier.
-template <bool SUB>
-__device__ __forceinline__ float group_sum(float v, int group, int id, int thread, float* scratch) {
-  if constexpr (SUB) {
-    for (int o = group >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-  } else {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (group == 32) return v;
-    if ((thread & 31) == 0) scratch[thread >> 5] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(group) : "memory");
-    return warp_sums(scratch, group);
-  }
+// How a row's threads lie: in a part of a warp, in whole warps of a CTA, or in both CTAs of a cluster.
+enum Span { kSub, kCta, kPair };
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// A barrier of the cluster's threads; what was written to either shared memory is there after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// A warp's sum to its place in the shared memory of both CTAs.
+__device__ __forceinline__ void tell_both(float* at, float v) {
+  *at = v;
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, %1;\n\tst.shared::cluster.f32 [r], %2;\n\t}" ::"r"(smem_u32(at)),
+      "r"(cluster_rank() ^ 1), "f"(v)
+      : "memory");
 }
 
-// Three sums at once.  scratch: [3][32].
-template <bool SUB>
-__device__ __forceinline__ void group_sum3(float (&v)[3], int group, int id, int thread, float* scratch) {
-  if constexpr (SUB) {
-    for (int o = group >> 1; o > 0; o >>= 1)
+// K sums over the group's threads at once, in every thread of it.  scratch: [K][32] floats of the group's own, zero past its
+// warps; free again once the group has passed another such barrier.
+template <Span SPAN, int K>
+__device__ __forceinline__ void group_sums(float (&v)[K], int group, int id, int thread, float* scratch) {
+  for (int o = SPAN == kSub ? group >> 1 : 16; o > 0; o >>= 1)
 #pragma unroll
-      for (int k = 0; k < 3; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  } else {
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if (SPAN == kSub || (SPAN == kCta && group == 32)) return;
+  if ((thread & 31) == 0) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int k = 0; k < 3; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if (group == 32) return;
-    if ((thread & 31) == 0)
-#pragma unroll
-      for (int k = 0; k < 3; ++k) scratch[k * 32 + (thread >> 5)] = v[k];
+    for (int k = 0; k < K; ++k) {
+      float* const at = scratch + k * 32 + (thread >> 5);
+      if constexpr (SPAN == kPair)
+        tell_both(at, v[k]);
+      else
+        *at = v[k];
+    }
+  }
+  if constexpr (SPAN == kPair)
+    cluster_sync();
+  else
     asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(group) : "memory");
 #pragma unroll
-    for (int k = 0; k < 3; ++k) v[k] = warp_sums(scratch + k * 32, group);
-  }
+  for (int k = 0; k < K; ++k) v[k] = warp_sums(scratch + k * 32, group);
 }
 
 __device__ __forceinline__ void copy16(uint8_t* dst, const void* src) {
@@ -275,12 +287,12 @@ struct Layout {
   }
 };
 
-// The product of the branch's weights, and the next norm's weight, as fp32: in shared memory ([2]
-// planes of a thread's 16-byte pieces, read without conflicts), or read anew where rows are too wide for that.
-template <typename T, bool SHARED>
+// The product of the branch's weights, and the next norm's weight, as fp32 in shared memory: [2]
+// planes of a thread's 16-byte pieces, read without conflicts.
+template <typename T>
 struct Weights {
   static constexpr int V = kV;
-  uint8_t* base;  // [branch, pre][piece][2][group] of 16 bytes
+  uint8_t* base;  // [branch, pre][piece][2][group] of 16 bytes; group: of this CTA
   const void *post, *gate, *pre;
   bool f32;
   int group, thread;
@@ -320,64 +332,75 @@ struct Weights {
   }
   // by the first group's threads, a barrier before the first use
   __device__ __forceinline__ void fill() const {
-    if constexpr (SHARED) {
 #pragma unroll
-      for (int i = 0; i < 2 * V; ++i) {
-        const Oct w = make(i < V, i % V);
-        *slot(i < V, i % V, 0) = make_ulonglong2(w.v[0], w.v[1]);
-        *slot(i < V, i % V, 1) = make_ulonglong2(w.v[2], w.v[3]);
-      }
+    for (int i = 0; i < 2 * V; ++i) {
+      const Oct w = make(i < V, i % V);
+      *slot(i < V, i % V, 0) = make_ulonglong2(w.v[0], w.v[1]);
+      *slot(i < V, i % V, 1) = make_ulonglong2(w.v[2], w.v[3]);
     }
   }
   __device__ __forceinline__ Oct get(bool branch, int i) const {
-    if constexpr (!SHARED) return make(branch, i);
     const ulonglong2 a = *slot(branch, i, 0), b = *slot(branch, i, 1);
     return Oct{{a.x, a.y, b.x, b.y}};
   }
 };
 
 // What the two kernels set up alike.
-template <typename T, bool SHARED, bool SUB>
+template <typename T, Span SPAN>
 struct Setup {
   static constexpr int V = kV;
-  static constexpr bool kShared = SHARED;
   int groups, id, thread, pitch, rows;  // rows: of a warp
+  int team, teams;                      // CTAs that deal with rows, alone or as pairs
   Layout<T> at;
-  Weights<T, kShared> weights;
+  Weights<T> weights;
   uint8_t *ring, *mine;
   __device__ __forceinline__ Setup(uint8_t* smem, int group, int dim, const void* post, const void* gate,
                                    const void* pre, bool f32) {
-    groups = blockDim.x / group, id = threadIdx.x / group, thread = threadIdx.x % group;
-    pitch = blockDim.x * 16, rows = SUB ? 32 / group : 1;
-    at = Layout<T>{dim, thread * Layout<T>::kRun, group * Layout<T>::kRun};
-    weights = Weights<T, kShared>{smem, post, gate, pre, f32, group, thread, at};
-    ring = smem + (kShared ? 2 * V * 2 * 16 * group : 0);
+    constexpr int kCtas = SPAN == kPair ? 2 : 1;
+    const int here = group / kCtas;  // threads of a row in this CTA
+    groups = blockDim.x / here, id = threadIdx.x / here, thread = threadIdx.x % here;
+    team = blockIdx.x / kCtas, teams = gridDim.x / kCtas;
+    pitch = blockDim.x * 16, rows = SPAN == kSub ? 32 / group : 1;
+    weights = Weights<T>{smem, post, gate, pre, f32, here, thread};
+    if constexpr (SPAN == kPair) thread += cluster_rank() * here;
+    weights.at = at = Layout<T>{dim, thread * Layout<T>::kRun, group * Layout<T>::kRun};
+    ring = smem + 2 * V * 2 * 16 * here;
     mine = ring + threadIdx.x * 16;
   }
-  // the row of this warp's first group: loops go by it, so that a warp stays together
-  __device__ __forceinline__ int64_t first_row(int64_t row) const { return SUB ? row - id % rows : row; }
+  // The first row of those that stay together, which loops go by: a warp's, or (their barrier is one) a pair's.
+  __device__ __forceinline__ int64_t first_row(int64_t row) const {
+    return SPAN == kSub ? row - id % rows : SPAN == kPair ? row - id : row;
+  }
   // Zeros where no copy goes.
   __device__ __forceinline__ void clear(int pieces) const {
     if (at.on(V - 1, Layout<T>::kRuns - 1)) return;
     for (int p = 0; p < pieces; ++p) *reinterpret_cast<uint4*>(mine + p * pitch) = make_uint4(0, 0, 0, 0);
   }
+  // All that was set up is there: the weights, and in a pair the other CTA with its scratch.
+  __device__ __forceinline__ void ready() const {
+    if (id == 0) weights.fill();
+    if constexpr (SPAN == kPair)
+      cluster_sync();
+    else
+      __syncthreads();
+  }
 };
 
 // A row for each group of threads in turn; Y: there is a block's output.
-template <typename T, int NT, bool SHARED, bool SUB, bool Y>
+template <typename T, int NT, Span SPAN, bool Y>
 __global__ void __launch_bounds__(NT, 1) block_norm_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float scratch[kMaxBarriers][2][2][32];  // two sums of a row, rows in turn
   for (int i = threadIdx.x; i < kMaxBarriers * 128; i += blockDim.x) (&scratch[0][0][0][0])[i] = 0.0f;
   grid_dependency_wait();
   constexpr int V = kV;
-  const Setup<T, SHARED, SUB> g(smem, a.group, a.dim, a.w_post, a.gate, a.w_pre, a.w_f32);
+  const Setup<T, SPAN> g(smem, a.group, a.dim, a.w_post, a.gate, a.w_pre, a.w_f32);
   const Layout<T>& at = g.at;
   constexpr int kX = Layout<T>::kPieces, kPieces = kX + (Y ? 1 : 0);  // of x, of y
-  const int pitch = g.pitch, step = gridDim.x * g.groups;
+  const int pitch = g.pitch, step = g.teams * g.groups;
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
   g.clear(a.stages * V * kPieces);
-  int64_t row = static_cast<int64_t>(blockIdx.x) * g.groups + g.id, next = row;
+  int64_t row = static_cast<int64_t>(g.team) * g.groups + g.id, next = row;
   auto copy = [&](uint8_t* to) {
     if (next < a.n_rows) {
       const T* const x = static_cast<const T*>(a.x) + next * a.ldx;
@@ -395,15 +418,14 @@ __global__ void __launch_bounds__(NT, 1) block_norm_kernel(const NormArgs a) {
   for (int s = 0; s < a.stages; ++s) copy(g.mine + s * V * kPieces * pitch);
   float gate = a.branch;  // of a row, read a row ahead
   if (Y && a.row_gate && row < a.n_rows) gate *= a.row_gate[row];
-  if (g.id == 0) g.weights.fill();
-  __syncthreads();
+  g.ready();
   const F2 skip = pair(a.skip, a.skip);
   uint8_t* from = g.mine;
   int stage = 0, turn = 0;
   const int own = a.group > 32 ? g.id : 0;  // smaller groups use no scratch
 #pragma unroll 1
   for (; g.first_row(row) < a.n_rows; row += step, turn ^= 1) {
-    const bool live = !SUB || row < a.n_rows;
+    const bool live = SPAN == kCta || row < a.n_rows;
     float scale = gate;
     if (Y && a.row_gate && row + step < a.n_rows) gate = a.branch * a.row_gate[row + step];
     copies_wait(a.stages);
@@ -415,8 +437,9 @@ __global__ void __launch_bounds__(NT, 1) block_norm_kernel(const NormArgs a) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) sum = fma2(y.v[k], y.v[k], sum);
       }
-      const float s = group_sum<SUB>(both(sum), a.group, g.id, g.thread, scratch[own][0][turn]);
-      const float r1 = rsqrtf(fmaf(s, inv_dim, a.eps));
+      float s[1] = {both(sum)};
+      group_sums<SPAN>(s, a.group, g.id, g.thread, scratch[own][0][turn]);
+      const float r1 = rsqrtf(fmaf(s[0], inv_dim, a.eps));
       if (live && g.thread == 0 && a.rstd_post) a.rstd_post[row] = r1;
       scale *= r1;
     }
@@ -444,8 +467,9 @@ __global__ void __launch_bounds__(NT, 1) block_norm_kernel(const NormArgs a) {
       for (int i = 0; i < V; ++i) at.write(to, i, z[i]);
     }
     if (!a.h) continue;
-    const float s = group_sum<SUB>(both(sum), a.group, g.id, g.thread, scratch[own][1][turn]);
-    const float r2 = rsqrtf(fmaf(s, inv_dim, a.eps));
+    float s[1] = {both(sum)};
+    group_sums<SPAN>(s, a.group, g.id, g.thread, scratch[own][1][turn]);
+    const float r2 = rsqrtf(fmaf(s[0], inv_dim, a.eps));
     if (live && g.thread == 0 && a.rstd_pre) a.rstd_pre[row] = r2;
     const F2 r22 = pair(r2, r2);
     uint16_t* const to = a.h + row * a.ldh;
@@ -461,22 +485,22 @@ __global__ void __launch_bounds__(NT, 1) block_norm_kernel(const NormArgs a) {
 }
 
 // Its gradient, dealt the same.  NORM: there is a norm behind (dh); Y: there is a block's output.
-template <typename T, int NT, bool SHARED, bool SUB, bool NORM, bool Y>
+template <typename T, int NT, Span SPAN, bool NORM, bool Y>
 __global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float scratch[kMaxBarriers][2][3][32];  // three sums of a row, rows in turn
   for (int i = threadIdx.x; i < kMaxBarriers * 192; i += blockDim.x) (&scratch[0][0][0][0])[i] = 0.0f;
   grid_dependency_wait();
   constexpr int V = kV;
-  const Setup<T, SHARED, SUB> g(smem, a.group, a.dim, a.w_post, a.gate, a.w_pre, a.w_f32);
+  const Setup<T, SPAN> g(smem, a.group, a.dim, a.w_post, a.gate, a.w_pre, a.w_f32);
   const Layout<T>& at = g.at;
   // of x_out, dh, y, d_out
   constexpr int kP = Layout<T>::kPieces, kDh = NORM ? kP : 0, kY = kDh + (NORM ? 1 : 0);
   constexpr int kUp = kY + (Y ? 1 : 0), kPieces = kUp + kP;
-  const int pitch = g.pitch, step = gridDim.x * g.groups;
+  const int pitch = g.pitch, step = g.teams * g.groups;
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
   g.clear(a.stages * V * kPieces);
-  int64_t row = static_cast<int64_t>(blockIdx.x) * g.groups + g.id, next = row;
+  int64_t row = static_cast<int64_t>(g.team) * g.groups + g.id, next = row;
   auto copy = [&](uint8_t* slot) {
     if (next < a.n_rows) {
 #pragma unroll
@@ -504,8 +528,7 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs
     if (Y && a.row_gate) scale = a.branch * a.row_gate[of];
   };
   factors(row);
-  if (g.id == 0) g.weights.fill();
-  __syncthreads();
+  g.ready();
   Oct sum_pre[V] = {}, sum_branch[V] = {};
   const F2 skip = pair(a.skip, a.skip);
   uint8_t* slot = g.mine;
@@ -513,11 +536,11 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs
   const int own = a.group > 32 ? g.id : 0;  // smaller groups use no scratch
 #pragma unroll 1
   for (; g.first_row(row) < a.n_rows; row += step, turn ^= 1) {
-    const bool live = !SUB || row < a.n_rows;
+    const bool live = SPAN == kCta || row < a.n_rows;
     const float now_r1 = r1, now_r2 = r2, now_scale = scale;
     factors(row + step);
     copies_wait(a.stages);
-    if (SUB && !live) {  // past the last row: zeros, which add nothing to the sums over the rows
+    if (SPAN != kCta && !live) {  // past the last row: zeros, which add nothing to the sums over the rows
       for (int p = 0; p < V * kPieces; ++p) *reinterpret_cast<uint4*>(slot + p * pitch) = make_uint4(0, 0, 0, 0);
     }
     // e = d_out + r2 a, so that dz = e - r2 c2 v; the three sums of the row
@@ -558,7 +581,7 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs
     float c2 = 0.0f, c1 = 0.0f;
     if (NORM || (Y && (a.w_post || a.drow_gate))) {
       float sums[3] = {both(sum_av), both(sum_es), both(sum_vs)};
-      group_sum3<SUB>(sums, a.group, g.id, g.thread, scratch[own][turn][0]);
+      group_sums<SPAN>(sums, a.group, g.id, g.thread, scratch[own][turn][0]);
       c2 = now_r2 * (inv_dim * sums[0]);
       c1 = fmaf(-c2, sums[2], sums[1]);  // sum of gate w_post dz s
       if (Y && live && g.thread == 0 && a.drow_gate) a.drow_gate[row] = a.branch * c1;
@@ -598,7 +621,7 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs
   copies_wait(1);
   if (!a.want_pre && !a.want_branch) return;
   // the groups of a warp, then the groups (or warps) in order through shared memory, then the CTA's to the workspace
-  for (int o = a.group; SUB && o < 32; o <<= 1) {
+  for (int o = a.group; SPAN == kSub && o < 32; o <<= 1) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -610,7 +633,7 @@ __global__ void __launch_bounds__(NT, 1) block_norm_bwd_kernel(const NormBwdArgs
   const int parts = g.groups / g.rows, part_id = g.id / g.rows;
   const bool writes = g.id % g.rows == 0;
   float* const sums = reinterpret_cast<float*>(g.ring);
-  float* const part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.dim;
+  float* const part = a.part + static_cast<int64_t>(g.team) * 2 * a.dim;
   for (int k = 0; k < parts; ++k) {
     __syncthreads();  // also: every thread is through with the ring
     if (part_id != k || !writes) continue;
@@ -667,23 +690,26 @@ __global__ void __launch_bounds__(1024) block_norm_sum_kernel(const NormSumArgs 
   if (a.dgate) a.dgate[c] = a.w_post ? branch[0] * weight1(a.w_post, a.w_f32, c) : branch[0];
 }
 
-// How a call's rows are dealt: threads of a row, rows of a CTA, CTAs, and rows on the way.
+// How a call's rows are dealt: threads of a row, rows and CTAs of a cluster, clusters, and rows on the way.
 struct Deal {
-  int group, groups, grid, stages, smem;
+  int group, groups, ctas, grid, stages, smem;
 };
-Deal deal(int n_rows, int dim, int threads, int pieces, int least_ring) {
+Deal deal(int n_rows, int dim, int threads, int pieces, bool sums) {
   Deal d;
   const int need = (dim + 8 * kV - 1) / (8 * kV);
-  d.group = need > 32 ? (need + 31) / 32 * 32 : 1;
+  d.ctas = dim > kWide ? 2 : 1;
+  d.group = need > 32 ? (need + 32 * d.ctas - 1) / (32 * d.ctas) * (32 * d.ctas) : 1;
   while (d.group < need) d.group *= 2;  // within a warp: a power of two
+  const int teams = sm_count() / d.ctas, here = std::max(1, d.group / d.ctas);
   // few rows are spread over the SMs, one to a CTA (or a warp's)
-  d.groups = std::max(1, std::min(threads / d.group, (n_rows + sm_count() - 1) / sm_count()));
+  d.groups = std::max(1, std::min(threads / here, (n_rows + teams - 1) / teams));
   if (d.group < 32) d.groups = (d.groups + 32 / d.group - 1) / (32 / d.group) * (32 / d.group);
   if (d.group > 32) d.groups = std::min(d.groups, kMaxBarriers);
-  d.grid = std::max(1, std::min({(n_rows + d.groups - 1) / d.groups, sm_count(), kMaxParts}));
-  const int row = d.groups * d.group * kV * pieces * 16, weights = dim > kWide ? 0 : 2 * kV * 2 * 16 * d.group;
+  d.grid = std::max(1, std::min({(n_rows + d.groups - 1) / d.groups, teams, kMaxParts}));
+  const int row = d.groups * here * kV * pieces * 16, weights = 2 * kV * 2 * 16 * here;
   d.stages = std::max(1, std::min(kMaxStages, (kSharedBytes - weights) / row));
-  d.smem = weights + std::max(d.stages * row, least_ring);
+  // the groups' sums over the rows meet where the rows were
+  d.smem = weights + std::max(d.stages * row, sums && d.groups > 1 ? 2 * dim * 4 : 0);
   return d;
 }
 
@@ -691,37 +717,49 @@ template <typename Args>
 int launch(void (*kernel)(Args), const Deal& d, const Args& a, int id, cudaStream_t s) {
   KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kSharedBytes));
   LaunchScope scope(id, s);
-  return launch_pdl(kernel, dim3(d.grid), dim3(d.groups * d.group), d.smem, s, a) == cudaSuccess ? TWELL_OK
-                                                                                                : TWELL_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(d.grid * d.ctas);
+  cfg.blockDim = dim3(d.groups * d.group / d.ctas);
+  cfg.dynamicSmemBytes = d.smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = d.ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = d.ctas == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }
 
-template <typename T, int NT, bool SHARED, bool SUB>
+template <typename T, int NT, Span SPAN>
 auto fwd_kernel(const NormArgs& a) {
-  return a.y ? block_norm_kernel<T, NT, SHARED, SUB, true> : block_norm_kernel<T, NT, SHARED, SUB, false>;
+  return a.y ? block_norm_kernel<T, NT, SPAN, true> : block_norm_kernel<T, NT, SPAN, false>;
 }
 
 template <typename T>
 int launch_norm(NormArgs a, cudaStream_t s) {
-  const Deal d = deal(a.n_rows, a.dim, a.dim > kWide ? 1024 : kThreads, Layout<T>::kPieces + (a.y ? 1 : 0), 0);
+  const Deal d = deal(a.n_rows, a.dim, kThreads, Layout<T>::kPieces + (a.y ? 1 : 0), false);
   a.group = d.group, a.stages = d.stages;
-  return launch(d.group < 32 ? fwd_kernel<T, kThreads, true, true>(a)
-                : a.dim > kWide ? fwd_kernel<T, 1024, false, false>(a) : fwd_kernel<T, kThreads, true, false>(a),
+  return launch(d.ctas == 2 ? fwd_kernel<T, kThreads, kPair>(a)
+                : d.group < 32 ? fwd_kernel<T, kThreads, kSub>(a) : fwd_kernel<T, kThreads, kCta>(a),
                 d, a, TWELL_KERNEL_BLOCK_NORM, s);
 }
 
-template <typename T, int NT, bool SHARED, bool SUB>
+template <typename T, int NT, Span SPAN>
 auto bwd_kernel(const NormBwdArgs& a) {
-  if (a.dh) return a.y ? block_norm_bwd_kernel<T, NT, SHARED, SUB, true, true> : block_norm_bwd_kernel<T, NT, SHARED, SUB, true, false>;
-  return a.y ? block_norm_bwd_kernel<T, NT, SHARED, SUB, false, true> : block_norm_bwd_kernel<T, NT, SHARED, SUB, false, false>;
+  if (a.dh) return a.y ? block_norm_bwd_kernel<T, NT, SPAN, true, true> : block_norm_bwd_kernel<T, NT, SPAN, true, false>;
+  return a.y ? block_norm_bwd_kernel<T, NT, SPAN, false, true> : block_norm_bwd_kernel<T, NT, SPAN, false, false>;
 }
 
 template <typename T>
 int launch_norm_bwd(NormBwdArgs a, int* parts, cudaStream_t s) {
-  const Deal d = deal(a.n_rows, a.dim, a.dim > kWide ? 1024 : kBwdThreads,
-                      Layout<T>::kPieces * (a.dh ? 2 : 1) + (a.dh ? 1 : 0) + (a.y ? 1 : 0), 2 * a.dim * 4);
+  const Deal d = deal(a.n_rows, a.dim, kBwdThreads,
+                      Layout<T>::kPieces * (a.dh ? 2 : 1) + (a.dh ? 1 : 0) + (a.y ? 1 : 0), true);
   a.group = d.group, a.stages = d.stages, *parts = d.grid;
-  return launch(d.group < 32 ? bwd_kernel<T, kBwdThreads, true, true>(a)
-                : a.dim > kWide ? bwd_kernel<T, 1024, false, false>(a) : bwd_kernel<T, kBwdThreads, true, false>(a),
+  return launch(d.ctas == 2 ? bwd_kernel<T, kBwdThreads, kPair>(a)
+                : d.group < 32 ? bwd_kernel<T, kBwdThreads, kSub>(a) : bwd_kernel<T, kBwdThreads, kCta>(a),
                 d, a, TWELL_KERNEL_BLOCK_NORM_BWD, s);
 }
 

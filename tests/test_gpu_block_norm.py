@@ -151,6 +151,17 @@ def test_a_row_with_nan_or_infinity_keeps_to_itself(tw):
     assert o["h"][2].isnan().all() and o["h"][4].isnan().any()
 
 
+WIDE = [(76, 8200), (77, 16384), (401, 8208), (155, 12296), (229, 10240)]  # several rows side by side, the last round not full
+
+
+@pytest.mark.parametrize("flags", ["ypgrn", "yn", "ypr", "n"])
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,dim", WIDE)
+def test_forward_of_wide_rows(tw, rows, dim, stream, flags):
+    i = make(rows, dim, stream, flags, 31, pad=16)
+    check_forward(i, run(tw, i, 0.75, -1.25), 0.75, -1.25)
+
+
 # ---------------------------------------------------------------- the gradient
 def backward(tw, i, skip, branch, seed, dh=True, d_out=True, dx=True, dy=True, dw=True, stream=None, in_place=False):
     n, d = i["x"].shape
@@ -208,6 +219,24 @@ def test_backward_parts(tw, rows, dim, stream, flags):
 def test_backward_sizes(tw, rows, dim):
     i = make(rows, dim, torch.bfloat16, "ypgrn", 13)
     check_backward(*backward(tw, i, 1.0, 1.0, 14)[:3], rows)
+
+
+@pytest.mark.parametrize("flags", ["ypgrn", "yn", "ypr", "n"])
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,dim", WIDE)
+def test_backward_of_wide_rows(tw, rows, dim, stream, flags):
+    i = make(rows, dim, stream, flags, 32, pad=16)
+    out, want, size, call = backward(tw, i, 0.75, -1.25, 33)
+    check_backward(out, want, size, rows)
+    first = {k: v.clone() for k, v in out.items() if v is not None}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for k in first:
+        out[k].fill_(float("nan"))
+    graph.replay()
+    for k in first:
+        assert torch.equal(out[k], first[k]), k
 
 
 @pytest.mark.parametrize("given", [dict(dh=False), dict(d_out=False), dict(dx=False), dict(dy=False), dict(dw=False),
