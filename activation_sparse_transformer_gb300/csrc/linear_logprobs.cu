@@ -73,7 +73,8 @@ struct Job {
   int units, band;          // tiles, rows of tiles that are taken together
   int start, light0, light, extra;  // how the tiles are dealt, see Walk
   int a_mn, b_mn;           // operand stored [K][M] / [K][N]
-  int add, round;           // dH: earlier pieces have left sums; these are the last
+  int add, round;           // earlier pieces have left dH's sums; these are the last
+  int sum_rows;             // of one range's sums
 };
 
 struct Maps {
@@ -91,8 +92,7 @@ struct Args {
   float* of_target;   // [n_rows] x of the target
   // backward
   const float *lse, *entropy, *g, *ge;
-  const float* dh_sum;  // [ksplit][sum_rows][d_model]
-  int sum_rows;         // n_rows, up to whole tiles
+  const float* dh_sum;  // [ksplit][rows, up to whole tiles][d_model]
   int32_t* status;
   uint64_t wait_limit_ns;
   int stall;  // arrivals that every stage waits for in vain (the self-test)
@@ -430,12 +430,12 @@ __device__ __forceinline__ void epilogue_grad(const Args& a, const Job& j, const
   }
 }
 
-// A gradient's tile: bf16, or dH's sums in fp32 while pieces or ranges are still to be added.
+// A gradient's tile: bf16, or sums in fp32 while pieces (dH) or ranges are still to be added.
 __device__ __forceinline__ void epilogue_store(const Args& a, const Job& j, const Tile& t, int ks,
                                                const CUtensorMap* map, Box& out) {
   const int lane = threadIdx.x & 31, from = t.half * (kBN / 2);
   if (!j.round) {
-    const int y = ks * a.sum_rows + t.row - lane;
+    const int y = ks * j.sum_rows + t.row - lane;
 #pragma unroll 1
     for (int k = from; k < from + kBN / 2; k += 32) {
       if (t.col0 + k >= j.n) break;
@@ -794,30 +794,39 @@ __global__ void __launch_bounds__(32) linear_join_kernel(const JoinArgs a) {
   }
 }
 
-struct ReduceArgs {
+// A gradient whose K was cut.
+struct Ranges {
   const float* sum;
-  int ksplit, n_rows, sum_rows, dim;
+  int ksplit, rows, sum_rows;
   uint16_t* out;
   int64_t ld;
+  int blocks;
+};
+struct ReduceArgs {
+  Ranges of[2];  // dH, dW; no blocks: nothing to do
+  int dim;
 };
 
-// dH from the sums of K's ranges, added in order, 8 of them on the way at a time; 4 elements a thread.
-__global__ void __launch_bounds__(256) linear_reduce_kernel(const ReduceArgs a) {
+// dH and dW from the sums of K's ranges, added in order, 8 of them on the way at a time; 4 elements a thread.
+__global__ void __launch_bounds__(256) linear_reduce_kernel(const __grid_constant__ ReduceArgs a) {
   grid_dependency_wait();
-  const int64_t vecs = a.dim / 4, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= vecs * a.n_rows) return;
-  const int64_t row = i / vecs, c = i % vecs * 4, plane = static_cast<int64_t>(a.sum_rows) * a.dim;
-  const float* const at = a.sum + row * a.dim + c;
+  int block = blockIdx.x;
+  const Ranges& r = a.of[block < a.of[0].blocks ? 0 : 1];
+  if (block >= a.of[0].blocks) block -= a.of[0].blocks;
+  const int64_t vecs = a.dim / 4, i = static_cast<int64_t>(block) * 256 + threadIdx.x;
+  if (i >= vecs * r.rows) return;
+  const int64_t row = i / vecs, c = i % vecs * 4, plane = static_cast<int64_t>(r.sum_rows) * a.dim;
+  const float* const at = r.sum + row * a.dim + c;
   float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int k = 0; k < a.ksplit; k += 8) {
+  for (int k = 0; k < r.ksplit; k += 8) {
     float4 x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      x[e] = k + e < a.ksplit ? *reinterpret_cast<const float4*>(at + (k + e) * plane) : make_float4(0, 0, 0, 0);
+      x[e] = k + e < r.ksplit ? *reinterpret_cast<const float4*>(at + (k + e) * plane) : make_float4(0, 0, 0, 0);
 #pragma unroll
     for (int e = 0; e < 8; ++e) f.x += x[e].x, f.y += x[e].y, f.z += x[e].z, f.w += x[e].w;
   }
-  *reinterpret_cast<uint2*>(a.out + row * a.ld + c) = make_uint2(bf16_pair(f.x, f.y), bf16_pair(f.z, f.w));
+  *reinterpret_cast<uint2*>(r.out + row * r.ld + c) = make_uint2(bf16_pair(f.x, f.y), bf16_pair(f.z, f.w));
 }
 
 int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
@@ -826,14 +835,15 @@ size_t round_up(size_t x, size_t to) { return (x + to - 1) / to * to; }
 // CTAs to a tile: a pair from 129 rows on.
 int ctas_of(int64_t n_rows) { return n_rows > kBM ? 2 : 1; }
 
-// Rows of dH's fp32 sums: whole tiles, as a tile leaves whole.
-int64_t sum_rows(int64_t n_rows) { return (n_rows + 255) / 256 * 256; }
+// Rows of a gradient's fp32 sums: whole tiles, as a tile leaves whole.
+int64_t sum_rows(int64_t rows) { return (rows + 255) / 256 * 256; }
 
 // How a backward call is cut.
 struct Plan {
   int pieces, piece;  // columns of a piece, a multiple of 256
   int ksplit;         // ranges of the vocabulary in dH's product of a piece
-  size_t grad_bytes, sum_bytes, bytes;
+  int wsplit;         // ranges of the rows in dW's product
+  size_t grad_bytes, sum_bytes, wsum_bytes, bytes;
 };
 
 Plan plan_bwd(int64_t n_rows, int64_t d, int64_t vocab) {
@@ -852,7 +862,14 @@ Plan plan_bwd(int64_t n_rows, int64_t d, int64_t vocab) {
       std::max<int64_t>(1, std::min<int64_t>({kMaxKSplit, num_k / 8, kPlanSms / ctas / std::max<int64_t>(1, tiles)})));
   p.grad_bytes = round_up(static_cast<size_t>(n_rows) * p.piece * 2, 256);
   p.sum_bytes = p.pieces > 1 || p.ksplit > 1 ? round_up(static_cast<size_t>(p.ksplit) * sum_rows(n_rows) * d * 4, 256) : 0;
-  p.bytes = p.grad_bytes * (p.pieces > 1 ? 2 : 1) + p.sum_bytes + 256;
+  // So is dW's, over many rows (9080 x 376 x 232: 63 -> 26 us, 11351 x 520 x 1245 90 -> 58); with several pieces it
+  // has tiles enough.
+  const int64_t wtiles = ceil_div(vocab, kBM * ctas) * static_cast<int64_t>(ceil_div(d, kBN));
+  p.wsplit = p.pieces > 1 ? 1
+                          : static_cast<int>(std::max<int64_t>(
+                                1, std::min<int64_t>({kMaxKSplit, ceil_div(n_rows, kBK) / 8, kPlanSms / ctas / wtiles})));
+  p.wsum_bytes = p.wsplit > 1 ? round_up(static_cast<size_t>(p.wsplit) * sum_rows(vocab) * d * 4, 256) : 0;
+  p.bytes = p.grad_bytes * (p.pieces > 1 ? 2 : 1) + p.sum_bytes + p.wsum_bytes + 256;
   return p;
 }
 
@@ -1046,7 +1063,8 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
   base.n_rows = n_rows, base.d_model = d_model, base.vocab = vocab, base.targets = targets;
   base.inv_t = inv_temperature, base.lse = lse, base.entropy = entropy, base.g = d_logprob, base.ge = d_entropy;
   float* const dh_sum = reinterpret_cast<float*>(ws + plan.grad_bytes * (plan.pieces > 1 ? 2 : 1));
-  base.dh_sum = dh_sum, base.sum_rows = static_cast<int>(sum_rows(n_rows));
+  float* const dw_sum = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(dh_sum) + plan.sum_bytes);
+  base.dh_sum = dh_sum;
   base.status = status, base.wait_limit_ns = kWaitLimitNs;
   const int ctas = ctas_of(n_rows);
   for (int p = 0; p <= plan.pieces; ++p) {
@@ -1062,19 +1080,25 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
         j.type = kJobDHidden, j.m = n_rows, j.n = d_model, j.add = p > 1;
         j.round = p == plan.pieces && plan.ksplit == 1;
         // the first piece fills all ranges' sums; a narrower last one adds to no more than it has steps
-        j.ksplit = plan.ksplit;
+        j.ksplit = plan.ksplit, j.sum_rows = static_cast<int>(sum_rows(n_rows));
         if (j.round)
           KV_TRY(encode_tmap_2d(&maps.out[a.num_jobs], dH, d_model, n_rows, lddh * 2, 64, 32));
         else
           KV_TRY(encode_tmap_2d_f32(&maps.out[a.num_jobs], dh_sum, d_model,
-                                    static_cast<uint64_t>(plan.ksplit) * base.sum_rows,
+                                    static_cast<uint64_t>(plan.ksplit) * j.sum_rows,
                                     static_cast<uint64_t>(d_model) * 4, 32, 32));
         KV_TRY(set_job(&maps, &a, ctas, j, G, plan.piece, Wp, ldw, width));
       }
       if (dW) {
-        j.type = kJobDWeight, j.m = width, j.n = d_model, j.a_mn = 1, j.add = 0, j.round = 1, j.ksplit = 1;
-        KV_TRY(encode_tmap_2d(&maps.out[a.num_jobs], dW + static_cast<int64_t>(col0) * lddw, d_model, width, lddw * 2,
-                              64, 32));
+        j.type = kJobDWeight, j.m = width, j.n = d_model, j.a_mn = 1, j.add = 0;
+        j.round = plan.wsplit == 1, j.ksplit = plan.wsplit, j.sum_rows = static_cast<int>(sum_rows(vocab));
+        if (j.round)
+          KV_TRY(encode_tmap_2d(&maps.out[a.num_jobs], dW + static_cast<int64_t>(col0) * lddw, d_model, width, lddw * 2,
+                                64, 32));
+        else
+          KV_TRY(encode_tmap_2d_f32(&maps.out[a.num_jobs], dw_sum, d_model,
+                                    static_cast<uint64_t>(plan.wsplit) * j.sum_rows,
+                                    static_cast<uint64_t>(d_model) * 4, 32, 32));
         KV_TRY(set_job(&maps, &a, ctas, j, G, plan.piece, H, ldh, n_rows));
       }
     }
@@ -1089,11 +1113,15 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
     }
     KV_TRY((ctas == 2 ? launch_jobs<2, false>(maps, a, s) : launch_jobs<1, false>(maps, a, s)));
   }
-  if (!dH || plan.ksplit == 1) return TWELL_OK;
-  const ReduceArgs r{dh_sum, plan.ksplit, n_rows, base.sum_rows, d_model, dH, lddh};
+  auto blocks = [&](int rows) { return ceil_div(static_cast<int64_t>(rows) * (d_model / 4), 256); };
+  ReduceArgs r = {};
+  r.dim = d_model;
+  if (dH && plan.ksplit > 1)
+    r.of[0] = {dh_sum, plan.ksplit, n_rows, static_cast<int>(sum_rows(n_rows)), dH, lddh, blocks(n_rows)};
+  if (dW && plan.wsplit > 1)
+    r.of[1] = {dw_sum, plan.wsplit, vocab, static_cast<int>(sum_rows(vocab)), dW, lddw, blocks(vocab)};
+  const int all = r.of[0].blocks + r.of[1].blocks;
+  if (all == 0) return TWELL_OK;
   LaunchScope scope(TWELL_KERNEL_LINEAR_LOGPROBS_BWD, s);
-  return launch_pdl(linear_reduce_kernel, dim3(ceil_div(static_cast<int64_t>(n_rows) * (d_model / 4), 256)), dim3(256),
-                    0, s, r) == cudaSuccess
-             ? TWELL_OK
-             : TWELL_ERR_CUDA;
+  return launch_pdl(linear_reduce_kernel, dim3(all), dim3(256), 0, s, r) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }

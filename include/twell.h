@@ -582,7 +582,8 @@ TWELL_API size_t twell_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t d
  * 16384 p is off by more than its rounding to bf16.  With n_rows == 0 dW is set to zero.
  * workspace: >= twell_linear_logprobs_bwd_workspace_bytes(...), 256-byte aligned, needs no
  * initialisation: two pieces of G (128 MB each, or 4096 columns where rows are many) and dH in
- * fp32, much less where one piece is enough.  status as above.  Nothing is written over H or W. */
+ * fp32; where one piece is enough much less, and dW in fp32 for ranges of the rows.  status as above.
+ * Nothing is written over H or W. */
 TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw,
                                         int32_t n_rows, int32_t d_model, int32_t vocab, const int32_t* targets,
                                         float inv_temperature, const float* lse, const float* entropy,

@@ -216,6 +216,21 @@ def test_backward_in_pieces(tw, n, d, v):
     check_backward(h, w, t, 1.0, lse, ent, g, ge, dh, dw)
 
 
+@pytest.mark.parametrize("want", [dict(), dict(want_h=False), dict(want_w=False), dict(pad=8)])
+@pytest.mark.parametrize("n,d,v", [(1100, 264, 130), (2100, 72, 300), (1025, 520, 1000), (9080, 376, 232), (12000, 128, 1),
+                                   (4097, 8, 257)])
+def test_backward_of_many_rows_and_few_tokens(tw, n, d, v, want):
+    """dW's product runs over the rows, cut into ranges where its tiles are few."""
+    h, w, t = make(n, d, v, n + v)
+    lp, ent, lse = forward(tw, h, w, t, 1.0)
+    g, ge = gradient_inputs(n, 44)
+    dh, dw, call = backward(tw, h, w, t, 1.0, lse, ent, g, ge, **want)
+    check_backward(h, w, t, 1.0, lse, ent, g, ge, dh, dw)
+    first = [m.clone() for m in (dh, dw) if m is not None]
+    call()
+    assert all(torch.equal(a, b) for a, b in zip(first, [m for m in (dh, dw) if m is not None]))
+
+
 @pytest.mark.parametrize("given", ["logprob", "entropy", "hidden", "weight", "slices"])
 def test_backward_of_some(tw, given):
     pad = 40 if given == "slices" else 0
