@@ -21,6 +21,9 @@
 // rows' sums), which halves what shared memory feeds to the tensor cores; up to 128 rows there is
 // nothing for a second CTA, and a CTA takes 128 x 256 alone.
 //
+// Few tiles are cut along K, so that all CTAs have work: dH's and dW's with fp32 sums that linear_reduce_kernel adds, the
+// logits' with linear_ranges_kernel.
+//
 // The tensor cores cut off what does not fit when they add, one step in 16 products, so a
 // logit of d = 4096 would come out 4e-6 too near to zero.  The forward pass, whose results are
 // fp32, adds up runs of 512 products in registers instead (all at once: off by four times as much, 2 % faster), rounding to nearest, while the next run is multiplied.
@@ -43,6 +46,8 @@ constexpr uint32_t kSumBytes = kSlots * 128 * sizeof(float4);
 constexpr uint32_t kBoxBytes = 32 * 128;                     // backward: a box of 32 rows on its way out,
 constexpr uint32_t kOutBytes = kEpiWarps * 2 * kBoxBytes;    // two a warp
 constexpr uint32_t kMaxShared = 232448;
+// What a launch does: the forward pass's tiles, logits of ranges of K (see linear_ranges_kernel), the backward pass's jobs.
+enum Mode { kSums, kRanges, kJobs };
 // R CTAs to a tile; SUMS: the forward pass.  As many stages as there is room for.
 template <int R, bool SUMS>
 struct Cfg {
@@ -58,6 +63,8 @@ constexpr int kPlanSms = 152;            // plans do not depend on the device, w
 constexpr int64_t kPieceBytes = 1 << 27; // of G: what the L2 cache can hold
 constexpr int kMinPiece = 4096;          // columns; dH's sums are read and written once a piece
 constexpr int kMaxKSplit = 32;
+constexpr int kRangeSteps = kRun, kRangesSave = 12;  // of K: see logit_ranges
+constexpr int kJoinCols = 64;                // of ranges that are added by a CTA
 constexpr int kTileSteps = 5;            // of K, that a tile takes at least: until its results have left
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
@@ -88,8 +95,9 @@ struct Args {
   const int32_t* targets;
   float inv_t;
   // forward
-  float4* part;       // [n_rows][num_n]: m, S, U
+  float4* part;       // [n_rows][parts of the columns]: m, S, U
   float* of_target;   // [n_rows] x of the target
+  float* ranges;      // [ksplit][num_m][num_n][kBN][rows of a tile]: logits of ranges of K, unscaled
   // backward
   const float *lse, *entropy, *g, *ge;
   const float* dh_sum;  // [ksplit][rows, up to whole tiles][d_model]
@@ -343,6 +351,16 @@ __device__ __forceinline__ bool epilogue_sums(const Args& a, const Job& j, const
   return true;
 }
 
+// A range's logits, columns by rows: a warp's stores are whole lines.  at: of this thread's row and its first column.
+__device__ __forceinline__ void store_range(float* at, int pitch, int left, const Half& x) {
+#pragma unroll
+  for (int i = 0; i < kBN / 4; ++i) {
+    const float2 f = lanes(x.v[i]);
+    if (2 * i < left) at[2 * i * pitch] = f.x;
+    if (2 * i + 1 < left) at[(2 * i + 1) * pitch] = f.y;
+  }
+}
+
 // Results leave through shared memory by TMA, a box of 32 rows of 128 bytes a time, so that memory gets whole
 // lines and edges are cut by the copy (a row's 64 bytes from each thread are half sectors, 16 bytes at
 // a time).  Two boxes a warp: one is filled while the other is read.
@@ -377,27 +395,42 @@ struct Box {
   }
 };
 
+// What G needs of a row.
+struct GradRow {
+  F2 inv_t, minus_lse, a0, a1;
+  float g;
+  int target;
+  __device__ __forceinline__ GradRow(const Args& a, int row, bool valid) {
+    float lse = 0.0f, f0 = 0.0f, f1 = 0.0f;
+    g = 0.0f, target = -1;
+    if (valid) {
+      lse = a.lse[row];
+      if (a.targets) {
+        target = a.targets[row];
+        if (target >= 0 && target < a.vocab) g = a.inv_t * a.g[row];
+      }
+      f0 = -g;
+      if (a.ge) {
+        f1 = -a.inv_t * a.ge[row];
+        f0 = fmaf(f1, a.entropy[row], f0);
+      }
+      if (lse == -INFINITY) lse = 0.0f, f0 = 0.0f, f1 = 0.0f, g = 0.0f;  // a row of -inf only: zeros
+    }
+    inv_t = pair(a.inv_t, a.inv_t), minus_lse = pair(-lse, -lse), a0 = pair(f0, f0), a1 = pair(f1, f1);
+  }
+  // G of two logits, without the target's part
+  __device__ __forceinline__ float2 of(F2 logits) const {
+    const F2 x = fma2(logits, inv_t, minus_lse);
+    const float2 y = lanes(mul2(x, pair(kLog2e, kLog2e))), xs = lanes(x);
+    return lanes(mul2(pair(ex2(y.x), ex2(y.y)), fma2(a1, pair(fmaxf(xs.x, -1e30f), fmaxf(xs.y, -1e30f)), a0)));
+  }
+};
+
 // G of the tile as bf16.
 __device__ __forceinline__ void epilogue_grad(const Args& a, const Job& j, const Tile& t, const CUtensorMap* map,
                                               Box& out) {
   const int lane = threadIdx.x & 31;
-  float lse = 0.0f, a0 = 0.0f, a1 = 0.0f, g = 0.0f;
-  int target = -1;
-  if (t.valid) {
-    lse = a.lse[t.row];
-    if (a.targets) {
-      target = a.targets[t.row];
-      if (target >= 0 && target < a.vocab) g = a.inv_t * a.g[t.row];
-    }
-    a0 = -g;
-    if (a.ge) {
-      a1 = -a.inv_t * a.ge[t.row];
-      a0 = fmaf(a1, a.entropy[t.row], a0);
-    }
-    if (lse == -INFINITY) lse = 0.0f, a0 = 0.0f, a1 = 0.0f, g = 0.0f;  // a row of -inf only: zeros
-  }
-  const F2 inv_t2 = pair(a.inv_t, a.inv_t), minus = pair(-lse, -lse), log2e = pair(kLog2e, kLog2e);
-  const F2 a02 = pair(a0, a0), a12 = pair(a1, a1);
+  const GradRow row(a, t.row, t.valid);
   const int from = t.half * (kBN / 2);
 #pragma unroll 1
   for (int k = from; k < from + kBN / 2; k += 64) {
@@ -409,17 +442,13 @@ __device__ __forceinline__ void epilogue_grad(const Args& a, const Job& j, const
       uint32_t r[32];
       tmem_ld32(t.taddr + k + 32 * h, r);
       tmem_ld_wait();
-      const int own = target - j.col0 - col - 32 * h;
+      const int own = row.target - j.col0 - col - 32 * h;
       const bool here = __any_sync(0xffffffffu, own >= 0 && own < 32);
       uint32_t w[16];
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
-        const F2 x = fma2(pair(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), inv_t2, minus);
-        const float2 y = lanes(mul2(x, log2e)), xs = lanes(x);
-        const F2 q = mul2(pair(ex2(y.x), ex2(y.y)),
-                          fma2(a12, pair(fmaxf(xs.x, -1e30f), fmaxf(xs.y, -1e30f)), a02));
-        float2 f = lanes(q);
-        if (here) f.x += own == i ? g : 0.0f, f.y += own == i + 1 ? g : 0.0f;
+        float2 f = row.of(pair(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
+        if (here) f.x += own == i ? row.g : 0.0f, f.y += own == i + 1 ? row.g : 0.0f;
         w[i / 2] = bf16_pair(f.x, f.y);
       }
 #pragma unroll
@@ -526,13 +555,14 @@ struct Walk {
   }
 };
 
-// R CTAs a tile; SUMS: the forward pass (its one job), else the jobs of the backward pass.
-template <int R, bool SUMS>
+// R CTAs a tile; kSums, kRanges: one job.
+template <int R, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
   grid_dependency_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr bool SUMS = MODE != kJobs;
   using C = Cfg<R, SUMS>;
   constexpr int S = C::kStages;
   uint8_t* const sA = smem;
@@ -566,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort = 0;
     mbar_fence_init();
   }
-  if (SUMS)  // no tile has been there yet
+  if (MODE == kSums)  // no tile has been there yet
     for (int i = threadIdx.x; i < kSlots * 128; i += kThreads) reinterpret_cast<float4*>(extra)[i].w = __int_as_float(0);
   if (warp == 0 && lane < 2 * a.num_jobs) tma_prefetch_desc(lane & 1 ? &maps.b[lane >> 1] : &maps.a[lane >> 1]);
   __syncwarp();
@@ -722,12 +752,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (SUMS) {
         Half sums = {};
 #pragma unroll 1
-        for (int k = 0; k < j.num_k; k += kRun) {
+        for (int k = MODE == kSums ? 0 : x.kb0; k < (MODE == kSums ? j.num_k : x.kb1); k += kRun) {
           if (!wait_full()) break;
           add_run(sums, t.taddr + t.half * (kBN / 2));
           release();
         }
         if (!ok) break;
+        if constexpr (MODE == kRanges) {
+          constexpr int kRows = kBM * R;
+          const int64_t tile = (static_cast<int64_t>(x.ks) * j.num_m + x.m_blk) * j.num_n + x.n_blk;
+          const int col = t.half * (kBN / 2);
+          if (t.row - lane < j.m)  // else the warp's rows are all past the end
+            store_range(a.ranges + (tile * kBN + col) * kRows + t.row - x.m_blk * kRows, kRows, j.n - t.col0 - col, sums);
+          continue;
+        }
         ok = __all_sync(0xffffffffu, epilogue_sums(a, j, t, x.n_blk, sums, reinterpret_cast<float4*>(extra), ++turn, abort));
         if (!ok) report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
       } else {
@@ -748,6 +786,76 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) {
     tc_fence_after();
     Tc<R>::dealloc(tmem_base);
+  }
+}
+
+// Where the tiles are few, each is multiplied in ranges of K by several CTAs, and this adds a tile's ranges in order, four on
+// the way at a time (one after the other with 32 columns a thread: 10 x 3640 x 500 in 17 us, not 13), 32 rows (a lane
+// each) and kJoinCols columns a CTA: their sums for the join as the forward epilogue leaves a tile's, or (GRAD) G.
+template <bool GRAD>
+__global__ void __launch_bounds__(256) linear_ranges_kernel(const __grid_constant__ Args a, uint16_t* G, int64_t ldg) {
+  grid_dependency_wait();
+  constexpr int C = kJoinCols / 8;  // columns a thread
+  __shared__ float s[3][8][32];
+  const Job& j = a.job[0];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int parts = (j.n + kJoinCols - 1) / kJoinCols;
+  const int block = blockIdx.x % parts, row0 = blockIdx.x / parts * 32, row = row0 + lane;
+  const int tile_rows = j.sum_rows, m_blk = row0 / tile_rows;
+  const int col = block * kJoinCols + warp * C, left = min(j.n - col, C);
+  const float* const at = a.ranges + (static_cast<int64_t>(m_blk) * j.num_n * kBN + col) * tile_rows + row - m_blk * tile_rows;
+  const int64_t plane = static_cast<int64_t>(j.num_m) * j.num_n * kBN * tile_rows;
+  float x[C] = {};
+#pragma unroll 1
+  for (int k = 0; k < j.ksplit; k += 4) {
+    float r[4][C];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int i = 0; i < C; ++i) r[e][i] = k + e < j.ksplit && i < left ? at[(k + e) * plane + i * tile_rows] : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int i = 0; i < C; ++i) x[i] += r[e][i];
+  }
+  const bool valid = row < j.m;
+  if constexpr (GRAD) {
+    if (!valid || left <= 0) return;
+    const GradRow of(a, row, valid);
+    const int own = of.target - col;
+    uint32_t w[C / 2];
+#pragma unroll
+    for (int i = 0; i < C; i += 2) {
+      float2 f = of.of(pair(x[i], x[i + 1]));
+      f.x += own == i ? of.g : 0.0f, f.y += own == i + 1 ? of.g : 0.0f;
+      w[i / 2] = bf16_pair(f.x, f.y);
+    }
+    static_assert(C == 8, "16 bytes");
+    *reinterpret_cast<uint4*>(G + row * ldg + col) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    const int target = valid && a.targets ? a.targets[row] - col : -1;
+    if (target >= 0 && target < left) {
+      float own = 0.0f;
+      for (int k = 0; k < j.ksplit; ++k) own += at[k * plane + target * tile_rows];
+      a.of_target[row] = own * a.inv_t;
+    }
+    const float c = a.inv_t * kLog2e;
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < C; ++i) top = i < left ? fmaxf(top, x[i]) : top;
+    Sums all;
+    all.m = top * c;
+    const float ref = all.m == -INFINITY ? 0.0f : all.m;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const float y = i < left ? fmaf(x[i], c, -ref) : -INFINITY, e = ex2(y);
+      all.s += e, all.u = fmaf(e, fmaxf(y, -1e30f), all.u);
+    }
+    s[0][warp][lane] = all.m, s[1][warp][lane] = all.s, s[2][warp][lane] = all.u;
+    __syncthreads();
+    if (warp > 0 || !valid) return;
+    for (int k = 1; k < 8; ++k) all.join(s[0][k][lane], s[1][k][lane], s[2][k][lane]);
+    a.part[static_cast<int64_t>(row) * parts + block] = make_float4(all.m, all.s, all.u, 0.0f);
   }
 }
 
@@ -838,11 +946,28 @@ int ctas_of(int64_t n_rows) { return n_rows > kBM ? 2 : 1; }
 // Rows of a gradient's fp32 sums: whole tiles, as a tile leaves whole.
 int64_t sum_rows(int64_t rows) { return (rows + 255) / 256 * 256; }
 
+// Ranges of K that logits are multiplied in, where the tiles leave CTAs (or pairs) without one: a CTA's copies bound a step
+// (0.4 us), whatever the others do.  Adding the ranges costs a launch and their way through memory, about what 12 steps and
+// one for each MB take.  10 x 3640 x 500 in 31 us alone, 13 in ranges; 16 x 4096 x 8192 30 and 22, 4096 x 8192 x 256 46 and 32;
+// below the limit 1000 x 1024 x 1000 13 and 17, 2000 x 4096 x 1000 (at it) 28 and 29.
+int logit_ranges(int64_t n_rows, int64_t d, int64_t vocab) {
+  const int ctas = ctas_of(n_rows);
+  const int64_t tiles = ceil_div(n_rows, kBM * ctas) * static_cast<int64_t>(ceil_div(vocab, kBN)), num_k = ceil_div(d, kBK);
+  const int64_t n = std::min<int64_t>(kPlanSms / ctas / std::max<int64_t>(tiles, 1), num_k / kRangeSteps);
+  const int64_t written = n * ((n_rows + 31) / 32 * 32) * vocab * 4;
+  return n >= 2 && num_k - ceil_div(num_k, n) >= kRangesSave + (written >> 20) ? static_cast<int>(n) : 1;
+}
+size_t ranges_bytes(int64_t n_rows, int64_t d, int64_t vocab) {
+  const int n = logit_ranges(n_rows, d, vocab);
+  return n == 1 ? 0 : static_cast<size_t>(n) * sum_rows(n_rows) * ceil_div(vocab, kBN) * kBN * 4;
+}
+
 // How a backward call is cut.
 struct Plan {
   int pieces, piece;  // columns of a piece, a multiple of 256
   int ksplit;         // ranges of the vocabulary in dH's product of a piece
   int wsplit;         // ranges of the rows in dW's product
+  int ranges;         // of K in G's
   size_t grad_bytes, sum_bytes, wsum_bytes, bytes;
 };
 
@@ -869,12 +994,22 @@ Plan plan_bwd(int64_t n_rows, int64_t d, int64_t vocab) {
                           : static_cast<int>(std::max<int64_t>(
                                 1, std::min<int64_t>({kMaxKSplit, ceil_div(n_rows, kBK) / 8, kPlanSms / ctas / wtiles})));
   p.wsum_bytes = p.wsplit > 1 ? round_up(static_cast<size_t>(p.wsplit) * sum_rows(vocab) * d * 4, 256) : 0;
-  p.bytes = p.grad_bytes * (p.pieces > 1 ? 2 : 1) + p.sum_bytes + p.wsum_bytes + 256;
+  // G's logits in ranges lie where the products' sums come afterwards
+  p.ranges = p.pieces > 1 ? 1 : logit_ranges(n_rows, d, vocab);
+  const size_t ranged = p.ranges > 1 ? ranges_bytes(n_rows, d, vocab) : 0;
+  p.bytes = p.grad_bytes * (p.pieces > 1 ? 2 : 1) + std::max(p.sum_bytes + p.wsum_bytes, ranged) + 256;
   return p;
 }
 
-size_t fwd_bytes(int64_t n_rows, int64_t vocab) {
-  return round_up(static_cast<size_t>(n_rows) * 4 * (4 * ceil_div(vocab, kBN) + 1), 256) + 512;
+// Parts of the columns that the forward pass leaves sums of.
+int parts_of(int64_t n_rows, int64_t d, int64_t vocab) {
+  return ceil_div(vocab, logit_ranges(n_rows, d, vocab) > 1 ? kJoinCols : kBN);
+}
+size_t part_bytes(int64_t n_rows, int parts) {
+  return round_up(static_cast<size_t>(n_rows) * 4 * (4 * static_cast<size_t>(parts) + 1), 256) + 512;
+}
+size_t fwd_bytes(int64_t n_rows, int64_t d, int64_t vocab) {
+  return part_bytes(n_rows, parts_of(n_rows, d, vocab)) + ranges_bytes(n_rows, d, vocab);
 }
 
 // CTAs (or pairs) that work at a time.
@@ -917,9 +1052,10 @@ int deal(Args* args, int slots) {
   return all;
 }
 
-template <int R, bool SUMS>
-int launch_jobs(const Maps& maps, Args args, cudaStream_t s) {
-  const auto kernel = linear_kernel<R, SUMS>;
+template <int R, Mode MODE>
+int launch_jobs(const Maps& maps, Args args, int id, cudaStream_t s) {
+  constexpr bool SUMS = MODE != kJobs;
+  const auto kernel = linear_kernel<R, MODE>;
   KV_TRY(set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(Cfg<R, SUMS>::kShared)));
   const int all = deal(&args, slots_of(R));
   cudaLaunchConfig_t cfg = {};
@@ -935,8 +1071,24 @@ int launch_jobs(const Maps& maps, Args args, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  LaunchScope scope(SUMS ? TWELL_KERNEL_LINEAR_LOGPROBS : TWELL_KERNEL_LINEAR_LOGPROBS_BWD, s);
+  LaunchScope scope(id, s);
   return cudaLaunchKernelEx(&cfg, kernel, maps, args) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+}
+
+template <Mode MODE>
+int launch_jobs(int ctas, const Maps& maps, const Args& args, int id, cudaStream_t s) {
+  return ctas == 2 ? launch_jobs<2, MODE>(maps, args, id, s) : launch_jobs<1, MODE>(maps, args, id, s);
+}
+
+// Logits in ranges of K, and from them the tiles' sums or G.
+template <bool GRAD>
+int launch_ranges(int ctas, const Maps& maps, const Args& args, uint16_t* G, int64_t ldg, int id, cudaStream_t s) {
+  KV_TRY(launch_jobs<kRanges>(ctas, maps, args, id, s));
+  LaunchScope scope(id, s);
+  return launch_pdl(linear_ranges_kernel<GRAD>, dim3(ceil_div(args.job[0].n, kJoinCols) * ceil_div(args.n_rows, 32)), dim3(256), 0, s, args,
+                    G, ldg) == cudaSuccess
+             ? TWELL_OK
+             : TWELL_ERR_CUDA;
 }
 
 int check_linear(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw, int n_rows, int d, int vocab,
@@ -964,7 +1116,7 @@ using namespace twell;
 
 extern "C" TWELL_API size_t twell_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t d_model, int32_t vocab) {
   if (n_rows < 0 || d_model < 8 || d_model % 8 != 0 || vocab < 1 || std::max({n_rows, d_model, vocab}) > kMaxSize) return 0;
-  return fwd_bytes(n_rows, vocab);
+  return fwd_bytes(n_rows, d_model, vocab);
 }
 
 namespace {
@@ -978,7 +1130,7 @@ int linear_logprobs(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t l
   if (n_rows > 0) {
     if (!targets != !logprob) return TWELL_ERR_INVALID_ARG;
     KV_TRY(check_vectors({targets, logprob, entropy, lse}));
-    if (!workspace || workspace_bytes < fwd_bytes(n_rows, vocab)) return TWELL_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < fwd_bytes(n_rows, d_model, vocab)) return TWELL_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return TWELL_ERR_MISALIGNED;
   }
   if (!device_is_sm103()) return TWELL_ERR_NO_DEVICE;
@@ -990,11 +1142,16 @@ int linear_logprobs(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t l
   a.of_target = static_cast<float*>(workspace);
   a.part = reinterpret_cast<float4*>(static_cast<uint8_t*>(workspace) + round_up(static_cast<size_t>(n_rows) * 4, 256));
   Job j = {};
-  j.type = kJobSums, j.band = kBandWide, j.m = n_rows, j.n = vocab, j.ksplit = 1;
-  const int ctas = ctas_of(n_rows);
+  j.type = kJobSums, j.band = kBandWide, j.m = n_rows, j.n = vocab;
+  const int ctas = ctas_of(n_rows), parts = parts_of(n_rows, d_model, vocab);
+  j.ksplit = logit_ranges(n_rows, d_model, vocab), j.sum_rows = kBM * ctas;
+  a.ranges = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + part_bytes(n_rows, parts));
   KV_TRY(set_job(&maps, &a, ctas, j, H, ldh, W, ldw, d_model));
-  KV_TRY((ctas == 2 ? launch_jobs<2, true>(maps, a, s) : launch_jobs<1, true>(maps, a, s)));
-  const JoinArgs join{a.part, a.of_target, a.job[0].num_n, n_rows, vocab, targets, logprob, entropy, lse};
+  if (j.ksplit > 1)
+    KV_TRY(launch_ranges<false>(ctas, maps, a, nullptr, 0, TWELL_KERNEL_LINEAR_LOGPROBS, s));
+  else
+    KV_TRY(launch_jobs<kSums>(ctas, maps, a, TWELL_KERNEL_LINEAR_LOGPROBS, s));
+  const JoinArgs join{a.part, a.of_target, parts, n_rows, vocab, targets, logprob, entropy, lse};
   LaunchScope scope(TWELL_KERNEL_LINEAR_LOGPROBS, s);
   return launch_pdl(linear_join_kernel, dim3(std::min(n_rows, 24 * sm_count())), dim3(32), 0, s, join) == cudaSuccess
              ? TWELL_OK
@@ -1105,13 +1262,17 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
     if (p < plan.pieces) {  // G of piece p
       const int col0 = p * plan.piece;
       Job j = {};
-      j.type = kJobGrad, j.band = kBandWide, j.m = n_rows, j.n = std::min(plan.piece, vocab - col0), j.ksplit = 1;
-      j.col0 = col0;
+      j.type = kJobGrad, j.band = kBandWide, j.m = n_rows, j.n = std::min(plan.piece, vocab - col0);
+      j.col0 = col0, j.ksplit = plan.ranges, j.sum_rows = kBM * ctas;
+      a.ranges = dh_sum;
       KV_TRY(encode_tmap_2d(&maps.out[a.num_jobs], buffer[p & 1], plan.piece, n_rows,
                             static_cast<uint64_t>(plan.piece) * 2, 64, 32));
       KV_TRY(set_job(&maps, &a, ctas, j, H, ldh, W + static_cast<int64_t>(col0) * ldw, ldw, d_model));
     }
-    KV_TRY((ctas == 2 ? launch_jobs<2, false>(maps, a, s) : launch_jobs<1, false>(maps, a, s)));
+    if (p == 0 && plan.ranges > 1)
+      KV_TRY(launch_ranges<true>(ctas, maps, a, buffer[0], plan.piece, TWELL_KERNEL_LINEAR_LOGPROBS_BWD, s));
+    else
+      KV_TRY(launch_jobs<kJobs>(ctas, maps, a, TWELL_KERNEL_LINEAR_LOGPROBS_BWD, s));
   }
   auto blocks = [&](int rows) { return ceil_div(static_cast<int64_t>(rows) * (d_model / 4), 256); };
   ReduceArgs r = {};

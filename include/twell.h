@@ -562,7 +562,7 @@ TWELL_API size_t twell_block_norm_bwd_workspace_bytes(int32_t n_rows, int32_t d_
  * A row with a NaN or an infinite logit gives NaN, a row of -inf only logprob -inf, entropy 0, lse -inf.
  * workspace: >= twell_linear_logprobs_workspace_bytes(...), 256-byte aligned, needs no initialisation.
  * status: device int32, zero at first: the first TWELL_ERR_* code a kernel met (an expired wait).
- * Two launches. */
+ * Two launches, or three where few tokens meet long rows. */
 TWELL_API int twell_linear_logprobs(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw, int32_t n_rows,
                                     int32_t d_model, int32_t vocab, const int32_t* targets, float inv_temperature,
                                     float* logprob, float* entropy, float* lse, void* workspace,

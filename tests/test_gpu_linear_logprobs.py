@@ -365,6 +365,66 @@ def test_gradient_against_differences(tw):
         assert abs(float((got.double() * way).sum()) - numeric) <= 2.0 ** -7 * scale + 1e-6 * abs(numeric)
 
 
+# few tiles and long rows: the logits are multiplied in ranges of K
+RANGES = [(10, 3640, 500), (1, 4016, 1210), (33, 1600, 255), (128, 2048, 513), (129, 4096, 300), (300, 4096, 1001), (1, 16384, 1)]
+
+
+@pytest.mark.parametrize("pad", [0, 24])
+@pytest.mark.parametrize("n,d,v", RANGES)
+def test_few_tokens_and_long_rows(tw, n, d, v, pad):
+    h, w, t = make(n, d, v, n + v, pad=pad)
+    check_forward(tw, h, w, t, 1.3)
+    lp, ent, lse = forward(tw, h, w, t, 1.3)
+    again = forward(tw, h, w, t, 1.3)
+    assert all(torch.equal(a, b) for a, b in zip(again, (lp, ent, lse)))
+    g, ge = gradient_inputs(n, 24)
+    dh, dw, call = backward(tw, h, w, t, 1.3, lse, ent, g, ge, pad=pad)
+    check_backward(h, w, t, 1.3, lse, ent, g, ge, dh, dw)
+    first = (dh.clone(), dw.clone())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(stream=None)
+    dh.fill_(float("nan"))
+    dw.fill_(float("nan"))
+    graph.replay()
+    assert torch.equal(dh, first[0]) and torch.equal(dw, first[1])
+
+
+def test_long_rows_with_nan_infinity_or_nothing(tw):
+    h, w, t = make(40, 2048, 700, 25)
+    clean = forward(tw, h, w, t, 1.0)
+    h[3, 5], h[9, 2000], h[20, 1024] = float("nan"), float("inf"), float("-inf")
+    got = forward(tw, h, w, t, 1.0)
+    bad = [3, 9, 20]
+    keep = [i for i in range(40) if i not in bad]
+    for a, b in zip(got, clean):
+        assert torch.equal(a[keep], b[keep])
+    assert got[1][bad].isnan().all() and got[2][bad].isnan().all()
+    w2 = torch.zeros((300, 2048), dtype=torch.bfloat16, device="cuda")
+    w2[:, 1000] = float("-inf")
+    h2 = torch.ones((2, 2048), dtype=torch.bfloat16, device="cuda")
+    lp, ent, lse = forward(tw, h2, w2, torch.tensor([4, -1], dtype=torch.int32, device="cuda"), 1.0)
+    assert lse.tolist() == [float("-inf")] * 2 and ent.tolist() == [0.0, 0.0] and lp.tolist() == [float("-inf"), 0.0]
+    w2[290] = 0
+    lp, ent, lse = forward(tw, h2, w2, torch.tensor([290, 4], dtype=torch.int32, device="cuda"), 1.0)
+    assert lse.tolist() == [0.0, 0.0] and ent.tolist() == [0.0, 0.0] and lp.tolist() == [0.0, float("-inf")]
+
+
+@pytest.mark.parametrize("n", [40, 300])
+def test_an_expired_wait_of_ranges_is_reported(tw, n):
+    d, v = 4096, 500
+    h, w, t = make(n, d, v, 26)
+    ws = torch.empty(tw.linear_logprobs_workspace_bytes(n, d, v), dtype=torch.uint8, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rc = tw.load_library().twell_selftest_linear_stall(h.data_ptr(), d, w.data_ptr(), d, n, d, v, ws.data_ptr(),
+                                                       ws.numel(), st.data_ptr(), 1_000_000,
+                                                       torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    torch.cuda.synchronize()
+    assert int(st) == -7
+    check_forward(tw, h, w, t, 1.0)
+
+
 @pytest.mark.parametrize("n", [40, 300])  # a CTA to a tile, and a pair
 def test_an_expired_wait_is_reported(tw, n):
     """Every stage waits for an arrival that never comes: the call ends, says so, and the next one is sound."""
