@@ -943,8 +943,15 @@ size_t round_up(size_t x, size_t to) { return (x + to - 1) / to * to; }
 // CTAs to a tile: a pair from 129 rows on.
 int ctas_of(int64_t n_rows) { return n_rows > kBM ? 2 : 1; }
 
-// Rows of a gradient's fp32 sums: whole tiles, as a tile leaves whole.
-int64_t sum_rows(int64_t rows) { return (rows + 255) / 256 * 256; }
+// Rows of fp32 sums: whole tiles, as a tile leaves whole.
+int64_t sum_rows(int64_t rows, int ctas) { return (rows + kBM * ctas - 1) / (kBM * ctas) * (kBM * ctas); }
+
+// What ranges of a product's K may take at most, whatever rows there are up to these: there are never more tiles than CTAs.
+size_t split_bytes(int64_t ranges, int64_t rows, int64_t cols) {
+  constexpr int64_t kMost = static_cast<int64_t>(kPlanSms) * kBM * kBN;
+  const int64_t area = (rows + 255) / 256 * 256 * cols;
+  return ranges < 2 ? 0 : round_up(static_cast<size_t>(area > kMost / ranges ? kMost : ranges * area) * 4, 256);
+}
 
 // Ranges of K that logits are multiplied in, where the tiles leave CTAs (or pairs) without one: a CTA's copies bound a step
 // (0.4 us), whatever the others do.  Adding the ranges costs a launch and their way through memory, about what 12 steps and
@@ -959,7 +966,7 @@ int logit_ranges(int64_t n_rows, int64_t d, int64_t vocab) {
 }
 size_t ranges_bytes(int64_t n_rows, int64_t d, int64_t vocab) {
   const int n = logit_ranges(n_rows, d, vocab);
-  return n == 1 ? 0 : static_cast<size_t>(n) * sum_rows(n_rows) * ceil_div(vocab, kBN) * kBN * 4;
+  return n == 1 ? 0 : static_cast<size_t>(n) * sum_rows(n_rows, ctas_of(n_rows)) * ceil_div(vocab, kBN) * kBN * 4;
 }
 
 // How a backward call is cut.
@@ -986,19 +993,38 @@ Plan plan_bwd(int64_t n_rows, int64_t d, int64_t vocab) {
   p.ksplit = static_cast<int>(
       std::max<int64_t>(1, std::min<int64_t>({kMaxKSplit, num_k / 8, kPlanSms / ctas / std::max<int64_t>(1, tiles)})));
   p.grad_bytes = round_up(static_cast<size_t>(n_rows) * p.piece * 2, 256);
-  p.sum_bytes = p.pieces > 1 || p.ksplit > 1 ? round_up(static_cast<size_t>(p.ksplit) * sum_rows(n_rows) * d * 4, 256) : 0;
+  p.sum_bytes = p.pieces > 1 || p.ksplit > 1 ? round_up(static_cast<size_t>(p.ksplit) * sum_rows(n_rows, ctas) * d * 4, 256) : 0;
   // So is dW's, over many rows (9080 x 376 x 232: 63 -> 26 us, 11351 x 520 x 1245 90 -> 58); with several pieces it
   // has tiles enough.
   const int64_t wtiles = ceil_div(vocab, kBM * ctas) * static_cast<int64_t>(ceil_div(d, kBN));
   p.wsplit = p.pieces > 1 ? 1
                           : static_cast<int>(std::max<int64_t>(
                                 1, std::min<int64_t>({kMaxKSplit, ceil_div(n_rows, kBK) / 8, kPlanSms / ctas / wtiles})));
-  p.wsum_bytes = p.wsplit > 1 ? round_up(static_cast<size_t>(p.wsplit) * sum_rows(vocab) * d * 4, 256) : 0;
+  p.wsum_bytes = p.wsplit > 1 ? round_up(static_cast<size_t>(p.wsplit) * sum_rows(vocab, ctas) * d * 4, 256) : 0;
   // G's logits in ranges lie where the products' sums come afterwards
   p.ranges = p.pieces > 1 ? 1 : logit_ranges(n_rows, d, vocab);
   const size_t ranged = p.ranges > 1 ? ranges_bytes(n_rows, d, vocab) : 0;
   p.bytes = p.grad_bytes * (p.pieces > 1 ? 2 : 1) + std::max(p.sum_bytes + p.wsum_bytes, ranged) + 256;
   return p;
+}
+
+// Workspaces that are asked for hold what any fewer rows take, too: fewer rows have fewer tiles, which are cut into more ranges.
+size_t most_ranges_bytes(int64_t n_rows, int64_t d, int64_t vocab) {
+  return 2 * ceil_div(vocab, kBN) > kPlanSms
+             ? 0
+             : split_bytes(ceil_div(d, kBK) / kRangeSteps, n_rows, static_cast<int64_t>(ceil_div(vocab, kBN)) * kBN);
+}
+size_t most_bwd_bytes(int64_t n_rows, int64_t d, int64_t vocab) {
+  const Plan p = plan_bwd(n_rows, d, vocab);
+  // G: a piece is at most 255 columns wider than its limit
+  const size_t n = n_rows, rounded = 256 * n * 2;
+  const size_t grad = p.pieces == 1 ? p.grad_bytes
+                                    : 2 * round_up(std::max<size_t>(kPieceBytes, n * kMinPiece * 2) + rounded, 256);
+  const int64_t wtiles = ceil_div(vocab, 2 * kBM) * static_cast<int64_t>(ceil_div(d, kBN));
+  const size_t sum = std::max(p.pieces == 1 ? 0 : round_up(static_cast<size_t>(sum_rows(n_rows, 2)) * d * 4, 256),
+                              split_bytes(std::min(kMaxKSplit, ceil_div(vocab, kBK) / 8), n_rows, d));
+  const size_t wsum = 4 * wtiles > kPlanSms ? 0 : split_bytes(std::min(kMaxKSplit, ceil_div(n_rows, kBK) / 8), vocab, d);
+  return grad + std::max(sum + wsum, most_ranges_bytes(n_rows, d, vocab)) + 256;
 }
 
 // Parts of the columns that the forward pass leaves sums of.
@@ -1010,6 +1036,10 @@ size_t part_bytes(int64_t n_rows, int parts) {
 }
 size_t fwd_bytes(int64_t n_rows, int64_t d, int64_t vocab) {
   return part_bytes(n_rows, parts_of(n_rows, d, vocab)) + ranges_bytes(n_rows, d, vocab);
+}
+size_t most_fwd_bytes(int64_t n_rows, int64_t d, int64_t vocab) {
+  const size_t ranged = most_ranges_bytes(n_rows, d, vocab);
+  return part_bytes(n_rows, ceil_div(vocab, ranged > 0 ? kJoinCols : kBN)) + ranged;
 }
 
 // CTAs (or pairs) that work at a time.
@@ -1116,7 +1146,7 @@ using namespace twell;
 
 extern "C" TWELL_API size_t twell_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t d_model, int32_t vocab) {
   if (n_rows < 0 || d_model < 8 || d_model % 8 != 0 || vocab < 1 || std::max({n_rows, d_model, vocab}) > kMaxSize) return 0;
-  return fwd_bytes(n_rows, d_model, vocab);
+  return most_fwd_bytes(n_rows, d_model, vocab);
 }
 
 namespace {
@@ -1181,7 +1211,7 @@ extern "C" TWELL_API int twell_selftest_linear_stall(const uint16_t* H, int64_t 
 extern "C" TWELL_API size_t twell_linear_logprobs_bwd_workspace_bytes(int32_t n_rows, int32_t d_model,
                                                                       int32_t vocab) {
   if (n_rows < 0 || d_model < 8 || d_model % 8 != 0 || vocab < 1 || std::max({n_rows, d_model, vocab}) > kMaxSize) return 0;
-  return plan_bwd(n_rows, d_model, vocab).bytes;
+  return most_bwd_bytes(n_rows, d_model, vocab);
 }
 
 extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw,
@@ -1237,7 +1267,7 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
         j.type = kJobDHidden, j.m = n_rows, j.n = d_model, j.add = p > 1;
         j.round = p == plan.pieces && plan.ksplit == 1;
         // the first piece fills all ranges' sums; a narrower last one adds to no more than it has steps
-        j.ksplit = plan.ksplit, j.sum_rows = static_cast<int>(sum_rows(n_rows));
+        j.ksplit = plan.ksplit, j.sum_rows = static_cast<int>(sum_rows(n_rows, ctas));
         if (j.round)
           KV_TRY(encode_tmap_2d(&maps.out[a.num_jobs], dH, d_model, n_rows, lddh * 2, 64, 32));
         else
@@ -1248,7 +1278,7 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
       }
       if (dW) {
         j.type = kJobDWeight, j.m = width, j.n = d_model, j.a_mn = 1, j.add = 0;
-        j.round = plan.wsplit == 1, j.ksplit = plan.wsplit, j.sum_rows = static_cast<int>(sum_rows(vocab));
+        j.round = plan.wsplit == 1, j.ksplit = plan.wsplit, j.sum_rows = static_cast<int>(sum_rows(vocab, ctas));
         if (j.round)
           KV_TRY(encode_tmap_2d(&maps.out[a.num_jobs], dW + static_cast<int64_t>(col0) * lddw, d_model, width, lddw * 2,
                                 64, 32));
@@ -1278,9 +1308,9 @@ extern "C" TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ld
   ReduceArgs r = {};
   r.dim = d_model;
   if (dH && plan.ksplit > 1)
-    r.of[0] = {dh_sum, plan.ksplit, n_rows, static_cast<int>(sum_rows(n_rows)), dH, lddh, blocks(n_rows)};
+    r.of[0] = {dh_sum, plan.ksplit, n_rows, static_cast<int>(sum_rows(n_rows, ctas)), dH, lddh, blocks(n_rows)};
   if (dW && plan.wsplit > 1)
-    r.of[1] = {dw_sum, plan.wsplit, vocab, static_cast<int>(sum_rows(vocab)), dW, lddw, blocks(vocab)};
+    r.of[1] = {dw_sum, plan.wsplit, vocab, static_cast<int>(sum_rows(vocab, ctas)), dW, lddw, blocks(vocab)};
   const int all = r.of[0].blocks + r.of[1].blocks;
   if (all == 0) return TWELL_OK;
   LaunchScope scope(TWELL_KERNEL_LINEAR_LOGPROBS_BWD, s);

@@ -560,7 +560,8 @@ TWELL_API size_t twell_block_norm_bwd_workspace_bytes(int32_t n_rows, int32_t d_
  *   logprob x_target - lse; entropy; lse = log sum exp x: [n_rows] fp32, each may be null
  *           (targets and logprob together)
  * A row with a NaN or an infinite logit gives NaN, a row of -inf only logprob -inf, entropy 0, lse -inf.
- * workspace: >= twell_linear_logprobs_workspace_bytes(...), 256-byte aligned, needs no initialisation.
+ * workspace: >= twell_linear_logprobs_workspace_bytes(...), 256-byte aligned, needs no initialisation;
+ * one for n_rows holds what any fewer rows take.
  * status: device int32, zero at first: the first TWELL_ERR_* code a kernel met (an expired wait).
  * Two launches, or three where few tokens meet long rows. */
 TWELL_API int twell_linear_logprobs(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw, int32_t n_rows,
@@ -582,7 +583,8 @@ TWELL_API size_t twell_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t d
  * 16384 p is off by more than its rounding to bf16.  With n_rows == 0 dW is set to zero.
  * workspace: >= twell_linear_logprobs_bwd_workspace_bytes(...), 256-byte aligned, needs no
  * initialisation: two pieces of G (128 MB each, or 4096 columns where rows are many) and dH in
- * fp32; where one piece is enough much less, and dW in fp32 for ranges of the rows.  status as above.
+ * fp32; where one piece is enough much less, and dW in fp32 for ranges of the rows.  One for n_rows
+ * holds what any fewer rows take.  status as above.
  * Nothing is written over H or W. */
 TWELL_API int twell_linear_logprobs_bwd(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t ldw,
                                         int32_t n_rows, int32_t d_model, int32_t vocab, const int32_t* targets,

@@ -144,6 +144,29 @@ def test_linear_workspaces_are_host_arithmetic(tw):
             assert f(*bad) == 0
 
 
+def test_a_linear_workspace_holds_what_fewer_rows_take(tw, lib):
+    """With the bytes for n rows, calls of fewer rows get past the workspace's check (to that of the device, here without one)."""
+    import random
+
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the calls would go on to the GPU")
+    rng = random.Random(5)
+    size = lambda a, b: int(2 ** rng.uniform(a, b))  # noqa: E731
+    for _ in range(4000):
+        n, d, v = size(0, 17), 8 * size(0, 11), size(0, 18)
+        fewer = min(n, rng.choice([1, 128, 129, 256, 257, 1024, size(0, 17), n]))
+        shape = dict(n=fewer, d=d, vocab=v, ldh=d, ldw=d)
+        ws = tw.linear_logprobs_workspace_bytes(n, d, v)
+        assert lib.twell_linear_logprobs(*{**LIN, **shape, "ws_bytes": ws}.values()) == -8, (n, d, v, fewer)
+        ws = tw.linear_logprobs_bwd_workspace_bytes(n, d, v)
+        assert lib.twell_linear_logprobs_bwd(*{**LINB, **shape, "lddh": d, "lddw": d, "ws_bytes": ws}.values()) == -8, (
+            n, d, v, fewer)
+    # not much more than what n rows take themselves
+    assert tw.linear_logprobs_bwd_workspace_bytes(8192, 2048, 32768) < 400 << 20
+    assert tw.linear_logprobs_workspace_bytes(16, 4096, 131072) < 1 << 20
+
+
 def test_binding_of_the_linear_calls_checks(tw):
     import torch
     bf, i32 = torch.bfloat16, torch.int32
