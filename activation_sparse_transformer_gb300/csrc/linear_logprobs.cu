@@ -2,10 +2,12 @@
 // W [V][d] (twell_linear_logprobs) and their gradient (..._bwd): the logits
 // x = H W^T / T live in tensor memory only, a tile at a time.
 //
-// Forward: each 128 x 256 tile of x leaves a row's maximum m, S = sum 2^(y - m)
-// and U = sum 2^(y - m) (y - m) over the tile's columns, y = x log2(e); a second
-// kernel joins the tiles of a row:
-//   lse = ln2 (m + log2 S),  logprob = x_t - lse,  entropy = ln2 (log2 S - U / S).
+// Forward: with l = H W^T and d = (l - m) log2(e) / T, each 128 x 256 tile leaves a row's maximum m of l,
+// S = sum 2^d and U = sum 2^d d over the tile's columns; a second kernel joins the tiles of a row:
+//   lse = m / T + ln2 log2 S,  logprob = (l_t - m) / T - ln2 log2 S,  entropy = ln2 (log2 S - U / S).
+// m and l_t are kept as they were multiplied, and what is scaled is their distance: so neither the size of the
+// logits nor the ends of fp32 count, and as S >= 1 no log probability comes out above 0 (with x_t - lse
+// a token of all but 1e-9 of the mass came out off by 9e-7 at logits of 20 and 1e-5 at 400, a tenth of them above 0).
 // Backward, in pieces of the vocabulary: x again, from it
 //   G = (g (1[t] - p) - ge p (log p + entropy)) / T,  p = exp(x - lse),
 // as bf16 into the workspace (the tensor cores take bf16, and each entry is then
@@ -96,7 +98,7 @@ struct Args {
   float inv_t;
   // forward
   float4* part;       // [n_rows][parts of the columns]: m, S, U
-  float* of_target;   // [n_rows] x of the target
+  float* of_target;   // [n_rows] the target's logit, unscaled
   float* ranges;      // [ksplit][num_m][num_n][kBN][rows of a tile]: logits of ranges of K, unscaled
   // backward
   const float *lse, *entropy, *g, *ge;
@@ -242,18 +244,18 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return r;
 }
 
-// A row's running sums in base 2 relative to m (as y = acc c).
+// A row's running sums in base 2 relative to the unscaled logit m.
 struct Sums {
   float m = -INFINITY, s = 0.0f, u = 0.0f;
-  // joins sums that are relative to m2
-  __device__ __forceinline__ void join(float m2, float s2, float u2) {
+  // joins sums that are relative to m2; c scales logits to base 2
+  __device__ __forceinline__ void join(float m2, float s2, float u2, float c) {
     const float top = fmaxf(m, m2);
     if (top == -INFINITY) {  // neither has an entry above -inf: S is 0, or NaN where there was one
       s += s2, u += u2;
       return;
     }
     // a side without entries has S = U = 0 and m = -inf: its factor is 0, and so is its shift times S
-    const float d1 = fmaxf(m - top, -1e30f), d2 = fmaxf(m2 - top, -1e30f);
+    const float d1 = fmaxf((m - top) * c, -1e30f), d2 = fmaxf((m2 - top) * c, -1e30f);
     const float f1 = ex2(d1), f2 = ex2(d2);
     u = f1 * fmaf(d1, s, u) + f2 * fmaf(d2, s2, u2);
     s = f1 * s + f2 * s2;
@@ -309,19 +311,17 @@ __device__ __forceinline__ bool epilogue_sums(const Args& a, const Job& j, const
       asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %2, %3;\n\t@p mov.b64 %0, %1;\n\t}"
           : "+l"(own)
           : "l"(x.v[i]), "r"((target - col) / 2), "r"(i));
-    a.of_target[t.row] = ((target - col) & 1 ? lanes(own).y : lanes(own).x) * a.inv_t;
+    a.of_target[t.row] = (target - col) & 1 ? lanes(own).y : lanes(own).x;
   }
   Sums all;
-  float top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kBN / 4; ++i) top = fmaxf(top, fmaxf(lanes(x.v[i]).x, lanes(x.v[i]).y));
-  all.m = top * c;
+  for (int i = 0; i < kBN / 4; ++i) all.m = fmaxf(all.m, fmaxf(lanes(x.v[i]).x, lanes(x.v[i]).y));
   const float ref = all.m == -INFINITY ? 0.0f : all.m;
   const F2 c2 = pair(c, c), minus = pair(-ref, -ref);
   F2 s[2] = {0, 0}, u[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < kBN / 4; ++i) {
-    const float2 y = lanes(fma2(x.v[i], c2, minus));
+    const float2 y = lanes(mul2(add2(x.v[i], minus), c2));
     const F2 e = pair(ex2(y.x), ex2(y.y));
     s[i & 1] = add2(s[i & 1], e);
     u[i & 1] = fma2(e, pair(fmaxf(y.x, -1e30f), fmaxf(y.y, -1e30f)), u[i & 1]);  // 0 for an entry of -inf
@@ -346,7 +346,7 @@ __device__ __forceinline__ bool epilogue_sums(const Args& a, const Job& j, const
   }
   __threadfence_block();
   if (!t.valid) return true;
-  all.join(at[0], at[1], at[2]);
+  all.join(at[0], at[1], at[2], c);
   a.part[static_cast<int64_t>(t.row) * j.num_n + n_blk] = make_float4(all.m, all.s, all.u, 0.0f);
   return true;
 }
@@ -837,24 +837,22 @@ __global__ void __launch_bounds__(256) linear_ranges_kernel(const __grid_constan
     if (target >= 0 && target < left) {
       float own = 0.0f;
       for (int k = 0; k < j.ksplit; ++k) own += at[k * plane + target * tile_rows];
-      a.of_target[row] = own * a.inv_t;
+      a.of_target[row] = own;
     }
     const float c = a.inv_t * kLog2e;
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < C; ++i) top = i < left ? fmaxf(top, x[i]) : top;
     Sums all;
-    all.m = top * c;
+#pragma unroll
+    for (int i = 0; i < C; ++i) all.m = i < left ? fmaxf(all.m, x[i]) : all.m;
     const float ref = all.m == -INFINITY ? 0.0f : all.m;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const float y = i < left ? fmaf(x[i], c, -ref) : -INFINITY, e = ex2(y);
+      const float y = i < left ? (x[i] - ref) * c : -INFINITY, e = ex2(y);
       all.s += e, all.u = fmaf(e, fmaxf(y, -1e30f), all.u);
     }
     s[0][warp][lane] = all.m, s[1][warp][lane] = all.s, s[2][warp][lane] = all.u;
     __syncthreads();
     if (warp > 0 || !valid) return;
-    for (int k = 1; k < 8; ++k) all.join(s[0][k][lane], s[1][k][lane], s[2][k][lane]);
+    for (int k = 1; k < 8; ++k) all.join(s[0][k][lane], s[1][k][lane], s[2][k][lane], c);
     a.part[static_cast<int64_t>(row) * parts + block] = make_float4(all.m, all.s, all.u, 0.0f);
   }
 }
@@ -864,6 +862,7 @@ struct JoinArgs {
   const float* of_target;
   int num_n, n_rows, vocab;
   const int32_t* targets;
+  float inv_t;
   float *logprob, *entropy, *lse;
 };
 
@@ -871,13 +870,14 @@ struct JoinArgs {
 __global__ void __launch_bounds__(32) linear_join_kernel(const JoinArgs a) {
   grid_dependency_wait();
   const int lane = threadIdx.x;
+  const float c = a.inv_t * kLog2e;
   for (int row = blockIdx.x; row < a.n_rows; row += gridDim.x) {
     const float4* const at = a.part + static_cast<int64_t>(row) * a.num_n;
     Sums all;
 #pragma unroll 4
     for (int k = lane; k < a.num_n; k += 32) {
       const float4 p = at[k];
-      all.join(p.x, p.y, p.z);
+      all.join(p.x, p.y, p.z, c);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -887,17 +887,23 @@ __global__ void __launch_bounds__(32) linear_join_kernel(const JoinArgs a) {
       Sums low = all, high;
       high.m = m, high.s = s, high.u = u;
       if (lane & o) low = high, high = all;
-      low.join(high.m, high.s, high.u);
+      low.join(high.m, high.s, high.u, c);
       all = low;
     }
     if (lane > 0) continue;
-    const float log_s = log2f(all.s), lse = kLn2 * (all.m + log_s);
-    if (a.lse) a.lse[row] = lse;
+    // where the largest logit is finite and its scaled value is not, the row is as one of that value
+    const float top = a.inv_t * all.m;
+    if (top == INFINITY) all.s = __int_as_float(0x7FC00000);
+    if (top == -INFINITY && all.s >= 1.0f) all.s = 0.0f;
+    const float log_s = log2f(all.s);
+    if (a.lse) a.lse[row] = fmaf(a.inv_t, all.m, kLn2 * log_s);
     if (a.entropy) a.entropy[row] = all.s == 0.0f ? 0.0f : kLn2 * (log_s - all.u / all.s);
     if (a.logprob) {
       const int t = a.targets[row];
       // a row of -inf only: -inf, as all its log probabilities
-      a.logprob[row] = t < 0 || t >= a.vocab ? 0.0f : all.s == 0.0f ? -INFINITY : a.of_target[row] - lse;
+      a.logprob[row] = t < 0 || t >= a.vocab ? 0.0f
+                       : all.s == 0.0f       ? -INFINITY
+                                             : fmaf(a.inv_t, a.of_target[row] - all.m, -kLn2 * log_s);
     }
   }
 }
@@ -1181,7 +1187,7 @@ int linear_logprobs(const uint16_t* H, int64_t ldh, const uint16_t* W, int64_t l
     KV_TRY(launch_ranges<false>(ctas, maps, a, nullptr, 0, TWELL_KERNEL_LINEAR_LOGPROBS, s));
   else
     KV_TRY(launch_jobs<kSums>(ctas, maps, a, TWELL_KERNEL_LINEAR_LOGPROBS, s));
-  const JoinArgs join{a.part, a.of_target, parts, n_rows, vocab, targets, logprob, entropy, lse};
+  const JoinArgs join{a.part, a.of_target, parts, n_rows, vocab, targets, inv_temperature, logprob, entropy, lse};
   LaunchScope scope(TWELL_KERNEL_LINEAR_LOGPROBS, s);
   return launch_pdl(linear_join_kernel, dim3(std::min(n_rows, 24 * sm_count())), dim3(32), 0, s, join) == cudaSuccess
              ? TWELL_OK

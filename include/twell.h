@@ -558,8 +558,10 @@ TWELL_API size_t twell_block_norm_bwd_workspace_bytes(int32_t n_rows, int32_t d_
  *   H       [n_rows][d_model] bf16, W [vocab][d_model] bf16; d_model a multiple of 8
  *   targets [n_rows] int32; a target outside [0, vocab) is none: logprob 0
  *   logprob x_target - lse; entropy; lse = log sum exp x: [n_rows] fp32, each may be null
- *           (targets and logprob together)
- * A row with a NaN or an infinite logit gives NaN, a row of -inf only logprob -inf, entropy 0, lse -inf.
+ *           (targets and logprob together).  logprob is made from the row's sums, not from lse's
+ *           bits: it is as good at large logits as at small ones, and never above 0
+ * -inf is a masked token (p = 0).  A row with a NaN or +inf among its x gives NaN, a row of -inf only
+ * logprob -inf, entropy 0, lse -inf.
  * workspace: >= twell_linear_logprobs_workspace_bytes(...), 256-byte aligned, needs no initialisation;
  * one for n_rows holds what any fewer rows take.
  * status: device int32, zero at first: the first TWELL_ERR_* code a kernel met (an expired wait).
