@@ -27,8 +27,11 @@
 // logits' with linear_ranges_kernel.
 //
 // The tensor cores cut off what does not fit when they add, one step in 16 products, so a
-// logit of d = 4096 would come out 4e-6 too near to zero.  The forward pass, whose results are
-// fp32, adds up runs of 512 products in registers instead (all at once: off by four times as much, 2 % faster), rounding to nearest, while the next run is multiplied.
+// logit of d = 4096 would come out 4e-6 too near to zero.  Logits are therefore added up in registers in runs of
+// 512 products, rounding to nearest, while the next run is multiplied (forward 2 % slower than all at once, gradient 1 %,
+// with d = 128 3 %): by the forward pass, with or without ranges of K, and for G alike, so that p = exp(x - lse) is made
+// of the logits that lse was made of, bit for bit.  (With all of K at once p was too small by |x| 4e-6, which is all of
+// the 1 - p of a token at x = 20 that has all but 1e-4 of the mass.)
 #include <algorithm>
 
 #include "kv_internal.h"
@@ -40,7 +43,7 @@ namespace {
 // where they leave fewer CTAs idle in the last round (413 x 1032 x 50001: 192 columns 54 us, 128 73, 256 52).
 constexpr int kBM = 128, kBN = 256, kBK = 64, kUmmaK = 16;
 constexpr int kThreads = 384, kEpiWarps = 8;
-constexpr int kRun = 8;  // steps of K that the forward pass adds up in tensor memory
+constexpr int kRun = 8;  // steps of K that logits are added up over in tensor memory
 constexpr uint32_t kABytes = kBM * kBK * 2;
 constexpr uint32_t kBarBytes = 256;
 constexpr int kSlots = 4;                                    // forward: one half's sums, for the other half
@@ -130,6 +133,19 @@ __device__ __forceinline__ void cluster_sync() {
 }
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The gradient's epilogue holds a row's logits while it makes G of them: its warps take registers that the issuing ones have
+// no use for (without, they spill: gradient of 8192 x 1024 x 32768 1000 us, so 955; 8192 x 640 x 32768 842 and 738).
+constexpr int kRegsIssue = 88, kRegsEpilogue = 208;
+static_assert(4 * kRegsIssue + kEpiWarps * kRegsEpilogue == kThreads / 32 * 168, "the launch's registers");
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // The issuing warps stay converged and one elected lane issues: the operands then sit in uniform registers,
@@ -275,7 +291,8 @@ struct Half {
   F2 v[kBN / 4];
 };
 
-// Adds a run's sums to those of the runs before.
+// Adds a run's sums to those of the runs before, or (FIRST) takes them.
+template <bool FIRST = false>
 __device__ __forceinline__ void add_run(Half& x, uint32_t taddr) {
 #pragma unroll
   for (int k = 0; k < kBN / 2; k += 32) {
@@ -283,8 +300,10 @@ __device__ __forceinline__ void add_run(Half& x, uint32_t taddr) {
     tmem_ld32(taddr + k, r);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      x.v[k / 2 + i] = add2(x.v[k / 2 + i], pair(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
+    for (int i = 0; i < 16; ++i) {
+      const F2 v = pair(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+      x.v[k / 2 + i] = FIRST ? v : add2(x.v[k / 2 + i], v);
+    }
   }
 }
 
@@ -426,10 +445,41 @@ struct GradRow {
   }
 };
 
-// G of the tile as bf16.
+// G of the tile as bf16: 32 columns for a box that takes 64, from the logits v(0 .. 15), two a word.
+template <typename F>
+__device__ __forceinline__ void put_grad(const GradRow& row, int target, uint8_t* box, int h, F v) {
+  const int lane = threadIdx.x & 31;
+  const bool here = __any_sync(0xffffffffu, target >= 0 && target < 32);
+#pragma unroll
+  for (int q = 0; q < 32; q += 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = q; i < q + 8; i += 2) {
+      float2 f = row.of(v(i / 2));
+      if (here) f.x += target == i ? row.g : 0.0f, f.y += target == i + 1 ? row.g : 0.0f;
+      w[(i - q) / 2] = bf16_pair(f.x, f.y);
+    }
+    Box::put(box, lane, 4 * h + q / 8, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+}
+// from the sums of several runs
+__device__ __forceinline__ void epilogue_grad(const Args& a, const Job& j, const Tile& t, const Half& x,
+                                              const CUtensorMap* map, Box& out) {
+  const GradRow row(a, t.row, t.valid);
+#pragma unroll
+  for (int k = 0; k < kBN / 2; k += 64) {
+    const int col = t.col0 + t.half * (kBN / 2) + k;
+    if (col >= j.n) return;
+    uint8_t* const box = out.open();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      put_grad(row, row.target - j.col0 - col - 32 * h, box, h, [&](int i) { return x.v[(k + 32 * h) / 2 + i]; });
+    Box::send<false>(box, map, col, t.row - (threadIdx.x & 31));
+  }
+}
+// from tensor memory, where one run is all
 __device__ __forceinline__ void epilogue_grad(const Args& a, const Job& j, const Tile& t, const CUtensorMap* map,
                                               Box& out) {
-  const int lane = threadIdx.x & 31;
   const GradRow row(a, t.row, t.valid);
   const int from = t.half * (kBN / 2);
 #pragma unroll 1
@@ -442,20 +492,10 @@ __device__ __forceinline__ void epilogue_grad(const Args& a, const Job& j, const
       uint32_t r[32];
       tmem_ld32(t.taddr + k + 32 * h, r);
       tmem_ld_wait();
-      const int own = row.target - j.col0 - col - 32 * h;
-      const bool here = __any_sync(0xffffffffu, own >= 0 && own < 32);
-      uint32_t w[16];
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        float2 f = row.of(pair(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
-        if (here) f.x += own == i ? row.g : 0.0f, f.y += own == i + 1 ? row.g : 0.0f;
-        w[i / 2] = bf16_pair(f.x, f.y);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        Box::put(box, lane, 4 * h + q, make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
+      put_grad(row, row.target - j.col0 - col - 32 * h, box, h,
+               [&](int i) { return pair(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])); });
     }
-    Box::send<false>(box, map, col, t.row - lane);
+    Box::send<false>(box, map, col, t.row - (threadIdx.x & 31));
   }
 }
 
@@ -608,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint64_t limit = a.wait_limit_ns;
 
   if (warp < 4) {
+    if (MODE == kJobs) fewer_registers<kRegsIssue>();
     if (warp == 0 || warp == 2) {
       // ---------------- copies: one warp brings A, the other B (one for both takes longer to issue them than they
       // are multiplied)
@@ -660,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t ad0 = j.a_mn ? smem_desc_sw128_nmajor(smem_u32(sA), 8192) : smem_desc_sw128(smem_u32(sA));
         const uint64_t bd0 = j.b_mn ? smem_desc_sw128_nmajor(smem_u32(sB), 8192) : smem_desc_sw128(smem_u32(sB));
         for (int k0 = x.kb0; ok && k0 < x.kb1;) {
-          const int k1 = SUMS ? min(k0 + kRun, x.kb1) : x.kb1;
+          const int k1 = SUMS || j.type == kJobGrad ? min(k0 + kRun, x.kb1) : x.kb1;
           if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, limit, abort)) {
             ok = false;
             break;
@@ -716,6 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ---------------- epilogue: thread = row of the tile (a TMEM lane), two warps share a row's columns
+    if (MODE == kJobs) more_registers<kRegsEpilogue>();
     Tile t;
     t.lg = warp & 3;
     t.half = (warp - 4) >> 2;
@@ -749,6 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       };
+      const bool here = t.row - lane < j.m;  // else the warp's rows are all past the end
       if constexpr (SUMS) {
         Half sums = {};
 #pragma unroll 1
@@ -762,15 +805,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int kRows = kBM * R;
           const int64_t tile = (static_cast<int64_t>(x.ks) * j.num_m + x.m_blk) * j.num_n + x.n_blk;
           const int col = t.half * (kBN / 2);
-          if (t.row - lane < j.m)  // else the warp's rows are all past the end
+          if (here)
             store_range(a.ranges + (tile * kBN + col) * kRows + t.row - x.m_blk * kRows, kRows, j.n - t.col0 - col, sums);
           continue;
         }
         ok = __all_sync(0xffffffffu, epilogue_sums(a, j, t, x.n_blk, sums, reinterpret_cast<float4*>(extra), ++turn, abort));
         if (!ok) report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
+      } else if (j.type == kJobGrad && j.num_k > kRun) {
+        Half sums;
+        if (!wait_full()) break;
+        add_run<true>(sums, t.taddr + t.half * (kBN / 2));
+        release();
+#pragma unroll 1
+        for (int k = kRun; k < j.num_k; k += kRun) {
+          if (!wait_full()) break;
+          add_run(sums, t.taddr + t.half * (kBN / 2));
+          release();
+        }
+        if (!ok) break;
+        if (here) epilogue_grad(a, j, t, sums, &maps.out[x.job], out);
       } else {
         if (!wait_full()) break;
-        if (t.row - lane < j.m) {  // else the warp's rows are all past the end
+        if (here) {
           if (j.type == kJobGrad)
             epilogue_grad(a, j, t, &maps.out[x.job], out);
           else
@@ -1007,7 +1063,8 @@ Plan plan_bwd(int64_t n_rows, int64_t d, int64_t vocab) {
                           : static_cast<int>(std::max<int64_t>(
                                 1, std::min<int64_t>({kMaxKSplit, ceil_div(n_rows, kBK) / 8, kPlanSms / ctas / wtiles})));
   p.wsum_bytes = p.wsplit > 1 ? round_up(static_cast<size_t>(p.wsplit) * sum_rows(vocab, ctas) * d * 4, 256) : 0;
-  // G's logits in ranges lie where the products' sums come afterwards
+  // G's logits in ranges, as the forward pass has them (which cuts no more tiles than a piece has), lie where the products'
+  // sums come afterwards
   p.ranges = p.pieces > 1 ? 1 : logit_ranges(n_rows, d, vocab);
   const size_t ranged = p.ranges > 1 ? ranges_bytes(n_rows, d, vocab) : 0;
   p.bytes = p.grad_bytes * (p.pieces > 1 ? 2 : 1) + std::max(p.sum_bytes + p.wsum_bytes, ranged) + 256;

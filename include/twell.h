@@ -578,11 +578,13 @@ TWELL_API size_t twell_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t d
  *   G_j = inv_temperature * (d_logprob (1[j = target] - p_j) - d_entropy p_j (log p_j + entropy))
  *   dH = G W [n_rows][d_model] bf16,  dW = G^T H [vocab][d_model] bf16; either may be null
  * A p_j below 2^-126, less than any normal number of 32 bits, counts as zero.
- * G is made again in pieces of the vocabulary, rounded to bf16 (each entry off by at most 2^-8 of
- * itself: why dW is bf16, too), and multiplied with fp32 sums that are rounded once.  A row without a
- * target takes d_logprob as 0; a row whose lse is -inf gives zeros.  targets with d_logprob, or entropy with
- * d_entropy, may be null: that term is left out.  fp32 tells lse to 2^-24 of itself: beyond |lse| =
- * 16384 p is off by more than its rounding to bf16.  With n_rows == 0 dW is set to zero.
+ * G is made again in pieces of the vocabulary, from the same logits bit for bit as the forward call's lse, whatever the
+ * sizes, rounded to bf16 (each entry off by at most 2^-8 of itself: why dW is bf16, too), and multiplied with
+ * fp32 sums that are rounded once (tensor cores cut off a step of fp32 in 16 terms).  A row without a target takes
+ * d_logprob as 0; a row whose lse is -inf gives zeros.  targets with d_logprob, or entropy with d_entropy, may be
+ * null: that term is left out.  p is off by 2^-18 of itself, and by 2^-23 |lse| of itself as fp32 tells lse to 2^-24
+ * (beyond |lse| = 16384 by more than its rounding to bf16).  Rows that take no part still have to be finite: 0 times
+ * a NaN in H is one in dW.  With n_rows == 0 dW is set to zero.
  * workspace: >= twell_linear_logprobs_bwd_workspace_bytes(...), 256-byte aligned, needs no
  * initialisation: two pieces of G (128 MB each, or 4096 columns where rows are many) and dH in
  * fp32; where one piece is enough much less, and dW in fp32 for ranges of the rows.  One for n_rows
