@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(1024) block_norm_sum_kernel(const NormSumArgs 
 struct Deal {
   int group, groups, ctas, grid, stages, smem;
 };
-Deal deal(int n_rows, int dim, int threads, int pieces, bool sums) {
+Deal deal(int64_t n_rows, int dim, int threads, int pieces, bool sums) {
   Deal d;
   const int need = (dim + 8 * kV - 1) / (8 * kV);
   d.ctas = dim > kWide ? 2 : 1;
@@ -702,10 +702,10 @@ Deal deal(int n_rows, int dim, int threads, int pieces, bool sums) {
   while (d.group < need) d.group *= 2;  // within a warp: a power of two
   const int teams = sm_count() / d.ctas, here = std::max(1, d.group / d.ctas);
   // few rows are spread over the SMs, one to a CTA (or a warp's)
-  d.groups = std::max(1, std::min(threads / here, (n_rows + teams - 1) / teams));
+  d.groups = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(threads / here, (n_rows + teams - 1) / teams)));
   if (d.group < 32) d.groups = (d.groups + 32 / d.group - 1) / (32 / d.group) * (32 / d.group);
   if (d.group > 32) d.groups = std::min(d.groups, kMaxBarriers);
-  d.grid = std::max(1, std::min({(n_rows + d.groups - 1) / d.groups, teams, kMaxParts}));
+  d.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(n_rows + d.groups - 1) / d.groups, teams, kMaxParts})));
   const int row = d.groups * here * kV * pieces * 16, weights = 2 * kV * 2 * 16 * here;
   d.stages = std::max(1, std::min(kMaxStages, (kSharedBytes - weights) / row));
   // the groups' sums over the rows meet where the rows were
