@@ -131,8 +131,21 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// A pair's hand-over: the second CTA's copies to the first one's MMAs, and accumulators back.  Arrivals, and the waits for
+// them, have the cluster's scope (without one they have a CTA's, which promises nothing to the other) and order
+// shared memory by fences for it alone.  As arrive.release.cluster they would wait for everything that the CTA
+// has under way to memory: 8192 x 2048 x 32768 in 1403 us, not 577 to 600, its gradient 5496.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+      : "memory");
+}
+template <int R>
+__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort) {
+  const bool ok = mbar_wait<R == 2>(bar, parity, limit_ns, abort);
+  if (R == 2) asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+  return ok;
 }
 
 // The gradient's epilogue holds a row's logits while it makes G of them: its warps take registers that the issuing ones have
@@ -669,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int dx = mn ? 0 : kBK, dy = mn ? kBK : 0;
         int cx = mn ? at : x.kb0 * kBK, cy = mn ? x.kb0 * kBK : at;
         for (int n = x.kb1 - x.kb0; n > 0; --n, cx += dx, cy += dy) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, limit, abort)) {
+          if (!wait_pair<R>(&empty[stage], phase ^ 1u, limit, abort)) {
             ok = false;
             break;
           }
@@ -702,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t bd0 = j.b_mn ? smem_desc_sw128_nmajor(smem_u32(sB), 8192) : smem_desc_sw128(smem_u32(sB));
         for (int k0 = x.kb0; ok && k0 < x.kb1;) {
           const int k1 = SUMS || j.type == kJobGrad ? min(k0 + kRun, x.kb1) : x.kb1;
-          if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, limit, abort)) {
+          if (!wait_pair<R>(&tempty[acc], acc_phase ^ 1u, limit, abort)) {
             ok = false;
             break;
           }
@@ -710,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kBN);
           uint32_t add = 0;
           for (int n = k1 - k0; n > 0; --n) {
-            if (!mbar_wait(&full[stage], phase, limit, abort)) {
+            if (!wait_pair<R>(&full[stage], phase, limit, abort)) {
               ok = false;
               break;
             }
@@ -772,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       t.col0 = x.n_blk * kBN;
       t.valid = t.row < j.m;
       auto wait_full = [&]() {
-        ok = mbar_wait(&tfull[acc], acc_phase, limit, abort);
+        ok = wait_pair<R>(&tfull[acc], acc_phase, limit, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) report_error(a.status, TWELL_ERR_WAIT_TIMEOUT);
         tc_fence_after();
