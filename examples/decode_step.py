@@ -31,6 +31,7 @@ import activation_sparse_transformer_gb300 as tw
 
 D_MODEL, D_FF, LAYERS, Q_HEADS, KV_HEADS, HEAD_DIM, VOCAB = 512, 2048, 2, 8, 2, 64, 1000
 TILE, CAP, PAGE = 64, 8, 16
+EPS = torch.finfo(torch.float32).eps  # of the norms, as torch's rms_norm of fp32 rows has it
 
 
 class Decoder:
@@ -70,7 +71,7 @@ class Decoder:
         tw.twell_kv_plan(self.lens, new, self.table, self.ring, self.pool, PAGE, plan)
         x = self.embed[tokens]
         hidden = torch.empty_like(x)
-        tw.twell_block_norm(x, None, None, hidden, w_pre=self.norm)
+        tw.twell_block_norm(x, None, None, hidden, w_pre=self.norm, eps=EPS)
         o = torch.empty((n, Q_HEADS, HEAD_DIM), dtype=torch.bfloat16, device="cuda")
         ws = torch.empty(tw.kv_attention_workspace_bytes(n, requests, Q_HEADS, KV_HEADS, HEAD_DIM), dtype=torch.uint8,
                          device="cuda")
@@ -80,8 +81,8 @@ class Decoder:
             tw.twell_kv_append(k, v, plan.cu_q, plan.slots, cache)
             tw.twell_kv_attention(q, cache, self.table, plan.cu_q, plan.positions, plan.kv_lens, self.max_len,
                                   max_new, HEAD_DIM ** -0.5, o, ws)
-            tw.twell_block_norm(x, o.view(n, -1) @ layer["out"].T, x, hidden, w_pre=self.norm)
-            tw.twell_block_norm(x, self.ffn(hidden, layer), x, hidden, w_pre=self.norm)
+            tw.twell_block_norm(x, o.view(n, -1) @ layer["out"].T, x, hidden, w_pre=self.norm, eps=EPS)
+            tw.twell_block_norm(x, self.ffn(hidden, layer), x, hidden, w_pre=self.norm, eps=EPS)
         self.lens, self.pool = plan.kv_lens, plan.pool
         return hidden @ self.unembed.T, hidden, plan
 
