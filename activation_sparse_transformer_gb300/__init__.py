@@ -487,16 +487,19 @@ def twell_profile_read(kernel) -> tuple:
 KV_E4M3, KV_INT8 = 0, 1
 _torch = None
 _raw_stream = None
+_stream_of_device = None
+_device = None
 
 
 def _setup():
-    """torch, imported at the first call, and the current stream's handle without
-    the Stream object around it (these calls are as short as the kernels they start)."""
-    global _torch, _raw_stream
+    """torch, imported at the first call, and the current device and stream's handle without
+    the objects around them (these calls are as short as the kernels they start)."""
+    global _torch, _raw_stream, _stream_of_device, _device
     import torch
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    _raw_stream = ((lambda: get(torch._C._cuda_getDevice())) if get is not None
-                   else (lambda: torch.cuda.current_stream().cuda_stream))
+    _device = device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _stream_of_device = get = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                      lambda at: torch.cuda.current_stream(at).cuda_stream)
+    _raw_stream = lambda: get(device())  # noqa: E731
     _torch = torch
     return torch
 
@@ -518,9 +521,17 @@ def _arg(t, dtype, n: int, name: str) -> int:
 
 
 def _on_device(*tensors) -> None:
+    """All on the current device, where the call's kernels run: another one's memory may be out of their reach."""
+    here = None
     for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("tensors passed to libtwell must be CUDA tensors")
+        if t is not None:
+            at = t.get_device()
+            if at != here:
+                if at < 0:
+                    raise ValueError("tensors passed to libtwell must be CUDA tensors")
+                here = _device()
+                if at != here:
+                    raise ValueError(f"a tensor on device {at}, the current device is {here}")
 
 
 def _maybe(t, dtype, n: int, name: str):
@@ -848,13 +859,17 @@ def twell_block_norm(x, y, x_out=None, h=None, *, w_post=None, gate=None, w_pre=
     code, post, gate_p, pre = _weights(dim, w_post, gate, w_pre)
     row_p = _row(row_gate, f32, rows, "row_gate")
     r1, r2 = _row(rstd_post, f32, rows, "rstd_post"), _row(rstd_pre, f32, rows, "rstd_pre")
-    if not (x.is_cuda and (y is None or y.is_cuda) and (x_out is None or x_out.is_cuda) and (h is None or h.is_cuda)
-            and (w_post is None or w_post.is_cuda) and (gate is None or gate.is_cuda) and (w_pre is None or w_pre.is_cuda)
-            and (row_gate is None or row_gate.is_cuda) and (rstd_post is None or rstd_post.is_cuda)
-            and (rstd_pre is None or rstd_pre.is_cuda)):
-        raise ValueError("tensors passed to libtwell must be CUDA tensors")
+    at = x.get_device()  # one look at each: this call is the shortest of all
+    if (at < 0 or (y is not None and y.get_device() != at) or (x_out is not None and x_out.get_device() != at)
+            or (h is not None and h.get_device() != at) or (w_post is not None and w_post.get_device() != at)
+            or (gate is not None and gate.get_device() != at) or (w_pre is not None and w_pre.get_device() != at)
+            or (row_gate is not None and row_gate.get_device() != at)
+            or (rstd_post is not None and rstd_post.get_device() != at)
+            or (rstd_pre is not None and rstd_pre.get_device() != at) or at != _device()):
+        _on_device(x, y, x_out, h, w_post, gate, w_pre, row_gate, rstd_post, rstd_pre)
     rc = load_library().twell_block_norm(x_p, kind, ldx, y_p, ldy, rows, dim, post, gate_p, pre, code, row_p, skip_scale,
-                                         branch_scale, eps, o_p, ldo, h_p, ldh, r1, r2, _on(stream))
+                                         branch_scale, eps, o_p, ldo, h_p, ldh, r1, r2,
+                                         _stream_of_device(at) if stream is None else int(stream.cuda_stream))
     if rc:
         _check(rc, "twell_block_norm")
 
