@@ -11,7 +11,7 @@
 // Backward, in pieces of the vocabulary: x again, from it
 //   G = (g (1[t] - p) - ge p (log p + entropy)) / T,  p = exp(x - lse),
 // as bf16 into the workspace (the tensor cores take bf16, and each entry is then
-// off by 2^-9 of itself on average, as the bf16 results are), then
+// off by up to 2^-8 of itself, as the bf16 results are), then
 // dH += G W_piece and dW_piece = G^T H with fp32 sums.  A launch runs the products
 // of one piece together with G of the next one, which needs a buffer of its own.
 //
@@ -39,8 +39,8 @@
 namespace twell {
 namespace {
 
-// A tile: kBM rows a CTA, kBN columns.  A step of K takes 257 ns and 0.59 a column, so narrower tiles do not pay even
-// where they leave fewer CTAs idle in the last round (413 x 1032 x 50001: 192 columns 54 us, 128 73, 256 52).
+// A tile: kBM rows a CTA, kBN columns.  Narrower tiles do not pay even where they leave fewer CTAs idle in the last round:
+// 413 x 1032 x 50001 takes 257 ns and 0.59 a column for a step of K (192 columns 54 us, 128 73, 256 52).
 constexpr int kBM = 128, kBN = 256, kBK = 64, kUmmaK = 16;
 constexpr int kThreads = 384, kEpiWarps = 8;
 constexpr int kRun = 8;  // steps of K that logits are added up over in tensor memory
@@ -65,7 +65,9 @@ constexpr int kBandWide = 64, kBandGradients = 8;
 constexpr int kMaxJobs = 3;
 constexpr int kMaxSize = 1 << 30;        // rows, columns: indexes of whole tiles fit in 32 bits
 constexpr int kPlanSms = 152;            // plans do not depend on the device, workspaces neither
-constexpr int64_t kPieceBytes = 1 << 27; // of G: what the L2 cache can hold
+// Of G.  It comes back from memory, not from L2, but smaller pieces leave the last rounds of their launches emptier (single
+// calls of 8192 x 2048 x 32768: 32 MB 2165 us, 64 MB 1850, 128 MB 1772, 256 MB 1756 for twice the workspace).
+constexpr int64_t kPieceBytes = 1 << 27;
 constexpr int kMinPiece = 4096;          // columns; dH's sums are read and written once a piece
 constexpr int kMaxKSplit = 32;
 constexpr int kRangeSteps = kRun, kRangesSave = 12;  // of K: see logit_ranges
@@ -1069,7 +1071,7 @@ Plan plan_bwd(int64_t n_rows, int64_t d, int64_t vocab) {
       std::max<int64_t>(1, std::min<int64_t>({kMaxKSplit, num_k / 8, kPlanSms / ctas / std::max<int64_t>(1, tiles)})));
   p.grad_bytes = round_up(static_cast<size_t>(n_rows) * p.piece * 2, 256);
   p.sum_bytes = p.pieces > 1 || p.ksplit > 1 ? round_up(static_cast<size_t>(p.ksplit) * sum_rows(n_rows, ctas) * d * 4, 256) : 0;
-  // So is dW's, over many rows (9080 x 376 x 232: 63 -> 26 us, 11351 x 520 x 1245 90 -> 58); with several pieces it
+  // So is dW's, over many rows (9080 x 376 x 232: 63 -> 27 us, 11351 x 520 x 1245 90 -> 60); with several pieces it
   // has tiles enough.
   const int64_t wtiles = ceil_div(vocab, kBM * ctas) * static_cast<int64_t>(ceil_div(d, kBN));
   p.wsplit = p.pieces > 1 ? 1

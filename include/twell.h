@@ -579,8 +579,8 @@ TWELL_API size_t twell_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t d
  *   dH = G W [n_rows][d_model] bf16,  dW = G^T H [vocab][d_model] bf16; either may be null
  * A p_j below 2^-126, less than any normal number of 32 bits, counts as zero.
  * G is made again in pieces of the vocabulary, from the same logits bit for bit as the forward call's lse, whatever the
- * sizes, rounded to bf16 (each entry off by at most 2^-8 of itself: why dW is bf16, too), and multiplied with
- * fp32 sums that are rounded once (tensor cores cut off a step of fp32 in 16 terms).  A row without a target takes
+ * sizes, rounded to bf16 (each entry off by at most 2^-8 of itself), and multiplied with fp32 sums that are
+ * rounded once (tensor cores cut off a step of fp32 in 16 terms).  A row without a target takes
  * d_logprob as 0; a row whose lse is -inf gives zeros.  targets with d_logprob, or entropy with d_entropy, may be
  * null: that term is left out.  p is off by 2^-18 of itself, and by 2^-23 |lse| of itself as fp32 tells lse to 2^-24
  * (beyond |lse| = 16384 by more than its rounding to bf16).  Rows that take no part still have to be finite: 0 times
