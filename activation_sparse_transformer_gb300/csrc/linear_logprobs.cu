@@ -73,6 +73,7 @@ constexpr int kMaxKSplit = 32;
 constexpr int kRangeSteps = kRun, kRangesSave = 12;  // of K: see logit_ranges
 constexpr int kJoinCols = 64;                // of ranges that are added by a CTA
 constexpr int kTileSteps = 5;            // of K, that a tile takes at least: until its results have left
+constexpr float kFarthest = 16777216.0f;  // of |lse|: a step of fp32 is 2 from there on
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
 enum JobType { kJobSums, kJobGrad, kJobDHidden, kJobDWeight };
@@ -135,8 +136,8 @@ __device__ __forceinline__ void cluster_sync() {
 }
 // A pair's hand-over: the second CTA's copies to the first one's MMAs, and accumulators back.  Arrivals, and the waits for
 // them, have the cluster's scope (without one they have a CTA's, which promises nothing to the other) and order
-// shared memory by fences for it alone.  As arrive.release.cluster they would wait for everything that the CTA
-// has under way to memory: 8192 x 2048 x 32768 in 1403 us, not 577 to 600, its gradient 5496.
+// shared memory by fences for it alone.  With arrive.release.cluster, which orders global memory too,
+// 8192 x 2048 x 32768 takes 1403 us, not 577 to 600, and its gradient 5496.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile(
       "fence.release.sync_restrict::shared::cta.cluster;\n\t"
@@ -448,7 +449,9 @@ struct GradRow {
         f1 = -a.inv_t * a.ge[row];
         f0 = fmaf(f1, a.entropy[row], f0);
       }
-      if (lse == -INFINITY) lse = 0.0f, f0 = 0.0f, f1 = 0.0f, g = 0.0f;  // a row of -inf only: zeros
+      // a row of -inf only, or one so far from zero that fp32 tells lse to no better than 1, and so p to no
+      // better than a factor e (all tokens at -3e38: p = 1 for each): zeros
+      if (fabsf(lse) >= kFarthest) lse = INFINITY, f0 = 0.0f, f1 = 0.0f, g = 0.0f;
     }
     inv_t = pair(a.inv_t, a.inv_t), minus_lse = pair(-lse, -lse), a0 = pair(f0, f0), a1 = pair(f1, f1);
   }

@@ -583,8 +583,9 @@ TWELL_API size_t twell_linear_logprobs_workspace_bytes(int32_t n_rows, int32_t d
  * rounded once (tensor cores cut off a step of fp32 in 16 terms).  A row without a target takes
  * d_logprob as 0; a row whose lse is -inf gives zeros.  targets with d_logprob, or entropy with d_entropy, may be
  * null: that term is left out.  p is off by 2^-18 of itself, and by 2^-23 |lse| of itself as fp32 tells lse to 2^-24
- * (beyond |lse| = 16384 by more than its rounding to bf16).  Rows that take no part still have to be finite: 0 times
- * a NaN in H is one in dW.  With n_rows == 0 dW is set to zero.
+ * (beyond |lse| = 16384 by more than its rounding to bf16; from 2^24 on nothing is known of p, and the row gives
+ * zeros).  Rows that take no part still have to be finite: 0 times a NaN in H is one in dW.  With n_rows == 0 dW is
+ * set to zero.
  * workspace: >= twell_linear_logprobs_bwd_workspace_bytes(...), 256-byte aligned, needs no
  * initialisation: two pieces of G (128 MB each, or 4096 columns where rows are many) and dH in
  * fp32; where one piece is enough much less, and dW in fp32 for ranges of the rows.  One for n_rows
